@@ -337,6 +337,128 @@ specv_status specv_mss_verify(const specv_mss_args* args, void* workspace,
                               size_t workspace_bytes, void* stream);
 
 /*
+ * Sampling with temperature, top-k, top-p and min-p from given uniforms, and
+ * the logits that these rules leave.  No page has a counterpart: serving
+ * engines sample (and verify) under such rules, and the accept test keeps the
+ * target's law only if p and q are the distributions that are sampled from.
+ * For row (b, i), i < R, with T = temperature[b] and w_v = exp((z_v - max z)/T):
+ *   tokens with w_v < 2^-48 count as zero; in the order (logit descending,
+ *   index ascending) the first n tokens are kept, n = max(1, min(n_k, n_p, n_m)),
+ *   n_k = top_k[b] (0: every token), n_p = the smallest n whose weights reach
+ *   top_p[b] times the weight of the first n_k (top_p 1: n_k), n_m = the number
+ *   of w_v >= min_p[b].  T = 0 keeps the first maximum alone.
+ *   tokens[b, i] = the smallest kept v whose running sum of w in index order
+ *   exceeds uniforms[b, i] times the kept weight (SPECV_ROW_FALLBACK: none did,
+ *   a uniform of 1 or more: the last kept token); prob[b, i] = its share of the
+ *   kept weight; kept[b, i] = n.
+ *   filtered[b, i, v] = z_v if v is kept, else -inf: what specv_verify, in the
+ *   place of z, verifies under the rules.  It may be `logits` itself (same
+ *   strides); otherwise the two do not overlap.
+ * uniforms and tokens are given together, or both NULL for `filtered` alone.
+ * Sums carry about 30 bits more than their result needs (fp32 pairs, 64-bit
+ * totals), so cuts and draws agree with 64-bit arithmetic except next to a
+ * border by about 1e-10 of the row's weight.
+ * Row status: SPECV_ROW_NONFINITE, SPECV_ROW_BAD_TEMP, SPECV_ROW_BAD_FILTER,
+ * SPECV_ROW_DEVICE_TIMEOUT: token -1, prob 0, kept 0, filtered all -inf.
+ * One kernel, no workspace: a cluster of CTAs holds the row in shared memory,
+ * so V is at most about 780,000 (fp32) or 1,560,000 (bf16), else
+ * SPECV_ERR_UNSUPPORTED.
+ */
+#define SPECV_ROW_BAD_FILTER 64 /* top_k < 0, or top_p or min_p outside [0, 1] */
+
+typedef struct {
+  int32_t B, R, V;             /* R rows per batch entry share its rules (>= 1) */
+  int32_t dtype;               /* specv_dtype */
+  const void* logits;          /* row (b, i) at b * batch_stride + i * row_stride */
+  int64_t batch_stride, row_stride;
+  const float* temperature;    /* [B] */
+  const int32_t* top_k;        /* optional [B], 0: off */
+  const float* top_p;          /* optional [B], 1: off */
+  const float* min_p;          /* optional [B], 0: off */
+  const float* uniforms;       /* [B, R] in [0, 1), or NULL */
+  int32_t* tokens;             /* OUT [B, R], or NULL */
+  float* prob;                 /* OUT, optional [B, R] */
+  int32_t* kept;               /* OUT, optional [B, R] */
+  void* filtered;              /* OUT, optional (dtype) */
+  int64_t filtered_batch_stride, filtered_row_stride;
+  int32_t* row_status;         /* OUT, optional [B, R] */
+} specv_sample_args;
+
+specv_status specv_sample(const specv_sample_args* args, void* stream);
+
+/*
+ * The k largest logits of each row, by (logit descending, index ascending),
+ * and the row's log-sum-exp at a temperature: what a teacher keeps of its
+ * distribution for specv_distill.  -inf logits are never listed: ids -1 and
+ * values -inf pad a row with fewer than k others.  lse[b] = log sum_v
+ * exp(z_v / temperature).  SPECV_ROW_NONFINITE (NaN, +inf, all -inf) and
+ * SPECV_ROW_DEVICE_TIMEOUT: ids -1, values -inf, lse NaN.  One kernel, no
+ * workspace; V as in specv_sample.
+ */
+#define SPECV_MAX_TOP 1024
+
+typedef struct {
+  int32_t B, V, k;             /* rows; vocabulary; 1..SPECV_MAX_TOP */
+  int32_t dtype;               /* specv_dtype */
+  const void* logits;
+  int64_t row_stride;          /* elements, >= V */
+  float temperature;           /* of lse alone, in [1e-3, 1e3] */
+  int32_t* ids;                /* OUT [B, k] */
+  float* values;               /* OUT [B, k] */
+  float* lse;                  /* OUT, optional [B] */
+  int32_t* row_status;         /* OUT, optional [B] */
+} specv_top_args;
+
+specv_status specv_top_logits(const specv_top_args* args, void* stream);
+
+/*
+ * Distillation of a drafter from a teacher's top logits: the loss per row and
+ * its gradient.  With T = temperature, q = softmax(z / T), p_j =
+ * exp(t_j / T - L), L = teacher_lse[n] (the teacher's log-sum-exp at T over its
+ * whole vocabulary) or, without it, that of the row's listed entries:
+ *   loss[n] = weights[n] * D,   D = sum_j p_j (log p_j - log q(id_j))
+ *   SPECV_DISTILL_TAIL: + r (log r - log(1 - s)), r = 1 - sum_j p_j (below
+ *   2^-20: none), s = the listed ids' mass under q: all other tokens as one
+ *   outcome.  If the student has no mass outside the list and r > 0, the loss
+ *   is +inf and the gradient leaves that term out.
+ * Entries with id -1 are absent; an id listed twice counts as two entries of
+ * the sum.  A row of weight 0 is not read: loss and gradient 0.
+ * specv_distill writes loss, and if given the gradient of sum_n loss[n] and
+ * the statistics from which specv_distill_backward computes the gradient of
+ * sum_n grad_loss[n] * loss[n] (grad_loss NULL: ones) in one pass over the
+ * same inputs.  Each gradient is rounded once, to the logits' type.
+ * Row status: SPECV_ROW_BAD_TOKEN (an id outside [-1, V)), SPECV_ROW_NONFINITE
+ * (student row with NaN or +inf, or all -inf; teacher entry or lse NaN or
+ * +inf), SPECV_ROW_DEVICE_TIMEOUT: loss and gradient 0.
+ * One kernel each, no workspace; V as in specv_sample.  grad overlaps nothing.
+ */
+#define SPECV_DISTILL_TAIL 1
+
+typedef struct {
+  int32_t N, V, K;             /* rows; vocabulary; teacher entries, 1..SPECV_MAX_TOP */
+  int32_t dtype;               /* specv_dtype, of logits and grad */
+  const void* logits;          /* student rows */
+  int64_t row_stride;          /* elements, >= V */
+  const int32_t* teacher_ids;  /* [N, K], -1: none */
+  const float* teacher_logits; /* [N, K] */
+  int64_t teacher_stride;      /* row stride of the two, >= K */
+  const float* teacher_lse;    /* optional [N] */
+  const float* weights;        /* optional [N] */
+  float temperature;           /* in [1e-3, 1e3] */
+  int32_t flags;               /* SPECV_DISTILL_TAIL or 0 */
+  float* loss;                 /* OUT [N] (specv_distill) */
+  float* stats;                /* [N, 4], 16-byte aligned: OUT, optional
+                                  (specv_distill), or in (backward) */
+  const float* grad_loss;      /* optional [N] (backward) */
+  void* grad;                  /* OUT (optional for specv_distill) */
+  int64_t grad_row_stride;     /* elements, >= V */
+  int32_t* row_status;         /* OUT, optional [N] (specv_distill) */
+} specv_distill_args;
+
+specv_status specv_distill(const specv_distill_args* args, void* stream);
+specv_status specv_distill_backward(const specv_distill_args* args, void* stream);
+
+/*
  * Geometric fan-out ("Speculative Speculative Decoding" Theorem 12, proved in
  * Appendix A.2).  For a drafter with per-token acceptance rate a (0 < a < 1)
  * whose cache-miss probability at fan-out F is F^-r (r > 0), the fan-outs

@@ -11,6 +11,12 @@ Entry points (same names as the C ABI):
   specv_ssd_round(target, draft, draft_tokens, temperature, uniforms, F, ...)
   specv_predict_outcomes(draft, draft_tokens, F, ...)
   specv_check_hit(keys, accept_len, out_tokens, ...)
+  specv_sample(logits, temperature, uniforms, top_k=, top_p=, min_p=, ...)
+  specv_filter_logits(logits, temperature, top_k=, top_p=, min_p=, ...)
+  specv_top_logits(logits, k, ...)
+  specv_distill(logits, teacher_ids, teacher_logits, ...)
+  specv_distill_backward(logits, teacher_ids, teacher_logits, stats, ...)
+  distill_loss(logits, teacher_ids, teacher_logits, ...)  (differentiable)
 """
 from __future__ import annotations
 
@@ -26,6 +32,9 @@ SPECV_OK, SPECV_ERR_INVALID_ARG, SPECV_ERR_UNSUPPORTED, SPECV_ERR_CUDA, SPECV_ER
 SPECV_BF16, SPECV_FP32 = 0, 1
 ROW_BAD_TOKEN, ROW_NONFINITE, ROW_BAD_TEMP, ROW_FALLBACK, ROW_DEVICE_TIMEOUT = 1, 2, 4, 8, 16
 ROW_BAD_COUNT = 32
+ROW_BAD_FILTER = 64
+SPECV_MAX_TOP = 1024
+SPECV_DISTILL_TAIL = 1
 SPECV_NO_DRAFT_PROBS = 1
 SPECV_MSS_NAIVE = 1
 
@@ -69,6 +78,28 @@ class PredictArgs(ctypes.Structure):
                 ("draft_logits", _P), ("draft_batch_stride", _I64), ("draft_row_stride", _I64),
                 ("draft_tokens", _P), ("keys", _P), ("key_logits", _P), ("row_status", _P),
                 ("fanout", _P)]
+
+
+class SampleArgs(ctypes.Structure):
+    _fields_ = [("B", _I32), ("R", _I32), ("V", _I32), ("dtype", _I32), ("logits", _P),
+                ("batch_stride", _I64), ("row_stride", _I64), ("temperature", _P),
+                ("top_k", _P), ("top_p", _P), ("min_p", _P), ("uniforms", _P), ("tokens", _P),
+                ("prob", _P), ("kept", _P), ("filtered", _P), ("filtered_batch_stride", _I64),
+                ("filtered_row_stride", _I64), ("row_status", _P)]
+
+
+class TopArgs(ctypes.Structure):
+    _fields_ = [("B", _I32), ("V", _I32), ("k", _I32), ("dtype", _I32), ("logits", _P),
+                ("row_stride", _I64), ("temperature", ctypes.c_float), ("ids", _P),
+                ("values", _P), ("lse", _P), ("row_status", _P)]
+
+
+class DistillArgs(ctypes.Structure):
+    _fields_ = [("N", _I32), ("V", _I32), ("K", _I32), ("dtype", _I32), ("logits", _P),
+                ("row_stride", _I64), ("teacher_ids", _P), ("teacher_logits", _P),
+                ("teacher_stride", _I64), ("teacher_lse", _P), ("weights", _P),
+                ("temperature", ctypes.c_float), ("flags", _I32), ("loss", _P), ("stats", _P),
+                ("grad_loss", _P), ("grad", _P), ("grad_row_stride", _I64), ("row_status", _P)]
 
 
 class SpecvError(RuntimeError):
@@ -116,6 +147,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                            _P, _P]
     lib.specv_check_hit.restype = ctypes.c_int
     lib.specv_check_hit.argtypes = [_I32, _I32, _I32, _P, _P, _P, _P, _P]
+    for name, args in (("specv_sample", SampleArgs), ("specv_top_logits", TopArgs),
+                       ("specv_distill", DistillArgs), ("specv_distill_backward", DistillArgs)):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.POINTER(args), _P]
     lib.specv_status_string.restype = ctypes.c_char_p
     lib.specv_status_string.argtypes = [ctypes.c_int]
     lib.specv_last_error.restype = ctypes.c_char_p
@@ -450,3 +486,216 @@ def specv_check_hit(keys, accept_len, out_tokens, *, hit=None, stream=None):
     _check(lib.specv_check_hit(B, K1 - 1, F, _ptr(keys), _ptr(accept_len), _ptr(out_tokens),
                                _ptr(hit), _stream(stream)))
     return hit
+
+
+def _of(t, shape, dtype, what):
+    """t's pointer after a check of its type, shape, layout and (None: optional)."""
+    if t is None:
+        return None
+    assert tuple(t.shape) == tuple(shape), f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}"
+    assert t.dtype == dtype, f"{what}: {t.dtype}, expected {dtype}"
+    assert t.is_contiguous(), f"{what} must be contiguous"
+    return t.data_ptr()
+
+
+def _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, prob, kept, filtered,
+                 row_status, stream):
+    import torch
+    lib = load_library()
+    assert logits.dim() in (2, 3) and logits.stride(-1) == 1
+    lead = tuple(logits.shape[:-1])
+    B, V = lead[0], logits.shape[-1]
+    R = lead[1] if logits.dim() == 3 else 1
+    f32, i32, dev = torch.float32, torch.int32, logits.device
+
+    def strides(t):
+        return (t.stride(0), t.stride(1) if t.dim() == 3 else max(t.stride(0), V))
+
+    if uniforms is not None:
+        tokens = torch.empty(lead, dtype=i32, device=dev) if tokens is None else tokens
+        prob = torch.empty(lead, dtype=f32, device=dev) if prob is None else prob
+    kept = torch.empty(lead, dtype=i32, device=dev) if kept is None else kept
+    row_status = torch.empty(lead, dtype=i32, device=dev) if row_status is None else row_status
+    if filtered is not None:
+        assert filtered.shape == logits.shape and filtered.dtype == logits.dtype
+        assert filtered.stride(-1) == 1
+    bs, rs = strides(logits)
+    fbs, frs = strides(filtered) if filtered is not None else (0, 0)
+    args = SampleArgs(B, R, V, _dtype_code(logits), logits.data_ptr(), bs, rs,
+                      _of(temperature, (B,), f32, "temperature"), _of(top_k, (B,), i32, "top_k"),
+                      _of(top_p, (B,), f32, "top_p"), _of(min_p, (B,), f32, "min_p"),
+                      _of(uniforms, lead, f32, "uniforms"), _of(tokens, lead, i32, "tokens"),
+                      _of(prob, lead, f32, "prob"), _of(kept, lead, i32, "kept"),
+                      None if filtered is None else filtered.data_ptr(), fbs, frs,
+                      _of(row_status, lead, i32, "row_status"))
+    _check(lib.specv_sample(ctypes.byref(args), _stream(stream)))
+    out = dict(kept=kept, row_status=row_status)
+    if uniforms is not None:
+        out.update(tokens=tokens, prob=prob)
+    if filtered is not None:
+        out["filtered"] = filtered
+    return out
+
+
+def specv_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None, tokens=None,
+                 prob=None, kept=None, filtered=None, row_status=None, stream=None) -> dict:
+    """One token per row under temperature, top-k, top-p and min-p, by inverse
+    CDF of the given uniforms (see include/specv.h, specv_sample).
+
+    logits [B, V] or [B, R, V] (bf16 or fp32, CUDA, last dim contiguous);
+    temperature fp32 [B] (0: greedy), top_k int32 [B] (0: off), top_p fp32 [B]
+    (1: off), min_p fp32 [B] (0: off), shared by an entry's R rows; uniforms
+    fp32 [B] or [B, R].  Returns tokens int32, prob fp32, kept int32 and
+    row_status int32, shaped as uniforms, and `filtered` if that was given (a
+    tensor like logits, or logits itself) to be written.
+    """
+    assert uniforms is not None
+    return _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, prob, kept,
+                        filtered, row_status, stream)
+
+
+def specv_filter_logits(logits, temperature, *, top_k=None, top_p=None, min_p=None, filtered=None,
+                        kept=None, row_status=None, stream=None) -> dict:
+    """The logits that the rules of specv_sample keep, -inf elsewhere: filtered
+    target and draft rows are verified (specv_verify) under those rules.
+
+    Arguments as specv_sample; filtered may be logits itself.  Returns
+    filtered, kept, row_status.
+    """
+    import torch
+    if filtered is None:
+        filtered = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    return _sample_call(logits, temperature, None, top_k, top_p, min_p, None, None, kept, filtered,
+                        row_status, stream)
+
+
+def specv_top_logits(logits, k: int, *, temperature: float = 1.0, ids=None, values=None, lse=None,
+                     row_status=None, stream=None) -> dict:
+    """The k largest logits per row of logits [B, V] (bf16 or fp32, CUDA), by
+    (logit descending, index ascending), and log sum exp(logits / temperature)
+    (see include/specv.h).  Returns ids int32 [B, k], values fp32 [B, k], lse
+    fp32 [B], row_status int32 [B]."""
+    import torch
+    lib = load_library()
+    assert logits.dim() == 2 and logits.stride(-1) == 1
+    B, V = logits.shape
+    f32, i32, dev = torch.float32, torch.int32, logits.device
+    rows = max(int(k), 0)
+    ids = torch.empty((B, rows), dtype=i32, device=dev) if ids is None else ids
+    values = torch.empty((B, rows), dtype=f32, device=dev) if values is None else values
+    lse = torch.empty(B, dtype=f32, device=dev) if lse is None else lse
+    row_status = torch.empty(B, dtype=i32, device=dev) if row_status is None else row_status
+    args = TopArgs(B, V, int(k), _dtype_code(logits), logits.data_ptr(), max(logits.stride(0), V),
+                   float(temperature), _of(ids, (B, rows), i32, "ids"),
+                   _of(values, (B, rows), f32, "values"), _of(lse, (B,), f32, "lse"),
+                   _of(row_status, (B,), i32, "row_status"))
+    _check(lib.specv_top_logits(ctypes.byref(args), _stream(stream)))
+    return dict(ids=ids, values=values, lse=lse, row_status=row_status)
+
+
+def _distill_args(logits, ids, values, teacher_lse, weights, temperature, tail, grad):
+    import torch
+    assert logits.dim() == 2 and logits.stride(-1) == 1
+    N, V = logits.shape
+    K = ids.shape[1]
+    f32 = torch.float32
+    assert ids.shape == values.shape == (N, K) and ids.dtype == torch.int32 and values.dtype == f32
+    assert ids.stride(-1) == 1 and values.stride(-1) == 1
+    ts = max(ids.stride(0), K)
+    assert N <= 1 or ids.stride(0) == values.stride(0), "teacher_ids and teacher_logits share one row stride"
+    if grad is not None:
+        assert grad.shape == logits.shape and grad.dtype == logits.dtype and grad.stride(-1) == 1
+    return DistillArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), max(logits.stride(0), V),
+                       ids.data_ptr(), values.data_ptr(), ts,
+                       _of(teacher_lse, (N,), f32, "teacher_lse"),
+                       _of(weights, (N,), f32, "weights"), float(temperature),
+                       SPECV_DISTILL_TAIL if tail else 0, None, None, None,
+                       None if grad is None else grad.data_ptr(),
+                       0 if grad is None else max(grad.stride(0), V), None)
+
+
+def specv_distill(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temperature: float = 1.0,
+                  weights=None, tail: bool = False, with_grad: bool = False, loss=None, stats=None,
+                  grad=None, row_status=None, stream=None) -> dict:
+    """Distillation loss of student rows against a teacher's top logits (see
+    include/specv.h, specv_distill).
+
+    logits [N, V] (bf16 or fp32, CUDA); teacher_ids int32 and teacher_logits
+    fp32 [N, K], as specv_top_logits returns them (id -1: none); teacher_lse
+    fp32 [N] at the same temperature (None: the listed entries alone are
+    normalised; `tail` needs it); weights fp32 [N] or None.  Returns loss fp32
+    [N], stats fp32 [N, 4] (for specv_distill_backward), row_status int32 [N],
+    and grad (the gradient of loss.sum(), like logits) with with_grad or where
+    a buffer is given.
+    """
+    import torch
+    lib = load_library()
+    N, dev = logits.shape[0], logits.device
+    if grad is None and with_grad:
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    loss = torch.empty(N, dtype=torch.float32, device=dev) if loss is None else loss
+    stats = torch.empty((N, 4), dtype=torch.float32, device=dev) if stats is None else stats
+    row_status = torch.empty(N, dtype=torch.int32, device=dev) if row_status is None else row_status
+    args = _distill_args(logits, teacher_ids, teacher_logits, teacher_lse, weights, temperature,
+                         tail, grad)
+    args.loss = _of(loss, (N,), torch.float32, "loss")
+    args.stats = _of(stats, (N, 4), torch.float32, "stats")
+    args.row_status = _of(row_status, (N,), torch.int32, "row_status")
+    _check(lib.specv_distill(ctypes.byref(args), _stream(stream)))
+    out = dict(loss=loss, stats=stats, row_status=row_status)
+    if grad is not None:
+        out["grad"] = grad
+    return out
+
+
+def specv_distill_backward(logits, teacher_ids, teacher_logits, stats, *, grad_loss=None,
+                           teacher_lse=None, temperature: float = 1.0, weights=None,
+                           tail: bool = False, grad=None, stream=None):
+    """The gradient of (grad_loss * loss).sum() with respect to logits, from
+    the stats of specv_distill on the same inputs (see include/specv.h)."""
+    import torch
+    lib = load_library()
+    N = logits.shape[0]
+    if grad is None:
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    args = _distill_args(logits, teacher_ids, teacher_logits, teacher_lse, weights, temperature,
+                         tail, grad)
+    args.stats = _of(stats, (N, 4), torch.float32, "stats")
+    args.grad_loss = _of(grad_loss, (N,), torch.float32, "grad_loss")
+    _check(lib.specv_distill_backward(ctypes.byref(args), _stream(stream)))
+    return grad
+
+
+_DistillLoss = None
+
+
+def distill_loss(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temperature: float = 1.0,
+                 weights=None, tail: bool = False):
+    """specv_distill's loss per row [N], differentiable with respect to logits
+    (once: the backward pass is specv_distill_backward)."""
+    global _DistillLoss
+    if _DistillLoss is None:
+        import torch
+
+        class DistillLoss(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, ids, values, lse, temperature, weights, tail):
+                out = specv_distill(logits, ids, values, teacher_lse=lse, temperature=temperature,
+                                    weights=weights, tail=tail)
+                ctx.save_for_backward(logits, ids, values, lse, weights, out["stats"])
+                ctx.how = (temperature, tail)
+                return out["loss"]
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, up):
+                logits, ids, values, lse, weights, stats = ctx.saved_tensors
+                temperature, tail = ctx.how
+                grad = specv_distill_backward(logits, ids, values, stats, teacher_lse=lse,
+                                              grad_loss=up.to(torch.float32).contiguous(),
+                                              temperature=temperature, weights=weights, tail=tail)
+                return grad, None, None, None, None, None, None
+
+        _DistillLoss = DistillLoss
+    return _DistillLoss.apply(logits, teacher_ids, teacher_logits, teacher_lse, temperature, weights,
+                              tail)

@@ -5,6 +5,7 @@
 
 #include "specv.h"
 #include "decide_kernel.cuh"
+#include "filter_kernel.cuh"
 
 namespace specv {
 
@@ -24,6 +25,13 @@ cudaError_t launch_sample_rows(int dtype, int64_t rows, size_t smem, cudaStream_
 cudaError_t launch_predict_keys(const PredictKeysParams& kp, int B, cudaStream_t s);
 cudaError_t launch_check_hit(int B, int K, int F, const int32_t* keys, const int32_t* accept_len,
                              const int32_t* out_tokens, uint8_t* hit, cudaStream_t s);
+
+// A cluster per row (P.sp.C CTAs), `smem` bytes of dynamic shared memory.
+cudaError_t launch_sample_filter(int dtype, size_t smem, cudaStream_t s, const FilterParams& p);
+cudaError_t launch_top_logits(int dtype, size_t smem, cudaStream_t s, const TopParams& p);
+cudaError_t launch_distill(int dtype, size_t smem, cudaStream_t s, const DistillParams& p);
+// A CTA per chunk of a row.
+cudaError_t launch_distill_backward(int dtype, cudaStream_t s, const DistillParams& p);
 
 #define SPECV_LAUNCHERS(MODE, EXT)                                                             \
   EXT template cudaError_t launch_stats<MODE>(int, bool, bool, int, int64_t, cudaStream_t,   \

@@ -65,6 +65,28 @@ cudaError_t launch_dependent(Kern k, int64_t blocks, size_t smem, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, k, p);
 }
 
+// One cluster of C CTAs of kRowThreads per row.
+template <typename Kern, typename Params>
+cudaError_t launch_rows(Kern k, int C, int64_t rows, size_t smem, cudaStream_t stream, const Params& p) {
+  cudaError_t e = allow_cluster(k, C);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * C), 1, 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
 template <typename Kern, typename Params>
 cudaError_t launch_plain(Kern k, int64_t blocks, size_t smem, cudaStream_t s, const Params& p) {
   if (smem > 0) {  // static + dynamic shared memory may pass the 48 KB default

@@ -1,0 +1,252 @@
+// C ABI of the operators that hold a row on chip (filtered sampling, top
+// logits, distillation): argument checks, the row's split over a cluster, and
+// the launch on the caller's stream.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api.cuh"
+#include "launch.cuh"
+
+using namespace specv;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int elem_bytes(int32_t dtype) { return dtype == SPECV_BF16 ? 2 : 4; }
+
+// Rows of a [B, R, ...] layout start 16-byte aligned.
+bool rows_aligned(const void* base, int64_t bs, int64_t rs, int es) {
+  return aligned(base, 16) && (bs * es) % 16 == 0 && (rs * es) % 16 == 0;
+}
+
+specv_status check_rows(const char* what, int32_t n, int32_t V, int32_t dtype) {
+  if (n < 0) return api_fail(SPECV_ERR_INVALID_ARG, "%s=%d < 0", what, n);
+  if (V < 1) return api_fail(SPECV_ERR_INVALID_ARG, "V=%d < 1", V);
+  if (dtype != SPECV_BF16 && dtype != SPECV_FP32)
+    return api_fail(SPECV_ERR_INVALID_ARG, "dtype=%d is not SPECV_BF16 or SPECV_FP32", dtype);
+  return SPECV_OK;
+}
+
+constexpr size_t kSmemSm = 228 * 1024, kSmemCta = 227 * 1024, kSmemReserved = 1024;
+
+// The row's split over a cluster of C CTAs (a power of two) whose slices stay
+// in shared memory beside `extra` bytes per CTA.  C is the smallest for which
+// two CTAs fit an SM (one row's copies then run under the other's passes),
+// and more while rows are too few to fill the SMs.  False: V does not fit.
+bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, bool vec, RowSplit& sp, size_t& smem) {
+  const int vw = 16 / elem_bytes(dtype);
+  const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
+  const int64_t two = static_cast<int64_t>(kSmemSm / 2 - kSmemReserved - extra);
+  const int64_t one = static_cast<int64_t>(kSmemCta - extra);
+  auto slice = [&](int C) { return (nvec + C - 1) / C * 16; };
+  int C = 1;
+  while (C < 8 && slice(C) > two) C *= 2;
+  if (slice(C) > one) C = 16;
+  if (slice(C) > one) return false;
+  while (C < 8 && rows * C < api_sm_count() && slice(C) >= 32768) C *= 2;
+  sp.V = V;
+  sp.C = C;
+  sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
+  sp.gvec = (sp.svec + kRowWarps - 1) / kRowWarps;
+  sp.aligned = vec;
+  smem = static_cast<size_t>(sp.svec) * 16;
+  return true;
+}
+
+// 2^(j/64) as an fp32 value and the relative remainder.
+PairTable make_table() {
+  PairTable t;
+  for (int j = 0; j < kGrid; ++j) {
+    const double x = std::exp2(j / static_cast<double>(kGrid));
+    t.e[j].x = static_cast<float>(x);
+    t.e[j].y = static_cast<float>((x - static_cast<double>(t.e[j].x)) / static_cast<double>(t.e[j].x));
+  }
+  return t;
+}
+
+specv_status launched(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) return api_fail(SPECV_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+  return api_done(1);
+}
+
+}  // namespace
+
+extern "C" {
+
+specv_status specv_sample(const specv_sample_args* a, void* stream) {
+  api_done(0);
+  if (!a) return api_fail(SPECV_ERR_INVALID_ARG, "args is NULL");
+  const int32_t B = a->B, R = a->R, V = a->V;
+  specv_status st = check_rows("B", B, V, a->dtype);
+  if (st != SPECV_OK) return st;
+  if (R < 1) return api_fail(SPECV_ERR_INVALID_ARG, "R=%d < 1", R);
+  if ((a->uniforms == nullptr) != (a->tokens == nullptr))
+    return api_fail(SPECV_ERR_INVALID_ARG, "uniforms and tokens are given together");
+  if (!a->tokens && !a->filtered) return api_fail(SPECV_ERR_INVALID_ARG, "neither tokens nor filtered is given");
+  if (a->prob && !a->tokens) return api_fail(SPECV_ERR_INVALID_ARG, "prob needs tokens");
+  if (B == 0) return api_done(0);
+  if (!a->logits || !a->temperature) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  const int es = elem_bytes(a->dtype);
+  if (!aligned(a->logits, es) || !aligned(a->filtered, es) || !aligned(a->temperature, 4) || !aligned(a->top_k, 4) ||
+      !aligned(a->top_p, 4) || !aligned(a->min_p, 4) || !aligned(a->uniforms, 4) || !aligned(a->tokens, 4) ||
+      !aligned(a->prob, 4) || !aligned(a->kept, 4) || !aligned(a->row_status, 4))
+    return api_fail(SPECV_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  if (a->row_stride < V || (a->filtered && a->filtered_row_stride < V))
+    return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
+  if (B > 1 && (a->batch_stride < (R - 1) * a->row_stride + V ||
+                (a->filtered && a->filtered_batch_stride < (R - 1) * a->filtered_row_stride + V)))
+    return api_fail(SPECV_ERR_INVALID_ARG, "batch stride too small for %d rows", R);
+  const int64_t rows = static_cast<int64_t>(B) * R;
+  FilterParams p = {};
+  size_t smem;
+  if (!split_row(rows, V, a->dtype, sizeof(FilterShared), rows_aligned(a->logits, a->batch_stride, a->row_stride, es),
+                 p.sp, smem))
+    return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
+  if (rows * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B*R too large");
+  p.rows = static_cast<int32_t>(rows);
+  p.R = R;
+  p.z = a->logits;
+  p.bs = a->batch_stride;
+  p.rs = a->row_stride;
+  p.temp = a->temperature;
+  p.top_k = a->top_k;
+  p.top_p = a->top_p;
+  p.min_p = a->min_p;
+  p.u = a->uniforms;
+  p.tokens = a->tokens;
+  p.prob = a->prob;
+  p.kept = a->kept;
+  p.out = a->filtered;
+  p.obs = a->filtered_batch_stride;
+  p.ors = a->filtered_row_stride;
+  p.oaligned = a->filtered && rows_aligned(a->filtered, a->filtered_batch_stride, a->filtered_row_stride, es);
+  p.status = a->row_status;
+  static const PairTable table = make_table();
+  p.tab = table;
+  return launched(launch_sample_filter(a->dtype, smem, static_cast<cudaStream_t>(stream), p), "sample");
+}
+
+specv_status specv_top_logits(const specv_top_args* a, void* stream) {
+  api_done(0);
+  if (!a) return api_fail(SPECV_ERR_INVALID_ARG, "args is NULL");
+  const int32_t B = a->B, V = a->V, k = a->k;
+  specv_status st = check_rows("B", B, V, a->dtype);
+  if (st != SPECV_OK) return st;
+  if (k < 1 || k > SPECV_MAX_TOP) return api_fail(SPECV_ERR_INVALID_ARG, "k=%d outside [1, %d]", k, SPECV_MAX_TOP);
+  if (!(a->temperature >= 1e-3f && a->temperature <= 1e3f))
+    return api_fail(SPECV_ERR_INVALID_ARG, "temperature=%g outside [1e-3, 1e3]", static_cast<double>(a->temperature));
+  if (B == 0) return api_done(0);
+  if (!a->logits || !a->ids || !a->values) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  const int es = elem_bytes(a->dtype);
+  if (!aligned(a->logits, es) || !aligned(a->ids, 4) || !aligned(a->values, 4) || !aligned(a->lse, 4) ||
+      !aligned(a->row_status, 4))
+    return api_fail(SPECV_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  if (a->row_stride < V) return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
+  TopParams p = {};
+  size_t smem;
+  if (!split_row(B, V, a->dtype, sizeof(FilterShared), rows_aligned(a->logits, 0, a->row_stride, es), p.sp, smem))
+    return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
+  if (static_cast<int64_t>(B) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B too large");
+  p.rows = B;
+  p.k = k;
+  p.z = a->logits;
+  p.rs = a->row_stride;
+  p.T = a->temperature;
+  p.ids = a->ids;
+  p.values = a->values;
+  p.lse = a->lse;
+  p.status = a->row_status;
+  return launched(launch_top_logits(a->dtype, smem, static_cast<cudaStream_t>(stream), p), "top-logits");
+}
+
+}  // extern "C"
+
+namespace {
+
+specv_status check_distill(const specv_distill_args* a) {
+  if (!a) return api_fail(SPECV_ERR_INVALID_ARG, "args is NULL");
+  const int32_t N = a->N, V = a->V, K = a->K;
+  specv_status st = check_rows("N", N, V, a->dtype);
+  if (st != SPECV_OK) return st;
+  if (K < 1 || K > SPECV_MAX_TOP) return api_fail(SPECV_ERR_INVALID_ARG, "K=%d outside [1, %d]", K, SPECV_MAX_TOP);
+  if (!(a->temperature >= 1e-3f && a->temperature <= 1e3f))
+    return api_fail(SPECV_ERR_INVALID_ARG, "temperature=%g outside [1e-3, 1e3]", static_cast<double>(a->temperature));
+  if (a->flags & ~SPECV_DISTILL_TAIL) return api_fail(SPECV_ERR_INVALID_ARG, "unknown flags 0x%x", a->flags);
+  if ((a->flags & SPECV_DISTILL_TAIL) && N > 0 && !a->teacher_lse)
+    return api_fail(SPECV_ERR_INVALID_ARG, "SPECV_DISTILL_TAIL needs teacher_lse");
+  if (N == 0) return SPECV_OK;
+  if (!a->logits || !a->teacher_ids || !a->teacher_logits)
+    return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  const int es = elem_bytes(a->dtype);
+  if (!aligned(a->logits, es) || !aligned(a->grad, es) || !aligned(a->teacher_ids, 4) || !aligned(a->teacher_logits, 4) ||
+      !aligned(a->teacher_lse, 4) || !aligned(a->weights, 4) || !aligned(a->loss, 4) || !aligned(a->grad_loss, 4) ||
+      !aligned(a->row_status, 4))
+    return api_fail(SPECV_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  if (!aligned(a->stats, 16)) return api_fail(SPECV_ERR_INVALID_ARG, "stats is not 16-byte aligned");
+  if (a->row_stride < V || (a->grad && a->grad_row_stride < V))
+    return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
+  if (a->teacher_stride < K) return api_fail(SPECV_ERR_INVALID_ARG, "teacher_stride smaller than K");
+  return SPECV_OK;
+}
+
+DistillParams distill_params(const specv_distill_args* a) {
+  const int es = elem_bytes(a->dtype);
+  DistillParams p = {};
+  p.N = a->N;
+  p.K = a->K;
+  p.z = a->logits;
+  p.rs = a->row_stride;
+  p.ids = a->teacher_ids;
+  p.tl = a->teacher_logits;
+  p.ts = a->teacher_stride;
+  p.tlse = a->teacher_lse;
+  p.weight = a->weights;
+  p.T = a->temperature;
+  p.tail = (a->flags & SPECV_DISTILL_TAIL) != 0;
+  p.stats = reinterpret_cast<float4*>(a->stats);
+  p.grad = a->grad;
+  p.grs = a->grad_row_stride;
+  p.galigned = a->grad && rows_aligned(a->grad, 0, a->grad_row_stride, es);
+  p.sp.V = a->V;
+  p.sp.aligned = rows_aligned(a->logits, 0, a->row_stride, es);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+specv_status specv_distill(const specv_distill_args* a, void* stream) {
+  api_done(0);
+  specv_status st = check_distill(a);
+  if (st != SPECV_OK) return st;
+  if (a->N == 0) return api_done(0);
+  if (!a->loss) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (a->grad_loss) return api_fail(SPECV_ERR_INVALID_ARG, "grad_loss belongs to specv_distill_backward");
+  DistillParams p = distill_params(a);
+  size_t smem;
+  const size_t extra = static_cast<size_t>(a->K) * 20;
+  if (!split_row(a->N, a->V, a->dtype, extra + kSmemReserved, p.sp.aligned != 0, p.sp, smem))
+    return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
+  if (static_cast<int64_t>(a->N) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
+  p.loss = a->loss;
+  p.status = a->row_status;
+  return launched(launch_distill(a->dtype, smem + extra, static_cast<cudaStream_t>(stream), p), "distill");
+}
+
+specv_status specv_distill_backward(const specv_distill_args* a, void* stream) {
+  api_done(0);
+  specv_status st = check_distill(a);
+  if (st != SPECV_OK) return st;
+  if (a->N == 0) return api_done(0);
+  if (!a->stats || !a->grad) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (static_cast<int64_t>(a->N) * ((a->V - 1) / (kRowThreads * kBackVecs * (16 / elem_bytes(a->dtype))) + 1) > 0x7fffffffLL)
+    return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
+  DistillParams p = distill_params(a);
+  p.gloss = a->grad_loss;
+  return launched(launch_distill_backward(a->dtype, static_cast<cudaStream_t>(stream), p), "distill-backward");
+}
+
+}  // extern "C"

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "specv.h"
+#include "api.cuh"
 #include "launch.cuh"
 
 using namespace specv;
@@ -40,6 +41,28 @@ specv_status ok() {
   g_err.clear();
   return SPECV_OK;
 }
+
+}  // namespace
+
+namespace specv {
+
+specv_status api_fail(specv_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+
+specv_status api_done(int32_t launches) {
+  g_launches = launches;
+  return ok();
+}
+
+}  // namespace specv
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -123,7 +146,9 @@ struct Plan {
 // at 8 (12: 0.4140 -> 0.4152 ms).
 constexpr int kTopFIters = 12;
 
-int sm_count() {
+}  // namespace
+
+int specv::api_sm_count() {
   static const int n = [] {
     int dev = 0, c = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -133,6 +158,10 @@ int sm_count() {
   }();
   return n;
 }
+
+namespace {
+
+int sm_count() { return api_sm_count(); }
 
 // min_cb: the smallest cluster; an MSS node may stream its rows once per
 // rejection, and two CTAs per node halve each pass (measured best at 2048
