@@ -27,7 +27,8 @@ struct DistillParams {
   const float* tlse;    // or NULL
   const float* weight;  // or NULL
   const float* gloss;   // backward: upstream gradient per row, or NULL
-  float T;
+  double invT;          // 1 / T
+  float c;              // log2(e) / T
   int32_t tail;
   float* loss;
   float4* stats;        // (max logit, alpha / sum, log(beta q / p) - (z - t) / T, L), sum =
@@ -108,17 +109,24 @@ __device__ __forceinline__ float same_id(const int32_t* ids, const float* p, int
   return warp_sum_f(s);
 }
 
-// Block-wide sum of doubles (every thread gets it); `scratch`: kRowWarps.
-__device__ __forceinline__ double block_sum_d(double x, double* scratch) {
-  x = warp_sum_d(x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
-  __syncthreads();
-  double s = 0;
+// Block-wide sum of entries of size up to about 1 (threads from K on hold
+// none), exact in units of 2^-40: fp64 sums would cost a block microseconds.
+__device__ __forceinline__ uint64_t block_sum_fixed(float x, int K, uint64_t* scratch) {
+  uint64_t v = 0;
+  if ((threadIdx.x & ~31u) < static_cast<unsigned>(K)) {
+    v = __float2ull_rn(x * 1099511627776.f);
 #pragma unroll
-  for (int w = 0; w < kRowWarps; ++w) s += scratch[w];
-  return s;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kRowWarps; ++w) v += scratch[w];
+  return v;
 }
+constexpr double kFixedUnit = 9.094947017729282e-13;  // 2^-40
 
 __device__ __forceinline__ float block_max_nan(float x, float* scratch) {
 #pragma unroll
@@ -146,6 +154,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   __shared__ uint64_t bars[kRowWarps];
   __shared__ float fred[kRowWarps];
   __shared__ double dred[kRowWarps];
+  __shared__ uint64_t ured[kRowWarps];
+  __shared__ float rred[kRowWarps], lred[kRowWarps];
+  __shared__ double row_L;
   __shared__ DistillPart part[kMaxCluster];
   __shared__ int badbits, row_dead;
   __shared__ float row_max, row_alpha, row_beta;
@@ -169,10 +180,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   float* pj = tl + K;
   float* zj = pj + K;
   float* sj = zj + K;  // p of the entry's id, or -1: not its first entry
-  const double invT = 1.0 / static_cast<double>(P.T);
-  const float c = static_cast<float>(1.4426950408889634 * invT);
+  const double invT = P.invT;
+  const float c = P.c;
   int bad = 0;
-  double L = 0, m = 0;
+  double L = 0;
+  uint64_t mass = 0;  // sum of p, in units of 2^-40
   if (!skip) {
     // the teacher's entries, in every CTA
     float tmax = neg_inf();
@@ -191,17 +203,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
       L = P.tlse[row];
       if (!isfinite(L)) bad |= kNonFinite;
     } else if (tmax > neg_inf()) {
-      double s = 0;
+      float s = 0;
       for (int j = threadIdx.x; j < K; j += kRowThreads)
-        s += exp_d((static_cast<double>(tl[j]) - tmax) * invT);
-      L = tmax * invT + log(block_sum_d(s, dred));
+        s += exp_d((static_cast<double>(tl[j]) - static_cast<double>(tmax)) * invT);
+      const uint64_t all = block_sum_fixed(s, K, ured);
+      if (threadIdx.x == 0) row_L = static_cast<double>(tmax) * invT + log(static_cast<double>(all) * kFixedUnit);
+      __syncthreads();
+      L = row_L;
     }
+    float p_sum = 0.f;
     for (int j = threadIdx.x; j < K; j += kRowThreads) {
       const float p = tl[j] > neg_inf() ? exp_d(static_cast<double>(tl[j]) * invT - L) : 0.f;
       pj[j] = p;
-      m += p;
+      p_sum += p;
     }
-    m = block_sum_d(m, dred);  // (also: ids and pj are in place)
+    mass = block_sum_fixed(fminf(p_sum, 1e6f), K, ured);  // (also: ids and pj are in place)
     if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
   }
   const float mc = block_max_nan(skip ? 0.f : sl.warp_max(), fred);
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
       __syncwarp();
       if (lane == 0) {
         if (pj[j] > 0.f)
-          a += static_cast<double>(pj[j]) * (static_cast<double>(tl[j]) * invT - L - static_cast<double>(z) * invT);
+          a += static_cast<double>(pj[j]) * ((static_cast<double>(tl[j]) - static_cast<double>(z)) * invT - L);
         zj[j] = z;
         sj[j] = first ? ps : -1.f;
       }
@@ -245,15 +261,28 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   __syncthreads();
   if (!skip) sl.each([&](float z, int) { rest += ex2((z - mref) * c); });
   if (bad) atomicOr(&badbits, bad);
-  const double rest_c = block_sum_d(rest, dred), listed_c = block_sum_d(listed, dred), a_c = block_sum_d(a, dred);
+  rest = warp_sum_f(rest);
+  listed = warp_sum_f(listed);
+  if (lane == 0) {
+    rred[warp] = rest;
+    lred[warp] = listed;
+    dred[warp] = a;
+  }
+  __syncthreads();
   cluster_wait();
-  DistillPart mine;
-  mine.m = mc;
-  mine.rest = static_cast<float>(rest_c);
-  mine.listed = static_cast<float>(listed_c);
-  mine.bad = badbits;
-  mine.a = a_c;
-  push_all(part, rank, C, mine);
+  if (static_cast<int>(threadIdx.x) < C) {
+    DistillPart mine;
+    mine.m = mc;
+    mine.rest = mine.listed = 0.f;
+    mine.a = 0;
+    mine.bad = badbits;
+    for (int w = 0; w < kRowWarps; ++w) {
+      mine.rest += rred[w];
+      mine.listed += lred[w];
+      mine.a += dred[w];
+    }
+    *peer(part + rank, static_cast<int>(threadIdx.x)) = mine;
+  }
   cluster_sync();
 
   if (threadIdx.x == 0) {  // the row's scalars, once per CTA (64-bit arithmetic is slow)
@@ -272,6 +301,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
       A += part[r].a;
     }
     const bool dead = skip || anybad || !finite;
+    const double m = static_cast<double>(mass) * kFixedUnit;
     const double total = S_rest + S_listed;
     const double r = P.tail ? (1.0 - m < kNoTail ? 0.0 : 1.0 - m) : 0.0;
     double alpha = m, beta = m;
@@ -348,8 +378,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(const Dis
   const float wt = (P.weight ? P.weight[row] : 1.f);
   const float up = P.gloss ? P.gloss[row] : 1.f;
   const bool dead = wt == 0.f || st.w != st.w;
-  const double invT = 1.0 / static_cast<double>(P.T);
-  const float c = static_cast<float>(1.4426950408889634 * invT);
+  const double invT = P.invT;
+  const float c = P.c;
   const float f = dead ? 0.f : static_cast<float>(wt * static_cast<double>(up) * invT);
   const float ga = f * st.y;
   const int64_t i0 = static_cast<int64_t>(chunk) * kRowThreads * kBackVecs * E::VW;

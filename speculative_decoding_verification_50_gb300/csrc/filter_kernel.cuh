@@ -10,12 +10,14 @@
 //
 // Whole numbers come out of these sums (the cut, the token), so weights are
 // pairs of fp32: 2^(E/64) from a table, exact to fp32, and the rest to first
-// order apart, about 2^-30 relative together; totals are held in 64 bits.  A
+// order apart, about 2^-30 relative together; totals are 64-bit integers in
+// units of 2^-fbits of the largest weight (an SM does two fp64 operations a
+// clock: a block's reductions in fp64 cost more than its passes over the row).  A
 // sum in plain fp32 moves the cut of a flat distribution in one row of a
 // hundred.
 #pragma once
 
-#include "distill_kernel.cuh"  // store_vec, block_sum_d
+#include "distill_kernel.cuh"  // store_vec, block_max_nan
 
 namespace specv {
 
@@ -59,7 +61,8 @@ struct TopParams {
   int32_t rows, k;
   const void* z;
   int64_t rs;
-  float T;
+  double invT;   // 1 / T
+  float c;       // log2(e) / T
   int32_t* ids;
   float* values;
   float* lse;
@@ -81,8 +84,7 @@ struct Scale {
   float shift, chi, clo;
   int gm;
 
-  __device__ void set(float m, float T) {
-    const double c = 1.4426950408889634074 / static_cast<double>(T);
+  __device__ void set(float m, double c) {  // c = log2(e) / T
     chi = static_cast<float>(c);
     clo = static_cast<float>(c - static_cast<double>(chi));
     // |y| stays within the rounding trick's range; shifted logits are exact
@@ -130,10 +132,17 @@ struct PairSum {
     a = s;
     b = t;
   }
-  __device__ __forceinline__ double value() const {
-    return (static_cast<double>(a) - 4.0) + ((static_cast<double>(b) - 4.0) + static_cast<double>(c));
+  __device__ __forceinline__ uint64_t fixed(float unit) const {  // unit = 2^fbits
+    return static_cast<uint64_t>(__float2ll_rn((a - 4.f) * unit) + __float2ll_rn((b - 4.f) * unit) +
+                                 __float2ll_rn(c * unit));
   }
 };
+
+__device__ __forceinline__ uint64_t warp_sum_u(uint64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
 
 // What the CTA of rank 0 decides and every CTA reads.
 struct Decision {
@@ -143,8 +152,8 @@ struct Decision {
   uint32_t kmin, kmax;
   int32_t tie_seg, tie_rank;
   int32_t seg;        // the segment the token lies in
-  double rem;         // u W minus what lies before that segment
-  double W;
+  uint64_t rem;       // u W minus what lies before that segment
+  uint64_t W;
   int32_t kept;
   int32_t fallback;
 };
@@ -155,20 +164,24 @@ struct FilterShared {
   uint32_t hist[kCap * 2];   // the CTA's histogram; in rank 0 the gathered keys (8 bytes each)
   uint32_t total[kBins];     // the row's histogram
   float xmax[kMaxCluster];
-  double xsum[kMaxCluster];
+  uint64_t xsum[kMaxCluster];
+  float xexp[kMaxCluster];
   int32_t xbad[kMaxCluster];
   int32_t xidx[kMaxCluster];
-  double scratch[kRowWarps];
+  uint64_t scratch[kRowWarps];
   float fscratch[kRowWarps];
   int32_t iscratch[kRowWarps];
   // rank 0: per segment of the row
-  double segsum[kMaxSegs];
+  uint64_t segsum[kMaxSegs];
   int32_t segabove[kMaxSegs], segband[kMaxSegs];
   uint32_t segkmin[kMaxSegs], segkmax[kMaxSegs];
   int32_t ngather;
   int32_t lo, hi;
-  double before;
+  int32_t before;
   int32_t above;
+  Scale sc;
+  float zf, zt;
+  uint64_t goal;
   Decision dec;
 };
 static_assert(kBins <= kCap * 2, "the histogram fits its array");
@@ -190,6 +203,8 @@ struct FilterRow {
   int rank, C, V, lane, warp;
   float zc;
   int ic;
+  int fbits;    // sums are in units of 2^-fbits, so that V weights stay below 2^62
+  float unit;   // 2^fbits
 
   __device__ FilterRow(FilterShared& s) : S(s) {}
 
@@ -298,7 +313,7 @@ struct FilterRow {
         }
       }
     }
-    const double w = warp_sum_d(acc.value());
+    const uint64_t w = warp_sum_u(acc.fixed(unit));
     above = __reduce_add_sync(0xffffffffu, above);
     band = __reduce_add_sync(0xffffffffu, band);
     kmin = __reduce_min_sync(0xffffffffu, kmin);
@@ -335,22 +350,29 @@ struct FilterRow {
       }
   }
 
+  // Block-wide sum (every thread gets it).
+  __device__ uint64_t block_sum_u(uint64_t x) {
+    x = warp_sum_u(x);
+    __syncthreads();
+    if (lane == 0) S.scratch[warp] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < kRowWarps; ++w) x += S.scratch[w];
+    return x;
+  }
+
   // Rank 0: totals over the segments of the gather before.
-  __device__ void seg_totals(double& w, int& above, int& band) {
+  __device__ void seg_totals(uint64_t& w, int& above, int& band) {
     const int n = C * kRowWarps;
-    double x = 0;
-    int a = 0, b = 0;
+    uint64_t x = 0, y = 0;
     if (static_cast<int>(threadIdx.x) < n) {
       x = S.segsum[threadIdx.x];
-      a = S.segabove[threadIdx.x];
-      b = S.segband[threadIdx.x];
+      y = (static_cast<uint64_t>(S.segabove[threadIdx.x]) << 32) | static_cast<uint32_t>(S.segband[threadIdx.x]);
     }
-    w = block_sum_d(x, S.scratch);
-    int all;
-    block_scan(a, S.iscratch, all);
-    above = all;
-    block_scan(b, S.iscratch, all);
-    band = all;
+    w = block_sum_u(x);
+    y = block_sum_u(y);
+    above = static_cast<int>(y >> 32);
+    band = static_cast<int>(y & 0xffffffffu);
   }
 
   __device__ void publish() {  // rank 0's decision to every CTA
@@ -362,68 +384,67 @@ struct FilterRow {
     cluster_sync();
   }
 
+  // A bin's mass, v counted in 2^-bits of its scale 2^(-d/64).
+  __device__ __forceinline__ uint64_t mass(uint32_t v, int d, int bits) const {
+    const uint32_t t = (__float_as_uint(S.tab[(-d) & (kGrid - 1)].x) << 8) | 0x80000000u;  // 2^31 2^(j/64)
+    const int s = bits + 31 - fbits - ((-d) >> 6);
+    const uint64_t x = static_cast<uint64_t>(v) * t;
+    return s >= 64 ? 0 : s >= 0 ? x >> s : x << -s;
+  }
+
   // Bins -> the band between the first bin where the cut may lie and the
-  // first where it must.  count: the k-th token; else the mass `target` of
-  // weights held in units of 2^-bits per bin scale.  S.before / S.above: mass
-  // and count before the band.  Returns false if the set ends before the cut.
-  __device__ bool find_bins(bool count, int64_t k, double target, int bits, Band& b) {
+  // first where it must.  COUNT: the goal-th token; else the mass `goal`, the
+  // bins' masses being good to 2^-bits.  S.before: the count before the band.
+  // False if the set ends before the goal-th token.
+  template <bool COUNT>
+  __device__ bool find_bins(uint64_t goal, int bits, Band& b) {
     const int b0 = threadIdx.x * kBinsPerThread;
-    uint32_t v[kBinsPerThread];
-    double x = 0;
+    uint64_t v[kBinsPerThread], x = 0;
 #pragma unroll
     for (int q = 0; q < kBinsPerThread; ++q) {
-      v[q] = b0 + q < kBins ? S.total[b0 + q] : 0u;
-      x += v[q] ? unit(count, b0 + q, bits) * v[q] : 0.0;
+      const uint32_t n = b0 + q < kBins ? S.total[b0 + q] : 0u;
+      v[q] = COUNT ? n : mass(n, b0 + q, bits);
+      x += v[q];
     }
-    double all;
-    double run = block_scan(x, S.scratch, all);
-    const double start = run;
-    const double slack = count ? 0.0 : ldexp(1.0, -bits);
-    const double goal = count ? static_cast<double>(k) : target;
-    if (count && all < goal) return false;
+    uint64_t all;
+    uint64_t run = block_scan(x, S.scratch, all);
+    if (COUNT && all < goal) return false;
 #pragma unroll
     for (int q = 0; q < kBinsPerThread; ++q) {
-      if (b0 + q >= kBins) break;
-      run += v[q] ? unit(count, b0 + q, bits) * v[q] : 0.0;
-      if (v[q] && run * (1.0 + slack) >= goal) atomicMin(&S.lo, b0 + q);
-      if (v[q] && run * (1.0 - slack) >= goal) atomicMin(&S.hi, b0 + q);
+      const uint64_t before = run;
+      run += v[q];
+      const uint64_t slack = COUNT ? 0 : (run >> bits) + 1;
+      if (v[q] && run + slack >= goal) {
+        if (COUNT && before < goal) S.before = static_cast<int32_t>(before);
+        atomicMin(&S.lo, b0 + q);
+      }
+      if (v[q] && run - slack >= goal) {
+        atomicMin(&S.hi, b0 + q);
+        break;
+      }
     }
     __syncthreads();
     b.by_key = false;
     b.lo = S.lo == INT_MAX ? kBins - 1 : S.lo;
     b.hi = S.hi == INT_MAX ? kBins - 1 : S.hi;
-    // the count before the band (exact in count mode, unused otherwise)
-    if (b.lo >= b0 && b.lo < b0 + kBinsPerThread) {
-      double r = start;
-#pragma unroll
-      for (int q = 0; q < kBinsPerThread; ++q)
-        if (b0 + q < b.lo) r += v[q] ? unit(count, b0 + q, bits) * v[q] : 0.0;
-      S.before = r;
-    }
     // 64 y >= gm - hi - 1/2 for every token of the band, with room for rounding
-    const double y = (static_cast<double>(sc.gm) - b.hi - 0.5) / kGrid;
-    const double e = static_cast<double>(sc.shift) + y / (static_cast<double>(sc.chi) + sc.clo);
-    b.edge = static_cast<float>(e - 1e-6 * (fabs(e) + fabs(static_cast<double>(sc.shift))) - 1e-30);
-    if (b.hi >= kBins - 1) b.edge = neg_inf();
+    const float e = sc.shift + (static_cast<float>(sc.gm - b.hi) - 0.5f) / (static_cast<float>(kGrid) * sc.chi);
+    b.edge = b.hi >= kBins - 1 ? kNegMax : fmaxf(e - 1e-6f * (fabsf(e) + fabsf(sc.shift)) - 1e-30f, kNegMax);
     __syncthreads();
     return true;
   }
 
-  __device__ double unit(bool count, int d, int bits) const {
-    return count ? 1.0 : ldexp(static_cast<double>(S.tab[(-d) & (kGrid - 1)].x), ((-d) >> 6) - bits);
-  }
-
-  __device__ double exact_weight(float z) const {
+  __device__ uint64_t fixed_weight(float z) const {
     float h, l, g;
     int d;
     sc.weight(z, S.tab, h, l, d, g);
-    return static_cast<double>(h) + static_cast<double>(l);
+    return static_cast<uint64_t>(__float2ll_rn(h * unit) + __float2ll_rn(l * unit));
   }
 
   // Narrows a band too full to gather: counts by key over [kmin, kmax] into
-  // 2048 bins.  count: the cut is the r-th token of the band; else the mass
-  // `rem` into it.
-  __device__ void narrow(Band& b, bool count, int64_t r, double rem) {
+  // 2048 bins.  count: the cut is the goal-th token of the band; else the
+  // mass `goal` into it.
+  __device__ void narrow(Band& b, bool count, uint64_t goal) {
     const uint32_t kmin = b.kmin, kmax = b.kmax;
     int shift = 0;
     while (((kmax - kmin) >> shift) >= 2048u) ++shift;
@@ -438,29 +459,29 @@ struct FilterRow {
     merge(2048);
     constexpr int per = 2048 / kRowThreads;
     const int b0 = threadIdx.x * per;
-    double hi_x = 0, lo_x = 0, hw[per], lw[per];
+    uint64_t hi_x = 0, lo_x = 0, hw[per], lw[per];
     for (int q = 0; q < per; ++q) {
       const uint32_t n = S.total[b0 + q];
       const uint32_t top = kmax - (static_cast<uint32_t>(b0 + q) << shift);
       const uint32_t span = (1u << shift) - 1;
       const uint32_t low = top - kmin < span ? kmin : top - span;
-      hw[q] = n == 0 ? 0.0 : count ? n : n * exact_weight(key_value(top));
-      lw[q] = n == 0 ? 0.0 : count ? n : n * exact_weight(key_value(low));
+      hw[q] = n == 0 ? 0 : count ? n : n * (fixed_weight(key_value(top)) + 1);
+      lw[q] = n == 0 ? 0 : count ? n : n * fixed_weight(key_value(low));
       hi_x += hw[q];
       lo_x += lw[q];
     }
-    double all;
-    double hi_run = block_scan(hi_x, S.scratch, all);
-    double lo_run = block_scan(lo_x, S.scratch, all);
-    const double goal = count ? static_cast<double>(r) : rem;
-    const double slack = count ? 0.0 : shift == 0 ? kSlack : 1e-9;
+    uint64_t all;
+    uint64_t hi_run = block_scan(hi_x, S.scratch, all);
+    uint64_t lo_run = block_scan(lo_x, S.scratch, all);
+    const bool exact = count || shift == 0;
     int last = -1;
     for (int q = 0; q < per; ++q) {
       hi_run += hw[q];
       lo_run += lw[q];
-      if (hw[q] > 0) last = b0 + q;
-      if (hw[q] > 0 && hi_run * (1.0 + slack) >= goal) atomicMin(&S.lo, b0 + q);
-      if (hw[q] > 0 && lo_run * (shift == 0 ? 1.0 + slack : 1.0 - slack) >= goal) atomicMin(&S.hi, b0 + q);
+      if (hw[q] == 0) continue;
+      last = b0 + q;
+      if ((exact ? lo_run : hi_run + (hi_run >> 30)) >= goal) atomicMin(&S.lo, b0 + q);
+      if ((exact ? lo_run : lo_run - (lo_run >> 30)) >= goal) atomicMin(&S.hi, b0 + q);
     }
     if (threadIdx.x == 0) S.above = -1;
     __syncthreads();
@@ -483,7 +504,7 @@ struct FilterRow {
   // cut, whose sums give the token as well (min-p's threshold zt is then
   // part of it).  False where min-p ends the kept tokens first: its cut is set,
   // its sums are not.
-  __device__ bool cut(Band b, bool count, int64_t k, double target, bool fin, float zt, const float* u) {
+  __device__ bool cut(Band b, bool count, uint64_t goal, bool fin, float zt, const float* u) {
     for (int it = 0; it < 40; ++it) {  // (each turn shrinks the band; three are the usual most)
       if (fin && b.by_key && order_key(zt) > b.kmax) {
         zc = zt;
@@ -493,12 +514,12 @@ struct FilterRow {
       gather(b, !count || (fin && u != nullptr));
       const int n = *peer(&S.ngather, 0);
       if (n <= kCap) {
-        if (rank == 0) resolve(n, count, k, target, fin, zt, u);
+        if (rank == 0) resolve(n, count, goal, fin, zt, u);
         publish();
         break;
       }
       if (rank == 0) {
-        double w;
+        uint64_t w;
         int above, band;
         seg_totals(w, above, band);
         uint32_t lo = 0xffffffffu, hi = 0;
@@ -512,7 +533,7 @@ struct FilterRow {
           S.dec.kept = above;
           S.dec.W = w;
         }
-        if (lo == hi) resolve_tie(band, above, w, key_value(lo), count, k, target, fin, zt, u);
+        if (lo == hi) resolve_tie(band, above, w, key_value(lo), count, goal, fin, zt, u);
       }
       publish();
       b.kmin = S.dec.kmin;
@@ -521,10 +542,9 @@ struct FilterRow {
         find_tie(key_value(b.kmin));
         break;
       }
-      const int64_t above = S.dec.kept;
-      const double w = S.dec.W;
+      const uint64_t before = count ? static_cast<uint64_t>(S.dec.kept) : S.dec.W;
       __syncthreads();
-      narrow(b, count, k - above, target - w);
+      narrow(b, count, goal > before ? goal - before : 0);
     }
     zc = S.dec.zc;
     ic = S.dec.ic;
@@ -532,9 +552,9 @@ struct FilterRow {
   }
 
   // Rank 0, the band gathered: where the cut falls in it.
-  __device__ void resolve(int n, bool count, int64_t k, double target, bool fin, float zt, const float* u) {
+  __device__ void resolve(int n, bool count, uint64_t goal, bool fin, float zt, const float* u) {
     uint64_t* list = reinterpret_cast<uint64_t*>(S.hist);
-    double w;
+    uint64_t w;
     int above, band;
     seg_totals(w, above, band);
     sort(n);
@@ -542,22 +562,22 @@ struct FilterRow {
     __syncthreads();
     int nb;
     if (count) {
-      nb = min(static_cast<int>(k - above), n);
+      nb = min(static_cast<int>(goal) - above, n);
     } else {
       constexpr int per = kCap / kRowThreads;
       const int i0 = threadIdx.x * per;
-      double v[per], x = 0;
+      uint64_t v[per], x = 0;
 #pragma unroll
       for (int q = 0; q < per; ++q) {
-        v[q] = i0 + q < n ? exact_weight(key_value(~static_cast<uint32_t>(list[i0 + q] >> 32))) : 0.0;
+        v[q] = i0 + q < n ? fixed_weight(key_value(~static_cast<uint32_t>(list[i0 + q] >> 32))) : 0;
         x += v[q];
       }
-      double all;
-      double run = w + block_scan(x, S.scratch, all);
+      uint64_t all;
+      uint64_t run = w + block_scan(x, S.scratch, all);
 #pragma unroll
       for (int q = 0; q < per; ++q) {
         run += v[q];
-        if (i0 + q < n && run * (1.0 + kSlack) >= target) atomicMin(&S.lo, i0 + q);
+        if (i0 + q < n && run >= goal) atomicMin(&S.lo, i0 + q);
       }
       __syncthreads();
       nb = min(S.lo + 1, n);
@@ -584,10 +604,11 @@ struct FilterRow {
 
   // Rank 0, a band of n > kCap equal logits: how many of them are kept, and
   // which segment holds the last one.
-  __device__ void resolve_tie(int n, int above, double w, float z, bool count, int64_t k, double target, bool fin,
-                              float zt, const float* u) {
-    double r = count ? static_cast<double>(k - above) : ceil((target * (1.0 - kSlack) - w) / exact_weight(z));
-    int nb = static_cast<int>(fmin(fmax(r, 1.0), static_cast<double>(n)));
+  __device__ void resolve_tie(int n, int above, uint64_t w, float z, bool count, uint64_t goal, bool fin, float zt,
+                              const float* u) {
+    const uint64_t before = count ? static_cast<uint64_t>(above) : w, one = count ? 1 : fixed_weight(z);
+    const uint64_t left_over = goal > before ? goal - before : 0;
+    int nb = static_cast<int>(min(max((left_over + one - 1) / one, uint64_t(1)), static_cast<uint64_t>(n)));
     if (fin && z < zt) nb = 0;
     if (threadIdx.x == 0) {
       S.dec.tie_seg = -1;
@@ -653,9 +674,8 @@ struct FilterRow {
     const uint64_t* list = reinterpret_cast<const uint64_t*>(S.hist);
     uint64_t* fix = reinterpret_cast<uint64_t*>(S.total);  // free by now
     const int n = C * kRowWarps;
-    const double scale = ldexp(1.0, 62 - (32 - __clz(V)));
     __syncthreads();
-    for (int s = threadIdx.x; s < n; s += kRowThreads) fix[s] = __double2ull_rn(S.segsum[s] * scale);
+    for (int s = threadIdx.x; s < n; s += kRowThreads) fix[s] = S.segsum[s];
     __syncthreads();
     const int seg = sl_segment_size();
     for (int i = threadIdx.x; i < nb; i += kRowThreads) {
@@ -663,10 +683,10 @@ struct FilterRow {
       const int idx = static_cast<int>(list[i] & 0xffffffffu);
       const int cta = idx / cta_size();
       const int s = cta * kRowWarps + (idx - cta * cta_size()) / seg;
-      atomicAdd(reinterpret_cast<unsigned long long*>(&fix[s]), __double2ull_rn(exact_weight(x) * scale));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&fix[s]), fixed_weight(x));
     }
     if (nt > 0 && threadIdx.x == 0) {
-      const uint64_t one = __double2ull_rn(exact_weight(z) * scale);
+      const uint64_t one = fixed_weight(z);
       for (int s = 0; s < n && nt > 0; ++s) {
         const int take = min(nt, S.segband[s]);
         fix[s] += one * static_cast<uint64_t>(take);
@@ -685,9 +705,10 @@ struct FilterRow {
         if (lane >= o) inc += y;
       }
       const uint64_t all = __shfl_sync(0xffffffffu, inc, 31);
-      const double W = static_cast<double>(all) / scale;
-      const double t = static_cast<double>(u) * static_cast<double>(all) * (1.0 + kSlack);
-      const unsigned over = __ballot_sync(0xffffffffu, static_cast<double>(inc) > t);
+      // (whole numbers: run > u W exactly if run > its floor)
+      const uint64_t t =
+          __double2ull_rd(fmax(static_cast<double>(u), 0.0) * static_cast<double>(all) * (1.0 + kSlack));
+      const unsigned over = __ballot_sync(0xffffffffu, u < 1.f && inc > t);
       const unsigned some = __ballot_sync(0xffffffffu, x > 0);
       const bool fell = over == 0;
       const int who = fell ? 31 - __clz(some) : __ffs(over) - 1;
@@ -701,11 +722,11 @@ struct FilterRow {
           at = s;
           before = run;
           run += fix[s];
-          if (!fell && static_cast<double>(run) > t) break;
+          if (!fell && run > t) break;
         }
         S.dec.seg = at;
-        S.dec.rem = fell ? static_cast<double>(pos_inf()) : (t - static_cast<double>(before)) / scale;
-        S.dec.W = W;
+        S.dec.rem = fell ? ~0ull : t - before;
+        S.dec.W = all;
         S.dec.fallback = fell;
       }
     }
@@ -741,6 +762,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   F.sl.load(zrow, P.sp, &S.bars[warp]);
   for (int j = threadIdx.x; j < kGrid; j += kRowThreads) S.tab[j] = P.tab.e[j];
   if (threadIdx.x == 0) S.above = 0;  // (this CTA's error bits, until the exchange)
+  F.fbits = min(44, 62 - (32 - __clz(V)));
+  F.unit = __int_as_float((127 + F.fbits) << 23);
   const float T = P.temp[b];
   const int k = P.top_k ? P.top_k[b] : 0;
   const float tp = P.top_p ? P.top_p[b] : 1.f;
@@ -749,6 +772,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   int bad = 0;
   if (!(T >= 0.f) || T > 3.4e38f) bad |= kBadTemp;
   if (k < 0 || !(tp >= 0.f && tp <= 1.f) || !(mp >= 0.f && mp <= 1.f)) bad |= kBadFilter;
+  // The row's scales in fp64, by one thread while the copies run.
+  double c = 0, tf = 0, tm = 0;
+  if (threadIdx.x == 0) {
+    const double Td = fmaxf(T, 1e-30f), lnf = -kWindow * 0.69314718055994530942;
+    c = 1.4426950408889634074 / Td;
+    tf = Td * lnf;
+    tm = mp > 0.f ? Td * fmax(log(static_cast<double>(mp)), lnf) : tf;
+  }
   __syncthreads();
   if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.above, kTimeout);
   const float mc = block_max_nan(F.sl.warp_max(), S.fscratch);
@@ -794,12 +825,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (P.status) P.status[row] = 0;
     }
   } else {
-    const float Tc = fmaxf(T, 1e-30f);
-    F.sc.set(m, Tc);
-    const double lnf = -kWindow * 0.69314718055994530942;
-    const float zf = __double2float_ru(static_cast<double>(m) + static_cast<double>(Tc) * lnf);
-    const float zt =
-        fmaxf(zf, __double2float_ru(static_cast<double>(m) + static_cast<double>(Tc) * fmax(log(static_cast<double>(mp)), lnf)));
+    if (threadIdx.x == 0) {
+      S.sc.set(m, c);
+      S.zf = __double2float_ru(static_cast<double>(m) + tf);
+      S.zt = fmaxf(S.zf, __double2float_ru(static_cast<double>(m) + tm));
+    }
+    __syncthreads();
+    F.sc = S.sc;
+    const float zf = S.zf, zt = S.zt;
     F.zc = zf;
     F.ic = INT_MAX;
     const bool use_k = k > 0 && k < V, use_p = tp < 1.f;
@@ -825,21 +858,29 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
           }
         }
       });
-      if (!count) push_all(S.xsum, rank, C, block_sum_d(acc.value(), S.scratch));
+      if (!count) push_all(S.xsum, rank, C, F.block_sum_u(acc.fixed(F.unit)));
       __syncthreads();
       F.merge(kBins);
-      double Z = 0;
-      if (!count)
-        for (int r = 0; r < C; ++r) Z += S.xsum[r];
+      uint64_t goal = k;
+      if (!count) {
+        if (threadIdx.x == 0) {
+          uint64_t Z = 0;
+          for (int r = 0; r < C; ++r) Z += S.xsum[r];
+          S.goal = __double2ull_ru(static_cast<double>(tp) * static_cast<double>(Z) * (1.0 - kSlack));
+        }
+        __syncthreads();
+        goal = S.goal;
+      }
       Band band;
-      if (!F.find_bins(count, k, static_cast<double>(tp) * Z, bits, band)) continue;  // fewer than k
+      if (!(count ? F.template find_bins<true>(goal, bits, band) : F.template find_bins<false>(goal, bits, band)))
+        continue;  // fewer than k
       const bool fin = !count || !use_p;
       if (fin && dt < band.lo) {  // min-p ends the kept tokens before the cut
         F.zc = zt;
         F.ic = INT_MAX;
         continue;
       }
-      done = F.cut(band, count, k, static_cast<double>(tp) * Z, fin, zt, u) && fin;
+      done = F.cut(band, count, goal, fin, zt, u) && fin;
     }
     if (!done) {  // no cut by bins: the tokens above min-p's threshold, if that is higher
       if (zt > F.zc) {
@@ -853,7 +894,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       all.edge = F.zc;
       F.gather(all, u != nullptr);
       if (rank == 0) {
-        double w;
+        uint64_t w;
         int above, none;
         F.seg_totals(w, above, none);
         if (threadIdx.x == 0) S.dec.kept = above;
@@ -869,47 +910,44 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   }
 
   if (pick) {  // one warp of the cluster
-    const double rem = S.dec.rem;
-    double run = 0;
+    const uint64_t rem = S.dec.rem;
+    uint64_t run = 0;
     int last = -1, token = -1;
     float lastz = 0.f, tz = 0.f;
     for (int j0 = 0; j0 < F.sl.nv; j0 += 32) {
       const int j = j0 + lane;
       const int i0 = static_cast<int>(F.sl.base) + (F.sl.v0 + j) * E::VW;
       float z[E::VW];
-      double w[E::VW], x = 0;
+      uint64_t w[E::VW], x = 0;
       if (j < F.sl.nv) E::unpack(F.sl.data[F.sl.v0 + j], z);
 #pragma unroll
       for (int q = 0; q < E::VW; ++q) {
         const bool in = j < F.sl.nv && F.in_set(z[q], i0 + q);
-        w[q] = in ? F.exact_weight(z[q]) : 0.0;
+        w[q] = in ? F.fixed_weight(z[q]) : 0;
         x += w[q];
         if (in) {
           last = i0 + q;
           lastz = z[q];
         }
       }
-      double inc = x;
+      uint64_t inc = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, inc, o);
+        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
       }
       const unsigned over = __ballot_sync(0xffffffffu, x > 0 && run + inc > rem);
       if (over) {
         const int who = __ffs(over) - 1;
         if (lane == who) {
-          double y = run + inc - x;
-          token = last;
-          tz = lastz;
+          uint64_t y = run + inc;
 #pragma unroll
-          for (int q = E::VW - 1; q >= 0; --q) {  // the first whose sum passes: scanned from the end
-            double s = y;
-            for (int e = 0; e <= q; ++e) s += w[e];
-            if (w[q] > 0 && s > rem) {
+          for (int q = E::VW - 1; q >= 0; --q) {  // the first whose sum passes: from the end
+            if (w[q] > 0 && y > rem) {
               token = i0 + q;
               tz = z[q];
             }
+            y -= w[q];
           }
         }
         token = __shfl_sync(0xffffffffu, token, who);
@@ -926,7 +964,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     }
     if (lane == 0) {
       P.tokens[row] = token;
-      if (P.prob) P.prob[row] = static_cast<float>(F.exact_weight(tz) / S.dec.W);
+      if (P.prob) P.prob[row] = static_cast<float>(static_cast<double>(F.fixed_weight(tz)) / static_cast<double>(S.dec.W));
     }
   }
 
@@ -997,23 +1035,30 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   F.sc.gm = 0;
   F.zc = kNegMax;
   F.ic = INT_MAX;
+  F.fbits = 0;
+  F.unit = 1.f;
   F.clear_hist(kBins);
-  const float c = static_cast<float>(1.4426950408889634 / static_cast<double>(P.T));
+  const float c = P.c;
   float s = 0.f;
   F.sl.each([&](float z, int) {
     s += ex2((z - m) * c);
     if (z >= kNegMax) atomicAdd(&S.hist[max(F.sc.template bin<true>(z), 0)], 1u);
   });
-  push_all(S.xsum, rank, C, block_sum_d(s, S.scratch));
+  s = warp_sum_f(s);
+  if (lane == 0) S.fscratch[warp] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int w = 0; w < kRowWarps; ++w) s += S.fscratch[w];
+  push_all(S.xexp, rank, C, s);
   __syncthreads();
   F.merge(kBins);
   Band band;
-  if (!F.find_bins(true, k, 0.0, 0, band)) {
+  if (!F.template find_bins<true>(k, 0, band)) {
     band.by_key = false;
     band.hi = kBins - 1;
     band.edge = kNegMax;
   } else if (S.before + S.total[band.hi] > kCap) {
-    F.cut(band, true, k, 0.0, false, kNegMax, nullptr);
+    F.cut(band, true, k, false, kNegMax, nullptr);
     F.clear_hist(0);
     cluster_sync();
     band.by_key = false;
@@ -1032,8 +1077,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   }
   if (threadIdx.x == 0) {
     double t = 0;
-    for (int r = 0; r < C; ++r) t += S.xsum[r];
-    if (P.lse) P.lse[row] = static_cast<float>(static_cast<double>(m) / static_cast<double>(P.T) + log(t));
+    for (int r = 0; r < C; ++r) t += S.xexp[r];
+    if (P.lse) P.lse[row] = static_cast<float>(static_cast<double>(m) * P.invT + log(t));
     if (P.status) P.status[row] = 0;
   }
 }

@@ -153,7 +153,8 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   p.k = k;
   p.z = a->logits;
   p.rs = a->row_stride;
-  p.T = a->temperature;
+  p.invT = 1.0 / static_cast<double>(a->temperature);
+  p.c = static_cast<float>(1.4426950408889634 * p.invT);
   p.ids = a->ids;
   p.values = a->values;
   p.lse = a->lse;
@@ -203,7 +204,8 @@ DistillParams distill_params(const specv_distill_args* a) {
   p.ts = a->teacher_stride;
   p.tlse = a->teacher_lse;
   p.weight = a->weights;
-  p.T = a->temperature;
+  p.invT = 1.0 / static_cast<double>(a->temperature);
+  p.c = static_cast<float>(1.4426950408889634 * p.invT);
   p.tail = (a->flags & SPECV_DISTILL_TAIL) != 0;
   p.stats = reinterpret_cast<float4*>(a->stats);
   p.grad = a->grad;
