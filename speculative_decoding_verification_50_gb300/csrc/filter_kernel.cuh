@@ -17,7 +17,7 @@
 // hundred.
 #pragma once
 
-#include "distill_kernel.cuh"  // store_vec, block_max_nan
+#include "distill_kernel.cuh"  // block_max_nan
 
 namespace specv {
 
@@ -51,7 +51,6 @@ struct FilterParams {
   int32_t* kept;
   void* out;              // filtered logits, or NULL
   int64_t obs, ors;
-  int32_t oaligned;
   int32_t* status;
   PairTable tab;
 };
@@ -283,7 +282,7 @@ struct FilterRow {
 #pragma unroll
         for (int k = 0; k < Elem<DT>::VW; ++k) z[k] = neg_inf();
       }
-      const int i0 = static_cast<int>(sl.base) + (sl.v0 + j) * Elem<DT>::VW;
+      const int i0 = sl.base + (sl.v0 + j) * Elem<DT>::VW;
 #pragma unroll
       for (int k = 0; k < Elem<DT>::VW; ++k) {
         const bool cand = z[k] >= edge && in_set(z[k], i0 + k);
@@ -641,7 +640,7 @@ struct FilterRow {
         const int j = j0 + lane;
         float x[Elem<DT>::VW];
         int mine = 0;
-        const int i0 = static_cast<int>(sl.base) + (sl.v0 + j) * Elem<DT>::VW;
+        const int i0 = sl.base + (sl.v0 + j) * Elem<DT>::VW;
         if (j < sl.nv) {
           Elem<DT>::unpack(sl.data[sl.v0 + j], x);
 #pragma unroll
@@ -757,8 +756,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   F.lane = lane;
   F.warp = warp;
   F.split = P.sp;
-  F.sl.init(smem, P.sp, rank);
   const char* zrow = reinterpret_cast<const char*>(P.z) + (b * P.bs + (row - b * P.R) * P.rs) * E::ES;
+  F.sl.init(smem, P.sp, rank);
   F.sl.load(zrow, P.sp, &S.bars[warp]);
   for (int j = threadIdx.x; j < kGrid; j += kRowThreads) S.tab[j] = P.tab.e[j];
   if (threadIdx.x == 0) S.above = 0;  // (this CTA's error bits, until the exchange)
@@ -916,7 +915,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     float lastz = 0.f, tz = 0.f;
     for (int j0 = 0; j0 < F.sl.nv; j0 += 32) {
       const int j = j0 + lane;
-      const int i0 = static_cast<int>(F.sl.base) + (F.sl.v0 + j) * E::VW;
+      const int i0 = F.sl.base + (F.sl.v0 + j) * E::VW;
       float z[E::VW];
       uint64_t w[E::VW], x = 0;
       if (j < F.sl.nv) E::unpack(F.sl.data[F.sl.v0 + j], z);
@@ -970,13 +969,17 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 
   if (P.out) {
     char* orow = reinterpret_cast<char*>(P.out) + (b * P.obs + (row - b * P.R) * P.ors) * E::ES;
-    for (int j = lane; j < F.sl.nv; j += 32) {
-      float z[E::VW];
-      E::unpack(F.sl.data[F.sl.v0 + j], z);
-      const int i0 = static_cast<int>(F.sl.base) + (F.sl.v0 + j) * E::VW;
+    for (int j0 = 0; j0 < F.sl.nv; j0 += 32) {
+      const int j = j0 + lane, i0 = F.sl.base + (F.sl.v0 + j) * E::VW;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (j < F.sl.nv) {
+        float z[E::VW];
+        E::unpack(F.sl.data[F.sl.v0 + j], z);
 #pragma unroll
-      for (int q = 0; q < E::VW; ++q) z[q] = F.in_set(z[q], i0 + q) ? z[q] : neg_inf();
-      store_vec<DT>(orow, i0, V, P.oaligned, z);
+        for (int q = 0; q < E::VW; ++q) z[q] = F.in_set(z[q], i0 + q) ? z[q] : neg_inf();
+        w = pack_vec<DT>(z);
+      }
+      store_warp<DT>(orow, i0, V, j < F.sl.nv, w);
     }
   }
 }
@@ -999,8 +1002,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   F.lane = lane;
   F.warp = warp;
   F.split = P.sp;
+  const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
   F.sl.init(smem, P.sp, rank);
-  F.sl.load(reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES, P.sp, &S.bars[warp]);
+  F.sl.load(zrow, P.sp, &S.bars[warp]);
   if (threadIdx.x == 0) S.above = 0;
   __syncthreads();
   if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.above, kTimeout);

@@ -16,11 +16,6 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 int elem_bytes(int32_t dtype) { return dtype == SPECV_BF16 ? 2 : 4; }
 
-// Rows of a [B, R, ...] layout start 16-byte aligned.
-bool rows_aligned(const void* base, int64_t bs, int64_t rs, int es) {
-  return aligned(base, 16) && (bs * es) % 16 == 0 && (rs * es) % 16 == 0;
-}
-
 specv_status check_rows(const char* what, int32_t n, int32_t V, int32_t dtype) {
   if (n < 0) return api_fail(SPECV_ERR_INVALID_ARG, "%s=%d < 0", what, n);
   if (V < 1) return api_fail(SPECV_ERR_INVALID_ARG, "V=%d < 1", V);
@@ -35,7 +30,7 @@ constexpr size_t kSmemSm = 228 * 1024, kSmemCta = 227 * 1024, kSmemReserved = 10
 // in shared memory beside `extra` bytes per CTA.  C is the smallest for which
 // two CTAs fit an SM (one row's copies then run under the other's passes),
 // and more while rows are too few to fill the SMs.  False: V does not fit.
-bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, bool vec, RowSplit& sp, size_t& smem) {
+bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& sp, size_t& smem) {
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
   const int64_t two = static_cast<int64_t>(kSmemSm / 2 - kSmemReserved - extra);
@@ -50,7 +45,6 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, bool vec, R
   sp.C = C;
   sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
   sp.gvec = (sp.svec + kRowWarps - 1) / kRowWarps;
-  sp.aligned = vec;
   smem = static_cast<size_t>(sp.svec) * 16;
   return true;
 }
@@ -101,8 +95,7 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   const int64_t rows = static_cast<int64_t>(B) * R;
   FilterParams p = {};
   size_t smem;
-  if (!split_row(rows, V, a->dtype, sizeof(FilterShared), rows_aligned(a->logits, a->batch_stride, a->row_stride, es),
-                 p.sp, smem))
+  if (!split_row(rows, V, a->dtype, sizeof(FilterShared), p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (rows * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B*R too large");
   p.rows = static_cast<int32_t>(rows);
@@ -121,7 +114,6 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   p.out = a->filtered;
   p.obs = a->filtered_batch_stride;
   p.ors = a->filtered_row_stride;
-  p.oaligned = a->filtered && rows_aligned(a->filtered, a->filtered_batch_stride, a->filtered_row_stride, es);
   p.status = a->row_status;
   static const PairTable table = make_table();
   p.tab = table;
@@ -146,7 +138,7 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   if (a->row_stride < V) return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
   TopParams p = {};
   size_t smem;
-  if (!split_row(B, V, a->dtype, sizeof(FilterShared), rows_aligned(a->logits, 0, a->row_stride, es), p.sp, smem))
+  if (!split_row(B, V, a->dtype, sizeof(FilterShared), p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (static_cast<int64_t>(B) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B too large");
   p.rows = B;
@@ -193,7 +185,6 @@ specv_status check_distill(const specv_distill_args* a) {
 }
 
 DistillParams distill_params(const specv_distill_args* a) {
-  const int es = elem_bytes(a->dtype);
   DistillParams p = {};
   p.N = a->N;
   p.K = a->K;
@@ -204,15 +195,15 @@ DistillParams distill_params(const specv_distill_args* a) {
   p.ts = a->teacher_stride;
   p.tlse = a->teacher_lse;
   p.weight = a->weights;
-  p.invT = 1.0 / static_cast<double>(a->temperature);
-  p.c = static_cast<float>(1.4426950408889634 * p.invT);
+  const double inv = 1.0 / static_cast<double>(a->temperature);
+  p.ih = static_cast<float>(inv);
+  p.il = static_cast<float>(inv - static_cast<double>(p.ih));
+  p.c = static_cast<float>(1.4426950408889634 * inv);
   p.tail = (a->flags & SPECV_DISTILL_TAIL) != 0;
   p.stats = reinterpret_cast<float4*>(a->stats);
   p.grad = a->grad;
   p.grs = a->grad_row_stride;
-  p.galigned = a->grad && rows_aligned(a->grad, 0, a->grad_row_stride, es);
   p.sp.V = a->V;
-  p.sp.aligned = rows_aligned(a->logits, 0, a->row_stride, es);
   return p;
 }
 
@@ -230,7 +221,7 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   DistillParams p = distill_params(a);
   size_t smem;
   const size_t extra = static_cast<size_t>(a->K) * 20;
-  if (!split_row(a->N, a->V, a->dtype, extra + kSmemReserved, p.sp.aligned != 0, p.sp, smem))
+  if (!split_row(a->N, a->V, a->dtype, extra + kSmemReserved, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
   if (static_cast<int64_t>(a->N) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   p.loss = a->loss;
@@ -244,7 +235,7 @@ specv_status specv_distill_backward(const specv_distill_args* a, void* stream) {
   if (st != SPECV_OK) return st;
   if (a->N == 0) return api_done(0);
   if (!a->stats || !a->grad) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
-  if (static_cast<int64_t>(a->N) * ((a->V - 1) / (kRowThreads * kBackVecs * (16 / elem_bytes(a->dtype))) + 1) > 0x7fffffffLL)
+  if (static_cast<int64_t>(a->N) * ((a->V + 6) / (kRowThreads * kBackVecs * (16 / elem_bytes(a->dtype))) + 1) > 0x7fffffffLL)
     return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   DistillParams p = distill_params(a);
   p.gloss = a->grad_loss;
