@@ -8,13 +8,16 @@
 // are gathered, sorted and summed exactly.  A band too full to gather is split
 // by the bits of the logits, then (all equal) by index.
 //
-// Whole numbers come out of these sums (the cut, the token), so weights are
-// pairs of fp32: 2^(E/64) from a table, exact to fp32, and the rest to first
-// order apart, about 2^-30 relative together; totals are 64-bit integers in
-// units of 2^-fbits of the largest weight (an SM does two fp64 operations a
-// clock: a block's reductions in fp64 cost more than its passes over the row).  A
-// sum in plain fp32 moves the cut of a flat distribution in one row of a
-// hundred.
+// Whole numbers come out of the sums of weights 2^(y - max) (the cut, the
+// token), and a sum in plain fp32 moves the cut of a flat distribution in one
+// row of a hundred.  So a weight is held to about 2^-31 of it, in two forms:
+//   for the cut: 2^(-d/64) (v 2^-bits + e), d its bin, v a whole number (the
+//     bins sum v exactly), e the rest in fp32;
+//   for the draw: h + l, h = 2^(-d/64) rounded to fp32, l the rest (their sums
+//     recover each rounding).
+// Totals are 64-bit integers in units of 2^-fbits of the largest weight (an SM
+// does two fp64 operations a clock: a block's reductions in fp64 cost more than
+// its passes over the row).
 #pragma once
 
 #include "distill_kernel.cuh"  // block_max_nan
@@ -24,16 +27,16 @@ namespace specv {
 constexpr int kGrid = 64;                 // bins per unit of log2
 constexpr int kWindow = 48;               // units below the maximum that carry weight
 constexpr int kBins = kGrid * kWindow + 16;
-constexpr int kCap = 2048;                // tokens sorted at once
-constexpr int kBinsPerThread = (kBins + kRowThreads - 1) / kRowThreads;
+constexpr int kLocal = 2048;              // tokens of a band that a CTA collects
+constexpr int kCap = 1024;                // ... and that rank 0 works on
 constexpr int kBadFilter = 64;
 constexpr float kMagic = 196608.f;        // 1.5 * 2^17: adding it rounds to 1/64
-// Equal within 2^-36 counts as equal, so that sums of equal weights which meet
-// a border exactly fall on its right side.
-constexpr double kSlack = 1.4551915228366852e-11;
+// kSlack: sums equal within 2^-36 (x >> 36) count as equal, so that equal
+// weights which meet a border exactly fall on its right side.
 
-struct PairTable {
-  float2 e[kGrid];  // 2^(j/64): (rounded to fp32, relative remainder)
+struct BinTable {
+  uint64_t e[kGrid];  // 2^(63 + j/64)
+  float2 p[kGrid];    // 2^(j/64): rounded to fp32, and what that leaves of it
 };
 
 struct FilterParams {
@@ -52,7 +55,7 @@ struct FilterParams {
   void* out;              // filtered logits, or NULL
   int64_t obs, ors;
   int32_t* status;
-  PairTable tab;
+  BinTable tab;
 };
 
 struct TopParams {
@@ -77,44 +80,73 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
-// The row's exponent scale: y = (z - shift) (chi + clo), Gm = the maximum's
-// place on the grid of 1/64.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+
+// The row's exponent scale: y = (z - shift) (chi + clo), gm = the maximum's
+// place on the grid of 1/64.  Weights are relative to 2^(gm / 64).
 struct Scale {
-  float shift, chi, clo;
+  float shift, chi, clo, gmf;  // gmf = gm / 64
   int gm;
 
-  __device__ void set(float m, double c) {  // c = log2(e) / T
+  // c = log2(e) / T.  bf16: chi has 16 digits, so that its products are exact.
+  template <int DT>
+  __device__ void set_factor(double c) {
     chi = static_cast<float>(c);
+    if (DT == 0) chi = __int_as_float(__float_as_int(chi) & 0xffffff00);
     clo = static_cast<float>(c - static_cast<double>(chi));
+  }
+  __device__ void set_max(float m) {
     // |y| stays within the rounding trick's range; shifted logits are exact
     // where they carry weight (within 48 units of a maximum of 2^14 units).
     shift = fabsf(m) * chi > 16384.f ? m : 0.f;
     const float r = __fadd_rn(__fmul_rn(m - shift, chi), kMagic);
     gm = __float_as_int(r) - __float_as_int(kMagic);
+    gmf = __fadd_rn(r, -kMagic);
   }
-  // Distance from the maximum in bins (0 at the maximum).  CLAMP: for logits
-  // that may lie anywhere below it (else: within the window).
+  // Distance from the maximum in bins: rounding is monotone, so 0 <= bin <=
+  // 48 * 64 + 3 for a logit of the window.  CLAMP: for any logit below the
+  // maximum.
   template <bool CLAMP>
   __device__ __forceinline__ int bin(float z) const {
     float p = __fmul_rn(z - shift, chi);
     if (CLAMP) p = fmaxf(p, -60000.f);
     const float r = __fadd_rn(p, kMagic);
-    const int d = gm - (__float_as_int(r) - __float_as_int(kMagic));
+    const int d = gm + __float_as_int(kMagic) - __float_as_int(r);
     return CLAMP ? min(d, kBins - 1) : d;
   }
-  // The weight 2^(y - gm/64) as h + l; d = its bin, g = what is left of y.
-  __device__ __forceinline__ void weight(float z, const float2* tab, float& h, float& l, int& d, float& g) const {
+  // What y leaves beside its bin (|g| <= 2^-7) and the bin's place below the
+  // maximum.
+  template <int DT>
+  __device__ __forceinline__ float split(float z, int& d, float& cb) const {
     const float x = z - shift;
     const float p = __fmul_rn(x, chi);
-    const float pe = fmaf(x, chi, -p);
     const float r = __fadd_rn(p, kMagic);
-    g = __fadd_rn(p, -__fadd_rn(r, -kMagic)) + fmaf(x, clo, pe);
-    const int e = __float_as_int(r) - __float_as_int(kMagic) - gm;
-    d = -e;
-    const float2 t = tab[e & (kGrid - 1)];
-    h = __int_as_float(__float_as_int(t.x) + ((e >> 6) << 23));
-    // 2^g - 1 for |g| <= 2^-7 (the next term is below 2^-34)
+    cb = __fadd_rn(r, -kMagic);
+    d = gm + __float_as_int(kMagic) - __float_as_int(r);
+    const float g = __fadd_rn(p, -cb);  // exact
+    return DT == 0 ? fmaf(x, clo, g) : g + fmaf(x, clo, fmaf(x, chi, -p));
+  }
+  // h and l of a logit of the window, d its bin.
+  template <int DT>
+  __device__ __forceinline__ void pair(float z, const float2* tab, float& h, float& l, int& d) const {
+    float cb;
+    const float g = split<DT>(z, d, cb);
+    const float2 t = tab[(-d) & (kGrid - 1)];
+    h = __int_as_float(__float_as_int(t.x) - (((d + kGrid - 1) & -kGrid) << 17));
+    // 2^g - 1 to 2^-34
     l = h * fmaf(g, fmaf(g, fmaf(g, 0.05550411f, 0.24022651f), 0.69314718f), t.y);
+  }
+  // d, v and e 2^(-d/64) of a logit of the window; lin = ln 2 * 2^bits, inv =
+  // 2^-bits, one = 2^bits less kRound's bits.
+  template <int DT>
+  __device__ __forceinline__ void weight(float z, float lin, float inv, int one, int& d, uint32_t& v, float& e) const {
+    float cb;
+    const float g = split<DT>(z, d, cb);
+    const float n = __fadd_rn(__fmul_rn(g, lin), kRound);
+    v = static_cast<uint32_t>(__float_as_int(n) + one);
+    // 2^g - 1 for |g| <= 2^-7 (the next term is below 2^-34)
+    const float t = __fmul_rn(g, fmaf(g, fmaf(g, 0.05550411f, 0.24022651f), 0.69314718f));
+    e = __fmul_rn(ex2(cb - gmf), fmaf(__fadd_rn(n, -kRound), -inv, t));
   }
 };
 
@@ -159,14 +191,15 @@ struct Decision {
 
 struct FilterShared {
   uint64_t bars[kRowWarps];
-  float2 tab[kGrid];
-  uint32_t hist[kCap * 2];   // the CTA's histogram; in rank 0 the gathered keys (8 bytes each)
-  uint32_t total[kBins];     // the row's histogram
+  BinTable tab;
+  uint32_t hist[kLocal * 2]; // the CTA's histogram; then the band's keys (8 bytes each) that it collects
+  uint32_t total[kBins];     // the row's histogram; then the warps' queues; then, in rank 0, the band's keys
   float xmax[kMaxCluster];
   uint64_t xsum[kMaxCluster];
   float xexp[kMaxCluster];
   int32_t xbad[kMaxCluster];
   int32_t xidx[kMaxCluster];
+  int32_t xcount[kMaxCluster];
   uint64_t scratch[kRowWarps];
   float fscratch[kRowWarps];
   int32_t iscratch[kRowWarps];
@@ -180,10 +213,9 @@ struct FilterShared {
   int32_t above;
   Scale sc;
   float zf, zt;
-  uint64_t goal;
   Decision dec;
 };
-static_assert(kBins <= kCap * 2, "the histogram fits its array");
+static_assert(kBins <= kLocal * 2 && kCap * 2 <= kBins && kRowWarps * 128 <= kBins, "arrays that share memory fit");
 
 // The set being cut and the band of it that is looked at: tokens above the
 // band are certainly kept by the cut, those below certainly not.
@@ -203,7 +235,20 @@ struct FilterRow {
   float zc;
   int ic;
   int fbits;    // sums are in units of 2^-fbits, so that V weights stay below 2^62
+  int bits;     // a bin's v in units of 2^-bits, so that V of them fit 32 bits
+  int one;      // for Scale::weight, as the next two
+  float lin, inv;
   float unit;   // 2^fbits
+
+  __device__ void set_units() {
+    const int n = 32 - __clz(V);
+    fbits = min(44, 62 - n);
+    bits = min(14, 31 - n);
+    unit = __int_as_float((127 + fbits) << 23);
+    inv = __int_as_float((127 - bits) << 23);
+    lin = 0.69314718f * __int_as_float((127 + bits) << 23);
+    one = (1 << bits) - __float_as_int(kRound);
+  }
 
   __device__ FilterRow(FilterShared& s) : S(s) {}
 
@@ -223,12 +268,24 @@ struct FilterRow {
   // twice.  Before it: S.hist filled by this CTA (and a __syncthreads).
   __device__ void merge(int bins) {
     cluster_sync();
-    const int per = (bins + C - 1) / C;
-    const int b0 = rank * per, b1 = min(bins, b0 + per);
+    const int per = (bins / 4 + C - 1) / C;
+    const int b0 = rank * per, b1 = min(bins / 4, b0 + per);
     for (int b = b0 + static_cast<int>(threadIdx.x); b < b1; b += kRowThreads) {
-      uint32_t t = 0;
-      for (int r = 0; r < C; ++r) t += peer(S.hist, r)[b];
-      for (int r = 0; r < C; ++r) peer(S.total, r)[b] = t;
+      uint4 t = make_uint4(0u, 0u, 0u, 0u);
+      for (int r0 = 0; r0 < C; r0 += 8) {  // loads of eight CTAs in flight
+        uint4 x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          x[q] = r0 + q < C ? reinterpret_cast<const uint4*>(peer(S.hist, r0 + q))[b] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          t.x += x[q].x;
+          t.y += x[q].y;
+          t.z += x[q].z;
+          t.w += x[q].w;
+        }
+      }
+      for (int r = 0; r < C; ++r) reinterpret_cast<uint4*>(peer(S.total, r))[b] = t;
     }
     cluster_sync();
   }
@@ -255,7 +312,7 @@ struct FilterRow {
   }
 
   __device__ void clear_hist(int bins) {
-    for (int b = threadIdx.x; b < bins; b += kRowThreads) S.hist[b] = 0;
+    for (int b = threadIdx.x; b < bins / 4; b += kRowThreads) reinterpret_cast<uint4*>(S.hist)[b] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) {
       S.ngather = 0;
       S.lo = S.hi = INT_MAX;
@@ -263,55 +320,80 @@ struct FilterRow {
     __syncthreads();
   }
 
-  // Gathers the band's tokens at rank 0 and leaves, per segment, the number
-  // and (sums) the weight of the tokens above the band, and the band's count
-  // and range of keys.  Ends with a cluster barrier.
+  // Collects the band's tokens, a list in each CTA, and leaves at rank 0, per
+  // segment, the number and (sums) the weight of the tokens above the band,
+  // and the band's count and range of keys.  Ends with a cluster barrier.
+  // Where a warp's vectors hold few of these tokens (peaked rows), it queues
+  // them and works on 32 at a time; where they hold many, it works in place.
   __device__ void gather(const Band& b, bool sums) {
     PairSum acc;
     int above = 0, band = 0;
     uint32_t kmin = 0xffffffffu, kmax = 0;
-    uint64_t* list = reinterpret_cast<uint64_t*>(peer(S.hist, 0));
-    int* counter = peer(&S.ngather, 0);
+    uint64_t* list = reinterpret_cast<uint64_t*>(S.hist);
+    uint2* queue = reinterpret_cast<uint2*>(S.total) + warp * 64;
     const float edge = b.edge;
+    auto work = [&](bool cand, float z, int i) {
+      const int pl = place(z, b);
+      const bool over = cand && pl == 0;
+      above += over;
+      if (!CLAMP && sums) {
+        float h, l;
+        int d;
+        sc.template pair<DT>(z, S.tab.p, h, l, d);
+        acc.add(over ? h : 0.f, over ? l : 0.f);
+      }
+      if (cand && pl == 1) {
+        ++band;
+        const uint32_t key = order_key(z);
+        kmin = min(kmin, key);
+        kmax = max(kmax, key);
+        const int pos = atomicAdd(&S.ngather, 1);
+        if (pos < kLocal) list[pos] = (static_cast<uint64_t>(~key) << 32) | static_cast<uint32_t>(i);
+      }
+    };
+    int queued = 0;
+    auto flush = [&](int n) {
+      __syncwarp();
+      const uint2 it = queue[lane];
+      work(lane < n, lane < n ? __uint_as_float(it.x) : edge_safe(), it.y);
+    };
     for (int j0 = 0; j0 < sl.nv; j0 += 32) {
       const int j = j0 + lane;
       float z[Elem<DT>::VW];
+      float top = neg_inf();
       if (j < sl.nv) {
         Elem<DT>::unpack(sl.data[sl.v0 + j], z);
-      } else {
 #pragma unroll
-        for (int k = 0; k < Elem<DT>::VW; ++k) z[k] = neg_inf();
+        for (int k = 0; k < Elem<DT>::VW; k += 2) top = max3(top, z[k], z[k + 1]);
       }
+      const unsigned lanes = __ballot_sync(0xffffffffu, top >= edge);
+      if (!lanes) continue;
       const int i0 = sl.base + (sl.v0 + j) * Elem<DT>::VW;
+      if (__popc(lanes) >= 24) {  // most lanes hold one at least
+#pragma unroll
+        for (int k = 0; k < Elem<DT>::VW; ++k) {
+          const bool cand = top >= edge && z[k] >= edge && in_set(z[k], i0 + k);
+          work(cand, cand ? z[k] : edge_safe(), i0 + k);
+        }
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < Elem<DT>::VW; ++k) {
-        const bool cand = z[k] >= edge && in_set(z[k], i0 + k);
-        if (!__any_sync(0xffffffffu, cand)) continue;
-        const int pl = cand ? place(z[k], b) : 2;
-        if (pl == 0) {
-          ++above;
-          if (sums) {
-            float h, l, g;
-            int d;
-            sc.weight(z[k], S.tab, h, l, d, g);
-            acc.add(h, l);
-          }
-        }
-        const unsigned in = __ballot_sync(0xffffffffu, pl == 1);
-        if (in) {
-          int pos = 0;
-          if (lane == __ffs(in) - 1) pos = atomicAdd(counter, __popc(in));
-          pos = __shfl_sync(0xffffffffu, pos, __ffs(in) - 1) + __popc(in & ((1u << lane) - 1));
-          if (pl == 1) {
-            ++band;
-            const uint32_t key = order_key(z[k]);
-            kmin = min(kmin, key);
-            kmax = max(kmax, key);
-            if (pos < kCap) list[pos] = (static_cast<uint64_t>(~key) << 32) | static_cast<uint32_t>(i0 + k);
-          }
+        const bool cand = top >= edge && z[k] >= edge && in_set(z[k], i0 + k);
+        const unsigned mask = __ballot_sync(0xffffffffu, cand);
+        if (cand) queue[queued + __popc(mask & ((1u << lane) - 1))] = make_uint2(__float_as_uint(z[k]), i0 + k);
+        queued += __popc(mask);
+        if (queued >= 32) {
+          flush(32);
+          queued -= 32;
+          const uint2 rest = queue[32 + lane];
+          __syncwarp();
+          if (lane < queued) queue[lane] = rest;
+          __syncwarp();
         }
       }
     }
+    if (queued > 0) flush(queued);
     const uint64_t w = warp_sum_u(acc.fixed(unit));
     above = __reduce_add_sync(0xffffffffu, above);
     band = __reduce_add_sync(0xffffffffu, band);
@@ -325,28 +407,87 @@ struct FilterRow {
       peer(S.segkmin, 0)[s] = kmin;
       peer(S.segkmax, 0)[s] = kmax;
     }
+    __syncthreads();
+    push_all(S.xcount, rank, C, S.ngather);
     cluster_sync();
   }
 
-  // Sorts rank 0's gathered keys ascending: logit descending, index ascending.
-  __device__ void sort(int n) {
-    uint64_t* list = reinterpret_cast<uint64_t*>(S.hist);
-    int P = 2;
-    while (P < n) P <<= 1;
-    for (int i = n + static_cast<int>(threadIdx.x); i < P; i += kRowThreads) list[i] = ~0ull;
+  // Tokens in the band gathered last (more than kCap: not all were collected).
+  __device__ int gathered() const {
+    int n = 0;
+    bool over = false;
+    for (int r = 0; r < C; ++r) {
+      over |= S.xcount[r] > kLocal;
+      n += S.xcount[r];
+    }
+    return over ? max(n, kCap + 1) : n;
+  }
+
+  // Rank 0: the n <= kCap collected keys into S.total (ends with a barrier).
+  __device__ void pull(int n) {
+    uint64_t* list = reinterpret_cast<uint64_t*>(S.total);
+    for (int t = threadIdx.x; t < n; t += kRowThreads) {
+      int r = 0, i = t;
+      while (i >= S.xcount[r]) i -= S.xcount[r++];
+      list[t] = reinterpret_cast<const uint64_t*>(peer(S.hist, r))[i];
+    }
     __syncthreads();
-    for (int size = 2; size <= P; size <<= 1)
+  }
+
+  // Sorts n <= kCap keys ascending: logit descending, index ascending.
+  __device__ void sort(uint64_t* list, int n) {
+    int P = 16;
+    while (P < n) P <<= 1;
+    if (P <= kRowThreads / 2) {  // few: G threads count the keys before each
+      const int G = kRowThreads / P, i = threadIdx.x / G, sub = threadIdx.x % G;
+      const uint64_t x = i < n ? list[i] : 0;
+      int before = 0;
+      for (int j = sub; j < n; j += G) before += list[j] < x;
+      for (int o = G / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      __syncthreads();
+      if (sub == 0 && i < n) list[before] = x;
+      __syncthreads();
+      return;
+    }
+    // two keys a thread (i = 2 t and 2 t + 1), steps below 64 within a warp
+    uint64_t a = ~0ull, b = ~0ull;
+    const int i = 2 * threadIdx.x;
+    if (i < n) a = list[i];
+    if (i + 1 < n) b = list[i + 1];
+    for (int size = 2; size <= P; size <<= 1) {
+      const bool up = (i & size) == 0;
       for (int step = size >> 1; step > 0; step >>= 1) {
-        for (int t = threadIdx.x; t < P / 2; t += kRowThreads) {
-          const int i = 2 * t - (t & (step - 1)), j = i + step;
-          const uint64_t x = list[i], y = list[j];
-          if ((x > y) == ((i & size) == 0)) {
-            list[i] = y;
-            list[j] = x;
+        if (step == 1) {
+          if ((a > b) == up) {
+            const uint64_t t = a;
+            a = b;
+            b = t;
           }
+          continue;
         }
-        __syncthreads();
+        uint64_t x, y;
+        if (step < 64) {
+          x = __shfl_xor_sync(0xffffffffu, a, step >> 1);
+          y = __shfl_xor_sync(0xffffffffu, b, step >> 1);
+        } else {
+          __syncthreads();
+          if (i < P) {
+            list[i] = a;
+            list[i + 1] = b;
+          }
+          __syncthreads();
+          x = i < P ? list[i ^ step] : a;
+          y = i < P ? list[(i + 1) ^ step] : b;
+        }
+        const bool lower = (i & step) == 0;
+        if ((a > x) == (lower == up)) a = x;
+        if ((b > y) == (lower == up)) b = y;
       }
+    }
+    __syncthreads();
+    if (i < n) list[i] = a;
+    if (i + 1 < n) list[i + 1] = b;
+    __syncthreads();
   }
 
   // Block-wide sum (every thread gets it).
@@ -383,43 +524,102 @@ struct FilterRow {
     cluster_sync();
   }
 
-  // A bin's mass, v counted in 2^-bits of its scale 2^(-d/64).
-  __device__ __forceinline__ uint64_t mass(uint32_t v, int d, int bits) const {
-    const uint32_t t = (__float_as_uint(S.tab[(-d) & (kGrid - 1)].x) << 8) | 0x80000000u;  // 2^31 2^(j/64)
-    const int s = bits + 31 - fbits - ((-d) >> 6);
-    const uint64_t x = static_cast<uint64_t>(v) * t;
-    return s >= 64 ? 0 : s >= 0 ? x >> s : x << -s;
+  // v 2^-bits 2^(-d/64) in units of 2^-fbits.
+  __device__ __forceinline__ uint64_t mass(uint32_t v, int d) const {
+    const uint64_t t = S.tab.e[(-d) & (kGrid - 1)];
+    const uint64_t x = static_cast<uint64_t>(v) * (t >> 32) + ((static_cast<uint64_t>(v) * (t & 0xffffffffu)) >> 32);
+    const int s = bits + 31 - fbits - ((-d) >> 6);  // 0 or 1, and the halvings of d
+    return s > 0 ? (x + (1ull << (s - 1))) >> s : x;
+  }
+
+  // A token's weight without its e, which is added to `low`.
+  __device__ __forceinline__ uint64_t part_weight(float z, float& low) const {
+    int d;
+    uint32_t v;
+    float e;
+    sc.template weight<DT>(z, lin, inv, one, d, v, e);
+    low += e;
+    return mass(v, d);
+  }
+
+  // A logit of the window, for lanes without one of their own.
+  __device__ __forceinline__ float edge_safe() const { return sc.shift; }
+
+  // A token's weight for the draw.
+  __device__ __forceinline__ uint64_t draw_weight(float z) const {
+    float h, l;
+    int d;
+    sc.template pair<DT>(z, S.tab.p, h, l, d);
+    return static_cast<uint64_t>(__float2ll_rn(h * unit) + __float2ll_rn(l * unit));
+  }
+
+  // A token's weight for the cut.
+  __device__ __forceinline__ uint64_t fixed_weight(float z) const {
+    float e = 0.f;
+    const uint64_t w = part_weight(z, e);
+    return w + static_cast<uint64_t>(__float2ll_rn(e * unit));
   }
 
   // Bins -> the band between the first bin where the cut may lie and the
-  // first where it must.  COUNT: the goal-th token; else the mass `goal`, the
-  // bins' masses being good to 2^-bits.  S.before: the count before the band.
-  // False if the set ends before the goal-th token.
+  // first where it must.  COUNT: the goal-th token; else the mass `share` of
+  // the whole set's, left in goal (the bins' masses are good to 2^-bits; the
+  // rest of each weight, summed, is in S.xsum).  S.before: the count before the
+  // band.  False if the set ends before the goal-th token.
   template <bool COUNT>
-  __device__ bool find_bins(uint64_t goal, int bits, Band& b) {
-    const int b0 = threadIdx.x * kBinsPerThread;
-    uint64_t v[kBinsPerThread], x = 0;
+  __device__ bool find_bins(uint64_t& goal, float share, Band& b) {
+    // warp w holds bins [w * kBinsPerWarp, ...), a lane every 32nd
+    constexpr int kBinsPerWarp = (kBins + kRowWarps - 1) / kRowWarps, per = (kBinsPerWarp + 31) / 32;
+    const int b0 = warp * kBinsPerWarp, b1 = min(kBins, b0 + kBinsPerWarp);
+    uint64_t v[per], x = 0;
 #pragma unroll
-    for (int q = 0; q < kBinsPerThread; ++q) {
-      const uint32_t n = b0 + q < kBins ? S.total[b0 + q] : 0u;
-      v[q] = COUNT ? n : mass(n, b0 + q, bits);
+    for (int q = 0; q < per; ++q) {
+      const int d = b0 + q * 32 + lane;
+      const uint32_t n = d < b1 ? S.total[d] : 0u;
+      v[q] = COUNT ? n : n ? mass(n, d) : 0;
       x += v[q];
     }
-    uint64_t all;
-    uint64_t run = block_scan(x, S.scratch, all);
-    if (COUNT && all < goal) return false;
+    x = warp_sum_u(x);
+    if (lane == 0) S.scratch[warp] = x;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
 #pragma unroll
-    for (int q = 0; q < kBinsPerThread; ++q) {
-      const uint64_t before = run;
-      run += v[q];
-      const uint64_t slack = COUNT ? 0 : (run >> bits) + 1;
-      if (v[q] && run + slack >= goal) {
-        if (COUNT && before < goal) S.before = static_cast<int32_t>(before);
-        atomicMin(&S.lo, b0 + q);
-      }
-      if (v[q] && run - slack >= goal) {
-        atomicMin(&S.hi, b0 + q);
-        break;
+    for (int w = 0; w < kRowWarps; ++w) {
+      if (w < warp) before += S.scratch[w];
+      all += S.scratch[w];
+    }
+    if (COUNT) {
+      if (all < goal) return false;
+    } else {
+      for (int r = 0; r < C; ++r) all += S.xsum[r];
+      goal = __umul64hi(all, __float2ull_rd(share * 18446744073709551616.f)) + 1;
+      goal -= goal >> 36;  // kSlack
+    }
+    const uint64_t end = before + x;
+    if (x && end + (COUNT ? 0 : (end >> bits) + 1) >= goal && (before < goal + (COUNT ? 0 : (goal >> (bits - 1)) + 2))) {
+      // the cut may lie among this warp's bins
+      uint64_t run = before;
+#pragma unroll
+      for (int q = 0; q < per; ++q) {
+        uint64_t inc = v[q];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const uint64_t mine = run + inc;
+        const uint64_t slack = COUNT ? 0 : (mine >> bits) + 1;
+        const int d = b0 + q * 32 + lane;
+        const unsigned may = __ballot_sync(0xffffffffu, v[q] && mine + slack >= goal);
+        const unsigned must = __ballot_sync(0xffffffffu, v[q] && mine - slack >= goal);
+        if (may && lane == __ffs(may) - 1) {
+          atomicMin(&S.lo, d);
+          if (COUNT && mine - v[q] < goal) S.before = static_cast<int32_t>(mine - v[q]);
+        }
+        if (must) {
+          if (lane == __ffs(must) - 1) atomicMin(&S.hi, d);
+          break;
+        }
+        run = __shfl_sync(0xffffffffu, mine, 31);
       }
     }
     __syncthreads();
@@ -429,15 +629,7 @@ struct FilterRow {
     // 64 y >= gm - hi - 1/2 for every token of the band, with room for rounding
     const float e = sc.shift + (static_cast<float>(sc.gm - b.hi) - 0.5f) / (static_cast<float>(kGrid) * sc.chi);
     b.edge = b.hi >= kBins - 1 ? kNegMax : fmaxf(e - 1e-6f * (fabsf(e) + fabsf(sc.shift)) - 1e-30f, kNegMax);
-    __syncthreads();
     return true;
-  }
-
-  __device__ uint64_t fixed_weight(float z) const {
-    float h, l, g;
-    int d;
-    sc.weight(z, S.tab, h, l, d, g);
-    return static_cast<uint64_t>(__float2ll_rn(h * unit) + __float2ll_rn(l * unit));
   }
 
   // Narrows a band too full to gather: counts by key over [kmin, kmax] into
@@ -511,7 +703,7 @@ struct FilterRow {
         return false;
       }
       gather(b, !count || (fin && u != nullptr));
-      const int n = *peer(&S.ngather, 0);
+      const int n = gathered();
       if (n <= kCap) {
         if (rank == 0) resolve(n, count, goal, fin, zt, u);
         publish();
@@ -550,55 +742,146 @@ struct FilterRow {
     return true;
   }
 
-  // Rank 0, the band gathered: where the cut falls in it.
+  __device__ __forceinline__ static float listed_logit(uint64_t k) { return key_value(~static_cast<uint32_t>(k >> 32)); }
+
+  // Rank 0, the band collected: where the cut falls in it.  More keys than are
+  // sorted quickly are first split into bins of their own.
   __device__ void resolve(int n, bool count, uint64_t goal, bool fin, float zt, const float* u) {
-    uint64_t* list = reinterpret_cast<uint64_t*>(S.hist);
+    uint64_t* list = reinterpret_cast<uint64_t*>(S.total);
     uint64_t w;
     int above, band;
+    pull(n);
     seg_totals(w, above, band);
-    sort(n);
-    if (threadIdx.x == 0) S.lo = S.hi = n;
-    __syncthreads();
-    int nb;
-    if (count) {
-      nb = min(static_cast<int>(goal) - above, n);
-    } else {
-      constexpr int per = kCap / kRowThreads;
-      const int i0 = threadIdx.x * per;
-      uint64_t v[per], x = 0;
-#pragma unroll
-      for (int q = 0; q < per; ++q) {
-        v[q] = i0 + q < n ? fixed_weight(key_value(~static_cast<uint32_t>(list[i0 + q] >> 32))) : 0;
-        x += v[q];
+    if (count) w = above;
+    uint64_t* sub = list;
+    int m = n;
+    if (n > kRowThreads / 2) {
+      // bins of the keys' range, a thread's each: counts or masses
+      uint64_t* bin = reinterpret_cast<uint64_t*>(S.hist);
+      uint32_t lo = 0xffffffffu, hi = 0;
+      for (int i = threadIdx.x; i < n; i += kRowThreads) {
+        lo = min(lo, static_cast<uint32_t>(list[i] >> 32));
+        hi = max(hi, static_cast<uint32_t>(list[i] >> 32));
       }
-      uint64_t all;
-      uint64_t run = w + block_scan(x, S.scratch, all);
-#pragma unroll
-      for (int q = 0; q < per; ++q) {
-        run += v[q];
-        if (i0 + q < n && run >= goal) atomicMin(&S.lo, i0 + q);
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      bin[threadIdx.x] = 0;
+      if (threadIdx.x == 0) {
+        S.lo = INT_MAX;
+        S.hi = 0;
       }
+      if (lane == 0) S.scratch[warp] = (static_cast<uint64_t>(lo) << 32) | hi;
       __syncthreads();
-      nb = min(S.lo + 1, n);
-    }
-    if (fin) {  // min-p may end the kept tokens earlier
+      for (int x = 0; x < kRowWarps; ++x) {
+        lo = min(lo, static_cast<uint32_t>(S.scratch[x] >> 32));
+        hi = max(hi, static_cast<uint32_t>(S.scratch[x]));
+      }
+      int shift = 0;
+      while (((hi - lo) >> shift) >= kRowThreads) ++shift;
       for (int i = threadIdx.x; i < n; i += kRowThreads)
-        if (key_value(~static_cast<uint32_t>(list[i] >> 32)) < zt) atomicMin(&S.hi, i);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&bin[(static_cast<uint32_t>(list[i] >> 32) - lo) >> shift]),
+                  count ? 1ull : fixed_weight(listed_logit(list[i])));
       __syncthreads();
-      nb = min(nb, S.hi);
+      const uint64_t mine = bin[threadIdx.x];
+      uint64_t all;
+      const uint64_t before = w + block_scan(mine, S.scratch, all);
+      if (mine && before + mine >= goal) atomicMin(&S.lo, static_cast<int>(threadIdx.x));
+      __syncthreads();
+      const int at = S.lo == INT_MAX ? static_cast<int>((hi - lo) >> shift) : S.lo;
+      if (static_cast<int>(threadIdx.x) == at) S.scratch[0] = before;
+      __syncthreads();
+      w = S.scratch[0];
+      // the keys of that bin
+      sub = reinterpret_cast<uint64_t*>(S.hist) + kRowThreads;
+      for (int i = threadIdx.x; i < n; i += kRowThreads)
+        if (static_cast<int>((static_cast<uint32_t>(list[i] >> 32) - lo) >> shift) == at) sub[atomicAdd(&S.hi, 1)] = list[i];
+      __syncthreads();
+      m = S.hi;
     }
     if (threadIdx.x == 0) {
-      S.dec.tie_seg = -1;
-      if (nb > 0) {
-        S.dec.zc = key_value(~static_cast<uint32_t>(list[nb - 1] >> 32));
-        S.dec.ic = static_cast<int32_t>(list[nb - 1] & 0xffffffffu);
-      } else {
-        S.dec.zc = zt;
-        S.dec.ic = INT_MAX;
-      }
-      S.dec.kept = above + nb;
+      S.lo = m;
+      S.above = 0;
     }
-    if (fin && u) finish(nb, 0, 0.f, *u);
+    sort(sub, m);
+    constexpr int per = kCap / kRowThreads;
+    const int i0 = threadIdx.x * per;
+    uint64_t v[per], x = 0;
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      v[q] = i0 + q < m ? (count ? 1ull : fixed_weight(listed_logit(sub[i0 + q]))) : 0;
+      x += v[q];
+    }
+    uint64_t all;
+    uint64_t run = w + block_scan(x, S.scratch, all);
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      run += v[q];
+      if (i0 + q < m && run >= goal) atomicMin(&S.lo, i0 + q);
+    }
+    __syncthreads();
+    const uint64_t cutkey = sub[max(0, min(S.lo, m - 1))];
+    float z = listed_logit(cutkey);
+    int idx = static_cast<int>(cutkey & 0xffffffffu);
+    if (fin && z < zt) {  // min-p ends the kept tokens earlier
+      z = zt;
+      idx = INT_MAX;
+    }
+    zc = z;
+    ic = idx;
+    // the band's tokens that the cut keeps
+    int kept = 0;
+    for (int i = threadIdx.x; i < n; i += kRowThreads)
+      kept += in_set(listed_logit(list[i]), static_cast<int>(list[i] & 0xffffffffu));
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if (lane == 0 && kept) atomicAdd(&S.above, kept);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      S.dec.tie_seg = -1;
+      S.dec.zc = z;
+      S.dec.ic = idx;
+      S.dec.kept = above + S.above;
+    }
+    if (fin && u) finish(n, 0, 0.f, *u);
+  }
+
+  // Rank 0, every token down to the k-th's bin collected (n of them): top-k,
+  // top-p and min-p on the sorted list.
+  __device__ void resolve_top(int n, int k, float tp, float zt, const float* u) {
+    uint64_t* list = reinterpret_cast<uint64_t*>(S.total);
+    pull(n);
+    sort(list, n);
+    const int m = min(k, n);
+    constexpr int per = kCap / kRowThreads;
+    const int i0 = threadIdx.x * per;
+    uint64_t v[per], x = 0;
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      v[q] = i0 + q < m ? fixed_weight(listed_logit(list[i0 + q])) : 0;
+      x += v[q];
+    }
+    uint64_t all;
+    uint64_t run = block_scan(x, S.scratch, all);
+    uint64_t goal = tp < 1.f ? __umul64hi(all, __float2ull_rd(tp * 18446744073709551616.f)) + 1 : all;
+    goal -= goal >> 36;  // kSlack
+    if (threadIdx.x == 0) S.lo = m - 1;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      run += v[q];
+      if (i0 + q < m && (tp < 1.f && run >= goal)) atomicMin(&S.lo, i0 + q);
+      if (i0 + q < m && i0 + q > 0 && listed_logit(list[i0 + q]) < zt) atomicMin(&S.lo, i0 + q - 1);
+    }
+    __syncthreads();
+    const int last = S.lo;
+    zc = listed_logit(list[last]);
+    ic = static_cast<int>(list[last] & 0xffffffffu);
+    if (threadIdx.x == 0) {
+      S.dec.tie_seg = -1;
+      S.dec.zc = zc;
+      S.dec.ic = ic;
+      S.dec.kept = last + 1;
+    }
+    if (u) finish(n, 0, 0.f, *u);
   }
 
   // Rank 0, a band of n > kCap equal logits: how many of them are kept, and
@@ -668,24 +951,25 @@ struct FilterRow {
 
   // Rank 0: total weight of the kept tokens, and the segment where the
   // running sum in index order passes u times it.  Kept: the segments' sums,
-  // the first nb gathered tokens, and the first nt logits equal to z.
-  __device__ void finish(int nb, int nt, float z, float u) {
-    const uint64_t* list = reinterpret_cast<const uint64_t*>(S.hist);
-    uint64_t* fix = reinterpret_cast<uint64_t*>(S.total);  // free by now
+  // those of the n collected tokens that zc, ic keep, and the first nt logits
+  // equal to z.
+  __device__ void finish(int n_list, int nt, float z, float u) {
+    const uint64_t* list = reinterpret_cast<const uint64_t*>(S.total);
+    uint64_t* fix = reinterpret_cast<uint64_t*>(S.hist);  // free by now
     const int n = C * kRowWarps;
     __syncthreads();
     for (int s = threadIdx.x; s < n; s += kRowThreads) fix[s] = S.segsum[s];
     __syncthreads();
-    const int seg = sl_segment_size();
-    for (int i = threadIdx.x; i < nb; i += kRowThreads) {
-      const float x = key_value(~static_cast<uint32_t>(list[i] >> 32));
+    for (int i = threadIdx.x; i < n_list; i += kRowThreads) {
+      const float x = listed_logit(list[i]);
       const int idx = static_cast<int>(list[i] & 0xffffffffu);
-      const int cta = idx / cta_size();
-      const int s = cta * kRowWarps + (idx - cta * cta_size()) / seg;
-      atomicAdd(reinterpret_cast<unsigned long long*>(&fix[s]), fixed_weight(x));
+      if (!in_set(x, idx)) continue;
+      const int vec = idx / Elem<DT>::VW, cta = quotient(vec, split.svec);
+      const int s = cta * kRowWarps + quotient(vec - cta * split.svec, split.gvec);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&fix[s]), draw_weight(x));
     }
     if (nt > 0 && threadIdx.x == 0) {
-      const uint64_t one = fixed_weight(z);
+      const uint64_t one = draw_weight(z);
       for (int s = 0; s < n && nt > 0; ++s) {
         const int take = min(nt, S.segband[s]);
         fix[s] += one * static_cast<uint64_t>(take);
@@ -705,8 +989,8 @@ struct FilterRow {
       }
       const uint64_t all = __shfl_sync(0xffffffffu, inc, 31);
       // (whole numbers: run > u W exactly if run > its floor)
-      const uint64_t t =
-          __double2ull_rd(fmax(static_cast<double>(u), 0.0) * static_cast<double>(all) * (1.0 + kSlack));
+      uint64_t t = u > 0.f && u < 1.f ? __umul64hi(all, __float2ull_rd(u * 18446744073709551616.f)) : 0;
+      t += t >> 36;  // kSlack
       const unsigned over = __ballot_sync(0xffffffffu, u < 1.f && inc > t);
       const unsigned some = __ballot_sync(0xffffffffu, x > 0);
       const bool fell = over == 0;
@@ -732,8 +1016,12 @@ struct FilterRow {
     __syncthreads();
   }
 
-  __device__ int cta_size() const { return split.svec * Elem<DT>::VW; }
-  __device__ int sl_segment_size() const { return split.gvec * Elem<DT>::VW; }
+  // a / b for 0 <= a < 2^24.
+  __device__ __forceinline__ static int quotient(int a, int b) {
+    int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+    q -= q * b > a;
+    return q + ((q + 1) * b <= a);
+  }
   RowSplit split;
 };
 
@@ -759,10 +1047,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   const char* zrow = reinterpret_cast<const char*>(P.z) + (b * P.bs + (row - b * P.R) * P.rs) * E::ES;
   F.sl.init(smem, P.sp, rank);
   F.sl.load(zrow, P.sp, &S.bars[warp]);
-  for (int j = threadIdx.x; j < kGrid; j += kRowThreads) S.tab[j] = P.tab.e[j];
+  for (int j = threadIdx.x; j < kGrid; j += kRowThreads) {
+    S.tab.e[j] = P.tab.e[j];
+    S.tab.p[j] = P.tab.p[j];
+  }
   if (threadIdx.x == 0) S.above = 0;  // (this CTA's error bits, until the exchange)
-  F.fbits = min(44, 62 - (32 - __clz(V)));
-  F.unit = __int_as_float((127 + F.fbits) << 23);
+  F.set_units();
   const float T = P.temp[b];
   const int k = P.top_k ? P.top_k[b] : 0;
   const float tp = P.top_p ? P.top_p[b] : 1.f;
@@ -772,10 +1062,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   if (!(T >= 0.f) || T > 3.4e38f) bad |= kBadTemp;
   if (k < 0 || !(tp >= 0.f && tp <= 1.f) || !(mp >= 0.f && mp <= 1.f)) bad |= kBadFilter;
   // The row's scales in fp64, by one thread while the copies run.
-  double c = 0, tf = 0, tm = 0;
+  double tf = 0, tm = 0;
   if (threadIdx.x == 0) {
     const double Td = fmaxf(T, 1e-30f), lnf = -kWindow * 0.69314718055994530942;
-    c = 1.4426950408889634074 / Td;
+    S.sc.set_factor<DT>(1.4426950408889634074 / Td);
     tf = Td * lnf;
     tm = mp > 0.f ? Td * fmax(log(static_cast<double>(mp)), lnf) : tf;
   }
@@ -824,55 +1114,67 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (P.status) P.status[row] = 0;
     }
   } else {
+    F.sc = S.sc;
+    F.sc.set_max(m);
     if (threadIdx.x == 0) {
-      S.sc.set(m, c);
       S.zf = __double2float_ru(static_cast<double>(m) + tf);
       S.zt = fmaxf(S.zf, __double2float_ru(static_cast<double>(m) + tm));
     }
-    __syncthreads();
-    F.sc = S.sc;
+    F.clear_hist(kBins);  // (a barrier)
     const float zf = S.zf, zt = S.zt;
     F.zc = zf;
     F.ic = INT_MAX;
     const bool use_k = k > 0 && k < V, use_p = tp < 1.f;
     const int dt = zt > zf ? F.sc.template bin<false>(zt) : kBins;
     bool done = false;
-    // the shift that lets a bin hold every token's mass in 32 bits
-    const int bits = min(14, 31 - (32 - __clz(V)));
     for (int stage = use_k ? 0 : 1; stage < (use_p ? 2 : 1); ++stage) {
       const bool count = stage == 0;
-      F.clear_hist(kBins);
-      PairSum acc;
-      const float one = ldexpf(1.f, bits), lin = one * 0.69314718f;
-      F.sl.each([&](float z, int i) {
-        if (F.in_set(z, i)) {
-          if (count) {
-            atomicAdd(&S.hist[min(static_cast<unsigned>(F.sc.template bin<false>(z)), kBins - 1u)], 1u);
-          } else {
-            float h, l, g;
-            int d;
-            F.sc.weight(z, S.tab, h, l, d, g);
-            acc.add(h, l);
-            atomicAdd(&S.hist[min(static_cast<unsigned>(d), kBins - 1u)], static_cast<uint32_t>(__float2int_rn(fmaf(g, lin, one))));
-          }
+      if (!count && use_k) F.clear_hist(kBins);
+      if (count) {
+        F.sl.each([&](float z, int) {
+          if (z >= zf) atomicAdd(&S.hist[F.sc.template bin<false>(z)], 1u);
+        });
+      } else {
+        float low = 0.f;
+        const float cut = F.zc;
+        const int last = F.ic;
+        auto add = [&](float z) {
+          int d;
+          uint32_t v;
+          float e;
+          F.sc.template weight<DT>(z, F.lin, F.inv, F.one, d, v, e);
+          low += e;
+          atomicAdd(&S.hist[d], v);
+        };
+        if (last == INT_MAX) {
+          F.sl.each([&](float z, int) {
+            if (z >= cut) add(z);
+          });
+        } else {
+          F.sl.each([&](float z, int i) {
+            if (z >= cut && F.in_set(z, i)) add(z);
+          });
         }
-      });
-      if (!count) push_all(S.xsum, rank, C, F.block_sum_u(acc.fixed(F.unit)));
+        push_all(S.xsum, rank, C, F.block_sum_u(static_cast<uint64_t>(__float2ll_rn(low * F.unit))));
+      }
       __syncthreads();
       F.merge(kBins);
       uint64_t goal = k;
-      if (!count) {
-        if (threadIdx.x == 0) {
-          uint64_t Z = 0;
-          for (int r = 0; r < C; ++r) Z += S.xsum[r];
-          S.goal = __double2ull_ru(static_cast<double>(tp) * static_cast<double>(Z) * (1.0 - kSlack));
-        }
-        __syncthreads();
-        goal = S.goal;
-      }
       Band band;
-      if (!(count ? F.template find_bins<true>(goal, bits, band) : F.template find_bins<false>(goal, bits, band)))
+      if (!(count ? F.template find_bins<true>(goal, 0.f, band) : F.template find_bins<false>(goal, tp, band)))
         continue;  // fewer than k
+      if (count && S.before + static_cast<int>(S.total[band.hi]) <= kCap) {
+        // few enough to collect: the rest is done on the list
+        __syncthreads();
+        band.lo = 0;
+        F.gather(band, false);
+        if (rank == 0) F.resolve_top(F.gathered(), k, tp, zt, u);
+        F.publish();
+        F.zc = S.dec.zc;
+        F.ic = S.dec.ic;
+        done = true;
+        break;
+      }
       const bool fin = !count || !use_p;
       if (fin && dt < band.lo) {  // min-p ends the kept tokens before the cut
         F.zc = zt;
@@ -922,7 +1224,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 #pragma unroll
       for (int q = 0; q < E::VW; ++q) {
         const bool in = j < F.sl.nv && F.in_set(z[q], i0 + q);
-        w[q] = in ? F.fixed_weight(z[q]) : 0;
+        w[q] = in ? F.draw_weight(z[q]) : 0;
         x += w[q];
         if (in) {
           last = i0 + q;
@@ -963,7 +1265,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     }
     if (lane == 0) {
       P.tokens[row] = token;
-      if (P.prob) P.prob[row] = static_cast<float>(static_cast<double>(F.fixed_weight(tz)) / static_cast<double>(S.dec.W));
+      if (P.prob) P.prob[row] = static_cast<float>(static_cast<double>(F.draw_weight(tz)) / static_cast<double>(S.dec.W));
     }
   }
 
@@ -1039,8 +1341,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   F.sc.gm = 0;
   F.zc = kNegMax;
   F.ic = INT_MAX;
-  F.fbits = 0;
-  F.unit = 1.f;
+  F.set_units();
   F.clear_hist(kBins);
   const float c = P.c;
   float s = 0.f;
@@ -1057,24 +1358,29 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   __syncthreads();
   F.merge(kBins);
   Band band;
-  if (!F.template find_bins<true>(k, 0, band)) {
+  uint64_t goal = k;
+  const bool enough = F.template find_bins<true>(goal, 0.f, band);
+  const int upto = enough ? S.before + static_cast<int>(S.total[band.hi]) : 0;
+  __syncthreads();
+  if (!enough) {
     band.by_key = false;
     band.hi = kBins - 1;
     band.edge = kNegMax;
-  } else if (S.before + S.total[band.hi] > kCap) {
+  } else if (upto > kCap) {
     F.cut(band, true, k, false, kNegMax, nullptr);
     F.clear_hist(0);
-    cluster_sync();
     band.by_key = false;
     band.hi = kBins - 1;
     band.edge = F.zc;
   }
   band.lo = 0;
   F.gather(band, false);
-  if (rank != 0) return;  // (nothing of the other CTAs is read from here on)
-  const int n = S.ngather;
-  F.sort(n);
-  const uint64_t* list = reinterpret_cast<const uint64_t*>(S.hist);
+  const int n = F.gathered();
+  if (rank == 0) F.pull(n);
+  cluster_sync();  // the other CTAs' lists have been read
+  if (rank != 0) return;
+  uint64_t* list = reinterpret_cast<uint64_t*>(S.total);
+  F.sort(list, n);
   for (int j = threadIdx.x; j < k; j += kRowThreads) {
     P.ids[row * k + j] = j < n ? static_cast<int32_t>(list[j] & 0xffffffffu) : -1;
     P.values[row * k + j] = j < n ? key_value(~static_cast<uint32_t>(list[j] >> 32)) : neg_inf();

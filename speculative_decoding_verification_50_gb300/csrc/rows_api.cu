@@ -49,13 +49,13 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
   return true;
 }
 
-// 2^(j/64) as an fp32 value and the relative remainder.
-PairTable make_table() {
-  PairTable t;
+BinTable make_table() {
+  BinTable t;
   for (int j = 0; j < kGrid; ++j) {
-    const double x = std::exp2(j / static_cast<double>(kGrid));
-    t.e[j].x = static_cast<float>(x);
-    t.e[j].y = static_cast<float>((x - static_cast<double>(t.e[j].x)) / static_cast<double>(t.e[j].x));
+    const long double x = std::exp2(static_cast<long double>(j) / kGrid);
+    t.e[j] = static_cast<uint64_t>(std::ldexp(x, 63));
+    t.p[j].x = static_cast<float>(x);
+    t.p[j].y = static_cast<float>((x - t.p[j].x) / x);
   }
   return t;
 }
@@ -115,7 +115,7 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   p.obs = a->filtered_batch_stride;
   p.ors = a->filtered_row_stride;
   p.status = a->row_status;
-  static const PairTable table = make_table();
+  static const BinTable table = make_table();
   p.tab = table;
   return launched(launch_sample_filter(a->dtype, smem, static_cast<cudaStream_t>(stream), p), "sample");
 }
