@@ -49,14 +49,11 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
   return true;
 }
 
+// 2^(63 + j/32).
 BinTable make_table() {
   BinTable t;
-  for (int j = 0; j < kGrid; ++j) {
-    const long double x = std::exp2(static_cast<long double>(j) / kGrid);
-    t.e[j] = static_cast<uint64_t>(std::ldexp(x, 63));
-    t.p[j].x = static_cast<float>(x);
-    t.p[j].y = static_cast<float>((x - t.p[j].x) / x);
-  }
+  for (int j = 0; j < kGrid; ++j)
+    t.e[j] = static_cast<uint64_t>(std::ldexp(std::exp2(static_cast<long double>(j) / kGrid), 63));
   return t;
 }
 
