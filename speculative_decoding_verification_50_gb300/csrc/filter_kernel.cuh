@@ -99,12 +99,14 @@ struct Scale {
   float shift, chi, clo;
   int gm;
 
-  // c = log2(e) / T.  bf16: chi has 16 digits, so that its products are exact.
+  // chi + clo = log2(e) / T, to about 2^-47.  bf16: chi has 16 digits, so that
+  // its products are exact.
   template <int DT>
-  __device__ void set_factor(double c) {
-    chi = static_cast<float>(c);
-    if (DT == 0) chi = __int_as_float(__float_as_int(chi) & 0xffffff00);
-    clo = static_cast<float>(c - static_cast<double>(chi));
+  __device__ void set_factor(float T) {
+    const float q = __fdiv_rn(1.44269502f, T);  // log2(e) = 1.44269502 + 1.925963e-8
+    const float rest = __fdiv_rn(fmaf(-q, T, 1.44269502f) + 1.925963e-8f, T);
+    chi = DT == 0 ? __int_as_float(__float_as_int(q) & 0xffffff00) : q;
+    clo = (q - chi) + rest;
   }
   __device__ void set_max(float m) {
     // |y| stays within the rounding trick's range; shifted logits are exact
@@ -181,7 +183,6 @@ struct FilterShared {
   uint32_t kmin, kmax;
   int32_t lo, hi;
   int32_t before;
-  Scale sc;
   float zf, zt;
   Decision dec;
 };
@@ -382,33 +383,37 @@ struct FilterRow {
   // and `mine` (the CTA's weight in bins before the band) with what tokens
   // above the band but in its bins add.  Ends with a cluster barrier.
   __device__ void collect(const Band& b, uint64_t mine) {
+    constexpr int VW = Elem<DT>::VW;
     int above = 0;
     uint64_t acc = 0;
     for (int j = lane; j < sl.nv; j += 32) {
-      float z[Elem<DT>::VW];
-      Elem<DT>::unpack(sl.data[sl.v0 + j], z);
-      bool zone = false;
+      const auto vec = sl.data[sl.v0 + j];
+      if (!(vec_max<DT>(vec, neg_inf()) >= b.elo)) continue;
+      float z[VW];
+      Elem<DT>::unpack(vec, z);
+      unsigned zone = 0;
 #pragma unroll
-      for (int k = 0; k < Elem<DT>::VW; ++k) {
+      for (int k = 0; k < VW; ++k) {
         above += z[k] >= b.ehi;
-        zone |= z[k] >= b.elo && z[k] < b.ehi;
+        zone |= z[k] >= b.elo && z[k] < b.ehi ? 1u << k : 0u;
       }
-      if (!zone) continue;
-      const int i0 = sl.base + (sl.v0 + j) * Elem<DT>::VW;
-#pragma unroll
-      for (int k = 0; k < Elem<DT>::VW; ++k) {
-        if (!(z[k] >= b.elo && z[k] < b.ehi) || !in_set(z[k], i0 + k)) continue;
-        const int pl = place(z[k], b);
+      while (zone) {  // (few: read again rather than kept in registers by number)
+        const int at = (sl.v0 + j) * VW + __ffs(zone) - 1;
+        zone &= zone - 1;
+        const float x = sl.at(at);
+        const int i = sl.base + at;
+        if (!in_set(x, i)) continue;
+        const int pl = place(x, b);
         if (pl == 0) {
           ++above;
-          if (!CLAMP && b.by_key && sc.template bin<false>(z[k]) >= b.lo) acc += weight(z[k]);
+          if (!CLAMP && b.by_key && sc.template bin<false>(x) >= b.lo) acc += weight(x);
         } else if (pl == 1) {
           const int pos = atomicAdd(&S.ncollect, 1);
           if (pos < kCap) {
-            own_list()[pos] = token_key(z[k], i0 + k);
+            own_list()[pos] = token_key(x, i);
           } else {  // (too many: the range of all of them is wanted)
-            atomicMin(&S.kmin, order_key(z[k]));
-            atomicMax(&S.kmax, order_key(z[k]));
+            atomicMin(&S.kmin, order_key(x));
+            atomicMax(&S.kmax, order_key(x));
           }
         }
       }
@@ -562,7 +567,7 @@ struct FilterRow {
       uint64_t w;
       before_band(above, w);
       if (n <= kCap) {
-        if (rank == 0) resolve(n, above, w, kind, goal, fin, zt, u);
+        if (rank == 0) resolve(b, n, above, w, kind, goal, fin, zt, u);
         publish();
         break;
       }
@@ -649,36 +654,27 @@ struct FilterRow {
 
   // Rank 0, the band collected: where the cut falls in it.  More tokens than
   // are sorted quickly are first split into bins of their own.
-  __device__ void resolve(int n, int above, uint64_t w, CutKind kind, uint64_t goal, bool fin, float zt, const float* u) {
+  __device__ void resolve(const Band& b, int n, int above, uint64_t w, CutKind kind, uint64_t goal, bool fin, float zt,
+                          const float* u) {
     const bool count = kind == kByCount;
+    if (n > kRowThreads / 2) {
+      reinterpret_cast<uint64_t*>(S.total)[threadIdx.x] = 0;
+      if (threadIdx.x == 0) {
+        S.lo = INT_MAX;
+        S.hi = 0;
+      }
+    }
     pull(n);
     if (n > 0) {
       uint64_t* sub = list();
       int m = n;
       if (count) w = above;
       if (n > kRowThreads / 2) {
-        // bins of the keys' range, a thread's each: counts or masses
+        // bins of the band's range of keys, a thread's each: counts or masses
         uint64_t* bin = reinterpret_cast<uint64_t*>(S.total);
-        uint32_t lo = 0xffffffffu, hi = 0;
-        for (int i = threadIdx.x; i < n; i += kRowThreads) {
-          lo = min(lo, static_cast<uint32_t>(list()[i] >> 32));
-          hi = max(hi, static_cast<uint32_t>(list()[i] >> 32));
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        bin[threadIdx.x] = 0;
-        if (threadIdx.x == 0) {
-          S.lo = INT_MAX;
-          S.hi = 0;
-        }
-        if (lane == 0) S.scratch[warp] = (static_cast<uint64_t>(lo) << 32) | hi;
-        __syncthreads();
-        for (int x = 0; x < kRowWarps; ++x) {
-          lo = min(lo, static_cast<uint32_t>(S.scratch[x] >> 32));
-          hi = max(hi, static_cast<uint32_t>(S.scratch[x]));
-        }
-        int shift = 0;
-        while (((hi - lo) >> shift) >= kRowThreads) ++shift;
+        const uint32_t lo = ~(b.by_key ? b.kmax : order_key(b.ehi));
+        const uint32_t hi = ~(b.by_key ? b.kmin : order_key(b.elo));
+        const int shift = max(0, 32 - __clz(hi - lo) - 9);
         for (int i = threadIdx.x; i < n; i += kRowThreads)
           atomicAdd(reinterpret_cast<unsigned long long*>(&bin[(static_cast<uint32_t>(list()[i] >> 32) - lo) >> shift]),
                     count ? 1ull : weight(token_logit(list()[i])));
@@ -688,15 +684,14 @@ struct FilterRow {
         const uint64_t before = w + block_scan(in_bin, S.scratch, all);
         if (in_bin && before + in_bin >= goal) atomicMin(&S.lo, static_cast<int>(threadIdx.x));
         __syncthreads();
-        const int at = min(S.lo, static_cast<int>((hi - lo) >> shift));
-        if (static_cast<int>(threadIdx.x) == at) S.scratch[0] = before;
-        __syncthreads();
-        w = S.scratch[0];
+        const int at = min(S.lo, kRowThreads - 1);
+        if (static_cast<int>(threadIdx.x) == at) S.fix[0] = before;
         sub = own_list();  // the tokens of that bin
         for (int i = threadIdx.x; i < n; i += kRowThreads)
           if (static_cast<int>((static_cast<uint32_t>(list()[i] >> 32) - lo) >> shift) == at)
             sub[atomicAdd(&S.hi, 1)] = list()[i];
         __syncthreads();
+        w = S.fix[0];
         m = S.hi;
       }
       if (threadIdx.x == 0) S.lo = m - 1;
@@ -906,11 +901,18 @@ struct FilterRow {
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < C) S.fix[threadIdx.x] = S.xmass[threadIdx.x];
     __syncthreads();
-    for (int i = threadIdx.x; i < n_list; i += kRowThreads) {
-      const uint64_t k = list()[i];
-      if (in_set(token_logit(k), token_index(k)))
-        atomicAdd(reinterpret_cast<unsigned long long*>(&S.fix[quotient(token_index(k) / Elem<DT>::VW, split.svec)]),
-                  weight(token_logit(k)));
+    for (int i0 = warp * 32; i0 < n_list; i0 += kRowThreads) {
+      const int i = i0 + lane;
+      const uint64_t k = i < n_list ? list()[i] : 0;
+      const bool in = i < n_list && in_set(token_logit(k), token_index(k));
+      const uint64_t x = in ? weight(token_logit(k)) : 0;
+      const int cta = in ? quotient(token_index(k) / Elem<DT>::VW, split.svec) : 0;
+      // one addition per CTA met, not per token (the list comes CTA by CTA)
+      const int first = __reduce_min_sync(0xffffffffu, in ? cta : kMaxCluster), last = __reduce_max_sync(0xffffffffu, cta);
+      for (int r = first; r <= last; ++r) {
+        const uint64_t s = warp_sum_u(in && cta == r ? x : 0);
+        if (lane == 0 && s) atomicAdd(reinterpret_cast<unsigned long long*>(&S.fix[r]), s);
+      }
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -1059,13 +1061,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   int bad = 0;
   if (!(T >= 0.f) || T > 3.4e38f) bad |= kBadTemp;
   if (k < 0 || !(tp >= 0.f && tp <= 1.f) || !(mp >= 0.f && mp <= 1.f)) bad |= kBadFilter;
-  // The row's scales in fp64, by one thread while the copies run.
+  // Thresholds below the maximum in fp64, by one thread while the copies run.
+  const float Tc = fmaxf(T, 1e-30f);
   double tf = 0, tm = 0;
   if (threadIdx.x == 0) {
-    const double Td = fmaxf(T, 1e-30f), lnf = -kWindow * 0.69314718055994530942;
-    S.sc.set_factor<DT>(1.4426950408889634074 / Td);
-    tf = Td * lnf;
-    tm = mp > 0.f ? Td * fmax(log(static_cast<double>(mp)), lnf) : tf;
+    const double lnf = -kWindow * 0.69314718055994530942;
+    tf = static_cast<double>(Tc) * lnf;
+    tm = mp > 0.f ? static_cast<double>(Tc) * fmax(log(static_cast<double>(mp)), lnf) : tf;
   }
   __syncthreads();
   if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.bad, kTimeout);
@@ -1111,7 +1113,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (P.status) P.status[row] = 0;
     }
   } else {
-    F.sc = S.sc;
+    F.sc.set_factor<DT>(Tc);
     F.sc.set_max(m);
     if (threadIdx.x == 0) {
       S.zf = __double2float_ru(static_cast<double>(m) + tf);

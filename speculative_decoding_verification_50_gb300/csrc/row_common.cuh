@@ -75,6 +75,20 @@ __device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, int
                     __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
 }
 
+// The maximum of a vector's logits, NaN if any is (bf16: in pairs).
+template <int DT>
+__device__ __forceinline__ float vec_max(const typename Elem<DT>::Vec& v, float m) {
+  if constexpr (DT == 0) {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return max3_nan(m, __uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  } else {
+    return max3_nan(max3_nan(m, v.x, v.y), v.z, v.w);
+  }
+}
+
 // One CTA's slice of a row.
 template <int DT>
 struct RowSlice {
@@ -168,15 +182,19 @@ struct RowSlice {
   // The maximum over the segment (all lanes), NaN if any logit is NaN.
   __device__ float warp_max() const {
     float m = neg_inf();
-    for (int j = lane; j < nv; j += 32) {
-      float z[E::VW];
-      E::unpack(data[v0 + j], z);
-#pragma unroll
-      for (int k = 0; k < E::VW; k += 2) m = max3_nan(m, z[k], z[k + 1]);
-    }
+#pragma unroll 4
+    for (int j = lane; j < nv; j += 32) m = vec_max<DT>(data[v0 + j], m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
+  }
+
+  // The logit at place i of the slice.
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (DT == 0)
+      return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(data)[i]) << 16);
+    else
+      return reinterpret_cast<const float*>(data)[i];
   }
 };
 
