@@ -489,51 +489,64 @@ def specv_check_hit(keys, accept_len, out_tokens, *, hit=None, stream=None):
 
 
 def _of(t, shape, dtype, what):
-    """t's pointer after a check of its type, shape, layout and (None: optional)."""
+    """t's pointer after a check of its type, shape and layout (None: optional)."""
     if t is None:
         return None
-    assert tuple(t.shape) == tuple(shape), f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}"
-    assert t.dtype == dtype, f"{what}: {t.dtype}, expected {dtype}"
-    assert t.is_contiguous(), f"{what} must be contiguous"
+    assert t.shape == shape and t.dtype is dtype and t.is_contiguous(), (
+        f"{what}: {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {tuple(shape)}")
     return t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    """The stream's handle (the device's current stream by default; asked for
+    directly, since a decode step makes many small calls)."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _cuda(t, what):
+    assert t.is_cuda and t.stride(-1) == 1, f"{what} must be a CUDA tensor with a contiguous last dimension"
 
 
 def _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, prob, kept, filtered,
                  row_status, stream):
     import torch
-    lib = load_library()
-    assert logits.dim() in (2, 3) and logits.stride(-1) == 1
-    lead = tuple(logits.shape[:-1])
-    B, V = lead[0], logits.shape[-1]
-    R = lead[1] if logits.dim() == 3 else 1
+    code = _dtype_code(logits)
+    shape = logits.shape
+    lead, V, flat = shape[:-1], shape[-1], len(shape) == 2
+    assert flat or len(shape) == 3, "logits must be [B, V] or [B, R, V]"
+    B, R = lead[0], 1 if flat else lead[1]
     f32, i32, dev = torch.float32, torch.int32, logits.device
-
-    def strides(t):
-        return (t.stride(0), t.stride(1) if t.dim() == 3 else max(t.stride(0), V))
-
+    per = (B,)
+    T = _of(temperature, per, f32, "temperature")
+    k, p, m = _of(top_k, per, i32, "top_k"), _of(top_p, per, f32, "top_p"), _of(min_p, per, f32, "min_p")
+    u = _of(uniforms, lead, f32, "uniforms")
+    out = {}
     if uniforms is not None:
-        tokens = torch.empty(lead, dtype=i32, device=dev) if tokens is None else tokens
-        prob = torch.empty(lead, dtype=f32, device=dev) if prob is None else prob
-    kept = torch.empty(lead, dtype=i32, device=dev) if kept is None else kept
-    row_status = torch.empty(lead, dtype=i32, device=dev) if row_status is None else row_status
+        out["tokens"] = tokens = torch.empty(lead, dtype=i32, device=dev) if tokens is None else tokens
+        out["prob"] = prob = torch.empty(lead, dtype=f32, device=dev) if prob is None else prob
+    out["kept"] = kept = torch.empty(lead, dtype=i32, device=dev) if kept is None else kept
+    out["row_status"] = row_status = (torch.empty(lead, dtype=i32, device=dev) if row_status is None
+                                      else row_status)
+    _cuda(logits, "logits")
+    st = logits.stride()
+    rs = max(st[-2], V)
+    bs = max(st[0], V) if flat else st[0]
+    fptr, fbs, frs = None, 0, 0
     if filtered is not None:
-        assert filtered.shape == logits.shape and filtered.dtype == logits.dtype
-        assert filtered.stride(-1) == 1
-    bs, rs = strides(logits)
-    fbs, frs = strides(filtered) if filtered is not None else (0, 0)
-    args = SampleArgs(B, R, V, _dtype_code(logits), logits.data_ptr(), bs, rs,
-                      _of(temperature, (B,), f32, "temperature"), _of(top_k, (B,), i32, "top_k"),
-                      _of(top_p, (B,), f32, "top_p"), _of(min_p, (B,), f32, "min_p"),
-                      _of(uniforms, lead, f32, "uniforms"), _of(tokens, lead, i32, "tokens"),
-                      _of(prob, lead, f32, "prob"), _of(kept, lead, i32, "kept"),
-                      None if filtered is None else filtered.data_ptr(), fbs, frs,
-                      _of(row_status, lead, i32, "row_status"))
-    _check(lib.specv_sample(ctypes.byref(args), _stream(stream)))
-    out = dict(kept=kept, row_status=row_status)
-    if uniforms is not None:
-        out.update(tokens=tokens, prob=prob)
-    if filtered is not None:
+        assert filtered.shape == shape and filtered.dtype is logits.dtype, "filtered must be like logits"
+        _cuda(filtered, "filtered")
+        fst = filtered.stride()
+        fptr, frs = filtered.data_ptr(), max(fst[-2], V)
+        fbs = max(fst[0], V) if flat else fst[0]
         out["filtered"] = filtered
+    args = SampleArgs(B, R, V, code, logits.data_ptr(), bs, rs, T, k, p, m, u,
+                      _of(tokens, lead, i32, "tokens"), _of(prob, lead, f32, "prob"),
+                      _of(kept, lead, i32, "kept"), fptr, fbs, frs,
+                      _of(row_status, lead, i32, "row_status"))
+    _check(load_library().specv_sample(ctypes.byref(args), _raw_stream(stream, dev)))
     return out
 
 
@@ -563,7 +576,7 @@ def specv_filter_logits(logits, temperature, *, top_k=None, top_p=None, min_p=No
     filtered, kept, row_status.
     """
     import torch
-    if filtered is None:
+    if filtered is None:  # (not empty_like: that keeps gaps between strided rows)
         filtered = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     return _sample_call(logits, temperature, None, top_k, top_p, min_p, None, None, kept, filtered,
                         row_status, stream)
@@ -576,8 +589,8 @@ def specv_top_logits(logits, k: int, *, temperature: float = 1.0, ids=None, valu
     (see include/specv.h).  Returns ids int32 [B, k], values fp32 [B, k], lse
     fp32 [B], row_status int32 [B]."""
     import torch
-    lib = load_library()
-    assert logits.dim() == 2 and logits.stride(-1) == 1
+    assert logits.dim() == 2
+    code = _dtype_code(logits)
     B, V = logits.shape
     f32, i32, dev = torch.float32, torch.int32, logits.device
     rows = max(int(k), 0)
@@ -585,17 +598,19 @@ def specv_top_logits(logits, k: int, *, temperature: float = 1.0, ids=None, valu
     values = torch.empty((B, rows), dtype=f32, device=dev) if values is None else values
     lse = torch.empty(B, dtype=f32, device=dev) if lse is None else lse
     row_status = torch.empty(B, dtype=i32, device=dev) if row_status is None else row_status
-    args = TopArgs(B, V, int(k), _dtype_code(logits), logits.data_ptr(), max(logits.stride(0), V),
+    _cuda(logits, "logits")
+    args = TopArgs(B, V, int(k), code, logits.data_ptr(), max(logits.stride(0), V),
                    float(temperature), _of(ids, (B, rows), i32, "ids"),
                    _of(values, (B, rows), f32, "values"), _of(lse, (B,), f32, "lse"),
                    _of(row_status, (B,), i32, "row_status"))
-    _check(lib.specv_top_logits(ctypes.byref(args), _stream(stream)))
+    _check(load_library().specv_top_logits(ctypes.byref(args), _raw_stream(stream, dev)))
     return dict(ids=ids, values=values, lse=lse, row_status=row_status)
 
 
 def _distill_args(logits, ids, values, teacher_lse, weights, temperature, tail, grad):
     import torch
-    assert logits.dim() == 2 and logits.stride(-1) == 1
+    assert logits.dim() == 2
+    code = _dtype_code(logits)
     N, V = logits.shape
     K = ids.shape[1]
     f32 = torch.float32
@@ -603,9 +618,11 @@ def _distill_args(logits, ids, values, teacher_lse, weights, temperature, tail, 
     assert ids.stride(-1) == 1 and values.stride(-1) == 1
     ts = max(ids.stride(0), K)
     assert N <= 1 or ids.stride(0) == values.stride(0), "teacher_ids and teacher_logits share one row stride"
+    _cuda(logits, "logits")
     if grad is not None:
-        assert grad.shape == logits.shape and grad.dtype == logits.dtype and grad.stride(-1) == 1
-    return DistillArgs(N, V, K, _dtype_code(logits), logits.data_ptr(), max(logits.stride(0), V),
+        assert grad.shape == logits.shape and grad.dtype == logits.dtype, "grad must be like logits"
+        _cuda(grad, "grad")
+    return DistillArgs(N, V, K, code, logits.data_ptr(), max(logits.stride(0), V),
                        ids.data_ptr(), values.data_ptr(), ts,
                        _of(teacher_lse, (N,), f32, "teacher_lse"),
                        _of(weights, (N,), f32, "weights"), float(temperature),
@@ -629,7 +646,6 @@ def specv_distill(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temp
     a buffer is given.
     """
     import torch
-    lib = load_library()
     N, dev = logits.shape[0], logits.device
     if grad is None and with_grad:
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
@@ -641,7 +657,7 @@ def specv_distill(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temp
     args.loss = _of(loss, (N,), torch.float32, "loss")
     args.stats = _of(stats, (N, 4), torch.float32, "stats")
     args.row_status = _of(row_status, (N,), torch.int32, "row_status")
-    _check(lib.specv_distill(ctypes.byref(args), _stream(stream)))
+    _check(load_library().specv_distill(ctypes.byref(args), _raw_stream(stream, dev)))
     out = dict(loss=loss, stats=stats, row_status=row_status)
     if grad is not None:
         out["grad"] = grad
@@ -654,7 +670,6 @@ def specv_distill_backward(logits, teacher_ids, teacher_logits, stats, *, grad_l
     """The gradient of (grad_loss * loss).sum() with respect to logits, from
     the stats of specv_distill on the same inputs (see include/specv.h)."""
     import torch
-    lib = load_library()
     N = logits.shape[0]
     if grad is None:
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
@@ -662,7 +677,7 @@ def specv_distill_backward(logits, teacher_ids, teacher_logits, stats, *, grad_l
                          tail, grad)
     args.stats = _of(stats, (N, 4), torch.float32, "stats")
     args.grad_loss = _of(grad_loss, (N,), torch.float32, "grad_loss")
-    _check(lib.specv_distill_backward(ctypes.byref(args), _stream(stream)))
+    _check(load_library().specv_distill_backward(ctypes.byref(args), _raw_stream(stream, logits.device)))
     return grad
 
 

@@ -383,22 +383,28 @@ struct FilterRow {
   // and `mine` (the CTA's weight in bins before the band) with what tokens
   // above the band but in its bins add.  Ends with a cluster barrier.
   __device__ void collect(const Band& b, uint64_t mine) {
-    constexpr int VW = Elem<DT>::VW;
+    constexpr int VW = Elem<DT>::VW, G = 32 / VW;  // vectors whose logits a mask of 32 bits covers
     int above = 0;
     uint64_t acc = 0;
-    for (int j = lane; j < sl.nv; j += 32) {
-      const auto vec = sl.data[sl.v0 + j];
-      if (!(vec_max<DT>(vec, neg_inf()) >= b.elo)) continue;
-      float z[VW];
-      Elem<DT>::unpack(vec, z);
+    for (int j0 = lane; j0 < sl.nv; j0 += 32 * G) {
       unsigned zone = 0;
 #pragma unroll
-      for (int k = 0; k < VW; ++k) {
-        above += z[k] >= b.ehi;
-        zone |= z[k] >= b.elo && z[k] < b.ehi ? 1u << k : 0u;
+      for (int g = 0; g < G; ++g) {
+        const int j = j0 + 32 * g;
+        if (j >= sl.nv) break;
+        const auto vec = sl.data[sl.v0 + j];
+        if (DT == 0 && !(vec_max<DT>(vec, neg_inf()) >= b.elo)) continue;
+        float z[VW];
+        Elem<DT>::unpack(vec, z);
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          above += z[k] >= b.ehi;
+          if (z[k] >= b.elo && z[k] < b.ehi) zone |= 1u << (g * VW + k);
+        }
       }
       while (zone) {  // (few: read again rather than kept in registers by number)
-        const int at = (sl.v0 + j) * VW + __ffs(zone) - 1;
+        const int bit = __ffs(zone) - 1;
+        const int at = (sl.v0 + j0 + 32 * (bit / VW)) * VW + bit % VW;
         zone &= zone - 1;
         const float x = sl.at(at);
         const int i = sl.base + at;

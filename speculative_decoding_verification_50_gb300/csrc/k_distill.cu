@@ -4,8 +4,8 @@
 namespace specv {
 
 cudaError_t launch_distill(int dtype, size_t smem, cudaStream_t s, const DistillParams& p) {
-  return dtype == SPECV_BF16 ? launch_rows(distill_kernel<0>, p.sp.C, p.N, smem, s, p)
-                             : launch_rows(distill_kernel<1>, p.sp.C, p.N, smem, s, p);
+  return dtype == SPECV_BF16 ? launch_rows<distill_kernel<0>>(p.sp.C, p.N, smem, s, p)
+                             : launch_rows<distill_kernel<1>>(p.sp.C, p.N, smem, s, p);
 }
 
 cudaError_t launch_distill_backward(int dtype, cudaStream_t s, const DistillParams& p) {

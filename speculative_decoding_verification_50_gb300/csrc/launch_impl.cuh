@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "launch.cuh"
 
@@ -65,13 +66,27 @@ cudaError_t launch_dependent(Kern k, int64_t blocks, size_t smem, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, k, p);
 }
 
-// One cluster of C CTAs of kRowThreads per row.
-template <typename Kern, typename Params>
-cudaError_t launch_rows(Kern k, int C, int64_t rows, size_t smem, cudaStream_t stream, const Params& p) {
-  cudaError_t e = allow_cluster(k, C);
+// One cluster of C CTAs of kRowThreads per row.  The kernel is a template
+// argument, so that each has its own record of the attributes set (they hold
+// for the life of the device's context): they are set again only where a call
+// needs more shared memory than any before it, or clusters beyond 8.
+template <auto K, typename Params>
+cudaError_t launch_rows(int C, int64_t rows, size_t smem, cudaStream_t stream, const Params& p) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> allowed[kDevices];
+  static std::mutex setting;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  const int bytes = static_cast<int>(smem);
+  if (dev >= kDevices || C > 8 || bytes > allowed[dev].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(setting);
+    const int most = dev < kDevices ? std::max(bytes, allowed[dev].load()) : bytes;
+    e = allow_cluster(K, C);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices) allowed[dev].store(most, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C), 1, 1);
   cfg.blockDim = dim3(kRowThreads, 1, 1);
@@ -84,7 +99,7 @@ cudaError_t launch_rows(Kern k, int C, int64_t rows, size_t smem, cudaStream_t s
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, p);
+  return cudaLaunchKernelEx(&cfg, K, p);
 }
 
 template <typename Kern, typename Params>
