@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
     }
     if (lane == 0) ured[warp] = v;
     if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
-    const float wm = sl.warp_max();
+    float own;
+    const float wm = sl.warp_max(own);
     if (lane == 0) mred[warp] = wm;
     if (bad) atomicOr(&badbits, bad);
     __syncthreads();  // ids, tl, pj, the copies, the sums

@@ -30,6 +30,10 @@ constexpr float kMagic = 393216.f;        // 1.5 * 2^18: adding it rounds to 1/3
 // Sums equal within 2^-36 (x >> 36) count as equal, so that equal weights which
 // meet a border exactly fall on its right side.
 constexpr int kSlack = 36;
+// The threads' maxima bound the k-th largest logit where there are at least
+// this many of them per token wanted (their k-th is then exceeded by about
+// 1.15 k logits).
+constexpr int kFewTop = 4;
 
 struct BinTable {
   uint64_t e[kGrid];  // 2^(63 + j/32)
@@ -59,7 +63,6 @@ struct TopParams {
   int32_t rows, k;
   const void* z;
   int64_t rs;
-  double invT;   // 1 / T
   float c;       // log2(e) / T
   int32_t* ids;
   float* values;
@@ -134,8 +137,37 @@ struct Scale {
     float g = __fadd_rn(p, -__fadd_rn(r, -kMagic));  // exact
     g = DT == 0 ? fmaf(x, clo, g) : g + fmaf(x, clo, fmaf(x, chi, -p));
     // 2^g - 1 for |g| <= 2^-6 (the next term is below 2^-39)
-    const float t = g * fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f);
-    return 0x80000000u + static_cast<uint32_t>(__float2int_rn(t * 2147483648.f));
+    const float t = __fmul_rn(g * 2147483648.f, fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f));
+    return 0x80000000u + static_cast<uint32_t>(__float2int_rn(t));
+  }
+  // weight() of two logits at once, in paired arithmetic.
+  template <int DT>
+  __device__ __forceinline__ void weights(uint64_t z, int& d0, int& d1, uint32_t& v0, uint32_t& v1) const {
+    const uint64_t x = f2_add(z, f2(-shift, -shift)), c = f2(chi, chi), magic = f2(kMagic, kMagic);
+    // The product is rounded by itself (a paired multiplication and the
+    // subtraction below came out fused: its rounding was counted twice).
+    float a, b;
+    f2_split(x, a, b);
+    const uint64_t p = f2(__fmul_rn(a, chi), __fmul_rn(b, chi));
+    const uint64_t r = f2_add(p, magic);
+    uint64_t g = f2_sub(p, f2_sub(r, magic));
+    if (DT == 0) {
+      g = f2_fma(x, f2(clo, clo), g);
+    } else {
+      const uint64_t pe = f2_sub(f2(0.f, 0.f), p);
+      g = f2_add(g, f2_fma(x, f2(clo, clo), f2_fma(x, c, pe)));
+    }
+    uint64_t t = f2_fma(g, f2(0.009618129f, 0.009618129f), f2(0.05550411f, 0.05550411f));
+    t = f2_fma(g, t, f2(0.24022651f, 0.24022651f));
+    t = f2_fma(g, t, f2(0.69314718f, 0.69314718f));
+    // (the scale by 2^31 is exact)
+    t = f2_mul(f2_mul(g, f2(2147483648.f, 2147483648.f)), t);
+    f2_split(r, a, b);
+    d0 = gm + __float_as_int(kMagic) - __float_as_int(a);
+    d1 = gm + __float_as_int(kMagic) - __float_as_int(b);
+    f2_split(t, a, b);
+    v0 = 0x80000000u + static_cast<uint32_t>(__float2int_rn(a));
+    v1 = 0x80000000u + static_cast<uint32_t>(__float2int_rn(b));
   }
   // A logit that every logit of bins <= d is at or above, with room for
   // rounding (side -1); that every logit at or above it has a bin < d (+1).
@@ -368,6 +400,22 @@ struct FilterRow {
     const int hi = min(S.hi, kBins - 1);
     set_band(b, min(S.lo, hi), hi);
     return true;
+  }
+
+  // Collects a superset of the set's k first tokens: the k-th largest of the
+  // threads' own maxima (`mine`) is a bound for the k-th largest logit, so a
+  // histogram of one value per thread takes the place of one of every logit.
+  // False where that names no band, or one too full to collect.
+  __device__ bool collect_top(int k, float mine, Band& b) {
+    if (mine >= zc) atomicAdd(&hist()[max(0, sc.template bin<CLAMP>(mine))], 1u);
+    __syncthreads();
+    merge<false>(kBins);
+    if (!find_bins<false>(static_cast<float>(k), b)) return false;
+    b.lo = 0;
+    b.ehi = pos_inf();
+    __syncthreads();  // (the histogram's place is the list's now)
+    collect(b, 0);
+    return collected() <= kCap;
   }
 
   __device__ void set_band(Band& b, int lo, int hi) const {
@@ -1077,7 +1125,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   }
   __syncthreads();
   if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.bad, kTimeout);
-  const float mc = block_max_nan(F.sl.warp_max(), S.fscratch);
+  float own;
+  const float mc = block_max_nan(F.sl.warp_max(own), S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);
   push_all(S.xbad, rank, C, S.bad);
@@ -1132,7 +1181,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     const bool use_k = k > 0 && k < V, use_p = tp < 1.f;
     Band band;
     bool done = false;
-    if (use_k) {
+    if (use_k && kFewTop * k <= C * kRowThreads) {
+      if (F.collect_top(k, own, band)) {
+        if (rank == 0) F.resolve_top(F.collected(), k, tp, zt, u);
+        F.publish();
+        F.zc = S.dec.zc;
+        F.ic = S.dec.ic;
+        done = true;
+      } else {
+        F.clear(2 * kBins);
+      }
+    }
+    if (use_k && !done) {
       F.sl.each([&](float z, int) {
         if (z >= zf) atomicAdd(&F.hist()[F.sc.template bin<false>(z)], 1u);
       });
@@ -1171,20 +1231,27 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       CutKind kind = kGiven;
       if (use_p || u) {
         const float cut = F.zc;
-        auto add = [&](float z) {
-          int d;
-          const uint32_t v = F.sc.template weight<DT>(z, d);
-          atomicAdd(&F.hist()[d], v >> 16);
-          atomicAdd(&F.hist()[kBins + d], v & 0xffffu);
+        const bool whole = F.ic == INT_MAX;
+        auto add = [&](float z, int i, int d, uint32_t v) {
+          if (z >= cut && (whole || F.in_set(z, i))) {
+            atomicAdd(&F.hist()[d], v >> 16);
+            atomicAdd(&F.hist()[kBins + d], v & 0xffffu);
+          }
         };
-        if (F.ic == INT_MAX) {
-          F.sl.each([&](float z, int) {
-            if (z >= cut) add(z);
-          });
-        } else {
-          F.sl.each([&](float z, int i) {
-            if (z >= cut && F.in_set(z, i)) add(z);
-          });
+        for (int j = lane; j < F.sl.nv; j += 32) {
+          uint64_t z[E::VW / 2];
+          unpack_pairs<DT>(F.sl.data[F.sl.v0 + j], z);
+          const int i0 = F.sl.base + (F.sl.v0 + j) * E::VW;
+#pragma unroll
+          for (int q = 0; q < E::VW / 2; ++q) {
+            int d0, d1;
+            uint32_t v0, v1;
+            float a, b;
+            F.sc.template weights<DT>(z[q], d0, d1, v0, v1);
+            f2_split(z[q], a, b);
+            add(a, i0 + 2 * q, d0, v0);
+            add(b, i0 + 2 * q + 1, d1, v1);
+          }
         }
         __syncthreads();
         F.template merge<true>(kBins);
@@ -1279,7 +1346,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   if (threadIdx.x == 0) S.bad = 0;
   F.clear(kBins);  // (a barrier)
   if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.bad, kTimeout);
-  const float mc = block_max_nan(F.sl.warp_max(), S.fscratch);
+  float own;
+  const float mc = block_max_nan(F.sl.warp_max(own), S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);
   push_all(S.xbad, rank, C, S.bad);
@@ -1310,12 +1378,26 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   F.sc.gm = 0;
   F.zc = kNegMax;
   F.ic = INT_MAX;
-  const float c = P.c;
+  // log-sum-exp: 2^(z c - ref), ref = max c rounded
+  const float c = P.c, ref = m * c;
+  const uint64_t c2 = f2(c, c), r2 = f2(-ref, -ref);
   float s = 0.f;
-  F.sl.each([&](float z, int) {
-    s += ex2((z - m) * c);
-    if (z >= kNegMax) atomicAdd(&F.hist()[max(F.sc.template bin<true>(z), 0)], 1u);
-  });
+  const bool plain = !(fabsf(ref) < 1e6f);  // (the rounding of ref alone would be a power of two too far)
+  if (plain) F.sl.each([&](float z, int) { s += ex2((z - m) * c); });
+#pragma unroll 2
+  for (int j = plain ? F.sl.nv : lane; j < F.sl.nv; j += 32) {
+    uint64_t z[E::VW / 2], t = 0;
+    unpack_pairs<DT>(F.sl.data[F.sl.v0 + j], z);
+#pragma unroll
+    for (int q = 0; q < E::VW / 2; ++q) {
+      float a, b;
+      f2_split(f2_fma(z[q], c2, r2), a, b);
+      t = f2_add(t, f2(ex2(a), ex2(b)));
+    }
+    float a, b;
+    f2_split(t, a, b);
+    s += a + b;
+  }
   s = warp_sum_f(s);
   if (lane == 0) S.fscratch[warp] = s;
   __syncthreads();
@@ -1323,21 +1405,29 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
 #pragma unroll
   for (int w = 0; w < kRowWarps; ++w) s += S.fscratch[w];
   push_all(S.xexp, rank, C, s);
-  F.template merge<false>(kBins);
   Band band;
-  if (!F.template find_bins<false>(static_cast<float>(k), band)) {
-    F.set_band(band, 0, kBins - 1);
-  } else if (S.before + static_cast<int>(S.total[band.hi]) > kCap) {
+  bool done = kFewTop * k <= C * kRowThreads && F.collect_top(k, own, band);
+  if (!done) {
+    if (kFewTop * k <= C * kRowThreads) F.clear(kBins);
+    F.sl.each([&](float z, int) {
+      if (z >= kNegMax) atomicAdd(&F.hist()[max(F.sc.template bin<true>(z), 0)], 1u);
+    });
     __syncthreads();
-    F.cut(band, kByCount, k, 0, false, kNegMax, nullptr);
-    F.clear(0);
-    F.set_band(band, 0, kBins - 1);
-    band.elo = F.zc;
+    F.template merge<false>(kBins);
+    if (!F.template find_bins<false>(static_cast<float>(k), band)) {
+      F.set_band(band, 0, kBins - 1);
+    } else if (S.before + static_cast<int>(S.total[band.hi]) > kCap) {
+      __syncthreads();
+      F.cut(band, kByCount, k, 0, false, kNegMax, nullptr);
+      F.clear(0);
+      F.set_band(band, 0, kBins - 1);
+      band.elo = F.zc;
+    }
+    __syncthreads();
+    band.lo = 0;
+    band.ehi = pos_inf();
+    F.collect(band, 0);
   }
-  __syncthreads();
-  band.lo = 0;
-  band.ehi = pos_inf();
-  F.collect(band, 0);
   const int n = F.collected();
   if (rank == 0) F.pull(n);
   cluster_sync();  // the other CTAs' lists have been read
@@ -1351,7 +1441,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   if (threadIdx.x == 0) {
     double t = 0;
     for (int r = 0; r < C; ++r) t += S.xexp[r];
-    if (P.lse) P.lse[row] = static_cast<float>(static_cast<double>(m) * P.invT + log(t));
+    if (P.lse) P.lse[row] = static_cast<float>((plain ? static_cast<double>(m) * c : static_cast<double>(ref)) * 0.69314718055994531 + log(t));
     if (P.status) P.status[row] = 0;
   }
 }

@@ -179,11 +179,13 @@ struct RowSlice {
     }
   }
 
-  // The maximum over the segment (all lanes), NaN if any logit is NaN.
-  __device__ float warp_max() const {
+  // The maximum over the segment (all lanes), NaN if any logit is NaN; `mine`:
+  // over this lane's logits.
+  __device__ float warp_max(float& mine) const {
     float m = neg_inf();
 #pragma unroll 4
     for (int j = lane; j < nv; j += 32) m = vec_max<DT>(data[v0 + j], m);
+    mine = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
@@ -275,6 +277,20 @@ __device__ __forceinline__ void store_warp(void* row, int i, int V, bool on, uin
       else reinterpret_cast<uint32_t*>(at)[k] = own[k % 4];
     }
   }
+}
+
+// A vector's logits as pairs of fp32 for the paired arithmetic.
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(const typename Elem<DT>::Vec& v, uint64_t (&z)[Elem<DT>::VW / 2]) {
+  float x[Elem<DT>::VW];
+  Elem<DT>::unpack(v, x);
+#pragma unroll
+  for (int k = 0; k < Elem<DT>::VW / 2; ++k) z[k] = f2(x[2 * k], x[2 * k + 1]);
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
 // v into slot[my rank] of every CTA of the cluster (threads 0..C-1 of the CTA
