@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
   char* grow = reinterpret_cast<char*>(P.grad) + row * P.grs * E::ES;
   RowSlice<DT> sl;
-  sl.init(smem, P.sp, rank);
+  sl.init(smem, P.sp, zrow, rank);
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;
   if (threadIdx.x == 0) badbits = again = 0;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   uint64_t mass = 0;        // sum of exp((t - tmax) / T), in units of 2^-40
   float tmax = 0.f, pscale = 0.f;
   if (!skip) {
-    sl.load(zrow, P.sp, &bars[warp]);
+    sl.load(&bars[warp]);
     // the teacher's entries, in every CTA
     int bad = 0;
     float mx = neg_inf();
@@ -180,9 +180,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     if (lane == 0) ured[warp] = v;
-    if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
     float own;
-    const float wm = sl.warp_max(own);
+    bool landed;
+    const float wm = sl.warp_max(&bars[warp], own, landed);
+    if (!landed) bad |= kTimeout;
     if (lane == 0) mred[warp] = wm;
     if (bad) atomicOr(&badbits, bad);
     __syncthreads();  // ids, tl, pj, the copies, the sums
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
     }
     for (int j = lane; j < sl.nv; j += 32) {
       float z[E::VW];
-      E::unpack(sl.data[sl.v0 + j], z);
+      E::unpack(sl.data[j], z);
       float x = 0.f;
 #pragma unroll
       for (int k = 0; k < E::VW; ++k) x += ex2((z[k] - mref) * c);
@@ -351,12 +352,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if (on && !dead) {
       float z[E::VW];
-      E::unpack(sl.data[sl.v0 + j], z);
+      E::unpack(sl.data[j], z);
 #pragma unroll
       for (int k = 0; k < E::VW; ++k) z[k] = ga * ex2((z[k] - mx) * c);
       w = pack_vec<DT>(z);
     }
-    store_warp<DT>(grow, sl.base + (sl.v0 + j) * E::VW, V, on, w);
+    store_warp<DT>(grow, sl.index(j), V, on, w);
   }
   if (dead) return;
   __syncthreads();  // the listed ids' gradients go over what was just written

@@ -10,9 +10,9 @@
 //
 // Whole numbers come out of the sums of weights 2^(y - max) (the cut, the
 // token), and a sum in plain fp32 moves the cut of a flat distribution in one
-// row of a hundred.  So a weight is 2^(-d/32) v 2^-31, d its bin and v a whole
-// number (good to about 2^-30, random): the bins sum v exactly, in two halves of
-// 16 bits, and totals are 64-bit integers in units of 2^-fbits of the largest
+// row of a hundred.  So a weight is 2^(-d/32) v 2^-28, d its bin and v a whole
+// number (good to 2^-29, random): the bins sum v exactly, in two halves of 14
+// bits (of up to 250,000 logits per CTA), and totals are 64-bit integers in units of 2^-fbits of the largest
 // weight.  (An SM does two fp64 operations a clock: a block's reductions in fp64
 // cost more than its passes over the row.)
 #pragma once
@@ -25,6 +25,7 @@ constexpr int kGrid = 32;                 // bins per unit of log2
 constexpr int kWindow = 48;               // units below the maximum that carry weight
 constexpr int kBins = kGrid * kWindow + 16;
 constexpr int kCap = 1024;                // tokens of a band that are worked on as a list
+constexpr int kMaxBinned = 250000;        // logits of a CTA, so that a bin's halves fit 32 bits
 constexpr int kBadFilter = 64;
 constexpr float kMagic = 393216.f;        // 1.5 * 2^18: adding it rounds to 1/32
 // Sums equal within 2^-36 (x >> 36) count as equal, so that equal weights which
@@ -137,8 +138,8 @@ struct Scale {
     float g = __fadd_rn(p, -__fadd_rn(r, -kMagic));  // exact
     g = DT == 0 ? fmaf(x, clo, g) : g + fmaf(x, clo, fmaf(x, chi, -p));
     // 2^g - 1 for |g| <= 2^-6 (the next term is below 2^-39)
-    const float t = __fmul_rn(g * 2147483648.f, fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f));
-    return 0x80000000u + static_cast<uint32_t>(__float2int_rn(t));
+    const float t = __fmul_rn(g * 268435456.f, fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f));
+    return 0x10000000u + static_cast<uint32_t>(__float2int_rn(t));
   }
   // weight() of two logits at once, in paired arithmetic.
   template <int DT>
@@ -160,14 +161,14 @@ struct Scale {
     uint64_t t = f2_fma(g, f2(0.009618129f, 0.009618129f), f2(0.05550411f, 0.05550411f));
     t = f2_fma(g, t, f2(0.24022651f, 0.24022651f));
     t = f2_fma(g, t, f2(0.69314718f, 0.69314718f));
-    // (the scale by 2^31 is exact)
-    t = f2_mul(f2_mul(g, f2(2147483648.f, 2147483648.f)), t);
+    // (the scale by 2^28 is exact)
+    t = f2_mul(f2_mul(g, f2(268435456.f, 268435456.f)), t);
     f2_split(r, a, b);
     d0 = gm + __float_as_int(kMagic) - __float_as_int(a);
     d1 = gm + __float_as_int(kMagic) - __float_as_int(b);
     f2_split(t, a, b);
-    v0 = 0x80000000u + static_cast<uint32_t>(__float2int_rn(a));
-    v1 = 0x80000000u + static_cast<uint32_t>(__float2int_rn(b));
+    v0 = 0x10000000u + static_cast<uint32_t>(__float2int_rn(a));
+    v1 = 0x10000000u + static_cast<uint32_t>(__float2int_rn(b));
   }
   // A logit that every logit of bins <= d is at or above, with room for
   // rounding (side -1); that every logit at or above it has a bin < d (+1).
@@ -265,9 +266,9 @@ struct FilterRow {
     return d < b.lo ? 0 : d <= b.hi ? 1 : 2;
   }
 
-  // v 2^-31 2^(-d/32) in units of 2^-fbits; v < 2^31 V.
+  // v 2^-28 2^(-d/32) in units of 2^-fbits; v < 2^28 V.
   __device__ __forceinline__ uint64_t mass(uint64_t v, int d) const {
-    const uint64_t x = __umul64hi(v << (fbits - 30), S.tab[(-d) & (kGrid - 1)]);
+    const uint64_t x = __umul64hi(v << (fbits - 27), S.tab[(-d) & (kGrid - 1)]);
     const int s = (d + kGrid - 1) / kGrid;
     return s > 0 ? (x + (1ull << (s - 1))) >> s : x;
   }
@@ -276,6 +277,12 @@ struct FilterRow {
     int d;
     const uint32_t v = sc.template weight<DT>(z, d);
     return max(mass(v, d), uint64_t(1));
+  }
+
+  // The cluster's barrier.
+  __device__ __forceinline__ void sync_all() const {
+    if (C == 1) __syncthreads();
+    else cluster_sync();
   }
 
   // Exclusive prefix over the block's threads; `all` gets the total.
@@ -333,14 +340,17 @@ struct FilterRow {
   // cluster.  Barriers: the cluster's, twice.
   template <bool MASS>
   __device__ void merge(int bins) {
-    cluster_sync();
+    sync_all();
     const int per = (bins + C - 1) / C;
     const int b0 = rank * per, b1 = min(bins, b0 + per);
     for (int b = b0 + warp * 32; b < b1; b += kRowThreads) {
       const int d = b + lane;
       const bool on = d < b1;
       uint64_t v = 0;
-      for (int r0 = 0; r0 < C; r0 += 8) {  // loads of eight CTAs in flight
+      if (C == 1) {
+        if (on) v = MASS ? (static_cast<uint64_t>(hist()[d]) << 14) + hist()[kBins + d] : hist()[d];
+      }
+      for (int r0 = 0; C > 1 && r0 < C; r0 += 8) {  // loads of eight CTAs in flight
         uint32_t x[8], y[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -350,7 +360,7 @@ struct FilterRow {
           y[q] = MASS && read ? h[kBins + d] : 0u;
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v += MASS ? (static_cast<uint64_t>(x[q]) << 16) + y[q] : x[q];
+        for (int q = 0; q < 8; ++q) v += MASS ? (static_cast<uint64_t>(x[q]) << 14) + y[q] : x[q];
       }
       if (MASS) {
         v = v ? mass(v, d) : 0;
@@ -361,7 +371,7 @@ struct FilterRow {
       if (on)
         for (int r = 0; r < C; ++r) peer(S.total, r)[d] = f;
     }
-    cluster_sync();
+    sync_all();
   }
 
   // Bins -> the band between the first bin where the cut may lie and the first
@@ -431,19 +441,20 @@ struct FilterRow {
   // and `mine` (the CTA's weight in bins before the band) with what tokens
   // above the band but in its bins add.  Ends with a cluster barrier.
   __device__ void collect(const Band& b, uint64_t mine) {
-    constexpr int VW = Elem<DT>::VW, G = 32 / VW;  // vectors whose logits a mask of 32 bits covers
+    constexpr int VW = Elem<DT>::VW, G = 4;  // vectors loaded together, a mask bit for each logit
     int above = 0;
     uint64_t acc = 0;
     for (int j0 = lane; j0 < sl.nv; j0 += 32 * G) {
       unsigned zone = 0;
+      typename Elem<DT>::Vec vec[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (j0 + 32 * g < sl.nv) vec[g] = sl.vec(j0 + 32 * g);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const int j = j0 + 32 * g;
-        if (j >= sl.nv) break;
-        const auto vec = sl.data[sl.v0 + j];
-        if (DT == 0 && !(vec_max<DT>(vec, neg_inf()) >= b.elo)) continue;
+        if (j0 + 32 * g >= sl.nv || (DT == 0 && !(vec_max<DT>(vec[g], neg_inf()) >= b.elo))) continue;
         float z[VW];
-        Elem<DT>::unpack(vec, z);
+        Elem<DT>::unpack(vec[g], z);
 #pragma unroll
         for (int k = 0; k < VW; ++k) {
           above += z[k] >= b.ehi;
@@ -452,10 +463,10 @@ struct FilterRow {
       }
       while (zone) {  // (few: read again rather than kept in registers by number)
         const int bit = __ffs(zone) - 1;
-        const int at = (sl.v0 + j0 + 32 * (bit / VW)) * VW + bit % VW;
+        const int j = j0 + 32 * (bit / VW);
         zone &= zone - 1;
-        const float x = sl.at(at);
-        const int i = sl.base + at;
+        const float x = sl.at(j, bit % VW);
+        const int i = sl.index(j) + bit % VW;
         if (!in_set(x, i)) continue;
         const int pl = place(x, b);
         if (pl == 0) {
@@ -486,7 +497,7 @@ struct FilterRow {
       peer(S.xcount, r)[rank] = n;
       peer(S.xmass, r)[rank] = mine + S.mass;
     }
-    cluster_sync();
+    sync_all();
   }
 
   // Tokens in the band collected last.
@@ -524,7 +535,7 @@ struct FilterRow {
     __syncthreads();
     push_all(S.xkmin, rank, C, S.kmin);
     push_all(S.xkmax, rank, C, S.kmax);
-    cluster_sync();
+    sync_all();
     for (int r = 0; r < C; ++r) {
       lo = min(lo, S.xkmin[r]);
       hi = max(hi, S.xkmax[r]);
@@ -912,11 +923,11 @@ struct FilterRow {
       for (int w = 0; w < warp; ++w) left -= S.iscratch[w];
       if (left >= 0 && left < mine) {  // this warp's segment
         for (int j0 = 0; j0 < sl.nv && left >= 0; j0 += 32) {
-          const int j = j0 + lane, i0 = sl.base + (sl.v0 + j) * Elem<DT>::VW;
+          const int j = j0 + lane, i0 = sl.index(j);
           float x[Elem<DT>::VW];
           int here = 0;
           if (j < sl.nv) {
-            Elem<DT>::unpack(sl.data[sl.v0 + j], x);
+            Elem<DT>::unpack(sl.vec(j), x);
 #pragma unroll
             for (int q = 0; q < Elem<DT>::VW; ++q) here += x[q] == z && in_set(x[q], i0 + q);
           }
@@ -937,7 +948,7 @@ struct FilterRow {
         }
       }
     }
-    cluster_sync();
+    sync_all();
   }
 
   // a / b for 0 <= a < 2^24.
@@ -1005,7 +1016,7 @@ struct FilterRow {
       const Decision d = S.dec;
       if (static_cast<int>(threadIdx.x) < C && threadIdx.x > 0) *peer(&S.dec, static_cast<int>(threadIdx.x)) = d;
     }
-    cluster_sync();
+    sync_all();
   }
 
   // The CTA that the token lies in: the first kept token whose running sum
@@ -1013,14 +1024,9 @@ struct FilterRow {
   __device__ void draw(uint64_t rem, uint64_t W, int32_t* token, float* prob) {
     constexpr int VW = Elem<DT>::VW;
     uint64_t mine = 0;
-    for (int j = lane; j < sl.nv; j += 32) {
-      float z[VW];
-      Elem<DT>::unpack(sl.data[sl.v0 + j], z);
-      const int i0 = sl.base + (sl.v0 + j) * VW;
-#pragma unroll
-      for (int q = 0; q < VW; ++q)
-        if (in_set(z[q], i0 + q)) mine += weight(z[q]);
-    }
+    sl.each([&](float z, int i) {
+      if (in_set(z, i)) mine += weight(z);
+    });
     mine = warp_sum_u(mine);
     __syncthreads();
     if (lane == 0) S.scratch[warp] = mine;
@@ -1037,10 +1043,10 @@ struct FilterRow {
     float lastz = 0.f, tz = 0.f;
     for (int j0 = 0; j0 < sl.nv; j0 += 32) {
       const int j = j0 + lane;
-      const int i0 = sl.base + (sl.v0 + j) * VW;
+      const int i0 = sl.index(j);
       float z[VW];
       uint64_t w[VW], x = 0;
-      if (j < sl.nv) Elem<DT>::unpack(sl.data[sl.v0 + j], z);
+      if (j < sl.nv) Elem<DT>::unpack(sl.vec(j), z);
 #pragma unroll
       for (int q = 0; q < VW; ++q) {
         const bool in = j < sl.nv && in_set(z[q], i0 + q);
@@ -1103,8 +1109,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   FilterRow<DT, false> F(S, P.sp);
   const int rank = F.rank, lane = F.lane, warp = F.warp;
   const char* zrow = reinterpret_cast<const char*>(P.z) + (b * P.bs + (row - b * P.R) * P.rs) * E::ES;
-  F.sl.init(smem, P.sp, rank);
-  F.sl.load(zrow, P.sp, &S.bars[warp]);
+  F.sl.init(smem, P.sp, zrow, rank);
+  F.sl.load(&S.bars[warp]);
   if (threadIdx.x < kGrid) S.tab[threadIdx.x] = P.tab.e[threadIdx.x];
   if (threadIdx.x == 0) S.bad = 0;
   const float T = P.temp[b];
@@ -1124,13 +1130,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     tm = mp > 0.f ? static_cast<double>(Tc) * fmax(log(static_cast<double>(mp)), lnf) : tf;
   }
   __syncthreads();
-  if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.bad, kTimeout);
   float own;
-  const float mc = block_max_nan(F.sl.warp_max(own), S.fscratch);
+  bool landed;
+  const float wm = F.sl.warp_max(&S.bars[warp], own, landed);
+  if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
+  const float mc = block_max_nan(wm, S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);
   push_all(S.xbad, rank, C, S.bad);
-  cluster_sync();
+  F.sync_all();
   float m = neg_inf();
   for (int r = 0; r < C; ++r) {
     m = max_nan(m, S.xmax[r]);
@@ -1157,7 +1165,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     __syncthreads();
     for (int w = 0; w < kRowWarps; ++w) first = min(first, S.iscratch[w]);
     push_all(S.xidx, rank, C, first);
-    cluster_sync();
+    F.sync_all();
     for (int r = 0; r < C; ++r) first = min(first, S.xidx[r]);
     F.zc = m;
     F.ic = first;
@@ -1234,14 +1242,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
         const bool whole = F.ic == INT_MAX;
         auto add = [&](float z, int i, int d, uint32_t v) {
           if (z >= cut && (whole || F.in_set(z, i))) {
-            atomicAdd(&F.hist()[d], v >> 16);
-            atomicAdd(&F.hist()[kBins + d], v & 0xffffu);
+            atomicAdd(&F.hist()[d], v >> 14);
+            atomicAdd(&F.hist()[kBins + d], v & 0x3fffu);
           }
         };
-        for (int j = lane; j < F.sl.nv; j += 32) {
+        F.sl.vecs([&](const typename E::Vec& vec, int j) {
           uint64_t z[E::VW / 2];
-          unpack_pairs<DT>(F.sl.data[F.sl.v0 + j], z);
-          const int i0 = F.sl.base + (F.sl.v0 + j) * E::VW;
+          unpack_pairs<DT>(vec, z);
+          const int i0 = F.sl.index(j);
 #pragma unroll
           for (int q = 0; q < E::VW / 2; ++q) {
             int d0, d1;
@@ -1252,7 +1260,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
             add(a, i0 + 2 * q, d0, v0);
             add(b, i0 + 2 * q + 1, d1, v1);
           }
-        }
+        });
         __syncthreads();
         F.template merge<true>(kBins);
         if (use_p) {
@@ -1275,7 +1283,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (use_p || u) {  // this CTA's weight in the bins before the band
         uint64_t x = 0;
         for (int d = threadIdx.x; d < min(band.lo, kBins); d += kRowThreads) {
-          const uint64_t v = (static_cast<uint64_t>(F.hist()[d]) << 16) + F.hist()[kBins + d];
+          const uint64_t v = (static_cast<uint64_t>(F.hist()[d]) << 14) + F.hist()[kBins + d];
           if (v) x += max(F.mass(v, d), uint64_t(1));
         }
         mine = F.block_sum_u(x);
@@ -1315,11 +1323,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   if (P.out) {
     char* orow = reinterpret_cast<char*>(P.out) + (b * P.obs + (row - b * P.R) * P.ors) * E::ES;
     for (int j0 = 0; j0 < F.sl.nv; j0 += 32) {
-      const int j = j0 + lane, i0 = F.sl.base + (F.sl.v0 + j) * E::VW;
+      const int j = j0 + lane, i0 = F.sl.index(j);
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (j < F.sl.nv) {
         float z[E::VW];
-        E::unpack(F.sl.data[F.sl.v0 + j], z);
+        E::unpack(F.sl.vec(j), z);
 #pragma unroll
         for (int q = 0; q < E::VW; ++q) z[q] = F.in_set(z[q], i0 + q) ? z[q] : neg_inf();
         w = pack_vec<DT>(z);
@@ -1341,17 +1349,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   FilterRow<DT, true> F(S, P.sp);
   const int rank = F.rank, lane = F.lane, warp = F.warp;
   const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
-  F.sl.init(smem, P.sp, rank);
-  F.sl.load(zrow, P.sp, &S.bars[warp]);
+  F.sl.init(smem, P.sp, zrow, rank);
+  F.sl.load(&S.bars[warp]);
   if (threadIdx.x == 0) S.bad = 0;
   F.clear(kBins);  // (a barrier)
-  if (!F.sl.load_wait(&S.bars[warp]) && lane == 0) atomicOr(&S.bad, kTimeout);
   float own;
-  const float mc = block_max_nan(F.sl.warp_max(own), S.fscratch);
+  bool landed;
+  const float wm = F.sl.warp_max(&S.bars[warp], own, landed);
+  if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
+  const float mc = block_max_nan(wm, S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);
   push_all(S.xbad, rank, C, S.bad);
-  cluster_sync();
+  F.sync_all();
   float m = neg_inf();
   int bad = 0;
   for (int r = 0; r < C; ++r) {
@@ -1384,20 +1394,20 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   float s = 0.f;
   const bool plain = !(fabsf(ref) < 1e6f);  // (the rounding of ref alone would be a power of two too far)
   if (plain) F.sl.each([&](float z, int) { s += ex2((z - m) * c); });
-#pragma unroll 2
-  for (int j = plain ? F.sl.nv : lane; j < F.sl.nv; j += 32) {
-    uint64_t z[E::VW / 2], t = 0;
-    unpack_pairs<DT>(F.sl.data[F.sl.v0 + j], z);
+  if (!plain)
+    F.sl.vecs([&](const typename E::Vec& vec, int) {
+      uint64_t z[E::VW / 2], t = 0;
+      unpack_pairs<DT>(vec, z);
 #pragma unroll
-    for (int q = 0; q < E::VW / 2; ++q) {
+      for (int q = 0; q < E::VW / 2; ++q) {
+        float a, b;
+        f2_split(f2_fma(z[q], c2, r2), a, b);
+        t = f2_add(t, f2(ex2(a), ex2(b)));
+      }
       float a, b;
-      f2_split(f2_fma(z[q], c2, r2), a, b);
-      t = f2_add(t, f2(ex2(a), ex2(b)));
-    }
-    float a, b;
-    f2_split(t, a, b);
-    s += a + b;
-  }
+      f2_split(t, a, b);
+      s += a + b;
+    });
   s = warp_sum_f(s);
   if (lane == 0) S.fscratch[warp] = s;
   __syncthreads();
@@ -1430,7 +1440,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   }
   const int n = F.collected();
   if (rank == 0) F.pull(n);
-  cluster_sync();  // the other CTAs' lists have been read
+  F.sync_all();  // the other CTAs' lists have been read
   if (rank != 0) return;
   const uint64_t* list = F.list();
   F.sort(F.list(), n);

@@ -5,7 +5,10 @@
 // result).  A cluster of C CTAs takes one row: each CTA copies its slice into
 // shared memory once (one bulk copy per warp's segment) and every pass after
 // that reads shared memory, so HBM sees each logit once.  CTAs exchange a few
-// values through distributed shared memory between cluster barriers.
+// values through distributed shared memory between cluster barriers.  With
+// enough rows to fill the SMs, sampling takes one CTA per row instead, of whose
+// row a part is held and the rest read again from L2 in each pass: the fixed
+// costs of a CTA and the waits of a cluster then come once per row.
 #pragma once
 
 #include "specv_common.cuh"
@@ -27,6 +30,7 @@ struct RowSplit {
   int32_t C;       // CTAs per row
   int32_t svec;    // vectors per CTA
   int32_t gvec;    // vectors per warp segment
+  int32_t rvec;    // of them, those held in shared memory (the first)
 };
 
 __device__ __forceinline__ int cluster_rank() {
@@ -89,19 +93,21 @@ __device__ __forceinline__ float vec_max(const typename Elem<DT>::Vec& v, float 
   }
 }
 
-// One CTA's slice of a row.
+// One CTA's slice of a row, as one warp sees it: its segment.
 template <int DT>
 struct RowSlice {
   using E = Elem<DT>;
   using Vec = typename E::Vec;
-  Vec* data;      // shared memory, svec vectors
-  int v0;         // the segment's first vector, within the slice
-  int nv;         // its vectors
-  int base;       // index of the slice's first place in the row
+  Vec* data;        // the held vectors of the segment, in shared memory
+  const char* src;  // the segment in memory
+  int v0;           // the segment's first vector, within the slice
+  int nv, rv;       // its vectors; of them, those held
+  int base;         // index of the slice's first place in the row
+  int left;         // logits of the row from the segment's first on
+  int mis;          // bytes by which the row starts past a 16-byte boundary
   int lane;
 
-  __device__ void init(char* smem, const RowSplit& sp, int rank) {
-    data = reinterpret_cast<Vec*>(smem);
+  __device__ void init(char* smem, const RowSplit& sp, const void* row, int rank) {
     lane = threadIdx.x & 31;
     const int w = threadIdx.x >> 5;
     const int nvec = static_cast<int>((static_cast<int64_t>(sp.V) + E::VW - 1) / E::VW);
@@ -109,52 +115,59 @@ struct RowSlice {
     const int mine = max(0, min(sp.svec, nvec - first));
     v0 = min(w * sp.gvec, mine);
     nv = min((w + 1) * sp.gvec, mine) - v0;
+    rv = min(nv, sp.rvec);
     base = first * E::VW;
+    data = reinterpret_cast<Vec*>(smem) + w * sp.rvec;
+    left = sp.V - base - v0 * E::VW;
+    src = reinterpret_cast<const char*>(row) + static_cast<int64_t>(base + v0 * E::VW) * E::ES;
+    mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
   }
 
-  // Starts this warp's copies; load_wait() before the segment is read.  `bar`
-  // is the warp's own barrier.  Rows that start at a 16-byte boundary take one
-  // bulk copy; others are loaded in aligned vectors, two for each of the row's,
-  // and shifted.
-  __device__ void load(const void* row, const RowSplit& sp, uint64_t* bar) {
-    const int i0 = base + v0 * E::VW;  // the segment's first logit
-    const int full = max(0, min(nv, (sp.V - i0) / E::VW));
-    const char* src = reinterpret_cast<const char*>(row) + static_cast<int64_t>(i0) * E::ES;
-    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+  // Vector j of the segment from memory (-inf after the row's last logit).
+  // Rows that start past a 16-byte boundary: two aligned vectors, shifted.
+  __device__ __forceinline__ Vec fetch(int j) const {
+    union {
+      Vec v;
+      uint4 u;
+      typename E::Raw r[E::VW];
+    } x;
+    const char* at = src + static_cast<int64_t>(j) * 16 - mis;
+    // whole, with both aligned vectors inside the row
+    if (mis == 0 ? (j + 1) * E::VW <= left
+                 : (v0 + j + base > 0 && (j + 1) * E::VW + (16 - mis) / E::ES <= left)) {
+      x.u = __ldcg(reinterpret_cast<const uint4*>(at));
+      if (mis != 0) x.u = shift_bytes(x.u, __ldcg(reinterpret_cast<const uint4*>(at) + 1), mis);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E::VW; ++k)
+        x.r[k] = j * E::VW + k < left ? reinterpret_cast<const typename E::Raw*>(src)[j * E::VW + k] : E::neg_inf_raw();
+    }
+    return x.v;
+  }
+
+  // Vector j < nv, held or not.
+  __device__ __forceinline__ Vec vec(int j) const { return j < rv ? data[j] : fetch(j); }
+
+  // Starts this warp's copies; load_wait() before the held vectors are read.
+  // `bar` is the warp's own barrier.  Rows that start at a 16-byte boundary
+  // take one bulk copy.
+  __device__ void load(uint64_t* bar) {
+    const int full = mis == 0 ? max(0, min(rv, left / E::VW)) : 0;
     if (lane == 0) {
-      const uint32_t bytes = mis == 0 ? static_cast<uint32_t>(full) * 16u : 0u;
       mbar_init(bar, 1);
       fence_mbar_init();
-      mbar_arrive_expect_tx(bar, bytes);
-      if (bytes > 0) bulk_load(data + v0, src, bytes, bar);
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(full) * 16u);
+      if (full > 0) bulk_load(data, src, static_cast<uint32_t>(full) * 16u, bar, rv == nv);
     }
-    if (mis == 0) {
-      if (lane == 1 && full < nv) data[v0 + full] = E::gather(row, i0 + full * E::VW, sp.V);
-    } else {
-      constexpr int U = 4;
-      for (int j0 = lane; j0 < nv; j0 += 32 * U) {
-        uint4 a[U], b[U];
-        bool in[U];
+    constexpr int U = 4;
+    for (int j0 = full + lane; j0 < rv; j0 += 32 * U) {
+      Vec x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + 32 * u, i = i0 + j * E::VW;
-          // both aligned vectors lie inside the row
-          in[u] = j < nv && i * E::ES >= mis && static_cast<int64_t>(i) * E::ES - mis + 32 <= static_cast<int64_t>(sp.V) * E::ES;
-          if (in[u]) {
-            const uint4* p = reinterpret_cast<const uint4*>(src + static_cast<int64_t>(j) * 16 - mis);
-            a[u] = __ldg(p);
-            b[u] = __ldg(p + 1);
-          }
-        }
+      for (int u = 0; u < U; ++u)
+        if (j0 + 32 * u < rv) x[u] = fetch(j0 + 32 * u);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + 32 * u;
-          if (in[u])
-            *reinterpret_cast<uint4*>(data + v0 + j) = shift_bytes(a[u], b[u], mis);
-          else if (j < nv)
-            data[v0 + j] = E::gather(row, i0 + j * E::VW, sp.V);
-        }
-      }
+      for (int u = 0; u < U; ++u)
+        if (j0 + 32 * u < rv) data[j0 + 32 * u] = x[u];
     }
     __syncwarp();
   }
@@ -167,36 +180,71 @@ struct RowSlice {
     return ok;
   }
 
-  // f(z, index) over this lane's logits of the segment, padding (-inf) included.
+  // f(vector, its number) over this lane's vectors of the segment, loads two
+  // vectors ahead.
   template <typename Fn>
-  __device__ __forceinline__ void each(Fn&& f) const {
+  __device__ __forceinline__ void vecs(Fn&& f) const {
+    if (lane >= nv) return;
+    Vec a = vec(lane), b = a;
+    if (lane + 32 < nv) b = vec(lane + 32);
     for (int j = lane; j < nv; j += 32) {
-      float z[E::VW];
-      E::unpack(data[v0 + j], z);
-      const int i0 = base + (v0 + j) * E::VW;
-#pragma unroll
-      for (int k = 0; k < E::VW; ++k) f(z[k], i0 + k);
+      Vec c = b;
+      if (j + 64 < nv) c = vec(j + 64);
+      f(a, j);
+      a = b;
+      b = c;
     }
   }
 
+  // f(z, index) over this lane's logits of the segment, padding (-inf) included.
+  template <typename Fn>
+  __device__ __forceinline__ void each(Fn&& f) const {
+    vecs([&](const Vec& v, int j) {
+      float z[E::VW];
+      E::unpack(v, z);
+      const int i0 = index(j);
+#pragma unroll
+      for (int k = 0; k < E::VW; ++k) f(z[k], i0 + k);
+    });
+  }
+
+  // Index in the row of vector j's first logit.
+  __device__ __forceinline__ int index(int j) const { return base + (v0 + j) * E::VW; }
+
   // The maximum over the segment (all lanes), NaN if any logit is NaN; `mine`:
-  // over this lane's logits.
-  __device__ float warp_max(float& mine) const {
+  // over this lane's logits.  The vectors not held come first, while the copies
+  // of the others run; sets `landed` as load_wait.
+  __device__ float warp_max(uint64_t* bar, float& mine, bool& landed) {
     float m = neg_inf();
+    constexpr int U = 4;
+    int j = lane;
+    while (j < rv) j += 32;
+    for (; j < nv; j += 32 * U) {
+      Vec x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u] = fetch(min(j + 32 * u, nv - 1));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j + 32 * u < nv) m = vec_max<DT>(x[u], m);
+    }
+    landed = load_wait(bar);
 #pragma unroll 4
-    for (int j = lane; j < nv; j += 32) m = vec_max<DT>(data[v0 + j], m);
+    for (int i = lane; i < rv; i += 32) m = vec_max<DT>(data[i], m);
     mine = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
   }
 
-  // The logit at place i of the slice.
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (DT == 0)
-      return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(data)[i]) << 16);
-    else
-      return reinterpret_cast<const float*>(data)[i];
+  // Logit k of vector j of the segment.
+  __device__ __forceinline__ float at(int j, int k) const {
+    typename E::Raw r;
+    if (j < rv) r = reinterpret_cast<const typename E::Raw*>(data)[j * E::VW + k];
+    else r = j * E::VW + k < left ? reinterpret_cast<const typename E::Raw*>(src)[j * E::VW + k] : E::neg_inf_raw();
+    if constexpr (DT == 0) return __uint_as_float(static_cast<uint32_t>(r) << 16);
+    else return r;
   }
 };
 

@@ -35,7 +35,8 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
   const int64_t two = static_cast<int64_t>(kSmemSm / 2 - kSmemReserved - extra);
   const int64_t one = static_cast<int64_t>(kSmemCta - extra);
-  auto slice = [&](int C) { return (nvec + C - 1) / C * 16; };
+  auto segment = [&](int C) { return ((nvec + C - 1) / C + kRowWarps - 1) / kRowWarps; };
+  auto slice = [&](int C) { return segment(C) * kRowWarps * 16; };
   int C = 1;
   while (C < 8 && slice(C) > two) C *= 2;
   if (slice(C) > one) C = 16;
@@ -44,8 +45,26 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
   sp.V = V;
   sp.C = C;
   sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
-  sp.gvec = (sp.svec + kRowWarps - 1) / kRowWarps;
-  smem = static_cast<size_t>(sp.svec) * 16;
+  sp.gvec = static_cast<int32_t>(segment(C));
+  sp.rvec = sp.gvec;
+  smem = static_cast<size_t>(sp.gvec) * kRowWarps * 16;
+  return true;
+}
+
+// As split_row, but one CTA per row, of whose vectors as many are held as two
+// CTAs per SM leave room for, where there are rows enough for that.
+bool split_filter(int64_t rows, int32_t V, int32_t dtype, RowSplit& sp, size_t& smem) {
+  constexpr size_t extra = sizeof(FilterShared);
+  if (!split_row(rows, V, dtype, extra, sp, smem)) return false;
+  if (rows < api_sm_count() || V > kMaxBinned || sp.C == 1) return true;
+  const int vw = 16 / elem_bytes(dtype);
+  const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
+  sp.C = 1;
+  sp.svec = static_cast<int32_t>(nvec);
+  sp.gvec = static_cast<int32_t>((nvec + kRowWarps - 1) / kRowWarps);
+  const size_t room = kSmemSm / 2 - kSmemReserved - extra;
+  sp.rvec = static_cast<int32_t>(std::min<int64_t>(sp.gvec, static_cast<int64_t>(room / (16 * kRowWarps)) / 32 * 32));
+  smem = static_cast<size_t>(sp.rvec) * kRowWarps * 16;
   return true;
 }
 
@@ -92,7 +111,7 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   const int64_t rows = static_cast<int64_t>(B) * R;
   FilterParams p = {};
   size_t smem;
-  if (!split_row(rows, V, a->dtype, sizeof(FilterShared), p.sp, smem))
+  if (!split_filter(rows, V, a->dtype, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (rows * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B*R too large");
   p.rows = static_cast<int32_t>(rows);
@@ -135,7 +154,7 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   if (a->row_stride < V) return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
   TopParams p = {};
   size_t smem;
-  if (!split_row(B, V, a->dtype, sizeof(FilterShared), p.sp, smem))
+  if (!split_filter(B, V, a->dtype, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (static_cast<int64_t>(B) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B too large");
   p.rows = B;
