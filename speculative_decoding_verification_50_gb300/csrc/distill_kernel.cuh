@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
   char* grow = reinterpret_cast<char*>(P.grad) + row * P.grs * E::ES;
   RowSlice<DT> sl;
-  sl.init(smem, P.sp, zrow, rank);
+  sl.init(smem, P.sp, zrow, rank, warp);
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;
   if (threadIdx.x == 0) badbits = again = 0;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     if (lane == 0) ured[warp] = v;
-    float own;
+    float own[4];
     bool landed;
     const float wm = sl.warp_max(&bars[warp], own, landed);
     if (!landed) bad |= kTimeout;

@@ -26,6 +26,8 @@ constexpr int kWindow = 48;               // units below the maximum that carry 
 constexpr int kBins = kGrid * kWindow + 16;
 constexpr int kCap = 1024;                // tokens of a band that are worked on as a list
 constexpr int kMaxBinned = 250000;        // logits of a CTA, so that a bin's halves fit 32 bits
+constexpr int kMaxParts = 16;             // parts of a row that are summed apart: C * H
+constexpr int kMaxH = 4;
 constexpr int kBadFilter = 64;
 constexpr float kMagic = 393216.f;        // 1.5 * 2^18: adding it rounds to 1/32
 // Sums equal within 2^-36 (x >> 36) count as equal, so that equal weights which
@@ -141,35 +143,6 @@ struct Scale {
     const float t = __fmul_rn(g * 268435456.f, fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f));
     return 0x10000000u + static_cast<uint32_t>(__float2int_rn(t));
   }
-  // weight() of two logits at once, in paired arithmetic.
-  template <int DT>
-  __device__ __forceinline__ void weights(uint64_t z, int& d0, int& d1, uint32_t& v0, uint32_t& v1) const {
-    const uint64_t x = f2_add(z, f2(-shift, -shift)), c = f2(chi, chi), magic = f2(kMagic, kMagic);
-    // The product is rounded by itself (a paired multiplication and the
-    // subtraction below came out fused: its rounding was counted twice).
-    float a, b;
-    f2_split(x, a, b);
-    const uint64_t p = f2(__fmul_rn(a, chi), __fmul_rn(b, chi));
-    const uint64_t r = f2_add(p, magic);
-    uint64_t g = f2_sub(p, f2_sub(r, magic));
-    if (DT == 0) {
-      g = f2_fma(x, f2(clo, clo), g);
-    } else {
-      const uint64_t pe = f2_sub(f2(0.f, 0.f), p);
-      g = f2_add(g, f2_fma(x, f2(clo, clo), f2_fma(x, c, pe)));
-    }
-    uint64_t t = f2_fma(g, f2(0.009618129f, 0.009618129f), f2(0.05550411f, 0.05550411f));
-    t = f2_fma(g, t, f2(0.24022651f, 0.24022651f));
-    t = f2_fma(g, t, f2(0.69314718f, 0.69314718f));
-    // (the scale by 2^28 is exact)
-    t = f2_mul(f2_mul(g, f2(268435456.f, 268435456.f)), t);
-    f2_split(r, a, b);
-    d0 = gm + __float_as_int(kMagic) - __float_as_int(a);
-    d1 = gm + __float_as_int(kMagic) - __float_as_int(b);
-    f2_split(t, a, b);
-    v0 = 0x10000000u + static_cast<uint32_t>(__float2int_rn(a));
-    v1 = 0x10000000u + static_cast<uint32_t>(__float2int_rn(b));
-  }
   // A logit that every logit of bins <= d is at or above, with room for
   // rounding (side -1); that every logit at or above it has a bin < d (+1).
   __device__ __forceinline__ float edge(int d, int side) const {
@@ -185,10 +158,10 @@ struct Decision {
   int32_t ic;
   int32_t kept;
   int32_t fallback;
-  int32_t tie_cta, tie_rank;  // -1, or where the last kept of many equal logits lies
-  int32_t cta;                // -1, or the CTA that the token is to be drawn from
-  int32_t token;              // the token, if rank 0 has it (cta = -1)
-  uint64_t rem;               // u W less what lies before that CTA
+  int32_t tie_part, tie_rank; // -1, or where the last kept of many equal logits lies
+  int32_t part;               // -1, or the part that the token is to be drawn from
+  int32_t token;              // the token, if rank 0 has it (part = -1)
+  uint64_t rem;               // u W less what lies before that part
   uint64_t W;
   uint64_t weight;            // the token's
 };
@@ -196,13 +169,11 @@ struct Decision {
 struct FilterShared {
   uint64_t bars[kRowWarps];
   uint64_t tab[kGrid];
-  // The CTA's histogram (two halves); then the band's tokens that it collects,
-  // and in rank 0, behind them, those of all CTAs.
-  uint64_t work[2 * kCap];
   float total[kBins];        // the row's histogram; then, in rank 0, bins of the list
   uint64_t Z;                // the row's weight
-  // one value per CTA, pushed to every CTA
-  uint64_t xmass[kMaxCluster];
+  // one value per CTA, pushed to every CTA (xmass, xband: per part)
+  uint64_t xmass[kMaxParts];
+  int32_t xband[kMaxParts];
   float xmax[kMaxCluster], xexp[kMaxCluster];
   int32_t xbad[kMaxCluster], xidx[kMaxCluster], xabove[kMaxCluster], xcount[kMaxCluster];
   uint32_t xkmin[kMaxCluster], xkmax[kMaxCluster];
@@ -210,8 +181,10 @@ struct FilterShared {
   uint64_t scratch[kRowWarps];
   float fscratch[kRowWarps];
   int32_t iscratch[kRowWarps];
-  uint64_t fix[kMaxCluster];
-  uint64_t mass;             // of tokens above the band that share its bins
+  uint64_t fix[kMaxParts];
+  uint64_t mine[kMaxH];      // per part: the weight in the bins before the band
+  uint64_t mass[kMaxH];      // per part: of tokens above the band that share its bins
+  int32_t band[kMaxH];       // per part: the band's tokens
   int32_t above, ncollect, bad;
   uint32_t kmin, kmax;
   int32_t lo, hi;
@@ -220,6 +193,13 @@ struct FilterShared {
   Decision dec;
 };
 static_assert(2 * kBins <= 4 * kCap && 2 * kRowThreads <= kBins, "arrays that share memory fit");
+
+// Bytes of a CTA's work space, behind the held vectors: its parts' histograms
+// (two halves each); then the band's tokens that it collects, and in rank 0,
+// behind them, those of all CTAs.
+__host__ __device__ constexpr int work_bytes(int H) {
+  return H * 2 * kBins * 4 > 2 * kCap * 8 ? H * 2 * kBins * 4 : 2 * kCap * 8;
+}
 
 // The part of the set that the cut lies in: bins [lo, hi], by keys [kmin, kmax]
 // of them once it has been narrowed.  Tokens above it are certainly kept by the
@@ -238,21 +218,29 @@ template <int DT, bool CLAMP>
 struct FilterRow {
   FilterShared& S;
   RowSlice<DT> sl;
-  RowSplit split;
+  const RowSplit& split;  // (of the launch's arguments: no registers)
+  const int &C, &V, &H;
   Scale sc;
-  int rank, C, V, lane, warp;
+  char* smem;        // the held vectors
+  uint64_t* work;
+  int rank, lane, warp;
+  int sub;           // the part of the CTA's slice that this warp's segment belongs to
   float zc;
   int ic;
   int fbits;  // sums are in units of 2^-fbits, so that V weights stay below 2^62
 
-  __device__ FilterRow(FilterShared& s, const RowSplit& sp)
-      : S(s), split(sp), rank(cluster_rank()), C(sp.C), V(sp.V), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
+  __device__ FilterRow(FilterShared& s, const RowSplit& sp, char* shared, const void* z)
+      : S(s), split(sp), C(sp.C), V(sp.V), H(sp.H), smem(shared), rank(cluster_rank()), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
+    work = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(sp.rvec) * kRowWarps * 16);
+    sub = warp * sp.H / kRowWarps;
+    sl.init(smem, sp, z, rank, warp);
     fbits = min(44, 62 - (32 - __clz(V)));
   }
 
-  __device__ uint32_t* hist() const { return reinterpret_cast<uint32_t*>(S.work); }
-  __device__ uint64_t* own_list() const { return S.work; }
-  __device__ uint64_t* list() const { return S.work + kCap; }
+  __device__ __forceinline__ int shift_H() const { return H >> 1; }  // log2 of 1, 2, 4
+  __device__ uint32_t* hist(int part) const { return reinterpret_cast<uint32_t*>(work) + part * (2 * kBins); }
+  __device__ uint64_t* own_list() const { return work; }
+  __device__ uint64_t* list() const { return work + kCap; }
 
   __device__ __forceinline__ bool in_set(float z, int i) const { return z > zc || (z == zc && i <= ic); }
 
@@ -320,13 +308,16 @@ struct FilterRow {
     return x;
   }
 
-  // An empty histogram and no tokens collected.  Ends with a barrier.
-  __device__ void clear(int words) {
-    for (int b = threadIdx.x; b < words / 4; b += kRowThreads)
-      reinterpret_cast<uint4*>(S.work)[b] = make_uint4(0u, 0u, 0u, 0u);
+  // Empty histograms and no tokens collected.  Ends with a barrier.
+  __device__ void clear() {
+    for (int b = threadIdx.x; b < H * (kBins / 2); b += kRowThreads)
+      reinterpret_cast<uint4*>(work)[b] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x < kMaxH) {
+      S.mass[threadIdx.x] = 0;
+      S.band[threadIdx.x] = 0;
+    }
     if (threadIdx.x == 0) {
       S.Z = 0;
-      S.mass = 0;
       S.above = S.ncollect = 0;
       S.kmin = 0xffffffffu;
       S.kmax = 0;
@@ -337,25 +328,23 @@ struct FilterRow {
 
   // The row's histogram into S.total on every CTA, as counts or (MASS) masses,
   // whose exact sum goes to S.Z.  Each CTA adds up a share of the bins over the
-  // cluster.  Barriers: the cluster's, twice.
+  // cluster's parts.  Barriers: the cluster's, twice.
   template <bool MASS>
   __device__ void merge(int bins) {
     sync_all();
-    const int per = (bins + C - 1) / C;
+    const int per = (bins + C - 1) / C, parts = C * H;
     const int b0 = rank * per, b1 = min(bins, b0 + per);
     for (int b = b0 + warp * 32; b < b1; b += kRowThreads) {
       const int d = b + lane;
       const bool on = d < b1;
       uint64_t v = 0;
-      if (C == 1) {
-        if (on) v = MASS ? (static_cast<uint64_t>(hist()[d]) << 14) + hist()[kBins + d] : hist()[d];
-      }
-      for (int r0 = 0; C > 1 && r0 < C; r0 += 8) {  // loads of eight CTAs in flight
+      for (int p0 = 0; p0 < parts; p0 += 8) {  // loads of eight parts in flight
         uint32_t x[8], y[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const uint32_t* h = reinterpret_cast<const uint32_t*>(peer(S.work, min(r0 + q, C - 1)));
-          const bool read = on && r0 + q < C;
+          const int p = min(p0 + q, parts - 1);
+          const uint32_t* h = peer(hist(p & (H - 1)), p >> shift_H());
+          const bool read = on && p0 + q < parts;
           x[q] = read ? h[d] : 0u;
           y[q] = MASS && read ? h[kBins + d] : 0u;
         }
@@ -413,18 +402,20 @@ struct FilterRow {
   }
 
   // Collects a superset of the set's k first tokens: the k-th largest of the
-  // threads' own maxima (`mine`) is a bound for the k-th largest logit, so a
-  // histogram of one value per thread takes the place of one of every logit.
+  // threads' own maxima (`mine`, four each) is a bound for the k-th largest
+  // logit, so a histogram of those takes the place of one of every logit.
   // False where that names no band, or one too full to collect.
-  __device__ bool collect_top(int k, float mine, Band& b) {
-    if (mine >= zc) atomicAdd(&hist()[max(0, sc.template bin<CLAMP>(mine))], 1u);
+  __device__ bool collect_top(int k, const float (&mine)[4], Band& b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (mine[u] >= zc) atomicAdd(&hist(sub)[max(0, sc.template bin<CLAMP>(mine[u]))], 1u);
     __syncthreads();
     merge<false>(kBins);
     if (!find_bins<false>(static_cast<float>(k), b)) return false;
     b.lo = 0;
     b.ehi = pos_inf();
     __syncthreads();  // (the histogram's place is the list's now)
-    collect(b, 0);
+    collect(b);
     return collected() <= kCap;
   }
 
@@ -437,12 +428,12 @@ struct FilterRow {
   }
 
   // Collects the band's tokens, a list in each CTA; every CTA gets each CTA's
-  // numbers: tokens above the band and in it, the range of the latter's keys,
-  // and `mine` (the CTA's weight in bins before the band) with what tokens
-  // above the band but in its bins add.  Ends with a cluster barrier.
-  __device__ void collect(const Band& b, uint64_t mine) {
+  // numbers: tokens above the band and in it, and per part S.mine (its weight in
+  // bins before the band) with what tokens above the band but in its bins add.
+  // Ends with a cluster barrier.
+  __device__ void collect(const Band& b) {
     constexpr int VW = Elem<DT>::VW, G = 4;  // vectors loaded together, a mask bit for each logit
-    int above = 0;
+    int above = 0, in_band = 0;
     uint64_t acc = 0;
     for (int j0 = lane; j0 < sl.nv; j0 += 32 * G) {
       unsigned zone = 0;
@@ -473,6 +464,7 @@ struct FilterRow {
           ++above;
           if (!CLAMP && b.by_key && sc.template bin<false>(x) >= b.lo) acc += weight(x);
         } else if (pl == 1) {
+          ++in_band;
           const int pos = atomicAdd(&S.ncollect, 1);
           if (pos < kCap) {
             own_list()[pos] = token_key(x, i);
@@ -484,18 +476,26 @@ struct FilterRow {
       }
     }
     above = __reduce_add_sync(0xffffffffu, above);
-    if (lane == 0 && above) atomicAdd(&S.above, above);
+    in_band = __reduce_add_sync(0xffffffffu, in_band);
+    if (lane == 0) {
+      if (above) atomicAdd(&S.above, above);
+      if (in_band) atomicAdd(&S.band[sub], in_band);
+    }
     if (!CLAMP && __any_sync(0xffffffffu, acc != 0)) {
       acc = warp_sum_u(acc);
-      if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&S.mass), acc);
+      if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&S.mass[sub]), acc);
     }
     __syncthreads();
-    const int n = S.ncollect;
     if (threadIdx.x < static_cast<unsigned>(C)) {
       const int r = threadIdx.x;
       peer(S.xabove, r)[rank] = S.above;
-      peer(S.xcount, r)[rank] = n;
-      peer(S.xmass, r)[rank] = mine + S.mass;
+      peer(S.xcount, r)[rank] = S.ncollect;
+#pragma unroll
+      for (int h = 0; h < kMaxH; ++h)
+        if (h < H) {
+          peer(S.xband, r)[rank * H + h] = S.band[h];
+          peer(S.xmass, r)[rank * H + h] = S.mine[h] + S.mass[h];
+        }
     }
     sync_all();
   }
@@ -511,10 +511,8 @@ struct FilterRow {
   __device__ void before_band(int& above, uint64_t& w) const {
     above = 0;
     w = 0;
-    for (int r = 0; r < C; ++r) {
-      above += S.xabove[r];
-      w += S.xmass[r];
-    }
+    for (int r = 0; r < C; ++r) above += S.xabove[r];
+    for (int p = 0; p < C * H; ++p) w += S.xmass[p];
   }
 
   // A band that is too full: the range of its keys, on every CTA.
@@ -552,11 +550,11 @@ struct FilterRow {
     const uint32_t kmin = b.kmin, kmax = b.kmax;
     int shift = 0;
     while (((kmax - kmin) >> shift) >= static_cast<uint32_t>(bins)) ++shift;
-    clear(bins);
+    clear();
     sl.each([&](float z, int i) {
       if (z >= b.elo && z < b.ehi && in_set(z, i) && place(z, b) == 1) {
         const uint32_t key = order_key(z);
-        if (key >= kmin && key <= kmax) atomicAdd(&hist()[(kmax - key) >> shift], 1u);
+        if (key >= kmin && key <= kmax) atomicAdd(&hist(sub)[(kmax - key) >> shift], 1u);
       }
     });
     __syncthreads();
@@ -617,16 +615,16 @@ struct FilterRow {
   }
 
   // Cuts the set at the goal-th token, where the mass `goal` is reached, or
-  // (kGiven) at zt, starting from a band of bins, and sets zc, ic.  `mine`: the
-  // CTA's weight in bins before the band.  `fin`: the last cut, whose sums give
-  // the token as well (min-p's threshold zt is then part of it).
-  __device__ void cut(Band b, CutKind kind, uint64_t goal, uint64_t mine, bool fin, float zt, const float* u) {
+  // (kGiven) at zt, starting from a band of bins, and sets zc, ic.  `fin`: the
+  // last cut, whose sums give the token as well (min-p's threshold zt is then
+  // part of it).
+  __device__ void cut(Band b, CutKind kind, uint64_t goal, bool fin, float zt, const float* u) {
     for (int it = 0; it < 40; ++it) {  // (each turn shrinks the band; three are the usual most)
       if (fin && kind != kGiven && b.by_key && order_key(zt) > b.kmax) {  // min-p ends the kept tokens first
         set_given(b, zt);
         kind = kGiven;
       }
-      collect(b, mine);
+      collect(b);
       const int n = collected();
       int above;
       uint64_t w;
@@ -656,9 +654,70 @@ struct FilterRow {
     for (int t = threadIdx.x; t < n; t += kRowThreads) {
       int r = 0, i = t;
       while (i >= S.xcount[r]) i -= S.xcount[r++];
-      list()[t] = peer(S.work, r)[i];
+      list()[t] = peer(work, r)[i];
     }
     __syncthreads();
+  }
+
+  // Sorts n <= kCap tokens of own_list() or list() through bins of their range
+  // of keys, a thread's each: within a bin every token counts those before it.
+  // False (nothing done) where a bin is too full for that.
+  __device__ bool sort_by_bins(uint64_t* a, int n) {
+    uint32_t* count = reinterpret_cast<uint32_t*>(S.total);
+    uint32_t lo = 0xffffffffu, hi = 0;
+    constexpr int per = kCap / kRowThreads;
+    uint64_t x[per];
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      const int i = threadIdx.x + q * kRowThreads;
+      x[q] = i < n ? a[i] : ~0ull;
+      if (i < n) {
+        lo = min(lo, static_cast<uint32_t>(x[q] >> 32));
+        hi = max(hi, static_cast<uint32_t>(x[q] >> 32));
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    __syncthreads();  // (S.total and the scratch are free)
+    if (lane == 0) S.scratch[warp] = (static_cast<uint64_t>(lo) << 32) | hi;
+    count[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+      lo = min(lo, static_cast<uint32_t>(S.scratch[w] >> 32));
+      hi = max(hi, static_cast<uint32_t>(S.scratch[w]));
+    }
+    const int shift = max(0, 32 - __clz(hi - lo) - 9);
+    int at[per];
+#pragma unroll
+    for (int q = 0; q < per; ++q)
+      if (x[q] != ~0ull) at[q] = atomicAdd(&count[(static_cast<uint32_t>(x[q] >> 32) - lo) >> shift], 1u);
+    __syncthreads();
+    const uint32_t mine = count[threadIdx.x];
+    const bool full = __syncthreads_or(mine > 48);
+    if (full) return false;
+    uint32_t all;
+    const uint32_t start = block_scan(mine, reinterpret_cast<uint32_t*>(S.iscratch), all);
+    count[threadIdx.x] = start << 16 | mine;
+    __syncthreads();
+    // binned into place, then counted within the bin
+#pragma unroll
+    for (int q = 0; q < per; ++q)
+      if (x[q] != ~0ull) a[(count[(static_cast<uint32_t>(x[q] >> 32) - lo) >> shift] >> 16) + at[q]] = x[q];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < per; ++q)
+      if (x[q] != ~0ull) {
+        const uint32_t c = count[(static_cast<uint32_t>(x[q] >> 32) - lo) >> shift];
+        at[q] = c >> 16;
+        for (uint32_t j = c >> 16; j < (c >> 16) + (c & 0xffffu); ++j) at[q] += a[j] < x[q];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < per; ++q)
+      if (x[q] != ~0ull) a[at[q]] = x[q];
+    __syncthreads();
+    return true;
   }
 
   // Sorts n <= kCap tokens.
@@ -676,6 +735,7 @@ struct FilterRow {
       __syncthreads();
       return;
     }
+    if (sort_by_bins(a, n)) return;
     // two tokens a thread (places 2 t and 2 t + 1), steps below 64 within a warp
     uint64_t p = ~0ull, q = ~0ull;
     const int i = 2 * threadIdx.x;
@@ -794,7 +854,7 @@ struct FilterRow {
     if (lane == 0 && kept) atomicAdd(&S.above, kept);
     __syncthreads();
     if (threadIdx.x == 0) {
-      S.dec.tie_cta = -1;
+      S.dec.tie_part = -1;
       S.dec.zc = zc;
       S.dec.ic = ic;
       S.dec.kept = above + S.above;
@@ -833,7 +893,7 @@ struct FilterRow {
     zc = token_logit(list()[nk - 1]);
     ic = token_index(list()[nk - 1]);
     if (threadIdx.x == 0) {
-      S.dec.tie_cta = -1;
+      S.dec.tie_part = -1;
       S.dec.zc = zc;
       S.dec.ic = ic;
       S.dec.kept = nk;
@@ -873,7 +933,7 @@ struct FilterRow {
       last = __shfl_xor_sync(0xffffffffu, last, o) && last;
     }
     if (sub == 0 && i < nk && (fell ? last : before <= t && (t < before + wt[i] || last))) {
-      S.dec.cta = -1;
+      S.dec.part = -1;
       S.dec.token = idx;
       S.dec.weight = wt[i];
       S.dec.W = W;
@@ -883,7 +943,7 @@ struct FilterRow {
   }
 
   // Rank 0, a band of n > kCap equal logits: how many of them are kept, and
-  // which CTA holds the last one.
+  // which part holds the last one.
   __device__ void resolve_tie(int n, int above, uint64_t w, float z, CutKind kind, uint64_t goal, bool fin, float zt,
                               const float* u) {
     const bool count = kind == kByCount;
@@ -892,27 +952,27 @@ struct FilterRow {
     int nb = static_cast<int>(min(max((left_over + one - 1) / one, uint64_t(1)), static_cast<uint64_t>(n)));
     if (fin && z < zt) nb = 0;
     if (threadIdx.x == 0) {
-      S.dec.tie_cta = -1;
+      S.dec.tie_part = -1;
       S.dec.zc = nb > 0 ? z : zt;
       S.dec.ic = INT_MAX;
       S.dec.kept = above + nb;
       int left = nb;
-      for (int r = 0; r < C && left > 0; ++r) {
-        if (S.xcount[r] >= left) {
-          S.dec.tie_cta = r;
+      for (int p = 0; p < C * H && left > 0; ++p) {
+        if (S.xband[p] >= left) {
+          S.dec.tie_part = p;
           S.dec.tie_rank = left - 1;
           break;
         }
-        left -= S.xcount[r];
+        left -= S.xband[p];
       }
     }
     __syncthreads();
     if (fin && u) finish(0, nb, z, *u);
   }
 
-  // The index of the tie_rank-th logit equal to z in CTA tie_cta, to every CTA.
+  // The index of the tie_rank-th logit equal to z in part tie_part, to every CTA.
   __device__ void find_tie(float z) {
-    if (S.dec.tie_cta == rank) {
+    if (S.dec.tie_part >= 0 && S.dec.tie_part >> shift_H() == rank) {
       int mine = 0;
       sl.each([&](float x, int i) { mine += x == z && in_set(x, i); });
       mine = __reduce_add_sync(0xffffffffu, mine);
@@ -920,8 +980,9 @@ struct FilterRow {
       __syncthreads();
       if (lane == 0) S.iscratch[warp] = mine;
       __syncthreads();
-      for (int w = 0; w < warp; ++w) left -= S.iscratch[w];
-      if (left >= 0 && left < mine) {  // this warp's segment
+      const bool here_part = (S.dec.tie_part & (H - 1)) == sub;
+      for (int w = sub * (kRowWarps >> shift_H()); w < warp; ++w) left -= S.iscratch[w];
+      if (here_part && left >= 0 && left < mine) {  // this warp's segment
         for (int j0 = 0; j0 < sl.nv && left >= 0; j0 += 32) {
           const int j = j0 + lane, i0 = sl.index(j);
           float x[Elem<DT>::VW];
@@ -958,36 +1019,41 @@ struct FilterRow {
     return q + ((q + 1) * b <= a);
   }
 
-  // Rank 0: total weight of the kept tokens, and the CTA where the running sum
-  // in index order passes u times it.  Kept: the CTAs' weights above the band,
+  // Rank 0: total weight of the kept tokens, and the part where the running sum
+  // in index order passes u times it.  Kept: the parts' weights above the band,
   // those of the n_list collected tokens that zc, ic keep, and the first nt
   // logits equal to z.
   __device__ void finish(int n_list, int nt, float z, float u) {
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < C) S.fix[threadIdx.x] = S.xmass[threadIdx.x];
+    const int parts = C * H;
+    if (static_cast<int>(threadIdx.x) < parts) S.fix[threadIdx.x] = S.xmass[threadIdx.x];
     __syncthreads();
     for (int i0 = warp * 32; i0 < n_list; i0 += kRowThreads) {
       const int i = i0 + lane;
       const uint64_t k = i < n_list ? list()[i] : 0;
       const bool in = i < n_list && in_set(token_logit(k), token_index(k));
       const uint64_t x = in ? weight(token_logit(k)) : 0;
-      const int cta = in ? quotient(token_index(k) / Elem<DT>::VW, split.svec) : 0;
-      // one addition per CTA met, not per token (the list comes CTA by CTA)
-      const int first = __reduce_min_sync(0xffffffffu, in ? cta : kMaxCluster), last = __reduce_max_sync(0xffffffffu, cta);
-      for (int r = first; r <= last; ++r) {
-        const uint64_t s = warp_sum_u(in && cta == r ? x : 0);
-        if (lane == 0 && s) atomicAdd(reinterpret_cast<unsigned long long*>(&S.fix[r]), s);
+      int part = 0;
+      if (in) {
+        const int vec = token_index(k) / Elem<DT>::VW, cta = quotient(vec, split.svec);
+        part = cta * H + quotient(vec - cta * split.svec, split.gvec) * H / kRowWarps;
+      }
+      // one addition per part met, not per token
+      const int first = __reduce_min_sync(0xffffffffu, in ? part : kMaxParts), last = __reduce_max_sync(0xffffffffu, part);
+      for (int p = first; p <= last; ++p) {
+        const uint64_t s = warp_sum_u(in && part == p ? x : 0);
+        if (lane == 0 && s) atomicAdd(reinterpret_cast<unsigned long long*>(&S.fix[p]), s);
       }
     }
     __syncthreads();
     if (threadIdx.x == 0) {
       const uint64_t one = nt > 0 ? weight(z) : 0;
       uint64_t W = 0;
-      for (int r = 0; r < C; ++r) {
-        const int take = min(nt, S.xcount[r]);
-        if (nt > 0) S.fix[r] += one * static_cast<uint64_t>(take);
-        nt -= nt > 0 ? take : 0;
-        W += S.fix[r];
+      for (int p = 0; p < parts; ++p) {
+        const int take = nt > 0 ? min(nt, S.xband[p]) : 0;
+        if (take > 0) S.fix[p] += one * static_cast<uint64_t>(take);
+        nt -= take;
+        W += S.fix[p];
       }
       const bool fell = !(u < 1.f);
       // (whole numbers: a sum exceeds u W exactly if it exceeds its floor)
@@ -995,14 +1061,14 @@ struct FilterRow {
       t += t >> kSlack;
       uint64_t run = 0, before = 0;
       int at = 0;
-      for (int r = 0; r < C; ++r) {
-        if (S.fix[r] == 0) continue;
-        at = r;
+      for (int p = 0; p < parts; ++p) {
+        if (S.fix[p] == 0) continue;
+        at = p;
         before = run;
-        run += S.fix[r];
+        run += S.fix[p];
         if (!fell && run > t) break;
       }
-      S.dec.cta = at;
+      S.dec.part = at;
       S.dec.rem = fell ? ~0ull : t - before;
       S.dec.W = W;
       S.dec.fallback = fell;
@@ -1019,12 +1085,16 @@ struct FilterRow {
     sync_all();
   }
 
-  // The CTA that the token lies in: the first kept token whose running sum
-  // from the slice's start exceeds `rem`, or the last one.
-  __device__ void draw(uint64_t rem, uint64_t W, int32_t* token, float* prob) {
+  // The CTA that the token's part `p` lies in: the first kept token whose
+  // running sum from the part's start exceeds `rem`, or its last one.  Every
+  // warp takes a piece of the part.
+  __device__ void draw(const void* row, int p, uint64_t rem, uint64_t W, int32_t* token, float* prob) {
     constexpr int VW = Elem<DT>::VW;
+    const int per = kRowWarps >> shift_H();  // segments of the part
+    const RowSlice<DT> piece =
+        sl.part(smem, split, row, rank, (p & (H - 1)) * per + (warp >> shift_H()), warp & (H - 1), H);
     uint64_t mine = 0;
-    sl.each([&](float z, int i) {
+    piece.each([&](float z, int i) {
       if (in_set(z, i)) mine += weight(z);
     });
     mine = warp_sum_u(mine);
@@ -1038,18 +1108,18 @@ struct FilterRow {
       later |= w > warp && S.scratch[w] > 0;
     }
     if (mine == 0 || run > rem || (run + mine <= rem && later)) return;
-    // this warp's segment
+    // this warp's piece
     int last = -1, found = -1;
     float lastz = 0.f, tz = 0.f;
-    for (int j0 = 0; j0 < sl.nv; j0 += 32) {
+    for (int j0 = 0; j0 < piece.nv; j0 += 32) {
       const int j = j0 + lane;
-      const int i0 = sl.index(j);
+      const int i0 = piece.index(j);
       float z[VW];
       uint64_t w[VW], x = 0;
-      if (j < sl.nv) Elem<DT>::unpack(sl.vec(j), z);
+      if (j < piece.nv) Elem<DT>::unpack(piece.vec(j), z);
 #pragma unroll
       for (int q = 0; q < VW; ++q) {
-        const bool in = j < sl.nv && in_set(z[q], i0 + q);
+        const bool in = j < piece.nv && in_set(z[q], i0 + q);
         w[q] = in ? weight(z[q]) : 0;
         x += w[q];
         if (in) {
@@ -1083,7 +1153,7 @@ struct FilterRow {
       }
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (found < 0) {  // the segment's last kept token
+    if (found < 0) {  // the piece's last kept token
       const int most = __reduce_max_sync(0xffffffffu, last);
       const int who = __ffs(__ballot_sync(0xffffffffu, last == most)) - 1;
       found = most;
@@ -1106,13 +1176,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   const int64_t row = blockIdx.x / C;
   const int64_t b = row / P.R;
   cluster_arrive();  // waited for before the first remote write
-  FilterRow<DT, false> F(S, P.sp);
-  const int rank = F.rank, lane = F.lane, warp = F.warp;
   const char* zrow = reinterpret_cast<const char*>(P.z) + (b * P.bs + (row - b * P.R) * P.rs) * E::ES;
-  F.sl.init(smem, P.sp, zrow, rank);
+  FilterRow<DT, false> F(S, P.sp, smem, zrow);
+  const int rank = F.rank, lane = F.lane, warp = F.warp;
   F.sl.load(&S.bars[warp]);
   if (threadIdx.x < kGrid) S.tab[threadIdx.x] = P.tab.e[threadIdx.x];
   if (threadIdx.x == 0) S.bad = 0;
+  if (threadIdx.x < kMaxH) S.mine[threadIdx.x] = 0;
   const float T = P.temp[b];
   const int k = P.top_k ? P.top_k[b] : 0;
   const float tp = P.top_p ? P.top_p[b] : 1.f;
@@ -1130,7 +1200,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     tm = mp > 0.f ? static_cast<double>(Tc) * fmax(log(static_cast<double>(mp)), lnf) : tf;
   }
   __syncthreads();
-  float own;
+  float own[4];
   bool landed;
   const float wm = F.sl.warp_max(&S.bars[warp], own, landed);
   if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
@@ -1182,14 +1252,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       S.zf = __double2float_ru(static_cast<double>(m) + tf);
       S.zt = fmaxf(S.zf, __double2float_ru(static_cast<double>(m) + tm));
     }
-    F.clear(2 * kBins);  // (a barrier)
+    F.clear();  // (a barrier)
     const float zf = S.zf, zt = S.zt;
     F.zc = zf;
     F.ic = INT_MAX;
     const bool use_k = k > 0 && k < V, use_p = tp < 1.f;
     Band band;
     bool done = false;
-    if (use_k && kFewTop * k <= C * kRowThreads) {
+    if (use_k && kFewTop * k <= 4 * C * kRowThreads) {
       if (F.collect_top(k, own, band)) {
         if (rank == 0) F.resolve_top(F.collected(), k, tp, zt, u);
         F.publish();
@@ -1197,12 +1267,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
         F.ic = S.dec.ic;
         done = true;
       } else {
-        F.clear(2 * kBins);
+        F.clear();
       }
     }
     if (use_k && !done) {
       F.sl.each([&](float z, int) {
-        if (z >= zf) atomicAdd(&F.hist()[F.sc.template bin<false>(z)], 1u);
+        if (z >= zf) atomicAdd(&F.hist(F.sub)[F.sc.template bin<false>(z)], 1u);
       });
       __syncthreads();
       F.template merge<false>(kBins);
@@ -1212,7 +1282,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
         if (upto <= kCap) {  // few enough to collect: the rest is done on the list
           band.lo = 0;
           band.ehi = pos_inf();
-          F.collect(band, 0);
+          F.collect(band);
           if (rank == 0) F.resolve_top(F.collected(), k, tp, zt, u);
           F.publish();
           F.zc = S.dec.zc;
@@ -1229,38 +1299,33 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
               kind = kGiven;
             }
           }
-          F.cut(band, kind, k, 0, done, zt, u);
+          F.cut(band, kind, k, done, zt, u);
         }
       }
-      if (!done) F.clear(2 * kBins);
+      if (!done) F.clear();
     }
     if (!done) {
-      uint64_t goal = 0, mine = 0;
+      uint64_t goal = 0;
       CutKind kind = kGiven;
       if (use_p || u) {
         const float cut = F.zc;
         const bool whole = F.ic == INT_MAX;
-        auto add = [&](float z, int i, int d, uint32_t v) {
-          if (z >= cut && (whole || F.in_set(z, i))) {
-            atomicAdd(&F.hist()[d], v >> 14);
-            atomicAdd(&F.hist()[kBins + d], v & 0x3fffu);
-          }
+        uint32_t* hist = F.hist(F.sub);
+        auto add = [&](float z) {
+          int d;
+          const uint32_t v = F.sc.template weight<DT>(z, d);
+          atomicAdd(&hist[d], v >> 14);
+          atomicAdd(&hist[kBins + d], v & 0x3fffu);
         };
-        F.sl.vecs([&](const typename E::Vec& vec, int j) {
-          uint64_t z[E::VW / 2];
-          unpack_pairs<DT>(vec, z);
-          const int i0 = F.sl.index(j);
-#pragma unroll
-          for (int q = 0; q < E::VW / 2; ++q) {
-            int d0, d1;
-            uint32_t v0, v1;
-            float a, b;
-            F.sc.template weights<DT>(z[q], d0, d1, v0, v1);
-            f2_split(z[q], a, b);
-            add(a, i0 + 2 * q, d0, v0);
-            add(b, i0 + 2 * q + 1, d1, v1);
-          }
-        });
+        if (whole) {
+          F.sl.each([&](float z, int) {
+            if (z >= cut) add(z);
+          });
+        } else {
+          F.sl.each([&](float z, int i) {
+            if (z >= cut && F.in_set(z, i)) add(z);
+          });
+        }
         __syncthreads();
         F.template merge<true>(kBins);
         if (use_p) {
@@ -1280,19 +1345,29 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       } else if (kind == kGiven) {
         F.set_whole(band);
       }
-      if (use_p || u) {  // this CTA's weight in the bins before the band
+      if (use_p || u) {  // the parts' weights in the bins before the band
+        // (a part's bins shared by its own warps)
         uint64_t x = 0;
-        for (int d = threadIdx.x; d < min(band.lo, kBins); d += kRowThreads) {
-          const uint64_t v = (static_cast<uint64_t>(F.hist()[d]) << 14) + F.hist()[kBins + d];
+        const int width = kRowThreads / P.sp.H;
+        const uint32_t* hist = F.hist(F.sub);
+        for (int d = threadIdx.x % width; d < min(band.lo, kBins); d += width) {
+          const uint64_t v = (static_cast<uint64_t>(hist[d]) << 14) + hist[kBins + d];
           if (v) x += max(F.mass(v, d), uint64_t(1));
         }
-        mine = F.block_sum_u(x);
-        __syncthreads();  // the histogram's place is the list's now
+        x = warp_sum_u(x);
+        if (lane == 0) S.scratch[warp] = x;
+        __syncthreads();  // (and the histogram's place is the list's now)
+        if (static_cast<int>(threadIdx.x) < P.sp.H) {
+          const int per = kRowWarps / P.sp.H;
+          x = 0;
+          for (int w = 0; w < per; ++w) x += S.scratch[threadIdx.x * per + w];
+          S.mine[threadIdx.x] = x;
+        }
       }
       // (without a cut of its own, the set's)
       const float zg = kind == kGiven ? fmaxf(zt, F.zc) : zt;
       if (kind == kGiven && zt <= F.zc) {
-        F.collect(band, mine);
+        F.collect(band);
         if (rank == 0) {
           int above;
           uint64_t w;
@@ -1306,18 +1381,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
         }
         F.publish();
       } else {
-        F.cut(band, kind, goal, mine, true, zg, u);
+        F.cut(band, kind, goal, true, zg, u);
       }
     }
     if (rank == 0 && threadIdx.x == 0) {
       if (P.kept) P.kept[row] = S.dec.kept;
       if (P.status) P.status[row] = (u && S.dec.fallback) ? kFallback : 0;
-      if (u && S.dec.cta < 0) {
+      if (u && S.dec.part < 0) {
         P.tokens[row] = S.dec.token;
         if (P.prob) P.prob[row] = static_cast<float>(static_cast<double>(S.dec.weight) / static_cast<double>(S.dec.W));
       }
     }
-    if (u && S.dec.cta == rank) F.draw(S.dec.rem, S.dec.W, P.tokens + row, P.prob ? P.prob + row : nullptr);
+    if (u && S.dec.part >= 0 && S.dec.part >> F.shift_H() == rank)
+      F.draw(zrow, S.dec.part, S.dec.rem, S.dec.W, P.tokens + row, P.prob ? P.prob + row : nullptr);
   }
 
   if (P.out) {
@@ -1339,21 +1415,20 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 
 // One row per cluster: the k largest logits, in order, and the log-sum-exp.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopParams P) {
+__global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid_constant__ TopParams P) {
   using E = Elem<DT>;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) FilterShared S;
   const int C = P.sp.C, k = P.k;
   const int64_t row = blockIdx.x / C;
   cluster_arrive();
-  FilterRow<DT, true> F(S, P.sp);
+  FilterRow<DT, true> F(S, P.sp, smem, reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES);
   const int rank = F.rank, lane = F.lane, warp = F.warp;
-  const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
-  F.sl.init(smem, P.sp, zrow, rank);
   F.sl.load(&S.bars[warp]);
   if (threadIdx.x == 0) S.bad = 0;
-  F.clear(kBins);  // (a barrier)
-  float own;
+  if (threadIdx.x < kMaxH) S.mine[threadIdx.x] = 0;
+  F.clear();  // (a barrier)
+  float own[4];
   bool landed;
   const float wm = F.sl.warp_max(&S.bars[warp], own, landed);
   if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
@@ -1416,11 +1491,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
   for (int w = 0; w < kRowWarps; ++w) s += S.fscratch[w];
   push_all(S.xexp, rank, C, s);
   Band band;
-  bool done = kFewTop * k <= C * kRowThreads && F.collect_top(k, own, band);
+  bool done = kFewTop * k <= 4 * C * kRowThreads && F.collect_top(k, own, band);
   if (!done) {
-    if (kFewTop * k <= C * kRowThreads) F.clear(kBins);
+    if (kFewTop * k <= 4 * C * kRowThreads) F.clear();
     F.sl.each([&](float z, int) {
-      if (z >= kNegMax) atomicAdd(&F.hist()[max(F.sc.template bin<true>(z), 0)], 1u);
+      if (z >= kNegMax) atomicAdd(&F.hist(F.sub)[max(F.sc.template bin<true>(z), 0)], 1u);
     });
     __syncthreads();
     F.template merge<false>(kBins);
@@ -1428,15 +1503,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const TopPar
       F.set_band(band, 0, kBins - 1);
     } else if (S.before + static_cast<int>(S.total[band.hi]) > kCap) {
       __syncthreads();
-      F.cut(band, kByCount, k, 0, false, kNegMax, nullptr);
-      F.clear(0);
+      F.cut(band, kByCount, k, false, kNegMax, nullptr);
+      F.clear();
       F.set_band(band, 0, kBins - 1);
       band.elo = F.zc;
     }
     __syncthreads();
     band.lo = 0;
     band.ehi = pos_inf();
-    F.collect(band, 0);
+    F.collect(band);
   }
   const int n = F.collected();
   if (rank == 0) F.pull(n);

@@ -31,6 +31,7 @@ struct RowSplit {
   int32_t svec;    // vectors per CTA
   int32_t gvec;    // vectors per warp segment
   int32_t rvec;    // of them, those held in shared memory (the first)
+  int32_t H;       // parts of a CTA's slice that are summed apart (1, 2 or 4)
 };
 
 __device__ __forceinline__ int cluster_rank() {
@@ -107,9 +108,8 @@ struct RowSlice {
   int mis;          // bytes by which the row starts past a 16-byte boundary
   int lane;
 
-  __device__ void init(char* smem, const RowSplit& sp, const void* row, int rank) {
+  __device__ void init(char* smem, const RowSplit& sp, const void* row, int rank, int w) {
     lane = threadIdx.x & 31;
-    const int w = threadIdx.x >> 5;
     const int nvec = static_cast<int>((static_cast<int64_t>(sp.V) + E::VW - 1) / E::VW);
     const int first = rank * sp.svec;
     const int mine = max(0, min(sp.svec, nvec - first));
@@ -146,7 +146,11 @@ struct RowSlice {
   }
 
   // Vector j < nv, held or not.
-  __device__ __forceinline__ Vec vec(int j) const { return j < rv ? data[j] : fetch(j); }
+  __device__ __forceinline__ Vec vec(int j) const {
+    if (j >= rv && (mis != 0 || (j + 1) * E::VW > left)) return fetch(j);
+    const char* at = j < rv ? reinterpret_cast<const char*>(data) : src;
+    return *reinterpret_cast<const Vec*>(at + static_cast<int64_t>(j) * 16);
+  }
 
   // Starts this warp's copies; load_wait() before the held vectors are read.
   // `bar` is the warp's own barrier.  Rows that start at a 16-byte boundary
@@ -196,6 +200,21 @@ struct RowSlice {
     }
   }
 
+  // The q-th of n parts of warp w's segment.
+  __device__ RowSlice part(char* smem, const RowSplit& sp, const void* row, int rank, int w, int q, int n) const {
+    RowSlice s;
+    s.init(smem, sp, row, rank, w);
+    const int per = (s.nv + n - 1) / n, at = min(q * per, s.nv);
+    s.data += at;
+    s.src += static_cast<int64_t>(at) * 16;
+    s.v0 += at;
+    s.rv = max(0, s.rv - at);
+    s.nv = min(per, s.nv - at);
+    s.rv = min(s.rv, s.nv);
+    s.left -= at * E::VW;
+    return s;
+  }
+
   // f(z, index) over this lane's logits of the segment, padding (-inf) included.
   template <typename Fn>
   __device__ __forceinline__ void each(Fn&& f) const {
@@ -212,27 +231,28 @@ struct RowSlice {
   __device__ __forceinline__ int index(int j) const { return base + (v0 + j) * E::VW; }
 
   // The maximum over the segment (all lanes), NaN if any logit is NaN; `mine`:
-  // over this lane's logits.  The vectors not held come first, while the copies
-  // of the others run; sets `landed` as load_wait.
-  __device__ float warp_max(uint64_t* bar, float& mine, bool& landed) {
-    float m = neg_inf();
+  // over each quarter of this lane's vectors (in turn).  The vectors not held
+  // come first, while the copies of the others run; sets `landed` as load_wait.
+  __device__ float warp_max(uint64_t* bar, float (&mine)[4], bool& landed) {
     constexpr int U = 4;
-    int j = lane;
-    while (j < rv) j += 32;
-    for (; j < nv; j += 32 * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) mine[u] = neg_inf();
+    for (int j = lane + (max(rv - lane, 0) + 31) / 32 * 32; j < nv; j += 32 * U) {
       Vec x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        x[u] = fetch(min(j + 32 * u, nv - 1));
-      }
+      for (int u = 0; u < U; ++u)
+        if (j + 32 * u < nv) x[u] = vec(j + 32 * u);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (j + 32 * u < nv) m = vec_max<DT>(x[u], m);
+        if (j + 32 * u < nv) mine[u] = vec_max<DT>(x[u], mine[u]);
     }
     landed = load_wait(bar);
-#pragma unroll 4
-    for (int i = lane; i < rv; i += 32) m = vec_max<DT>(data[i], m);
-    mine = m;
+    for (int j = lane; j < rv; j += 32 * U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j + 32 * u < rv) mine[u] = vec_max<DT>(data[j + 32 * u], mine[u]);
+    }
+    float m = max_nan(max3_nan(mine[0], mine[1], mine[2]), mine[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;

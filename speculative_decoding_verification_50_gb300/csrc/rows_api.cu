@@ -47,24 +47,36 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
   sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
   sp.gvec = static_cast<int32_t>(segment(C));
   sp.rvec = sp.gvec;
+  sp.H = 1;
   smem = static_cast<size_t>(sp.gvec) * kRowWarps * 16;
   return true;
 }
 
-// As split_row, but one CTA per row, of whose vectors as many are held as two
-// CTAs per SM leave room for, where there are rows enough for that.
+// L2 that rows being read again may take.
+constexpr int64_t kL2Rows = 96 << 20;
+
+// The split for sampling and the top logits.  Few rows: as split_row.  With
+// rows for several waves of CTAs, as few CTAs per row as leave the rows in
+// flight to L2 (two CTAs run on an SM), since a CTA's fixed costs and a
+// cluster's waits then come less often per row; what a CTA does not hold is
+// read again in each pass, and four histograms per CTA keep the part of the row
+// small that a token is drawn from.
 bool split_filter(int64_t rows, int32_t V, int32_t dtype, RowSplit& sp, size_t& smem) {
-  constexpr size_t extra = sizeof(FilterShared);
-  if (!split_row(rows, V, dtype, extra, sp, smem)) return false;
-  if (rows < api_sm_count() || V > kMaxBinned || sp.C == 1) return true;
+  if (!split_row(rows, V, dtype, sizeof(FilterShared) + work_bytes(1), sp, smem)) return false;
+  smem += work_bytes(1);
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
-  sp.C = 1;
-  sp.svec = static_cast<int32_t>(nvec);
-  sp.gvec = static_cast<int32_t>((nvec + kRowWarps - 1) / kRowWarps);
-  const size_t room = kSmemSm / 2 - kSmemReserved - extra;
-  sp.rvec = static_cast<int32_t>(std::min<int64_t>(sp.gvec, static_cast<int64_t>(room / (16 * kRowWarps)) / 32 * 32));
-  smem = static_cast<size_t>(sp.rvec) * kRowWarps * 16;
+  const int64_t slots = 2LL * api_sm_count();
+  int C = 1;
+  while (C < 8 && (slots / C * nvec * 16 > kL2Rows || rows * C < 4 * slots || V / (C * kMaxH) > kMaxBinned)) C *= 2;
+  if (C * kMaxH > kMaxParts || C >= sp.C) return true;
+  const size_t room = kSmemSm / 2 - kSmemReserved - sizeof(FilterShared) - work_bytes(kMaxH);
+  sp.C = C;
+  sp.H = kMaxH;
+  sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
+  sp.gvec = (sp.svec + kRowWarps - 1) / kRowWarps;
+  sp.rvec = std::min(sp.gvec, static_cast<int32_t>(room / (16 * kRowWarps)) / 32 * 32);
+  smem = static_cast<size_t>(sp.rvec) * kRowWarps * 16 + work_bytes(kMaxH);
   return true;
 }
 
