@@ -432,20 +432,17 @@ struct FilterRow {
   // bins before the band) with what tokens above the band but in its bins add.
   // Ends with a cluster barrier.
   __device__ void collect(const Band& b) {
-    constexpr int VW = Elem<DT>::VW, G = 4;  // vectors loaded together, a mask bit for each logit
+    constexpr int VW = Elem<DT>::VW, G = 4;  // vectors looked at together, a mask bit for each logit
+    using Vec = typename Elem<DT>::Vec;
     int above = 0, in_band = 0;
     uint64_t acc = 0;
-    for (int j0 = lane; j0 < sl.nv; j0 += 32 * G) {
+    sl.template groups<G>([&](const Vec(&x)[G], int j0) {
       unsigned zone = 0;
-      typename Elem<DT>::Vec vec[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        if (j0 + 32 * g < sl.nv) vec[g] = sl.vec(j0 + 32 * g);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        if (j0 + 32 * g >= sl.nv || (DT == 0 && !(vec_max<DT>(vec[g], neg_inf()) >= b.elo))) continue;
+        if (DT == 0 && !(vec_max<DT>(x[g], neg_inf()) >= b.elo)) continue;
         float z[VW];
-        Elem<DT>::unpack(vec[g], z);
+        Elem<DT>::unpack(x[g], z);
 #pragma unroll
         for (int k = 0; k < VW; ++k) {
           above += z[k] >= b.ehi;
@@ -456,25 +453,25 @@ struct FilterRow {
         const int bit = __ffs(zone) - 1;
         const int j = j0 + 32 * (bit / VW);
         zone &= zone - 1;
-        const float x = sl.at(j, bit % VW);
+        const float z = sl.at(j, bit % VW);
         const int i = sl.index(j) + bit % VW;
-        if (!in_set(x, i)) continue;
-        const int pl = place(x, b);
+        if (!in_set(z, i)) continue;
+        const int pl = place(z, b);
         if (pl == 0) {
           ++above;
-          if (!CLAMP && b.by_key && sc.template bin<false>(x) >= b.lo) acc += weight(x);
+          if (!CLAMP && b.by_key && sc.template bin<false>(z) >= b.lo) acc += weight(z);
         } else if (pl == 1) {
           ++in_band;
           const int pos = atomicAdd(&S.ncollect, 1);
           if (pos < kCap) {
-            own_list()[pos] = token_key(x, i);
+            own_list()[pos] = token_key(z, i);
           } else {  // (too many: the range of all of them is wanted)
-            atomicMin(&S.kmin, order_key(x));
-            atomicMax(&S.kmax, order_key(x));
+            atomicMin(&S.kmin, order_key(z));
+            atomicMax(&S.kmax, order_key(z));
           }
         }
       }
-    }
+    });
     above = __reduce_add_sync(0xffffffffu, above);
     in_band = __reduce_add_sync(0xffffffffu, in_band);
     if (lane == 0) {
@@ -1470,18 +1467,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   const bool plain = !(fabsf(ref) < 1e6f);  // (the rounding of ref alone would be a power of two too far)
   if (plain) F.sl.each([&](float z, int) { s += ex2((z - m) * c); });
   if (!plain)
-    F.sl.vecs([&](const typename E::Vec& vec, int) {
-      uint64_t z[E::VW / 2], t = 0;
-      unpack_pairs<DT>(vec, z);
+    F.sl.template groups<4>([&](const typename E::Vec(&x)[4], int) {
 #pragma unroll
-      for (int q = 0; q < E::VW / 2; ++q) {
+      for (int u = 0; u < 4; ++u) {
+        uint64_t z[E::VW / 2], t = 0;
+        unpack_pairs<DT>(x[u], z);
+#pragma unroll
+        for (int q = 0; q < E::VW / 2; ++q) {
+          float a, b;
+          f2_split(f2_fma(z[q], c2, r2), a, b);
+          t = f2_add(t, f2(ex2(a), ex2(b)));
+        }
         float a, b;
-        f2_split(f2_fma(z[q], c2, r2), a, b);
-        t = f2_add(t, f2(ex2(a), ex2(b)));
+        f2_split(t, a, b);
+        s += a + b;
       }
-      float a, b;
-      f2_split(t, a, b);
-      s += a + b;
     });
   s = warp_sum_f(s);
   if (lane == 0) S.fscratch[warp] = s;

@@ -105,6 +105,7 @@ struct RowSlice {
   int nv, rv;       // its vectors; of them, those held
   int base;         // index of the slice's first place in the row
   int left;         // logits of the row from the segment's first on
+  int plain;        // vectors that one aligned load brings (none of a row that starts past a boundary)
   int mis;          // bytes by which the row starts past a 16-byte boundary
   int lane;
 
@@ -121,6 +122,7 @@ struct RowSlice {
     left = sp.V - base - v0 * E::VW;
     src = reinterpret_cast<const char*>(row) + static_cast<int64_t>(base + v0 * E::VW) * E::ES;
     mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+    plain = mis == 0 ? max(0, min(nv, left / E::VW)) : 0;
   }
 
   // Vector j of the segment from memory (-inf after the row's last logit).
@@ -147,10 +149,24 @@ struct RowSlice {
 
   // Vector j < nv, held or not.
   __device__ __forceinline__ Vec vec(int j) const {
-    if (j >= rv && (mis != 0 || (j + 1) * E::VW > left)) return fetch(j);
-    const char* at = j < rv ? reinterpret_cast<const char*>(data) : src;
-    return *reinterpret_cast<const Vec*>(at + static_cast<int64_t>(j) * 16);
+    if (j < rv) return data[j];
+    if (j < plain) return load_plain(j);
+    return fetch(j);
   }
+  __device__ __forceinline__ Vec load_plain(int j) const {
+    return *reinterpret_cast<const Vec*>(src + static_cast<int64_t>(j) * 16);
+  }
+  __device__ __forceinline__ static Vec none() {
+    union {
+      typename E::Raw r[E::VW];
+      Vec v;
+    } x;
+#pragma unroll
+    for (int k = 0; k < E::VW; ++k) x.r[k] = E::neg_inf_raw();
+    return x.v;
+  }
+  // This lane's first vector from number n on.
+  __device__ __forceinline__ int from(int n) const { return lane + (max(n - lane, 0) + 31) / 32 * 32; }
 
   // Starts this warp's copies; load_wait() before the held vectors are read.
   // `bar` is the warp's own barrier.  Rows that start at a 16-byte boundary
@@ -184,20 +200,40 @@ struct RowSlice {
     return ok;
   }
 
-  // f(vector, its number) over this lane's vectors of the segment, loads two
-  // vectors ahead.
-  template <typename Fn>
-  __device__ __forceinline__ void vecs(Fn&& f) const {
-    if (lane >= nv) return;
-    Vec a = vec(lane), b = a;
-    if (lane + 32 < nv) b = vec(lane + 32);
-    for (int j = lane; j < nv; j += 32) {
-      Vec c = b;
-      if (j + 64 < nv) c = vec(j + 64);
-      f(a, j);
-      a = b;
-      b = c;
+  // f(vectors, number of the first) over groups of U of this lane's vectors of
+  // the segment, 32 apart (-inf past its end): those held, those of memory.
+  template <int U, typename Fn>
+  __device__ __forceinline__ void held_groups(Fn&& f) const {
+#pragma unroll 1
+    for (int j = lane; j < rv; j += 32 * U) {
+      Vec x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = u == 0 || j + 32 * u < rv ? data[j + 32 * u] : none();
+      f(x, j);
     }
+  }
+  template <int U, typename Fn>
+  __device__ __forceinline__ void memory_groups(Fn&& f) const {
+    int j = from(rv);
+#pragma unroll 1
+    for (; j + 32 * (U - 1) < plain; j += 32 * U) {
+      Vec x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = load_plain(j + 32 * u);
+      f(x, j);
+    }
+#pragma unroll 1
+    for (; j < nv; j += 32 * U) {
+      Vec x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = j + 32 * u < nv ? fetch(j + 32 * u) : none();
+      f(x, j);
+    }
+  }
+  template <int U, typename Fn>
+  __device__ __forceinline__ void groups(Fn&& f) const {
+    held_groups<U>(f);
+    memory_groups<U>(f);
   }
 
   // The q-th of n parts of warp w's segment.
@@ -212,18 +248,22 @@ struct RowSlice {
     s.nv = min(per, s.nv - at);
     s.rv = min(s.rv, s.nv);
     s.left -= at * E::VW;
+    s.plain = s.mis == 0 ? max(0, min(s.nv, s.left / E::VW)) : 0;
     return s;
   }
 
   // f(z, index) over this lane's logits of the segment, padding (-inf) included.
   template <typename Fn>
   __device__ __forceinline__ void each(Fn&& f) const {
-    vecs([&](const Vec& v, int j) {
-      float z[E::VW];
-      E::unpack(v, z);
-      const int i0 = index(j);
+    groups<2>([&](const Vec(&x)[2], int j) {
 #pragma unroll
-      for (int k = 0; k < E::VW; ++k) f(z[k], i0 + k);
+      for (int u = 0; u < 2; ++u) {
+        float z[E::VW];
+        E::unpack(x[u], z);
+        const int i0 = index(j + 32 * u);
+#pragma unroll
+        for (int k = 0; k < E::VW; ++k) f(z[k], i0 + k);
+      }
     });
   }
 
@@ -234,24 +274,15 @@ struct RowSlice {
   // over each quarter of this lane's vectors (in turn).  The vectors not held
   // come first, while the copies of the others run; sets `landed` as load_wait.
   __device__ float warp_max(uint64_t* bar, float (&mine)[4], bool& landed) {
-    constexpr int U = 4;
 #pragma unroll
-    for (int u = 0; u < U; ++u) mine[u] = neg_inf();
-    for (int j = lane + (max(rv - lane, 0) + 31) / 32 * 32; j < nv; j += 32 * U) {
-      Vec x[U];
+    for (int u = 0; u < 4; ++u) mine[u] = neg_inf();
+    auto add = [&](const Vec(&x)[4], int) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + 32 * u < nv) x[u] = vec(j + 32 * u);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + 32 * u < nv) mine[u] = vec_max<DT>(x[u], mine[u]);
-    }
+      for (int u = 0; u < 4; ++u) mine[u] = vec_max<DT>(x[u], mine[u]);
+    };
+    memory_groups<4>(add);
     landed = load_wait(bar);
-    for (int j = lane; j < rv; j += 32 * U) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + 32 * u < rv) mine[u] = vec_max<DT>(data[j + 32 * u], mine[u]);
-    }
+    held_groups<4>(add);
     float m = max_nan(max3_nan(mine[0], mine[1], mine[2]), mine[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));

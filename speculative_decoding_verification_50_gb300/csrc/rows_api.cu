@@ -55,20 +55,29 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
 // L2 that rows being read again may take.
 constexpr int64_t kL2Rows = 96 << 20;
 
-// The split for sampling and the top logits.  Few rows: as split_row.  With
-// rows for several waves of CTAs, as few CTAs per row as leave the rows in
-// flight to L2 (two CTAs run on an SM), since a CTA's fixed costs and a
-// cluster's waits then come less often per row; what a CTA does not hold is
-// read again in each pass, and four histograms per CTA keep the part of the row
-// small that a token is drawn from.
-bool split_filter(int64_t rows, int32_t V, int32_t dtype, RowSplit& sp, size_t& smem) {
+// The split for sampling and the top logits.  Few rows: as split_row.  Rows that
+// fill the SMs' slots (two CTAs each): as few CTAs per row as leave the rows in
+// flight to L2, since a CTA's fixed costs and a cluster's waits then come less
+// often per row; what a CTA does not hold is read again in each pass, and four
+// histograms per CTA keep the part of the row small that a token is drawn from.
+// Measured (us; rows x V; C = 1, 2, held whole): sampling 576 x 152064 fp32 435,
+// 389, 667; 128 x 128256 bf16 91, 66, 79; 320 x 128256 bf16, where the second
+// wave is nearly empty, 190, 146, 114 (so `whole_waves`).  The 256 top logits of
+// 256 x 152064 bf16 42, 58, 70; of 64 rows 29, 25, 23; 100 of 333 x 50257 fp32
+// 58, 69, 78.
+bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool whole_waves, RowSplit& sp, size_t& smem) {
   if (!split_row(rows, V, dtype, sizeof(FilterShared) + work_bytes(1), sp, smem)) return false;
   smem += work_bytes(1);
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
   const int64_t slots = 2LL * api_sm_count();
+  auto fits = [&](int C) {
+    const int64_t n = rows * C;
+    return slots / C * nvec * 16 <= kL2Rows && V / (C * kMaxH) <= kMaxBinned && 5 * n >= 4 * slots &&
+           (!whole_waves || n <= slots || 2 * n >= 7 * slots);
+  };
   int C = 1;
-  while (C < 8 && (slots / C * nvec * 16 > kL2Rows || rows * C < 4 * slots || V / (C * kMaxH) > kMaxBinned)) C *= 2;
+  while (C < sp.C && !fits(C)) C *= 2;
   if (C * kMaxH > kMaxParts || C >= sp.C) return true;
   const size_t room = kSmemSm / 2 - kSmemReserved - sizeof(FilterShared) - work_bytes(kMaxH);
   sp.C = C;
@@ -123,7 +132,7 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   const int64_t rows = static_cast<int64_t>(B) * R;
   FilterParams p = {};
   size_t smem;
-  if (!split_filter(rows, V, a->dtype, p.sp, smem))
+  if (!split_filter(rows, V, a->dtype, true, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (rows * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B*R too large");
   p.rows = static_cast<int32_t>(rows);
@@ -166,7 +175,7 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   if (a->row_stride < V) return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
   TopParams p = {};
   size_t smem;
-  if (!split_filter(B, V, a->dtype, p.sp, smem))
+  if (!split_filter(B, V, a->dtype, false, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (static_cast<int64_t>(B) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B too large");
   p.rows = B;
