@@ -99,25 +99,44 @@ struct DistillPart {  // one CTA's share of a row
   int32_t bad, pad;
 };
 
-// The logit at place i of a slice, -inf left there.  What two threads take from
-// one place: the logit for one of them, -inf for the other.
+// g 2^((z - m) c) of a vector's logits, in their type.
 template <int DT>
-__device__ __forceinline__ float take(void* slice, int i) {
-  if (DT == 1) return __uint_as_float(atomicExch(reinterpret_cast<unsigned*>(slice) + i, 0xff800000u));
-  unsigned* w = reinterpret_cast<unsigned*>(slice) + i / 2;
-  const int sh = (i & 1) * 16;
-  unsigned old = *reinterpret_cast<volatile unsigned*>(w), seen;
-  do {
-    seen = old;
-    old = atomicCAS(w, seen, (seen & ~(0xffffu << sh)) | (0xff80u << sh));
-  } while (old != seen);
-  return __uint_as_float((old >> sh) << 16);
+__device__ __forceinline__ uint4 gradients(const typename Elem<DT>::Vec& v, uint64_t m2, uint64_t c2, uint64_t g2) {
+  constexpr int VW = Elem<DT>::VW;
+  uint64_t z[VW / 2];
+  unpack_pairs<DT>(v, z);
+  float x[VW];
+#pragma unroll
+  for (int k = 0; k < VW / 2; ++k) {
+    float a, b;
+    f2_split(f2_mul(f2_add(z[k], m2), c2), a, b);
+    f2_split(f2_mul(f2(ex2(a), ex2(b)), g2), x[2 * k], x[2 * k + 1]);
+  }
+  return pack_vec<DT>(x);
 }
 
-// Loss, statistics and (grad given) the gradient of the rows: a cluster per row.
+// Bytes of a CTA's work space behind the held vectors: a bit per logit of the
+// slice (the listed ids) and five words per teacher entry.
+__host__ __device__ constexpr size_t distill_bytes(int svec, int vw, int K) {
+  return (static_cast<size_t>(svec) * vw / 8 + 19) / 16 * 16 + static_cast<size_t>(K) * 20;
+}
+
+// The bits of vector v of the slice, a bit per logit.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillParams P) {
+__device__ __forceinline__ unsigned vector_bits(const unsigned char* bits, int v) {
+  if (DT == 0) return bits[v];
+  return (bits[v >> 1] >> ((v & 1) * 4)) & 15u;
+}
+
+// Loss, statistics and (grad given) the gradient of the rows: a cluster per
+// row.  One pass for the maximum and the sum of the logits that are not listed
+// (each thread's sum relative to its own running maximum, joined at the end),
+// one for the gradient.
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_constant__ DistillParams P) {
   using E = Elem<DT>;
+  using Vec = typename E::Vec;
+  constexpr int VW = E::VW;
   extern __shared__ __align__(16) char smem[];
   __shared__ uint64_t bars[kRowWarps];
   __shared__ float tred[kRowWarps], mred[kRowWarps], rred[kRowWarps], lred[kRowWarps], ared[kRowWarps];
@@ -138,18 +157,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;
   if (threadIdx.x == 0) badbits = again = 0;
-  int32_t* ids = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(P.sp.svec) * 16);
+  const int words = (P.sp.svec * VW + 31) / 32;
+  unsigned* bits = reinterpret_cast<unsigned*>(smem + static_cast<size_t>(P.sp.rvec) * kRowWarps * 16);
+  int32_t* ids = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(P.sp.rvec) * kRowWarps * 16 +
+                                            distill_bytes(P.sp.svec, VW, 0));
   float* tl = reinterpret_cast<float*>(ids + K);
   float* pj = tl + K;
   float* zj = pj + K;
   float* sj = zj + K;  // p of the entry's id, or -1: not its first entry
   const float ih = P.ih, il = P.il, c = P.c;
-  const int lo = sl.base, hi = lo + P.sp.svec * E::VW;  // the slice's indices
-  float L = 0.f, mc = 0.f;  // mc: the slice's maximum
-  uint64_t mass = 0;        // sum of exp((t - tmax) / T), in units of 2^-40
-  float tmax = 0.f, pscale = 0.f;
+  const int lo = sl.base, hi = min(V, lo + P.sp.svec * VW);  // the slice's indices
+  float L = 0.f, tmax = 0.f, pscale = 1.f;
+  uint64_t mass = 0;  // sum of pj, in units of 2^-40
+  float run = neg_inf(), sum = 0.f, zmax = neg_inf(), a = 0.f;
+  bool some = true;  // (without a log-sum-exp: there are entries)
   if (!skip) {
     sl.load(&bars[warp]);
+    for (int i = threadIdx.x; i < words; i += kRowThreads) bits[i] = 0;
     // the teacher's entries, in every CTA
     int bad = 0;
     float mx = neg_inf();
@@ -160,111 +184,122 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
       const bool there = id >= 0 && id < V;
       ids[j] = there ? id : -1;
       tl[j] = there ? t : neg_inf();
+      if (there && !(t < pos_inf())) bad |= kNonFinite;  // NaN or +inf
       if (there) mx = max_nan(mx, t);
     }
-    tmax = block_max_nan(mx, tred);
-    if (!(tmax < pos_inf())) bad |= kNonFinite;  // NaN or +inf
+    uint64_t v = 0;
     if (P.tlse) {
       L = P.tlse[row];
       if (!isfinite(L)) bad |= kNonFinite;
-    }
-    const bool some = tmax > neg_inf() && tmax < pos_inf();
-    uint64_t v = 0;
-    for (int j = threadIdx.x; j < K; j += kRowThreads) {
-      const float e = some && tl[j] > neg_inf() ? exp_over(tl[j] - tmax, ih, il) : 0.f;
-      pj[j] = e;
-      v += __float2ull_rn(e * kFixed);
+      // p = exp(t / T - L), the product's rounding to first order
+      for (int j = threadIdx.x; j < K; j += kRowThreads) {
+        const float t = tl[j], x = __fmul_rn(t, ih);
+        const float p = t > neg_inf() ? expf(x - L) * (1.f + fmaf(t, il, fmaf(t, ih, -x))) : 0.f;
+        pj[j] = p;
+        v += __float2ull_rn(fminf(p, 1e6f) * kFixed);
+      }
+    } else {  // relative to the largest, normalised below
+      tmax = block_max_nan(mx, tred);
+      some = tmax > neg_inf() && tmax < pos_inf();
+      for (int j = threadIdx.x; j < K; j += kRowThreads) {
+        const float e = some && tl[j] > neg_inf() ? exp_over(tl[j] - tmax, ih, il) : 0.f;
+        pj[j] = e;
+        v += __float2ull_rn(e * kFixed);
+      }
     }
     if ((threadIdx.x & ~31u) < static_cast<unsigned>(K)) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     if (lane == 0) ured[warp] = v;
-    float own[4];
-    bool landed;
-    const float wm = sl.warp_max(&bars[warp], own, landed);
-    if (!landed) bad |= kTimeout;
-    if (lane == 0) mred[warp] = wm;
-    if (bad) atomicOr(&badbits, bad);
-    __syncthreads();  // ids, tl, pj, the copies, the sums
-    mc = mred[0];
+    __syncthreads();  // ids, tl, pj, no bits, the sums
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-      mc = max_nan(mc, mred[w]);
-      mass += ured[w];
+    for (int w = 0; w < kRowWarps; ++w) mass += ured[w];
+    if (!P.tlse) {
+      const float S = static_cast<float>(mass) * (1.f / kFixed);
+      pscale = some && mass ? 1.f / S : 0.f;
+      L = some && mass ? tmax * ih + logf(S) : 0.f;
     }
-    // p_j = pscale * pj[j]
-    const float S = static_cast<float>(mass) * (1.f / kFixed);
-    if (!some) {
-      pscale = 0.f;
-    } else if (P.tlse) {
-      const float x = __fmul_rn(tmax, ih);
-      const float e = fmaf(tmax, il, fmaf(tmax, ih, -x));
-      pscale = expf(x - L) * (1.f + e);
-    } else {
-      pscale = 1.f / S;
-      L = tmax * ih + logf(S);
-    }
-  }
-  const float mref = mc > neg_inf() ? mc : 0.f;
-  float listed = 0.f, rest = 0.f, a = 0.f;
-  if (!skip) {
-    // The listed ids of this slice: their logits kept apart, -inf in place.
+    // The listed ids of this slice: their logits, and a bit for each.
     for (int j = threadIdx.x; j < K; j += kRowThreads) {
       const int id = ids[j];
       if (id < lo || id >= hi) continue;
-      const float z = take<DT>(smem, id - lo), p = pj[j] * pscale;
+      const float z = E::scalar(zrow, id), p = pj[j] * pscale;
+      const unsigned bit = 1u << ((id - lo) & 31);
+      if (atomicOr(&bits[(id - lo) >> 5], bit) & bit) again = 1;
       zj[j] = z;
       sj[j] = p;
-      if (z == neg_inf()) again = 1;  // -inf itself, or an id listed twice
-      listed += ex2((z - mref) * c);
+      zmax = max_nan(zmax, z);
       if (p > 0.f) a += p * ((tl[j] - z) * ih);
     }
     __syncthreads();
-    if (again) {  // rare: entries of one id share its logit, and the first its sum
-      listed = a = 0.f;
+    if (again) {  // rare: an id listed twice; its first entry stands for them
       for (int j = warp; j < K; j += kRowWarps) {
         const int id = ids[j];
         if (id < lo || id >= hi) continue;
         bool first;
         const float ps = same_id(ids, pj, K, j, lane, first) * pscale;
-        float z = neg_inf();
-        for (int i = lane; i < K; i += 32)
-          if (ids[i] == id) z = fmaxf(z, zj[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-        const float p = pj[j] * pscale;
-        if (lane == 0) {
-          if (first) listed += ex2((z - mref) * c);
-          if (p > 0.f) a += p * ((tl[j] - z) * ih);
-          sj[j] = first ? ps : -1.f;
-        }
+        if (lane == 0) sj[j] = first ? ps : -1.f;
       }
       __syncthreads();
-      for (int j = warp; j < K; j += kRowWarps) {  // (each id's logit to its first entry)
-        const int id = ids[j];
-        if (id < lo || id >= hi || sj[j] < 0.f) continue;
-        float z = neg_inf();
-        for (int i = lane; i < K; i += 32)
-          if (ids[i] == id) z = fmaxf(z, zj[i]);
+    }
+    // the logits that are not listed
+    const unsigned char* byte = reinterpret_cast<const unsigned char*>(bits);
+    const uint64_t c2 = f2(c, c);
+    auto add = [&](const Vec(&y)[2], int j) {
+      uint64_t z[2][VW / 2];
+      float top = run;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-        __syncwarp();
-        if (lane == 0) zj[j] = z;
+      for (int u = 0; u < 2; ++u) {
+        const unsigned listed = j + 32 * u < sl.nv ? vector_bits<DT>(byte, sl.v0 + j + 32 * u) : 0u;
+        if (listed) {
+          float x[VW];
+          E::unpack(y[u], x);
+#pragma unroll
+          for (int k = 0; k < VW; ++k) x[k] = (listed >> k) & 1u ? neg_inf() : x[k];
+#pragma unroll
+          for (int k = 0; k < VW / 2; ++k) {
+            z[u][k] = f2(x[2 * k], x[2 * k + 1]);
+            top = max3_nan(top, x[2 * k], x[2 * k + 1]);
+          }
+        } else {
+          unpack_pairs<DT>(y[u], z[u]);
+          top = vec_max<DT>(y[u], top);
+        }
       }
-    }
-    for (int j = lane; j < sl.nv; j += 32) {
-      float z[E::VW];
-      E::unpack(sl.data[j], z);
-      float x = 0.f;
+      const float ref = top > neg_inf() ? top : 0.f;
+      sum *= ex2((run - ref) * c);
+      run = top;
+      const uint64_t r2 = f2(-ref, -ref);
+      uint64_t t = 0;
 #pragma unroll
-      for (int k = 0; k < E::VW; ++k) x += ex2((z[k] - mref) * c);
-      rest += x;
-    }
-    rest = warp_sum_f(rest);
-    listed = warp_sum_f(listed);
-    a = warp_sum_f(a);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < VW / 2; ++k) {
+          float e0, e1;
+          f2_split(f2_mul(f2_add(z[u][k], r2), c2), e0, e1);
+          t = f2_add(t, f2(ex2(e0), ex2(e1)));
+        }
+      float e0, e1;
+      f2_split(t, e0, e1);
+      sum += e0 + e1;
+    };
+    sl.template memory_groups<2>(add);
+    if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
+    sl.template held_groups<2>(add);
+    if (bad) atomicOr(&badbits, bad);
   }
+  // the slice's maximum, listed ids included
+  const float mc = block_max_nan(max_nan(run, zmax), mred);
+  const float mref = mc > neg_inf() ? mc : 0.f;
+  float listed = 0.f;
+  if (!skip) {
+    for (int j = threadIdx.x; j < K; j += kRowThreads)
+      if (ids[j] >= lo && ids[j] < hi && sj[j] >= 0.f) listed += ex2((zj[j] - mref) * c);
+  }
+  float rest = warp_sum_f(sum > 0.f ? sum * ex2((run - mref) * c) : 0.f);
+  listed = warp_sum_f(listed);
+  a = warp_sum_f(a);
   if (lane == 0) {
     rred[warp] = rest;
     lred[warp] = listed;
@@ -284,7 +319,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
     }
     *peer(part + rank, static_cast<int>(threadIdx.x)) = mine;
   }
-  cluster_sync();
+  if (C == 1) __syncthreads();
+  else cluster_sync();
 
   if (threadIdx.x == 0) {  // the row's scalars
     float mx = neg_inf();
@@ -303,7 +339,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
     }
     const bool dead = skip || anybad || !finite;
     const float total = S_rest + S_listed, inv = 1.f / total;
-    // m = pscale * mass, r = 1 - m (to fp32's rounding of m)
     const float m = P.tlse ? pscale * (static_cast<float>(mass) * (1.f / kFixed)) : (mass ? 1.f : 0.f);
     float r = P.tail ? fmaf(-pscale, static_cast<float>(mass) * (1.f / kFixed), 1.f) : 0.f;
     if (r < kNoTail) r = 0.f;
@@ -346,18 +381,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   const float mx = row_max;
   const float f = wt * ih;
   const float ga = f * row_alpha;
-  for (int j0 = 0; j0 < sl.nv; j0 += 32) {
-    const int j = j0 + lane;
-    const bool on = j < sl.nv;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (on && !dead) {
-      float z[E::VW];
-      E::unpack(sl.data[j], z);
+  const uint64_t c2 = f2(c, c), m2 = f2(-mx, -mx), g2 = f2(ga, ga);
+  for (int j0 = 0; j0 < sl.nv; j0 += 64) {
+    Vec y[2];
 #pragma unroll
-      for (int k = 0; k < E::VW; ++k) z[k] = ga * ex2((z[k] - mx) * c);
-      w = pack_vec<DT>(z);
+    for (int u = 0; u < 2; ++u)
+      if (!dead && j0 + 32 * u + lane < sl.nv) y[u] = sl.vec(j0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = j0 + 32 * u + lane;
+      if (j0 + 32 * u >= sl.nv) break;
+      const bool on = j < sl.nv;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (on && !dead) w = gradients<DT>(y[u], m2, c2, g2);
+      store_warp<DT>(grow, sl.index(j), V, on, w);
     }
-    store_warp<DT>(grow, sl.index(j), V, on, w);
   }
   if (dead) return;
   __syncthreads();  // the listed ids' gradients go over what was just written
@@ -369,16 +407,20 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const DistillPa
   }
 }
 
-// The gradient from the statistics of an earlier distill_kernel: one pass,
-// kBackVecs vectors per thread, a CTA per chunk of a row.
-constexpr int kBackVecs = 4;
+// The gradient from the statistics of an earlier distill_kernel: one pass, a
+// CTA per piece of a row, of kBackGroups groups of kBackVecs vectors a thread.
+constexpr int kBackVecs = 4, kBackGroups = 4;
+__host__ __device__ constexpr int back_piece(int vw) { return kRowThreads * kBackVecs * kBackGroups * vw; }
 
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(const DistillParams P, int chunks) {
+__global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const __grid_constant__ DistillParams P,
+                                                                          int pieces) {
   using E = Elem<DT>;
+  using Vec = typename E::Vec;
+  constexpr int VW = E::VW;
   extern __shared__ __align__(16) char smem[];
-  const int64_t row = blockIdx.x / chunks;
-  const int chunk = blockIdx.x % chunks;
+  const int64_t row = blockIdx.x / pieces;
+  const int piece = blockIdx.x % pieces;
   const int K = P.K, V = P.sp.V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
@@ -395,22 +437,26 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(const Dis
   const float ga = f * st.y;
   // vectors at 16-byte boundaries of memory: `off` places before the row's first logit
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(zrow) & 15) / E::ES;
-  constexpr int per = kRowThreads * kBackVecs * E::VW;
-  const int i0 = chunk * per - off, i1 = min(V, i0 + per);
-  typename E::Vec v[kBackVecs];
-  if (!dead) {
+  constexpr int per = kRowThreads * kBackVecs * VW;
+  const int i0 = piece * per * kBackGroups - off, i1 = min(V, i0 + per * kBackGroups);
+  const uint64_t c2 = f2(c, c), m2 = f2(-st.x, -st.x), g2 = f2(ga, ga);
+  auto load = [&](int at, Vec(&v)[kBackVecs]) {
 #pragma unroll
     for (int k = 0; k < kBackVecs; ++k) {
-      const int i = i0 + (k * kRowThreads + static_cast<int>(threadIdx.x)) * E::VW;
-      if (i >= i1) continue;
-      if (i >= 0 && i + E::VW <= V) {
+      const int i = at + (k * kRowThreads + static_cast<int>(threadIdx.x)) * VW;
+      if (dead || i >= i1) continue;
+      if (i >= 0 && i + VW <= V) {
         v[k] = E::vec(zrow, i);
       } else {
         typename E::Raw* d = reinterpret_cast<typename E::Raw*>(&v[k]);
 #pragma unroll
-        for (int e = 0; e < E::VW; ++e) d[e] = (i + e >= 0 && i + e < V) ? E::raw(zrow, i + e) : E::neg_inf_raw();
+        for (int e = 0; e < VW; ++e) d[e] = (i + e >= 0 && i + e < V) ? E::raw(zrow, i + e) : E::neg_inf_raw();
       }
     }
+  };
+  Vec v[kBackVecs];
+  load(i0, v);
+  if (!dead) {  // the teacher's entries, while the first loads run
     const float L = P.tlse ? P.tlse[row] : st.w;
     for (int j = threadIdx.x; j < K; j += kRowThreads) {
       const int id = P.ids[row * P.ts + j];
@@ -422,20 +468,21 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(const Dis
       pj[j] = there ? expf(x - L) * (1.f + fmaf(t, il, fmaf(t, ih, -x))) : 0.f;
     }
   }
+#pragma unroll 1
+  for (int at = i0; at < i1; at += per) {
+    Vec now[kBackVecs];
 #pragma unroll
-  for (int k = 0; k < kBackVecs; ++k) {
-    const int i = i0 + (k * kRowThreads + static_cast<int>(threadIdx.x)) * E::VW;
-    if (i0 + (k * kRowThreads + warp * 32) * E::VW >= i1) break;  // (the same for the whole warp)
-    const bool on = i < i1;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (on && !dead) {
-      float x[E::VW];
-      E::unpack(v[k], x);
+    for (int k = 0; k < kBackVecs; ++k) now[k] = v[k];
+    if (at + per < i1) load(at + per, v);  // (ahead of this group's stores)
 #pragma unroll
-      for (int e = 0; e < E::VW; ++e) x[e] = ga * ex2((x[e] - st.x) * c);
-      w = pack_vec<DT>(x);
+    for (int k = 0; k < kBackVecs; ++k) {
+      const int i = at + (k * kRowThreads + static_cast<int>(threadIdx.x)) * VW;
+      if (at + (k * kRowThreads + warp * 32) * VW >= i1) break;  // (the same for the whole warp)
+      const bool on = i < i1;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (on && !dead) w = gradients<DT>(now[k], m2, c2, g2);
+      store_warp<DT>(grow, i, V, on, w);
     }
-    store_warp<DT>(grow, i, V, on, w);
   }
   if (dead) return;
   __syncthreads();

@@ -9,8 +9,8 @@ cudaError_t launch_distill(int dtype, size_t smem, cudaStream_t s, const Distill
 }
 
 cudaError_t launch_distill_backward(int dtype, cudaStream_t s, const DistillParams& p) {
-  const int per = kRowThreads * kBackVecs * (dtype == SPECV_BF16 ? Elem<0>::VW : Elem<1>::VW);
-  const int chunks = (p.sp.V + 6) / per + 1;  // of a row that starts up to 7 places into a vector
+  const int vw = dtype == SPECV_BF16 ? Elem<0>::VW : Elem<1>::VW;
+  const int chunks = (p.sp.V + vw - 2) / back_piece(vw) + 1;  // of a row that starts inside a vector
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.N) * chunks);
   const size_t smem = static_cast<size_t>(p.K) * 12;
   if (dtype == SPECV_BF16)

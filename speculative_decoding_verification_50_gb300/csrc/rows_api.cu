@@ -55,37 +55,52 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
 // L2 that rows being read again may take.
 constexpr int64_t kL2Rows = 96 << 20;
 
-// The split for sampling and the top logits.  Few rows: as split_row.  Rows that
-// fill the SMs' slots (two CTAs each): as few CTAs per row as leave the rows in
-// flight to L2, since a CTA's fixed costs and a cluster's waits then come less
-// often per row; what a CTA does not hold is read again in each pass, and four
-// histograms per CTA keep the part of the row small that a token is drawn from.
-// Measured (us; rows x V; C = 1, 2, held whole): sampling 576 x 152064 fp32 435,
-// 389, 667; 128 x 128256 bf16 91, 66, 79; 320 x 128256 bf16, where the second
-// wave is nearly empty, 190, 146, 114 (so `whole_waves`).  The 256 top logits of
-// 256 x 152064 bf16 42, 58, 70; of 64 rows 29, 25, 23; 100 of 333 x 50257 fp32
-// 58, 69, 78.
-bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool whole_waves, RowSplit& sp, size_t& smem) {
-  if (!split_row(rows, V, dtype, sizeof(FilterShared) + work_bytes(1), sp, smem)) return false;
-  smem += work_bytes(1);
+// The split of rows that fill the SMs' slots (two CTAs each): as few CTAs per
+// row as leave the rows in flight to L2 (`again`: they are read again), since a
+// CTA's fixed costs and a cluster's waits then come less often per row; what a
+// CTA does not hold is read again in each pass.  extra(svec): a CTA's bytes
+// beside the held vectors.  False: few rows, or no fewer CTAs than sp has; those
+// are held whole.
+//   `whole_waves`: not where the last wave of CTAs would be nearly empty.
+template <typename Extra>
+bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool whole_waves, int max_c, Extra&& extra,
+                  RowSplit& sp, size_t& smem) {
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
   const int64_t slots = 2LL * api_sm_count();
   auto fits = [&](int C) {
     const int64_t n = rows * C;
-    return slots / C * nvec * 16 <= kL2Rows && V / (C * kMaxH) <= kMaxBinned && 5 * n >= 4 * slots &&
+    return (!again || slots / C * nvec * 16 <= kL2Rows) && 5 * n >= 4 * slots &&
            (!whole_waves || n <= slots || 2 * n >= 7 * slots);
   };
   int C = 1;
   while (C < sp.C && !fits(C)) C *= 2;
-  if (C * kMaxH > kMaxParts || C >= sp.C) return true;
-  const size_t room = kSmemSm / 2 - kSmemReserved - sizeof(FilterShared) - work_bytes(kMaxH);
+  if (C > max_c || C >= sp.C) return false;
+  const int32_t svec = static_cast<int32_t>((nvec + C - 1) / C);
+  const size_t work = extra(svec), room = kSmemSm / 2 - kSmemReserved;
+  if (work > room) return false;
   sp.C = C;
-  sp.H = kMaxH;
-  sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
-  sp.gvec = (sp.svec + kRowWarps - 1) / kRowWarps;
-  sp.rvec = std::min(sp.gvec, static_cast<int32_t>(room / (16 * kRowWarps)) / 32 * 32);
-  smem = static_cast<size_t>(sp.rvec) * kRowWarps * 16 + work_bytes(kMaxH);
+  sp.svec = svec;
+  sp.gvec = (svec + kRowWarps - 1) / kRowWarps;
+  sp.rvec = std::min(sp.gvec, again ? static_cast<int32_t>((room - work) / (16 * kRowWarps)) / 32 * 32 : 0);
+  smem = static_cast<size_t>(sp.rvec) * kRowWarps * 16;
+  return true;
+}
+
+// The split for sampling (and, `top`, the top logits); four histograms per CTA
+// keep the part of a row small that a token is drawn from.
+// Measured (us; rows x V; C = 1, 2, held whole): sampling 576 x 152064 fp32 435,
+// 389, 667; 128 x 128256 bf16 91, 66, 79; 320 x 128256 bf16, where the second
+// wave is nearly empty, 190, 146, 114 (so `whole_waves`).  The 256 top logits of
+// 256 x 152064 bf16 42, 58, 70; of 64 rows 29, 25, 23; 100 of 333 x 50257 fp32
+// 58, 69, 78.
+bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool top, RowSplit& sp, size_t& smem) {
+  constexpr size_t fixed = sizeof(FilterShared);
+  const int H = top ? 1 : kMaxH;
+  if (!split_row(rows, V, dtype, fixed + work_bytes(1), sp, smem)) return false;
+  const int max_c = V / H <= kMaxBinned ? kMaxParts / H : 0;
+  if (split_stream(rows, V, dtype, true, !top, max_c, [&](int32_t) { return fixed + work_bytes(H); }, sp, smem)) sp.H = H;
+  smem += work_bytes(sp.H);
   return true;
 }
 
@@ -132,7 +147,7 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   const int64_t rows = static_cast<int64_t>(B) * R;
   FilterParams p = {};
   size_t smem;
-  if (!split_filter(rows, V, a->dtype, true, p.sp, smem))
+  if (!split_filter(rows, V, a->dtype, false, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (rows * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B*R too large");
   p.rows = static_cast<int32_t>(rows);
@@ -175,7 +190,7 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   if (a->row_stride < V) return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
   TopParams p = {};
   size_t smem;
-  if (!split_filter(B, V, a->dtype, false, p.sp, smem))
+  if (!split_filter(B, V, a->dtype, true, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (static_cast<int64_t>(B) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B too large");
   p.rows = B;
@@ -256,13 +271,18 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   if (a->grad_loss) return api_fail(SPECV_ERR_INVALID_ARG, "grad_loss belongs to specv_distill_backward");
   DistillParams p = distill_params(a);
   size_t smem;
-  const size_t extra = static_cast<size_t>(a->K) * 20;
-  if (!split_row(a->N, a->V, a->dtype, extra + kSmemReserved, p.sp, smem))
+  const int vw = 16 / elem_bytes(a->dtype);
+  // (a held row's bits are at most a 16th of its bytes)
+  const size_t bits = distill_bytes((a->V + vw - 1) / vw, vw, a->K);
+  if (!split_row(a->N, a->V, a->dtype, kSmemReserved + std::min<size_t>(bits, 16384 + static_cast<size_t>(a->K) * 20), p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
+  split_stream(a->N, a->V, a->dtype, a->grad != nullptr, false, kMaxCluster,
+               [&](int32_t svec) { return kSmemReserved + distill_bytes(svec, vw, a->K); }, p.sp, smem);
+  smem += distill_bytes(p.sp.svec, vw, a->K);
   if (static_cast<int64_t>(a->N) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   p.loss = a->loss;
   p.status = a->row_status;
-  return launched(launch_distill(a->dtype, smem + extra, static_cast<cudaStream_t>(stream), p), "distill");
+  return launched(launch_distill(a->dtype, smem, static_cast<cudaStream_t>(stream), p), "distill");
 }
 
 specv_status specv_distill_backward(const specv_distill_args* a, void* stream) {
@@ -271,7 +291,7 @@ specv_status specv_distill_backward(const specv_distill_args* a, void* stream) {
   if (st != SPECV_OK) return st;
   if (a->N == 0) return api_done(0);
   if (!a->stats || !a->grad) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
-  if (static_cast<int64_t>(a->N) * ((a->V + 6) / (kRowThreads * kBackVecs * (16 / elem_bytes(a->dtype))) + 1) > 0x7fffffffLL)
+  if (static_cast<int64_t>(a->N) * ((a->V + 6) / back_piece(16 / elem_bytes(a->dtype)) + 1) > 0x7fffffffLL)
     return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   DistillParams p = distill_params(a);
   p.gloss = a->grad_loss;
