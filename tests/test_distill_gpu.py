@@ -235,3 +235,37 @@ def test_top_logits_feed_the_loss(sv):
         o = sv.specv_distill(z, top["ids"], top["values"], teacher_lse=top["lse"], temperature=T, tail=True,
                              with_grad=True)
         assert o["loss"].abs().max() <= REL and o["grad"].abs().max() <= REL
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 30016), (torch.float32, 50255), (torch.bfloat16, 60032),
+                                     (torch.bfloat16, 100001)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_many_rows(sv, dtype, V, tail):
+    """Rows enough to fill the GPU take another split than a few do."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    N, K = 400, 40
+    z = (torch.randn(N, V, generator=g, device="cuda") * 3).to(dtype)
+    teacher = z.float() + torch.randn(N, V, generator=g, device="cuda")
+    val, ids = teacher.topk(K, dim=1)
+    ids = ids.int()
+    lse = torch.logsumexp(teacher, 1) if tail else None
+    ids[::11, 3] = ids[::11, 9]        # repeats
+    val[::11] -= 1.0
+    ids[::13, 20:] = -1
+    w = torch.rand(N, generator=g, device="cuda") + 0.1
+    w[::17] = 0
+    kw = lambda s: dict(teacher_lse=None if lse is None else lse[s], weights=w[s], tail=tail)  # noqa: E731
+    whole = sv.specv_distill(z, ids, val, with_grad=True, **kw(slice(None)))
+    alone = sv.specv_distill(z, ids, val, **kw(slice(None)))  # without the gradient: a third split
+    assert (whole["loss"] - alone["loss"]).abs().max() <= REL * (1 + whole["loss"].abs().max())
+    for a in range(0, N, 40):
+        s = slice(a, a + 8)
+        q = sv.specv_distill(z[s], ids[s], val[s], with_grad=True, **kw(s))
+        assert (q["loss"] - whole["loss"][s]).abs().max() <= REL * (1 + q["loss"].abs().max())
+        top = q["grad"].float().abs().amax(1, keepdim=True)
+        off = (q["grad"].float() - whole["grad"][s].float()).abs()
+        eps = torch.finfo(dtype).eps
+        assert (off <= REL * top + eps * q["grad"].float().abs()).all()
+    some = torch.arange(0, N, 23, device="cuda")
+    check(sv, z[some].contiguous(), ids[some].contiguous(), val[some].contiguous(),
+          None if lse is None else lse[some].contiguous(), 1.0, w[some].contiguous(), tail)

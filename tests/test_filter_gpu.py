@@ -281,3 +281,45 @@ def test_filtered_verification_keeps_the_rules(sv):
     x = sv.specv_sample(target[:, :K], T, u[:, :K].contiguous(), **rules)["tokens"]
     o = sv.specv_verify(ft, ft[:, :K], x, T, u[:, K:].contiguous())
     assert (o["accept_len"] == K).all()
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 30016), (torch.float32, 30011), (torch.bfloat16, 60032),
+                                     (torch.bfloat16, 60005), (torch.float32, 152064)])
+def test_many_rows(sv, dtype, V):
+    """Rows enough to fill the GPU several times take another split than a few
+    do: the same whole numbers, and the definition on some of them."""
+    rng = np.random.default_rng(V)
+    B = 1300
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn(B, V, generator=g, device="cuda")
+    z *= torch.rand(B, 1, generator=g, device="cuda") * 3 + 0.3
+    z[:, 5:9] += 6
+    z[::7] = (z[::7] * 4).round() / 4          # many ties
+    z[3::50] = -1.25                           # nothing but ties
+    z[11::50, 1:] = -float("inf")
+    z = z.to(dtype)
+    T, k, p, mp, u = rules_of(rng, B, V)
+    k[40:80] = rng.choice([1500, V // 2, 3], 40)
+    dev = lambda x, t: torch.from_numpy(np.asarray(x, t)).cuda()  # noqa: E731
+    rules = [dev(k, np.int32), dev(p, np.float32), dev(mp, np.float32)]
+    T32, u32 = dev(T, np.float32), dev(u, np.float32)
+    f = torch.empty_like(z)
+    o = sv.specv_sample(z, T32, u32, top_k=rules[0], top_p=rules[1], min_p=rules[2], filtered=f)
+    fo = sv.specv_filter_logits(z, T32, top_k=rules[0], top_p=rules[1], min_p=rules[2])
+    assert torch.equal(fo["filtered"], f) and torch.equal(fo["kept"], o["kept"])
+    del fo
+    for a in range(0, B, 20):
+        s = slice(a, a + 20)
+        few = torch.empty_like(z[s])
+        q = sv.specv_sample(z[s], T32[s], u32[s], top_k=rules[0][s], top_p=rules[1][s], min_p=rules[2][s], filtered=few)
+        assert torch.equal(few, f[s]), a
+        for n in ("tokens", "kept", "row_status"):
+            assert torch.equal(q[n], o[n][s]), (a, n)
+        assert (q["prob"] - o["prob"][s]).abs().max() <= PROB_RTOL
+    for b in range(0, B, 37):
+        row = z[b].float().cpu().numpy().astype(np.float64)
+        keep, tok, pr, near = restate(row, T[b], k[b], p[b], mp[b], u[b])
+        if not near:
+            assert int(o["kept"][b]) == keep.sum() and int(o["tokens"][b]) == tok
+            assert abs(float(o["prob"][b]) - pr) <= PROB_RTOL * pr
+            assert np.array_equal(f[b].float().cpu().numpy() > -np.inf, keep)

@@ -73,3 +73,21 @@ def test_flagged_rows_and_layout(sv):
     assert o["row_status"].tolist() == [sv.ROW_NONFINITE] * 3 + [0]
     assert (o["ids"][:3] == -1).all() and torch.isneginf(o["values"][:3]).all() and o["lse"][:3].isnan().all()
     assert o["ids"][3].tolist() == list(range(999, 991, -1))
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 30016), (torch.float32, 50255), (torch.bfloat16, 152064)])
+@pytest.mark.parametrize("k", [3, 300, 1000])
+def test_many_rows(sv, dtype, V, k):
+    """Rows enough to fill the GPU take another split than a few do."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn(400, V, generator=g, device="cuda") * 3
+    z[::9] = (z[::9] * 2).round() / 2
+    z[5] = 1.0
+    z[6, 100:] = -float("inf")
+    z = z.to(dtype)
+    o = sv.specv_top_logits(z, k)
+    for a in range(0, 400, 8):
+        q = sv.specv_top_logits(z[a:a + 8], k)
+        assert torch.equal(q["ids"], o["ids"][a:a + 8]) and torch.equal(q["values"], o["values"][a:a + 8]), a
+        assert ((q["lse"] - o["lse"][a:a + 8]).abs() <= 2.0 ** -20 * (1 + q["lse"].abs())).all()
+    check(sv, z[::40].contiguous(), k)
