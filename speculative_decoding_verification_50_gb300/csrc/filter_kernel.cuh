@@ -24,7 +24,7 @@ namespace specv {
 constexpr int kGrid = 32;                 // bins per unit of log2
 constexpr int kWindow = 48;               // units below the maximum that carry weight
 constexpr int kBins = kGrid * kWindow + 16;
-constexpr int kCap = 1024;                // tokens of a band that are worked on as a list
+constexpr int kCap = 1536;                // tokens of a band that are worked on as a list
 constexpr int kMaxBinned = 250000;        // logits of a CTA, so that a bin's halves fit 32 bits
 constexpr int kMaxParts = 16;             // parts of a row that are summed apart: C * H
 constexpr int kMaxH = 4;
@@ -185,7 +185,8 @@ struct FilterShared {
   uint64_t mine[kMaxH];      // per part: the weight in the bins before the band
   uint64_t mass[kMaxH];      // per part: of tokens above the band that share its bins
   int32_t band[kMaxH];       // per part: the band's tokens
-  int32_t above, ncollect, bad;
+  int32_t above, ncollect, kept, bad;
+  uint32_t fix32[3][kMaxParts];  // per part, in pieces of 15 bits
   uint32_t kmin, kmax;
   int32_t lo, hi;
   int32_t before;
@@ -432,6 +433,74 @@ struct FilterRow {
   // bins before the band) with what tokens above the band but in its bins add.
   // Ends with a cluster barrier.
   __device__ void collect(const Band& b) {
+    if (!b.by_key) {
+      collect_bins(b);
+      if (collected() <= kCap) return;
+      sync_all();  // (everyone has read the counts)
+      if (threadIdx.x == 0) S.above = S.ncollect = 0;
+      __syncthreads();
+    }
+    collect_exact(b);
+  }
+
+  // ... for a band of bins: every token of the bins' range first, with the
+  // test by bin after the pass, on the list.  Above kCap tokens in a CTA the
+  // numbers are not complete.
+  __device__ void collect_bins(const Band& b) {
+    constexpr int VW = Elem<DT>::VW, G = 4;
+    using Vec = typename Elem<DT>::Vec;
+    uint64_t* raw = list();
+    int above = 0;
+    sl.template groups<G>([&](const Vec(&x)[G], int j0) {
+      unsigned zone = 0;  // a bit for each logit
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (DT == 0 && !(vec_max<DT>(x[g], neg_inf()) >= b.elo)) continue;
+        float z[VW];
+        Elem<DT>::unpack(x[g], z);
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          above += z[k] >= b.ehi;
+          if (z[k] >= b.elo && z[k] < b.ehi) zone |= 1u << (g * VW + k);
+        }
+      }
+      if (!zone) return;
+      int pos = atomicAdd(&S.ncollect, __popc(zone));
+      while (zone) {  // (few: read again rather than kept in registers by number)
+        const int bit = __ffs(zone) - 1, j = j0 + 32 * (bit / VW);
+        zone &= zone - 1;
+        if (pos < kCap)
+          raw[pos++] = (static_cast<uint64_t>(__float_as_uint(sl.at(j, bit % VW))) << 32) |
+                       static_cast<uint32_t>(sl.index(j) + bit % VW);
+      }
+    });
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 0 && above) atomicAdd(&S.above, above);
+    if (threadIdx.x == 0) S.kept = 0;
+    __syncthreads();
+    const int n = min(S.ncollect, kCap);
+    for (int i = threadIdx.x; i < n; i += kRowThreads) {
+      const float z = __uint_as_float(static_cast<uint32_t>(raw[i] >> 32));
+      const int idx = static_cast<int>(raw[i] & 0xffffffffu);
+      if (!in_set(z, idx)) continue;
+      const int pl = place(z, b);
+      if (pl == 0) atomicAdd(&S.above, 1);
+      else if (pl == 1) own_list()[atomicAdd(&S.kept, 1)] = token_key(z, idx);
+    }
+    __syncthreads();
+    if (threadIdx.x < static_cast<unsigned>(C)) {
+      const int r = threadIdx.x;
+      peer(S.xabove, r)[rank] = S.above;
+      peer(S.xcount, r)[rank] = S.ncollect > kCap ? kCap + 1 : S.kept;
+#pragma unroll
+      for (int h = 0; h < kMaxH; ++h)
+        if (h < H) peer(S.xmass, r)[rank * H + h] = S.mine[h];
+    }
+    sync_all();
+  }
+
+  // ... for any band, the numbers complete whatever is collected.
+  __device__ void collect_exact(const Band& b) {
     constexpr int VW = Elem<DT>::VW, G = 4;  // vectors looked at together, a mask bit for each logit
     using Vec = typename Elem<DT>::Vec;
     int above = 0, in_band = 0;
@@ -627,7 +696,7 @@ struct FilterRow {
       uint64_t w;
       before_band(above, w);
       if (n <= kCap) {
-        if (rank == 0) resolve(b, n, above, w, kind, goal, fin, zt, u);
+        if (rank == 0) resolve(n, above, w, kind, goal, fin, zt, u);
         publish();
         break;
       }
@@ -656,9 +725,10 @@ struct FilterRow {
     __syncthreads();
   }
 
-  // Sorts n <= kCap tokens of own_list() or list() through bins of their range
-  // of keys, a thread's each: within a bin every token counts those before it.
-  // False (nothing done) where a bin is too full for that.
+  // Sorts n <= kCap tokens through bins of their range of keys, a thread's each:
+  // within a bin every token counts those before it.  bf16 logits have few
+  // values in a band and many tokens of each: there a bin is a value and a
+  // range of indices.  False (nothing done) where a bin is too full.
   __device__ bool sort_by_bins(uint64_t* a, int n) {
     uint32_t* count = reinterpret_cast<uint32_t*>(S.total);
     uint32_t lo = 0xffffffffu, hi = 0;
@@ -684,14 +754,22 @@ struct FilterRow {
       lo = min(lo, static_cast<uint32_t>(S.scratch[w] >> 32));
       hi = max(hi, static_cast<uint32_t>(S.scratch[w]));
     }
-    const int shift = max(0, 32 - __clz(hi - lo) - 9);
+    const uint32_t values = ((hi - lo) >> 16) + 1;
+    const bool by_value = DT == 0 && values <= kRowThreads;
+    const int shift = by_value ? 16 : max(0, 32 - __clz(hi - lo) - 9);
+    const uint32_t wide = by_value ? kRowThreads / values : 1;  // bins per value
+    const uint32_t scale = wide * (0xffffffffu / static_cast<uint32_t>(V));
+    auto bin = [&](uint64_t t) {
+      const uint32_t v = (static_cast<uint32_t>(t >> 32) - lo) >> shift;
+      return by_value ? v * wide + __umulhi(static_cast<uint32_t>(t), scale) : v;
+    };
     int at[per];
 #pragma unroll
     for (int q = 0; q < per; ++q)
-      if (x[q] != ~0ull) at[q] = atomicAdd(&count[(static_cast<uint32_t>(x[q] >> 32) - lo) >> shift], 1u);
+      if (x[q] != ~0ull) at[q] = atomicAdd(&count[bin(x[q])], 1u);
     __syncthreads();
     const uint32_t mine = count[threadIdx.x];
-    const bool full = __syncthreads_or(mine > 48);
+    const bool full = __syncthreads_or(mine > 64);
     if (full) return false;
     uint32_t all;
     const uint32_t start = block_scan(mine, reinterpret_cast<uint32_t*>(S.iscratch), all);
@@ -700,12 +778,12 @@ struct FilterRow {
     // binned into place, then counted within the bin
 #pragma unroll
     for (int q = 0; q < per; ++q)
-      if (x[q] != ~0ull) a[(count[(static_cast<uint32_t>(x[q] >> 32) - lo) >> shift] >> 16) + at[q]] = x[q];
+      if (x[q] != ~0ull) a[(count[bin(x[q])] >> 16) + at[q]] = x[q];
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < per; ++q)
       if (x[q] != ~0ull) {
-        const uint32_t c = count[(static_cast<uint32_t>(x[q] >> 32) - lo) >> shift];
+        const uint32_t c = count[bin(x[q])];
         at[q] = c >> 16;
         for (uint32_t j = c >> 16; j < (c >> 16) + (c & 0xffffu); ++j) at[q] += a[j] < x[q];
       }
@@ -733,6 +811,22 @@ struct FilterRow {
       return;
     }
     if (sort_by_bins(a, n)) return;
+    if (n > 2 * kRowThreads) {  // equal logits, most likely: every token counts all before it
+      constexpr int per = kCap / kRowThreads;
+      uint64_t x[per];
+      int at[per] = {};
+#pragma unroll
+      for (int q = 0; q < per; ++q) x[q] = threadIdx.x + q * kRowThreads < n ? a[threadIdx.x + q * kRowThreads] : ~0ull;
+      for (int j = 0; j < n; ++j)
+#pragma unroll
+        for (int q = 0; q < per; ++q) at[q] += a[j] < x[q];
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < per; ++q)
+        if (x[q] != ~0ull) a[at[q]] = x[q];
+      __syncthreads();
+      return;
+    }
     // two tokens a thread (places 2 t and 2 t + 1), steps below 64 within a warp
     uint64_t p = ~0ull, q = ~0ull;
     const int i = 2 * threadIdx.x;
@@ -774,89 +868,46 @@ struct FilterRow {
     __syncthreads();
   }
 
-  // Rank 0, the band collected: where the cut falls in it.  More tokens than
-  // are sorted quickly are first split into bins of their own.
-  __device__ void resolve(const Band& b, int n, int above, uint64_t w, CutKind kind, uint64_t goal, bool fin, float zt,
-                          const float* u) {
+  // Rank 0, the band collected: where the cut falls in it.
+  __device__ void resolve(int n, int above, uint64_t w, CutKind kind, uint64_t goal, bool fin, float zt, const float* u) {
     const bool count = kind == kByCount;
-    if (n > kRowThreads / 2) {
-      reinterpret_cast<uint64_t*>(S.total)[threadIdx.x] = 0;
-      if (threadIdx.x == 0) {
-        S.lo = INT_MAX;
-        S.hi = 0;
-      }
-    }
+    if (threadIdx.x == 0) S.lo = n - 1;
     pull(n);
-    if (n > 0) {
-      uint64_t* sub = list();
-      int m = n;
-      if (count) w = above;
-      if (n > kRowThreads / 2) {
-        // bins of the band's range of keys, a thread's each: counts or masses
-        uint64_t* bin = reinterpret_cast<uint64_t*>(S.total);
-        const uint32_t lo = ~(b.by_key ? b.kmax : order_key(b.ehi));
-        const uint32_t hi = ~(b.by_key ? b.kmin : order_key(b.elo));
-        const int shift = max(0, 32 - __clz(hi - lo) - 9);
-        for (int i = threadIdx.x; i < n; i += kRowThreads)
-          atomicAdd(reinterpret_cast<unsigned long long*>(&bin[(static_cast<uint32_t>(list()[i] >> 32) - lo) >> shift]),
-                    count ? 1ull : weight(token_logit(list()[i])));
-        __syncthreads();
-        const uint64_t in_bin = bin[threadIdx.x];
-        uint64_t all;
-        const uint64_t before = w + block_scan(in_bin, S.scratch, all);
-        if (in_bin && before + in_bin >= goal) atomicMin(&S.lo, static_cast<int>(threadIdx.x));
-        __syncthreads();
-        const int at = min(S.lo, kRowThreads - 1);
-        if (static_cast<int>(threadIdx.x) == at) S.fix[0] = before;
-        sub = own_list();  // the tokens of that bin
-        for (int i = threadIdx.x; i < n; i += kRowThreads)
-          if (static_cast<int>((static_cast<uint32_t>(list()[i] >> 32) - lo) >> shift) == at)
-            sub[atomicAdd(&S.hi, 1)] = list()[i];
-        __syncthreads();
-        w = S.fix[0];
-        m = S.hi;
-      }
-      if (threadIdx.x == 0) S.lo = m - 1;
-      sort(sub, m);
-      constexpr int per = kCap / kRowThreads;
-      const int i0 = threadIdx.x * per;
-      uint64_t v[per], x = 0;
+    sort(list(), n);
+    constexpr int per = kCap / kRowThreads;
+    const int i0 = threadIdx.x * per;
+    uint64_t v[per], x = 0;
+    float z[per];
 #pragma unroll
-      for (int q = 0; q < per; ++q) {
-        v[q] = i0 + q < m ? (count ? 1ull : weight(token_logit(sub[i0 + q]))) : 0;
-        x += v[q];
-      }
-      uint64_t all;
-      uint64_t run = w + block_scan(x, S.scratch, all);
-#pragma unroll
-      for (int q = 0; q < per; ++q) {
-        run += v[q];
-        if (i0 + q < m && run >= goal) atomicMin(&S.lo, i0 + q);
-      }
-      __syncthreads();
-      const uint64_t last = sub[S.lo];
-      zc = token_logit(last);
-      ic = token_index(last);
+    for (int q = 0; q < per; ++q) {
+      z[q] = i0 + q < n ? token_logit(list()[i0 + q]) : 0.f;
+      v[q] = i0 + q < n ? (count ? 1ull : weight(z[q])) : 0;
+      x += v[q];
     }
-    if (kind == kGiven || (fin && n > 0 && zc < zt)) {  // min-p ends the kept tokens
+    uint64_t all;
+    uint64_t run = (count ? static_cast<uint64_t>(above) : w) + block_scan(x, S.scratch, all);
+#pragma unroll
+    for (int q = 0; q < per; ++q) {
+      run += v[q];
+      if (i0 + q < n && run >= goal) atomicMin(&S.lo, i0 + q);
+      if (i0 + q < n && fin && z[q] < zt) atomicMin(&S.lo, i0 + q - 1);  // min-p ends the kept tokens
+    }
+    __syncthreads();
+    const int nb = S.lo + 1;  // the band's tokens that the cut keeps
+    if (kind == kGiven || nb == 0) {
       zc = zt;
       ic = INT_MAX;
+    } else {
+      zc = token_logit(list()[nb - 1]);
+      ic = token_index(list()[nb - 1]);
     }
-    // the band's tokens that the cut keeps
-    if (threadIdx.x == 0) S.above = 0;
-    __syncthreads();
-    int kept = 0;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) kept += in_set(token_logit(list()[i]), token_index(list()[i]));
-    kept = __reduce_add_sync(0xffffffffu, kept);
-    if (lane == 0 && kept) atomicAdd(&S.above, kept);
-    __syncthreads();
     if (threadIdx.x == 0) {
       S.dec.tie_part = -1;
       S.dec.zc = zc;
       S.dec.ic = ic;
-      S.dec.kept = above + S.above;
+      S.dec.kept = above + nb;
     }
-    if (fin && u) finish(n, 0, 0.f, *u);
+    if (fin && u) finish(nb, 0, 0.f, *u);
   }
 
   // Rank 0, every token down to the k-th's bin collected (n of them): top-k,
@@ -897,7 +948,7 @@ struct FilterRow {
     }
     if (!u) return;
     if (nk > kRowThreads / 2) {
-      finish(n, 0, 0.f, *u);
+      finish(nk, 0, 0.f, *u);
       return;
     }
     // the draw: G threads add up the weights of lower index for each
@@ -1018,59 +1069,58 @@ struct FilterRow {
 
   // Rank 0: total weight of the kept tokens, and the part where the running sum
   // in index order passes u times it.  Kept: the parts' weights above the band,
-  // those of the n_list collected tokens that zc, ic keep, and the first nt
-  // logits equal to z.
+  // those of the first n_list tokens of list(), and the first nt logits equal
+  // to z.
   __device__ void finish(int n_list, int nt, float z, float u) {
+    if (threadIdx.x < 3 * kMaxParts) S.fix32[threadIdx.x / kMaxParts][threadIdx.x % kMaxParts] = 0;
     __syncthreads();
-    const int parts = C * H;
-    if (static_cast<int>(threadIdx.x) < parts) S.fix[threadIdx.x] = S.xmass[threadIdx.x];
-    __syncthreads();
-    for (int i0 = warp * 32; i0 < n_list; i0 += kRowThreads) {
-      const int i = i0 + lane;
-      const uint64_t k = i < n_list ? list()[i] : 0;
-      const bool in = i < n_list && in_set(token_logit(k), token_index(k));
-      const uint64_t x = in ? weight(token_logit(k)) : 0;
-      int part = 0;
-      if (in) {
-        const int vec = token_index(k) / Elem<DT>::VW, cta = quotient(vec, split.svec);
-        part = cta * H + quotient(vec - cta * split.svec, split.gvec) * H / kRowWarps;
-      }
-      // one addition per part met, not per token
-      const int first = __reduce_min_sync(0xffffffffu, in ? part : kMaxParts), last = __reduce_max_sync(0xffffffffu, part);
-      for (int p = first; p <= last; ++p) {
-        const uint64_t s = warp_sum_u(in && part == p ? x : 0);
-        if (lane == 0 && s) atomicAdd(reinterpret_cast<unsigned long long*>(&S.fix[p]), s);
-      }
+    for (int i = threadIdx.x; i < n_list; i += kRowThreads) {
+      const uint64_t k = list()[i], w = weight(token_logit(k));
+      const int vec = token_index(k) / Elem<DT>::VW, cta = quotient(vec, split.svec);
+      const int part = cta * H + ((quotient(vec - cta * split.svec, split.gvec) << shift_H()) / kRowWarps);
+      atomicAdd(&S.fix32[0][part], static_cast<uint32_t>(w) & 0x7fffu);
+      atomicAdd(&S.fix32[1][part], static_cast<uint32_t>(w >> 15) & 0x7fffu);
+      atomicAdd(&S.fix32[2][part], static_cast<uint32_t>(w >> 30));
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      const uint64_t one = nt > 0 ? weight(z) : 0;
-      uint64_t W = 0;
-      for (int p = 0; p < parts; ++p) {
-        const int take = nt > 0 ? min(nt, S.xband[p]) : 0;
-        if (take > 0) S.fix[p] += one * static_cast<uint64_t>(take);
-        nt -= take;
-        W += S.fix[p];
+    if (threadIdx.x < 32) {  // a lane per part
+      const bool on = lane < C * H;
+      uint64_t x = 0;
+      int ties = on && nt > 0 ? S.xband[lane] : 0;
+      if (on)
+        x = S.xmass[lane] + S.fix32[0][lane] + (static_cast<uint64_t>(S.fix32[1][lane]) << 15) +
+            (static_cast<uint64_t>(S.fix32[2][lane]) << 30);
+      if (nt > 0) {
+        int inc = ties;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        ties = max(0, min(ties, nt - (inc - ties)));
+        x += weight(z) * static_cast<uint64_t>(ties);
       }
+      uint64_t inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint64_t W = __shfl_sync(0xffffffffu, inc, 31);
       const bool fell = !(u < 1.f);
       // (whole numbers: a sum exceeds u W exactly if it exceeds its floor)
       uint64_t t = u > 0.f && !fell ? fraction(u, W) : 0;
       t += t >> kSlack;
-      uint64_t run = 0, before = 0;
-      int at = 0;
-      for (int p = 0; p < parts; ++p) {
-        if (S.fix[p] == 0) continue;
-        at = p;
-        before = run;
-        run += S.fix[p];
-        if (!fell && run > t) break;
+      const unsigned over = __ballot_sync(0xffffffffu, x > 0 && !fell && inc > t);
+      const unsigned some = __ballot_sync(0xffffffffu, x > 0);
+      const int who = over ? __ffs(over) - 1 : 31 - __clz(some);
+      if (lane == who) {
+        S.dec.part = lane;
+        S.dec.rem = fell ? ~0ull : t - (inc - x);
+        S.dec.W = W;
+        S.dec.fallback = fell;
       }
-      S.dec.part = at;
-      S.dec.rem = fell ? ~0ull : t - before;
-      S.dec.W = W;
-      S.dec.fallback = fell;
     }
-    __syncthreads();
   }
 
   __device__ void publish() {  // rank 0's decision to every CTA
