@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   const int lo = sl.base, hi = min(V, lo + P.sp.svec * VW);  // the slice's indices
   float L = 0.f, tmax = 0.f, pscale = 1.f;
   uint64_t mass = 0;  // sum of pj, in units of 2^-40
-  float run = neg_inf(), sum = 0.f, zmax = neg_inf(), a = 0.f;
+  RunningSum rs;  // over the logits that are not listed
+  float zmax = neg_inf(), a = 0.f;
   bool some = true;  // (without a log-sum-exp: there are entries)
   if (!skip) {
     sl.load(&bars[warp]);
@@ -245,10 +246,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     }
     // the logits that are not listed
     const unsigned char* byte = reinterpret_cast<const unsigned char*>(bits);
-    const uint64_t c2 = f2(c, c);
     auto add = [&](const Vec(&y)[2], int j) {
-      uint64_t z[2][VW / 2];
-      float top = run;
+      uint64_t z[VW];
+      float top = rs.run;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const unsigned listed = j + 32 * u < sl.nv ? vector_bits<DT>(byte, sl.v0 + j + 32 * u) : 0u;
@@ -259,30 +259,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
           for (int k = 0; k < VW; ++k) x[k] = (listed >> k) & 1u ? neg_inf() : x[k];
 #pragma unroll
           for (int k = 0; k < VW / 2; ++k) {
-            z[u][k] = f2(x[2 * k], x[2 * k + 1]);
+            z[u * (VW / 2) + k] = f2(x[2 * k], x[2 * k + 1]);
             top = max3_nan(top, x[2 * k], x[2 * k + 1]);
           }
         } else {
-          unpack_pairs<DT>(y[u], z[u]);
+          uint64_t x[VW / 2];
+          unpack_pairs<DT>(y[u], x);
+#pragma unroll
+          for (int k = 0; k < VW / 2; ++k) z[u * (VW / 2) + k] = x[k];
           top = vec_max<DT>(y[u], top);
         }
       }
-      const float ref = top > neg_inf() ? top : 0.f;
-      sum *= ex2((run - ref) * c);
-      run = top;
-      const uint64_t r2 = f2(-ref, -ref);
-      uint64_t t = 0;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < VW / 2; ++k) {
-          float e0, e1;
-          f2_split(f2_mul(f2_add(z[u][k], r2), c2), e0, e1);
-          t = f2_add(t, f2(ex2(e0), ex2(e1)));
-        }
-      float e0, e1;
-      f2_split(t, e0, e1);
-      sum += e0 + e1;
+      rs.add(z, top, c);
     };
     sl.template memory_groups<2>(add);
     if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
@@ -290,14 +278,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     if (bad) atomicOr(&badbits, bad);
   }
   // the slice's maximum, listed ids included
-  const float mc = block_max_nan(max_nan(run, zmax), mred);
+  const float mc = block_max_nan(max_nan(rs.run, zmax), mred);
   const float mref = mc > neg_inf() ? mc : 0.f;
   float listed = 0.f;
   if (!skip) {
     for (int j = threadIdx.x; j < K; j += kRowThreads)
       if (ids[j] >= lo && ids[j] < hi && sj[j] >= 0.f) listed += ex2((zj[j] - mref) * c);
   }
-  float rest = warp_sum_f(sum > 0.f ? sum * ex2((run - mref) * c) : 0.f);
+  float rest = warp_sum_f(rs.at(mref, c));
   listed = warp_sum_f(listed);
   a = warp_sum_f(a);
   if (lane == 0) {

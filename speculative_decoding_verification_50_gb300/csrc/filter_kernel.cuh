@@ -66,6 +66,7 @@ struct TopParams {
   int32_t rows, k;
   const void* z;
   int64_t rs;
+  double invT;   // 1 / T
   float c;       // log2(e) / T
   int32_t* ids;
   float* values;
@@ -1477,7 +1478,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   F.clear();  // (a barrier)
   float own[4];
   bool landed;
-  const float wm = F.sl.warp_max(&S.bars[warp], own, landed);
+  RunningSum rs;  // (the log-sum-exp's share, in the same pass)
+  const float wm = F.sl.warp_max(&S.bars[warp], own, landed, &rs, P.c);
   if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
   const float mc = block_max_nan(wm, S.fscratch);
   cluster_wait();
@@ -1510,29 +1512,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   F.sc.gm = 0;
   F.zc = kNegMax;
   F.ic = INT_MAX;
-  // log-sum-exp: 2^(z c - ref), ref = max c rounded
-  const float c = P.c, ref = m * c;
-  const uint64_t c2 = f2(c, c), r2 = f2(-ref, -ref);
-  float s = 0.f;
-  const bool plain = !(fabsf(ref) < 1e6f);  // (the rounding of ref alone would be a power of two too far)
-  if (plain) F.sl.each([&](float z, int) { s += ex2((z - m) * c); });
-  if (!plain)
-    F.sl.template groups<4>([&](const typename E::Vec(&x)[4], int) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint64_t z[E::VW / 2], t = 0;
-        unpack_pairs<DT>(x[u], z);
-#pragma unroll
-        for (int q = 0; q < E::VW / 2; ++q) {
-          float a, b;
-          f2_split(f2_fma(z[q], c2, r2), a, b);
-          t = f2_add(t, f2(ex2(a), ex2(b)));
-        }
-        float a, b;
-        f2_split(t, a, b);
-        s += a + b;
-      }
-    });
+  float s = rs.at(m, P.c);
   s = warp_sum_f(s);
   if (lane == 0) S.fscratch[warp] = s;
   __syncthreads();
@@ -1576,7 +1556,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   if (threadIdx.x == 0) {
     double t = 0;
     for (int r = 0; r < C; ++r) t += S.xexp[r];
-    if (P.lse) P.lse[row] = static_cast<float>((plain ? static_cast<double>(m) * c : static_cast<double>(ref)) * 0.69314718055994531 + log(t));
+    if (P.lse) P.lse[row] = static_cast<float>(static_cast<double>(m) * P.invT + log(t));
     if (P.status) P.status[row] = 0;
   }
 }

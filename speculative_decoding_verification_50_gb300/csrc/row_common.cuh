@@ -94,6 +94,47 @@ __device__ __forceinline__ float vec_max(const typename Elem<DT>::Vec& v, float 
   }
 }
 
+// A vector's logits as pairs of fp32 for the paired arithmetic.
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(const typename Elem<DT>::Vec& v, uint64_t (&z)[Elem<DT>::VW / 2]) {
+  float x[Elem<DT>::VW];
+  Elem<DT>::unpack(v, x);
+#pragma unroll
+  for (int k = 0; k < Elem<DT>::VW / 2; ++k) z[k] = f2(x[2 * k], x[2 * k + 1]);
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// One thread's share of a softmax: its running maximum and the sum of
+// 2^((z - run) c) over what it has seen.
+struct RunningSum {
+  float run = neg_inf(), sum = 0.f;
+
+  // U vectors as pairs, `top` the larger of their maximum and run.
+  template <int N>
+  __device__ __forceinline__ void add(const uint64_t (&z)[N], float top, float c) {
+    const float ref = top > neg_inf() ? top : 0.f;
+    sum *= ex2((run - ref) * c);
+    run = top;
+    const uint64_t r2 = f2(-ref, -ref), c2 = f2(c, c);
+    uint64_t t = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float a, b;
+      f2_split(f2_mul(f2_add(z[k], r2), c2), a, b);
+      t = f2_add(t, f2(ex2(a), ex2(b)));
+    }
+    float a, b;
+    f2_split(t, a, b);
+    sum += a + b;
+  }
+  // The sum relative to m >= run.
+  __device__ __forceinline__ float at(float m, float c) const { return sum > 0.f ? sum * ex2((run - m) * c) : 0.f; }
+};
+
 // One CTA's slice of a row, as one warp sees it: its segment.
 template <int DT>
 struct RowSlice {
@@ -273,12 +314,27 @@ struct RowSlice {
   // The maximum over the segment (all lanes), NaN if any logit is NaN; `mine`:
   // over each quarter of this lane's vectors (in turn).  The vectors not held
   // come first, while the copies of the others run; sets `landed` as load_wait.
-  __device__ float warp_max(uint64_t* bar, float (&mine)[4], bool& landed) {
+  // `rs`, if given, gets this lane's running sum on the way.
+  __device__ float warp_max(uint64_t* bar, float (&mine)[4], bool& landed, RunningSum* rs = nullptr, float c = 0.f) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) mine[u] = neg_inf();
     auto add = [&](const Vec(&x)[4], int) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) mine[u] = vec_max<DT>(x[u], mine[u]);
+      if (rs) {
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+          uint64_t z[E::VW], lo[E::VW / 2], hi[E::VW / 2];
+          unpack_pairs<DT>(x[h], lo);
+          unpack_pairs<DT>(x[h + 1], hi);
+#pragma unroll
+          for (int k = 0; k < E::VW / 2; ++k) {
+            z[k] = lo[k];
+            z[E::VW / 2 + k] = hi[k];
+          }
+          rs->add(z, max_nan(max3_nan(mine[0], mine[1], mine[2]), mine[3]), c);
+        }
+      }
     };
     memory_groups<4>(add);
     landed = load_wait(bar);
@@ -376,20 +432,6 @@ __device__ __forceinline__ void store_warp(void* row, int i, int V, bool on, uin
       else reinterpret_cast<uint32_t*>(at)[k] = own[k % 4];
     }
   }
-}
-
-// A vector's logits as pairs of fp32 for the paired arithmetic.
-template <int DT>
-__device__ __forceinline__ void unpack_pairs(const typename Elem<DT>::Vec& v, uint64_t (&z)[Elem<DT>::VW / 2]) {
-  float x[Elem<DT>::VW];
-  Elem<DT>::unpack(v, x);
-#pragma unroll
-  for (int k = 0; k < Elem<DT>::VW / 2; ++k) z[k] = f2(x[2 * k], x[2 * k + 1]);
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 
 // v into slot[my rank] of every CTA of the cluster (threads 0..C-1 of the CTA

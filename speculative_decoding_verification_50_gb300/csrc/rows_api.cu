@@ -197,7 +197,8 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   p.k = k;
   p.z = a->logits;
   p.rs = a->row_stride;
-  p.c = static_cast<float>(1.4426950408889634 / static_cast<double>(a->temperature));
+  p.invT = 1.0 / static_cast<double>(a->temperature);
+  p.c = static_cast<float>(1.4426950408889634 * p.invT);
   p.ids = a->ids;
   p.values = a->values;
   p.lse = a->lse;
