@@ -246,35 +246,35 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     }
     // the logits that are not listed
     const unsigned char* byte = reinterpret_cast<const unsigned char*>(bits);
-    auto add = [&](const Vec(&y)[2], int j) {
-      uint64_t z[VW];
-      float top = rs.run;
+    auto add = [&](const Vec(&y)[4], int j0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const unsigned listed = j + 32 * u < sl.nv ? vector_bits<DT>(byte, sl.v0 + j + 32 * u) : 0u;
-        if (listed) {
+      for (int h = 0; h < 4; h += 2) {
+        uint64_t z[VW];
+        float top = rs.run;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = j0 + 32 * (h + u);
+          const unsigned listed = j < sl.nv ? vector_bits<DT>(byte, sl.v0 + j) : 0u;
           float x[VW];
-          E::unpack(y[u], x);
+          E::unpack(y[h + u], x);
+          if (listed) {
 #pragma unroll
-          for (int k = 0; k < VW; ++k) x[k] = (listed >> k) & 1u ? neg_inf() : x[k];
-#pragma unroll
-          for (int k = 0; k < VW / 2; ++k) {
-            z[u * (VW / 2) + k] = f2(x[2 * k], x[2 * k + 1]);
-            top = max3_nan(top, x[2 * k], x[2 * k + 1]);
+            for (int k = 0; k < VW; ++k) {
+              x[k] = (listed >> k) & 1u ? neg_inf() : x[k];
+              top = max_nan(top, x[k]);
+            }
+          } else {
+            top = vec_max<DT>(y[h + u], top);
           }
-        } else {
-          uint64_t x[VW / 2];
-          unpack_pairs<DT>(y[u], x);
 #pragma unroll
-          for (int k = 0; k < VW / 2; ++k) z[u * (VW / 2) + k] = x[k];
-          top = vec_max<DT>(y[u], top);
+          for (int k = 0; k < VW / 2; ++k) z[u * (VW / 2) + k] = f2(x[2 * k], x[2 * k + 1]);
         }
+        rs.add(z, top, c);
       }
-      rs.add(z, top, c);
     };
-    sl.template memory_groups<2>(add);
+    sl.template memory_groups<4>(add);
     if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
-    sl.template held_groups<2>(add);
+    sl.template held_groups<4>(add);
     if (bad) atomicOr(&badbits, bad);
   }
   // the slice's maximum, listed ids included
@@ -370,13 +370,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   const float f = wt * ih;
   const float ga = f * row_alpha;
   const uint64_t c2 = f2(c, c), m2 = f2(-mx, -mx), g2 = f2(ga, ga);
-  for (int j0 = 0; j0 < sl.nv; j0 += 64) {
-    Vec y[2];
+  for (int j0 = 0; j0 < sl.nv; j0 += 128) {
+    Vec y[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 4; ++u)
       if (!dead && j0 + 32 * u + lane < sl.nv) y[u] = sl.vec(j0 + 32 * u + lane);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 4; ++u) {
       const int j = j0 + 32 * u + lane;
       if (j0 + 32 * u >= sl.nv) break;
       const bool on = j < sl.nv;

@@ -394,7 +394,7 @@ __device__ __forceinline__ void store_warp(void* row, int i, int V, bool on, uin
   const bool inside = on && i >= 0 && i + E::VW <= V;
   if (mis == 0) {
     if (inside) {
-      *reinterpret_cast<uint4*>(at) = w;
+      __stcs(reinterpret_cast<uint4*>(at), w);  // (not read again: rows that are stay in L2)
       return;
     }
   } else {
@@ -410,7 +410,7 @@ __device__ __forceinline__ void store_warp(void* row, int i, int V, bool on, uin
     const bool prev = __shfl_up_sync(0xffffffffu, inside, 1) && lane > 0;
     if (inside) {
       const int skip = 16 - mis;
-      if (next) *reinterpret_cast<uint4*>(at + skip) = shift_bytes(w, n, skip);
+      if (next) __stcs(reinterpret_cast<uint4*>(at + skip), shift_bytes(w, n, skip));
       // what no aligned vector covers: the first lane's head, the last's tail
       const uint32_t own[4] = {w.x, w.y, w.z, w.w};
       const int head = skip / E::ES;
