@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   using Vec = typename E::Vec;
   constexpr int VW = E::VW;
   extern __shared__ __align__(16) char smem[];
-  __shared__ uint64_t bars[kRowWarps];
+  __shared__ uint64_t bars[kRowWarps * kMaxRing];
   __shared__ float tred[kRowWarps], mred[kRowWarps], rred[kRowWarps], lred[kRowWarps], ared[kRowWarps];
   __shared__ uint64_t ured[kRowWarps];
   __shared__ DistillPart part[kMaxCluster];
@@ -152,14 +152,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   cluster_arrive();  // waited for before the first remote write
   const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
   char* grow = reinterpret_cast<char*>(P.grad) + row * P.grs * E::ES;
-  RowSlice<DT> sl;
-  sl.init(smem, P.sp, zrow, rank, warp);
+  RowSlice<DT, true> sl;
+  sl.init(smem, bars, P.sp, zrow, rank, warp);
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;
   if (threadIdx.x == 0) badbits = again = 0;
   const int words = (P.sp.svec * VW + 31) / 32;
-  unsigned* bits = reinterpret_cast<unsigned*>(smem + static_cast<size_t>(P.sp.rvec) * kRowWarps * 16);
-  int32_t* ids = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(P.sp.rvec) * kRowWarps * 16 +
+  unsigned* bits = reinterpret_cast<unsigned*>(smem + row_bytes(P.sp.rvec, P.sp.stages));
+  int32_t* ids = reinterpret_cast<int32_t*>(smem + row_bytes(P.sp.rvec, P.sp.stages) +
                                             distill_bytes(P.sp.svec, VW, 0));
   float* tl = reinterpret_cast<float*>(ids + K);
   float* pj = tl + K;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   float zmax = neg_inf(), a = 0.f;
   bool some = true;  // (without a log-sum-exp: there are entries)
   if (!skip) {
-    sl.load(&bars[warp]);
+    sl.load();
     for (int i = threadIdx.x; i < words; i += kRowThreads) bits[i] = 0;
     // the teacher's entries, in every CTA
     int bad = 0;
@@ -246,35 +246,31 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     }
     // the logits that are not listed
     const unsigned char* byte = reinterpret_cast<const unsigned char*>(bits);
-    auto add = [&](const Vec(&y)[4], int j0) {
+    sl.ready();
+    sl.groups([&](const Vec(&y)[2], int j) {
+      uint64_t z[VW];
+      float top = rs.run;
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        uint64_t z[VW];
-        float top = rs.run;
+      for (int u = 0; u < 2; ++u) {
+        const unsigned listed = j + 32 * u < sl.nv ? vector_bits<DT>(byte, sl.v0 + j + 32 * u) : 0u;
+        float x[VW];
+        E::unpack(y[u], x);
+        if (listed) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int j = j0 + 32 * (h + u);
-          const unsigned listed = j < sl.nv ? vector_bits<DT>(byte, sl.v0 + j) : 0u;
-          float x[VW];
-          E::unpack(y[h + u], x);
-          if (listed) {
-#pragma unroll
-            for (int k = 0; k < VW; ++k) {
-              x[k] = (listed >> k) & 1u ? neg_inf() : x[k];
-              top = max_nan(top, x[k]);
-            }
-          } else {
-            top = vec_max<DT>(y[h + u], top);
+          for (int k = 0; k < VW; ++k) {
+            x[k] = (listed >> k) & 1u ? neg_inf() : x[k];
+            top = max_nan(top, x[k]);
           }
-#pragma unroll
-          for (int k = 0; k < VW / 2; ++k) z[u * (VW / 2) + k] = f2(x[2 * k], x[2 * k + 1]);
+        } else {
+          top = vec_max<DT>(y[u], top);
         }
-        rs.add(z, top, c);
+#pragma unroll
+        for (int k = 0; k < VW / 2; ++k) z[u * (VW / 2) + k] = f2(x[2 * k], x[2 * k + 1]);
       }
-    };
-    sl.template memory_groups<4>(add);
-    if (!sl.load_wait(&bars[warp])) bad |= kTimeout;
-    sl.template held_groups<4>(add);
+      rs.add(z, top, c);
+    });
+    if (!sl.landed) bad |= kTimeout;
+    if (P.grad && sl.stages > 0) sl.prime();  // (the second pass's first copies)
     if (bad) atomicOr(&badbits, bad);
   }
   // the slice's maximum, listed ids included
@@ -370,21 +366,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   const float f = wt * ih;
   const float ga = f * row_alpha;
   const uint64_t c2 = f2(c, c), m2 = f2(-mx, -mx), g2 = f2(ga, ga);
-  for (int j0 = 0; j0 < sl.nv; j0 += 128) {
-    Vec y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (!dead && j0 + 32 * u + lane < sl.nv) y[u] = sl.vec(j0 + 32 * u + lane);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = j0 + 32 * u + lane;
-      if (j0 + 32 * u >= sl.nv) break;
-      const bool on = j < sl.nv;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (on && !dead) w = gradients<DT>(y[u], m2, c2, g2);
-      store_warp<DT>(grow, sl.index(j), V, on, w);
-    }
+  if (skip) {  // (nothing was copied)
+    for (int j0 = 0; j0 < sl.nv; j0 += 32)
+      store_warp<DT>(grow, sl.index(j0 + lane), V, j0 + lane < sl.nv, make_uint4(0u, 0u, 0u, 0u));
+    return;
   }
+  sl.groups([&](const Vec(&y)[2], int j) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint4 w = dead ? make_uint4(0u, 0u, 0u, 0u) : gradients<DT>(y[u], m2, c2, g2);
+      store_warp<DT>(grow, sl.index(j + 32 * u), V, j + 32 * u < sl.nv, w);
+    }
+  });
   if (dead) return;
   __syncthreads();  // the listed ids' gradients go over what was just written
   for (int j = threadIdx.x; j < K; j += kRowThreads) {

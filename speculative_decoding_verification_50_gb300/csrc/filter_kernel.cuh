@@ -168,7 +168,7 @@ struct Decision {
 };
 
 struct FilterShared {
-  uint64_t bars[kRowWarps];
+  uint64_t bars[kRowWarps * kMaxRing];
   uint64_t tab[kGrid];
   float total[kBins];        // the row's histogram; then, in rank 0, bins of the list
   uint64_t Z;                // the row's weight
@@ -219,7 +219,7 @@ enum CutKind { kByCount, kByMass, kGiven };
 template <int DT, bool CLAMP>
 struct FilterRow {
   FilterShared& S;
-  RowSlice<DT> sl;
+  RowSlice<DT, false> sl;
   const RowSplit& split;  // (of the launch's arguments: no registers)
   const int &C, &V, &H;
   Scale sc;
@@ -233,9 +233,9 @@ struct FilterRow {
 
   __device__ FilterRow(FilterShared& s, const RowSplit& sp, char* shared, const void* z)
       : S(s), split(sp), C(sp.C), V(sp.V), H(sp.H), smem(shared), rank(cluster_rank()), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {
-    work = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(sp.rvec) * kRowWarps * 16);
+    work = reinterpret_cast<uint64_t*>(smem + row_bytes(sp.rvec, 0));
     sub = warp * sp.H / kRowWarps;
-    sl.init(smem, sp, z, rank, warp);
+    sl.init(smem, S.bars, sp, z, rank, warp);
     fbits = min(44, 62 - (32 - __clz(V)));
   }
 
@@ -404,12 +404,12 @@ struct FilterRow {
   }
 
   // Collects a superset of the set's k first tokens: the k-th largest of the
-  // threads' own maxima (`mine`, four each) is a bound for the k-th largest
+  // threads' own maxima (`mine`, two each) is a bound for the k-th largest
   // logit, so a histogram of those takes the place of one of every logit.
   // False where that names no band, or one too full to collect.
-  __device__ bool collect_top(int k, const float (&mine)[4], Band& b) {
+  __device__ bool collect_top(int k, const float (&mine)[2], Band& b) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 2; ++u)
       if (mine[u] >= zc) atomicAdd(&hist(sub)[max(0, sc.template bin<CLAMP>(mine[u]))], 1u);
     __syncthreads();
     merge<false>(kBins);
@@ -448,11 +448,11 @@ struct FilterRow {
   // test by bin after the pass, on the list.  Above kCap tokens in a CTA the
   // numbers are not complete.
   __device__ void collect_bins(const Band& b) {
-    constexpr int VW = Elem<DT>::VW, G = 4;
+    constexpr int VW = Elem<DT>::VW, G = 2;
     using Vec = typename Elem<DT>::Vec;
     uint64_t* raw = list();
     int above = 0;
-    sl.template groups<G>([&](const Vec(&x)[G], int j0) {
+    sl.groups([&](const Vec(&x)[G], int j0) {
       unsigned zone = 0;  // a bit for each logit
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -502,11 +502,11 @@ struct FilterRow {
 
   // ... for any band, the numbers complete whatever is collected.
   __device__ void collect_exact(const Band& b) {
-    constexpr int VW = Elem<DT>::VW, G = 4;  // vectors looked at together, a mask bit for each logit
+    constexpr int VW = Elem<DT>::VW, G = 2;  // a mask bit for each logit of two vectors
     using Vec = typename Elem<DT>::Vec;
     int above = 0, in_band = 0;
     uint64_t acc = 0;
-    sl.template groups<G>([&](const Vec(&x)[G], int j0) {
+    sl.groups([&](const Vec(&x)[G], int j0) {
       unsigned zone = 0;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -1139,8 +1139,8 @@ struct FilterRow {
   __device__ void draw(const void* row, int p, uint64_t rem, uint64_t W, int32_t* token, float* prob) {
     constexpr int VW = Elem<DT>::VW;
     const int per = kRowWarps >> shift_H();  // segments of the part
-    const RowSlice<DT> piece =
-        sl.part(smem, split, row, rank, (p & (H - 1)) * per + (warp >> shift_H()), warp & (H - 1), H);
+    RowSlice<DT, false> piece =
+        sl.piece(smem, S.bars, split, row, rank, (p & (H - 1)) * per + (warp >> shift_H()), warp & (H - 1), H);
     uint64_t mine = 0;
     piece.each([&](float z, int i) {
       if (in_set(z, i)) mine += weight(z);
@@ -1227,7 +1227,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   const char* zrow = reinterpret_cast<const char*>(P.z) + (b * P.bs + (row - b * P.R) * P.rs) * E::ES;
   FilterRow<DT, false> F(S, P.sp, smem, zrow);
   const int rank = F.rank, lane = F.lane, warp = F.warp;
-  F.sl.load(&S.bars[warp]);
+  F.sl.load();
   if (threadIdx.x < kGrid) S.tab[threadIdx.x] = P.tab.e[threadIdx.x];
   if (threadIdx.x == 0) S.bad = 0;
   if (threadIdx.x < kMaxH) S.mine[threadIdx.x] = 0;
@@ -1248,10 +1248,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     tm = mp > 0.f ? static_cast<double>(Tc) * fmax(log(static_cast<double>(mp)), lnf) : tf;
   }
   __syncthreads();
-  float own[4];
-  bool landed;
-  const float wm = F.sl.warp_max(&S.bars[warp], own, landed);
-  if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
+  float own[2];
+  const float wm = F.sl.warp_max(own);
+  if (!F.sl.landed && lane == 0) atomicOr(&S.bad, kTimeout);
   const float mc = block_max_nan(wm, S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);
@@ -1307,7 +1306,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     const bool use_k = k > 0 && k < V, use_p = tp < 1.f;
     Band band;
     bool done = false;
-    if (use_k && kFewTop * k <= 4 * C * kRowThreads) {
+    if (use_k && kFewTop * k <= 2 * C * kRowThreads) {
       if (F.collect_top(k, own, band)) {
         if (rank == 0) F.resolve_top(F.collected(), k, tp, zt, u);
         F.publish();
@@ -1446,18 +1445,17 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 
   if (P.out) {
     char* orow = reinterpret_cast<char*>(P.out) + (b * P.obs + (row - b * P.R) * P.ors) * E::ES;
-    for (int j0 = 0; j0 < F.sl.nv; j0 += 32) {
-      const int j = j0 + lane, i0 = F.sl.index(j);
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (j < F.sl.nv) {
+    F.sl.groups([&](const typename E::Vec(&x)[2], int j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i0 = F.sl.index(j + 32 * h);
         float z[E::VW];
-        E::unpack(F.sl.vec(j), z);
+        E::unpack(x[h], z);
 #pragma unroll
         for (int q = 0; q < E::VW; ++q) z[q] = F.in_set(z[q], i0 + q) ? z[q] : neg_inf();
-        w = pack_vec<DT>(z);
+        store_warp<DT>(orow, i0, V, j + 32 * h < F.sl.nv, pack_vec<DT>(z));
       }
-      store_warp<DT>(orow, i0, V, j < F.sl.nv, w);
-    }
+    });
   }
 }
 
@@ -1472,15 +1470,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   cluster_arrive();
   FilterRow<DT, true> F(S, P.sp, smem, reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES);
   const int rank = F.rank, lane = F.lane, warp = F.warp;
-  F.sl.load(&S.bars[warp]);
+  F.sl.load();
   if (threadIdx.x == 0) S.bad = 0;
   if (threadIdx.x < kMaxH) S.mine[threadIdx.x] = 0;
   F.clear();  // (a barrier)
-  float own[4];
-  bool landed;
+  float own[2];
   RunningSum rs;  // (the log-sum-exp's share, in the same pass)
-  const float wm = F.sl.warp_max(&S.bars[warp], own, landed, &rs, P.c);
-  if (!landed && lane == 0) atomicOr(&S.bad, kTimeout);
+  const float wm = F.sl.warp_max(own, &rs, P.c);
+  if (!F.sl.landed && lane == 0) atomicOr(&S.bad, kTimeout);
   const float mc = block_max_nan(wm, S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);
@@ -1521,9 +1518,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   for (int w = 0; w < kRowWarps; ++w) s += S.fscratch[w];
   push_all(S.xexp, rank, C, s);
   Band band;
-  bool done = kFewTop * k <= 4 * C * kRowThreads && F.collect_top(k, own, band);
+  bool done = kFewTop * k <= 2 * C * kRowThreads && F.collect_top(k, own, band);
   if (!done) {
-    if (kFewTop * k <= 4 * C * kRowThreads) F.clear();
+    if (kFewTop * k <= 2 * C * kRowThreads) F.clear();
     F.sl.each([&](float z, int) {
       if (z >= kNegMax) atomicAdd(&F.hist(F.sub)[max(F.sc.template bin<true>(z), 0)], 1u);
     });

@@ -1,14 +1,14 @@
-// Rows of logits held on chip by a thread-block cluster.
+// Rows of logits over thread-block clusters.
 //
 // The kernels of filtered sampling, of the top logits and of the distillation
 // loss need several passes over a row (its maximum, a histogram, a cut, a
-// result).  A cluster of C CTAs takes one row: each CTA copies its slice into
-// shared memory once (one bulk copy per warp's segment) and every pass after
-// that reads shared memory, so HBM sees each logit once.  CTAs exchange a few
-// values through distributed shared memory between cluster barriers.  With
-// enough rows to fill the SMs, sampling takes one CTA per row instead, of whose
-// row a part is held and the rest read again from L2 in each pass: the fixed
-// costs of a CTA and the waits of a cluster then come once per row.
+// result).  A cluster of C CTAs takes one row.  Few rows: each CTA copies its
+// slice into shared memory once (one bulk copy per warp's segment) and every
+// pass reads it there.  Rows enough to fill the SMs: fewer CTAs per row (one or
+// two), and every pass streams the slice, the first from HBM and the others from
+// L2, so that the fixed costs of a CTA and the waits of a cluster come less
+// often per row.  CTAs exchange a few values through distributed shared memory
+// between cluster barriers.
 #pragma once
 
 #include "specv_common.cuh"
@@ -18,7 +18,13 @@ namespace specv {
 constexpr int kRowThreads = 512;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kMaxSegs = kMaxCluster * kRowWarps;
+constexpr int kStage = 64;     // vectors of a ring's stage: two per lane
+constexpr int kMaxRing = 6;
+
+// Bytes of a CTA's held vectors and its warps' rings.
+__host__ __device__ constexpr size_t row_bytes(int rvec, int stages) {
+  return static_cast<size_t>(rvec + stages * kStage) * kRowWarps * 16;
+}
 
 // How a row is spread, in vectors of 16 bytes from its first logit on: CTA r
 // holds vectors [r * svec, (r + 1) * svec), its warp w the segment [w * gvec,
@@ -31,6 +37,7 @@ struct RowSplit {
   int32_t svec;    // vectors per CTA
   int32_t gvec;    // vectors per warp segment
   int32_t rvec;    // of them, those held in shared memory (the first)
+  int32_t stages;  // of the ring that the others are streamed through, kStage vectors each; 0: plain loads
   int32_t H;       // parts of a CTA's slice that are summed apart (1, 2 or 4)
 };
 
@@ -135,35 +142,53 @@ struct RunningSum {
   __device__ __forceinline__ float at(float m, float c) const { return sum > 0.f ? sum * ex2((run - m) * c) : 0.f; }
 };
 
-// One CTA's slice of a row, as one warp sees it: its segment.
-template <int DT>
+// One CTA's slice of a row, as one warp sees it: its segment.  RING: either
+// held whole or streamed through the ring; else held in part (or whole) and the
+// rest streamed by plain loads.  (The ring pays where a pass is short: loss and
+// gradient of 1024 x 128256 bf16 149 us with loads, 133 with a ring of 1 KB
+// stages.  Sampling's longer passes and its histograms, which leave room for
+// three stages, go the other way: 2304 x 152064 fp32 1176 us with loads, 1369
+// with the ring; the 256 top logits of 2048 x 152064 bf16 250, 311.)
+template <int DT, bool RING>
 struct RowSlice {
   using E = Elem<DT>;
   using Vec = typename E::Vec;
-  Vec* data;        // the held vectors of the segment, in shared memory
+  Vec* data;        // in shared memory: the held vectors, or the warp's ring
+  uint64_t* bars;   // the warp's barriers: one, or one per stage
   const char* src;  // the segment in memory
   int v0;           // the segment's first vector, within the slice
   int nv, rv;       // its vectors; of them, those held
   int base;         // index of the slice's first place in the row
   int left;         // logits of the row from the segment's first on
-  int plain;        // vectors that one aligned load brings (none of a row that starts past a boundary)
-  int mis;          // bytes by which the row starts past a 16-byte boundary
+  int plain;        // vectors that aligned copies bring (none of a row that starts past a 16-byte boundary)
+  int mis;          // bytes by which the row starts past one
   int lane;
+  int stages;       // 0: held
+  int stage;        // the ring's next stage to be read ...
+  uint32_t parity;  // ... and its barrier's phase
+  bool primed;      // the next pass's first copies are under way
+  bool landed;      // every copy waited for arrived in time
 
-  __device__ void init(char* smem, const RowSplit& sp, const void* row, int rank, int w) {
+  __device__ void init(char* smem, uint64_t* barriers, const RowSplit& sp, const void* row, int rank, int w) {
     lane = threadIdx.x & 31;
     const int nvec = static_cast<int>((static_cast<int64_t>(sp.V) + E::VW - 1) / E::VW);
     const int first = rank * sp.svec;
     const int mine = max(0, min(sp.svec, nvec - first));
     v0 = min(w * sp.gvec, mine);
     nv = min((w + 1) * sp.gvec, mine) - v0;
-    rv = min(nv, sp.rvec);
     base = first * E::VW;
-    data = reinterpret_cast<Vec*>(smem) + w * sp.rvec;
+    rv = min(nv, sp.rvec);
+    stages = RING ? sp.stages : 0;
+    data = reinterpret_cast<Vec*>(smem) + w * (sp.rvec + stages * kStage);
+    bars = barriers + w * kMaxRing;
     left = sp.V - base - v0 * E::VW;
     src = reinterpret_cast<const char*>(row) + static_cast<int64_t>(base + v0 * E::VW) * E::ES;
     mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
     plain = mis == 0 ? max(0, min(nv, left / E::VW)) : 0;
+    stage = 0;
+    parity = 0;
+    primed = false;
+    landed = true;
   }
 
   // Vector j of the segment from memory (-inf after the row's last logit).
@@ -189,14 +214,8 @@ struct RowSlice {
   }
 
   // Vector j < nv, held or not.
-  __device__ __forceinline__ Vec vec(int j) const {
-    if (j < rv) return data[j];
-    if (j < plain) return load_plain(j);
-    return fetch(j);
-  }
-  __device__ __forceinline__ Vec load_plain(int j) const {
-    return *reinterpret_cast<const Vec*>(src + static_cast<int64_t>(j) * 16);
-  }
+  __device__ __forceinline__ Vec vec(int j) const { return j < rv ? data[j] : fetch(j); }
+
   __device__ __forceinline__ static Vec none() {
     union {
       typename E::Raw r[E::VW];
@@ -206,22 +225,42 @@ struct RowSlice {
     for (int k = 0; k < E::VW; ++k) x.r[k] = E::neg_inf_raw();
     return x.v;
   }
-  // This lane's first vector from number n on.
-  __device__ __forceinline__ int from(int n) const { return lane + (max(n - lane, 0) + 31) / 32 * 32; }
 
-  // Starts this warp's copies; load_wait() before the held vectors are read.
-  // `bar` is the warp's own barrier.  Rows that start at a 16-byte boundary
-  // take one bulk copy.
-  __device__ void load(uint64_t* bar) {
-    const int full = mis == 0 ? max(0, min(rv, left / E::VW)) : 0;
+  // Lane 0: chunk c of the segment into stage s of the ring.
+  __device__ __forceinline__ void issue(int c, int s) const {
+    const uint32_t bytes = static_cast<uint32_t>(min(kStage, plain - c * kStage)) * 16u;
+    mbar_arrive_expect_tx(&bars[s], bytes);
+    bulk_load(data + s * kStage, src + static_cast<int64_t>(c) * kStage * 16, bytes, &bars[s], false);
+  }
+  // (All lanes: what the last pass read has been used by every lane.)
+  __device__ void prime() {
+    __syncwarp();
+    if (lane == 0)
+      for (int c = 0; c < stages && c * kStage < plain; ++c) issue(c, (stage + c) % stages);
+    primed = true;
+  }
+
+  // Starts this warp's copies.  Held rows that start at a 16-byte boundary take
+  // one bulk copy.
+  __device__ void load() {
+    if (RING && stages > 0) {
+      if (lane == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+      }
+      __syncwarp();
+      prime();
+      return;
+    }
     if (lane == 0) {
-      mbar_init(bar, 1);
+      mbar_init(bars, 1);
       fence_mbar_init();
-      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(full) * 16u);
-      if (full > 0) bulk_load(data, src, static_cast<uint32_t>(full) * 16u, bar, rv == nv);
+      const uint32_t bytes = static_cast<uint32_t>(min(plain, rv)) * 16u;
+      mbar_arrive_expect_tx(bars, bytes);
+      if (bytes > 0) bulk_load(data, src, bytes, bars, rv == nv);
     }
     constexpr int U = 4;
-    for (int j0 = full + lane; j0 < rv; j0 += 32 * U) {
+    for (int j0 = plain + lane; j0 < rv; j0 += 32 * U) {
       Vec x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -233,61 +272,102 @@ struct RowSlice {
     __syncwarp();
   }
 
-  // False where the copies did not land within the bound (about two seconds).
-  __device__ bool load_wait(uint64_t* bar) {
-    bool ok = mbar_wait_bounded(bar, 0);
-    if (!ok) ok = mbar_wait_bounded(bar, 0);
-    __syncwarp();
-    return ok;
+  // A bounded wait (about two seconds) for a barrier of the warp's.
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase) {
+    if (!mbar_wait_bounded(bar, phase) && !mbar_wait_bounded(bar, phase)) landed = false;
   }
 
-  // f(vectors, number of the first) over groups of U of this lane's vectors of
-  // the segment, 32 apart (-inf past its end): those held, those of memory.
-  template <int U, typename Fn>
-  __device__ __forceinline__ void held_groups(Fn&& f) const {
-#pragma unroll 1
-    for (int j = lane; j < rv; j += 32 * U) {
-      Vec x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = u == 0 || j + 32 * u < rv ? data[j + 32 * u] : none();
-      f(x, j);
+  // Before held vectors are read for the first time.
+  __device__ void ready() {
+    if (!RING || stages == 0) {
+      wait(bars, 0);
+      __syncwarp();
     }
-  }
-  template <int U, typename Fn>
-  __device__ __forceinline__ void memory_groups(Fn&& f) const {
-    int j = from(rv);
-#pragma unroll 1
-    for (; j + 32 * (U - 1) < plain; j += 32 * U) {
-      Vec x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = load_plain(j + 32 * u);
-      f(x, j);
-    }
-#pragma unroll 1
-    for (; j < nv; j += 32 * U) {
-      Vec x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = j + 32 * u < nv ? fetch(j + 32 * u) : none();
-      f(x, j);
-    }
-  }
-  template <int U, typename Fn>
-  __device__ __forceinline__ void groups(Fn&& f) const {
-    held_groups<U>(f);
-    memory_groups<U>(f);
   }
 
-  // The q-th of n parts of warp w's segment.
-  __device__ RowSlice part(char* smem, const RowSplit& sp, const void* row, int rank, int w, int q, int n) const {
+  // f(two vectors 32 apart, number of the first) over this lane's vectors of the
+  // segment, -inf past its end.  The whole warp calls f together; j < nv says
+  // whether the lane's vectors exist (the second: j + 32 < nv).  first: the
+  // pass waits for the held vectors, after those that are streamed.
+  template <typename Fn>
+  __device__ __forceinline__ void groups(Fn&& f, bool first = false) {
+    if (!RING) {
+      int j0 = rv;  // (a multiple of kStage, or the segment's end)
+#pragma unroll 1
+      for (; j0 + 2 * kStage <= plain; j0 += 2 * kStage) {  // four loads under way
+        const Vec* at = reinterpret_cast<const Vec*>(src) + j0 + lane;
+        const Vec x[2] = {at[0], at[32]}, y[2] = {at[64], at[96]};
+        f(x, j0 + lane);
+        f(y, j0 + lane + kStage);
+      }
+#pragma unroll 1
+      for (; j0 < nv; j0 += kStage) {
+        const int j = j0 + lane;
+        const Vec x[2] = {j < nv ? fetch(j) : none(), j + 32 < nv ? fetch(j + 32) : none()};
+        f(x, j);
+      }
+    }
+    if (first) ready();
+    if (!RING || stages == 0) {
+#pragma unroll 1
+      for (int j0 = 0; j0 < rv; j0 += kStage) {
+        const int j = j0 + lane;
+        const Vec x[2] = {j < rv ? data[j] : none(), j + 32 < rv ? data[j + 32] : none()};
+        f(x, j);
+      }
+      return;
+    }
+    int j0 = 0;
+    if (!primed) prime();
+    primed = false;
+#pragma unroll 1
+    for (int c = 0; j0 < plain; ++c, j0 += kStage) {
+      const int j = j0 + lane;
+      wait(&bars[stage], parity);
+      const Vec* at = data + stage * kStage + lane;
+      Vec x[2] = {at[0], at[32]};
+      // Every lane has been through f for the chunk before, so its reads of that
+      // stage have ended and it can be filled again.  (Not this chunk's stage:
+      // its reads are only under way.  Filled here, a copy from L2 overtook them.)
+      __syncwarp();
+      if (lane == 0 && c > 0 && (c - 1 + stages) * kStage < plain)
+        issue(c - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
+      if (++stage == stages) {
+        stage = 0;
+        parity ^= 1;
+      }
+      if (j0 + kStage > plain) {  // the segment's last chunk: the rest is read without a copy
+        if (j >= plain) x[0] = j < nv ? fetch(j) : none();
+        if (j + 32 >= plain) x[1] = j + 32 < nv ? fetch(j + 32) : none();
+      }
+      f(x, j);
+    }
+#pragma unroll 1
+    for (; j0 < nv; j0 += kStage) {
+      const int j = j0 + lane;
+      const Vec x[2] = {j < nv ? fetch(j) : none(), j + 32 < nv ? fetch(j + 32) : none()};
+      f(x, j);
+    }
+  }
+
+  // The q-th of n pieces of warp w's segment, through this warp's ring.
+  __device__ RowSlice piece(char* smem, uint64_t* barriers, const RowSplit& sp, const void* row, int rank, int w, int q,
+                            int n) const {
     RowSlice s;
-    s.init(smem, sp, row, rank, w);
+    s.init(smem, barriers, sp, row, rank, w);
     const int per = (s.nv + n - 1) / n, at = min(q * per, s.nv);
-    s.data += at;
+    if (RING && stages > 0) {
+      s.data = data;
+      s.bars = bars;
+      s.stage = stage;
+      s.parity = parity;
+    } else {
+      s.data += at;
+    }
+    s.rv = max(0, min(per, s.rv - at));
     s.src += static_cast<int64_t>(at) * 16;
     s.v0 += at;
-    s.rv = max(0, s.rv - at);
     s.nv = min(per, s.nv - at);
-    s.rv = min(s.rv, s.nv);
     s.left -= at * E::VW;
     s.plain = s.mis == 0 ? max(0, min(s.nv, s.left / E::VW)) : 0;
     return s;
@@ -295,8 +375,8 @@ struct RowSlice {
 
   // f(z, index) over this lane's logits of the segment, padding (-inf) included.
   template <typename Fn>
-  __device__ __forceinline__ void each(Fn&& f) const {
-    groups<2>([&](const Vec(&x)[2], int j) {
+  __device__ __forceinline__ void each(Fn&& f) {
+    groups([&](const Vec(&x)[2], int j) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float z[E::VW];
@@ -312,34 +392,26 @@ struct RowSlice {
   __device__ __forceinline__ int index(int j) const { return base + (v0 + j) * E::VW; }
 
   // The maximum over the segment (all lanes), NaN if any logit is NaN; `mine`:
-  // over each quarter of this lane's vectors (in turn).  The vectors not held
-  // come first, while the copies of the others run; sets `landed` as load_wait.
-  // `rs`, if given, gets this lane's running sum on the way.
-  __device__ float warp_max(uint64_t* bar, float (&mine)[4], bool& landed, RunningSum* rs = nullptr, float c = 0.f) {
+  // over each half of this lane's vectors (in turn); `rs`, if given, gets this
+  // lane's running sum on the way.
+  __device__ float warp_max(float (&mine)[2], RunningSum* rs = nullptr, float c = 0.f) {
+    mine[0] = mine[1] = neg_inf();
+    groups([&](const Vec(&x)[2], int) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mine[u] = neg_inf();
-    auto add = [&](const Vec(&x)[4], int) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) mine[u] = vec_max<DT>(x[u], mine[u]);
+      for (int u = 0; u < 2; ++u) mine[u] = vec_max<DT>(x[u], mine[u]);
       if (rs) {
+        uint64_t z[E::VW], lo[E::VW / 2], hi[E::VW / 2];
+        unpack_pairs<DT>(x[0], lo);
+        unpack_pairs<DT>(x[1], hi);
 #pragma unroll
-        for (int h = 0; h < 4; h += 2) {
-          uint64_t z[E::VW], lo[E::VW / 2], hi[E::VW / 2];
-          unpack_pairs<DT>(x[h], lo);
-          unpack_pairs<DT>(x[h + 1], hi);
-#pragma unroll
-          for (int k = 0; k < E::VW / 2; ++k) {
-            z[k] = lo[k];
-            z[E::VW / 2 + k] = hi[k];
-          }
-          rs->add(z, max_nan(max3_nan(mine[0], mine[1], mine[2]), mine[3]), c);
+        for (int k = 0; k < E::VW / 2; ++k) {
+          z[k] = lo[k];
+          z[E::VW / 2 + k] = hi[k];
         }
+        rs->add(z, max_nan(mine[0], mine[1]), c);
       }
-    };
-    memory_groups<4>(add);
-    landed = load_wait(bar);
-    held_groups<4>(add);
-    float m = max_nan(max3_nan(mine[0], mine[1], mine[2]), mine[3]);
+    }, true);
+    float m = max_nan(mine[0], mine[1]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;

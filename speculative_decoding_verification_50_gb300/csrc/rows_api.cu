@@ -25,6 +25,7 @@ specv_status check_rows(const char* what, int32_t n, int32_t V, int32_t dtype) {
 }
 
 constexpr size_t kSmemSm = 228 * 1024, kSmemCta = 227 * 1024, kSmemReserved = 1024;
+constexpr size_t kDistillStatic = 2048;  // (at least what distill_kernel declares)
 
 // The row's split over a cluster of C CTAs (a power of two) whose slices stay
 // in shared memory beside `extra` bytes per CTA.  C is the smallest for which
@@ -47,8 +48,9 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
   sp.svec = static_cast<int32_t>((nvec + C - 1) / C);
   sp.gvec = static_cast<int32_t>(segment(C));
   sp.rvec = sp.gvec;
+  sp.stages = 0;
   sp.H = 1;
-  smem = static_cast<size_t>(sp.gvec) * kRowWarps * 16;
+  smem = row_bytes(sp.rvec, 0);
   return true;
 }
 
@@ -57,14 +59,14 @@ constexpr int64_t kL2Rows = 96 << 20;
 
 // The split of rows that fill the SMs' slots (two CTAs each): as few CTAs per
 // row as leave the rows in flight to L2 (`again`: they are read again), since a
-// CTA's fixed costs and a cluster's waits then come less often per row; what a
-// CTA does not hold is read again in each pass.  extra(svec): a CTA's bytes
-// beside the held vectors.  False: few rows, or no fewer CTAs than sp has; those
+// CTA's fixed costs and a cluster's waits then come less often per row; the row
+// is streamed again in each pass.  extra(svec): a CTA's bytes beside its rings.
+// False: few rows, or no fewer CTAs than sp has; those
 // are held whole.
 //   `whole_waves`: not where the last wave of CTAs would be nearly empty.
 template <typename Extra>
-bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool whole_waves, int max_c, Extra&& extra,
-                  RowSplit& sp, size_t& smem) {
+bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool whole_waves, bool ring, int max_c,
+                  Extra&& extra, RowSplit& sp, size_t& smem) {
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
   const int64_t slots = 2LL * api_sm_count();
@@ -79,11 +81,14 @@ bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool whole
   const int32_t svec = static_cast<int32_t>((nvec + C - 1) / C);
   const size_t work = extra(svec), room = kSmemSm / 2 - kSmemReserved;
   if (work > room) return false;
+  const int64_t fits_too = static_cast<int64_t>(room - work) / row_bytes(1, 0);  // vectors per warp
+  if (ring && fits_too < 2 * kStage) return false;
   sp.C = C;
   sp.svec = svec;
   sp.gvec = (svec + kRowWarps - 1) / kRowWarps;
-  sp.rvec = std::min(sp.gvec, again ? static_cast<int32_t>((room - work) / (16 * kRowWarps)) / 32 * 32 : 0);
-  smem = static_cast<size_t>(sp.rvec) * kRowWarps * 16;
+  sp.rvec = ring ? 0 : std::min(sp.gvec, static_cast<int32_t>(fits_too) / kStage * kStage);
+  sp.stages = ring ? std::min(kMaxRing, static_cast<int>(fits_too / kStage)) : 0;
+  smem = row_bytes(sp.rvec, sp.stages);
   return true;
 }
 
@@ -99,7 +104,7 @@ bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool top, RowSplit& sp
   const int H = top ? 1 : kMaxH;
   if (!split_row(rows, V, dtype, fixed + work_bytes(1), sp, smem)) return false;
   const int max_c = V / H <= kMaxBinned ? kMaxParts / H : 0;
-  if (split_stream(rows, V, dtype, true, !top, max_c, [&](int32_t) { return fixed + work_bytes(H); }, sp, smem)) sp.H = H;
+  if (split_stream(rows, V, dtype, true, !top, false, max_c, [&](int32_t) { return fixed + work_bytes(H); }, sp, smem)) sp.H = H;
   smem += work_bytes(sp.H);
   return true;
 }
@@ -275,10 +280,10 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   const int vw = 16 / elem_bytes(a->dtype);
   // (a held row's bits are at most a 16th of its bytes)
   const size_t bits = distill_bytes((a->V + vw - 1) / vw, vw, a->K);
-  if (!split_row(a->N, a->V, a->dtype, kSmemReserved + std::min<size_t>(bits, 16384 + static_cast<size_t>(a->K) * 20), p.sp, smem))
+  if (!split_row(a->N, a->V, a->dtype, kDistillStatic + std::min<size_t>(bits, 16384 + static_cast<size_t>(a->K) * 20), p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
-  split_stream(a->N, a->V, a->dtype, a->grad != nullptr, false, kMaxCluster,
-               [&](int32_t svec) { return kSmemReserved + distill_bytes(svec, vw, a->K); }, p.sp, smem);
+  split_stream(a->N, a->V, a->dtype, a->grad != nullptr, false, true, kMaxCluster,
+               [&](int32_t svec) { return kDistillStatic + distill_bytes(svec, vw, a->K); }, p.sp, smem);
   smem += distill_bytes(p.sp.svec, vw, a->K);
   if (static_cast<int64_t>(a->N) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   p.loss = a->loss;
