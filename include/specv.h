@@ -38,11 +38,14 @@
  *     specv_mss_verify are two kernels: one streaming pass over every logit
  *     (per-chunk statistics and candidates into the workspace), then one
  *     decision per batch row (launched as a programmatic dependent of the
- *     first).  The workspace needs no initialisation: everything a call
+ *     first).  specv_sample, specv_top_logits, specv_distill and
+ *     specv_distill_backward are one kernel each, without a workspace.
+ *     The workspace needs no initialisation: everything a call
  *     reads from it is written earlier in the same call.  A call only
  *     enqueues kernels on the given stream, so it can be captured in a CUDA
  *     graph and replayed (on new inputs written into the same buffers).
- *   - Limits: 1 <= K <= 32, 0 <= B, 1 <= F <= 32, 1 <= V < 2^31 (in practice
+ *   - Limits: 1 <= K <= 32, 0 <= B, 1 <= F <= 32 (teacher entries and top
+ *     logits: up to SPECV_MAX_TOP), 1 <= V < 2^31 (in practice
  *     up to about 10^8: beyond that a CTA's table of partial sums no longer
  *     fits in shared memory and the call returns SPECV_ERR_UNSUPPORTED).
  */
@@ -355,13 +358,13 @@ specv_status specv_mss_verify(const specv_mss_args* args, void* workspace,
  *   place of z, verifies under the rules.  It may be `logits` itself (same
  *   strides); otherwise the two do not overlap.
  * uniforms and tokens are given together, or both NULL for `filtered` alone.
- * Sums carry about 30 bits more than their result needs (fp32 pairs, 64-bit
- * totals), so cuts and draws agree with 64-bit arithmetic except next to a
- * border by about 1e-10 of the row's weight.
+ * A weight is held to 2^-29 of itself and sums are of whole numbers, so cuts
+ * and draws agree with 64-bit arithmetic except next to a border by about 1e-10
+ * of the row's weight; sums that meet a border within 2^-36 count as on it.
  * Row status: SPECV_ROW_NONFINITE, SPECV_ROW_BAD_TEMP, SPECV_ROW_BAD_FILTER,
  * SPECV_ROW_DEVICE_TIMEOUT: token -1, prob 0, kept 0, filtered all -inf.
- * One kernel, no workspace: a cluster of CTAs holds the row in shared memory,
- * so V is at most about 780,000 (fp32) or 1,560,000 (bf16), else
+ * One kernel, no workspace: few rows are held in the shared memory of a cluster
+ * of CTAs each, so V is at most about 770,000 (fp32) or 1,540,000 (bf16), else
  * SPECV_ERR_UNSUPPORTED.
  */
 #define SPECV_ROW_BAD_FILTER 64 /* top_k < 0, or top_p or min_p outside [0, 1] */

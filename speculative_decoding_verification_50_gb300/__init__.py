@@ -687,7 +687,11 @@ _DistillLoss = None
 def distill_loss(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temperature: float = 1.0,
                  weights=None, tail: bool = False):
     """specv_distill's loss per row [N], differentiable with respect to logits
-    (once: the backward pass is specv_distill_backward)."""
+    (once: the backward pass is specv_distill_backward).  To capture a training
+    step in a CUDA graph, call specv_distill with a gradient buffer, or
+    specv_distill_backward, in it: an autograd graph of the same leaves that was
+    built outside the capture must not be alive while one is captured.
+    """
     global _DistillLoss
     if _DistillLoss is None:
         import torch

@@ -182,7 +182,6 @@ struct FilterShared {
   uint64_t scratch[kRowWarps];
   float fscratch[kRowWarps];
   int32_t iscratch[kRowWarps];
-  uint64_t fix[kMaxParts];
   uint64_t mine[kMaxH];      // per part: the weight in the bins before the band
   uint64_t mass[kMaxH];      // per part: of tokens above the band that share its bins
   int32_t band[kMaxH];       // per part: the band's tokens

@@ -53,11 +53,6 @@ __device__ __forceinline__ T* peer(T* p, int rank) {
   return cg::this_cluster().map_shared_rank(p, rank);
 }
 
-__device__ __forceinline__ double warp_sum_d(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 __device__ __forceinline__ float warp_sum_f(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -108,11 +103,6 @@ __device__ __forceinline__ void unpack_pairs(const typename Elem<DT>::Vec& v, ui
   Elem<DT>::unpack(v, x);
 #pragma unroll
   for (int k = 0; k < Elem<DT>::VW / 2; ++k) z[k] = f2(x[2 * k], x[2 * k + 1]);
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 
 // One thread's share of a softmax: its running maximum and the sum of
@@ -350,20 +340,13 @@ struct RowSlice {
     }
   }
 
-  // The q-th of n pieces of warp w's segment, through this warp's ring.
+  // The q-th of n pieces of warp w's segment.
   __device__ RowSlice piece(char* smem, uint64_t* barriers, const RowSplit& sp, const void* row, int rank, int w, int q,
                             int n) const {
     RowSlice s;
     s.init(smem, barriers, sp, row, rank, w);
     const int per = (s.nv + n - 1) / n, at = min(q * per, s.nv);
-    if (RING && stages > 0) {
-      s.data = data;
-      s.bars = bars;
-      s.stage = stage;
-      s.parity = parity;
-    } else {
-      s.data += at;
-    }
+    s.data += at;
     s.rv = max(0, min(per, s.rv - at));
     s.src += static_cast<int64_t>(at) * 16;
     s.v0 += at;
