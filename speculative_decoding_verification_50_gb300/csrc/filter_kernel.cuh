@@ -24,6 +24,8 @@ namespace specv {
 constexpr int kGrid = 32;                 // bins per unit of log2
 constexpr int kWindow = 48;               // units below the maximum that carry weight
 constexpr int kBins = kGrid * kWindow + 16;
+constexpr int kHead = 8 * kGrid;          // bins above a guessed maximum
+constexpr int kHist = kBins + kHead;      // of a CTA's histogram
 constexpr int kCap = 1536;                // tokens of a band that are worked on as a list
 constexpr int kMaxBinned = 250000;        // logits of a CTA, so that a bin's halves fit 32 bits
 constexpr int kMaxParts = 16;             // parts of a row that are summed apart: C * H
@@ -106,43 +108,47 @@ struct Scale {
   float shift, chi, clo;
   int gm;
 
-  // chi + clo = log2(e) / T, to about 2^-47.  bf16: chi has 16 digits, so that
-  // its products are exact.
-  template <int DT>
+  // chi + clo = log2(e) / T, to about 2^-47.
   __device__ void set_factor(float T) {
-    const float q = __fdiv_rn(1.44269502f, T);  // log2(e) = 1.44269502 + 1.925963e-8
-    const float rest = __fdiv_rn(fmaf(-q, T, 1.44269502f) + 1.925963e-8f, T);
-    chi = DT == 0 ? __int_as_float(__float_as_int(q) & 0xffffff00) : q;
-    clo = (q - chi) + rest;
+    chi = __fdiv_rn(1.44269502f, T);  // log2(e) = 1.44269502 + 1.925963e-8
+    clo = __fdiv_rn(fmaf(-chi, T, 1.44269502f) + 1.925963e-8f, T);
   }
   __device__ void set_max(float m) {
     // |y| stays within the rounding trick's range; shifted logits are exact
     // where they carry weight (within 48 units of a maximum of 2^14 units).
     shift = fabsf(m) * chi > 16384.f ? m : 0.f;
-    gm = __float_as_int(__fadd_rn(__fmul_rn(m - shift, chi), kMagic)) - __float_as_int(kMagic);
+    gm = place(m - shift);
   }
-  // Distance from the maximum in bins: rounding is monotone, so 0 <= bin <=
-  // 48 * 32 + 3 for a logit of the window.  CLAMP: for any logit below the
-  // maximum.
+  // x chi on the grid, as bits above those of 0 (rounding is monotone).
+  __device__ __forceinline__ int place(float x) const { return __float_as_int(fmaf(x, chi, kMagic)) - __float_as_int(kMagic); }
+  // Distance from the maximum in bins: 0 <= bin <= 48 * 32 + 3 for a logit of
+  // the window.  CLAMP: for any logit below the maximum.
   template <bool CLAMP>
   __device__ __forceinline__ int bin(float z) const {
-    float p = __fmul_rn(z - shift, chi);
-    if (CLAMP) p = fmaxf(p, -60000.f);
-    const int d = gm + __float_as_int(kMagic) - __float_as_int(__fadd_rn(p, kMagic));
-    return CLAMP ? min(d, kBins - 1) : d;
+    if (!CLAMP) return gm - place(z - shift);
+    const float r = fmaxf(fmaf(z - shift, chi, kMagic), kMagic - 60000.f);
+    return min(gm + __float_as_int(kMagic) - __float_as_int(r), kBins - 1);
+  }
+  // v of a logit of the window, and its place on the grid with the bits of 0's.
+  // SHIFT false: shift is 0.
+  template <bool SHIFT>
+  __device__ __forceinline__ uint32_t weight_at(float z, int& at) const {
+    const float x = SHIFT ? z - shift : z;
+    const float r = fmaf(x, chi, kMagic);
+    at = __float_as_int(r);
+    const float g = fmaf(x, clo, fmaf(x, chi, kMagic - r));  // to 2^-30
+    // 2^28 (2^g - 1) for |g| <= 2^-6 (the next term is below 2^-39), rounded to a
+    // whole number by adding 1.5 * 2^23
+    const float t = fmaf(g * 268435456.f, fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f),
+                         12582912.f);
+    return __float_as_uint(t) - (0x4b400000u - 0x10000000u);
   }
   // v and d of a logit of the window.
-  template <int DT>
   __device__ __forceinline__ uint32_t weight(float z, int& d) const {
-    const float x = z - shift;
-    const float p = __fmul_rn(x, chi);
-    const float r = __fadd_rn(p, kMagic);
-    d = gm + __float_as_int(kMagic) - __float_as_int(r);
-    float g = __fadd_rn(p, -__fadd_rn(r, -kMagic));  // exact
-    g = DT == 0 ? fmaf(x, clo, g) : g + fmaf(x, clo, fmaf(x, chi, -p));
-    // 2^g - 1 for |g| <= 2^-6 (the next term is below 2^-39)
-    const float t = __fmul_rn(g * 268435456.f, fmaf(g, fmaf(g, fmaf(g, 0.009618129f, 0.05550411f), 0.24022651f), 0.69314718f));
-    return 0x10000000u + static_cast<uint32_t>(__float2int_rn(t));
+    int at;
+    const uint32_t v = weight_at<true>(z, at);
+    d = gm + __float_as_int(kMagic) - at;
+    return v;
   }
   // A logit that every logit of bins <= d is at or above, with room for
   // rounding (side -1); that every logit at or above it has a bin < d (+1).
@@ -170,6 +176,7 @@ struct Decision {
 struct FilterShared {
   uint64_t bars[kRowWarps * kMaxRing];
   uint64_t tab[kGrid];
+  uint32_t tab32[kGrid];     // its upper halves, rounded
   float total[kBins];        // the row's histogram; then, in rank 0, bins of the list
   uint64_t Z;                // the row's weight
   // one value per CTA, pushed to every CTA (xmass, xband: per part)
@@ -199,7 +206,7 @@ static_assert(2 * kBins <= 4 * kCap && 2 * kRowThreads <= kBins, "arrays that sh
 // (two halves each); then the band's tokens that it collects, and in rank 0,
 // behind them, those of all CTAs.
 __host__ __device__ constexpr int work_bytes(int H) {
-  return H * 2 * kBins * 4 > 2 * kCap * 8 ? H * 2 * kBins * 4 : 2 * kCap * 8;
+  return H * 2 * kHist * 4 > 2 * kCap * 8 ? H * 2 * kHist * 4 : 2 * kCap * 8;
 }
 
 // The part of the set that the cut lies in: bins [lo, hi], by keys [kmin, kmax]
@@ -228,6 +235,7 @@ struct FilterRow {
   int sub;           // the part of the CTA's slice that this warp's segment belongs to
   float zc;
   int ic;
+  int off;    // the histograms' bin of the maximum
   int fbits;  // sums are in units of 2^-fbits, so that V weights stay below 2^62
 
   __device__ FilterRow(FilterShared& s, const RowSplit& sp, char* shared, const void* z)
@@ -235,11 +243,12 @@ struct FilterRow {
     work = reinterpret_cast<uint64_t*>(smem + row_bytes(sp.rvec, 0));
     sub = warp * sp.H / kRowWarps;
     sl.init(smem, S.bars, sp, z, rank, warp);
+    off = 0;
     fbits = min(44, 62 - (32 - __clz(V)));
   }
 
   __device__ __forceinline__ int shift_H() const { return H >> 1; }  // log2 of 1, 2, 4
-  __device__ uint32_t* hist(int part) const { return reinterpret_cast<uint32_t*>(work) + part * (2 * kBins); }
+  __device__ uint32_t* hist(int part) const { return reinterpret_cast<uint32_t*>(work) + part * (2 * kHist) + off; }
   __device__ uint64_t* own_list() const { return work; }
   __device__ uint64_t* list() const { return work + kCap; }
 
@@ -261,11 +270,15 @@ struct FilterRow {
     const int s = (d + kGrid - 1) / kGrid;
     return s > 0 ? (x + (1ull << (s - 1))) >> s : x;
   }
-  // (At least one unit: every kept token can be drawn.)
+  // A token's weight, good to 2^-32 of itself, in the same units: at least one,
+  // so that every kept token can be drawn.  (A list's and a part's tokens; the
+  // histograms' masses take the exact product.)
   __device__ __forceinline__ uint64_t weight(float z) const {
     int d;
-    const uint32_t v = sc.template weight<DT>(z, d);
-    return max(mass(v, d), uint64_t(1));
+    const uint32_t v = sc.weight(z, d);
+    const uint64_t x = static_cast<uint64_t>(v) * S.tab32[(-d) & (kGrid - 1)];
+    const int s = min(58 - fbits + ((d + kGrid - 1) >> 5), 62);
+    return max(((x >> s) + 1) >> 1, uint64_t(1));
   }
 
   // The cluster's barrier.
@@ -309,9 +322,70 @@ struct FilterRow {
     return x;
   }
 
+  // A logit's weight into this warp's histogram, if z >= cut and `also`: `base`,
+  // the shared address of the bin whose place has bits 0; places above `most`
+  // count as that one.  (Computed for every logit, only the additions under a
+  // predicate: as a branch the compiler guarded each logit's arithmetic.)
+  template <bool SHIFT>
+  __device__ __forceinline__ void add_mass(uint32_t base, int most, float z, float cut, bool also) const {
+    int at;
+    const uint32_t v = sc.template weight_at<SHIFT>(z, at);
+    const uint32_t bin = base - 4u * static_cast<uint32_t>(min(at, most));
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %6, 0;\n\tsetp.ge.and.f32 p, %1, %2, q;\n\t"
+        "@p red.shared.add.u32 [%0], %3;\n\t@p red.shared.add.u32 [%0 + %5], %4;\n\t}"
+        :: "r"(bin), "f"(z), "f"(cut), "r"(v >> 14), "r"(v & 0x3fffu), "n"(4 * kHist), "r"(static_cast<uint32_t>(also))
+        : "memory");
+  }
+  __device__ __forceinline__ int most() const { return sc.gm + __float_as_int(kMagic) + off; }
+  __device__ __forceinline__ uint32_t base() const {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(hist(sub))) +
+           4u * static_cast<uint32_t>(sc.gm + __float_as_int(kMagic));
+  }
+
+  // A guess at the row's maximum, the same in every CTA: over the first vectors
+  // of every warp's segment.  (cluster_wait has been called.)
+  __device__ float guess_max() {
+    float m = neg_inf();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (lane + 32 * u < sl.nv) m = vec_max<DT>(sl.fetch(lane + 32 * u), m);
+    m = block_max_nan(m, S.fscratch);
+    push_all(S.xexp, rank, C, m);
+    sync_all();
+    m = neg_inf();
+    for (int r = 0; r < C; ++r) m = max_nan(m, S.xexp[r]);
+    return m;
+  }
+
+  // The first pass over a row, from memory: the maximum, and on the way the
+  // masses by bins below a guessed one (`sc`, without a shift; the first kHead bins are for
+  // logits above it).  The guess holds if the maximum turns out to lie there.
+  __device__ float max_and_masses(float cut) {
+    constexpr int VW = Elem<DT>::VW;
+    using Vec = typename Elem<DT>::Vec;
+    const uint32_t to = base();
+    const int top = most();
+    float m = neg_inf();
+    sl.groups([&](const Vec(&x)[2], int) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        m = vec_max<DT>(x[u], m);
+        float z[VW];
+        Elem<DT>::unpack(x[u], z);
+#pragma unroll
+        for (int k = 0; k < VW; ++k)
+          add_mass<false>(to, top, z[k], cut, true);
+      }
+    }, true);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  }
+
   // Empty histograms and no tokens collected.  Ends with a barrier.
   __device__ void clear() {
-    for (int b = threadIdx.x; b < H * (kBins / 2); b += kRowThreads)
+    for (int b = threadIdx.x; b < H * (kHist / 2); b += kRowThreads)
       reinterpret_cast<uint4*>(work)[b] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x < kMaxH) {
       S.mass[threadIdx.x] = 0;
@@ -330,8 +404,9 @@ struct FilterRow {
   // The row's histogram into S.total on every CTA, as counts or (MASS) masses,
   // whose exact sum goes to S.Z.  Each CTA adds up a share of the bins over the
   // cluster's parts.  Barriers: the cluster's, twice.
+  // `last`: the last bin that counts.
   template <bool MASS>
-  __device__ void merge(int bins) {
+  __device__ void merge(int bins, int last = kBins) {
     sync_all();
     const int per = (bins + C - 1) / C, parts = C * H;
     const int b0 = rank * per, b1 = min(bins, b0 + per);
@@ -345,9 +420,9 @@ struct FilterRow {
         for (int q = 0; q < 8; ++q) {
           const int p = min(p0 + q, parts - 1);
           const uint32_t* h = peer(hist(p & (H - 1)), p >> shift_H());
-          const bool read = on && p0 + q < parts;
+          const bool read = on && d <= last && p0 + q < parts;
           x[q] = read ? h[d] : 0u;
-          y[q] = MASS && read ? h[kBins + d] : 0u;
+          y[q] = MASS && read ? h[kHist + d] : 0u;
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) v += MASS ? (static_cast<uint64_t>(x[q]) << 14) + y[q] : x[q];
@@ -449,7 +524,7 @@ struct FilterRow {
   __device__ void collect_bins(const Band& b) {
     constexpr int VW = Elem<DT>::VW, G = 2;
     using Vec = typename Elem<DT>::Vec;
-    uint64_t* raw = list();
+    uint32_t* raw = reinterpret_cast<uint32_t*>(list());
     int above = 0;
     sl.groups([&](const Vec(&x)[G], int j0) {
       unsigned zone = 0;  // a bit for each logit
@@ -466,12 +541,11 @@ struct FilterRow {
       }
       if (!zone) return;
       int pos = atomicAdd(&S.ncollect, __popc(zone));
-      while (zone) {  // (few: read again rather than kept in registers by number)
-        const int bit = __ffs(zone) - 1, j = j0 + 32 * (bit / VW);
+      const int i0 = sl.index(j0);
+      while (zone) {  // (few; their logits are read again below, all at a time)
+        const int bit = __ffs(zone) - 1;
         zone &= zone - 1;
-        if (pos < kCap)
-          raw[pos++] = (static_cast<uint64_t>(__float_as_uint(sl.at(j, bit % VW))) << 32) |
-                       static_cast<uint32_t>(sl.index(j) + bit % VW);
+        if (pos < kCap) raw[pos++] = i0 + 32 * VW * (bit / VW) + bit % VW;
       }
     });
     above = __reduce_add_sync(0xffffffffu, above);
@@ -480,8 +554,8 @@ struct FilterRow {
     __syncthreads();
     const int n = min(S.ncollect, kCap);
     for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float z = __uint_as_float(static_cast<uint32_t>(raw[i] >> 32));
-      const int idx = static_cast<int>(raw[i] & 0xffffffffu);
+      const int idx = static_cast<int>(raw[i]);
+      const float z = sl.logit(idx);
       if (!in_set(z, idx)) continue;
       const int pl = place(z, b);
       if (pl == 0) atomicAdd(&S.above, 1);
@@ -1140,11 +1214,30 @@ struct FilterRow {
     const int per = kRowWarps >> shift_H();  // segments of the part
     RowSlice<DT, false> piece =
         sl.piece(smem, S.bars, split, row, rank, (p & (H - 1)) * per + (warp >> shift_H()), warp & (H - 1), H);
-    uint64_t mine = 0;
-    piece.each([&](float z, int i) {
-      if (in_set(z, i)) mine += weight(z);
+    // sums of up to 32 blocks of the warp's piece, a lane's each
+    const int per_block = (piece.nv + 32 * kStage - 1) / (32 * kStage) * kStage;
+    uint64_t block = 0;
+    piece.groups([&](const typename Elem<DT>::Vec(&x)[2], int j) {
+      uint64_t sum = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float z[VW];
+        Elem<DT>::unpack(x[h], z);
+        const int i0 = piece.index(j + 32 * h);
+#pragma unroll
+        for (int q = 0; q < VW; ++q)
+          if (in_set(z[q], i0 + q)) sum += weight(z[q]);
+      }
+      sum = warp_sum_u(sum);
+      if (lane == (j - lane) / per_block) block += sum;
     });
-    mine = warp_sum_u(mine);
+    uint64_t inc = block;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint64_t mine = __shfl_sync(0xffffffffu, inc, 31);
     __syncthreads();
     if (lane == 0) S.scratch[warp] = mine;
     __syncthreads();
@@ -1155,10 +1248,13 @@ struct FilterRow {
       later |= w > warp && S.scratch[w] > 0;
     }
     if (mine == 0 || run > rem || (run + mine <= rem && later)) return;
-    // this warp's piece
+    // this warp's piece: the block, or else the last that holds kept tokens
+    const unsigned past = __ballot_sync(0xffffffffu, block > 0 && run + inc > rem);
+    const int at = past ? __ffs(past) - 1 : 31 - __clz(__ballot_sync(0xffffffffu, block > 0));
+    run += __shfl_sync(0xffffffffu, inc - block, at);
     int last = -1, found = -1;
     float lastz = 0.f, tz = 0.f;
-    for (int j0 = 0; j0 < piece.nv; j0 += 32) {
+    for (int j0 = at * per_block; j0 < min(piece.nv, (at + 1) * per_block); j0 += 32) {
       const int j = j0 + lane;
       const int i0 = piece.index(j);
       float z[VW];
@@ -1174,17 +1270,17 @@ struct FilterRow {
           lastz = z[q];
         }
       }
-      uint64_t inc = x;
+      uint64_t upto = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
-      const unsigned over = __ballot_sync(0xffffffffu, x > 0 && run + inc > rem);
+      const unsigned over = __ballot_sync(0xffffffffu, x > 0 && run + upto > rem);
       if (over) {
         const int who = __ffs(over) - 1;
         if (lane == who) {
-          uint64_t y = run + inc;
+          uint64_t y = run + upto;
 #pragma unroll
           for (int q = VW - 1; q >= 0; --q) {  // the first whose sum passes: from the end
             if (w[q] > 0 && y > rem) {
@@ -1198,7 +1294,7 @@ struct FilterRow {
         tz = __shfl_sync(0xffffffffu, tz, who);
         break;
       }
-      run += __shfl_sync(0xffffffffu, inc, 31);
+      run += __shfl_sync(0xffffffffu, upto, 31);
     }
     if (found < 0) {  // the piece's last kept token
       const int most = __reduce_max_sync(0xffffffffu, last);
@@ -1227,7 +1323,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
   FilterRow<DT, false> F(S, P.sp, smem, zrow);
   const int rank = F.rank, lane = F.lane, warp = F.warp;
   F.sl.load();
-  if (threadIdx.x < kGrid) S.tab[threadIdx.x] = P.tab.e[threadIdx.x];
+  if (threadIdx.x < kGrid) {
+    S.tab[threadIdx.x] = P.tab.e[threadIdx.x];
+    S.tab32[threadIdx.x] = static_cast<uint32_t>((P.tab.e[threadIdx.x] + 0x80000000u) >> 32);
+  }
   if (threadIdx.x == 0) S.bad = 0;
   if (threadIdx.x < kMaxH) S.mine[threadIdx.x] = 0;
   const float T = P.temp[b];
@@ -1247,11 +1346,25 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     tm = mp > 0.f ? static_cast<double>(Tc) * fmax(log(static_cast<double>(mp)), lnf) : tf;
   }
   __syncthreads();
-  float own[2];
-  const float wm = F.sl.warp_max(own);
+  cluster_wait();
+  // Streamed rows without top-k: masses and maximum in one pass.
+  bool guessed = P.sp.rvec < P.sp.gvec && bad == 0 && T > 0.f && (k == 0 || k >= V) && (tp < 1.f || u);
+  float own[2], wm;
+  if (guessed) {
+    F.sc.set_factor(Tc);
+    const float m0 = F.guess_max();
+    guessed = fabsf(m0) * F.sc.chi < 16000.f;  // (false for infinities and NaN)
+    if (guessed) {
+      F.sc.set_max(m0);
+      if (threadIdx.x == 0) S.zf = __double2float_ru(static_cast<double>(m0) + tf);
+      F.off = kHead;
+      F.clear();  // (a barrier)
+      wm = F.max_and_masses(S.zf);
+    }
+  }
+  if (!guessed) wm = F.sl.warp_max(own);
   if (!F.sl.landed && lane == 0) atomicOr(&S.bad, kTimeout);
   const float mc = block_max_nan(wm, S.fscratch);
-  cluster_wait();
   push_all(S.xmax, rank, C, mc);
   push_all(S.xbad, rank, C, S.bad);
   F.sync_all();
@@ -1292,13 +1405,20 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (P.status) P.status[row] = 0;
     }
   } else {
-    F.sc.set_factor<DT>(Tc);
+    F.sc.set_factor(Tc);
+    const int guess = F.sc.gm;
     F.sc.set_max(m);
+    if (guessed) {
+      F.off += guess - F.sc.gm;
+      guessed = F.off >= 0;
+      if (!guessed) F.off = 0;
+    }
     if (threadIdx.x == 0) {
       S.zf = __double2float_ru(static_cast<double>(m) + tf);
       S.zt = fmaxf(S.zf, __double2float_ru(static_cast<double>(m) + tm));
     }
-    F.clear();  // (a barrier)
+    if (guessed) __syncthreads();
+    else F.clear();  // (a barrier)
     const float zf = S.zf, zt = S.zt;
     F.zc = zf;
     F.ic = INT_MAX;
@@ -1356,24 +1476,20 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (use_p || u) {
         const float cut = F.zc;
         const bool whole = F.ic == INT_MAX;
-        uint32_t* hist = F.hist(F.sub);
-        auto add = [&](float z) {
-          int d;
-          const uint32_t v = F.sc.template weight<DT>(z, d);
-          atomicAdd(&hist[d], v >> 14);
-          atomicAdd(&hist[kBins + d], v & 0x3fffu);
-        };
-        if (whole) {
+        const uint32_t to = F.base();
+        const int top = F.most();
+        if (guessed) {
+        } else if (whole) {
           F.sl.each([&](float z, int) {
-            if (z >= cut) add(z);
+            F.template add_mass<true>(to, top, z, cut, true);
           });
         } else {
           F.sl.each([&](float z, int i) {
-            if (z >= cut && F.in_set(z, i)) add(z);
+            F.template add_mass<true>(to, top, z, cut, F.in_set(z, i));
           });
         }
         __syncthreads();
-        F.template merge<true>(kBins);
+        F.template merge<true>(kBins, F.sc.template bin<false>(zf));
         if (use_p) {
           goal = fraction(tp, S.Z) + 1;
           goal -= goal >> kSlack;
@@ -1397,7 +1513,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
         const int width = kRowThreads / P.sp.H;
         const uint32_t* hist = F.hist(F.sub);
         for (int d = threadIdx.x % width; d < min(band.lo, kBins); d += width) {
-          const uint64_t v = (static_cast<uint64_t>(hist[d]) << 14) + hist[kBins + d];
+          const uint64_t v = (static_cast<uint64_t>(hist[d]) << 14) + hist[kHist + d];
           if (v) x += max(F.mass(v, d), uint64_t(1));
         }
         x = warp_sum_u(x);

@@ -340,12 +340,12 @@ struct RowSlice {
     }
   }
 
-  // The q-th of n pieces of warp w's segment.
+  // The q-th of n pieces of warp w's segment, of whole stages.
   __device__ RowSlice piece(char* smem, uint64_t* barriers, const RowSplit& sp, const void* row, int rank, int w, int q,
                             int n) const {
     RowSlice s;
     s.init(smem, barriers, sp, row, rank, w);
-    const int per = (s.nv + n - 1) / n, at = min(q * per, s.nv);
+    const int per = ((s.nv + n - 1) / n + kStage - 1) / kStage * kStage, at = min(q * per, s.nv);
     s.data += at;
     s.rv = max(0, min(per, s.rv - at));
     s.src += static_cast<int64_t>(at) * 16;
@@ -398,6 +398,11 @@ struct RowSlice {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
+  }
+
+  // The row's logit of index i, from memory.
+  __device__ __forceinline__ float logit(int i) const {
+    return E::scalar(src - static_cast<int64_t>(base + v0 * E::VW) * E::ES, i);
   }
 
   // Logit k of vector j of the segment.
