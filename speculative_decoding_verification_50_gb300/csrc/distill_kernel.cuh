@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   cluster_arrive();  // waited for before the first remote write
   const char* zrow = reinterpret_cast<const char*>(P.z) + row * P.rs * E::ES;
   char* grow = reinterpret_cast<char*>(P.grad) + row * P.grs * E::ES;
-  RowSlice<DT, true> sl;
+  RowSlice<DT, true, false> sl;
   sl.init(smem, bars, P.sp, zrow, rank, warp);
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;

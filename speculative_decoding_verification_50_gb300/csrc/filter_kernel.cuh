@@ -225,7 +225,8 @@ enum CutKind { kByCount, kByMass, kGiven };
 template <int DT, bool CLAMP>
 struct FilterRow {
   FilterShared& S;
-  RowSlice<DT, false> sl;
+  using Slice = RowSlice<DT, false, CLAMP>;
+  Slice sl;
   const RowSplit& split;  // (of the launch's arguments: no registers)
   const int &C, &V, &H;
   Scale sc;
@@ -1212,7 +1213,7 @@ struct FilterRow {
   __device__ void draw(const void* row, int p, uint64_t rem, uint64_t W, int32_t* token, float* prob) {
     constexpr int VW = Elem<DT>::VW;
     const int per = kRowWarps >> shift_H();  // segments of the part
-    RowSlice<DT, false> piece =
+    Slice piece =
         sl.piece(smem, S.bars, split, row, rank, (p & (H - 1)) * per + (warp >> shift_H()), warp & (H - 1), H);
     // sums of up to 32 blocks of the warp's piece, a lane's each
     const int per_block = (piece.nv + 32 * kStage - 1) / (32 * kStage) * kStage;

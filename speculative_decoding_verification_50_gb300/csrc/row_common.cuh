@@ -139,7 +139,11 @@ struct RunningSum {
 // stages.  Sampling's longer passes and its histograms, which leave room for
 // three stages, go the other way: 2304 x 152064 fp32 1176 us with loads, 1369
 // with the ring; the 256 top logits of 2048 x 152064 bf16 250, 311.)
-template <int DT, bool RING>
+// AHEAD: streamed vectors are loaded two by two, the next two while f has two;
+// else four at a time.  (The 256 top logits of 2048 x 152064 bf16 235 us ahead,
+// 247 by four; sampling, whose passes have no registers to spare, 2304 x 152064
+// fp32 1035 us and 1022.)
+template <int DT, bool RING, bool AHEAD>
 struct RowSlice {
   using E = Elem<DT>;
   using Vec = typename E::Vec;
@@ -283,12 +287,31 @@ struct RowSlice {
   __device__ __forceinline__ void groups(Fn&& f, bool first = false) {
     if (!RING) {
       int j0 = rv;  // (a multiple of kStage, or the segment's end)
+      if (!AHEAD) {
 #pragma unroll 1
-      for (; j0 + 2 * kStage <= plain; j0 += 2 * kStage) {  // four loads under way
+        for (; j0 + 2 * kStage <= plain; j0 += 2 * kStage) {
+          const Vec* at = reinterpret_cast<const Vec*>(src) + j0 + lane;
+          const Vec x[2] = {at[0], at[32]}, y[2] = {at[64], at[96]};
+          f(x, j0 + lane);
+          f(y, j0 + lane + kStage);
+        }
+      } else if (j0 + kStage <= plain) {
         const Vec* at = reinterpret_cast<const Vec*>(src) + j0 + lane;
-        const Vec x[2] = {at[0], at[32]}, y[2] = {at[64], at[96]};
-        f(x, j0 + lane);
-        f(y, j0 + lane + kStage);
+        Vec x[2] = {at[0], at[32]}, y[2] = {x[0], x[1]};
+#pragma unroll 1
+        for (;;) {
+          const bool more = j0 + 2 * kStage <= plain;
+          if (more) y[0] = at[kStage], y[1] = at[kStage + 32];
+          f(x, j0 + lane);
+          j0 += kStage;
+          if (!more) break;
+          const bool again = j0 + 2 * kStage <= plain;
+          if (again) x[0] = at[2 * kStage], x[1] = at[2 * kStage + 32];
+          at += 2 * kStage;
+          f(y, j0 + lane);
+          j0 += kStage;
+          if (!again) break;
+        }
       }
 #pragma unroll 1
       for (; j0 < nv; j0 += kStage) {
