@@ -323,3 +323,49 @@ def test_many_rows(sv, dtype, V):
             assert int(o["kept"][b]) == keep.sum() and int(o["tokens"][b]) == tok
             assert abs(float(o["prob"][b]) - pr) <= PROB_RTOL * pr
             assert np.array_equal(f[b].float().cpu().numpy() > -np.inf, keep)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_maximum_where_no_guess_finds_it(sv, dtype):
+    """Many rows whose largest logits lie at the ends of the row: a little or far
+    above all others, alone, infinite, or of a size that is shifted first."""
+    V, B = 30016, 352
+    rng = np.random.default_rng(5)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.randn(B, V, generator=g, device="cuda") * 2
+    kind = torch.arange(B, device="cuda") % 11
+    for i, up in enumerate((1.0, 4.0, 5.5, 6.0, 20.0, 300.0)):
+        z[kind == i, -3] = 9.0 + up
+    z[kind == 6, : V - 8] = -float("inf")
+    z[kind == 7] = z[kind == 7] * 30000 - 4e5
+    z[kind == 8, -5] = float("nan")
+    z[kind == 9, -2] = float("inf")
+    z = z.to(dtype)  # kind 10: as drawn
+    T = rng.uniform(0.3, 1.5, B).astype(np.float32)
+    p = rng.uniform(0.5, 1.0, B).astype(np.float32)
+    p[::5] = 1.0
+    mp = rng.choice([0.0, 1e-3], B).astype(np.float32)
+    u = rng.uniform(0, 1, B).astype(np.float32)
+    dev = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    f = torch.empty_like(z)
+    o = sv.specv_sample(z, dev(T), dev(u), top_p=dev(p), min_p=dev(mp), filtered=f)
+    for a in range(0, B, 16):
+        s = slice(a, a + 16)
+        few = torch.empty_like(z[s])
+        q = sv.specv_sample(z[s], dev(T[s]), dev(u[s]), top_p=dev(p[s]), min_p=dev(mp[s]), filtered=few)
+        assert torch.equal(few, f[s]), a
+        for n in ("tokens", "kept", "row_status"):
+            assert torch.equal(q[n], o[n][s]), (a, n)
+        assert (q["prob"] - o["prob"][s]).abs().max() <= PROB_RTOL
+    bad = ((kind == 8) | (kind == 9)).cpu().numpy()
+    assert np.array_equal(o["row_status"].cpu().numpy() != 0, bad)
+    for b in list(range(0, 33)) + list(range(33, B, 29)):
+        if bad[b]:
+            assert int(o["tokens"][b]) == -1 and int(o["kept"][b]) == 0
+            continue
+        row = z[b].float().cpu().numpy().astype(np.float64)
+        keep, tok, pr, near = restate(row, T[b], 0, p[b], mp[b], u[b])
+        if not near:
+            assert int(o["kept"][b]) == keep.sum() and int(o["tokens"][b]) == tok, b
+            assert abs(float(o["prob"][b]) - pr) <= PROB_RTOL * pr
+            assert np.array_equal(f[b].float().cpu().numpy() > -np.inf, keep)
