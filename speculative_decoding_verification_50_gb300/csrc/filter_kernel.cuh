@@ -12,9 +12,11 @@
 // token), and a sum in plain fp32 moves the cut of a flat distribution in one
 // row of a hundred.  So a weight is 2^(-d/32) v 2^-28, d its bin and v a whole
 // number (good to 2^-29, random): the bins sum v exactly, in two halves of 14
-// bits (of up to 250,000 logits per CTA), and totals are 64-bit integers in units of 2^-fbits of the largest
-// weight.  (An SM does two fp64 operations a clock: a block's reductions in fp64
-// cost more than its passes over the row.)
+// bits (of up to 250,000 logits per part), and totals are 64-bit integers in
+// units of 2^-fbits of the largest weight.  (An SM does two fp64 operations a
+// clock: a block's reductions in fp64 cost more than its passes over the row.
+// One 64-bit shared atomic a logit takes 56 clocks a warp where the two of 32
+// bits take 6.6.)
 #pragma once
 
 #include "distill_kernel.cuh"  // block_max_nan
@@ -37,7 +39,8 @@ constexpr float kMagic = 393216.f;        // 1.5 * 2^18: adding it rounds to 1/3
 constexpr int kSlack = 36;
 // The threads' maxima bound the k-th largest logit where there are at least
 // this many of them per token wanted (their k-th is then exceeded by about
-// 1.15 k logits).
+// 1.15 k logits).  Against a histogram of every logit (us): the 256 largest of
+// 2048 x 152064 bf16 236, 366; of 64 rows 21, 27; 100 of 333 x 50257 fp32 47, 61.
 constexpr int kFewTop = 4;
 
 struct BinTable {
@@ -359,7 +362,8 @@ struct FilterRow {
     return m;
   }
 
-  // The first pass over a row, from memory: the maximum, and on the way the
+  // The first pass over a row, from memory (2304 x 152064 fp32 1117 us; with a
+  // pass for the maximum before that for the masses 1195): the maximum, and on the way the
   // masses by bins below a guessed one (`sc`, without a shift; the first kHead bins are for
   // logits above it).  The guess holds if the maximum turns out to lie there.
   __device__ float max_and_masses(float cut) {
@@ -870,7 +874,10 @@ struct FilterRow {
     return true;
   }
 
-  // Sorts n <= kCap tokens.
+  // Sorts n <= kCap tokens.  By counts or by bins (us): 32 tokens of 4 rows of
+  // 32000 12.7, 14.6.  By bins or, as where a bin is too full, by exchanges: the
+  // 256 largest of 2048 x 152064 bf16 236, 283; a draw from 2304 x 152064 fp32
+  // 1030, 1184.
   __device__ void sort(uint64_t* a, int n) {
     int P = 16;
     while (P < n) P <<= 1;
@@ -1026,7 +1033,8 @@ struct FilterRow {
       finish(nk, 0, 0.f, *u);
       return;
     }
-    // the draw: G threads add up the weights of lower index for each
+    // The draw: G threads add up the weights of lower index for each.  (In place
+    // of a part's sums and a pass over it: 50 tokens of a row of 32000 19 us, 25.)
     uint64_t* wt = reinterpret_cast<uint64_t*>(S.total);
 #pragma unroll
     for (int q = 0; q < per; ++q) {

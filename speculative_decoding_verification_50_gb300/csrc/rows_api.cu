@@ -30,7 +30,9 @@ constexpr size_t kDistillStatic = 2048;  // (at least what distill_kernel declar
 // The row's split over a cluster of C CTAs (a power of two) whose slices stay
 // in shared memory beside `extra` bytes per CTA.  C is the smallest for which
 // two CTAs fit an SM (one row's copies then run under the other's passes),
-// and more while rows are too few to fill the SMs.  False: V does not fit.
+// and more while rows are too few to fill the SMs (us, against that smallest C:
+// sampling 32 x 128256 bf16 under mixed rules 39.5, 41.4; 37 x 50257 35, 41).
+// False: V does not fit.
 bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& sp, size_t& smem) {
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
@@ -57,27 +59,22 @@ bool split_row(int64_t rows, int32_t V, int32_t dtype, size_t extra, RowSplit& s
 // L2 that rows being read again may take.
 constexpr int64_t kL2Rows = 96 << 20;
 
-// The split of rows that fill the SMs' slots (two CTAs each): as few CTAs per
-// row as leave the rows in flight to L2 (`again`: they are read again), since a
-// CTA's fixed costs and a cluster's waits then come less often per row; the row
-// is streamed again in each pass.  extra(svec): a CTA's bytes beside its rings.
-// False: few rows, or no fewer CTAs than sp has; those
-// are held whole.
-//   `whole_waves`: not where the last wave of CTAs would be nearly empty.
+// The split of rows that fill the SMs' slots (two CTAs each): few CTAs per row,
+// since a CTA's fixed costs and a cluster's waits then come less often; the row
+// is streamed again in each pass.  `again`: as few as leave the rows in flight to
+// L2; else as few as fill the slots.  extra(svec): a CTA's bytes beside its
+// rings.  False: few rows, or no fewer CTAs than sp has; those are held whole.
+//   `first_wave`: held too where a second wave of CTAs would be nearly empty.
 template <typename Extra>
-bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool whole_waves, bool ring, int max_c,
+bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool first_wave, bool ring, int max_c,
                   Extra&& extra, RowSplit& sp, size_t& smem) {
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
   const int64_t slots = 2LL * api_sm_count();
-  auto fits = [&](int C) {
-    const int64_t n = rows * C;
-    return (!again || slots / C * nvec * 16 <= kL2Rows) && 5 * n >= 4 * slots &&
-           (!whole_waves || n <= slots || 2 * n >= 7 * slots);
-  };
   int C = 1;
-  while (C < sp.C && !fits(C)) C *= 2;
+  while (C < sp.C && ((again && slots / C * nvec * 16 > kL2Rows) || 5 * rows * C < 4 * slots)) C *= 2;
   if (C > max_c || C >= sp.C) return false;
+  if (first_wave && rows * C > slots && 4 * rows * C < 5 * slots) return false;
   const int32_t svec = static_cast<int32_t>((nvec + C - 1) / C);
   const size_t work = extra(svec), room = kSmemSm / 2 - kSmemReserved;
   if (work > room) return false;
@@ -93,18 +90,23 @@ bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool whole
 }
 
 // The split for sampling (and, `top`, the top logits); four histograms per CTA
-// keep the part of a row small that a token is drawn from.
-// Measured (us; rows x V; C = 1, 2, held whole): sampling 576 x 152064 fp32 435,
-// 389, 667; 128 x 128256 bf16 91, 66, 79; 320 x 128256 bf16, where the second
-// wave is nearly empty, 190, 146, 114 (so `whole_waves`).  The 256 top logits of
-// 256 x 152064 bf16 42, 58, 70; of 64 rows 29, 25, 23; 100 of 333 x 50257 fp32
-// 58, 69, 78.
+// keep the part of a row small that a token is drawn from (2304 x 152064 fp32
+// in clusters of two: one 1760 us, two 1371, four 1179).
+// Measured (us; rows x V; C = 1, 2, held whole).  Sampling, whose first pass is
+// its longest, takes the smallest C although rows in flight may overflow L2:
+// 2304 x 152064 fp32 top-p 917, 1028, 2123; 320 rows 207, 243, 324; 1024 x 128256
+// bf16 mixed 250, 259, 338; but 320 rows of it, filtered, 132, 146, 115 (held in
+// clusters of four; hence first_wave).  Top logits leave rows to L2: the 256
+// largest of 1024 x 152064 fp32 254, 238, 419; of 2048 x 152064 bf16 236, 328, 429;
+// 100 of 333 x 50257 fp32 47, 60, 74.
 bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool top, RowSplit& sp, size_t& smem) {
   constexpr size_t fixed = sizeof(FilterShared);
   const int H = top ? 1 : kMaxH;
   if (!split_row(rows, V, dtype, fixed + work_bytes(1), sp, smem)) return false;
   const int max_c = V / H <= kMaxBinned ? kMaxParts / H : 0;
-  if (split_stream(rows, V, dtype, true, !top, false, max_c, [&](int32_t) { return fixed + work_bytes(H); }, sp, smem)) sp.H = H;
+  if (split_stream(rows, V, dtype, top, !top && sp.C <= 4, false, max_c, [&](int32_t) { return fixed + work_bytes(H); },
+                   sp, smem))
+    sp.H = H;
   smem += work_bytes(sp.H);
   return true;
 }
