@@ -1319,6 +1319,12 @@ struct FilterRow {
 };
 
 // One row per cluster: the cut, the token, the filtered logits.
+// Many rows are bound by issue slots and shared atomics: 2304 x 152064 fp32 top-p
+// 0.91 ms (1401 MB, 1.54 TB/s), of a row's time a third in the pass for the
+// masses (25 operations and two atomics a logit), a fifth in the band's
+// collection, the rest in the merge, the sorted list and the draw.  320 x 128256
+// bf16 filtered 118 us (164 MB).  Few rows are bound by the chain of these steps,
+// 1 to 3 us each: one row of 32000 with top-k 19 us, 32 x 128256 bf16 mixed 40.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __grid_constant__ FilterParams P) {
   using E = Elem<DT>;
@@ -1584,6 +1590,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 }
 
 // One row per cluster: the k largest logits, in order, and the log-sum-exp.
+// 256 of 2048 x 152064 bf16 234 us (623 MB, 2.7 TB/s): a row's collection and
+// sort follow its pass for maximum and sum, and the other CTA on the SM covers
+// only part of them.  32 of 4 x 32000 fp32 13 us, 100 of 333 x 50257 fp32 47.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid_constant__ TopParams P) {
   using E = Elem<DT>;

@@ -5,8 +5,8 @@
 // result).  A cluster of C CTAs takes one row.  Few rows: each CTA copies its
 // slice into shared memory once (one bulk copy per warp's segment) and every
 // pass reads it there.  Rows enough to fill the SMs: fewer CTAs per row (one or
-// two), and every pass streams the slice, the first from HBM and the others from
-// L2, so that the fixed costs of a CTA and the waits of a cluster come less
+// two), and every pass streams the slice, the first from HBM and the others mostly
+// from L2, so that the fixed costs of a CTA and the waits of a cluster come less
 // often per row.  CTAs exchange a few values through distributed shared memory
 // between cluster barriers.
 #pragma once
