@@ -207,6 +207,35 @@ struct RowSlice {
     return x.v;
   }
 
+  // Vectors j0 + lane and 32 further (-inf past nv), the whole warp.  Inside a
+  // row that starts past a 16-byte boundary each lane loads its aligned vector
+  // once and takes the bytes of the next from the lane above (608 x 152064 fp32
+  // top-p 504 -> 475 us, loss + gradient of 1024 x 128256 bf16 233 -> 216).
+  __device__ __forceinline__ void fetch_two(int j0, Vec (&x)[2]) const {
+    const int j = j0 + lane;
+    if (mis != 0 && v0 + j0 + base > 0 && j0 + kStage <= nv && (j0 + kStage) * E::VW + (16 - mis) / E::ES <= left) {
+      x[0] = shifted(j);
+      x[1] = shifted(j + 32);
+      return;
+    }
+    x[0] = j < nv ? fetch(j) : none();
+    x[1] = j + 32 < nv ? fetch(j + 32) : none();
+  }
+  __device__ __forceinline__ Vec shifted(int j) const {
+    const uint4* at = reinterpret_cast<const uint4*>(src + static_cast<int64_t>(j) * 16 - mis);
+    union {
+      uint4 u;
+      Vec v;
+    } a;
+    a.u = __ldcg(at);
+    uint4 n = a.u;
+    if (lane == 31) n = __ldcg(at + 1);
+    const uint4 up = make_uint4(__shfl_down_sync(0xffffffffu, a.u.x, 1), __shfl_down_sync(0xffffffffu, a.u.y, 1),
+                                __shfl_down_sync(0xffffffffu, a.u.z, 1), __shfl_down_sync(0xffffffffu, a.u.w, 1));
+    a.u = shift_bytes(a.u, lane == 31 ? n : up, mis);
+    return a.v;
+  }
+
   // Vector j < nv, held or not.
   __device__ __forceinline__ Vec vec(int j) const { return j < rv ? data[j] : fetch(j); }
 
@@ -315,9 +344,9 @@ struct RowSlice {
       }
 #pragma unroll 1
       for (; j0 < nv; j0 += kStage) {
-        const int j = j0 + lane;
-        const Vec x[2] = {j < nv ? fetch(j) : none(), j + 32 < nv ? fetch(j + 32) : none()};
-        f(x, j);
+        Vec x[2];
+        fetch_two(j0, x);
+        f(x, j0 + lane);
       }
     }
     if (first) ready();
@@ -357,9 +386,9 @@ struct RowSlice {
     }
 #pragma unroll 1
     for (; j0 < nv; j0 += kStage) {
-      const int j = j0 + lane;
-      const Vec x[2] = {j < nv ? fetch(j) : none(), j + 32 < nv ? fetch(j + 32) : none()};
-      f(x, j);
+      Vec x[2];
+      fetch_two(j0, x);
+      f(x, j0 + lane);
     }
   }
 
