@@ -269,3 +269,10 @@ def test_many_rows(sv, dtype, V, tail):
     some = torch.arange(0, N, 23, device="cuda")
     check(sv, z[some].contiguous(), ids[some].contiguous(), val[some].contiguous(),
           None if lse is None else lse[some].contiguous(), 1.0, w[some].contiguous(), tail)
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 769999), (torch.bfloat16, 1539999)])
+def test_widest_rows(sv, dtype, V):
+    z, ids, val, teacher = make(V, 2, V, 1024, dtype)
+    lse = torch.logsumexp(teacher.double(), 1).float().cuda()
+    check(sv, z, ids, val, lse, 1.0, None, True)

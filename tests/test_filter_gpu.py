@@ -369,3 +369,27 @@ def test_maximum_where_no_guess_finds_it(sv, dtype):
             assert int(o["kept"][b]) == keep.sum() and int(o["tokens"][b]) == tok, b
             assert abs(float(o["prob"][b]) - pr) <= PROB_RTOL * pr
             assert np.array_equal(f[b].float().cpu().numpy() > -np.inf, keep)
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 769999), (torch.bfloat16, 1539999)], ids=["fp32", "bf16"])
+def test_widest_rows(sv, dtype, V):
+    """The widest rows that are taken, held by sixteen CTAs each."""
+    rng = np.random.default_rng(12)
+    z = rng.normal(0, 2, (3, V)).astype(np.float32)
+    check(sv, z, [1.0, 0.7, 0.0], [0, 900, 0], [0.9, 0.95, 1.0], [0.0, 0.001, 0.0], [0.37, 0.62, 0.5], dtype=dtype)
+
+
+def test_widest_rows_streamed(sv):
+    """Wide rows enough to fill the GPU: more of them in flight than L2 holds."""
+    V, B = 600001, 260
+    g = torch.Generator(device="cuda").manual_seed(13)
+    z = torch.randn(B, V, generator=g, device="cuda") * 2
+    T = torch.full((B,), 0.9, device="cuda")
+    u, p = torch.rand(B, generator=g, device="cuda"), torch.rand(B, generator=g, device="cuda") * 0.4 + 0.6
+    o = sv.specv_sample(z, T, u, top_p=p)
+    for a in range(0, B, 26):
+        s = slice(a, a + 3)
+        q = sv.specv_sample(z[s], T[s], u[s], top_p=p[s])
+        for n in ("tokens", "kept", "row_status"):
+            assert torch.equal(q[n], o[n][s]), (a, n)
+        assert (q["prob"] - o["prob"][s]).abs().max() <= PROB_RTOL

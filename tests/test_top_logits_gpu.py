@@ -91,3 +91,9 @@ def test_many_rows(sv, dtype, V, k):
         assert torch.equal(q["ids"], o["ids"][a:a + 8]) and torch.equal(q["values"], o["values"][a:a + 8]), a
         assert ((q["lse"] - o["lse"][a:a + 8]).abs() <= 2.0 ** -20 * (1 + q["lse"].abs())).all()
     check(sv, z[::40].contiguous(), k)
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 769999), (torch.bfloat16, 1539999)])
+def test_widest_rows(sv, dtype, V):
+    g = torch.Generator().manual_seed(V)
+    check(sv, (torch.randn(2, V, generator=g) * 2).to(dtype).cuda(), 700)
