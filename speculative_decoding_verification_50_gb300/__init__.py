@@ -488,12 +488,16 @@ def specv_check_hit(keys, accept_len, out_tokens, *, hit=None, stream=None):
     return hit
 
 
+def _on_gpu(t) -> bool:
+    return t.is_cuda
+
+
 def _of(t, shape, dtype, what):
-    """t's pointer after a check of its type, shape and layout (None: optional)."""
+    """t's pointer after a check of its type, shape, layout and place (None: optional)."""
     if t is None:
         return None
-    assert t.shape == shape and t.dtype is dtype and t.is_contiguous(), (
-        f"{what}: {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {tuple(shape)}")
+    assert t.shape == shape and t.dtype is dtype and t.is_contiguous() and _on_gpu(t), (
+        f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous {dtype} {tuple(shape)} on a GPU")
     return t.data_ptr()
 
 
@@ -507,7 +511,14 @@ def _raw_stream(stream, device):
 
 
 def _cuda(t, what):
-    assert t.is_cuda and t.stride(-1) == 1, f"{what} must be a CUDA tensor with a contiguous last dimension"
+    assert _on_gpu(t) and (t.stride(-1) == 1 or t.shape[-1] == 1), (
+        f"{what} must be a CUDA tensor with a contiguous last dimension")
+
+
+def _stride(t, dim, width):
+    """t's stride along dim; `width`, the least that is taken, where dim has one
+    entry (whose stride means nothing)."""
+    return t.stride(dim) if t.shape[dim] > 1 else width
 
 
 def _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, prob, kept, filtered,
@@ -531,16 +542,13 @@ def _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, pro
     out["row_status"] = row_status = (torch.empty(lead, dtype=i32, device=dev) if row_status is None
                                       else row_status)
     _cuda(logits, "logits")
-    st = logits.stride()
-    rs = max(st[-2], V)
-    bs = max(st[0], V) if flat else st[0]
+    bs, rs = _stride(logits, 0, V), V if flat else _stride(logits, 1, V)
     fptr, fbs, frs = None, 0, 0
     if filtered is not None:
         assert filtered.shape == shape and filtered.dtype is logits.dtype, "filtered must be like logits"
         _cuda(filtered, "filtered")
-        fst = filtered.stride()
-        fptr, frs = filtered.data_ptr(), max(fst[-2], V)
-        fbs = max(fst[0], V) if flat else fst[0]
+        fptr = filtered.data_ptr()
+        fbs, frs = _stride(filtered, 0, V), V if flat else _stride(filtered, 1, V)
         out["filtered"] = filtered
     args = SampleArgs(B, R, V, code, logits.data_ptr(), bs, rs, T, k, p, m, u,
                       _of(tokens, lead, i32, "tokens"), _of(prob, lead, f32, "prob"),
@@ -599,7 +607,7 @@ def specv_top_logits(logits, k: int, *, temperature: float = 1.0, ids=None, valu
     lse = torch.empty(B, dtype=f32, device=dev) if lse is None else lse
     row_status = torch.empty(B, dtype=i32, device=dev) if row_status is None else row_status
     _cuda(logits, "logits")
-    args = TopArgs(B, V, int(k), code, logits.data_ptr(), max(logits.stride(0), V),
+    args = TopArgs(B, V, int(k), code, logits.data_ptr(), _stride(logits, 0, V),
                    float(temperature), _of(ids, (B, rows), i32, "ids"),
                    _of(values, (B, rows), f32, "values"), _of(lse, (B,), f32, "lse"),
                    _of(row_status, (B,), i32, "row_status"))
@@ -615,20 +623,21 @@ def _distill_args(logits, ids, values, teacher_lse, weights, temperature, tail, 
     K = ids.shape[1]
     f32 = torch.float32
     assert ids.shape == values.shape == (N, K) and ids.dtype == torch.int32 and values.dtype == f32
-    assert ids.stride(-1) == 1 and values.stride(-1) == 1
-    ts = max(ids.stride(0), K)
+    _cuda(ids, "teacher_ids")
+    _cuda(values, "teacher_logits")
+    ts = _stride(ids, 0, K)
     assert N <= 1 or ids.stride(0) == values.stride(0), "teacher_ids and teacher_logits share one row stride"
     _cuda(logits, "logits")
     if grad is not None:
         assert grad.shape == logits.shape and grad.dtype == logits.dtype, "grad must be like logits"
         _cuda(grad, "grad")
-    return DistillArgs(N, V, K, code, logits.data_ptr(), max(logits.stride(0), V),
+    return DistillArgs(N, V, K, code, logits.data_ptr(), _stride(logits, 0, V),
                        ids.data_ptr(), values.data_ptr(), ts,
                        _of(teacher_lse, (N,), f32, "teacher_lse"),
                        _of(weights, (N,), f32, "weights"), float(temperature),
                        SPECV_DISTILL_TAIL if tail else 0, None, None, None,
                        None if grad is None else grad.data_ptr(),
-                       0 if grad is None else max(grad.stride(0), V), None)
+                       0 if grad is None else _stride(grad, 0, V), None)
 
 
 def specv_distill(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temperature: float = 1.0,

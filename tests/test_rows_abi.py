@@ -123,3 +123,35 @@ def test_python_checks_of_types_and_shapes():
         sv.specv_filter_logits(z.half(), one)
     with pytest.raises(AssertionError):
         sv.specv_distill(z, torch.zeros(2, 3), torch.zeros(2, 3))
+
+
+def test_rows_that_overlap_are_refused(lib, monkeypatch):
+    """Broadcast and overlapping rows keep their strides, which are refused (no
+    launch comes of any of these calls)."""
+    torch = pytest.importorskip("torch")
+    for name in ("_on_gpu", "_cuda"):
+        if hasattr(sv, name):
+            monkeypatch.setattr(sv, name, lambda *a: True)
+    monkeypatch.setattr(sv, "_raw_stream", lambda *a: None)
+    B, V, K = 3, 64, 8
+    one, two = torch.zeros(1, V).expand(B, V), torch.zeros(B * V).as_strided((B, V), (V // 2, 1))
+    good = torch.zeros(B, V)
+    T, u = torch.ones(B), torch.full((B,), 0.5)
+    ids, val = torch.zeros(B, K, dtype=torch.int32), torch.zeros(B, K)
+    few = torch.zeros(1, K, dtype=torch.int32).expand(B, K), torch.zeros(1, K).expand(B, K)
+    stats = torch.zeros(B, 4)
+    calls = [lambda z=z, f=f: f(z) for z in (one, two) for f in (
+        lambda z: sv.specv_sample(z, T, u),
+        lambda z: sv.specv_sample(z[:, None], T, u[:, None]),
+        lambda z: sv.specv_filter_logits(z, T),
+        lambda z: sv.specv_filter_logits(good, T, filtered=z),
+        lambda z: sv.specv_sample(z[None], T[:1], u[None]),
+        lambda z: sv.specv_top_logits(z, 4),
+        lambda z: sv.specv_distill(z, ids, val),
+        lambda z: sv.specv_distill(good, ids, val, grad=z),
+        lambda z: sv.specv_distill_backward(z, ids, val, stats))]
+    calls.append(lambda: sv.specv_distill(good, *few))
+    for i, call in enumerate(calls):
+        with pytest.raises(sv.SpecvError) as e:
+            call()
+        assert e.value.status == INV, (i, str(e.value))
