@@ -284,6 +284,8 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   const size_t bits = distill_bytes((a->V + vw - 1) / vw, vw, a->K);
   if (!split_row(a->N, a->V, a->dtype, kDistillStatic + std::min<size_t>(bits, 16384 + static_cast<size_t>(a->K) * 20), p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
+  // (With a gradient the rows are read again: left to L2 1024 x 152064 fp32 take 287
+  // us, by one CTA each 315; 300 rows 92, 109.)
   split_stream(a->N, a->V, a->dtype, a->grad != nullptr, false, true, kMaxCluster,
                [&](int32_t svec) { return kDistillStatic + distill_bytes(svec, vw, a->K); }, p.sp, smem);
   smem += distill_bytes(p.sp.svec, vw, a->K);
