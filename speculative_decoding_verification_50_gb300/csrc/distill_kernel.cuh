@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
   __syncthreads();
   for (int j = warp; j < K; j += kRowWarps) {
     const int id = ids[j];
-    if (id < i0 || id >= i1) continue;
+    if (id < max(i0, 0) || id >= i1) continue;  // (i0 lies before a row that starts inside a vector; absent: -1)
     bool first;
     const float ps = same_id(ids, pj, K, j, lane, first);
     if (lane == 0 && first) {

@@ -1,0 +1,83 @@
+"""The distillation loss where a row ends, begins or is all but empty: every
+element of the gradients against the definition in 64 bits.
+
+Tolerances.  A weight 2^x is taken at an argument rounded twice (2^-24 of |x|
+each, |x| <= 64 in these inputs: 5.3e-6 of the weight) by a function good to
+2^-22, in a quotient of sums good to a few 2^-24: REL = 2^-17 of the value.
+Where the loss has no tail, a token outside the list has the gradient m q, a
+product: REL of its own value.  At a listed id the gradient is a difference:
+REL of the row's largest.  Rounding to the logits' type adds eps / 2.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from tests._rows64 import distill64  # noqa: E402
+
+REL = 2.0 ** -17
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_verification_50_gb300 import _build
+    _build.build()
+    import speculative_decoding_verification_50_gb300 as m
+    m.load_library()
+    return m
+
+
+def both(sv, z, ids, val, grads=(None, None), lse=None, T=1.0, w=None, tail=False):
+    """Loss and the two gradients: of the one call, and from its statistics."""
+    kw = dict(teacher_lse=lse, temperature=T, weights=w, tail=tail)
+    o = sv.specv_distill(z, ids, val, with_grad=True, grad=grads[0], **kw)
+    back = sv.specv_distill_backward(z, ids, val, o["stats"], grad=grads[1], **kw)
+    assert (o["row_status"] == 0).all()
+    return o["loss"], o["grad"], back
+
+
+def close(got, want, listed, dtype, tail):
+    """Every element; `want` fp64."""
+    top = want.abs().amax(1, keepdim=True)
+    own = want.abs()
+    room = REL * torch.where(listed | torch.tensor(tail, device=want.device), top, own)
+    room = room + torch.finfo(dtype).eps / 2 * own + torch.finfo(dtype).tiny
+    off = (got.double() - want).abs()
+    assert (off <= room).all(), (off - room).argmax()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [37, 4099, 50257, 65535])
+@pytest.mark.parametrize("off", [0, 1, 3])
+def test_absent_entries_of_unaligned_rows(sv, V, off, dtype):
+    """Lists with absent entries, rows at no 16-byte boundary: nothing is written
+    beside a row, and the rows' ends are their own."""
+    g = torch.Generator(device="cuda").manual_seed(V + off)
+    N, K = 24, 20
+    wide = V + off + 2
+    z = torch.zeros(N, wide, dtype=dtype, device="cuda")[:, off:off + V]
+    z.copy_(torch.randn(N, V, generator=g, device="cuda") * 2)
+    teacher = z.float() + torch.randn(N, V, generator=g, device="cuda")
+    val, ids = teacher.topk(K, dim=1)
+    length = torch.randint(0, K + 1, (N, 1), generator=g, device="cuda")
+    length[0], length[1], length[2] = 0, 1, K
+    gaps = torch.rand(N, K, generator=g, device="cuda") < 0.2
+    ids = torch.where((torch.arange(K, device="cuda") < length) & ~gaps, ids, -1).int()
+    ids[3, 0], ids[4, 1] = 0, V - 1  # the ends themselves
+    ids[3, 1:], ids[4, 2:], ids[4, 0] = -1, -1, -1
+    _, want, _, listed = distill64(z, ids, val)
+    bufs = [torch.full((N, wide), 9.0, dtype=dtype, device="cuda") for _ in range(2)]
+    _, fused, back = both(sv, z, ids, val, [b[:, off:off + V] for b in bufs])
+    for b, got in zip(bufs, (fused, back)):
+        assert (b[:, :off] == 9).all() and (b[:, off + V:] == 9).all()
+        close(got, want, listed, dtype, False)
+    # rows without a gap between them: the end of each is the next one's neighbour
+    zc = z.contiguous()
+    _, fused, back = both(sv, zc, ids, val)
+    for got in (fused, back):
+        close(got, want, listed, dtype, False)
+    again = sv.specv_distill_backward(zc, ids, val, sv.specv_distill(zc, ids, val)["stats"])
+    assert torch.equal(again, back)
