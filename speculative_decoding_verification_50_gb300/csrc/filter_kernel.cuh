@@ -365,7 +365,8 @@ struct FilterRow {
   // The first pass over a row, from memory (2304 x 152064 fp32 1117 us; with a
   // pass for the maximum before that for the masses 1195): the maximum, and on the way the
   // masses by bins below a guessed one (`sc`, without a shift; the first kHead bins are for
-  // logits above it).  The guess holds if the maximum turns out to lie there.
+  // logits above it).  The guess holds if the maximum turns out to lie there, on the same
+  // scale.
   __device__ float max_and_masses(float cut) {
     constexpr int VW = Elem<DT>::VW;
     using Vec = typename Elem<DT>::Vec;
@@ -1424,8 +1425,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     const int guess = F.sc.gm;
     F.sc.set_max(m);
     if (guessed) {
+      // (A maximum that is shifted first lies on another grid: no place of it is
+      // comparable with the guess.)
       F.off += guess - F.sc.gm;
-      guessed = F.off >= 0;
+      guessed = F.sc.shift == 0.f && F.off >= 0 && F.off <= kHead;
       if (!guessed) F.off = 0;
     }
     if (threadIdx.x == 0) {

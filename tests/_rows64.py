@@ -39,3 +39,44 @@ def distill64(z, ids, t, lse=None, T=1.0, w=None, tail=False):
     none = w == 0
     return (torch.where(none, 0.0, w * loss), torch.where(none[:, None], 0.0, w[:, None] * grad / T),
             torch.where(none, 0.0, w.abs() * scale), listed)
+
+
+def sample64(z, T, k, p, mp, u, near_by=1e-9):
+    """Kept mask [B, V], token, prob and whether a cut or the draw lies within
+    near_by of a border (equality apart), of rows z under rules given as
+    sequences; each kept token adds the 2^-44 to which its weight is held."""
+    dev = z.device
+    f = lambda x: torch.as_tensor(x, dtype=torch.float32).to(dev).double().view(-1, 1)  # noqa: E731
+    T, p, mp, u = f(T), f(p), f(mp), f(u)
+    k = torch.as_tensor(k, dtype=torch.int64).to(dev).view(-1, 1)
+    greedy = T == 0
+    T = torch.where(greedy, 1.0, T)
+    z = z.double()
+    V = z.shape[1]
+    zs, order = torch.sort(z, dim=1, descending=True, stable=True)
+    top = zs[:, :1]
+    live = zs >= top - T * 48 * math.log(2.0)
+    cum = torch.where(live, torch.exp((zs - top) / T), 0.0).cumsum(1)
+    n = live.sum(1, keepdim=True)
+    n_k = torch.where(k > 0, torch.minimum(k, n), n)
+    inside = torch.arange(V, device=dev) < n_k
+    goal = p * cum.gather(1, n_k - 1)
+    n_p = torch.minimum((inside & (cum < goal * (1 - 1e-13))).sum(1, keepdim=True) + 1, n_k)
+    n_p = torch.where(p < 1, n_p, n_k)
+    gap = (cum - goal).abs()
+    by = near_by * goal + n_k * 2.0 ** -44
+    near = ((gap > 1e-12 * goal) & (gap < by) & inside & (p < 1)).any(1)
+    n_m = (zs >= top + T * torch.log(mp.clamp_min(2.0 ** -48))).sum(1, keepdim=True)
+    n = torch.where(greedy, 1, torch.minimum(n_p, n_m).clamp_min(1))
+    keep = torch.zeros(z.shape, dtype=torch.bool, device=dev)
+    keep.scatter_(1, order, torch.arange(V, device=dev) < n)
+    w = torch.where(keep, torch.exp((z - top) / T), 0.0)
+    run = w.cumsum(1)
+    W = run[:, -1:]
+    t = u * W
+    last = torch.where(keep, torch.arange(V, device=dev), 0).amax(1, keepdim=True)
+    token = torch.minimum((run <= t * (1 + 1e-13)).sum(1, keepdim=True), last)
+    gap = (run - t).abs()
+    near |= ((gap > 1e-12 * W) & (gap < near_by * W + n * 2.0 ** -44) & keep).any(1)
+    near &= ~greedy[:, 0]
+    return keep, token[:, 0].int(), (w.gather(1, token) / W)[:, 0], near

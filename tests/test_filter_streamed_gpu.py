@@ -1,0 +1,127 @@
+"""Sampling over rows enough to be streamed, whose first pass adds up masses
+below a guessed maximum: every row against the definition in 64 bits.
+
+Whole numbers are equal unless the definition itself finds a cut or a draw
+next to a border (1e-9 of the weight, and 2^-44 per kept token, to which the
+kernel holds a weight).  prob: one rounding to fp32, 2^-24 of its value, and as
+much again for the sums and weights.
+
+The rows: V so that one CTA holds only a part of its row, and one and a half
+times the 2 CTAs per SM that run at once.
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from tests._rows64 import sample64  # noqa: E402
+
+PROB_RTOL = 2.0 ** -23
+SIZES = [(torch.float32, 30016), (torch.float32, 30011), (torch.bfloat16, 60032), (torch.bfloat16, 60005)]
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_verification_50_gb300 import _build
+    _build.build()
+    import speculative_decoding_verification_50_gb300 as m
+    m.load_library()
+    return m
+
+
+def many():
+    return 3 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def check(sv, z, T, k=None, p=None, mp=None, u=None, max_near=0.05, good=None):
+    B = z.shape[0]
+    dev = lambda x, t: None if x is None else torch.as_tensor(np.asarray(x), dtype=t).cuda()  # noqa: E731
+    T, k, p, mp = dev(T, torch.float32), dev(k, torch.int32), dev(p, torch.float32), dev(mp, torch.float32)
+    u = dev(u, torch.float32)
+    rules = dict(top_k=k, top_p=p, min_p=mp)
+    fill = dict(tokens=torch.full((B,), -7, dtype=torch.int32).cuda(), prob=torch.full((B,), -7.0).cuda())
+    filt = torch.full_like(z, 5.0)
+    o = sv.specv_sample(z, T, u, filtered=filt, **rules, **fill)
+    f = sv.specv_filter_logits(z, T, **rules)
+    alone = sv.specv_sample(z, T, u, **rules)
+    assert torch.equal(f["filtered"], filt) and torch.equal(f["kept"], o["kept"])
+    assert all(torch.equal(alone[n], o[n]) for n in ("tokens", "prob", "kept", "row_status"))
+    good = torch.ones(B, dtype=torch.bool).cuda() if good is None else good
+    bad = ~good
+    assert torch.equal(o["row_status"] != 0, bad)
+    assert (o["tokens"][bad] == -1).all() and (o["kept"][bad] == 0).all() and torch.isneginf(filt[bad]).all()
+    zero = lambda x, off: torch.full((B,), off).cuda() if x is None else x  # noqa: E731
+    keep, tok, pr, near = sample64(torch.where(bad[:, None], 0.0, z), T, zero(k, 0), zero(p, 1.0), zero(mp, 0.0), u)
+    assert near[good].sum() <= max(1, max_near * B)
+    ok = good & ~near
+    assert torch.equal(o["kept"][ok].long(), keep[ok].sum(1))
+    assert torch.equal(filt[ok], torch.where(keep, z, float("-inf"))[ok])
+    assert torch.equal(o["tokens"][ok], tok[ok])
+    assert ((o["prob"].double() - pr).abs() <= PROB_RTOL * pr)[ok].all()
+
+
+@pytest.mark.parametrize("dtype,V", SIZES)
+@pytest.mark.parametrize("how", ["top_p", "plain", "min_p", "both"])
+def test_low_temperatures(sv, dtype, V, how):
+    """The guess below the size from which logits are shifted before they are
+    scaled, the maximum above it, below it, or both above; of either sign."""
+    B = many()
+    rng = np.random.default_rng(V)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    T = rng.choice([1e-4, 3e-4, 1e-3, 3e-3, 1e-2, 0.1], B).astype(np.float32)
+    scale = torch.from_numpy(rng.choice([0.001, 0.1, 2.0], B)).cuda()[:, None]
+    shift = torch.from_numpy(rng.choice([-200.0, -9.0, -0.01, 0.0, 0.01, 8.0, 90.0], B)).cuda()[:, None]
+    z = torch.randn(B, V, generator=g, device="cuda", dtype=torch.float64) * scale + shift
+    # the largest logits, where no guess looks: as far apart as a few tens of T
+    top = z.amax(1, keepdim=True) + torch.from_numpy(rng.choice([0.0, 1e-3, 0.03, 0.5, 3.0, 11.0, 150.0], B)).cuda()[:, None]
+    room = torch.from_numpy(T.astype(np.float64)).cuda()[:, None]
+    z[:, -200:-1] = top - room * 40 * torch.rand(B, 199, generator=g, device="cuda", dtype=torch.float64)
+    z = z.to(dtype)
+    p = rng.uniform(0.3, 0.999, B) if how in ("top_p", "both") else None
+    mp = rng.choice([0.0, 1e-6, 0.01, 0.3], B) if how in ("min_p", "both") else None
+    check(sv, z, T, None, p, mp, rng.uniform(0, 1, B))
+
+
+@pytest.mark.parametrize("dtype,V", SIZES)
+def test_maximum_where_no_guess_finds_it(sv, dtype, V):
+    """The largest logits at the ends of rows: a little or far above all others,
+    alone, infinite, not a number, or of a size that is shifted first."""
+    B = many()
+    rng = np.random.default_rng(V + 1)
+    g = torch.Generator(device="cuda").manual_seed(V + 1)
+    z = torch.randn(B, V, generator=g, device="cuda") * 2
+    kind = torch.arange(B, device="cuda") % 13
+    for i, up in enumerate((0.5, 1.0, 4.0, 5.5, 6.0, 20.0, 300.0)):
+        z[kind == i, -3] = 9.0 + up
+    z[kind == 7, : V - 8] = -float("inf")
+    z[kind == 8] = z[kind == 8] * 30000 - 4e5
+    z[kind == 9, -5] = float("nan")
+    z[kind == 10, -2] = float("inf")
+    z[kind == 11, : V // 2] = torch.finfo(torch.float32).min
+    z = z.to(dtype)  # kind 12: as drawn
+    if dtype is torch.bfloat16:  # (the lowest value that bf16 has)
+        z[kind == 11, : V // 2] = torch.finfo(torch.bfloat16).min
+    T = rng.uniform(0.3, 1.5, B).astype(np.float32)
+    T[::17] = 0.0
+    p = rng.uniform(0.5, 1.0, B).astype(np.float32)
+    p[::5] = 1.0
+    check(sv, z, T, None, p, rng.choice([0.0, 1e-3], B), rng.uniform(0, 1, B), good=(kind != 9) & (kind != 10))
+
+
+@pytest.mark.parametrize("dtype,V", SIZES)
+def test_rules(sv, dtype, V):
+    """Every rule of its row's own, ties among the logits."""
+    B = many()
+    rng = np.random.default_rng(V + 2)
+    g = torch.Generator(device="cuda").manual_seed(V + 2)
+    z = torch.randn(B, V, generator=g, device="cuda") * (torch.rand(B, 1, generator=g, device="cuda") * 3 + 0.3)
+    z[::7] = (z[::7] * 4).round() / 4
+    z[3::50] = -1.25
+    z = z.to(dtype)
+    check(sv, z, rng.choice([0.0, 0.3, 0.7, 1.0, 1.7], B), rng.choice([0, 0, 1, 5, 50, 1500, V // 2, V, V + 3], B),
+          rng.choice([1.0, 1.0, 0.0, 0.1, 0.5, 0.9, 0.99], B), rng.choice([0.0, 0.0, 0.001, 0.1, 0.5, 1.0], B),
+          rng.integers(0, 1 << 24, B) * 2.0 ** -24)

@@ -5,8 +5,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests._rows64 import distill64  # noqa: E402
+from tests._rows64 import distill64, sample64  # noqa: E402
 from tests.test_distill_gpu import formula  # noqa: E402
+from tests.test_filter_gpu import restate, rules_of  # noqa: E402
 
 
 @pytest.mark.parametrize("how", ["renorm", "lse", "tail"])
@@ -35,3 +36,21 @@ def test_distillation(how, T):
         assert np.abs(grad[b].numpy() - dz).max() <= 1e-12, b
         assert scale[b] == s or np.isinf(want) or abs(float(scale[b]) - s) <= 1e-12 * (1 + s)
         assert set(np.flatnonzero(listed[b].numpy())) == {int(i) for i in ids[b] if i >= 0}
+
+
+@pytest.mark.parametrize("V", [1, 9, 400])
+def test_sampling(V):
+    rng = np.random.default_rng(V)
+    B = 200
+    z = rng.normal(0, 3, (B, V)).astype(np.float32)
+    z[::5] = np.round(z[::5])
+    z[1::7, 1:] = -np.inf
+    rules = rules_of(rng, B, V)
+    keep, token, prob, near = sample64(torch.from_numpy(z), *rules)
+    for b in range(B):
+        mask, tok, pr, close = restate(z[b].astype(np.float64), *(x[b] for x in rules))
+        assert close <= bool(near[b])  # (here a border is a little wider)
+        if not near[b]:
+            assert np.array_equal(keep[b].numpy(), mask) and int(token[b]) == tok
+            assert abs(float(prob[b]) - pr) <= 1e-12 * pr
+    assert near.sum() <= 4
