@@ -6,7 +6,7 @@
 //   D = sum_j p_j (log p_j - log q(id_j))  [+ r (log r - log(1 - s)), r = 1 - m]
 //   T dD/dz_v = alpha q_v                  v not listed
 //             = beta q_v - sum_{id_j=v} p_j  v listed
-//   alpha = m [- r s / (1 - s)],  beta = alpha [+ r / (1 - s)]
+//   alpha = m [- r s / (1 - s)],  beta = m [+ r]
 // 1 - s is summed over the logits that are not listed, and beta q - p is taken
 // as p (exp(log(beta q / p)) - 1), so neither cancels where the student comes
 // close to its teacher.
@@ -331,9 +331,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     float alpha = m, beta = m;
     const bool has_rest = S_rest > 0.f;
     if (r > 0.f && has_rest) {
-      const float over = r / S_rest;
-      alpha = m - over * S_listed;
-      beta = alpha + over * total;
+      alpha = m - (r / S_rest) * S_listed;
+      beta = m + r;  // (alpha + r / (1 - s), whose two large terms cancel)
     }
     const float2 lt = log_pair(total);
     // d = lz - L, the student's log-sum-exp less the teacher's (differences of

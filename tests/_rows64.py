@@ -7,7 +7,8 @@ import torch
 
 def distill64(z, ids, t, lse=None, T=1.0, w=None, tail=False):
     """Loss [N], its gradient [N, V] (of the sum), the sum of the absolute terms
-    of the loss [N], and the mask of listed ids [N, V]."""
+    of the loss [N], the mask of listed ids [N, V], and the sum of the absolute
+    terms of the gradient [N, V]."""
     T = float(torch.tensor(T, dtype=torch.float32))
     N, V = z.shape
     y = z.double() / T
@@ -25,7 +26,7 @@ def distill64(z, ids, t, lse=None, T=1.0, w=None, tail=False):
     lqj = lq.gather(1, ids.clamp_min(0).long())
     loss = torch.where(p > 0, p * (lp - lqj), 0.0).sum(1)
     scale = torch.where(p > 0, p * (lp.abs() + lqj.abs()), 0.0).sum(1)
-    grad = m * torch.exp(lq) - P
+    grad, size = m * torch.exp(lq) - P, m * torch.exp(lq) + P
     if tail:
         r = 1 - m
         r = torch.where(r >= 2.0 ** -20, r, 0.0)
@@ -34,11 +35,13 @@ def distill64(z, ids, t, lse=None, T=1.0, w=None, tail=False):
         loss = loss + term
         scale = scale + term.abs()
         share = torch.where(listed | torch.isneginf(rest), 0.0, torch.exp(lq - rest))
-        grad = grad + torch.where(torch.isneginf(rest), 0.0, r) * (torch.exp(lq) - share)
+        r = torch.where(torch.isneginf(rest), 0.0, r)
+        grad, size = grad + r * (torch.exp(lq) - share), size + r * (torch.exp(lq) + share)
     w = torch.ones(N, dtype=torch.float64, device=z.device) if w is None else w.double()
     none = w == 0
-    return (torch.where(none, 0.0, w * loss), torch.where(none[:, None], 0.0, w[:, None] * grad / T),
-            torch.where(none, 0.0, w.abs() * scale), listed)
+    each = lambda x: torch.where(none[:, None], 0.0, w[:, None] * x / T)  # noqa: E731
+    return (torch.where(none, 0.0, w * loss), each(grad), torch.where(none, 0.0, w.abs() * scale), listed,
+            each(size).abs())
 
 
 def sample64(z, T, k, p, mp, u, near_by=1e-9):

@@ -3,10 +3,11 @@ element of the gradients against the definition in 64 bits.
 
 Tolerances.  A weight 2^x is taken at an argument rounded twice (2^-24 of |x|
 each, |x| <= 64 in these inputs: 5.3e-6 of the weight) by a function good to
-2^-22, in a quotient of sums good to a few 2^-24: REL = 2^-17 of the value.
-Where the loss has no tail, a token outside the list has the gradient m q, a
-product: REL of its own value.  At a listed id the gradient is a difference:
-REL of the row's largest.  Rounding to the logits' type adds eps / 2.
+2^-22, in a quotient of sums good to a few 2^-24: REL = 2^-17 of the value, and
+of a gradient of several terms REL of the sum of their absolute values.  The
+teacher's tail r is one less a sum whose addends are good to 2^-21 (log p to
+2^-24 of up to 10, and its exponential): with r >= 1/16 a term in r is good to
+REL + 2^-17 = TAIL.  Rounding to the logits' type adds eps / 2.
 """
 import pytest
 
@@ -16,7 +17,7 @@ torch = pytest.importorskip("torch")
 
 from tests._rows64 import distill64  # noqa: E402
 
-REL = 2.0 ** -17
+REL, TAIL = 2.0 ** -17, 2.0 ** -16
 
 
 @pytest.fixture(scope="module")
@@ -39,12 +40,9 @@ def both(sv, z, ids, val, grads=(None, None), lse=None, T=1.0, w=None, tail=Fals
     return o["loss"], o["grad"], back
 
 
-def close(got, want, listed, dtype, tail):
-    """Every element; `want` fp64."""
-    top = want.abs().amax(1, keepdim=True)
-    own = want.abs()
-    room = REL * torch.where(listed | torch.tensor(tail, device=want.device), top, own)
-    room = room + torch.finfo(dtype).eps / 2 * own + torch.finfo(dtype).tiny
+def close(got, want, size, rel=REL):
+    """Every element; `want` fp64, `size` the sum of its absolute terms."""
+    room = rel * size + torch.finfo(got.dtype).eps / 2 * want.abs() + torch.finfo(got.dtype).tiny
     off = (got.double() - want).abs()
     assert (off <= room).all(), (off - room).argmax()
 
@@ -68,16 +66,40 @@ def test_absent_entries_of_unaligned_rows(sv, V, off, dtype):
     ids = torch.where((torch.arange(K, device="cuda") < length) & ~gaps, ids, -1).int()
     ids[3, 0], ids[4, 1] = 0, V - 1  # the ends themselves
     ids[3, 1:], ids[4, 2:], ids[4, 0] = -1, -1, -1
-    _, want, _, listed = distill64(z, ids, val)
+    _, want, _, _, size = distill64(z, ids, val)
     bufs = [torch.full((N, wide), 9.0, dtype=dtype, device="cuda") for _ in range(2)]
     _, fused, back = both(sv, z, ids, val, [b[:, off:off + V] for b in bufs])
     for b, got in zip(bufs, (fused, back)):
         assert (b[:, :off] == 9).all() and (b[:, off + V:] == 9).all()
-        close(got, want, listed, dtype, False)
+        close(got, want, size)
     # rows without a gap between them: the end of each is the next one's neighbour
     zc = z.contiguous()
     _, fused, back = both(sv, zc, ids, val)
     for got in (fused, back):
-        close(got, want, listed, dtype, False)
+        close(got, want, size)
     again = sv.specv_distill_backward(zc, ids, val, sv.specv_distill(zc, ids, val)["stats"])
     assert torch.equal(again, back)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,K", [(2000, 16), (30011, 200)])
+def test_confident_students(sv, V, K, dtype):
+    """Students with 1e-2 to 1e-17 of their mass outside the teacher's list."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    N = 64
+    teacher = torch.randn(N, V, generator=g, device="cuda") * 2
+    val, ids = teacher.topk(K, dim=1)
+    ids = ids.int()
+    lse = torch.logsumexp(teacher, 1)
+    z = torch.randn(N, V, generator=g, device="cuda") - 4
+    gap = torch.linspace(8.0, 40.0, N, device="cuda")[:, None]
+    z.scatter_add_(1, ids.long(), gap + 2 * torch.randn(N, K, generator=g, device="cuda"))
+    z = z.to(dtype)
+    loss, want, scale, listed, size = distill64(z, ids, val, lse, tail=True)
+    r = 1 - torch.exp(val.double() - lse.double()[:, None]).sum(1)
+    q = torch.where(listed, 0.0, torch.softmax(z.double(), 1)).sum(1)
+    assert r.min() >= 1 / 16 and q.max() > 1e-4 and q.min() < 1e-14
+    got, fused, back = both(sv, z, ids, val, lse=lse, tail=True)
+    assert ((got.double() - loss).abs() <= TAIL * scale).all()
+    close(fused, want, size, TAIL)
+    close(back, want, size, TAIL)

@@ -27,13 +27,14 @@ def test_distillation(how, T):
     lse = None if how == "renorm" else torch.logsumexp(teacher / T, 1)
     w = torch.rand(N, generator=g)
     w[9] = 0
-    loss, grad, scale, listed = distill64(z, ids, val, lse, T, w, how == "tail")
+    loss, grad, scale, listed, size = distill64(z, ids, val, lse, T, w, how == "tail")
     for b in range(N):
         want, dz, s = formula(z[b].double().numpy(), ids[b].numpy(), val[b].double().numpy(),
                               None if lse is None else float(lse[b]), T, float(w[b]), how == "tail")
         # differently ordered sums of 64-bit terms
         assert loss[b] == want or abs(float(loss[b]) - want) <= 1e-12 * (1 + abs(want)), b
         assert np.abs(grad[b].numpy() - dz).max() <= 1e-12, b
+        assert (size[b] >= grad[b].abs() * (1 - 1e-12)).all()
         assert scale[b] == s or np.isinf(want) or abs(float(scale[b]) - s) <= 1e-12 * (1 + s)
         assert set(np.flatnonzero(listed[b].numpy())) == {int(i) for i in ids[b] if i >= 0}
 
