@@ -9,7 +9,8 @@
 //   alpha = m [- r s / (1 - s)],  beta = m [+ r]
 // 1 - s is summed over the logits that are not listed, and beta q - p is taken
 // as p (exp(log(beta q / p)) - 1), so neither cancels where the student comes
-// close to its teacher.
+// close to its teacher.  The logarithms at listed ids are pairs of fp32 (z / T has
+// thousands of units at low temperatures), computed alike by both kernels.
 //
 // All of it in fp32, differences taken before they are scaled; sums of p are
 // exact in units of 2^-40.  (An SM does two fp64 operations a clock: a few of
@@ -35,8 +36,8 @@ struct DistillParams {
   float c;              // log2(e) / T
   int32_t tail;
   float* loss;
-  float4* stats;        // (max logit, alpha / sum, log(beta q / p) - (z - t) / T, L), sum =
-                        // sum exp((z - max) / T); L NaN: a row without result
+  float4* stats;        // (max logit, alpha / sum, the same logit, beta / sum), sum =
+                        // sum exp((z - max) / T); max NaN: a row without result
   void* grad;
   int64_t grs;
   int32_t* status;
@@ -70,12 +71,95 @@ __device__ __forceinline__ float block_max_nan(float x, float* scratch) {
   return m;
 }
 
+// (a - b) / T as hi + lo, to about 2^-45 of it (infinite: as hi alone).
+__device__ __forceinline__ float2 over(float a, float b, float ih, float il) {
+  const float d = a - b, bb = d - a;
+  const float e = (a - (d - bb)) - (b + bb);  // what the difference lost
+  const float hi = __fmul_rn(d, ih);
+  return make_float2(hi, fabsf(hi) < 1e30f ? fmaf(e, ih, fmaf(d, il, fmaf(d, ih, -hi))) : 0.f);
+}
+
+// What a CTA knows of a row's teacher.
+struct Teacher {
+  float L;         // the log-sum-exp that was given
+  float tmax;      // without one: the largest entry, and
+  float pscale;    //   one by the sum of exp((t - tmax) / T); p_j = pj pscale
+  uint64_t mass;   // sum of pj, in units of 2^-40 (where it was asked for)
+  int bad;         // this thread's findings
+
+  __device__ __forceinline__ float sum() const { return static_cast<float>(mass) * (1.f / kFixed); }
+  // log p_j less t_j / T (tmax / T without a log-sum-exp), as a pair, negated
+  __device__ __forceinline__ float2 norm(bool given) const { return given ? make_float2(L, 0.f) : log_pair(sum()); }
+};
+
+// The row's entries into shared memory (ids, -1 where absent; logits, -inf
+// there; pj), by the whole CTA.  With MASS it ends with a barrier; without, a
+// barrier is left to the caller (where a log-sum-exp is given there is none:
+// the backward pass of 1024 x 152064 fp32 is 3 us shorter without).
+template <bool MASS>
+__device__ Teacher load_teacher(const DistillParams& P, int64_t row, int32_t* ids, float* tl, float* pj, float* fred,
+                                uint64_t* ured) {
+  const int K = P.K, V = P.sp.V;
+  const float ih = P.ih, il = P.il;
+  Teacher t = {};
+  t.pscale = 1.f;
+  bool some = true;  // (without a log-sum-exp: there are entries)
+  float mx = neg_inf();
+  for (int j = threadIdx.x; j < K; j += kRowThreads) {
+    const int id = P.ids[row * P.ts + j];
+    const float x = P.tl[row * P.ts + j];
+    if (id < -1 || id >= V) t.bad |= kBadToken;
+    const bool there = id >= 0 && id < V;
+    ids[j] = there ? id : -1;
+    tl[j] = there ? x : neg_inf();
+    if (there && !(x < pos_inf())) t.bad |= kNonFinite;  // NaN or +inf
+    if (there) mx = max_nan(mx, x);
+  }
+  uint64_t v = 0;
+  if (P.tlse) {
+    t.L = P.tlse[row];
+    if (!isfinite(t.L)) t.bad |= kNonFinite;
+    // p = exp(t / T - L), the product's rounding to first order
+    for (int j = threadIdx.x; j < K; j += kRowThreads) {
+      const float x = __fmul_rn(tl[j], ih);
+      const float p = tl[j] > neg_inf() ? expf(x - t.L) * (1.f + fmaf(tl[j], il, fmaf(tl[j], ih, -x))) : 0.f;
+      pj[j] = p;
+      if (MASS) v += __float2ull_rn(fminf(p, 1e6f) * kFixed);
+    }
+  } else {  // relative to the largest, normalised by pscale
+    t.tmax = block_max_nan(mx, fred);
+    some = t.tmax > neg_inf() && t.tmax < pos_inf();
+    for (int j = threadIdx.x; j < K; j += kRowThreads) {
+      const float e = some && tl[j] > neg_inf() ? exp_over(tl[j] - t.tmax, ih, il) : 0.f;
+      pj[j] = e;
+      v += __float2ull_rn(e * kFixed);
+    }
+  }
+  if (MASS || !P.tlse) {
+    if ((threadIdx.x & ~31u) < static_cast<unsigned>(K)) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    if ((threadIdx.x & 31) == 0) ured[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) t.mass += ured[w];
+  }
+  if (!P.tlse) t.pscale = some && t.mass ? 1.f / t.sum() : 0.f;
+  return t;
+}
+
 // beta q - p at a listed id: z its logit, t and p those of its entry, ps the
-// sum of p over its entries, d = log(beta q / p) - (z - t) / T, bq = beta q to
-// fp32's accuracy.
-__device__ __forceinline__ float listed_grad(float z, float t, float p, float ps, float ih, float d, float bq) {
-  if (p > 0.f && ps == p) return p * expm1f((z - t) * ih + d);
-  return bq - ps;
+// sum of p over its entries, b = beta / sum, lb its logarithm, ln the entries'
+// normaliser.  Like sizes of the two logarithms are taken apart first.
+__device__ __forceinline__ float listed_grad(const DistillParams& P, const Teacher& te, float z, float t, float p,
+                                             float ps, float mx, float b, float2 lb, float2 ln) {
+  const float2 q = over(z, mx, P.ih, P.il);  // log(beta q) less lb
+  const float bq = q.x > -100.f ? b * (expf(q.x) * (1.f + q.y)) : 0.f;
+  if (!(p > 0.f && ps == p)) return bq - ps;
+  const float2 o = over(t, P.tlse ? 0.f : te.tmax, P.ih, P.il);
+  const float x = ((q.x - (o.x - ln.x)) + lb.x) + ((q.y - o.y) + (ln.y + lb.y));
+  return x < 1.f ? p * expm1f(x) : bq - p;
 }
 
 // For teacher entry j of a row (ids, p in shared memory): the sum of p over
@@ -145,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   __shared__ uint64_t ured[kRowWarps];
   __shared__ DistillPart part[kMaxCluster];
   __shared__ int badbits, again;
-  __shared__ float row_max, row_alpha, row_beta, row_delta;
+  __shared__ float row_max, row_alpha, row_beta;
   __shared__ int row_dead;
   const int C = P.sp.C, K = P.K, V = P.sp.V;
   const int rank = cluster_rank();
@@ -167,67 +251,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   float* pj = tl + K;
   float* zj = pj + K;
   float* sj = zj + K;  // p of the entry's id, or -1: not its first entry
-  const float ih = P.ih, il = P.il, c = P.c;
+  const float ih = P.ih, c = P.c;
   const int lo = sl.base, hi = min(V, lo + P.sp.svec * VW);  // the slice's indices
-  float L = 0.f, tmax = 0.f, pscale = 1.f;
-  uint64_t mass = 0;  // sum of pj, in units of 2^-40
+  Teacher te = {};
+  te.pscale = 1.f;
+  int bad = 0;
   RunningSum rs;  // over the logits that are not listed
   float zmax = neg_inf(), a = 0.f;
-  bool some = true;  // (without a log-sum-exp: there are entries)
   if (!skip) {
     sl.load();
     for (int i = threadIdx.x; i < words; i += kRowThreads) bits[i] = 0;
-    // the teacher's entries, in every CTA
-    int bad = 0;
-    float mx = neg_inf();
-    for (int j = threadIdx.x; j < K; j += kRowThreads) {
-      const int id = P.ids[row * P.ts + j];
-      const float t = P.tl[row * P.ts + j];
-      if (id < -1 || id >= V) bad |= kBadToken;
-      const bool there = id >= 0 && id < V;
-      ids[j] = there ? id : -1;
-      tl[j] = there ? t : neg_inf();
-      if (there && !(t < pos_inf())) bad |= kNonFinite;  // NaN or +inf
-      if (there) mx = max_nan(mx, t);
-    }
-    uint64_t v = 0;
-    if (P.tlse) {
-      L = P.tlse[row];
-      if (!isfinite(L)) bad |= kNonFinite;
-      // p = exp(t / T - L), the product's rounding to first order
-      for (int j = threadIdx.x; j < K; j += kRowThreads) {
-        const float t = tl[j], x = __fmul_rn(t, ih);
-        const float p = t > neg_inf() ? expf(x - L) * (1.f + fmaf(t, il, fmaf(t, ih, -x))) : 0.f;
-        pj[j] = p;
-        v += __float2ull_rn(fminf(p, 1e6f) * kFixed);
-      }
-    } else {  // relative to the largest, normalised below
-      tmax = block_max_nan(mx, tred);
-      some = tmax > neg_inf() && tmax < pos_inf();
-      for (int j = threadIdx.x; j < K; j += kRowThreads) {
-        const float e = some && tl[j] > neg_inf() ? exp_over(tl[j] - tmax, ih, il) : 0.f;
-        pj[j] = e;
-        v += __float2ull_rn(e * kFixed);
-      }
-    }
-    if ((threadIdx.x & ~31u) < static_cast<unsigned>(K)) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    }
-    if (lane == 0) ured[warp] = v;
-    __syncthreads();  // ids, tl, pj, no bits, the sums
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) mass += ured[w];
-    if (!P.tlse) {
-      const float S = static_cast<float>(mass) * (1.f / kFixed);
-      pscale = some && mass ? 1.f / S : 0.f;
-      L = some && mass ? tmax * ih + logf(S) : 0.f;
-    }
+    te = load_teacher<true>(P, row, ids, tl, pj, tred, ured);  // (a barrier: no bits, too)
+    bad = te.bad;
     // The listed ids of this slice: their logits, and a bit for each.
     for (int j = threadIdx.x; j < K; j += kRowThreads) {
       const int id = ids[j];
       if (id < lo || id >= hi) continue;
-      const float z = E::scalar(zrow, id), p = pj[j] * pscale;
+      const float z = E::scalar(zrow, id), p = pj[j] * te.pscale;
       const unsigned bit = 1u << ((id - lo) & 31);
       if (atomicOr(&bits[(id - lo) >> 5], bit) & bit) again = 1;
       zj[j] = z;
@@ -241,7 +281,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
         const int id = ids[j];
         if (id < lo || id >= hi) continue;
         bool first;
-        const float ps = same_id(ids, pj, K, j, lane, first) * pscale;
+        const float ps = same_id(ids, pj, K, j, lane, first) * te.pscale;
         if (lane == 0) sj[j] = first ? ps : -1.f;
       }
       __syncthreads();
@@ -325,8 +365,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     }
     const bool dead = skip || anybad || !finite;
     const float total = S_rest + S_listed, inv = 1.f / total;
-    const float m = P.tlse ? pscale * (static_cast<float>(mass) * (1.f / kFixed)) : (mass ? 1.f : 0.f);
-    float r = P.tail ? fmaf(-pscale, static_cast<float>(mass) * (1.f / kFixed), 1.f) : 0.f;
+    const float m = P.tlse ? te.sum() : (te.mass ? 1.f : 0.f);
+    float r = P.tail ? static_cast<float>((1ll << 40) - static_cast<int64_t>(te.mass)) * (1.f / kFixed) : 0.f;
     if (r < kNoTail) r = 0.f;
     float alpha = m, beta = m;
     const bool has_rest = S_rest > 0.f;
@@ -340,23 +380,22 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     float d;
     if (P.tlse) {
       const float x = __fmul_rn(mx, ih);
-      d = (x - L) + lt.x + (lt.y + fmaf(mx, il, fmaf(mx, ih, -x)));
+      d = (x - te.L) + lt.x + (lt.y + fmaf(mx, P.il, fmaf(mx, ih, -x)));
     } else {
-      const float2 ls = log_pair(static_cast<float>(mass) * (1.f / kFixed));
-      d = mass ? (mx - tmax) * ih + (lt.x - ls.x) + (lt.y - ls.y) : 0.f;
+      const float2 ls = te.norm(false);
+      d = te.mass ? (mx - te.tmax) * ih + (lt.x - ls.x) + (lt.y - ls.y) : 0.f;
     }
     row_dead = dead;
     row_max = mx;
     row_alpha = alpha * inv;
     row_beta = beta * inv;
-    row_delta = logf(beta) - d;
     if (rank == 0) {
       float loss = A + m * d;
       if (r > 0.f) loss += has_rest ? r * logf(r * total / S_rest) : pos_inf();
       P.loss[row] = dead ? 0.f : wt * loss;
       if (P.stats)
-        P.stats[row] = dead ? make_float4(0.f, 0.f, 0.f, __int_as_float(0x7fc00000))
-                            : make_float4(mx, row_alpha, row_delta, L);
+        P.stats[row] = dead ? make_float4(__int_as_float(0x7fc00000), 0.f, 0.f, 0.f)
+                            : make_float4(mx, row_alpha, mx, row_beta);
       if (P.status) P.status[row] = skip ? 0 : (anybad | (finite ? 0 : kNonFinite));
     }
   }
@@ -381,11 +420,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   });
   if (dead) return;
   __syncthreads();  // the listed ids' gradients go over what was just written
+  const float b = row_beta;
+  const float2 lb = log_pair(b), ln = te.norm(P.tlse != nullptr);
   for (int j = threadIdx.x; j < K; j += kRowThreads) {
     const int id = ids[j];
     if (id < lo || id >= hi || sj[j] < 0.f) continue;
-    store_elem<DT>(grow, id, f * listed_grad(zj[j], tl[j], pj[j] * pscale, sj[j], ih, row_delta,
-                                             row_beta * ex2((zj[j] - mx) * c)));
+    store_elem<DT>(grow, id, f * listed_grad(P, te, zj[j], tl[j], pj[j] * te.pscale, sj[j], mx, b, lb, ln));
   }
 }
 
@@ -403,6 +443,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
   using Vec = typename E::Vec;
   constexpr int VW = E::VW;
   extern __shared__ __align__(16) char smem[];
+  __shared__ float tred[kRowWarps];
+  __shared__ uint64_t ured[kRowWarps];
+  __shared__ Teacher te;
   const int64_t row = blockIdx.x / pieces;
   const int piece = blockIdx.x % pieces;
   const int K = P.K, V = P.sp.V;
@@ -415,9 +458,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
   const float4 st = P.stats[row];
   const float wt = (P.weight ? P.weight[row] : 1.f);
   const float up = P.gloss ? P.gloss[row] : 1.f;
-  const bool dead = wt == 0.f || st.w != st.w;
-  const float ih = P.ih, il = P.il, c = P.c;
-  const float f = dead ? 0.f : wt * up * ih;
+  const bool dead = wt == 0.f || st.x != st.x;
+  const float c = P.c;
+  const float f = dead ? 0.f : wt * up * P.ih;
   const float ga = f * st.y;
   // vectors at 16-byte boundaries of memory: `off` places before the row's first logit
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(zrow) & 15) / E::ES;
@@ -441,16 +484,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
   Vec v[kBackVecs];
   load(i0, v);
   if (!dead) {  // the teacher's entries, while the first loads run
-    const float L = P.tlse ? P.tlse[row] : st.w;
-    for (int j = threadIdx.x; j < K; j += kRowThreads) {
-      const int id = P.ids[row * P.ts + j];
-      const float t = P.tl[row * P.ts + j];
-      const bool there = id >= 0 && id < V && t > neg_inf();
-      const float x = __fmul_rn(t, ih);
-      ids[j] = (id >= 0 && id < V) ? id : -1;
-      tl[j] = t;
-      pj[j] = there ? expf(x - L) * (1.f + fmaf(t, il, fmaf(t, ih, -x))) : 0.f;
-    }
+    const Teacher t = load_teacher<false>(P, row, ids, tl, pj, tred, ured);
+    if (threadIdx.x == 0) te = t;
   }
 #pragma unroll 1
   for (int at = i0; at < i1; at += per) {
@@ -469,18 +504,31 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
     }
   }
   if (dead) return;
-  __syncthreads();
+  __syncthreads();  // the listed ids' gradients go over what was just written
+  const float2 lb = log_pair(st.w), ln = te.norm(P.tlse != nullptr);
+  // Each warp gathers its entries of this piece, then takes them a lane each.
+  int own = -1, held = 0;
+  float own_ps = 0.f;
+  auto store = [&] {
+    if (own >= 0)
+      store_elem<DT>(grow, ids[own], f * listed_grad(P, te, E::scalar(zrow, ids[own]), tl[own], pj[own] * te.pscale,
+                                                     own_ps, st.z, st.w, lb, ln));
+    own = -1;
+    held = 0;
+  };
   for (int j = warp; j < K; j += kRowWarps) {
     const int id = ids[j];
     if (id < max(i0, 0) || id >= i1) continue;  // (i0 lies before a row that starts inside a vector; absent: -1)
     bool first;
-    const float ps = same_id(ids, pj, K, j, lane, first);
-    if (lane == 0 && first) {
-      const float z = E::scalar(zrow, id);
-      const float bq = expf(st.z + st.x * ih - st.w) * ex2((z - st.x) * c);
-      store_elem<DT>(grow, id, f * listed_grad(z, tl[j], pj[j], ps, ih, st.z, bq));
+    const float ps = same_id(ids, pj, K, j, lane, first) * te.pscale;
+    if (!first) continue;
+    if (lane == held) {
+      own = j;
+      own_ps = ps;
     }
+    if (++held == 32) store();
   }
+  store();
 }
 
 }  // namespace specv

@@ -4,7 +4,8 @@ element of the gradients against the definition in 64 bits.
 Tolerances.  A weight 2^x is taken at an argument rounded twice (2^-24 of |x|
 each, |x| <= 64 in these inputs: 5.3e-6 of the weight) by a function good to
 2^-22, in a quotient of sums good to a few 2^-24: REL = 2^-17 of the value, and
-of a gradient of several terms REL of the sum of their absolute values.  The
+of a gradient of several terms REL of the sum of their absolute values (weights
+below 2^-64: 2^-64 of the row's largest).  The
 teacher's tail r is one less a sum whose addends are good to 2^-21 (log p to
 2^-24 of up to 10, and its exponential): with r >= 1/16 a term in r is good to
 REL + 2^-17 = TAIL.  Rounding to the logits' type adds eps / 2.
@@ -42,7 +43,7 @@ def both(sv, z, ids, val, grads=(None, None), lse=None, T=1.0, w=None, tail=Fals
 
 def close(got, want, size, rel=REL):
     """Every element; `want` fp64, `size` the sum of its absolute terms."""
-    room = rel * size + torch.finfo(got.dtype).eps / 2 * want.abs() + torch.finfo(got.dtype).tiny
+    room = rel * size + 2.0 ** -64 * size.amax(1, keepdim=True) + torch.finfo(got.dtype).eps / 2 * want.abs() + torch.finfo(got.dtype).tiny
     off = (got.double() - want).abs()
     assert (off <= room).all(), (off - room).argmax()
 
@@ -103,3 +104,25 @@ def test_confident_students(sv, V, K, dtype):
     assert ((got.double() - loss).abs() <= TAIL * scale).all()
     close(fused, want, size, TAIL)
     close(back, want, size, TAIL)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1.0, 0.1, 0.01, 0.001])
+@pytest.mark.parametrize("given", [False, True])
+def test_low_temperatures(sv, T, given, dtype):
+    """Logits of thousands of units (z / T), the gradient from saved statistics as
+    good as that of the one call."""
+    g = torch.Generator(device="cuda").manual_seed(int(1 / T))
+    N, V, K = 32, 5003, 40
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    teacher = 20 * normal(N, 1) + 2 * T * normal(N, V)
+    val, ids = teacher.topk(K, dim=1)
+    ids = ids.int()
+    ids[::5, 30:] = -1
+    z = (20 * normal(N, 1) + 2 * T * normal(N, V)).to(dtype)
+    z[::2] = teacher[::2].to(dtype)
+    lse = torch.logsumexp(teacher.double() / float(torch.tensor(T)), 1).float() if given else None
+    loss, want, scale, _, size = distill64(z, ids, val, lse, T)
+    got, fused, back = both(sv, z, ids, val, lse=lse, T=T)
+    close(fused, want, size)
+    close(back, want, size)
