@@ -422,8 +422,9 @@ specv_status specv_top_logits(const specv_top_args* args, void* stream);
  *   loss[n] = weights[n] * D,   D = sum_j p_j (log p_j - log q(id_j))
  *   SPECV_DISTILL_TAIL: + r (log r - log(1 - s)), r = 1 - sum_j p_j (below
  *   2^-20: none), s = the listed ids' mass under q: all other tokens as one
- *   outcome.  If the student has no mass outside the list and r > 0, the loss
- *   is +inf and the gradient leaves that term out.
+ *   outcome.  If the student has no mass outside the list (its logits there are
+ *   -inf, or the type's lowest value below others) and r > 0, the loss is +inf
+ *   and the gradient leaves that term out.
  * Entries with id -1 are absent; an id listed twice counts as two entries of
  * the sum.  A row of weight 0 is not read: loss and gradient 0.
  * specv_distill writes loss, and if given the gradient of sum_n loss[n] and

@@ -7,7 +7,9 @@
 //   T dD/dz_v = alpha q_v                  v not listed
 //             = beta q_v - sum_{id_j=v} p_j  v listed
 //   alpha = m [- r s / (1 - s)],  beta = m [+ r]
-// 1 - s is summed over the logits that are not listed, and beta q - p is taken
+// 1 - s is summed over the logits that are not listed, relative to the largest of
+// them (they may all lie 100 / T and more below the listed ones, where exp(z - max)
+// underflows but neither log(1 - s) nor q / (1 - s) does), and beta q - p is taken
 // as p (exp(log(beta q / p)) - 1), so neither cancels where the student comes
 // close to its teacher.  The logarithms at listed ids are pairs of fp32 (z / T has
 // thousands of units at low temperatures), computed alike by both kernels.
@@ -36,8 +38,8 @@ struct DistillParams {
   float c;              // log2(e) / T
   int32_t tail;
   float* loss;
-  float4* stats;        // (max logit, alpha / sum, the same logit, beta / sum), sum =
-                        // sum exp((z - max) / T); max NaN: a row without result
+  float4* stats;        // (ref, A, max logit, beta / sum), sum = sum exp((z - max) / T),
+                        // alpha q_v = A exp((z_v - ref) / T); ref NaN: a row without result
   void* grad;
   int64_t grs;
   int32_t* status;
@@ -58,6 +60,12 @@ __device__ __forceinline__ float exp_over(float d, float ih, float il) {
 __device__ __forceinline__ float2 log_pair(float x) {
   const float hi = logf(x);
   return make_float2(hi, x > 0.f && x < 1e30f ? fmaf(x, expf(-hi), -1.f) : 0.f);
+}
+
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
 
 __device__ __forceinline__ float block_max_nan(float x, float* scratch) {
@@ -179,9 +187,26 @@ __device__ __forceinline__ float same_id(const int32_t* ids, const float* p, int
 }
 
 struct DistillPart {  // one CTA's share of a row
-  float m, rest, listed, a;
-  int32_t bad, pad;
+  float mr, ml;        // the largest logit that is not listed, and that is
+  float rest, listed;  // sums relative to them
+  float a;
+  int32_t bad;
 };
+
+// The sum of n <= 32 parts, by a whole warp.
+__device__ __forceinline__ DistillPart join(const DistillPart* p, int n, float c) {
+  const int lane = threadIdx.x & 31;
+  DistillPart t = {neg_inf(), neg_inf(), 0.f, 0.f, 0.f, 0};
+  if (lane < n) t = p[lane];
+  const float mr = warp_max_nan(t.mr), ml = warp_max_nan(t.ml);
+  t.rest = warp_sum_f(t.rest > 0.f ? ex2((t.mr - mr) * c) * t.rest : 0.f);
+  t.listed = warp_sum_f(t.listed > 0.f ? ex2((t.ml - ml) * c) * t.listed : 0.f);
+  t.a = warp_sum_f(t.a);
+  t.bad = __reduce_or_sync(0xffffffffu, t.bad);
+  t.mr = mr;
+  t.ml = ml;
+  return t;
+}
 
 // g 2^((z - m) c) of a vector's logits, in their type.
 template <int DT>
@@ -225,11 +250,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   constexpr int VW = E::VW;
   extern __shared__ __align__(16) char smem[];
   __shared__ uint64_t bars[kRowWarps * kMaxRing];
-  __shared__ float tred[kRowWarps], mred[kRowWarps], rred[kRowWarps], lred[kRowWarps], ared[kRowWarps];
+  __shared__ float tred[kRowWarps];
   __shared__ uint64_t ured[kRowWarps];
-  __shared__ DistillPart part[kMaxCluster];
+  __shared__ DistillPart wpart[kRowWarps], part[kMaxCluster];
   __shared__ int badbits, again;
-  __shared__ float row_max, row_alpha, row_beta;
+  __shared__ float row_max, row_ref, row_alpha, row_beta;
   __shared__ int row_dead;
   const int C = P.sp.C, K = P.K, V = P.sp.V;
   const int rank = cluster_rank();
@@ -315,64 +340,53 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     if (P.grad && sl.stages > 0) sl.prime();  // (the second pass's first copies)
     if (bad) atomicOr(&badbits, bad);
   }
-  // the slice's maximum, listed ids included
-  const float mc = block_max_nan(max_nan(rs.run, zmax), mred);
-  const float mref = mc > neg_inf() ? mc : 0.f;
+  // Each warp's sums, relative to its own maxima.  The rest keeps one of its
+  // own: a student may put e^-100 and less of its mass outside the list.
+  const float mr = warp_max_nan(rs.run), ml = warp_max_nan(zmax);
   float listed = 0.f;
-  if (!skip) {
+  if (!skip && ml > neg_inf()) {
     for (int j = threadIdx.x; j < K; j += kRowThreads)
-      if (ids[j] >= lo && ids[j] < hi && sj[j] >= 0.f) listed += ex2((zj[j] - mref) * c);
+      if (ids[j] >= lo && ids[j] < hi && sj[j] >= 0.f) listed += ex2((zj[j] - ml) * c);
   }
-  float rest = warp_sum_f(rs.at(mref, c));
   listed = warp_sum_f(listed);
+  const float rest = warp_sum_f(rs.at(mr, c));
   a = warp_sum_f(a);
   if (lane == 0) {
-    rred[warp] = rest;
-    lred[warp] = listed;
-    ared[warp] = a;
+    DistillPart mine = {mr, ml, rest, listed, a, 0};
+    wpart[warp] = mine;
   }
   __syncthreads();
   cluster_wait();
-  if (static_cast<int>(threadIdx.x) < C) {
-    DistillPart mine = {};
-    mine.m = mc;
+  if (warp == 0) {
+    DistillPart mine = join(wpart, kRowWarps, c);
     mine.bad = badbits;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-      mine.rest += rred[w];
-      mine.listed += lred[w];
-      mine.a += ared[w];
-    }
-    *peer(part + rank, static_cast<int>(threadIdx.x)) = mine;
+    if (lane < C) *peer(part + rank, lane) = mine;
   }
   if (C == 1) __syncthreads();
   else cluster_sync();
 
+  DistillPart all;
+  if (warp == 0) all = join(part, C, c);
   if (threadIdx.x == 0) {  // the row's scalars
-    float mx = neg_inf();
-    int anybad = 0;
-    for (int r = 0; r < C; ++r) {
-      mx = max_nan(mx, part[r].m);
-      anybad |= part[r].bad;
-    }
+    const int anybad = all.bad;
+    const float ur = all.mr, mx = max_nan(all.mr, all.ml);
     const bool finite = mx > neg_inf() && mx < pos_inf();
-    float S_rest = 0.f, S_listed = 0.f, A = 0.f;
-    for (int r = 0; r < C; ++r) {
-      const float f = finite ? ex2((part[r].m - mx) * c) : 0.f;
-      S_rest += f * part[r].rest;
-      S_listed += f * part[r].listed;
-      A += part[r].a;
-    }
+    const float S_rest = all.rest, S_listed = all.listed > 0.f ? ex2((all.ml - mx) * c) * all.listed : 0.f;
     const bool dead = skip || anybad || !finite;
-    const float total = S_rest + S_listed, inv = 1.f / total;
+    const float2 gap = over(ur, mx, ih, P.il);  // log of the rest's largest weight
+    const float far = gap.x > -100.f ? expf(gap.x) * (1.f + gap.y) : 0.f;
+    const float total = far * S_rest + S_listed, inv = 1.f / total;
     const float m = P.tlse ? te.sum() : (te.mass ? 1.f : 0.f);
     float r = P.tail ? static_cast<float>((1ll << 40) - static_cast<int64_t>(te.mass)) * (1.f / kFixed) : 0.f;
     if (r < kNoTail) r = 0.f;
-    float alpha = m, beta = m;
-    const bool has_rest = S_rest > 0.f;
+    // alpha q_v = m q_v - r s share_v, share_v = exp((z_v - ur) / T) / S_rest.
+    // (A rest of the type's lowest values below others is masked: no mass.)
+    float beta = m, ref = mx, alpha = m * inv;
+    const bool has_rest = S_rest > 0.f && (far > 0.f || ur > E::lowest());
     if (r > 0.f && has_rest) {
-      alpha = m - (r / S_rest) * S_listed;
       beta = m + r;  // (alpha + r / (1 - s), whose two large terms cancel)
+      ref = ur;
+      alpha = m * (far * inv) - r * (S_listed * inv) / S_rest;
     }
     const float2 lt = log_pair(total);
     // d = lz - L, the student's log-sum-exp less the teacher's (differences of
@@ -387,25 +401,26 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     }
     row_dead = dead;
     row_max = mx;
-    row_alpha = alpha * inv;
+    row_ref = ref;
+    row_alpha = alpha;
     row_beta = beta * inv;
     if (rank == 0) {
-      float loss = A + m * d;
-      if (r > 0.f) loss += has_rest ? r * logf(r * total / S_rest) : pos_inf();
+      float loss = all.a + m * d;
+      if (r > 0.f) loss += has_rest ? r * (logf(r * total / S_rest) - gap.x) : pos_inf();
       P.loss[row] = dead ? 0.f : wt * loss;
       if (P.stats)
         P.stats[row] = dead ? make_float4(__int_as_float(0x7fc00000), 0.f, 0.f, 0.f)
-                            : make_float4(mx, row_alpha, mx, row_beta);
+                            : make_float4(ref, alpha, mx, row_beta);
       if (P.status) P.status[row] = skip ? 0 : (anybad | (finite ? 0 : kNonFinite));
     }
   }
   if (!P.grad) return;
   __syncthreads();
   const bool dead = row_dead;
-  const float mx = row_max;
+  const float mx = row_max, ref = row_ref;
   const float f = wt * ih;
   const float ga = f * row_alpha;
-  const uint64_t c2 = f2(c, c), m2 = f2(-mx, -mx), g2 = f2(ga, ga);
+  const uint64_t c2 = f2(c, c), m2 = f2(-ref, -ref), g2 = f2(ga, ga);
   if (skip) {  // (nothing was copied)
     for (int j0 = 0; j0 < sl.nv; j0 += 32)
       store_warp<DT>(grow, sl.index(j0 + lane), V, j0 + lane < sl.nv, make_uint4(0u, 0u, 0u, 0u));

@@ -88,6 +88,7 @@ struct Elem<0> {
     return __ldg(reinterpret_cast<const unsigned short*>(row) + v);
   }
   __device__ static Raw neg_inf_raw() { return 0xff80u; }
+  __device__ static float lowest() { return __uint_as_float(0xff7f0000u); }
   __device__ static float scalar(const void* row, int64_t v) {
     unsigned short h = __ldg(reinterpret_cast<const unsigned short*>(row) + v);
     return __uint_as_float(static_cast<uint32_t>(h) << 16);
@@ -133,6 +134,7 @@ struct Elem<1> {
     return __ldg(reinterpret_cast<const float*>(row) + v);
   }
   __device__ static Raw neg_inf_raw() { return neg_inf(); }
+  __device__ static float lowest() { return kNegMax; }
   __device__ static float scalar(const void* row, int64_t v) {
     return __ldg(reinterpret_cast<const float*>(row) + v);
   }

@@ -10,6 +10,8 @@ teacher's tail r is one less a sum whose addends are good to 2^-21 (log p to
 2^-24 of up to 10, and its exponential): with r >= 1/16 a term in r is good to
 REL + 2^-17 = TAIL.  Rounding to the logits' type adds eps / 2.
 """
+import math
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -126,3 +128,56 @@ def test_low_temperatures(sv, T, given, dtype):
     got, fused, back = both(sv, z, ids, val, lse=lse, T=T)
     close(fused, want, size)
     close(back, want, size)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1.0, 0.01])
+@pytest.mark.parametrize("V", [2000, 30011])
+def test_students_far_from_the_rest(sv, V, T, dtype):
+    """Students with e^-60 to e^-2000 of their mass outside the list: the tail's
+    term is finite, and its gradient goes to the tokens of the rest."""
+    g = torch.Generator(device="cuda").manual_seed(V + 1)
+    N, K = 48, 30
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    teacher = 2 * T * normal(N, V)
+    val, ids = teacher.topk(K, dim=1)
+    ids = ids.int()
+    lse = torch.logsumexp(teacher.double() / float(torch.tensor(T)), 1).float()
+    gap = torch.logspace(math.log10(60), math.log10(2000), N, device="cuda")[:, None]
+    z = T * normal(N, V)
+    z.scatter_add_(1, ids.long(), T * (gap + 2 * normal(N, K)))
+    z = z.to(dtype)
+    loss, want, scale, _, size = distill64(z, ids, val, lse, T, tail=True)
+    assert torch.isfinite(loss).all()
+    assert (1 - torch.exp(val.double() / float(torch.tensor(T)) - lse.double()[:, None]).sum(1)).min() >= 1 / 16
+    got, fused, back = both(sv, z, ids, val, lse=lse, T=T, tail=True)
+    assert ((got.double() - loss).abs() <= TAIL * scale).all()
+    close(fused, want, size, TAIL)
+    close(back, want, size, TAIL)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_masked_rest(sv, dtype):
+    """Outside the list: -inf, the type's lowest value (a mask: no mass), -1e9 (a
+    logit like others), and rows of nothing but the lowest value."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    N, V, K = 4, 3001, 12
+    z = torch.randn(N, V, generator=g, device="cuda")
+    val, ids = (z + 1).topk(K, dim=1)
+    ids = ids.int()
+    lse = torch.logsumexp(z + 1, 1)
+    rest = torch.ones(N, V, dtype=torch.bool, device="cuda").scatter_(1, ids.long(), False)
+    z = z.to(dtype)
+    for b, x in enumerate((-float("inf"), torch.finfo(dtype).min, -1e9)):
+        z[b][rest[b]] = x
+    z[3] = torch.finfo(dtype).min
+    loss, want, scale, _, size = distill64(torch.where(rest & (z < -2e9), -float("inf"), z)[:3], ids[:3], val[:3], lse[:3],
+                                           tail=True)
+    got, fused, back = both(sv, z, ids, val, lse=lse, tail=True)
+    assert got[:2].tolist() == [float("inf")] * 2
+    assert abs(float(got[2]) - float(loss[2])) <= TAIL * float(scale[2])
+    for grad in (fused, back):
+        close(grad[:3], want, size, TAIL)
+    _, want, _, _, size = distill64(torch.zeros(1, V).cuda(), ids[3:], val[3:], lse[3:], tail=True)  # equal logits
+    for grad in (fused, back):
+        close(grad[3:], want, size, TAIL)
