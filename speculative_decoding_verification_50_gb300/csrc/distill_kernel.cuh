@@ -248,11 +248,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   using E = Elem<DT>;
   using Vec = typename E::Vec;
   constexpr int VW = E::VW;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(128) char smem[];
   __shared__ uint64_t bars[kRowWarps * kMaxRing];
   __shared__ float tred[kRowWarps];
   __shared__ uint64_t ured[kRowWarps];
   __shared__ DistillPart wpart[kRowWarps], part[kMaxCluster];
+  __shared__ float2 origin;
   __shared__ int badbits, again;
   __shared__ float row_max, row_ref, row_alpha, row_beta;
   __shared__ int row_dead;
@@ -282,12 +283,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   te.pscale = 1.f;
   int bad = 0;
   RunningSum rs;  // over the logits that are not listed
-  float zmax = neg_inf(), a = 0.f;
+  float zmax = neg_inf();
   if (!skip) {
     sl.load();
     for (int i = threadIdx.x; i < words; i += kRowThreads) bits[i] = 0;
     te = load_teacher<true>(P, row, ids, tl, pj, tred, ured);  // (a barrier: no bits, too)
     bad = te.bad;
+    // The loss is sum p (log p - log q), of terms relative to an entry's (the first
+    // there is, in a sorted list the largest): logits of student and teacher may lie
+    // anywhere, thousands of T apart.
+    if (threadIdx.x == kRowThreads - 1) {
+      int j = 0;
+      while (j < K && ids[j] < 0) ++j;
+      const float t0 = j < K ? tl[j] : 0.f, z0 = j < K ? E::scalar(zrow, ids[j]) : 0.f;
+      origin = isfinite(t0) && isfinite(z0) ? make_float2(t0, z0) : make_float2(0.f, 0.f);
+    }
     // The listed ids of this slice: their logits, and a bit for each.
     for (int j = threadIdx.x; j < K; j += kRowThreads) {
       const int id = ids[j];
@@ -298,7 +308,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
       zj[j] = z;
       sj[j] = p;
       zmax = max_nan(zmax, z);
-      if (p > 0.f) a += p * ((tl[j] - z) * ih);
     }
     __syncthreads();
     if (again) {  // rare: an id listed twice; its first entry stands for them
@@ -343,10 +352,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   // Each warp's sums, relative to its own maxima.  The rest keeps one of its
   // own: a student may put e^-100 and less of its mass outside the list.
   const float mr = warp_max_nan(rs.run), ml = warp_max_nan(zmax);
-  float listed = 0.f;
-  if (!skip && ml > neg_inf()) {
-    for (int j = threadIdx.x; j < K; j += kRowThreads)
-      if (ids[j] >= lo && ids[j] < hi && sj[j] >= 0.f) listed += ex2((zj[j] - ml) * c);
+  float listed = 0.f, a = 0.f;
+  if (!skip) {
+    const float mref = ml > neg_inf() ? ml : 0.f;
+    for (int j = threadIdx.x; j < K; j += kRowThreads) {
+      if (ids[j] < lo || ids[j] >= hi) continue;
+      const float p = pj[j] * te.pscale, z = zj[j];
+      if (sj[j] >= 0.f) listed += ex2((z - mref) * c);
+      if (p > 0.f) a += p * (((tl[j] - origin.x) - (z - origin.y)) * ih);
+    }
   }
   listed = warp_sum_f(listed);
   const float rest = warp_sum_f(rs.at(mr, c));
@@ -389,16 +403,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
       alpha = m * (far * inv) - r * (S_listed * inv) / S_rest;
     }
     const float2 lt = log_pair(total);
-    // d = lz - L, the student's log-sum-exp less the teacher's (differences of
-    // like sizes first)
-    float d;
-    if (P.tlse) {
-      const float x = __fmul_rn(mx, ih);
-      d = (x - te.L) + lt.x + (lt.y + fmaf(mx, P.il, fmaf(mx, ih, -x)));
-    } else {
-      const float2 ls = te.norm(false);
-      d = te.mass ? (mx - te.tmax) * ih + (lt.x - ls.x) + (lt.y - ls.y) : 0.f;
-    }
+    // d = log p - log q at the origin (differences of like sizes first)
+    const float2 g = over(mx, origin.y, ih, P.il), o = over(origin.x, P.tlse ? 0.f : te.tmax, ih, P.il);
+    const float2 ln = te.norm(P.tlse != nullptr);
+    const float d = te.mass || P.tlse ? ((g.x + (o.x - ln.x)) + lt.x) + ((g.y + (o.y - ln.y)) + lt.y) : 0.f;
     row_dead = dead;
     row_max = mx;
     row_ref = ref;
@@ -457,7 +465,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
   using E = Elem<DT>;
   using Vec = typename E::Vec;
   constexpr int VW = E::VW;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(128) char smem[];
   __shared__ float tred[kRowWarps];
   __shared__ uint64_t ured[kRowWarps];
   __shared__ Teacher te;

@@ -1329,7 +1329,7 @@ struct FilterRow {
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __grid_constant__ FilterParams P) {
   using E = Elem<DT>;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) FilterShared S;
   const int C = P.sp.C, V = P.sp.V;
   const int64_t row = blockIdx.x / C;
@@ -1599,7 +1599,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid_constant__ TopParams P) {
   using E = Elem<DT>;
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) FilterShared S;
   const int C = P.sp.C, k = P.k;
   const int64_t row = blockIdx.x / C;

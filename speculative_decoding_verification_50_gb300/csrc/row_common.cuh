@@ -21,7 +21,8 @@ constexpr int kMaxCluster = 16;
 constexpr int kStage = 64;     // vectors of a ring's stage: two per lane
 constexpr int kMaxRing = 6;
 
-// Bytes of a CTA's held vectors and its warps' rings.
+// Bytes of a CTA's held vectors and its warps' rings.  (From a multiple of 128 bytes
+// on: 16 past one, loss + gradient of 1024 x 152064 fp32 take 8 % longer.)
 __host__ __device__ constexpr size_t row_bytes(int rvec, int stages) {
   return static_cast<size_t>(rvec + stages * kStage) * kRowWarps * 16;
 }

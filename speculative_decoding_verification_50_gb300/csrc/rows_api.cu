@@ -100,7 +100,7 @@ bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool first
 // largest of 1024 x 152064 fp32 254, 238, 419; of 2048 x 152064 bf16 236, 328, 429;
 // 100 of 333 x 50257 fp32 47, 60, 74.
 bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool top, RowSplit& sp, size_t& smem) {
-  constexpr size_t fixed = sizeof(FilterShared);
+  constexpr size_t fixed = (sizeof(FilterShared) + 127) / 128 * 128;
   const int H = top ? 1 : kMaxH;
   if (!split_row(rows, V, dtype, fixed + work_bytes(1), sp, smem)) return false;
   const int max_c = V / H <= kMaxBinned ? kMaxParts / H : 0;

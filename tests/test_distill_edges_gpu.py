@@ -126,6 +126,7 @@ def test_low_temperatures(sv, T, given, dtype):
     lse = torch.logsumexp(teacher.double() / float(torch.tensor(T)), 1).float() if given else None
     loss, want, scale, _, size = distill64(z, ids, val, lse, T)
     got, fused, back = both(sv, z, ids, val, lse=lse, T=T)
+    assert ((got.double() - loss).abs() <= REL * scale).all()
     close(fused, want, size)
     close(back, want, size)
 
@@ -181,3 +182,38 @@ def test_masked_rest(sv, dtype):
     _, want, _, _, size = distill64(torch.zeros(1, V).cuda(), ids[3:], val[3:], lse[3:], tail=True)  # equal logits
     for grad in (fused, back):
         close(grad[3:], want, size, TAIL)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [0.0, 1e4, -1e30, "lowest"])
+def test_equal_logits_of_any_size(sv, dtype, at):
+    """A student of equal logits has the loss of one of zeros."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    N, V, K = 6, 2500, 20
+    t = torch.randn(N, V, generator=g, device="cuda")
+    val, ids = t.topk(K, dim=1)
+    ids = ids.int()
+    ids[1, 0] = ids[2, 3] = -1
+    z = torch.full((N, V), torch.finfo(dtype).min if at == "lowest" else at, dtype=dtype, device="cuda")
+    for lse, tail in ((None, False), (torch.logsumexp(t, 1), True)):
+        loss, want, scale, _, size = distill64(torch.zeros(N, V).cuda(), ids, val, lse, tail=tail)
+        got, fused, back = both(sv, z, ids, val, lse=lse, tail=tail)
+        assert ((got.double() - loss).abs() <= TAIL * scale).all()
+        close(fused, want, size, TAIL)
+        close(back, want, size, TAIL)
+
+
+def test_ruled_out_first_entry(sv):
+    """-inf at the entry the loss is taken relative to, of mass and of none."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    z = torch.randn(2, 2000, generator=g, device="cuda")
+    val, ids = (z + 1).topk(16, dim=1)
+    ids = ids.int()
+    z[0, ids[0, 0].long()] = -float("inf")
+    val[1, 0] = -float("inf")
+    got, fused, back = both(sv, z, ids, val)
+    loss, want, scale, _, size = distill64(z[1:], ids[1:], val[1:])
+    assert got[0] == float("inf") and torch.isfinite(fused).all() and torch.isfinite(back).all()
+    assert abs(float(got[1]) - float(loss)) <= REL * float(scale)
+    close(fused[1:], want, size)
+    close(back[1:], want, size)
