@@ -173,7 +173,7 @@ struct Decision {
   int32_t token;              // the token, if rank 0 has it (part = -1)
   uint64_t rem;               // u W less what lies before that part
   uint64_t W;
-  uint64_t weight;            // the token's
+  float z;                    // the token's logit
 };
 
 struct FilterShared {
@@ -274,15 +274,24 @@ struct FilterRow {
     const int s = (d + kGrid - 1) / kGrid;
     return s > 0 ? (x + (1ull << (s - 1))) >> s : x;
   }
-  // A token's weight, good to 2^-32 of itself, in the same units: at least one,
-  // so that every kept token can be drawn.  (A list's and a part's tokens; the
-  // histograms' masses take the exact product.)
+  // A token's weight in whole units, at least one, so that every kept token can
+  // be drawn: what light tokens lose or gain by that, a unit each, is the draw's
+  // resolution.  (A list's and a part's tokens; the histograms' masses take the
+  // exact product.)
   __device__ __forceinline__ uint64_t weight(float z) const {
     int d;
     const uint32_t v = sc.weight(z, d);
     const uint64_t x = static_cast<uint64_t>(v) * S.tab32[(-d) & (kGrid - 1)];
     const int s = min(58 - fbits + ((d + kGrid - 1) >> 5), 62);
     return max(((x >> s) + 1) >> 1, uint64_t(1));
+  }
+
+  // A token's share of W, from its logit: 2^-29 of itself whatever its weight.
+  __device__ float share(float z, uint64_t W) const {
+    int d;
+    const uint32_t v = sc.weight(z, d);
+    const double w = static_cast<double>(v) * static_cast<double>(S.tab[(-d) & (kGrid - 1)]);
+    return static_cast<float>(ldexp(w, fbits - 91 - ((d + kGrid - 1) >> 5)) / static_cast<double>(W));
   }
 
   // The cluster's barrier.
@@ -1067,7 +1076,7 @@ struct FilterRow {
     if (sub == 0 && i < nk && (fell ? last : before <= t && (t < before + wt[i] || last))) {
       S.dec.part = -1;
       S.dec.token = idx;
-      S.dec.weight = wt[i];
+      S.dec.z = token_logit(list()[i]);
       S.dec.W = W;
       S.dec.fallback = fell;
     }
@@ -1314,7 +1323,7 @@ struct FilterRow {
     }
     if (lane == 0) {
       *token = found;
-      if (prob) *prob = static_cast<float>(static_cast<double>(weight(tz)) / static_cast<double>(W));
+      if (prob) *prob = share(tz, W);
     }
   }
 };
@@ -1569,7 +1578,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
       if (P.status) P.status[row] = (u && S.dec.fallback) ? kFallback : 0;
       if (u && S.dec.part < 0) {
         P.tokens[row] = S.dec.token;
-        if (P.prob) P.prob[row] = static_cast<float>(static_cast<double>(S.dec.weight) / static_cast<double>(S.dec.W));
+        if (P.prob) P.prob[row] = F.share(S.dec.z, S.dec.W);
       }
     }
     if (u && S.dec.part >= 0 && S.dec.part >> F.shift_H() == rank)

@@ -125,3 +125,31 @@ def test_rules(sv, dtype, V):
     check(sv, z, rng.choice([0.0, 0.3, 0.7, 1.0, 1.7], B), rng.choice([0, 0, 1, 5, 50, 1500, V // 2, V, V + 3], B),
           rng.choice([1.0, 1.0, 0.0, 0.1, 0.5, 0.9, 0.99], B), rng.choice([0.0, 0.0, 0.001, 0.1, 0.5, 1.0], B),
           rng.integers(0, 1 << 24, B) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("how", ["list", "few", "streamed"])
+def test_prob_of_light_tokens(sv, dtype, how):
+    """A uniform of 0 draws the first kept token, of weight 2^0 to 2^-47.9: its
+    share of the kept weight, to fp32's rounding."""
+    B = many() if how == "streamed" else 64
+    V = 60005 if how == "streamed" else 3001
+    g = torch.Generator(device="cuda").manual_seed(V)
+    T = 0.5 + torch.rand(B, generator=g, device="cuda")
+    ln2 = float(np.log(2.0))
+    z = torch.randn(B, V, generator=g, device="cuda") - 6
+    if how == "list":
+        z[:, 700:-1] = -float("inf")
+    z[:, -1] = 2.0
+    z[:, 0] = 2.0 - T * ln2 * torch.linspace(0.0, 47.9, B, device="cuda")
+    z = z.to(dtype)
+    k = torch.full((B,), 900, dtype=torch.int32, device="cuda") if how == "list" else None
+    o = sv.specv_sample(z, T, torch.zeros(B, device="cuda"), top_k=k)
+    y = z.double() / T.double()[:, None]
+    w = torch.exp(y - y.amax(1, keepdim=True))
+    kept = w >= 2.0 ** -48
+    want = torch.where(kept, w, 0.0)[:, 0] / torch.where(kept, w, 0.0).sum(1)
+    ok = kept[:, 0]
+    assert ok.sum() >= B - B // 32 - 1 and want[ok].min() < 2.0 ** -46
+    assert (o["tokens"][ok] == 0).all()
+    assert ((o["prob"].double() - want).abs() <= PROB_RTOL * want)[ok].all()
