@@ -1500,11 +1500,16 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     if (!done) {
       uint64_t goal = 0;
       CutKind kind = kGiven;
+      int last = 0;  // the last bin that counts
       if (use_p || u) {
         const float cut = F.zc;
         const bool whole = F.ic == INT_MAX;
         const uint32_t to = F.base();
         const int top = F.most();
+        // (Below a guessed maximum the last bin holds tokens under the floor too.  All of
+        // it is left out, at most 2^-47.9 for each of its kept ones: a part is drawn from
+        // only if it holds kept tokens.)
+        last = F.sc.template bin<false>(zf) - (guessed ? 1 : 0);
         if (guessed) {
         } else if (whole) {
           F.sl.each([&](float z, int) {
@@ -1516,7 +1521,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
           });
         }
         __syncthreads();
-        F.template merge<true>(kBins, F.sc.template bin<false>(zf));
+        F.template merge<true>(kBins, last);
         if (use_p) {
           goal = fraction(tp, S.Z) + 1;
           goal -= goal >> kSlack;
@@ -1539,7 +1544,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
         uint64_t x = 0;
         const int width = kRowThreads / P.sp.H;
         const uint32_t* hist = F.hist(F.sub);
-        for (int d = threadIdx.x % width; d < min(band.lo, kBins); d += width) {
+        for (int d = threadIdx.x % width; d < min(band.lo, last + 1); d += width) {
           const uint64_t v = (static_cast<uint64_t>(hist[d]) << 14) + hist[kHist + d];
           if (v) x += max(F.mass(v, d), uint64_t(1));
         }

@@ -153,3 +153,44 @@ def test_prob_of_light_tokens(sv, dtype, how):
     assert ok.sum() >= B - B // 32 - 1 and want[ok].min() < 2.0 ** -46
     assert (o["tokens"][ok] == 0).all()
     assert ((o["prob"].double() - want).abs() <= PROB_RTOL * want)[ok].all()
+
+
+@pytest.mark.parametrize("dtype,V", SIZES)
+@pytest.mark.parametrize("end", ["first", "last"])
+def test_parts_of_nothing_but_light_tokens(sv, dtype, V, end):
+    """A first (last) quarter of tokens just above or below the floor of 2^-48, and
+    the maximum where no guess finds it: a uniform of 0 (1) draws a kept token of that
+    end."""
+    B = many()
+    z = torch.full((B, V), -float("inf"), device="cuda")
+    light = 40.0 - float(np.log(2.0)) * torch.linspace(47.9, 48.6, B, device="cuda")[:, None]
+    if end == "first":
+        z[:, : V // 3] = light
+        z[:, V // 2: V // 2 + 3000] = 38.0
+        z[:, -3] = 40.0
+    else:
+        z[:, -V // 3:] = light
+        z[:, :3000] = 38.0
+        z[:, V // 2] = 40.0
+    z = z.to(dtype)
+    if dtype is torch.bfloat16:  # (steps of 2^-5 there: all rows' light tokens above the floor, or below)
+        assert ((z > -float("inf")) & (z < 20)).any(1).all()
+    T = torch.ones(B, device="cuda")
+    fill = dict(tokens=torch.full((B,), -7, dtype=torch.int32).cuda())
+    u = torch.full((B,), 0.0 if end == "first" else 1.0, device="cuda")
+    o = sv.specv_sample(z, T, u, **fill)
+    keep, tok, pr, _ = sample64(z, T, torch.zeros(B), torch.ones(B), torch.zeros(B), u)
+    assert torch.equal(o["kept"].long(), keep.sum(1))
+    assert (o["row_status"] == (sv.ROW_FALLBACK if end == "last" else 0)).all()
+    # (The light tokens' sum is below the draw's resolution of 2^-44 for each kept
+    # token: any of them may be drawn, or the first, last, that is heavier.)
+    at = torch.arange(V, device="cuda")
+    got = o["tokens"].long()
+    assert ((got >= 0) & (got < V)).all() and keep.gather(1, got[:, None]).all()
+    heavy = keep & (z > 30.0)
+    if end == "first":
+        assert (got <= torch.where(heavy, at, V).amin(1)).all()
+    else:
+        assert (got >= torch.where(heavy, at, -1).amax(1)).all()
+        light = keep.any(1) & ((keep & ~heavy & (z.double() > 40.0 - 47.9 * np.log(2.0))).any(1))
+        assert torch.equal(got[light], torch.where(keep, at, -1).amax(1)[light])
