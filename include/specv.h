@@ -85,7 +85,7 @@ typedef enum { SPECV_BF16 = 0, SPECV_FP32 = 1 } specv_dtype;
                                  the row instead of waiting forever (not
                                  expected on a healthy GPU; for tests, the
                                  environment variable SPECV_TEST_STALL="A:<i>"
-                                 or "B:<b>", read once per process, makes one
+                                 to "D:<n>", read once per process, makes one
                                  such wait run out) */
 
 /*

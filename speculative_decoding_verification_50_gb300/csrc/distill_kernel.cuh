@@ -43,6 +43,7 @@ struct DistillParams {
   void* grad;
   int64_t grs;
   int32_t* status;
+  int32_t stall[2];     // test hook: 1 + the row whose first, second pass waits in vain
 };
 
 constexpr float kNoTail = 9.5367431640625e-07f;  // 2^-20: a smaller teacher tail counts as none
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   __shared__ uint64_t ured[kRowWarps];
   __shared__ DistillPart wpart[kRowWarps], part[kMaxCluster];
   __shared__ float2 origin;
-  __shared__ int badbits, again;
+  __shared__ int badbits, again, late;
   __shared__ float row_max, row_ref, row_alpha, row_beta;
   __shared__ int row_dead;
   const int C = P.sp.C, K = P.K, V = P.sp.V;
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   sl.init(smem, bars, P.sp, zrow, rank, warp);
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;
-  if (threadIdx.x == 0) badbits = again = 0;
+  if (threadIdx.x == 0) badbits = again = late = 0;
   const int words = (P.sp.svec * VW + 31) / 32;
   unsigned* bits = reinterpret_cast<unsigned*>(smem + row_bytes(P.sp.rvec, P.sp.stages));
   int32_t* ids = reinterpret_cast<int32_t*>(smem + row_bytes(P.sp.rvec, P.sp.stages) +
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   RunningSum rs;  // over the logits that are not listed
   float zmax = neg_inf();
   if (!skip) {
-    sl.load();
+    sl.load(P.stall[0] == row + 1 && rank == 0 && warp == 0);
     for (int i = threadIdx.x; i < words; i += kRowThreads) bits[i] = 0;
     te = load_teacher<true>(P, row, ids, tl, pj, tred, ured);  // (a barrier: no bits, too)
     bad = te.bad;
@@ -345,8 +346,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
       }
       rs.add(z, top, c);
     });
-    if (!sl.landed) bad |= kTimeout;
-    if (P.grad && sl.stages > 0) sl.prime();  // (the second pass's first copies)
+    if (sl.late) bad |= kTimeout;
+    if (P.grad && sl.stages > 0) sl.prime(P.stall[1] == row + 1 && rank == 0 && warp == 0);  // (the second pass's first copies)
     if (bad) atomicOr(&badbits, bad);
   }
   // Each warp's sums, relative to its own maxima.  The rest keeps one of its
@@ -442,6 +443,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     }
   });
   if (dead) return;
+  if (sl.late) {
+    for (int r = 0; r < C; ++r) *peer(&late, r) = 1;
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+  // (Without release: it would wait for this pass's stores, 3 % of the call.)
+  if (sl.stages > 0 && C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   __syncthreads();  // the listed ids' gradients go over what was just written
   const float b = row_beta;
   const float2 lb = log_pair(b), ln = te.norm(P.tlse != nullptr);
@@ -449,6 +456,17 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     const int id = ids[j];
     if (id < lo || id >= hi || sj[j] < 0.f) continue;
     store_elem<DT>(grow, id, f * listed_grad(P, te, zj[j], tl[j], pj[j] * te.pscale, sj[j], mx, b, lb, ln));
+  }
+  // A copy of this pass that was late, in any CTA: the row has no result.
+  if (sl.stages > 0 && C > 1) cluster_wait();
+  if (!late) return;
+  __syncthreads();
+  for (int j0 = 0; j0 < sl.nv; j0 += 32)
+    store_warp<DT>(grow, sl.index(j0 + lane), V, j0 + lane < sl.nv, make_uint4(0u, 0u, 0u, 0u));
+  if (rank == 0 && threadIdx.x == 0) {
+    P.loss[row] = 0.f;
+    if (P.stats) P.stats[row] = make_float4(__int_as_float(0x7fc00000), 0.f, 0.f, 0.f);
+    if (P.status) P.status[row] = kTimeout;
   }
 }
 

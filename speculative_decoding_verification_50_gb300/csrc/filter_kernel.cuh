@@ -1388,7 +1388,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
     }
   }
   if (!guessed) wm = F.sl.warp_max(own);
-  if (!F.sl.landed && lane == 0) atomicOr(&S.bad, kTimeout);
+  if (F.sl.late) atomicOr(&S.bad, kTimeout);
   const float mc = block_max_nan(wm, S.fscratch);
   push_all(S.xmax, rank, C, mc);
   push_all(S.xbad, rank, C, S.bad);
@@ -1627,7 +1627,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid
   float own[2];
   RunningSum rs;  // (the log-sum-exp's share, in the same pass)
   const float wm = F.sl.warp_max(own, &rs, P.c);
-  if (!F.sl.landed && lane == 0) atomicOr(&S.bad, kTimeout);
+  if (F.sl.late) atomicOr(&S.bad, kTimeout);
   const float mc = block_max_nan(wm, S.fscratch);
   cluster_wait();
   push_all(S.xmax, rank, C, mc);

@@ -162,7 +162,8 @@ struct RowSlice {
   int stage;        // the ring's next stage to be read ...
   uint32_t parity;  // ... and its barrier's phase
   bool primed;      // the next pass's first copies are under way
-  bool landed;      // every copy waited for arrived in time
+  int until;        // vectors that copies bring in a pass: `plain`, until one is late (none is issued from then on)
+  bool late;        // a copy did not land in time
 
   __device__ void init(char* smem, uint64_t* barriers, const RowSplit& sp, const void* row, int rank, int w) {
     lane = threadIdx.x & 31;
@@ -183,7 +184,8 @@ struct RowSlice {
     stage = 0;
     parity = 0;
     primed = false;
-    landed = true;
+    until = plain;
+    late = false;
   }
 
   // Vector j of the segment from memory (-inf after the row's last logit).
@@ -256,29 +258,33 @@ struct RowSlice {
     mbar_arrive_expect_tx(&bars[s], bytes);
     bulk_load(data + s * kStage, src + static_cast<int64_t>(c) * kStage * 16, bytes, &bars[s], false);
   }
-  // (All lanes: what the last pass read has been used by every lane.)
-  __device__ void prime() {
+  // (All lanes: what the last pass read has been used by every lane.)  stall (a
+  // test hook): the first stage waits for 16 bytes that no copy brings.
+  __device__ void prime(bool stall = false) {
     __syncwarp();
-    if (lane == 0)
+    if (lane == 0 && !late) {
+      if (stall) mbar_expect_tx(&bars[stage], 16);
       for (int c = 0; c < stages && c * kStage < plain; ++c) issue(c, (stage + c) % stages);
+    }
     primed = true;
   }
 
   // Starts this warp's copies.  Held rows that start at a 16-byte boundary take
   // one bulk copy.
-  __device__ void load() {
+  __device__ void load(bool stall = false) {
     if (RING && stages > 0) {
       if (lane == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
       }
       __syncwarp();
-      prime();
+      prime(stall);
       return;
     }
     if (lane == 0) {
       mbar_init(bars, 1);
       fence_mbar_init();
+      if (stall) mbar_expect_tx(bars, 16);
       const uint32_t bytes = static_cast<uint32_t>(min(plain, rv)) * 16u;
       mbar_arrive_expect_tx(bars, bytes);
       if (bytes > 0) bulk_load(data, src, bytes, bars, rv == nv);
@@ -296,15 +302,24 @@ struct RowSlice {
     __syncwarp();
   }
 
-  // A bounded wait (about two seconds) for a barrier of the warp's.
-  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase) {
-    if (!mbar_wait_bounded(bar, phase) && !mbar_wait_bounded(bar, phase)) landed = false;
+  // A bounded wait (about two seconds) for copy c of a pass.  After a late one
+  // only those that have been issued are waited for, then nothing.
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, int c) {
+    if (mbar_try_wait(bar, phase)) return;
+    if (late && c * kStage >= until) return;
+    const long long t0 = clock64();
+    for (uint32_t it = 0; it < (1u << 21); ++it) {
+      if (mbar_try_wait_sleep(bar, phase, 20000u)) return;
+      if (clock64() - t0 > 4000000000LL) break;
+    }
+    late = true;
+    until = min(until, (c + stages - (c > 0)) * kStage);
   }
 
   // Before held vectors are read for the first time.
   __device__ void ready() {
     if (!RING || stages == 0) {
-      wait(bars, 0);
+      wait(bars, 0, 0);
       __syncwarp();
     }
   }
@@ -366,14 +381,14 @@ struct RowSlice {
 #pragma unroll 1
     for (int c = 0; j0 < plain; ++c, j0 += kStage) {
       const int j = j0 + lane;
-      wait(&bars[stage], parity);
+      wait(&bars[stage], parity, c);
       const Vec* at = data + stage * kStage + lane;
       Vec x[2] = {at[0], at[32]};
       // Every lane has been through f for the chunk before, so its reads of that
       // stage have ended and it can be filled again.  (Not this chunk's stage:
       // its reads are only under way.  Filled here, a copy from L2 overtook them.)
       __syncwarp();
-      if (lane == 0 && c > 0 && (c - 1 + stages) * kStage < plain)
+      if (lane == 0 && c > 0 && (c - 1 + stages) * kStage < until)
         issue(c - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
       if (++stage == stages) {
         stage = 0;
@@ -385,6 +400,7 @@ struct RowSlice {
       }
       f(x, j);
     }
+    if (late) until = 0;
 #pragma unroll 1
     for (; j0 < nv; j0 += kStage) {
       Vec x[2];

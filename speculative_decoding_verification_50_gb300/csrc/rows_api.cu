@@ -292,6 +292,8 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   if (static_cast<int64_t>(a->N) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   p.loss = a->loss;
   p.status = a->row_status;
+  p.stall[0] = api_test_stall('C');
+  p.stall[1] = api_test_stall('D');
   return launched(launch_distill(a->dtype, smem, static_cast<cudaStream_t>(stream), p), "distill");
 }
 

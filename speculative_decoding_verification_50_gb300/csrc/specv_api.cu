@@ -278,7 +278,8 @@ bool persistent_path() {
 // Test hook, off unless SPECV_TEST_STALL is set: "A:<i>" makes the first
 // ring stage of row-statistics item i (staged path) wait for 16 bytes that no
 // copy brings, "B:<b>" the first residual stage of batch row b in the decision
-// kernel; the bounded wait then runs out (about a second) and the row comes
+// kernel, "C:<n>" and "D:<n>" the first copy of the first and of the second pass
+// over row n in the distillation kernel; the bounded wait then runs out (about a second) and the row comes
 // back flagged SPECV_ROW_DEVICE_TIMEOUT.  Returns 1 + that index for kernel
 // `which`, else 0.
 int test_stall(char which) {
@@ -288,11 +289,17 @@ int test_stall(char which) {
   };
   static const Stall st = [] {
     const char* e = getenv("SPECV_TEST_STALL");
-    if (e && (e[0] == 'A' || e[0] == 'B') && e[1] == ':') return Stall{e[0], atoi(e + 2)};
+    if (e && e[0] >= 'A' && e[0] <= 'D' && e[1] == ':') return Stall{e[0], atoi(e + 2)};
     return Stall{0, -1};
   }();
   return (st.v >= 0 && st.k == which) ? st.v + 1 : 0;
 }
+
+}  // namespace
+
+int specv::api_test_stall(char which) { return test_stall(which); }
+
+namespace {
 
 // Checks shared by specv_verify and specv_ssd_round.
 specv_status check_verify_args(const specv_verify_args* a, int draft_rows) {
