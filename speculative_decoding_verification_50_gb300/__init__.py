@@ -492,27 +492,48 @@ def _on_gpu(t) -> bool:
     return t.is_cuda
 
 
-def _of(t, shape, dtype, what):
-    """t's pointer after a check of its type, shape, layout and place (None: optional)."""
+def _of(t, shape, dtype, what, at):
+    """t's pointer after a check of its type, shape, layout and place: device `at`, the
+    logits', which _cuda holds to be a GPU (None: optional)."""
     if t is None:
         return None
-    assert t.shape == shape and t.dtype is dtype and t.is_contiguous() and _on_gpu(t), (
-        f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous {dtype} {tuple(shape)} on a GPU")
+    assert t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == at, (
+        f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous {dtype} {tuple(shape)} "
+        f"on the logits' GPU ({at})")
     return t.data_ptr()
 
 
-def _raw_stream(stream, device):
-    """The stream's handle (the device's current stream by default; asked for
+def _raw_stream(stream, at):
+    """The stream's handle (the current stream of device `at` by default; asked for
     directly, since a decode step makes many small calls)."""
     import torch
     if stream is not None:
+        its = getattr(stream, "device_index", at)
+        assert its == at, f"a stream of GPU {its} for tensors on GPU {at}"
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(at)
 
 
-def _cuda(t, what):
+def _current_device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+def _launch(fn, args, stream, at):
+    """The entry point fn on device `at`, where its operands lie: a kernel goes to
+    the current device, whatever device its stream or its pointers are of."""
+    if at < 0 or at == _current_device():
+        _check(fn(ctypes.byref(args), _raw_stream(stream, at)))
+        return
+    import torch
+    with torch.cuda.device(at):
+        _check(fn(ctypes.byref(args), _raw_stream(stream, at)))
+
+
+def _cuda(t, what, at=None):
     assert _on_gpu(t) and (t.stride(-1) == 1 or t.shape[-1] == 1), (
         f"{what} must be a CUDA tensor with a contiguous last dimension")
+    assert at is None or t.get_device() == at, f"{what} on {t.device}, the logits on GPU {at}"
 
 
 def _stride(t, dim, width):
@@ -530,10 +551,11 @@ def _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, pro
     assert flat or len(shape) == 3, "logits must be [B, V] or [B, R, V]"
     B, R = lead[0], 1 if flat else lead[1]
     f32, i32, dev = torch.float32, torch.int32, logits.device
+    at = logits.get_device()
     per = (B,)
-    T = _of(temperature, per, f32, "temperature")
-    k, p, m = _of(top_k, per, i32, "top_k"), _of(top_p, per, f32, "top_p"), _of(min_p, per, f32, "min_p")
-    u = _of(uniforms, lead, f32, "uniforms")
+    T = _of(temperature, per, f32, "temperature", at)
+    k, p = _of(top_k, per, i32, "top_k", at), _of(top_p, per, f32, "top_p", at)
+    m, u = _of(min_p, per, f32, "min_p", at), _of(uniforms, lead, f32, "uniforms", at)
     out = {}
     if uniforms is not None:
         out["tokens"] = tokens = torch.empty(lead, dtype=i32, device=dev) if tokens is None else tokens
@@ -546,15 +568,15 @@ def _sample_call(logits, temperature, uniforms, top_k, top_p, min_p, tokens, pro
     fptr, fbs, frs = None, 0, 0
     if filtered is not None:
         assert filtered.shape == shape and filtered.dtype is logits.dtype, "filtered must be like logits"
-        _cuda(filtered, "filtered")
+        _cuda(filtered, "filtered", at)
         fptr = filtered.data_ptr()
         fbs, frs = _stride(filtered, 0, V), V if flat else _stride(filtered, 1, V)
         out["filtered"] = filtered
     args = SampleArgs(B, R, V, code, logits.data_ptr(), bs, rs, T, k, p, m, u,
-                      _of(tokens, lead, i32, "tokens"), _of(prob, lead, f32, "prob"),
-                      _of(kept, lead, i32, "kept"), fptr, fbs, frs,
-                      _of(row_status, lead, i32, "row_status"))
-    _check(load_library().specv_sample(ctypes.byref(args), _raw_stream(stream, dev)))
+                      _of(tokens, lead, i32, "tokens", at), _of(prob, lead, f32, "prob", at),
+                      _of(kept, lead, i32, "kept", at), fptr, fbs, frs,
+                      _of(row_status, lead, i32, "row_status", at))
+    _launch(load_library().specv_sample, args, stream, at)
     return out
 
 
@@ -601,17 +623,17 @@ def specv_top_logits(logits, k: int, *, temperature: float = 1.0, ids=None, valu
     code = _dtype_code(logits)
     B, V = logits.shape
     f32, i32, dev = torch.float32, torch.int32, logits.device
-    rows = max(int(k), 0)
+    at, rows = logits.get_device(), max(int(k), 0)
     ids = torch.empty((B, rows), dtype=i32, device=dev) if ids is None else ids
     values = torch.empty((B, rows), dtype=f32, device=dev) if values is None else values
     lse = torch.empty(B, dtype=f32, device=dev) if lse is None else lse
     row_status = torch.empty(B, dtype=i32, device=dev) if row_status is None else row_status
     _cuda(logits, "logits")
     args = TopArgs(B, V, int(k), code, logits.data_ptr(), _stride(logits, 0, V),
-                   float(temperature), _of(ids, (B, rows), i32, "ids"),
-                   _of(values, (B, rows), f32, "values"), _of(lse, (B,), f32, "lse"),
-                   _of(row_status, (B,), i32, "row_status"))
-    _check(load_library().specv_top_logits(ctypes.byref(args), _raw_stream(stream, dev)))
+                   float(temperature), _of(ids, (B, rows), i32, "ids", at),
+                   _of(values, (B, rows), f32, "values", at), _of(lse, (B,), f32, "lse", at),
+                   _of(row_status, (B,), i32, "row_status", at))
+    _launch(load_library().specv_top_logits, args, stream, at)
     return dict(ids=ids, values=values, lse=lse, row_status=row_status)
 
 
@@ -621,20 +643,20 @@ def _distill_args(logits, ids, values, teacher_lse, weights, temperature, tail, 
     code = _dtype_code(logits)
     N, V = logits.shape
     K = ids.shape[1]
-    f32 = torch.float32
+    f32, at = torch.float32, logits.get_device()
     assert ids.shape == values.shape == (N, K) and ids.dtype == torch.int32 and values.dtype == f32
-    _cuda(ids, "teacher_ids")
-    _cuda(values, "teacher_logits")
+    _cuda(ids, "teacher_ids", at)
+    _cuda(values, "teacher_logits", at)
     ts = _stride(ids, 0, K)
     assert N <= 1 or ids.stride(0) == values.stride(0), "teacher_ids and teacher_logits share one row stride"
     _cuda(logits, "logits")
     if grad is not None:
         assert grad.shape == logits.shape and grad.dtype == logits.dtype, "grad must be like logits"
-        _cuda(grad, "grad")
+        _cuda(grad, "grad", at)
     return DistillArgs(N, V, K, code, logits.data_ptr(), _stride(logits, 0, V),
                        ids.data_ptr(), values.data_ptr(), ts,
-                       _of(teacher_lse, (N,), f32, "teacher_lse"),
-                       _of(weights, (N,), f32, "weights"), float(temperature),
+                       _of(teacher_lse, (N,), f32, "teacher_lse", at),
+                       _of(weights, (N,), f32, "weights", at), float(temperature),
                        SPECV_DISTILL_TAIL if tail else 0, None, None, None,
                        None if grad is None else grad.data_ptr(),
                        0 if grad is None else _stride(grad, 0, V), None)
@@ -655,7 +677,7 @@ def specv_distill(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temp
     a buffer is given.
     """
     import torch
-    N, dev = logits.shape[0], logits.device
+    N, dev, at = logits.shape[0], logits.device, logits.get_device()
     if grad is None and with_grad:
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     loss = torch.empty(N, dtype=torch.float32, device=dev) if loss is None else loss
@@ -663,10 +685,10 @@ def specv_distill(logits, teacher_ids, teacher_logits, *, teacher_lse=None, temp
     row_status = torch.empty(N, dtype=torch.int32, device=dev) if row_status is None else row_status
     args = _distill_args(logits, teacher_ids, teacher_logits, teacher_lse, weights, temperature,
                          tail, grad)
-    args.loss = _of(loss, (N,), torch.float32, "loss")
-    args.stats = _of(stats, (N, 4), torch.float32, "stats")
-    args.row_status = _of(row_status, (N,), torch.int32, "row_status")
-    _check(load_library().specv_distill(ctypes.byref(args), _raw_stream(stream, dev)))
+    args.loss = _of(loss, (N,), torch.float32, "loss", at)
+    args.stats = _of(stats, (N, 4), torch.float32, "stats", at)
+    args.row_status = _of(row_status, (N,), torch.int32, "row_status", at)
+    _launch(load_library().specv_distill, args, stream, at)
     out = dict(loss=loss, stats=stats, row_status=row_status)
     if grad is not None:
         out["grad"] = grad
@@ -679,14 +701,14 @@ def specv_distill_backward(logits, teacher_ids, teacher_logits, stats, *, grad_l
     """The gradient of (grad_loss * loss).sum() with respect to logits, from
     the stats of specv_distill on the same inputs (see include/specv.h)."""
     import torch
-    N = logits.shape[0]
+    N, at = logits.shape[0], logits.get_device()
     if grad is None:
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     args = _distill_args(logits, teacher_ids, teacher_logits, teacher_lse, weights, temperature,
                          tail, grad)
-    args.stats = _of(stats, (N, 4), torch.float32, "stats")
-    args.grad_loss = _of(grad_loss, (N,), torch.float32, "grad_loss")
-    _check(load_library().specv_distill_backward(ctypes.byref(args), _raw_stream(stream, logits.device)))
+    args.stats = _of(stats, (N, 4), torch.float32, "stats", at)
+    args.grad_loss = _of(grad_loss, (N,), torch.float32, "grad_loss", at)
+    _launch(load_library().specv_distill_backward, args, stream, at)
     return grad
 
 
