@@ -243,6 +243,15 @@ specv_status check_distill(const specv_distill_args* a) {
   return SPECV_OK;
 }
 
+// The split of rows that are held, and with it the widest row that is taken.
+// (a held row's bits are at most a 16th of its bytes)
+bool split_distill(const specv_distill_args* a, RowSplit& sp, size_t& smem) {
+  const int vw = 16 / elem_bytes(a->dtype);
+  const size_t entries = static_cast<size_t>(a->K) * 20;
+  const size_t bits = distill_bytes(static_cast<int32_t>((static_cast<int64_t>(a->V) + vw - 1) / vw), vw, 0);
+  return split_row(a->N, a->V, a->dtype, kDistillStatic + std::min<size_t>(bits, 16384) + entries, sp, smem);
+}
+
 DistillParams distill_params(const specv_distill_args* a) {
   DistillParams p = {};
   p.N = a->N;
@@ -280,9 +289,7 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   DistillParams p = distill_params(a);
   size_t smem;
   const int vw = 16 / elem_bytes(a->dtype);
-  // (a held row's bits are at most a 16th of its bytes)
-  const size_t bits = distill_bytes((a->V + vw - 1) / vw, vw, a->K);
-  if (!split_row(a->N, a->V, a->dtype, kDistillStatic + std::min<size_t>(bits, 16384 + static_cast<size_t>(a->K) * 20), p.sp, smem))
+  if (!split_distill(a, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
   // (With a gradient the rows are read again: left to L2 1024 x 152064 fp32 take 287
   // us, by one CTA each 315; 300 rows 92, 109.)
@@ -303,6 +310,10 @@ specv_status specv_distill_backward(const specv_distill_args* a, void* stream) {
   if (st != SPECV_OK) return st;
   if (a->N == 0) return api_done(0);
   if (!a->stats || !a->grad) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  RowSplit held;
+  size_t smem;
+  if (!split_distill(a, held, smem))  // (no statistics come of such rows, and the kernel's indices hold no others)
+    return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
   if (static_cast<int64_t>(a->N) * ((a->V + 6) / back_piece(16 / elem_bytes(a->dtype)) + 1) > 0x7fffffffLL)
     return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");
   DistillParams p = distill_params(a);
