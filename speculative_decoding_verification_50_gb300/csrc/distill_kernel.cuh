@@ -11,8 +11,9 @@
 // them (they may all lie 100 / T and more below the listed ones, where exp(z - max)
 // underflows but neither log(1 - s) nor q / (1 - s) does), and beta q - p is taken
 // as p (exp(log(beta q / p)) - 1), so neither cancels where the student comes
-// close to its teacher.  The logarithms at listed ids are pairs of fp32 (z / T has
-// thousands of units at low temperatures), computed alike by both kernels.
+// close to its teacher.  The logarithms that the loss and the listed ids' gradients
+// are differences of are pairs of fp32 (z / T has thousands of units at low
+// temperatures; a loss of 0.01 lies in the last bits of its terms).
 //
 // All of it in fp32, differences taken before they are scaled; sums of p are
 // exact in units of 2^-40.  (An SM does two fp64 operations a clock: a few of
@@ -20,6 +21,7 @@
 #pragma once
 
 #include "row_common.cuh"
+#include "specv_device.cuh"  // FF
 
 namespace specv {
 
@@ -57,10 +59,42 @@ __device__ __forceinline__ float exp_over(float d, float ih, float il) {
   return x > -100.f ? expf(x) * (1.f + e) : 0.f;
 }
 
-// log(x) as hi + lo: one Newton step on the rounded logarithm.
-__device__ __forceinline__ float2 log_pair(float x) {
-  const float hi = logf(x);
-  return make_float2(hi, x > 0.f && x < 1e30f ? fmaf(x, expf(-hi), -1.f) : 0.f);
+// The loss is a small difference of logarithms: the few numbers of a row that it
+// depends on are pairs of fp32 (FF).
+// Sums of a few terms: the low parts gather what the high parts lose, without
+// carries (a chain of ff_add takes three times as long).
+__device__ __forceinline__ FF ff_gather(FF x, FF y) {
+  const FF v = two_sum(x.hi, y.hi);
+  return FF{v.hi, (x.lo + y.lo) + v.lo};
+}
+__device__ __forceinline__ FF ff_times(FF x, float y) {
+  const float p = __fmul_rn(x.hi, y);
+  return FF{p, fmaf(x.lo, y, fmaf(x.hi, y, -p))};
+}
+
+constexpr float kLn2 = 0.693147182464599609375f, kLn2Rest = -1.904654e-9f;
+
+// log(x): the exponent's part as a pair, the mantissa's (0.7 to 1.4) to 2^-25.
+__device__ __forceinline__ FF log_pair(float x) {
+  if (!(x >= 1.17549435e-38f && x < pos_inf())) return ff(logf(x));
+  const int e = (__float_as_int(x) - 0x3f350000) >> 23;
+  const float k = static_cast<float>(e);
+  const FF m = ff_mul(k, kLn2);
+  return ff_gather(FF{m.hi, fmaf(k, kLn2Rest, m.lo)}, ff(logf(__int_as_float(__float_as_int(x) - (e << 23)))));
+}
+
+// exp(x) for x <= 0 (0 below -87): x = k ln 2 + f, and f's series to the 7th power,
+// good to about 2^-27.
+__device__ __forceinline__ FF exp_pair(FF x) {
+  if (!(x.hi > -87.f)) return ff(0.f);
+  const float k = rintf(x.hi * 1.44269504f);
+  const float f = fmaf(-k, kLn2, x.hi), rest = x.lo - k * kLn2Rest;
+  const float q = f * f *
+      fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.f / 5040, 1.f / 720), 1.f / 120), 1.f / 24), 1.f / 6), 0.5f);
+  const FF one = two_sum(1.f, f);
+  const float lo = one.lo + q, scale = __int_as_float((static_cast<int>(k) + 127) << 23);
+  const FF v = two_sum(one.hi, fmaf(one.hi + lo, rest, lo));
+  return FF{v.hi * scale, v.lo * scale};
 }
 
 __device__ __forceinline__ float warp_max_nan(float x) {
@@ -80,12 +114,11 @@ __device__ __forceinline__ float block_max_nan(float x, float* scratch) {
   return m;
 }
 
-// (a - b) / T as hi + lo, to about 2^-45 of it (infinite: as hi alone).
-__device__ __forceinline__ float2 over(float a, float b, float ih, float il) {
-  const float d = a - b, bb = d - a;
-  const float e = (a - (d - bb)) - (b + bb);  // what the difference lost
-  const float hi = __fmul_rn(d, ih);
-  return make_float2(hi, fabsf(hi) < 1e30f ? fmaf(e, ih, fmaf(d, il, fmaf(d, ih, -hi))) : 0.f);
+// (a - b) / T, to about 2^-45 of it (infinite: as hi alone).
+__device__ __forceinline__ FF over(float a, float b, float ih, float il) {
+  const FF d = two_sum(a, -b);
+  const float hi = __fmul_rn(d.hi, ih);
+  return FF{hi, fabsf(hi) < 1e30f ? fmaf(d.lo, ih, fmaf(d.hi, il, fmaf(d.hi, ih, -hi))) : 0.f};
 }
 
 // What a CTA knows of a row's teacher.
@@ -97,8 +130,14 @@ struct Teacher {
   int bad;         // this thread's findings
 
   __device__ __forceinline__ float sum() const { return static_cast<float>(mass) * (1.f / kFixed); }
+  // sum of p_j
+  __device__ __forceinline__ FF total(bool given) const {
+    if (!given) return ff(mass ? 1.f : 0.f);
+    const float hi = static_cast<float>(mass);
+    return FF{hi * (1.f / kFixed), static_cast<float>(static_cast<int64_t>(mass) - static_cast<int64_t>(hi)) * (1.f / kFixed)};
+  }
   // log p_j less t_j / T (tmax / T without a log-sum-exp), as a pair, negated
-  __device__ __forceinline__ float2 norm(bool given) const { return given ? make_float2(L, 0.f) : log_pair(sum()); }
+  __device__ __forceinline__ FF norm(bool given) const { return given ? ff(L) : log_pair(sum()); }
 };
 
 // The row's entries into shared memory (ids, -1 where absent; logits, -inf
@@ -162,12 +201,14 @@ __device__ Teacher load_teacher(const DistillParams& P, int64_t row, int32_t* id
 // sum of p over its entries, b = beta / sum, lb its logarithm, ln the entries'
 // normaliser.  Like sizes of the two logarithms are taken apart first.
 __device__ __forceinline__ float listed_grad(const DistillParams& P, const Teacher& te, float z, float t, float p,
-                                             float ps, float mx, float b, float2 lb, float2 ln) {
-  const float2 q = over(z, mx, P.ih, P.il);  // log(beta q) less lb
-  const float bq = q.x > -100.f ? b * (expf(q.x) * (1.f + q.y)) : 0.f;
+                                             float ps, float mx, float b, FF lb, FF ln) {
+  const FF q = over(z, mx, P.ih, P.il);  // log(beta q) less lb
+  const float bq = q.hi > -100.f ? b * (expf(q.hi) * (1.f + q.lo)) : 0.f;
   if (!(p > 0.f && ps == p)) return bq - ps;
-  const float2 o = over(t, P.tlse ? 0.f : te.tmax, P.ih, P.il);
-  const float x = ((q.x - (o.x - ln.x)) + lb.x) + ((q.y - o.y) + (ln.y + lb.y));
+  if (!(q.hi > -1e30f)) return -p;
+  const FF o = over(t, P.tlse ? 0.f : te.tmax, P.ih, P.il);
+  const FF d = ff_gather(ff_gather(q, ff_neg(o)), ff_gather(ln, lb));
+  const float x = d.hi + d.lo;
   return x < 1.f ? p * expm1f(x) : bq - p;
 }
 
@@ -187,23 +228,31 @@ __device__ __forceinline__ float same_id(const int32_t* ids, const float* p, int
   return warp_sum_f(s);
 }
 
-struct DistillPart {  // one CTA's share of a row
-  float mr, ml;        // the largest logit that is not listed, and that is
-  float rest, listed;  // sums relative to them
-  float a;
+struct DistillPart {  // a warp's or a CTA's share of a row
+  float mr, ml;                // the largest logit that is not listed, and that is
+  FF rest, listed;             // sums relative to them
+  FF a;
   int32_t bad;
 };
+constexpr int kRuledOut = 1 << 30;  // among the bad bits: a listed token has mass and no probability
 
-// The sum of n <= 32 parts, by a whole warp.
+// The sum of n <= 16 parts, by a whole warp.
 __device__ __forceinline__ DistillPart join(const DistillPart* p, int n, float c) {
   const int lane = threadIdx.x & 31;
-  DistillPart t = {neg_inf(), neg_inf(), 0.f, 0.f, 0.f, 0};
+  DistillPart t = {neg_inf(), neg_inf(), ff(0.f), ff(0.f), ff(0.f), 0};
   if (lane < n) t = p[lane];
   const float mr = warp_max_nan(t.mr), ml = warp_max_nan(t.ml);
-  t.rest = warp_sum_f(t.rest > 0.f ? ex2((t.mr - mr) * c) * t.rest : 0.f);
-  t.listed = warp_sum_f(t.listed > 0.f ? ex2((t.ml - ml) * c) * t.listed : 0.f);
-  t.a = warp_sum_f(t.a);
+  t.rest = t.rest.hi > 0.f ? ff_mul(t.rest, ex2((t.mr - mr) * c)) : ff(0.f);
+  t.listed = t.listed.hi > 0.f ? ff_mul(t.listed, ex2((t.ml - ml) * c)) : ff(0.f);
   t.bad = __reduce_or_sync(0xffffffffu, t.bad);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    t.rest = ff_gather(t.rest, shfl_xor(t.rest, o));
+    t.listed = ff_gather(t.listed, shfl_xor(t.listed, o));
+    t.a = ff_gather(t.a, shfl_xor(t.a, o));
+  }
+  t.rest = fast_two_sum(t.rest.hi, t.rest.lo);
+  t.listed = fast_two_sum(t.listed.hi, t.listed.lo);
   t.mr = mr;
   t.ml = ml;
   return t;
@@ -255,7 +304,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   __shared__ uint64_t ured[kRowWarps];
   __shared__ DistillPart wpart[kRowWarps], part[kMaxCluster];
   __shared__ float2 origin;
-  __shared__ int badbits, again, late;
+  __shared__ int again, late;
   __shared__ float row_max, row_ref, row_alpha, row_beta;
   __shared__ int row_dead;
   const int C = P.sp.C, K = P.K, V = P.sp.V;
@@ -269,7 +318,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   sl.init(smem, bars, P.sp, zrow, rank, warp);
   const float wt = P.weight ? P.weight[row] : 1.f;
   const bool skip = wt == 0.f;
-  if (threadIdx.x == 0) badbits = again = late = 0;
+  if (threadIdx.x == 0) again = late = 0;
   const int words = (P.sp.svec * VW + 31) / 32;
   unsigned* bits = reinterpret_cast<unsigned*>(smem + row_bytes(P.sp.rvec, P.sp.stages));
   int32_t* ids = reinterpret_cast<int32_t*>(smem + row_bytes(P.sp.rvec, P.sp.stages) +
@@ -348,7 +397,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     });
     if (sl.late) bad |= kTimeout;
     if (P.grad && sl.stages > 0) sl.prime(P.stall[1] == row + 1 && rank == 0 && warp == 0);  // (the second pass's first copies)
-    if (bad) atomicOr(&badbits, bad);
   }
   // Each warp's sums, relative to its own maxima.  The rest keeps one of its
   // own: a student may put e^-100 and less of its mass outside the list.
@@ -360,72 +408,90 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
       if (ids[j] < lo || ids[j] >= hi) continue;
       const float p = pj[j] * te.pscale, z = zj[j];
       if (sj[j] >= 0.f) listed += ex2((z - mref) * c);
-      if (p > 0.f) a += p * (((tl[j] - origin.x) - (z - origin.y)) * ih);
+      const float lead = ((tl[j] - origin.x) - (z - origin.y)) * ih;
+      if (p > 0.f && lead < pos_inf()) a += p * lead;
+      else if (p > 0.f) bad |= kRuledOut;
     }
   }
   listed = warp_sum_f(listed);
   const float rest = warp_sum_f(rs.at(mr, c));
   a = warp_sum_f(a);
+  bad = __reduce_or_sync(0xffffffffu, bad);
   if (lane == 0) {
-    DistillPart mine = {mr, ml, rest, listed, a, 0};
+    DistillPart mine = {mr, ml, ff(rest), ff(listed), ff(a), bad};
     wpart[warp] = mine;
   }
   __syncthreads();
   cluster_wait();
-  if (warp == 0) {
-    DistillPart mine = join(wpart, kRowWarps, c);
-    mine.bad = badbits;
-    if (lane < C) *peer(part + rank, lane) = mine;
-  }
-  if (C == 1) __syncthreads();
-  else cluster_sync();
-
   DistillPart all;
-  if (warp == 0) all = join(part, C, c);
-  if (threadIdx.x == 0) {  // the row's scalars
-    const int anybad = all.bad;
+  if (warp == 0) {
+    all = join(wpart, kRowWarps, c);
+    if (C > 1 && lane < C) *peer(part + rank, lane) = all;
+  }
+  if (C > 1) {
+    cluster_sync();
+    if (warp == 0) all = join(part, C, c);
+  }
+  // The row's scalars, by a warp (a lane each for what takes longest).
+  FF gap, total;  // log of the rest's largest weight; the row's sum
+  float r = 0.f;
+  bool dead = false, has_rest = false;
+  if (warp == 0) {
     const float ur = all.mr, mx = max_nan(all.mr, all.ml);
-    const bool finite = mx > neg_inf() && mx < pos_inf();
-    const float S_rest = all.rest, S_listed = all.listed > 0.f ? ex2((all.ml - mx) * c) * all.listed : 0.f;
-    const bool dead = skip || anybad || !finite;
-    const float2 gap = over(ur, mx, ih, P.il);  // log of the rest's largest weight
-    const float far = gap.x > -100.f ? expf(gap.x) * (1.f + gap.y) : 0.f;
-    const float total = far * S_rest + S_listed, inv = 1.f / total;
-    const float m = P.tlse ? te.sum() : (te.mass ? 1.f : 0.f);
-    float r = P.tail ? static_cast<float>((1ll << 40) - static_cast<int64_t>(te.mass)) * (1.f / kFixed) : 0.f;
+    dead = skip || (all.bad & ~kRuledOut) || !(mx > neg_inf() && mx < pos_inf());
+    gap = over(ur, mx, ih, P.il);
+    auto times = [](FF x, FF y) { return ff_gather(ff_times(x, y.hi), ff(x.hi * y.lo)); };
+    const FF e = exp_pair(lane == 0 ? gap : over(all.ml, mx, ih, P.il));
+    const FF far = shfl(e, 0), near = shfl(e, 1);
+    // all.rest is relative to ur, `total` to mx
+    const FF listed_sum = all.listed.hi > 0.f ? times(all.listed, near) : ff(0.f);
+    total = ff_gather(listed_sum, all.rest.hi > 0.f ? times(all.rest, far) : ff(0.f));
+    total = fast_two_sum(total.hi, total.lo);
+    const float inv = 1.f / total.hi;
+    const float m = te.total(P.tlse != nullptr).hi;
+    if (P.tail) r = static_cast<float>((1ll << 40) - static_cast<int64_t>(te.mass)) * (1.f / kFixed);
     if (r < kNoTail) r = 0.f;
-    // alpha q_v = m q_v - r s share_v, share_v = exp((z_v - ur) / T) / S_rest.
+    // alpha q_v = m q_v - r s share_v, share_v = exp((z_v - ur) / T) / all.rest.
     // (A rest of the type's lowest values below others is masked: no mass.)
     float beta = m, ref = mx, alpha = m * inv;
-    const bool has_rest = S_rest > 0.f && (far > 0.f || ur > E::lowest());
+    has_rest = all.rest.hi > 0.f && (far.hi > 0.f || ur > E::lowest());
     if (r > 0.f && has_rest) {
       beta = m + r;  // (alpha + r / (1 - s), whose two large terms cancel)
       ref = ur;
-      alpha = m * (far * inv) - r * (S_listed * inv) / S_rest;
+      alpha = m * (far.hi * inv) - r * (listed_sum.hi * inv) / all.rest.hi;
     }
-    const float2 lt = log_pair(total);
-    // d = log p - log q at the origin (differences of like sizes first)
-    const float2 g = over(mx, origin.y, ih, P.il), o = over(origin.x, P.tlse ? 0.f : te.tmax, ih, P.il);
-    const float2 ln = te.norm(P.tlse != nullptr);
-    const float d = te.mass || P.tlse ? ((g.x + (o.x - ln.x)) + lt.x) + ((g.y + (o.y - ln.y)) + lt.y) : 0.f;
-    row_dead = dead;
-    row_max = mx;
-    row_ref = ref;
-    row_alpha = alpha;
-    row_beta = beta * inv;
-    if (rank == 0) {
-      float loss = all.a + m * d;
-      if (r > 0.f) loss += has_rest ? r * (logf(r * total / S_rest) - gap.x) : pos_inf();
-      P.loss[row] = dead ? 0.f : wt * loss;
-      if (P.stats)
-        P.stats[row] = dead ? make_float4(__int_as_float(0x7fc00000), 0.f, 0.f, 0.f)
-                            : make_float4(ref, alpha, mx, row_beta);
-      if (P.status) P.status[row] = skip ? 0 : (anybad | (finite ? 0 : kNonFinite));
+    beta *= inv;
+    if (lane == 0) {
+      row_dead = dead;
+      row_max = mx;
+      row_ref = ref;
+      row_alpha = alpha;
+      row_beta = beta;
+      if (rank == 0) {
+        if (P.stats)
+          P.stats[row] = dead ? make_float4(__int_as_float(0x7fc00000), 0.f, 0.f, 0.f) : make_float4(ref, alpha, mx, beta);
+        if (P.status) P.status[row] = skip || !dead ? 0 : (all.bad & ~kRuledOut) | (mx > neg_inf() && mx < pos_inf() ? 0 : kNonFinite);
+      }
     }
   }
+  if (P.grad) __syncthreads();
+  if (warp == 0 && rank == 0) {  // the loss, while the others start on the gradient
+    FF l = log_pair(lane == 0 ? total.hi : lane == 1 ? all.rest.hi : lane == 2 ? r : te.sum());
+    if (lane < 2) l.lo += lane == 0 ? total.lo / total.hi : all.rest.lo / all.rest.hi;
+    const FF lt = shfl(l, 0), lrest = shfl(l, 1), lr = shfl(l, 2), ln = P.tlse ? ff(te.L) : shfl(l, 3);
+    FF loss = ff(0.f);
+    if (te.mass) {  // log p - log q at the origin, times m
+      const FF g = over(max_nan(all.mr, all.ml), origin.y, ih, P.il), o = over(origin.x, P.tlse ? 0.f : te.tmax, ih, P.il);
+      const FF d = ff_gather(ff_gather(g, lt), ff_gather(o, ff_neg(ln))), m = te.total(P.tlse != nullptr);
+      loss = ff_gather(all.a, ff_gather(ff_times(d, m.hi), ff(d.hi * m.lo)));
+    }
+    if (r > 0.f && has_rest)
+      loss = ff_gather(loss, ff_times(ff_gather(ff_gather(lt, ff_neg(gap)), ff_gather(lr, ff_neg(lrest))), r));
+    const bool infinite = (all.bad & kRuledOut) || (r > 0.f && !has_rest);
+    if (lane == 0) P.loss[row] = dead ? 0.f : wt * (infinite ? pos_inf() : loss.hi + loss.lo);
+  }
   if (!P.grad) return;
-  __syncthreads();
-  const bool dead = row_dead;
+  dead = row_dead;
   const float mx = row_max, ref = row_ref;
   const float f = wt * ih;
   const float ga = f * row_alpha;
@@ -451,7 +517,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   if (sl.stages > 0 && C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   __syncthreads();  // the listed ids' gradients go over what was just written
   const float b = row_beta;
-  const float2 lb = log_pair(b), ln = te.norm(P.tlse != nullptr);
+  const FF lb = log_pair(b), ln = te.norm(P.tlse != nullptr);
   for (int j = threadIdx.x; j < K; j += kRowThreads) {
     const int id = ids[j];
     if (id < lo || id >= hi || sj[j] < 0.f) continue;
@@ -546,7 +612,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_backward_kernel(const 
   }
   if (dead) return;
   __syncthreads();  // the listed ids' gradients go over what was just written
-  const float2 lb = log_pair(st.w), ln = te.norm(P.tlse != nullptr);
+  const FF lb = log_pair(st.w), ln = te.norm(P.tlse != nullptr);
   // Each warp gathers its entries of this piece, then takes them a lane each.
   int own = -1, held = 0;
   float own_ps = 0.f;

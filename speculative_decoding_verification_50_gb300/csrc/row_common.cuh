@@ -252,11 +252,11 @@ struct RowSlice {
     return x.v;
   }
 
-  // Lane 0: chunk c of the segment into stage s of the ring.
-  __device__ __forceinline__ void issue(int c, int s) const {
-    const uint32_t bytes = static_cast<uint32_t>(min(kStage, plain - c * kStage)) * 16u;
+  // Lane 0: the segment's vectors from v on into stage s of the ring.
+  __device__ __forceinline__ void issue(int v, int s) const {
+    const uint32_t bytes = static_cast<uint32_t>(min(kStage, plain - v)) * 16u;
     mbar_arrive_expect_tx(&bars[s], bytes);
-    bulk_load(data + s * kStage, src + static_cast<int64_t>(c) * kStage * 16, bytes, &bars[s], false);
+    bulk_load(data + s * kStage, src + static_cast<int64_t>(v) * 16, bytes, &bars[s], false);
   }
   // (All lanes: what the last pass read has been used by every lane.)  stall (a
   // test hook): the first stage waits for 16 bytes that no copy brings.
@@ -264,7 +264,7 @@ struct RowSlice {
     __syncwarp();
     if (lane == 0 && !late) {
       if (stall) mbar_expect_tx(&bars[stage], 16);
-      for (int c = 0; c < stages && c * kStage < plain; ++c) issue(c, (stage + c) % stages);
+      for (int c = 0; c < stages && c * kStage < plain; ++c) issue(c * kStage, (stage + c) % stages);
     }
     primed = true;
   }
@@ -302,18 +302,18 @@ struct RowSlice {
     __syncwarp();
   }
 
-  // A bounded wait (about two seconds) for copy c of a pass.  After a late one
-  // only those that have been issued are waited for, then nothing.
-  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, int c) {
+  // A bounded wait (about two seconds) for a pass's copy of the vectors from v on.
+  // After a late one only those that have been issued are waited for, then nothing.
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, int v) {
     if (mbar_try_wait(bar, phase)) return;
-    if (late && c * kStage >= until) return;
+    if (late && v >= until) return;
     const long long t0 = clock64();
     for (uint32_t it = 0; it < (1u << 21); ++it) {
       if (mbar_try_wait_sleep(bar, phase, 20000u)) return;
       if (clock64() - t0 > 4000000000LL) break;
     }
     late = true;
-    until = min(until, (c + stages - (c > 0)) * kStage);
+    until = min(until, v + (stages - (v > 0)) * kStage);
   }
 
   // Before held vectors are read for the first time.
@@ -379,17 +379,17 @@ struct RowSlice {
     if (!primed) prime();
     primed = false;
 #pragma unroll 1
-    for (int c = 0; j0 < plain; ++c, j0 += kStage) {
+    for (; j0 < plain; j0 += kStage) {
       const int j = j0 + lane;
-      wait(&bars[stage], parity, c);
+      wait(&bars[stage], parity, j0);
       const Vec* at = data + stage * kStage + lane;
       Vec x[2] = {at[0], at[32]};
       // Every lane has been through f for the chunk before, so its reads of that
       // stage have ended and it can be filled again.  (Not this chunk's stage:
       // its reads are only under way.  Filled here, a copy from L2 overtook them.)
       __syncwarp();
-      if (lane == 0 && c > 0 && (c - 1 + stages) * kStage < until)
-        issue(c - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
+      if (lane == 0 && j0 > 0 && j0 + (stages - 1) * kStage < until)
+        issue(j0 + (stages - 1) * kStage, stage == 0 ? stages - 1 : stage - 1);
       if (++stage == stages) {
         stage = 0;
         parity ^= 1;

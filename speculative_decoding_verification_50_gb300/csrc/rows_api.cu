@@ -25,7 +25,7 @@ specv_status check_rows(const char* what, int32_t n, int32_t V, int32_t dtype) {
 }
 
 constexpr size_t kSmemSm = 228 * 1024, kSmemCta = 227 * 1024, kSmemReserved = 1024;
-constexpr size_t kDistillStatic = 2048;  // (at least what distill_kernel declares)
+constexpr size_t kDistillStatic = 2304;  // (at least what distill_kernel declares)
 
 // The row's split over a cluster of C CTAs (a power of two) whose slices stay
 // in shared memory beside `extra` bytes per CTA.  C is the smallest for which
