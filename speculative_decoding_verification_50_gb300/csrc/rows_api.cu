@@ -64,9 +64,8 @@ constexpr int64_t kL2Rows = 96 << 20;
 // is streamed again in each pass.  `again`: as few as leave the rows in flight to
 // L2; else as few as fill the slots.  extra(svec): a CTA's bytes beside its
 // rings.  False: few rows, or no fewer CTAs than sp has; those are held whole.
-//   `first_wave`: held too where a second wave of CTAs would be nearly empty.
 template <typename Extra>
-bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool first_wave, bool ring, int max_c,
+bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool ring, int max_c,
                   Extra&& extra, RowSplit& sp, size_t& smem) {
   const int vw = 16 / elem_bytes(dtype);
   const int64_t nvec = (static_cast<int64_t>(V) + vw - 1) / vw;
@@ -74,7 +73,6 @@ bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool first
   int C = 1;
   while (C < sp.C && ((again && slots / C * nvec * 16 > kL2Rows) || 5 * rows * C < 4 * slots)) C *= 2;
   if (C > max_c || C >= sp.C) return false;
-  if (first_wave && rows * C > slots && 4 * rows * C < 5 * slots) return false;
   const int32_t svec = static_cast<int32_t>((nvec + C - 1) / C);
   const size_t work = extra(svec), room = kSmemSm / 2 - kSmemReserved;
   if (work > room) return false;
@@ -89,24 +87,32 @@ bool split_stream(int64_t rows, int32_t V, int32_t dtype, bool again, bool first
   return true;
 }
 
-// The split for sampling (and, `top`, the top logits); four histograms per CTA
-// keep the part of a row small that a token is drawn from (2304 x 152064 fp32
-// in clusters of two: one 1760 us, two 1371, four 1179).
+// What sampling's kernel is asked for, and the top logits.
+enum FilterKind { kTokens, kFilteredAlone, kTopLogits };
+
+// Their split; four histograms per CTA keep the part of a row small that a token is
+// drawn from (2304 x 152064 fp32 top-p takes 1.36 times as long with one, 1.09 with
+// two; 1024 x 128256 bf16 mixed 1.14, 1.05).
 // Measured (us; rows x V; C = 1, 2, held whole).  Sampling, whose first pass is
 // its longest, takes the smallest C although rows in flight may overflow L2:
 // 2304 x 152064 fp32 top-p 917, 1028, 2123; 320 rows 207, 243, 324; 1024 x 128256
-// bf16 mixed 250, 259, 338; but 320 rows of it, filtered, 132, 146, 115 (held in
-// clusters of four; hence first_wave).  Top logits leave rows to L2: the 256
-// largest of 1024 x 152064 fp32 254, 238, 419; of 2048 x 152064 bf16 236, 328, 429;
-// 100 of 333 x 50257 fp32 47, 60, 74.
-bool split_filter(int64_t rows, int32_t V, int32_t dtype, bool top, RowSplit& sp, size_t& smem) {
+// bf16 mixed 250, 259, 338.  So it does where a second wave of CTAs is nearly empty
+// (305 to 379 rows: tokens of 320 x 128256 bf16 101, held 117; of 320 x 50257 fp32
+// 70, 107), but for filtered bf16 rows alone whose slices fill their shared memory
+// to three quarters (320 x 128256 117, held 113, top-p alone 193, 166; 370 x 80000
+// 130, 113; less full, 345 x 90000 93, 111, 345 x 175000 164, 209).  Top logits
+// leave rows to L2: the 256 largest of 1024 x 152064 fp32 254, 238, 419; of 2048 x
+// 152064 bf16 236, 328, 429; 100 of 333 x 50257 fp32 47, 60, 74.
+bool split_filter(int64_t rows, int32_t V, int32_t dtype, FilterKind kind, RowSplit& sp, size_t& smem) {
   constexpr size_t fixed = (sizeof(FilterShared) + 127) / 128 * 128;
+  const bool top = kind == kTopLogits;
   const int H = top ? 1 : kMaxH;
   if (!split_row(rows, V, dtype, fixed + work_bytes(1), sp, smem)) return false;
-  const int max_c = V / H <= kMaxBinned ? kMaxParts / H : 0;
-  if (split_stream(rows, V, dtype, top, !top && sp.C <= 4, false, max_c, [&](int32_t) { return fixed + work_bytes(H); },
-                   sp, smem))
-    sp.H = H;
+  const int64_t slots = 2LL * api_sm_count();
+  const bool held = kind == kFilteredAlone && dtype == SPECV_BF16 && rows > slots && 4 * rows < 5 * slots &&
+                    4 * smem >= 3 * (kSmemSm / 2 - kSmemReserved - fixed - work_bytes(1));
+  const int max_c = !held && V / H <= kMaxBinned ? kMaxParts / H : 0;
+  if (split_stream(rows, V, dtype, top, false, max_c, [&](int32_t) { return fixed + work_bytes(H); }, sp, smem)) sp.H = H;
   smem += work_bytes(sp.H);
   return true;
 }
@@ -154,7 +160,7 @@ specv_status specv_sample(const specv_sample_args* a, void* stream) {
   const int64_t rows = static_cast<int64_t>(B) * R;
   FilterParams p = {};
   size_t smem;
-  if (!split_filter(rows, V, a->dtype, false, p.sp, smem))
+  if (!split_filter(rows, V, a->dtype, a->tokens ? kTokens : kFilteredAlone, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (rows * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B*R too large");
   p.rows = static_cast<int32_t>(rows);
@@ -197,7 +203,7 @@ specv_status specv_top_logits(const specv_top_args* a, void* stream) {
   if (a->row_stride < V) return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than V");
   TopParams p = {};
   size_t smem;
-  if (!split_filter(B, V, a->dtype, true, p.sp, smem))
+  if (!split_filter(B, V, a->dtype, kTopLogits, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", V);
   if (static_cast<int64_t>(B) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "B too large");
   p.rows = B;
@@ -293,7 +299,7 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
   // (With a gradient the rows are read again: left to L2 1024 x 152064 fp32 take 287
   // us, by one CTA each 315; 300 rows 92, 109.)
-  split_stream(a->N, a->V, a->dtype, a->grad != nullptr, false, true, kMaxCluster,
+  split_stream(a->N, a->V, a->dtype, a->grad != nullptr, true, kMaxCluster,
                [&](int32_t svec) { return kDistillStatic + distill_bytes(svec, vw, a->K); }, p.sp, smem);
   smem += distill_bytes(p.sp.svec, vw, a->K);
   if (static_cast<int64_t>(a->N) * p.sp.C > 0x7fffffffLL) return api_fail(SPECV_ERR_UNSUPPORTED, "N too large");

@@ -194,3 +194,36 @@ def test_parts_of_nothing_but_light_tokens(sv, dtype, V, end):
         assert (got >= torch.where(heavy, at, -1).amax(1)).all()
         light = keep.any(1) & ((keep & ~heavy & (z.double() > 40.0 - 47.9 * np.log(2.0))).any(1))
         assert torch.equal(got[light], torch.where(keep, at, -1).amax(1)[light])
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 30016), (torch.bfloat16, 64000), (torch.bfloat16, 90001)])
+def test_second_wave_nearly_empty(sv, dtype, V):
+    """Rows a few more than the CTAs that run at once: streamed for tokens, held
+    where filtered bf16 rows are wanted alone and fill their shared memory."""
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 16
+    rng = np.random.default_rng(V + 3)
+    g = torch.Generator(device="cuda").manual_seed(V + 3)
+    z = (torch.randn(B, V, generator=g, device="cuda") * 2).to(dtype)
+    check(sv, z, rng.choice([0.0, 0.5, 1.0], B), rng.choice([0, 0, 40, 2000], B), rng.choice([1.0, 0.8, 0.95], B),
+          rng.choice([0.0, 0.01], B), rng.uniform(0, 1, B))
+
+
+def test_widest_rows(sv):
+    """More of them in flight than L2 holds."""
+    V, B = 600001, 264
+    g = torch.Generator(device="cuda").manual_seed(14)
+    z = torch.randn(B, V, generator=g, device="cuda") * 2
+    T = torch.full((B,), 0.9, device="cuda")
+    u, p = torch.rand(B, generator=g, device="cuda"), torch.rand(B, generator=g, device="cuda") * 0.4 + 0.6
+    f = torch.empty_like(z)
+    o = sv.specv_sample(z, T, u, top_p=p, filtered=f)
+    close = 0
+    for a in range(0, B, 24):
+        s = slice(a, a + 24)
+        keep, tok, pr, near = sample64(z[s], T[s], torch.zeros(24), p[s], torch.zeros(24), u[s])
+        ok = ~near
+        close += int(near.sum())
+        assert torch.equal(o["kept"][s][ok].long(), keep[ok].sum(1)) and torch.equal(o["tokens"][s][ok], tok[ok])
+        assert torch.equal(f[s][ok], torch.where(keep, z[s], -float("inf"))[ok])
+        assert ((o["prob"][s].double() - pr).abs() <= PROB_RTOL * pr)[ok].all()
+    assert close <= B // 5  # (the borders here: 600001 units of 2^-42 beside 1e-9)
