@@ -474,18 +474,22 @@ struct FilterRow {
     float run = block_scan((v[0] + v[1]) + (v[2] + v[3]), S.fscratch, all);
     if (!MASS && all < goal) return false;
     constexpr float over = MASS ? 1.f + 0x1p-18f : 1.f, under = MASS ? 1.f - 0x1p-18f : 1.f;
-    if (run * under < goal) {  // (threads past the cut leave)
+    // (The smallest of all such bins, not the one where a sum passes the goal: one
+    // thread's sum and the next one's start differ by roundings.)
+    int lo_bin = INT_MAX, hi_bin = INT_MAX;
 #pragma unroll
-      for (int q = 0; q < per; ++q) {
-        const float before = run;
-        run += v[q];
-        if (v[q] > 0.f && run * over >= goal && before * over < goal) {
-          atomicMin(&S.lo, b0 + q);
-          if (!MASS) S.before = static_cast<int32_t>(before);
-        }
-        if (v[q] > 0.f && run * under >= goal && before * under < goal) atomicMin(&S.hi, b0 + q);
-      }
+    for (int q = 0; q < per; ++q) {
+      const float before = run;
+      run += v[q];
+      if (!(v[q] > 0.f)) continue;
+      if (run * over >= goal) lo_bin = min(lo_bin, b0 + q);
+      if (run * under >= goal) hi_bin = min(hi_bin, b0 + q);
+      if (!MASS && run >= goal && before < goal) S.before = static_cast<int32_t>(before);
     }
+    lo_bin = __reduce_min_sync(0xffffffffu, lo_bin);
+    hi_bin = __reduce_min_sync(0xffffffffu, hi_bin);
+    if (lane == 0 && lo_bin < INT_MAX) atomicMin(&S.lo, lo_bin);
+    if (lane == 0 && hi_bin < INT_MAX) atomicMin(&S.hi, hi_bin);
     __syncthreads();
     const int hi = min(S.hi, kBins - 1);
     set_band(b, min(S.lo, hi), hi);

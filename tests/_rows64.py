@@ -46,7 +46,7 @@ def distill64(z, ids, t, lse=None, T=1.0, w=None, tail=False):
 
 def sample64(z, T, k, p, mp, u, near_by=1e-9):
     """Kept mask [B, V], token, prob and whether a cut or the draw lies within
-    near_by of a border (equality apart), of rows z under rules given as
+    near_by of a border (equality to 1e-13 apart), of rows z under rules given as
     sequences; each kept token adds the 2^-44 to which its weight is held."""
     dev = z.device
     f = lambda x: torch.as_tensor(x, dtype=torch.float32).to(dev).double().view(-1, 1)  # noqa: E731
@@ -68,7 +68,7 @@ def sample64(z, T, k, p, mp, u, near_by=1e-9):
     n_p = torch.where(p < 1, n_p, n_k)
     gap = (cum - goal).abs()
     by = near_by * goal + n_k * 2.0 ** -44
-    near = ((gap > 1e-12 * goal) & (gap < by) & inside & (p < 1)).any(1)
+    near = ((gap > 1e-13 * goal) & (gap < by) & inside & (p < 1)).any(1)
     n_m = (zs >= top + T * torch.log(mp.clamp_min(2.0 ** -48))).sum(1, keepdim=True)
     n = torch.where(greedy, 1, torch.minimum(n_p, n_m).clamp_min(1))
     keep = torch.zeros(z.shape, dtype=torch.bool, device=dev)
@@ -80,6 +80,6 @@ def sample64(z, T, k, p, mp, u, near_by=1e-9):
     last = torch.where(keep, torch.arange(V, device=dev), 0).amax(1, keepdim=True)
     token = torch.minimum((run <= t * (1 + 1e-13)).sum(1, keepdim=True), last)
     gap = (run - t).abs()
-    near |= ((gap > 1e-12 * W) & (gap < near_by * W + n * 2.0 ** -44) & keep).any(1)
+    near |= ((gap > 1e-13 * W) & (gap < near_by * W + n * 2.0 ** -44) & keep).any(1)
     near &= ~greedy[:, 0]
     return keep, token[:, 0].int(), (w.gather(1, token) / W)[:, 0], near

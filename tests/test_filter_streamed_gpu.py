@@ -227,3 +227,14 @@ def test_widest_rows(sv):
         assert torch.equal(f[s][ok], torch.where(keep, z[s], -float("inf"))[ok])
         assert ((o["prob"][s].double() - pr).abs() <= PROB_RTOL * pr)[ok].all()
     assert close <= B // 5  # (the borders here: 600001 units of 2^-42 beside 1e-9)
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 20187), (torch.float32, 30016), (torch.bfloat16, 60005)])
+def test_cuts_far_down_the_tail(sv, dtype, V):
+    """top-p of 0.999 to 0.99999: the bins at the cut hold a few roundings of the
+    row's sum."""
+    g = torch.Generator(device="cuda").manual_seed(V + 4)
+    for B in (150, 4 * many()):
+        z = (torch.randn(B, V, generator=g, device="cuda") * (2 + 2 * torch.rand(B, 1, generator=g, device="cuda"))).to(dtype)
+        u, p = torch.rand(B, generator=g, device="cuda"), 1 - 10 ** -(3 + 2 * torch.rand(B, generator=g, device="cuda"))
+        check(sv, z, torch.ones(B), None, p.cpu(), None, u.cpu(), max_near=0.3)
