@@ -361,9 +361,10 @@ specv_status specv_mss_verify(const specv_mss_args* args, void* workspace,
  * A weight is computed to 2^-29 of itself, and so is prob (then rounded to fp32).
  * Cuts and draws compare sums of whole numbers of 2^-44 of the largest weight
  * (V above 2^18: 2^-(62 - b), b the bits of V), at least one for each kept token:
- * they agree with 64-bit arithmetic except next to a border, by about 1e-10 of the
- * row's weight and such a unit for each kept token (a draw may pass over those below
- * 2^-47.9); sums that meet a border within 2^-36 count as on it.
+ * they agree with 64-bit arithmetic except next to a border, by at most 2^-28 of the
+ * row's weight (about 1e-10 where thousands of tokens share it) and such a unit for
+ * each kept token (a draw may pass over those below 2^-47.9); sums that meet a border
+ * within 2^-36 count as on it.
  * Row status: SPECV_ROW_NONFINITE, SPECV_ROW_BAD_TEMP, SPECV_ROW_BAD_FILTER,
  * SPECV_ROW_DEVICE_TIMEOUT: token -1, prob 0, kept 0, filtered all -inf.
  * One kernel, no workspace: few rows are held in the shared memory of a cluster

@@ -198,6 +198,7 @@ struct FilterShared {
   int32_t above, ncollect, kept, bad;
   uint32_t fix32[3][kMaxParts];  // per part, in pieces of 15 bits
   uint32_t kmin, kmax;
+  uint32_t upper;            // a band that is a lower half: the upper one's largest key
   int32_t lo, hi;
   int32_t before;
   float zf, zt;
@@ -411,6 +412,7 @@ struct FilterRow {
       S.above = S.ncollect = 0;
       S.kmin = 0xffffffffu;
       S.kmax = 0;
+      S.upper = 0;
       S.lo = S.hi = INT_MAX;
     }
     __syncthreads();
@@ -703,7 +705,9 @@ struct FilterRow {
 
   // Narrows a band too full to collect: counts by key over [kmin, kmax] into
   // 1024 bins.  count: the cut is the goal-th token of the band; else the
-  // mass `goal` into it.
+  // mass `goal` into it.  Bounds on a bin's mass (a bin spans up to a thousandth of a
+  // wide range of keys) may leave the cut among too many tokens: then b is the lower
+  // half of those bins, and S.upper the upper half's largest key (else 0).
   __device__ void narrow(Band& b, bool count, uint64_t goal) {
     constexpr int bins = 2 * kRowThreads;
     const uint32_t kmin = b.kmin, kmax = b.kmax;
@@ -749,10 +753,20 @@ struct FilterRow {
     const int hi = min(S.hi, end), lo = min(S.lo, hi);
     b.by_key = true;
     b.kmax = kmax - (static_cast<uint32_t>(lo) << shift);
+    if (!exact && lo < hi) {
+      uint64_t tokens = 0;
+      for (int q = 0; q < 2; ++q)
+        if (b0 + q >= lo && b0 + q <= hi) tokens += static_cast<uint64_t>(S.total[b0 + q]);
+      if (block_sum_u(tokens) > kCap) {
+        if (threadIdx.x == 0) S.upper = b.kmax;
+        b.kmax = kmax - (static_cast<uint32_t>(((lo + hi) >> 1) + 1) << shift);
+      }
+    }
     const uint32_t last_top = kmax - (static_cast<uint32_t>(hi) << shift);
     const uint32_t span = (1u << shift) - 1;
     b.kmin = last_top - kmin < span ? kmin : last_top - span;
     b.elo = key_value(b.kmin);
+    __syncthreads();
   }
 
   // The band at min-p's threshold zt, which lies in its bins: no tokens in it,
@@ -778,8 +792,8 @@ struct FilterRow {
   // last cut, whose sums give the token as well (min-p's threshold zt is then
   // part of it).
   __device__ void cut(Band b, CutKind kind, uint64_t goal, bool fin, float zt, const float* u) {
-    for (int it = 0; it < 40; ++it) {  // (each turn shrinks the band; three are the usual most)
-      if (fin && kind != kGiven && b.by_key && order_key(zt) > b.kmax) {  // min-p ends the kept tokens first
+    for (int it = 0; it < 80; ++it) {  // (each two turns halve the band's keys; three are the usual most)
+      if (fin && S.upper == 0 && kind != kGiven && b.by_key && order_key(zt) > b.kmax) {  // min-p ends the kept tokens first
         set_given(b, zt);
         kind = kGiven;
       }
@@ -788,6 +802,16 @@ struct FilterRow {
       int above;
       uint64_t w;
       before_band(above, w);
+      if (S.upper != 0) {  // which half the cut lies in, by the exact mass above the lower one
+        if (w >= goal) {
+          b.kmin = b.kmax + 1;
+          b.kmax = S.upper;
+          b.elo = key_value(b.kmin);
+        }
+        sync_all();  // (everyone has read the masses)
+        clear();
+        continue;
+      }
       if (n <= kCap) {
         if (rank == 0) resolve(n, above, w, kind, goal, fin, zt, u);
         publish();

@@ -238,3 +238,30 @@ def test_cuts_far_down_the_tail(sv, dtype, V):
         z = (torch.randn(B, V, generator=g, device="cuda") * (2 + 2 * torch.rand(B, 1, generator=g, device="cuda"))).to(dtype)
         u, p = torch.rand(B, generator=g, device="cuda"), 1 - 10 ** -(3 + 2 * torch.rand(B, generator=g, device="cuda"))
         check(sv, z, torch.ones(B), None, p.cpu(), None, u.cpu(), max_near=0.3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [5000, 24762, 60005])
+@pytest.mark.parametrize("gap", [-50.0, 0.0, 30.0])
+def test_a_few_levels(sv, dtype, V, gap):
+    """Rows of a few values with thousands of tokens each, some far apart, and cuts
+    just before, at and after the end of a level."""
+    rng = np.random.default_rng(V)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    for B in (60, many()):
+        values = gap + torch.tensor([0.0, 0.01, 0.26, 0.5, 1.25, 7.0], device="cuda")
+        values = values[torch.randint(0, 6, (B, 5), generator=g, device="cuda")]
+        # shares of 0.5 to 0.97 for the first level, the rest of the row for the others
+        share = 0.5 + 0.47 * torch.rand(B, 1, generator=g, device="cuda")
+        which = torch.randint(1, 5, (B, V), generator=g, device="cuda")
+        which[torch.rand(B, V, generator=g, device="cuda") < share] = 0
+        z = values.gather(1, which).to(dtype)
+        T = torch.from_numpy(rng.choice([0.5, 1.0, 3.0], B)).float()
+        # p: the weight down to a level's end, a little more or less, or any
+        y = z.double() / T.cuda().double()[:, None]
+        w = torch.softmax(y, 1)
+        level = z.double().gather(1, torch.randint(0, V, (B, 1), generator=g, device="cuda"))
+        p = torch.where(z.double() >= level, w, 0.0).sum(1).float().cpu().numpy()
+        p = p + rng.choice([0.0, 0.0, 1e-7, -1e-7, 1e-4, -1e-4, -0.2, 0.01], B).astype(np.float32)
+        p[::7] = 0.9999
+        check(sv, z, T, None, np.clip(p, 0, 1), rng.choice([0.0, 0.0, 1e-3], B), rng.uniform(0, 1, B), max_near=0.5)
