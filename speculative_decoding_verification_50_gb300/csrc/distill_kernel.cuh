@@ -167,10 +167,12 @@ __device__ Teacher load_teacher(const DistillParams& P, int64_t row, int32_t* id
   if (P.tlse) {
     t.L = P.tlse[row];
     if (!isfinite(t.L)) t.bad |= kNonFinite;
-    // p = exp(t / T - L), the product's rounding to first order
+    // p = exp(t / T - L); the product's rounding, 0.01 and more where t / T is 10^5,
+    // belongs to the argument
     for (int j = threadIdx.x; j < K; j += kRowThreads) {
       const float x = __fmul_rn(tl[j], ih);
-      const float p = tl[j] > neg_inf() ? expf(x - t.L) * (1.f + fmaf(tl[j], il, fmaf(tl[j], ih, -x))) : 0.f;
+      const FF d = two_sum(x - t.L, fmaf(tl[j], il, fmaf(tl[j], ih, -x)));
+      const float p = tl[j] > neg_inf() && d.hi > -100.f ? expf(d.hi) * (1.f + d.lo) : 0.f;
       pj[j] = p;
       if (MASS) v += __float2ull_rn(fminf(p, 1e6f) * kFixed);
     }

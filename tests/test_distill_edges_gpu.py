@@ -239,3 +239,23 @@ def test_small_losses(sv, V, K):
     assert off.pow(2).mean().sqrt() <= 2.0 ** -24.5, off.pow(2).mean().sqrt()
     close(fused, want, size, TAIL)
     close(back, want, size, TAIL)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tail", [False, True])
+def test_logits_of_three_hundred_thousand_units(sv, dtype, tail):
+    """z / T of 3e5, whose roundings to fp32 are 0.03 apart."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    N, V, K, T = 40, 1999, 25, 0.001
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    teacher = -300 + 2 * T * normal(N, V)
+    val, ids = teacher.topk(K, dim=1)
+    ids = ids.int()
+    lse = torch.logsumexp(teacher.double() / float(torch.tensor(T)), 1).float()
+    z = (-300 + 2 * T * normal(N, V)).to(dtype)
+    assert (1 - torch.exp(val.double() / float(torch.tensor(T)) - lse.double()[:, None]).sum(1)).min() >= 1 / 16
+    loss, want, scale, _, size = distill64(z, ids, val, lse, T, tail=tail)
+    got, fused, back = both(sv, z, ids, val, lse=lse, T=T, tail=tail)
+    assert ((got.double() - loss).abs() <= TAIL * scale).all()
+    close(fused, want, size, TAIL)
+    close(back, want, size, TAIL)
