@@ -476,22 +476,32 @@ struct FilterRow {
     float run = block_scan((v[0] + v[1]) + (v[2] + v[3]), S.fscratch, all);
     if (!MASS && all < goal) return false;
     constexpr float over = MASS ? 1.f + 0x1p-18f : 1.f, under = MASS ? 1.f - 0x1p-18f : 1.f;
-    // (The smallest of all such bins, not the one where a sum passes the goal: one
-    // thread's sum and the next one's start differ by roundings.)
-    int lo_bin = INT_MAX, hi_bin = INT_MAX;
+    if (!MASS && run < goal) {  // counts are exact: one bin holds the cut
 #pragma unroll
-    for (int q = 0; q < per; ++q) {
-      const float before = run;
-      run += v[q];
-      if (!(v[q] > 0.f)) continue;
-      if (run * over >= goal) lo_bin = min(lo_bin, b0 + q);
-      if (run * under >= goal) hi_bin = min(hi_bin, b0 + q);
-      if (!MASS && run >= goal && before < goal) S.before = static_cast<int32_t>(before);
+      for (int q = 0; q < per; ++q) {
+        const float before = run;
+        run += v[q];
+        if (run >= goal && before < goal) {
+          S.lo = S.hi = b0 + q;
+          S.before = static_cast<int32_t>(before);
+        }
+      }
     }
-    lo_bin = __reduce_min_sync(0xffffffffu, lo_bin);
-    hi_bin = __reduce_min_sync(0xffffffffu, hi_bin);
-    if (lane == 0 && lo_bin < INT_MAX) atomicMin(&S.lo, lo_bin);
-    if (lane == 0 && hi_bin < INT_MAX) atomicMin(&S.hi, hi_bin);
+    if (MASS) {
+      // (The smallest of all such bins, not the one where a sum passes the goal: one
+      // thread's sum and the next one's start differ by roundings.)
+      int lo_bin = INT_MAX, hi_bin = INT_MAX;
+#pragma unroll
+      for (int q = 0; q < per; ++q) {
+        run += v[q];
+        if (v[q] > 0.f && run * over >= goal) lo_bin = min(lo_bin, b0 + q);
+        if (v[q] > 0.f && run * under >= goal) hi_bin = min(hi_bin, b0 + q);
+      }
+      lo_bin = __reduce_min_sync(0xffffffffu, lo_bin);
+      hi_bin = __reduce_min_sync(0xffffffffu, hi_bin);
+      if (lane == 0 && lo_bin < INT_MAX) atomicMin(&S.lo, lo_bin);
+      if (lane == 0 && hi_bin < INT_MAX) atomicMin(&S.hi, hi_bin);
+    }
     __syncthreads();
     const int hi = min(S.hi, kBins - 1);
     set_band(b, min(S.lo, hi), hi);
@@ -753,7 +763,7 @@ struct FilterRow {
     const int hi = min(S.hi, end), lo = min(S.lo, hi);
     b.by_key = true;
     b.kmax = kmax - (static_cast<uint32_t>(lo) << shift);
-    if (!exact && lo < hi) {
+    if (!CLAMP && !exact && lo < hi) {  // (top logits count: always exact)
       uint64_t tokens = 0;
       for (int q = 0; q < 2; ++q)
         if (b0 + q >= lo && b0 + q <= hi) tokens += static_cast<uint64_t>(S.total[b0 + q]);
@@ -793,7 +803,7 @@ struct FilterRow {
   // part of it).
   __device__ void cut(Band b, CutKind kind, uint64_t goal, bool fin, float zt, const float* u) {
     for (int it = 0; it < 80; ++it) {  // (each two turns halve the band's keys; three are the usual most)
-      if (fin && S.upper == 0 && kind != kGiven && b.by_key && order_key(zt) > b.kmax) {  // min-p ends the kept tokens first
+      if (fin && (CLAMP || S.upper == 0) && kind != kGiven && b.by_key && order_key(zt) > b.kmax) {  // min-p ends the kept tokens first
         set_given(b, zt);
         kind = kGiven;
       }
@@ -802,7 +812,7 @@ struct FilterRow {
       int above;
       uint64_t w;
       before_band(above, w);
-      if (S.upper != 0) {  // which half the cut lies in, by the exact mass above the lower one
+      if (!CLAMP && S.upper != 0) {  // which half the cut lies in, by the exact mass above the lower one
         if (w >= goal) {
           b.kmin = b.kmax + 1;
           b.kmax = S.upper;
