@@ -292,9 +292,9 @@ __device__ __forceinline__ unsigned vector_bits(const unsigned char* bits, int v
 // Loss, statistics and (grad given) the gradient of the rows: a cluster per
 // row.  One pass for the maximum and the sum of the logits that are not listed
 // (each thread's sum relative to its own running maximum, joined at the end),
-// one for the gradient.  1024 x 128256 bf16, K = 64, with the gradient 132 us (525
-// MB, 4.0 TB/s): 71 % of issue slots, and a quarter of the second read comes from
-// HBM again; 1024 x 152064 fp32, K = 256, loss alone 123 us (623 MB, 5.1 TB/s).
+// one for the gradient.  1024 x 128256 bf16, K = 64, with the gradient 134 us (525
+// MB, 3.9 TB/s): 69 % of issue slots, and a third of the second read comes from
+// HBM again; 1024 x 152064 fp32, K = 256, loss alone 124 us (623 MB, 5.0 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_constant__ DistillParams P) {
   using E = Elem<DT>;
@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     const FF listed_sum = all.listed.hi > 0.f ? times(all.listed, near) : ff(0.f);
     total = ff_gather(listed_sum, all.rest.hi > 0.f ? times(all.rest, far) : ff(0.f));
     total = fast_two_sum(total.hi, total.lo);
-    const float inv = 1.f / total.hi;
+    const float recip = 1.f / (lane == 0 ? total.hi : all.rest.hi);
+    const float inv = __shfl_sync(0xffffffffu, recip, 0), inv_rest = __shfl_sync(0xffffffffu, recip, 1);
     const float m = te.total(P.tlse != nullptr).hi;
     if (P.tail) r = static_cast<float>((1ll << 40) - static_cast<int64_t>(te.mass)) * (1.f / kFixed);
     if (r < kNoTail) r = 0.f;
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
     if (r > 0.f && has_rest) {
       beta = m + r;  // (alpha + r / (1 - s), whose two large terms cancel)
       ref = ur;
-      alpha = m * (far.hi * inv) - r * (listed_sum.hi * inv) / all.rest.hi;
+      alpha = m * (far.hi * inv) - r * (listed_sum.hi * inv) * inv_rest;
     }
     beta *= inv;
     if (lane == 0) {
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
   if (P.grad) __syncthreads();
   if (warp == 0 && rank == 0) {  // the loss, while the others start on the gradient
     FF l = log_pair(lane == 0 ? total.hi : lane == 1 ? all.rest.hi : lane == 2 ? r : te.sum());
-    if (lane < 2) l.lo += lane == 0 ? total.lo / total.hi : all.rest.lo / all.rest.hi;
+    if (lane < 2) l.lo += lane == 0 ? __fdividef(total.lo, total.hi) : __fdividef(all.rest.lo, all.rest.hi);
     const FF lt = shfl(l, 0), lrest = shfl(l, 1), lr = shfl(l, 2), ln = P.tlse ? ff(te.L) : shfl(l, 3);
     FF loss = ff(0.f);
     if (te.mass) {  // log p - log q at the origin, times m
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_kernel(const __grid_co
 // The gradient from the statistics of an earlier distill_kernel: one pass, a
 // CTA per piece of a row, of kBackGroups groups of kBackVecs vectors a thread (the
 // next group's loads ahead of this one's stores).  Bound by HBM: 1024 x 152064
-// fp32 215 us (1246 MB, 5.8 TB/s).
+// fp32 214 us (1246 MB, 5.8 TB/s).
 constexpr int kBackVecs = 4, kBackGroups = 4;
 __host__ __device__ constexpr int back_piece(int vw) { return kRowThreads * kBackVecs * kBackGroups * vw; }
 

@@ -292,7 +292,8 @@ struct FilterRow {
     int d;
     const uint32_t v = sc.weight(z, d);
     const double w = static_cast<double>(v) * static_cast<double>(S.tab[(-d) & (kGrid - 1)]);
-    return static_cast<float>(ldexp(w, fbits - 91 - ((d + kGrid - 1) >> 5)) / static_cast<double>(W));
+    const double unit = __hiloint2double((1023 + fbits - 91 - ((d + kGrid - 1) >> 5)) << 20, 0);  // a power of two
+    return static_cast<float>(w * unit / static_cast<double>(W));
   }
 
   // The cluster's barrier.
@@ -372,8 +373,8 @@ struct FilterRow {
     return m;
   }
 
-  // The first pass over a row, from memory (2304 x 152064 fp32 1117 us; with a
-  // pass for the maximum before that for the masses 1195): the maximum, and on the way the
+  // The first pass over a row, from memory (with a pass for the maximum before that for
+  // the masses 2304 x 152064 fp32 take 7 % longer): the maximum, and on the way the
   // masses by bins below a guessed one (`sc`, without a shift; the first kHead bins are for
   // logits above it).  The guess holds if the maximum turns out to lie there, on the same
   // scale.
@@ -922,10 +923,10 @@ struct FilterRow {
     return true;
   }
 
-  // Sorts n <= kCap tokens.  By counts or by bins (us): 32 tokens of 4 rows of
-  // 32000 12.7, 14.6.  By bins or, as where a bin is too full, by exchanges: the
-  // 256 largest of 2048 x 152064 bf16 236, 283; a draw from 2304 x 152064 fp32
-  // 1030, 1184.
+  // Sorts n <= kCap tokens.  By bins in the place of counts, 32 tokens of 4 rows of
+  // 32000 take 15 % longer.  By exchanges in the place of bins (as where a bin is too
+  // full), the 256 largest of 2048 x 152064 bf16 20 %, a draw from 2304 x 152064 fp32
+  // 15 %.
   __device__ void sort(uint64_t* a, int n) {
     int P = 16;
     while (P < n) P <<= 1;
@@ -1368,11 +1369,11 @@ struct FilterRow {
 
 // One row per cluster: the cut, the token, the filtered logits.
 // Many rows are bound by issue slots and shared atomics: 2304 x 152064 fp32 top-p
-// 0.91 ms (1401 MB, 1.54 TB/s), of a row's time a third in the pass for the
+// 0.93 ms (1401 MB, 1.51 TB/s), of a row's time a third in the pass for the
 // masses (25 operations and two atomics a logit), a fifth in the band's
 // collection, the rest in the merge, the sorted list and the draw.  320 x 128256
-// bf16 filtered 118 us (164 MB).  Few rows are bound by the chain of these steps,
-// 1 to 3 us each: one row of 32000 with top-k 19 us, 32 x 128256 bf16 mixed 40.
+// bf16 filtered 112 to 118 us by the rules drawn (164 MB).  Few rows are bound by the chain of these steps,
+// 1 to 3 us each: one row of 32000 with top-k 16 us, 32 x 128256 bf16 mixed 34.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __grid_constant__ FilterParams P) {
   using E = Elem<DT>;
@@ -1647,7 +1648,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) sample_filter_kernel(const __g
 // One row per cluster: the k largest logits, in order, and the log-sum-exp.
 // 256 of 2048 x 152064 bf16 234 us (623 MB, 2.7 TB/s): a row's collection and
 // sort follow its pass for maximum and sum, and the other CTA on the SM covers
-// only part of them.  32 of 4 x 32000 fp32 13 us, 100 of 333 x 50257 fp32 47.
+// only part of them.  32 of 4 x 32000 fp32 11 us, 100 of 333 x 50257 fp32 42.
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads, 2) top_logits_kernel(const __grid_constant__ TopParams P) {
   using E = Elem<DT>;

@@ -31,7 +31,9 @@ __host__ __device__ constexpr size_t row_bytes(int rvec, int stages) {
 // holds vectors [r * svec, (r + 1) * svec), its warp w the segment [w * gvec,
 // (w + 1) * gvec) of them (-inf after the row's last logit).  Index order is
 // (CTA, warp, vector), lanes taking the vectors of a segment in turn; it does
-// not depend on the row's alignment, so neither does any sum.
+// not depend on the row's alignment, so neither does any sum.  (It does depend on
+// the split: sums of whole numbers are rounded to their unit, others to fp32, part
+// by part.)
 struct RowSplit {
   int32_t V;
   int32_t C;       // CTAs per row
@@ -135,15 +137,15 @@ struct RunningSum {
 
 // One CTA's slice of a row, as one warp sees it: its segment.  RING: either
 // held whole or streamed through the ring; else held in part (or whole) and the
-// rest streamed by plain loads.  (The ring pays where a pass is short: loss and
-// gradient of 1024 x 128256 bf16 149 us with loads, 133 with a ring of 1 KB
-// stages.  Sampling's longer passes and its histograms, which leave room for
-// three stages, go the other way: 2304 x 152064 fp32 1176 us with loads, 1369
-// with the ring; the 256 top logits of 2048 x 152064 bf16 250, 311.)
+// rest streamed by plain loads.  (The ring pays where a pass is short: with loads,
+// loss and gradient of 1024 x 128256 bf16 take 12 % longer than with a ring of 1 KB
+// stages.  Sampling's longer passes and its histograms, which leave room for three
+// stages, go the other way: with the ring 2304 x 152064 fp32 take 16 % longer, the
+// 256 top logits of 2048 x 152064 bf16 24 %.)
 // AHEAD: streamed vectors are loaded two by two, the next two while f has two;
-// else four at a time.  (The 256 top logits of 2048 x 152064 bf16 235 us ahead,
-// 247 by four; sampling, whose passes have no registers to spare, 2304 x 152064
-// fp32 1035 us and 1022.)
+// else four at a time.  (By four the 256 top logits of 2048 x 152064 bf16 take 5 %
+// longer; sampling, whose passes have no registers to spare, 1 % less, 2304 x 152064
+// fp32.)
 template <int DT, bool RING, bool AHEAD>
 struct RowSlice {
   using E = Elem<DT>;
@@ -212,8 +214,8 @@ struct RowSlice {
 
   // Vectors j0 + lane and 32 further (-inf past nv), the whole warp.  Inside a
   // row that starts past a 16-byte boundary each lane loads its aligned vector
-  // once and takes the bytes of the next from the lane above (608 x 152064 fp32
-  // top-p 504 -> 475 us, loss + gradient of 1024 x 128256 bf16 233 -> 216).
+  // once and takes the bytes of the next from the lane above (6 % of 608 x 152064
+  // fp32 top-p, 7 % of loss + gradient of 1024 x 128256 bf16).
   __device__ __forceinline__ void fetch_two(int j0, Vec (&x)[2]) const {
     const int j = j0 + lane;
     if (mis != 0 && v0 + j0 + base > 0 && j0 + kStage <= nv && (j0 + kStage) * E::VW + (16 - mis) / E::ES <= left) {

@@ -93,16 +93,16 @@ enum FilterKind { kTokens, kFilteredAlone, kTopLogits };
 // Their split; four histograms per CTA keep the part of a row small that a token is
 // drawn from (2304 x 152064 fp32 top-p takes 1.36 times as long with one, 1.09 with
 // two; 1024 x 128256 bf16 mixed 1.14, 1.05).
-// Measured (us; rows x V; C = 1, 2, held whole).  Sampling, whose first pass is
-// its longest, takes the smallest C although rows in flight may overflow L2:
-// 2304 x 152064 fp32 top-p 917, 1028, 2123; 320 rows 207, 243, 324; 1024 x 128256
-// bf16 mixed 250, 259, 338.  So it does where a second wave of CTAs is nearly empty
+// Times of C = 1, of 2 and of rows held whole, by the first of them.  Sampling, whose
+// first pass is its longest, takes the smallest C although rows in flight may overflow
+// L2: 2304 x 152064 fp32 top-p 1, 1.12, 2.3; 320 rows 1, 1.17, 1.57; 1024 x 128256
+// bf16 mixed 1, 1.04, 1.35.  So it does (us) where a second wave of CTAs is nearly empty
 // (305 to 379 rows: tokens of 320 x 128256 bf16 101, held 117; of 320 x 50257 fp32
 // 70, 107), but for filtered bf16 rows alone whose slices fill their shared memory
 // to three quarters (320 x 128256 117, held 113, top-p alone 193, 166; 370 x 80000
 // 130, 113; less full, 345 x 90000 93, 111, 345 x 175000 164, 209).  Top logits
-// leave rows to L2: the 256 largest of 1024 x 152064 fp32 254, 238, 419; of 2048 x
-// 152064 bf16 236, 328, 429; 100 of 333 x 50257 fp32 47, 60, 74.
+// leave rows to L2: the 256 largest of 1024 x 152064 fp32 1.07, 1, 1.76; of 2048 x
+// 152064 bf16 1, 1.39, 1.82; 100 of 333 x 50257 fp32 1, 1.28, 1.57.
 bool split_filter(int64_t rows, int32_t V, int32_t dtype, FilterKind kind, RowSplit& sp, size_t& smem) {
   constexpr size_t fixed = (sizeof(FilterShared) + 127) / 128 * 128;
   const bool top = kind == kTopLogits;
@@ -297,8 +297,8 @@ specv_status specv_distill(const specv_distill_args* a, void* stream) {
   const int vw = 16 / elem_bytes(a->dtype);
   if (!split_distill(a, p.sp, smem))
     return api_fail(SPECV_ERR_UNSUPPORTED, "V=%d does not fit on chip", a->V);
-  // (With a gradient the rows are read again: left to L2 1024 x 152064 fp32 take 287
-  // us, by one CTA each 315; 300 rows 92, 109.)
+  // (With a gradient the rows are read again: by one CTA each, in the place of as few
+  // as leave them to L2, 1024 x 152064 fp32 take 10 % longer, 300 rows 18 %.)
   split_stream(a->N, a->V, a->dtype, a->grad != nullptr, true, kMaxCluster,
                [&](int32_t svec) { return kDistillStatic + distill_bytes(svec, vw, a->K); }, p.sp, smem);
   smem += distill_bytes(p.sp.svec, vw, a->K);
