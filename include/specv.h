@@ -467,6 +467,55 @@ specv_status specv_distill(const specv_distill_args* args, void* stream);
 specv_status specv_distill_backward(const specv_distill_args* args, void* stream);
 
 /*
+ * The cross entropy of given tokens under softmax(z), z = scale * hidden head^T, from the
+ * last hidden states [N, D] and the head [V, D] (bf16), without the logits [N, V] in
+ * memory, and its gradients: the loss beside specv_distill that a drafter is trained with,
+ * and the log-probabilities of given tokens.
+ *   loss[n] = weights[n] * nll[n],  nll[n] = log sum_v exp(z_nv) - z_n,targets[n]
+ *   stats[n] = (log sum_v exp(z_nv), nll[n])
+ * A row whose target is -1 or whose weight is 0 is left out: loss 0, stats 0, no gradient.
+ * specv_head_loss writes loss, and if given the gradients of sum_n loss[n] by hidden and
+ * by head (either or both); specv_head_loss_backward the gradients of sum_n grad_loss[n]
+ * * loss[n] (grad_loss NULL: ones) from the stats of a call on the same inputs.
+ * The vocabulary is taken in pieces: beside the inputs a call needs the workspace alone
+ * (with gradients at most 512 MB, and in it rows of 4 bytes x D and 8 bytes x V/128 each).
+ * Products are summed in fp32.  The gradients' products read the logits' gradient rounded
+ * to bf16 (off by 2^-8 of each element at most), and are rounded once, to bf16.
+ * Row status: SPECV_ROW_BAD_TOKEN (a target outside [-1, V)), SPECV_ROW_NONFINITE (a logit
+ * that is NaN or infinite; rows that are left out may hold anything): loss 0, stats NaN, no
+ * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row; in a call's gradients
+ * (row_status is added to by specv_head_loss_backward, if given) it leaves them undefined.
+ * workspace: device memory of specv_head_workspace_bytes(args) bytes (of the same pointers,
+ * sizes and strides), 256-byte aligned.  hidden, head and gradients whose rows start at
+ * 16-byte boundaries are read and written in place; others are copied into the workspace.
+ * fp32 is refused with SPECV_ERR_UNSUPPORTED.  The gradients overlap nothing.
+ */
+typedef struct {
+  int32_t N, V, D;             /* rows; vocabulary; width of a hidden state */
+  int32_t dtype;               /* SPECV_BF16, of hidden, head and their gradients */
+  const void* hidden;
+  int64_t hidden_stride;       /* elements, >= D */
+  const void* head;
+  int64_t head_stride;         /* elements, >= D */
+  const int32_t* targets;      /* [N], -1: none */
+  const float* weights;        /* optional [N] */
+  float scale;                 /* in [1e-6, 1e6] */
+  float* loss;                 /* OUT [N] (specv_head_loss) */
+  float* stats;                /* [N, 2]: OUT, optional (specv_head_loss), or in (backward) */
+  int32_t* row_status;         /* OUT, optional [N] */
+  const float* grad_loss;      /* optional [N] (backward) */
+  void* grad_hidden;           /* OUT, optional */
+  int64_t grad_hidden_stride;  /* elements, >= D */
+  void* grad_head;             /* OUT, optional */
+  int64_t grad_head_stride;    /* elements, >= D */
+} specv_head_args;
+
+size_t specv_head_workspace_bytes(const specv_head_args* args);
+specv_status specv_head_loss(const specv_head_args* args, void* workspace, size_t workspace_bytes, void* stream);
+specv_status specv_head_loss_backward(const specv_head_args* args, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
  * Geometric fan-out ("Speculative Speculative Decoding" Theorem 12, proved in
  * Appendix A.2).  For a drafter with per-token acceptance rate a (0 < a < 1)
  * whose cache-miss probability at fan-out F is F^-r (r > 0), the fan-outs

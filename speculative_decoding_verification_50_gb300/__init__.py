@@ -17,6 +17,9 @@ Entry points (same names as the C ABI):
   specv_distill(logits, teacher_ids, teacher_logits, ...)
   specv_distill_backward(logits, teacher_ids, teacher_logits, stats, ...)
   distill_loss(logits, teacher_ids, teacher_logits, ...)  (differentiable)
+  specv_head_loss(hidden, head, targets, ...)
+  specv_head_loss_backward(hidden, head, targets, stats, ...)
+  head_loss(hidden, head, targets, ...)  (differentiable)
 """
 from __future__ import annotations
 
@@ -102,6 +105,15 @@ class DistillArgs(ctypes.Structure):
                 ("grad_loss", _P), ("grad", _P), ("grad_row_stride", _I64), ("row_status", _P)]
 
 
+class HeadArgs(ctypes.Structure):
+    _fields_ = [("N", _I32), ("V", _I32), ("D", _I32), ("dtype", _I32),
+                ("hidden", _P), ("hidden_stride", _I64), ("head", _P), ("head_stride", _I64),
+                ("targets", _P), ("weights", _P), ("scale", ctypes.c_float),
+                ("loss", _P), ("stats", _P), ("row_status", _P), ("grad_loss", _P),
+                ("grad_hidden", _P), ("grad_hidden_stride", _I64),
+                ("grad_head", _P), ("grad_head_stride", _I64)]
+
+
 class SpecvError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"specv status {status}: {msg}")
@@ -152,6 +164,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.POINTER(args), _P]
+    lib.specv_head_workspace_bytes.restype = ctypes.c_size_t
+    lib.specv_head_workspace_bytes.argtypes = [ctypes.POINTER(HeadArgs)]
+    for name in ("specv_head_loss", "specv_head_loss_backward"):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.POINTER(HeadArgs), _P, ctypes.c_size_t, _P]
     lib.specv_status_string.restype = ctypes.c_char_p
     lib.specv_status_string.argtypes = [ctypes.c_int]
     lib.specv_last_error.restype = ctypes.c_char_p
@@ -519,15 +537,15 @@ def _current_device() -> int:
     return torch._C._cuda_getDevice()
 
 
-def _launch(fn, args, stream, at):
+def _launch(fn, args, stream, at, *space):
     """The entry point fn on device `at`, where its operands lie: a kernel goes to
     the current device, whatever device its stream or its pointers are of."""
     if at < 0 or at == _current_device():
-        _check(fn(ctypes.byref(args), _raw_stream(stream, at)))
+        _check(fn(ctypes.byref(args), *space, _raw_stream(stream, at)))
         return
     import torch
     with torch.cuda.device(at):
-        _check(fn(ctypes.byref(args), _raw_stream(stream, at)))
+        _check(fn(ctypes.byref(args), *space, _raw_stream(stream, at)))
 
 
 def _cuda(t, what, at=None):
@@ -749,3 +767,134 @@ def distill_loss(logits, teacher_ids, teacher_logits, *, teacher_lse=None, tempe
         _DistillLoss = DistillLoss
     return _DistillLoss.apply(logits, teacher_ids, teacher_logits, teacher_lse, temperature, weights,
                               tail)
+
+
+def _work(need, workspace, device, stream):
+    """The workspace's pointer, its size in bytes, and what keeps it.  Where none is given one
+    is allocated, as the stream's own that the call goes to."""
+    import torch
+    if workspace is None:
+        if stream is None or device.type != "cuda":
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    else:
+        assert workspace.is_contiguous() and workspace.device == device, f"workspace must be contiguous, on {device}"
+    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+
+
+def _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head):
+    import torch
+    assert hidden.dim() == 2 and head.dim() == 2 and hidden.shape[1] == head.shape[1], (
+        f"hidden [N, D] and head [V, D], got {tuple(hidden.shape)} and {tuple(head.shape)}")
+    code = _dtype_code(hidden)
+    assert head.dtype == hidden.dtype, f"hidden is {hidden.dtype}, head {head.dtype}"
+    (N, D), V, at = hidden.shape, head.shape[0], hidden.get_device()
+    _cuda(hidden, "hidden")
+    _cuda(head, "head", at)
+    for grad, like, what in ((grad_hidden, hidden, "grad_hidden"), (grad_head, head, "grad_head")):
+        if grad is not None:
+            assert grad.shape == like.shape and grad.dtype == like.dtype, f"{what} must be like what it is the gradient of"
+            _cuda(grad, what, at)
+    of = lambda t: (None, 0) if t is None else (t.data_ptr(), _stride(t, 0, D))  # noqa: E731
+    return HeadArgs(N, V, D, code, *of(hidden), *of(head), _of(targets, (N,), torch.int32, "targets", at),
+                    _of(weights, (N,), torch.float32, "weights", at), float(scale), None, None, None, None,
+                    *of(grad_hidden), *of(grad_head))
+
+
+def specv_head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None, with_grad: bool = False,
+                    loss=None, stats=None, row_status=None, grad_hidden=None, grad_head=None,
+                    workspace=None, stream=None) -> dict:
+    """Cross entropy of the tokens `targets` under softmax(scale * hidden @ head.T), without
+    the logits in memory (see include/specv.h, specv_head_loss).
+
+    hidden [N, D] and head [V, D] (bf16, CUDA, last dim contiguous); targets int32 [N] (-1: a
+    row that is left out); weights fp32 [N] or None.  Returns loss fp32 [N], stats fp32 [N, 2]
+    (the row's log-sum-exp and minus the target's log-probability), row_status int32 [N], and
+    with with_grad, or where a buffer is given, grad_hidden and grad_head (of loss.sum()).
+    """
+    import torch
+    N, dev, at = hidden.shape[0], hidden.device, hidden.get_device()
+    if with_grad:  # (not empty_like: that keeps gaps between strided rows)
+        grad_hidden = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev) if grad_hidden is None else grad_hidden
+        grad_head = torch.empty(head.shape, dtype=head.dtype, device=dev) if grad_head is None else grad_head
+    loss = torch.empty(N, dtype=torch.float32, device=dev) if loss is None else loss
+    stats = torch.empty((N, 2), dtype=torch.float32, device=dev) if stats is None else stats
+    row_status = torch.empty(N, dtype=torch.int32, device=dev) if row_status is None else row_status
+    args = _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head)
+    args.loss = _of(loss, (N,), torch.float32, "loss", at)
+    args.stats = _of(stats, (N, 2), torch.float32, "stats", at)
+    args.row_status = _of(row_status, (N,), torch.int32, "row_status", at)
+    lib = load_library()
+    ptr, size, _keep = _work(lib.specv_head_workspace_bytes(ctypes.byref(args)), workspace, dev, stream)
+    _launch(lib.specv_head_loss, args, stream, at, ptr, size)
+    out = dict(loss=loss, stats=stats, row_status=row_status)
+    if grad_hidden is not None:
+        out["grad_hidden"] = grad_hidden
+    if grad_head is not None:
+        out["grad_head"] = grad_head
+    return out
+
+
+def specv_head_loss_backward(hidden, head, targets, stats, *, grad_loss=None, scale: float = 1.0, weights=None,
+                             grad_hidden=None, grad_head=None, row_status=None, workspace=None, stream=None) -> dict:
+    """The gradients of (grad_loss * loss).sum() by hidden and head, from the stats of
+    specv_head_loss on the same inputs (see include/specv.h).  Where one of grad_hidden and
+    grad_head is given, that one alone; else both.  Returns a dict of them."""
+    import torch
+    N, dev, at = hidden.shape[0], hidden.device, hidden.get_device()
+    if grad_hidden is None and grad_head is None:
+        grad_hidden = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev)
+        grad_head = torch.empty(head.shape, dtype=head.dtype, device=dev)
+    args = _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head)
+    args.stats = _of(stats, (N, 2), torch.float32, "stats", at)
+    args.grad_loss = _of(grad_loss, (N,), torch.float32, "grad_loss", at)
+    args.row_status = _of(row_status, (N,), torch.int32, "row_status", at)
+    lib = load_library()
+    ptr, size, _keep = _work(lib.specv_head_workspace_bytes(ctypes.byref(args)), workspace, dev, stream)
+    _launch(lib.specv_head_loss_backward, args, stream, at, ptr, size)
+    out = {}
+    if grad_hidden is not None:
+        out["grad_hidden"] = grad_hidden
+    if grad_head is not None:
+        out["grad_head"] = grad_head
+    return out
+
+
+_HeadLoss = None
+
+
+def head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None):
+    """specv_head_loss's loss per row [N], differentiable with respect to hidden and head
+    (once: the backward pass is specv_head_loss_backward, which computes the logits again).
+    To capture a training step in a CUDA graph, call specv_head_loss with gradient buffers, or
+    specv_head_loss_backward, in it, as for distill_loss."""
+    global _HeadLoss
+    if _HeadLoss is None:
+        import torch
+
+        class HeadLoss(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, hidden, head, targets, scale, weights):
+                out = specv_head_loss(hidden, head, targets, scale=scale, weights=weights)
+                ctx.save_for_backward(hidden, head, targets, weights, out["stats"])
+                ctx.scale = scale
+                return out["loss"]
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, up):
+                hidden, head, targets, weights, stats = ctx.saved_tensors
+                want = {}
+                if ctx.needs_input_grad[0]:
+                    want["grad_hidden"] = torch.empty(hidden.shape, dtype=hidden.dtype, device=hidden.device)
+                if ctx.needs_input_grad[1]:
+                    want["grad_head"] = torch.empty(head.shape, dtype=head.dtype, device=head.device)
+                if want:
+                    specv_head_loss_backward(hidden, head, targets, stats, scale=ctx.scale, weights=weights,
+                                             grad_loss=up.to(torch.float32).contiguous(), **want)
+                return want.get("grad_hidden"), want.get("grad_head"), None, None, None
+
+        _HeadLoss = HeadLoss
+    return _HeadLoss.apply(hidden, head, targets, scale, weights)

@@ -1,0 +1,213 @@
+// The cross entropy of given tokens from hidden states h [N, D] and the head W [V, D],
+// and its gradients, without the logits in memory.
+//
+//   z = s h W^T,  nll_i = log(1 + sum_{v != t} exp(z_iv - z_it)),  lse_i = z_it + nll_i,
+//   dz_iv = g_i exp(z_iv - lse_i), at the target g_i (exp(-nll_i) - 1),
+//   dh = s dz W,  dW = s dz^T h.
+//
+// The target's logit is left out of the sums, so that the loss and the gradient at the
+// target keep their digits where the row is nearly certain.  The forward pass keeps, per
+// row and 128 columns, the largest logit and the sum relative to it (head_stats); a
+// second kernel joins them.  The backward pass computes the logits again, a piece of the
+// vocabulary at a time, turns them into dz (bf16, as the products that read it want it:
+// each element is off by at most 2^-8 of itself) and multiplies that by W and by h.
+// Rows that count for nothing (no target, weight 0) are left out of every product: the
+// others are gathered first.
+#pragma once
+
+#include "product_kernel.cuh"
+
+namespace specv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kPart = kProdHalf;  // columns per partial sum
+
+// What the backward pass knows of a row.
+struct HeadRow {
+  float lse2;  // lse log2(e)
+  float g;     // upstream weight x s; 0: no gradient
+  float at;    // dz at the target
+  int32_t target;
+};
+
+// (smallest of three, NaN ignored)
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The forward pass over a tile: 3.5 operations an element (maximum, minimum and NaN of
+// pairs, one fused multiply-add, one exponential, one addition), under the products of
+// the next tile.
+struct StatsEpi {
+  static constexpr int kStaging = 0;
+  struct Params {
+    const int32_t* target;  // [rows], -1: none
+    float2* part;           // [ceil(V / 128)][ld]: largest accumulator, sum relative to it
+    float* z_target;        // [rows]: the target's accumulator
+    int64_t ld;
+    int32_t V;
+    float c2;               // s log2(e)
+  };
+  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+    if (q.row0 >= q.rows || q.col0 >= e.V) return;
+    const int i = q.row0 + q.lane;
+    const int target = i < q.rows ? e.target[i] : -1;
+    float m = kNegMax, s[4] = {0.f, 0.f, 0.f, 0.f};
+    bool bad = false;
+#pragma unroll 1
+    for (int c = 0; c < kPart; c += 32) {
+      if (q.col0 + c >= e.V) break;
+      float v[32];
+      tmem_load32(q.tmem + c, v);
+      float hi = v[0], lo = v[0];
+#pragma unroll
+      for (int j = 1; j < 31; j += 2) {
+        hi = max3_nan(hi, v[j], v[j + 1]);
+        lo = min3(lo, v[j], v[j + 1]);
+      }
+      hi = max3_nan(hi, v[31], v[31]);
+      lo = fminf(lo, v[31]);
+      bad |= !(hi < pos_inf()) || !(lo > neg_inf());
+      const int at = target - (q.col0 + c), left = e.V - (q.col0 + c);
+      if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) || left < 32) {
+        hi = neg_inf();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j == at) e.z_target[i] = v[j];
+          if (j == at || j >= left) v[j] = neg_inf();
+          hi = fmaxf(hi, v[j]);
+        }
+      }
+      if (hi > m) {
+        const float f = ex2((m - hi) * e.c2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] *= f;
+        m = hi;
+      }
+      if (hi > neg_inf()) {
+        const float mc = -m * e.c2;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], e.c2, mc));
+      }
+    }
+    const float total = (s[0] + s[1]) + (s[2] + s[3]);
+    if (i < q.rows) e.part[static_cast<int64_t>(q.col0 / kPart) * e.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
+  }
+};
+
+// dz of a tile in bf16.
+struct ProbEpi {
+  static constexpr int kStaging = 4096;
+  struct Params {
+    Out16 out;
+    const HeadRow* row;  // [rows]
+    int32_t first;       // the piece's first token
+    float c2;
+  };
+  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+    // (the rows up to a multiple of 64 are read along K by the product for dW: zeros)
+    const int rows = max((q.rows + kProdBK - 1) / kProdBK * kProdBK, kProdBK);
+    if (q.row0 >= rows) return;
+    const int i = q.row0 + q.lane;
+    HeadRow r = {0.f, 0.f, 0.f, -1};
+    if (i < q.rows) {
+      const float4 x = *reinterpret_cast<const float4*>(e.row + i);
+      r = {x.x, x.y, x.z, __float_as_int(x.w)};
+    }
+#pragma unroll 1
+    for (int c = 0; c < kProdHalf; c += 64) {
+      if (q.col0 + c >= e.out.cols) break;
+      uint32_t w[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_load32(q.tmem + c + 32 * h, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fmaf(v[j], e.c2, -r.lse2));
+        const int at = r.target - e.first - (q.col0 + c + 32 * h);
+        if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u || r.g == 0.f)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = r.g == 0.f ? 0.f : j == at ? r.at : v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+      }
+      put16(e.out, q.staging, q.lane, q.row0, q.col0 + c, 0, rows, w);
+    }
+  }
+};
+
+// Joins a maximum and a sum relative to it (sums of nothing: kNegMax, 0).
+__device__ __forceinline__ void soft_join(float& m, float& s, float m2, float s2, float c) {
+  const float M = fmaxf(m, m2);
+  s = s * ex2((m - M) * c) + s2 * ex2((m2 - M) * c);
+  m = M;
+}
+
+// ---- rows
+
+struct HeadRowsParams {
+  int32_t N, V, D, gathered;  // gathered: rows without weight are left out
+  const int32_t* target;
+  const float* weight;     // optional
+  const float* up;         // optional (backward)
+  const float* stats;      // backward: [N, 2]; forward: null
+  float scale;
+  int32_t* count;          // rows in use
+  int32_t* place;          // [N]: a row's place among those in use, or -1
+  int32_t* source;         // [N]: and back
+  int32_t* use_target;     // [N], by place
+  HeadRow* row;            // [N], by place (backward)
+};
+
+constexpr int kRowsThreads = 1024;
+
+struct HeadGatherParams {
+  int32_t N, D, pad_to;    // rows up to a multiple of pad_to behind those in use are zeros
+  int32_t vec;             // source rows start at 16-byte boundaries
+  int32_t* bad;            // optional [N], by place: 1 for a row with an entry that is not finite; it becomes zeros
+  const int32_t* count;    // optional: rows in use
+  const int32_t* source;   // optional: by place
+  const uint16_t* in;
+  int64_t in_stride;
+  uint16_t* out;
+  int64_t out_stride;      // a multiple of 8
+};
+
+constexpr int kGatherThreads = 256;
+
+struct HeadJoinParams {
+  int32_t N, V, parts;
+  const float2* part;
+  const float* z_target;
+  int64_t ld;
+  float scale;
+  const int32_t* place;    // optional (null: a row is where it is)
+  const int32_t* target;
+  const float* weight;     // optional
+  const int32_t* bad;      // optional, by place: rows with entries that are not finite
+  const int32_t* err;      // [errs] of the forward pass
+  int32_t errs;
+  float* loss;
+  float* stats;            // [N, 2]
+  int32_t* status;         // optional
+  HeadRow* row;            // optional, by place: what the gradient's kernels read
+};
+
+constexpr int kJoinThreads = 256;
+
+struct HeadFinishParams {
+  int32_t N, D, splits;
+  const float* sum;        // [splits][rows][ld]
+  int64_t ld, split_stride;
+  const int32_t* place;    // optional
+  const HeadRow* row;      // by place
+  uint16_t* out;
+  int64_t stride;
+  int32_t vec;
+};
+
+}  // namespace specv

@@ -1,0 +1,223 @@
+// The kernels of the head's loss: products with their epilogues, and the rows around them.
+#include "head_kernel.cuh"
+#include "head_launch.cuh"
+#include "product_launch.cuh"
+
+namespace specv {
+
+__global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRowsParams p) {
+  __shared__ int warps[32];
+  __shared__ int before;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) before = 0;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  for (int first = 0; first < p.N; first += kRowsThreads) {
+    const int r = first + threadIdx.x;
+    bool use = false;
+    HeadRow row = {0.f, 0.f, 0.f, -1};
+    if (r < p.N) {
+      const int t = p.target[r];
+      const float w = p.weight ? p.weight[r] : 1.f;
+      use = t >= 0 && t < p.V && w != 0.f;
+      if (p.stats) {
+        const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
+        use = use && lse - lse == 0.f && nll - nll == 0.f;
+        if (use) {
+          const float g = w * (p.up ? p.up[r] : 1.f) * p.scale;
+          row = {lse * kLog2e, g, g * expm1f(-nll), t};
+        }
+      }
+      if (use) row.target = t;
+    }
+    int at = r;
+    if (p.gathered) {
+      const unsigned votes = __ballot_sync(0xffffffffu, use);
+      if (lane == 0) warps[warp] = __popc(votes);
+      __syncthreads();
+      if (warp == 0) {
+        const int n = warps[lane];
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        warps[lane] = before + x - n;
+        __syncwarp();
+        if (lane == 31) before += x;
+      }
+      __syncthreads();
+      at = use ? warps[warp] + __popc(votes & ((1u << lane) - 1)) : -1;
+      __syncthreads();
+    }
+    if (r < p.N) {
+      p.place[r] = at;
+      if (at >= 0) {
+        p.source[at] = r;
+        p.use_target[at] = row.target;
+        if (p.row) p.row[at] = row;
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) *p.count = p.gathered ? before : p.N;
+}
+
+// A row of 16-bit values per CTA: the rows in use brought together at 16-byte boundaries.
+// Bound by bytes (2 x 2 D per row).
+__global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadGatherParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int n = p.count ? *p.count : p.N;
+  const int all = (n + p.pad_to - 1) / p.pad_to * p.pad_to;
+  for (int i = blockIdx.x; i < max(all, p.pad_to); i += gridDim.x) {
+    uint16_t* out = p.out + i * p.out_stride;
+    const int D8 = (p.D + 7) / 8;
+    const uint16_t* in = i < n ? p.in + static_cast<int64_t>(p.source ? p.source[i] : i) * p.in_stride : nullptr;
+    auto get = [&](int j) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (!in) return v;
+      if (p.vec && 8 * j + 8 <= p.D) return __ldg(reinterpret_cast<const uint4*>(in) + j);
+      uint32_t h[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = 8 * j + k < p.D ? in[8 * j + k] : 0u;
+      return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    };
+    bool bad = false;
+    if (p.bad && in) {
+      for (int j = threadIdx.x; j < D8; j += kGatherThreads) {
+        const uint4 v = get(j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bad |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+    bad = __syncthreads_or(bad);
+    if (p.bad && in && threadIdx.x == 0) p.bad[i] = bad;
+    for (int j = threadIdx.x; j < D8; j += kGatherThreads)
+      reinterpret_cast<uint4*>(out)[j] = bad ? make_uint4(0, 0, 0, 0) : get(j);
+  }
+}
+
+// RB rows per CTA, 256 / RB threads each: the parts of a row joined, its loss and what the
+// backward pass reads.
+template <int RB>
+__global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinParams p) {
+  constexpr int T = kJoinThreads / RB;
+  __shared__ float2 got[kJoinThreads];
+  __shared__ int failed;
+  if (threadIdx.x == 0) failed = 0;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.errs; i += kJoinThreads)
+    if (p.err[i]) failed = 1;
+  const int r = blockIdx.x * RB + threadIdx.x % RB, k = threadIdx.x / RB;
+  const int t = r < p.N ? p.target[r] : -1;
+  const float w = r < p.N && p.weight ? p.weight[r] : 1.f;
+  const bool use = t >= 0 && t < p.V && w != 0.f;
+  const int at = r < p.N ? (p.place ? p.place[r] : r) : -1;
+  const float c2 = p.scale * kLog2e;
+  float m = kNegMax, s = 0.f;
+  if (use && at >= 0) {
+    for (int j = k; j < p.parts; j += T) {
+      const float2 x = p.part[j * p.ld + at];
+      soft_join(m, s, x.x, x.y, c2);
+    }
+  }
+  got[threadIdx.x] = make_float2(m, s);
+  __syncthreads();
+#pragma unroll
+  for (int o = T / 2; o > 0; o >>= 1) {
+    if (k < o) {
+      const float2 x = got[threadIdx.x + o * RB];
+      soft_join(m, s, x.x, x.y, c2);
+      got[threadIdx.x] = make_float2(m, s);
+    }
+    __syncthreads();
+  }
+  if (k != 0 || r >= p.N) return;
+  float lse = 0.f, nll = 0.f, loss = 0.f;
+  int status = t < -1 || t >= p.V ? kBadToken : 0;
+  HeadRow row = {0.f, 0.f, 0.f, -1};
+  if (use) {
+    const float zt = p.z_target[at], d2 = (m - zt) * c2;
+    // (relative to the target's logit where that is the largest, else to the largest of the others)
+    nll = s == 0.f ? 0.f : d2 <= 0.f ? log1pf(s * exp2f(d2)) : d2 * kLn2 + logf(s + exp2f(-d2));
+    lse = p.scale * zt + nll;
+    if (failed) status |= kTimeout;
+    if (p.bad && p.bad[at]) status |= kNonFinite;
+    if (!(s - s == 0.f) || !(lse - lse == 0.f)) status |= kNonFinite;
+    if (status) {
+      lse = nll = __int_as_float(0x7fc00000);
+    } else {
+      loss = w * nll;
+      const float g = w * p.scale;
+      row = {lse * kLog2e, g, g * expm1f(-nll), t};
+    }
+  }
+  p.loss[r] = loss;
+  if (p.stats) {
+    p.stats[2 * r] = lse;
+    p.stats[2 * r + 1] = nll;
+  }
+  if (p.status) p.status[r] = status;
+  if (p.row && at >= 0) p.row[at] = row;
+}
+
+// dh from the sums of K's parts, rows back in their places.
+__global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int D8 = (p.D + 7) / 8;
+  const int64_t all = static_cast<int64_t>(p.N) * D8;
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < all; x += static_cast<int64_t>(gridDim.x) * 256) {
+    const int r = static_cast<int>(x / D8), j = static_cast<int>(x - static_cast<int64_t>(r) * D8) * 8;
+    const int at = p.place ? p.place[r] : r;
+    float v[8] = {};
+    if (at >= 0 && p.row[at].g != 0.f) {
+      for (int k = 0; k < p.splits; ++k) {
+        const float* in = p.sum + k * p.split_stride + at * p.ld + j;
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(in)), b = __ldcs(reinterpret_cast<const float4*>(in) + 1);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+    }
+    uint16_t* out = p.out + r * p.stride + j;
+    const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    if (p.vec && j + 8 <= p.D) {
+      *reinterpret_cast<uint4*>(out) = w;
+    } else {
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+      for (int k = 0; k < min(8, p.D - j); ++k) out[k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+    }
+  }
+}
+
+cudaError_t launch_head_stats(ProductParams& p, const StatsEpi::Params& e, cudaStream_t s) {
+  return launch_product<false, false, StatsEpi>(p, e, s);
+}
+cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s) {
+  return launch_product<false, false, ProbEpi>(p, e, s);
+}
+cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s) {
+  return launch_product<false, true, SumEpi>(p, e, s);
+}
+cudaError_t launch_head_head(ProductParams& p, const StoreEpi::Params& e, cudaStream_t s) {
+  return launch_product<true, true, StoreEpi>(p, e, s);
+}
+cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t s) {
+  return launch_grid(head_rows_kernel, 1, kRowsThreads, s, p);
+}
+cudaError_t launch_head_gather(const HeadGatherParams& p, int blocks, cudaStream_t s) {
+  return launch_grid(head_gather_kernel, blocks, kGatherThreads, s, p);
+}
+cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t s) {
+  return p.N <= 1024 ? launch_grid(head_join_kernel<1>, p.N, kJoinThreads, s, p)
+                     : launch_grid(head_join_kernel<32>, (p.N + 31) / 32, kJoinThreads, s, p);
+}
+cudaError_t launch_head_finish(const HeadFinishParams& p, int blocks, cudaStream_t s) {
+  return launch_grid(head_finish_kernel, blocks, 256, s, p);
+}
+
+}  // namespace specv

@@ -1,0 +1,500 @@
+// Matrix products on the tensor cores with a fused epilogue: C = A B^T over tiles of
+// 256 x 256, for the head's loss and for orthogonalised updates.
+//
+// A pair of CTAs (one cluster, two SMs) computes a tile with tcgen05.mma.cta_group::2:
+// each CTA brings 128 rows of A and 128 rows of B, so each operand byte that is loaded
+// serves both SMs (one CTA alone would need 96 bytes a clock of its 128 x 256 tile from
+// L2, a pair needs 64 per SM), and holds 128 rows of the fp32 accumulator in its tensor
+// memory.  The accumulator has two stages of 256 columns: the epilogue of one tile runs
+// under the products of the next.  Warps of a CTA: 0-7 epilogue (warp w reads tensor
+// memory lanes 32 (w % 4), columns 128 (w / 4)), 8 loads, 9 issues the products (in the
+// first CTA of the pair).  Clusters take tiles in a fixed order, so that results do not
+// depend on timing.
+//
+// Operands are 16-bit, either "K-major" (rows of A or B contiguous along K) or
+// "MN-major" (contiguous along M or N: the transposed matrix as it lies in memory), in
+// shared memory under the 128-byte swizzle that TMA writes and the tensor core reads.
+// A tile's K is cut into blocks of 64; TMA fills what lies outside of a matrix with zeros.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "specv_common.cuh"
+
+namespace specv {
+
+constexpr int kProdTile = 256;              // rows and columns of a cluster's tile
+constexpr int kProdHalf = kProdTile / 2;    // rows of A, and of B, that one CTA loads
+constexpr int kProdBK = 64;                 // K per stage: 128 bytes, the width of the swizzle
+constexpr int kProdEpiWarps = 8;
+constexpr int kProdThreads = 32 * (kProdEpiWarps + 2);
+constexpr int kOperandBytes = kProdHalf * kProdBK * 2;  // 16 KB
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kProdBarrierBytes = 256;
+constexpr int kProdSmemMost = 227 * 1024;
+
+// Stages that fit beside STAGING bytes per epilogue warp, and all of a CTA's bytes.
+template <int STAGING>
+constexpr int kProdStages = (kProdSmemMost - 1024 - kProdBarrierBytes - kProdEpiWarps * STAGING) / kStageBytes;
+template <int STAGING>
+constexpr int kProdSmem = 1024 + kProdBarrierBytes + kProdEpiWarps * STAGING + kProdStages<STAGING> * kStageBytes;
+
+struct ProductParams {
+  CUtensorMap a, b;
+  int32_t M, N, K;         // the largest sizes (host), N exact
+  const int32_t* rows;     // device: the number of rows in use, in the place of M (rows_k: of K)
+  int32_t rows_k;
+  int32_t tn;              // tiles along N
+  int32_t batch, splits;   // splits: parts of K that are summed apart
+  int32_t symmetric;       // M == N, C symmetric: only tiles on and above the diagonal
+  uint32_t idesc;
+  int32_t late_wait;       // the previous launch is waited for at the end alone
+  int32_t* err;            // [clusters]: 0, or 1 where a wait ran out
+  int32_t* status;         // optional [status_n]: a wait that ran out is added (kTimeout)
+  int32_t status_n;
+  int32_t stall;           // test hook: 1 + the unit whose first copy is late
+};
+
+// Instruction descriptor of tcgen05.mma kind::f16 for 256 x 256 tiles, fp32 accumulators.
+constexpr uint32_t prod_idesc(bool bf16, bool a_mn, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(kProdTile >> 3) << 17) | (static_cast<uint32_t>(kProdTile >> 4) << 24);
+}
+
+// ---- instructions
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The shared::cluster address of `addr` in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// A box into this CTA's shared memory; its bytes count on `bar`, which may be the pair's other CTA's.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void tma_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void tma_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_all(uint32_t at) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes: thread l gets row l.
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(at)
+      : "memory");
+}
+
+// Shared-memory descriptor of an operand under the 128-byte swizzle (version 1, layout
+// type 2).  K-major: groups of 8 rows are 1024 bytes apart.  MN-major: a group of 64
+// along M or N is [64 (K)][128 bytes]; groups of 8 along K are 1024 bytes apart, groups
+// of 64 along M or N 8192.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  constexpr uint64_t lead = MN ? (kProdBK * 128) >> 4 : 1, stride = 1024 >> 4;
+  return (static_cast<uint64_t>(addr >> 4) & 0x3fff) | (lead << 16) | (stride << 32) | (1ull << 46) | (2ull << 61);
+}
+// The step from 16 of K to the next, in the descriptor's 16-byte units.
+template <bool MN>
+constexpr uint64_t kOperandStep = MN ? (16 * 128) >> 4 : (16 * 2) >> 4;
+
+// ---- units of work
+
+struct Unit {
+  int m, n, z, split, k0, k1;  // first row, first column, matrix, blocks of K
+};
+
+struct Units {
+  int tm, tn, per, blocks, count, splits, symmetric;
+  __device__ __forceinline__ Units(const ProductParams& p) {
+    int M = p.M, K = p.K;
+    if (p.rows) (p.rows_k ? K : M) = *p.rows;
+    // (without any row one tile is computed all the same: its zeros are read)
+    tm = max((M + kProdTile - 1) / kProdTile, 1);
+    tn = p.tn;
+    splits = p.splits;
+    symmetric = p.symmetric;
+    blocks = max((K + kProdBK - 1) / kProdBK, 1);
+    per = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * splits;
+    count = per * p.batch;
+  }
+  // Rows in groups of 16 tiles, along which the tile index runs first: clusters that run
+  // at the same time share columns of B, and the group's rows of A stay in L2.
+  __device__ __forceinline__ Unit at(int u) const {
+    Unit r;
+    r.z = u / per;
+    int t = u - r.z * per;
+    r.split = t % splits;
+    t /= splits;
+    int i, j;
+    if (symmetric) {
+      for (i = 0; t >= tn - i; ++i) t -= tn - i;
+      j = i + t;
+    } else {
+      constexpr int kGroup = 16;
+      const int g = t / (kGroup * tn), rows = min(tm - g * kGroup, kGroup);
+      t -= g * kGroup * tn;
+      i = g * kGroup + t % rows;
+      j = t / rows;
+    }
+    r.m = i * kProdTile;
+    r.n = j * kProdTile;
+    r.k0 = static_cast<int>(static_cast<int64_t>(blocks) * r.split / splits);
+    r.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (r.split + 1) / splits);
+    return r;
+  }
+};
+
+// What an epilogue warp is given: its 32 rows (one per lane) and 128 columns of a tile.
+struct EpiTile {
+  uint32_t tmem;      // of its first column
+  uint8_t* staging;   // its own, 1024-byte aligned
+  int row0, col0;     // its first row and column in C
+  int z, split, lane;
+  int rows;           // rows in use (M)
+  Unit unit;
+};
+
+// A bounded wait (about two seconds); false once any wait of the CTA ran out.
+__device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, volatile int* gone) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 0; it < (1u << 21); ++it) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (*gone) return false;
+    if (clock64() - t0 > 4000000000LL) break;
+  }
+  *gone = 1;
+  return false;
+}
+
+template <bool A_MN, bool B_MN, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
+    product_kernel(const __grid_constant__ ProductParams p, const __grid_constant__ typename Epi::Params e) {
+  constexpr int S = kProdStages<Epi::kStaging>;  // 6 with a 4 KB box per epilogue warp
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* staging = base + S * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kProdEpiWarps * Epi::kStaging);
+  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* gone = reinterpret_cast<volatile int*>(tmem_at + 1);
+  static_assert((2 * S + 5) * 8 + 8 <= kProdBarrierBytes, "barriers");
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);   // the first CTA's loader; both CTAs' bytes
+      mbar_init(&empty[s], 1);  // the products that read the stage
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 2 * kProdEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *gone = 0;
+    fence_mbar_init();
+    prefetch_map(&p.a);
+    prefetch_map(&p.b);
+  }
+  if (warp == kProdEpiWarps + 1) tmem_alloc_all(smem_u32(tmem_at));
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  if (!p.late_wait) pdl_wait_primary();
+  pdl_launch_dependents();
+
+  const Units units(p);
+  if (warp == kProdEpiWarps) {  // ---- loads
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int u = cluster; ok && u < units.count; u += clusters) {
+        const Unit t = units.at(u);
+        for (int k = t.k0; k < t.k1; ++k, ++it) {
+          const int s = it % S;
+          if (it >= S && !prod_wait(&empty[s], ((it / S) & 1) ^ 1, gone)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0)
+            mbar_arrive_expect_tx(&full[s], 2 * kStageBytes + ((p.stall == u + 1 && k == t.k0) ? 16 : 0));
+          const uint32_t bar = in_first_cta(smem_u32(&full[s]));
+          const uint32_t sa = smem_u32(base + s * kStageBytes), sb = sa + kOperandBytes;
+          const int kk = k * kProdBK, m = t.m + static_cast<int>(rank) * kProdHalf, n = t.n + static_cast<int>(rank) * kProdHalf;
+          if (A_MN) {
+            tma_load(sa, &p.a, m, kk, t.z, bar);
+            tma_load(sa + kOperandBytes / 2, &p.a, m + 64, kk, t.z, bar);
+          } else {
+            tma_load(sa, &p.a, kk, m, t.z, bar);
+          }
+          if (B_MN) {
+            tma_load(sb, &p.b, n, kk, t.z, bar);
+            tma_load(sb + kOperandBytes / 2, &p.b, n + 64, kk, t.z, bar);
+          } else {
+            tma_load(sb, &p.b, kk, n, t.z, bar);
+          }
+        }
+      }
+      // (a CTA leaves after every arrival at its barriers)
+      for (int i = max(0, it - S); ok && i < it; ++i) ok = prod_wait(&empty[i % S], (i / S) & 1, gone);
+      if (!ok && rank == 0) {  // copies in flight land before the CTAs leave
+        const long long t0 = clock64();
+        for (int i = max(0, it - S); i < it; ++i)
+          while (!mbar_try_wait_sleep(&full[i % S], (i / S) & 1, 20000u) && clock64() - t0 < 1000000000LL) {
+          }
+      }
+    }
+  } else if (warp == kProdEpiWarps + 1) {  // ---- products
+    if (lane == 0 && rank == 0) {
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int u = cluster; ok && u < units.count; u += clusters, ++n) {
+        const Unit t = units.at(u);
+        const int acc = n & 1;
+        if (n >= 2 && !prod_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, gone)) break;
+        tc_fence_after();
+        for (int k = t.k0; k < t.k1; ++k, ++it) {
+          const int s = it % S;
+          if (!prod_wait(&full[s], (it / S) & 1, gone)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(base + s * kStageBytes);
+          const uint64_t da = operand_desc<A_MN>(sa), db = operand_desc<B_MN>(sa + kOperandBytes);
+#pragma unroll
+          for (int j = 0; j < kProdBK / 16; ++j)
+            tc_mma(tmem + acc * kProdTile, da + j * kOperandStep<A_MN>, db + j * kOperandStep<B_MN>, p.idesc,
+                   k > t.k0 || j > 0);
+          tc_commit_pair(smem_u32(&empty[s]));
+        }
+        if (ok) tc_commit_pair(smem_u32(&tfull[acc]));
+      }
+      if (*gone) {  // products in flight end before tensor memory is freed
+        tc_commit_pair(smem_u32(drain));
+        const long long t0 = clock64();
+        while (!mbar_try_wait_sleep(drain, 0, 20000u) && clock64() - t0 < 1000000000LL) {
+        }
+      }
+    }
+  } else {  // ---- epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    int n = 0;
+    for (int u = cluster; u < units.count; u += clusters, ++n) {
+      const Unit t = units.at(u);
+      const int acc = n & 1;
+      if (!__all_sync(0xffffffffu, prod_wait(&tfull[acc], (n >> 1) & 1, gone))) break;
+      tc_fence_after();
+      EpiTile q;
+      q.tmem = tmem + acc * kProdTile + half * kProdHalf + (static_cast<uint32_t>(quarter * 32) << 16);
+      q.staging = staging + warp * Epi::kStaging;
+      q.row0 = t.m + static_cast<int>(rank) * kProdHalf + quarter * 32;
+      q.col0 = t.n + half * kProdHalf;
+      q.z = t.z;
+      q.split = t.split;
+      q.lane = lane;
+      q.unit = t;
+      q.rows = p.rows && !p.rows_k ? *p.rows : p.M;
+      Epi::tile(e, q);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(in_first_cta(smem_u32(&tempty[acc])));
+    }
+    if (Epi::kStaging > 0 && lane == 0) tma_wait_all();
+  }
+  __syncwarp();
+  if (p.late_wait) pdl_wait_primary();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kProdEpiWarps + 1) tmem_free_all(tmem);
+  const int failed = *gone;
+  if (threadIdx.x == 0 && p.err) p.err[blockIdx.x] = failed;
+  if (failed && p.status)
+    for (int i = threadIdx.x; i < p.status_n; i += kProdThreads) atomicOr(&p.status[i], kTimeout);
+}
+
+// ---- what epilogues share
+
+// 64 columns of 16-bit values (pairs) of this lane's row into the warp's staging buffer,
+// then out by TMA (`map`: boxes of 64 x 32 under the 128-byte swizzle), or, where C's rows
+// do not start at 16-byte boundaries, row by row from shared memory.
+struct Out16 {
+  CUtensorMap map;
+  uint16_t* direct;          // not null: stores without TMA
+  int64_t stride, zstride;   // elements
+  int32_t rows, cols;
+};
+
+__device__ __forceinline__ void stage16(uint8_t* staging, int lane, const uint32_t (&w)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(staging + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+// (rows: those of C in use; row0 and col0 of the 32 x 64 box)
+__device__ __forceinline__ void put16(const Out16& o, uint8_t* staging, int lane, int row0, int col0, int z, int rows,
+                                      const uint32_t (&w)[32]) {
+  if (row0 >= rows || col0 >= o.cols) return;
+  if (!o.direct) {
+    if (lane == 0) tma_wait_read<0>();
+    __syncwarp();
+    stage16(staging, lane, w);
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store(&o.map, col0, row0, z, smem_u32(staging));
+      tma_commit();
+    }
+    return;
+  }
+  __syncwarp();
+  stage16(staging, lane, w);
+  __syncwarp();
+  const int n = min(rows - row0, 32);
+  uint16_t* out = o.direct + z * o.zstride + static_cast<int64_t>(row0) * o.stride + col0;
+  const int width = min(o.cols - col0, 64);
+  for (int r = 0; r < n; ++r) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(staging + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+    if (2 * lane < width) out[r * o.stride + 2 * lane] = static_cast<uint16_t>(v);
+    if (2 * lane + 1 < width) out[r * o.stride + 2 * lane + 1] = static_cast<uint16_t>(v >> 16);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// C = alpha A B^T in bf16.
+struct StoreEpi {
+  static constexpr int kStaging = 4096;
+  struct Params {
+    Out16 out;
+    float alpha;
+  };
+  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+#pragma unroll 1
+    for (int c = 0; c < kProdHalf; c += 64) {
+      uint32_t w[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_load32(q.tmem + c + 32 * h, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16(v[2 * j] * e.alpha, v[2 * j + 1] * e.alpha);
+      }
+      put16(e.out, q.staging, q.lane, q.row0, q.col0 + c, q.z, q.rows, w);
+    }
+  }
+};
+
+// C in fp32 (boxes of 32 x 32), stored or added to what is there; a part of K (split)
+// goes to its own matrix.
+struct SumEpi {
+  static constexpr int kStaging = 4096;
+  struct Params {
+    CUtensorMap out;  // [splits][rows][cols]
+    int32_t cols;
+    int32_t add;
+  };
+  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+#pragma unroll 1
+    for (int c = 0; c < kProdHalf; c += 32) {
+      float v[32];
+      tmem_load32(q.tmem + c, v);
+      if (q.row0 >= q.rows || q.col0 + c >= e.cols) continue;
+      if (q.lane == 0) tma_wait_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(q.staging + q.lane * 128 + ((j ^ (q.lane & 7)) << 4)) =
+            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      fence_async_shared();
+      __syncwarp();
+      if (q.lane == 0) {
+        if (e.add)
+          tma_add(&e.out, q.col0 + c, q.row0, q.split, smem_u32(q.staging));
+        else
+          tma_store(&e.out, q.col0 + c, q.row0, q.split, smem_u32(q.staging));
+        tma_commit();
+      }
+    }
+  }
+};
+
+}  // namespace specv
