@@ -516,6 +516,40 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
                                       void* stream);
 
 /*
+ * Updates with their singular values drawn towards one (the step that a drafter's weight
+ * matrices take, in the place of their gradient or momentum G): for each of B matrices
+ * [m, n],  X = G / |G|_F, then `steps` times
+ *   X <- a X + (b S + c S S) X,  S = X X^T  (rows the longer side: a X + X (b S + c S S), S = X^T X)
+ * out = X in bf16; norm[k] = |G|_F.  With (3.4445, -4.7750, 2.0315) five steps bring singular
+ * values from 0.01 |G|_F on to between 0.7 and 1.2.
+ * Products are of fp16 operands, summed in fp32; X is kept to 21 bits beside them: out is off
+ * the exact steps by about 2e-3 of its norm at most, most of it the rounding to bf16
+ * (low-rank and badly scaled updates too).
+ * A matrix of zeros gives zeros.  Status of a matrix: SPECV_ROW_NONFINITE (an entry that is
+ * NaN or infinite): out 0, norm NaN; SPECV_ROW_DEVICE_TIMEOUT, on every matrix: out undefined.
+ * Coefficients that may let a singular value grow past 1024 within the steps (by bounds over
+ * [0, 1]) are refused with SPECV_ERR_INVALID_ARG.
+ * out may be update itself (bf16).  workspace: device memory of
+ * specv_orthogonalize_workspace_bytes() bytes (8 m n + 4 min(m, n)^2 per matrix, about),
+ * 256-byte aligned.
+ */
+typedef struct {
+  int32_t B, m, n;
+  int32_t dtype;               /* specv_dtype, of update */
+  const void* update;          /* matrix k at k * batch_stride, its row i at i * row_stride */
+  int64_t batch_stride, row_stride;          /* elements */
+  int32_t steps;               /* 1..32 */
+  float a, b, c;
+  void* out;                   /* OUT, bf16 */
+  int64_t out_batch_stride, out_row_stride;  /* elements */
+  float* norm;                 /* OUT, optional [B] */
+  int32_t* row_status;         /* OUT, optional [B] */
+} specv_orth_args;
+
+size_t specv_orthogonalize_workspace_bytes(int32_t B, int32_t m, int32_t n);
+specv_status specv_orthogonalize(const specv_orth_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Geometric fan-out ("Speculative Speculative Decoding" Theorem 12, proved in
  * Appendix A.2).  For a drafter with per-token acceptance rate a (0 < a < 1)
  * whose cache-miss probability at fan-out F is F^-r (r > 0), the fan-outs

@@ -20,6 +20,7 @@ Entry points (same names as the C ABI):
   specv_head_loss(hidden, head, targets, ...)
   specv_head_loss_backward(hidden, head, targets, stats, ...)
   head_loss(hidden, head, targets, ...)  (differentiable)
+  specv_orthogonalize(update, ...)
 """
 from __future__ import annotations
 
@@ -114,6 +115,13 @@ class HeadArgs(ctypes.Structure):
                 ("grad_head", _P), ("grad_head_stride", _I64)]
 
 
+class OrthArgs(ctypes.Structure):
+    _fields_ = [("B", _I32), ("m", _I32), ("n", _I32), ("dtype", _I32),
+                ("update", _P), ("batch_stride", _I64), ("row_stride", _I64), ("steps", _I32),
+                ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("out", _P), ("out_batch_stride", _I64), ("out_row_stride", _I64), ("norm", _P), ("row_status", _P)]
+
+
 class SpecvError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"specv status {status}: {msg}")
@@ -166,10 +174,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.argtypes = [ctypes.POINTER(args), _P]
     lib.specv_head_workspace_bytes.restype = ctypes.c_size_t
     lib.specv_head_workspace_bytes.argtypes = [ctypes.POINTER(HeadArgs)]
-    for name in ("specv_head_loss", "specv_head_loss_backward"):
+    lib.specv_orthogonalize_workspace_bytes.restype = ctypes.c_size_t
+    lib.specv_orthogonalize_workspace_bytes.argtypes = [_I32, _I32, _I32]
+    for name, args in (("specv_head_loss", HeadArgs), ("specv_head_loss_backward", HeadArgs),
+                       ("specv_orthogonalize", OrthArgs)):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
-        fn.argtypes = [ctypes.POINTER(HeadArgs), _P, ctypes.c_size_t, _P]
+        fn.argtypes = [ctypes.POINTER(args), _P, ctypes.c_size_t, _P]
     lib.specv_status_string.restype = ctypes.c_char_p
     lib.specv_status_string.argtypes = [ctypes.c_int]
     lib.specv_last_error.restype = ctypes.c_char_p
@@ -898,3 +909,34 @@ def head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None):
 
         _HeadLoss = HeadLoss
     return _HeadLoss.apply(hidden, head, targets, scale, weights)
+
+
+def specv_orthogonalize(update, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), out=None, norm=None,
+                        row_status=None, workspace=None, stream=None) -> dict:
+    """An update with its singular values drawn towards one, by `steps` of X <- a X + (b S +
+    c S S) X with S = X X^T from X = update / |update|_F (see include/specv.h).
+
+    update [m, n], or [B, m, n] for B matrices (bf16 or fp32, CUDA, last dim contiguous).
+    Returns orthogonal (bf16, shaped as update; `out`, which may be update itself), norm fp32
+    and row_status int32 (scalars, or [B])."""
+    import torch
+    assert update.dim() in (2, 3), "update must be [m, n] or [B, m, n]"
+    flat, dev, at = update.dim() == 2, update.device, update.get_device()
+    lead = update.shape[:-2]
+    code = _dtype_code(update)
+    if out is None:
+        out = torch.empty(update.shape, dtype=torch.bfloat16, device=dev)
+    norm = torch.empty(lead, dtype=torch.float32, device=dev) if norm is None else norm
+    row_status = torch.empty(lead, dtype=torch.int32, device=dev) if row_status is None else row_status
+    _cuda(update, "update")
+    assert out.shape == update.shape and out.dtype == torch.bfloat16, "out must be bfloat16, shaped as update"
+    _cuda(out, "out", at)
+    B, (m, n) = 1 if flat else update.shape[0], update.shape[-2:]
+    a, b, c = (float(x) for x in coefficients)
+    strides = lambda t: (m * n if flat else _stride(t, 0, m * n), _stride(t, -2, n))  # noqa: E731
+    args = OrthArgs(B, m, n, code, update.data_ptr(), *strides(update), int(steps), a, b, c, out.data_ptr(), *strides(out),
+                    _of(norm, lead, torch.float32, "norm", at), _of(row_status, lead, torch.int32, "row_status", at))
+    lib = load_library()
+    ptr, size, _keep = _work(lib.specv_orthogonalize_workspace_bytes(B, m, n), workspace, dev, stream)
+    _launch(lib.specv_orthogonalize, args, stream, at, ptr, size)
+    return dict(orthogonal=out, norm=norm, row_status=row_status)

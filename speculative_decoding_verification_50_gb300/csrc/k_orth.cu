@@ -1,0 +1,183 @@
+// The kernels of the orthogonalised update.
+#include "orth_launch.cuh"
+#include "product_launch.cuh"
+
+namespace specv {
+
+namespace {
+
+__device__ __forceinline__ void squares_join(ScaledSquares& a, const ScaledSquares& b) {
+  const float m = fmaxf(a.m, b.m), x = a.m / m, y = b.m / m;  // (powers of two)
+  a.s = a.s * (x * x) + b.s * (y * y);
+  a.m = m;
+}
+__device__ __forceinline__ ScaledSquares squares_shfl(const ScaledSquares& a, int o) {
+  return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o)};
+}
+__device__ __forceinline__ void squares_warp(ScaledSquares& a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) squares_join(a, squares_shfl(a, o));
+}
+
+constexpr float kSquaresLeast = 1.17549435e-38f;  // 2^-126
+
+template <int VW>
+__device__ __forceinline__ void squares_add(ScaledSquares& a, float& inv, const float (&x)[VW]) {
+  float most = 0.f;
+#pragma unroll
+  for (int k = 0; k < VW; ++k) most = fmaxf(most, fabsf(x[k]));
+  if (most >= 2.f * a.m) {
+    // the power of two at or below it (infinity: its own, and the sum becomes NaN)
+    const float m = __uint_as_float(__float_as_uint(most) & 0x7f800000u);
+    const float f = a.m / m;
+    a.s *= f * f;
+    a.m = m;
+    inv = 1.f / m;
+  }
+#pragma unroll
+  for (int k = 0; k < VW; ++k) {
+    const float y = x[k] * inv;
+    a.s = fmaf(y, y, a.s);
+  }
+}
+
+// Vector j of a row: VW elements, zeros past its end.
+template <int DT>
+__device__ __forceinline__ void row_vec(const void* row, int j, int cols, bool vec, float (&x)[Elem<DT>::VW]) {
+  constexpr int VW = Elem<DT>::VW;
+  if (vec && (j + 1) * VW <= cols) {
+    Elem<DT>::unpack(Elem<DT>::vec(row, j * VW), x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < VW; ++k) x[k] = j * VW + k < cols ? Elem<DT>::scalar(row, j * VW + k) : 0.f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ const void* row_at(const OrthInParams& p, int z, int r) {
+  return static_cast<const char*>(p.in) + (z * p.batch_stride + r * p.row_stride) * Elem<DT>::ES;
+}
+
+}  // namespace
+
+// Sums of squares of a matrix's parts, at the scale of their largest entries (neither tiny
+// nor huge entries leave fp32's range).  Bound by bytes.
+template <int DT>
+__global__ void __launch_bounds__(kOrthThreads) orth_squares_kernel(const OrthInParams p) {
+  __shared__ ScaledSquares warps[kOrthThreads / 32];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  constexpr int VW = Elem<DT>::VW;
+  const int z = blockIdx.y, nv = (p.cols + VW - 1) / VW;
+  ScaledSquares a = {kSquaresLeast, 0.f};
+  float inv = 1.f / kSquaresLeast;
+  const int64_t all = static_cast<int64_t>(p.rows) * nv;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x; i < all;
+       i += static_cast<int64_t>(gridDim.x) * kOrthThreads) {
+    const int r = static_cast<int>(i / nv), j = static_cast<int>(i - static_cast<int64_t>(r) * nv);
+    float x[VW];
+    row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec, x);
+    squares_add<VW>(a, inv, x);
+  }
+  squares_warp(a);
+  if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kOrthThreads / 32; ++k) squares_join(a, warps[k]);
+    p.part[z * p.blocks + blockIdx.x] = a;
+  }
+}
+
+// X = G / |G| in fp16 and what that leaves out; zeros for a matrix that is zero, or not
+// finite (flagged).
+template <int DT>
+__global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInParams p) {
+  __shared__ ScaledSquares sum;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  constexpr int VW = Elem<DT>::VW;
+  const int z = blockIdx.y;
+  if (threadIdx.x < 32) {
+    ScaledSquares a = {kSquaresLeast, 0.f};
+    for (int k = threadIdx.x; k < p.blocks; k += 32) squares_join(a, p.part[z * p.blocks + k]);
+    squares_warp(a);
+    if (threadIdx.x == 0) sum = a;
+  }
+  __syncthreads();
+  const float root = sqrtf(sum.s);
+  const bool bad = !(sum.s < pos_inf());
+  const float inv = 1.f / sum.m, f = bad || sum.s == 0.f ? 0.f : p.scale / root;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (p.norm) p.norm[z] = bad ? __int_as_float(0x7fc00000) : sum.m * root;
+    if (p.status) p.status[z] = bad ? kNonFinite : 0;
+  }
+  const int nv = static_cast<int>(p.ld / VW);
+  const int64_t all = static_cast<int64_t>(p.rows) * nv;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x; i < all;
+       i += static_cast<int64_t>(gridDim.x) * kOrthThreads) {
+    const int r = static_cast<int>(i / nv), j = static_cast<int>(i - static_cast<int64_t>(r) * nv);
+    float x[VW];
+    row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec, x);
+    uint32_t hi[VW / 2], lo[VW / 2];
+#pragma unroll
+    for (int k = 0; k < VW / 2; ++k) {
+      const float u = bad ? 0.f : x[2 * k] * inv * f, v = bad ? 0.f : x[2 * k + 1] * inv * f;
+      hi[k] = pack_f16(u, v);
+      const float2 g = unpack_f16(hi[k]);
+      lo[k] = pack_f16(u - g.x, v - g.y);
+    }
+    const int64_t at = (static_cast<int64_t>(z) * p.rows + r) * p.ld + j * VW;
+    if constexpr (VW == 8) {
+      *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    } else {
+      *reinterpret_cast<uint2*>(p.hi + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(p.lo + at) = make_uint2(lo[0], lo[1]);
+    }
+  }
+}
+
+namespace {
+
+template <typename Kern>
+cudaError_t launch_in(Kern k, const OrthInParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(p.batch), 1);
+  cfg.blockDim = dim3(kOrthThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
+}  // namespace
+
+cudaError_t launch_orth_squares(int dtype, const OrthInParams& p, cudaStream_t s) {
+  return dtype == SPECV_BF16 ? launch_in(orth_squares_kernel<0>, p, s) : launch_in(orth_squares_kernel<1>, p, s);
+}
+cudaError_t launch_orth_scale(int dtype, const OrthInParams& p, cudaStream_t s) {
+  return dtype == SPECV_BF16 ? launch_in(orth_scale_kernel<0>, p, s) : launch_in(orth_scale_kernel<1>, p, s);
+}
+template <bool FINE>
+cudaError_t launch_orth_gram(bool mn, ProductParams& p, const typename SymEpi<false, FINE>::Params& e, cudaStream_t s) {
+  return mn ? launch_product<true, true, SymEpi<false, FINE>>(p, e, s) : launch_product<false, false, SymEpi<false, FINE>>(p, e, s);
+}
+template <bool FINE>
+cudaError_t launch_orth_poly(ProductParams& p, const typename SymEpi<true, FINE>::Params& e, cudaStream_t s) {
+  return launch_product<false, false, SymEpi<true, FINE>>(p, e, s);
+}
+template cudaError_t launch_orth_gram<false>(bool, ProductParams&, const SymEpi<false, false>::Params&, cudaStream_t);
+template cudaError_t launch_orth_gram<true>(bool, ProductParams&, const SymEpi<false, true>::Params&, cudaStream_t);
+template cudaError_t launch_orth_poly<false>(ProductParams&, const SymEpi<true, false>::Params&, cudaStream_t);
+template cudaError_t launch_orth_poly<true>(ProductParams&, const SymEpi<true, true>::Params&, cudaStream_t);
+cudaError_t launch_orth_step(bool mn, ProductParams& p, const StepEpi<false>::Params& e, cudaStream_t s) {
+  return mn ? launch_product<false, true, StepEpi<false>>(p, e, s) : launch_product<false, false, StepEpi<false>>(p, e, s);
+}
+cudaError_t launch_orth_last(bool mn, ProductParams& p, const StepEpi<true>::Params& e, cudaStream_t s) {
+  return mn ? launch_product<false, true, StepEpi<true>>(p, e, s) : launch_product<false, false, StepEpi<true>>(p, e, s);
+}
+
+}  // namespace specv

@@ -1,0 +1,252 @@
+// C ABI of the orthogonalised update: argument checks, the workspace, bounds on the
+// singular values, and the launches on the caller's stream.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api.cuh"
+#include "orth_launch.cuh"
+#include "product_launch.cuh"
+
+using namespace specv;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int64_t up_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+constexpr int kMostSteps = 32;
+constexpr double kMostGrowth = 1024;
+
+// The largest |a x + b x^3 + c x^5| for x in [0, r], and |b t + c t^2| for t in [0, r^2].
+double step_bound(double a, double b, double c, double r) {
+  auto f = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + t * c))); };
+  double most = f(r * r);
+  const double A = 5 * c, B = 3 * b, C = a, disc = B * B - 4 * A * C;
+  for (double t : {A != 0 && disc >= 0 ? (-B + std::sqrt(disc)) / (2 * A) : -1.0,
+                   A != 0 && disc >= 0 ? (-B - std::sqrt(disc)) / (2 * A) : -1.0, A == 0 && B != 0 ? -C / B : -1.0})
+    if (t > 0 && t < r * r) most = std::max(most, f(t));
+  return most;
+}
+double poly_bound(double b, double c, double r) {
+  auto g = [&](double t) { return std::fabs(t * (b + t * c)); };
+  double most = g(r * r);
+  const double t = c != 0 ? -b / (2 * c) : -1.0;
+  if (t > 0 && t < r * r) most = std::max(most, g(t));
+  return most;
+}
+// The power of two by which a matrix of entries up to `most` is kept in fp16 (up to 32768,
+// half of its range: the bounds hold for exact steps).
+double keep_scale(double most) { return std::exp2(std::floor(std::log2(32768.0 / std::max(most, 1e-30)))); }
+
+struct OrthSpace {
+  size_t part, hi[2], lo[2], gram[2], poly[2], bytes;  // (of S and P: fp16, and what that leaves out)
+  int64_t ld, lds;  // strides of X, of S and P
+  int32_t s, t, blocks;
+  bool tall, fine;
+};
+
+OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
+  OrthSpace w = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  w.tall = m > n;
+  w.s = std::min(m, n), w.t = std::max(m, n);
+  w.ld = up_to(n, 8), w.lds = up_to(w.s, 8);
+  // blocks of the passes over G: 8 vectors a thread, four blocks an SM over the batch at most
+  const int64_t vectors = static_cast<int64_t>(m) * ((n + 3) / 4);
+  w.blocks = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min((vectors + 8 * kOrthThreads - 1) / (8 * kOrthThreads), std::max<int64_t>(1, 8LL * api_sm_count() / B))));
+  w.part = take(sizeof(ScaledSquares) * static_cast<size_t>(B) * w.blocks);
+  const size_t x = 2 * static_cast<size_t>(B) * m * w.ld, q = 2 * static_cast<size_t>(B) * w.s * w.lds;
+  for (int k = 0; k < 2; ++k) w.hi[k] = take(x), w.lo[k] = take(x);
+  w.fine = w.s <= kProdTile;
+  for (int k = 0; k <= w.fine; ++k) w.gram[k] = take(q), w.poly[k] = take(q);
+  w.bytes = at;
+  return w;
+}
+
+specv_status check_orth(const specv_orth_args* a) {
+  if (!a) return api_fail(SPECV_ERR_INVALID_ARG, "args is NULL");
+  if (a->B < 0) return api_fail(SPECV_ERR_INVALID_ARG, "B=%d < 0", a->B);
+  if (a->m < 1 || a->n < 1) return api_fail(SPECV_ERR_INVALID_ARG, "m=%d, n=%d: less than 1", a->m, a->n);
+  if (a->dtype != SPECV_BF16 && a->dtype != SPECV_FP32)
+    return api_fail(SPECV_ERR_INVALID_ARG, "dtype=%d is not SPECV_BF16 or SPECV_FP32", a->dtype);
+  if (a->steps < 1 || a->steps > kMostSteps)
+    return api_fail(SPECV_ERR_INVALID_ARG, "steps=%d outside [1, %d]", a->steps, kMostSteps);
+  if (!std::isfinite(a->a) || !std::isfinite(a->b) || !std::isfinite(a->c))
+    return api_fail(SPECV_ERR_INVALID_ARG, "a coefficient is not finite");
+  double r = 1;
+  for (int k = 0; k < a->steps; ++k) {
+    r = 1.01 * step_bound(a->a, a->b, a->c, r);
+    if (!(r <= kMostGrowth))
+      return api_fail(SPECV_ERR_INVALID_ARG, "coefficients (%g, %g, %g) may let singular values grow past %g in %d steps",
+                      static_cast<double>(a->a), static_cast<double>(a->b), static_cast<double>(a->c), kMostGrowth, a->steps);
+  }
+  if (a->B == 0) return SPECV_OK;
+  if (!a->update || !a->out) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(a->update, a->dtype == SPECV_BF16 ? 2 : 4) || !aligned(a->out, 2) || !aligned(a->norm, 4) ||
+      !aligned(a->row_status, 4))
+    return api_fail(SPECV_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  if (a->m > 1 && (a->row_stride < a->n || a->out_row_stride < a->n))
+    return api_fail(SPECV_ERR_INVALID_ARG, "row stride smaller than n");
+  if (a->B > 1 && (a->batch_stride < (a->m - 1) * a->row_stride + a->n ||
+                   a->out_batch_stride < (a->m - 1) * a->out_row_stride + a->n))
+    return api_fail(SPECV_ERR_INVALID_ARG, "batch stride too small for %d rows", a->m);
+  const int64_t tiles = up_to(a->m, kProdTile) / kProdTile * (up_to(a->n, kProdTile) / kProdTile);
+  if (tiles * a->B > (1 << 30) || a->B > 65535) return api_fail(SPECV_ERR_UNSUPPORTED, "B, m and n too large");
+  return SPECV_OK;
+}
+
+#define TRY(x)                       \
+  do {                               \
+    const specv_status st_ = (x);    \
+    if (st_ != SPECV_OK) return st_; \
+  } while (0)
+
+struct OrthRun {
+  const specv_orth_args* a;
+  OrthSpace w;
+  uint8_t* ws;
+  cudaStream_t s;
+  int launches = 0;
+
+  uint16_t* at(size_t off) const { return reinterpret_cast<uint16_t*>(ws + off); }
+  specv_status done(cudaError_t e, const char* what) {
+    if (e != cudaSuccess) return api_fail(SPECV_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    ++launches;
+    return SPECV_OK;
+  }
+  ProductParams product(int32_t M, int32_t N, int32_t K, bool a_mn, bool b_mn, bool symmetric) const {
+    ProductParams p = {};
+    p.M = M, p.N = N, p.K = K, p.batch = a->B, p.splits = 1, p.symmetric = symmetric, p.fine = w.fine;
+    p.tn = static_cast<int32_t>(up_to(N, kProdTile) / kProdTile);
+    p.idesc = prod_idesc(false, a_mn, b_mn);
+    p.status = a->row_status, p.status_n = a->B;
+    return p;
+  }
+  int64_t zx() const { return a->m * w.ld; }
+  int64_t zs() const { return w.s * w.lds; }
+  specv_status x_map(CUtensorMap* m, bool mn, size_t off) const {
+    return operand_map(m, false, mn, at(off), a->n, a->m, a->B, w.ld, zx());
+  }
+  specv_status s_map(CUtensorMap* m, size_t off) const {
+    return operand_map(m, false, false, at(off), w.s, w.s, a->B, w.lds, zs());
+  }
+  specv_status out_map(Out16& o, size_t off, int64_t cols, int64_t rows, int64_t ld) const {
+    o.cols = static_cast<int32_t>(cols);
+    return product_map(&o.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at(off), cols, rows, a->B, 2 * ld, 2 * rows * ld, 32);
+  }
+
+  // S, then P = b S + c S S
+  template <bool FINE>
+  specv_status symmetric(int from, double sx, double ss, double sp) {
+    {
+      ProductParams p = product(w.s, w.s, w.t, w.tall, w.tall, true);
+      TRY(x_map(&p.a, w.tall, w.hi[from]));
+      if (FINE) TRY(x_map(&p.a_low, w.tall, w.lo[from]));
+      p.b = p.a, p.b_low = p.a_low;
+      typename SymEpi<false, FINE>::Params e = {};
+      TRY(sym_out(e, w.gram, FINE));
+      e.alpha = static_cast<float>(ss / (sx * sx));
+      TRY(done(launch_orth_gram<FINE>(w.tall, p, e, s), "orthogonalize-gram"));
+    }
+    ProductParams p = product(w.s, w.s, w.s, false, false, true);
+    TRY(s_map(&p.a, w.gram[0]));
+    if (FINE) TRY(s_map(&p.a_low, w.gram[1]));
+    p.b = p.a, p.b_low = p.a_low;
+    typename SymEpi<true, FINE>::Params e = {};
+    TRY(sym_out(e, w.poly, FINE));
+    e.chi = at(w.gram[0]), e.clo = at(w.gram[FINE]);
+    e.alpha = static_cast<float>(a->c * sp / (ss * ss)), e.beta = static_cast<float>(a->b * sp / ss);
+    return done(launch_orth_poly<FINE>(p, e, s), "orthogonalize-poly");
+  }
+  template <typename Params>
+  specv_status sym_out(Params& e, const size_t (&to)[2], bool fine) const {
+    TRY(out_map(e.hi, to[0], w.s, w.s, w.lds));
+    if (fine) TRY(out_map(e.lo, to[1], w.s, w.s, w.lds));
+    e.mirror_hi = at(to[0]), e.mirror_lo = at(to[fine]);
+    e.ld = w.lds, e.zstride = zs(), e.n = w.s;
+    return SPECV_OK;
+  }
+
+  specv_status all() {
+    double r = 1, sx = keep_scale(r);
+    {
+      OrthInParams p = {};
+      p.rows = a->m, p.cols = a->n, p.batch = a->B, p.blocks = w.blocks;
+      p.in = a->update, p.row_stride = a->m > 1 ? a->row_stride : a->n, p.batch_stride = a->B > 1 ? a->batch_stride : 0;
+      const int vw = a->dtype == SPECV_BF16 ? 8 : 4;
+      p.vec = aligned(a->update, 16) && p.row_stride % vw == 0 && p.batch_stride % vw == 0;
+      p.part = reinterpret_cast<ScaledSquares*>(ws + w.part);
+      p.hi = at(w.hi[0]), p.lo = at(w.lo[0]), p.ld = w.ld, p.scale = static_cast<float>(sx);
+      p.norm = a->norm, p.status = a->row_status;
+      TRY(done(launch_orth_squares(a->dtype, p, s), "orthogonalize-norm"));
+      TRY(done(launch_orth_scale(a->dtype, p, s), "orthogonalize-scale"));
+    }
+    for (int k = 0; k < a->steps; ++k) {
+      const int from = k & 1;
+      const bool last = k + 1 == a->steps;
+      const double ss = keep_scale(r * r), sp = keep_scale(poly_bound(a->b, a->c, r));
+      const double next = 1.01 * step_bound(a->a, a->b, a->c, r), sn = last ? 1.0 : keep_scale(next);
+      TRY(w.fine ? symmetric<true>(from, sx, ss, sp) : symmetric<false>(from, sx, ss, sp));
+      // X' = a X + P X, or a X + X P (P is its own transpose)
+      ProductParams p = product(a->m, a->n, w.s, false, !w.tall, false);
+      TRY(s_map(w.tall ? &p.b : &p.a, w.poly[0]));
+      TRY(x_map(w.tall ? &p.a : &p.b, !w.tall, w.hi[from]));
+      if (w.fine) {
+        TRY(s_map(w.tall ? &p.b_low : &p.a_low, w.poly[1]));
+        TRY(x_map(w.tall ? &p.a_low : &p.b_low, !w.tall, w.lo[from]));
+      }
+      const float alpha = static_cast<float>(sn / (sp * sx)), beta = static_cast<float>(a->a * sn / sx);
+      if (!last) {
+        StepEpi<false>::Params e = {};
+        TRY(out_map(e.hi, w.hi[from ^ 1], a->n, a->m, w.ld));
+        TRY(out_map(e.lo, w.lo[from ^ 1], a->n, a->m, w.ld));
+        e.xhi = at(w.hi[from]), e.xlo = at(w.lo[from]), e.ld = w.ld, e.zstride = zx();
+        e.rows = a->m, e.cols = a->n, e.alpha = alpha, e.beta = beta;
+        TRY(done(launch_orth_step(!w.tall, p, e, s), "orthogonalize-step"));
+      } else {
+        StepEpi<true>::Params e = {};
+        const int64_t rs = a->m > 1 ? a->out_row_stride : up_to(a->n, 8), bs = a->B > 1 ? a->out_batch_stride : 0;
+        e.hi.cols = a->n, e.hi.stride = rs, e.hi.zstride = bs;
+        if (aligned(a->out, 16) && rs % 8 == 0 && bs % 8 == 0)
+          TRY(product_map(&e.hi.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, a->n, a->m, a->B, 2 * rs, 2 * bs, 32));
+        else
+          e.hi.direct = static_cast<uint16_t*>(a->out);
+        e.xhi = at(w.hi[from]), e.xlo = at(w.lo[from]), e.ld = w.ld, e.zstride = zx();
+        e.rows = a->m, e.cols = a->n, e.alpha = alpha, e.beta = beta;
+        TRY(done(launch_orth_last(!w.tall, p, e, s), "orthogonalize-last"));
+      }
+      r = next, sx = sn;
+    }
+    return SPECV_OK;
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t specv_orthogonalize_workspace_bytes(int32_t B, int32_t m, int32_t n) {
+  if (B < 1 || m < 1 || n < 1) return 0;
+  return orth_space(B, m, n).bytes;
+}
+
+specv_status specv_orthogonalize(const specv_orth_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+  api_done(0);
+  TRY(check_orth(a));
+  if (a->B == 0) return api_done(0);
+  OrthRun run = {a, orth_space(a->B, a->m, a->n), static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
+  if (!workspace || workspace_bytes < run.w.bytes)
+    return api_fail(SPECV_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu", run.w.bytes, workspace ? workspace_bytes : 0);
+  if (!aligned(workspace, 256)) return api_fail(SPECV_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  TRY(run.all());
+  return api_done(run.launches);
+}
+
+}  // extern "C"

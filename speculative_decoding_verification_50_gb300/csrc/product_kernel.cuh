@@ -43,6 +43,8 @@ constexpr int kProdSmem = 1024 + kProdBarrierBytes + kProdEpiWarps * STAGING + k
 
 struct ProductParams {
   CUtensorMap a, b;
+  CUtensorMap a_low, b_low;  // fine: what a and b leave out
+  int32_t fine;              // C = A B^T + A B_low^T + A_low B^T, one after the other
   int32_t M, N, K;         // the largest sizes (host), N exact
   const int32_t* rows;     // device: the number of rows in use, in the place of M (rows_k: of K)
   int32_t rows_k;
@@ -166,7 +168,7 @@ struct Unit {
 };
 
 struct Units {
-  int tm, tn, per, blocks, count, splits, symmetric;
+  int tm, tn, per, span, blocks, count, splits, symmetric;  // span: blocks of K; blocks: with the parts of a fine product
   __device__ __forceinline__ Units(const ProductParams& p) {
     int M = p.M, K = p.K;
     if (p.rows) (p.rows_k ? K : M) = *p.rows;
@@ -175,7 +177,8 @@ struct Units {
     tn = p.tn;
     splits = p.splits;
     symmetric = p.symmetric;
-    blocks = max((K + kProdBK - 1) / kProdBK, 1);
+    span = max((K + kProdBK - 1) / kProdBK, 1);
+    blocks = p.fine ? 3 * span : span;
     per = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * splits;
     count = per * p.batch;
   }
@@ -288,18 +291,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
             mbar_arrive_expect_tx(&full[s], 2 * kStageBytes + ((p.stall == u + 1 && k == t.k0) ? 16 : 0));
           const uint32_t bar = in_first_cta(smem_u32(&full[s]));
           const uint32_t sa = smem_u32(base + s * kStageBytes), sb = sa + kOperandBytes;
-          const int kk = k * kProdBK, m = t.m + static_cast<int>(rank) * kProdHalf, n = t.n + static_cast<int>(rank) * kProdHalf;
+          const int part = p.fine ? k / units.span : 0;
+          const CUtensorMap *pa = part == 2 ? &p.a_low : &p.a, *pb = part == 1 ? &p.b_low : &p.b;
+          const int kk = (k - part * units.span) * kProdBK, m = t.m + static_cast<int>(rank) * kProdHalf, n = t.n + static_cast<int>(rank) * kProdHalf;
           if (A_MN) {
-            tma_load(sa, &p.a, m, kk, t.z, bar);
-            tma_load(sa + kOperandBytes / 2, &p.a, m + 64, kk, t.z, bar);
+            tma_load(sa, pa, m, kk, t.z, bar);
+            tma_load(sa + kOperandBytes / 2, pa, m + 64, kk, t.z, bar);
           } else {
-            tma_load(sa, &p.a, kk, m, t.z, bar);
+            tma_load(sa, pa, kk, m, t.z, bar);
           }
           if (B_MN) {
-            tma_load(sb, &p.b, n, kk, t.z, bar);
-            tma_load(sb + kOperandBytes / 2, &p.b, n + 64, kk, t.z, bar);
+            tma_load(sb, pb, n, kk, t.z, bar);
+            tma_load(sb + kOperandBytes / 2, pb, n + 64, kk, t.z, bar);
           } else {
-            tma_load(sb, &p.b, kk, n, t.z, bar);
+            tma_load(sb, pb, kk, n, t.z, bar);
           }
         }
       }
