@@ -27,12 +27,16 @@ int64_t piece_tokens(int32_t N, int32_t V) {
   return up_to((V + pieces - 1) / pieces, kProdTile);
 }
 
-// Parts that K (a piece's tokens) is cut into for dh, whose tiles alone would leave SMs
-// without work: three tiles per pair of SMs, parts of 8 blocks at least, 32 parts at most.
+// Parts that K (a piece's tokens) is cut into for dh, whose tiles alone are few: eight units
+// for each pair of SMs, so that a last round that is not full costs little (4096 x 4096 of
+// 128256 tokens, 0.7 of the rows in use: 192 tiles on 76 pairs), in parts of 64 blocks at
+// least; of 8 blocks at least as long as there are not two units a pair.
 int hidden_splits(int32_t N, int32_t D, int64_t tokens) {
   const int64_t tiles = up_to(N, kProdTile) / kProdTile * (up_to(D, kProdTile) / kProdTile);
   const int64_t pairs = api_sm_count() / 2, blocks = tokens / kProdBK;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(3 * pairs + tiles - 1) / tiles, blocks / 8, 32})));
+  const int64_t fine = std::min((8 * pairs + tiles - 1) / tiles, blocks / 64);
+  const int64_t few = std::min<int64_t>({(2 * pairs + tiles - 1) / tiles, blocks / 8, 32});
+  return static_cast<int>(std::max<int64_t>({1, fine, few}));
 }
 
 // Offsets of the workspace's parts (bytes; all multiples of 256).
@@ -188,7 +192,7 @@ struct HeadRun {
     TRY(head_map(&p.b, false, 0, a->V));
     p.err = at<int32_t>(w.err);
     p.stall = api_test_stall('E');
-    StatsEpi::Params e = {};
+    HeadStatsParams e = {};
     e.target = w.gather ? at<int32_t>(w.target) : a->targets;
     e.part = at<float2>(w.part), e.ld = w.ld, e.z_target = at<float>(w.z_target);
     e.V = a->V, e.c2 = a->scale * kLog2e;

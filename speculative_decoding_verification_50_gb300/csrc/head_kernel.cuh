@@ -38,60 +38,96 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return d;
 }
 
+struct HeadStatsParams {
+  const int32_t* target;  // [rows], -1: none
+  float2* part;           // [ceil(V / 128)][ld]: largest accumulator, sum relative to it
+  float* z_target;        // [rows]: the target's accumulator
+  int64_t ld;
+  int32_t V;
+  float c2;               // s log2(e)
+};
+
 // The forward pass over a tile: 3.5 operations an element (maximum, minimum and NaN of
 // pairs, one fused multiply-add, one exponential, one addition), under the products of
-// the next tile.
-struct StatsEpi {
-  static constexpr int kStaging = 0;
-  struct Params {
-    const int32_t* target;  // [rows], -1: none
-    float2* part;           // [ceil(V / 128)][ld]: largest accumulator, sum relative to it
-    float* z_target;        // [rows]: the target's accumulator
-    int64_t ld;
-    int32_t V;
-    float c2;               // s log2(e)
+// the next tile.  The tensor core cuts each sum off (towards zero), so that the error of a
+// long sum grows with its length: sums over more than kStatsChunk blocks of K are taken in
+// chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum).
+constexpr int kStatsChunk = 16;
+template <bool LONG>
+struct StatsEpi : PlainEpi {
+  static constexpr bool kChunks = LONG;
+  struct State {
+    float v[LONG ? kPart : 1];
   };
-  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+  static __device__ __forceinline__ void start(State& sum) {
+    if constexpr (LONG) {
+#pragma unroll
+      for (int j = 0; j < kPart; ++j) sum.v[j] = 0.f;
+    }
+  }
+  static __device__ __forceinline__ void add(EpiTile& q, State& sum) {
+    if constexpr (LONG) {
+#pragma unroll
+      for (int c = 0; c < kPart; c += 32) {
+        float v[32];
+        tmem_load32(q.tmem + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum.v[c + j] += v[j];
+      }
+    }
+  }
+  static constexpr int kStaging = 0;
+  using Params = HeadStatsParams;
+  // 32 columns: `at` is the target's place among them, `left` of them are the vocabulary's.
+  static __device__ __forceinline__ void part32(const Params& e, float (&v)[32], int i, int at, int left, float& m, float (&s)[4],
+                                                bool& bad) {
+    if (left <= 0) return;
+    float hi = v[0], lo = v[0];
+#pragma unroll
+    for (int j = 1; j < 31; j += 2) {
+      hi = max3_nan(hi, v[j], v[j + 1]);
+      lo = min3(lo, v[j], v[j + 1]);
+    }
+    hi = max3_nan(hi, v[31], v[31]);
+    lo = fminf(lo, v[31]);
+    bad |= !(hi < pos_inf()) || !(lo > neg_inf());
+    if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) || left < 32) {
+      hi = neg_inf();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (j == at) e.z_target[i] = v[j];
+        if (j == at || j >= left) v[j] = neg_inf();
+        hi = fmaxf(hi, v[j]);
+      }
+    }
+    if (hi > m) {
+      const float f = ex2((m - hi) * e.c2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] *= f;
+      m = hi;
+    }
+    if (hi > neg_inf()) {
+      const float mc = -m * e.c2;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], e.c2, mc));
+    }
+  }
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State& sum) {
     if (q.row0 >= q.rows || q.col0 >= e.V) return;
     const int i = q.row0 + q.lane;
     const int target = i < q.rows ? e.target[i] : -1;
     float m = kNegMax, s[4] = {0.f, 0.f, 0.f, 0.f};
     bool bad = false;
-#pragma unroll 1
+#pragma unroll(LONG ? kPart / 32 : 1)
     for (int c = 0; c < kPart; c += 32) {
-      if (q.col0 + c >= e.V) break;
       float v[32];
-      tmem_load32(q.tmem + c, v);
-      float hi = v[0], lo = v[0];
+      if constexpr (LONG) {
 #pragma unroll
-      for (int j = 1; j < 31; j += 2) {
-        hi = max3_nan(hi, v[j], v[j + 1]);
-        lo = min3(lo, v[j], v[j + 1]);
+        for (int j = 0; j < 32; ++j) v[j] = sum.v[c + j];
+      } else {
+        tmem_load32(q.tmem + c, v);
       }
-      hi = max3_nan(hi, v[31], v[31]);
-      lo = fminf(lo, v[31]);
-      bad |= !(hi < pos_inf()) || !(lo > neg_inf());
-      const int at = target - (q.col0 + c), left = e.V - (q.col0 + c);
-      if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u) || left < 32) {
-        hi = neg_inf();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j == at) e.z_target[i] = v[j];
-          if (j == at || j >= left) v[j] = neg_inf();
-          hi = fmaxf(hi, v[j]);
-        }
-      }
-      if (hi > m) {
-        const float f = ex2((m - hi) * e.c2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] *= f;
-        m = hi;
-      }
-      if (hi > neg_inf()) {
-        const float mc = -m * e.c2;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], e.c2, mc));
-      }
+      part32(e, v, i, target - (q.col0 + c), e.V - (q.col0 + c), m, s, bad);
     }
     const float total = (s[0] + s[1]) + (s[2] + s[3]);
     if (i < q.rows) e.part[static_cast<int64_t>(q.col0 / kPart) * e.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
@@ -99,7 +135,7 @@ struct StatsEpi {
 };
 
 // dz of a tile in bf16.
-struct ProbEpi {
+struct ProbEpi : PlainEpi {
   static constexpr int kStaging = 4096;
   struct Params {
     Out16 out;
@@ -107,7 +143,7 @@ struct ProbEpi {
     int32_t first;       // the piece's first token
     float c2;
   };
-  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
     // (the rows up to a multiple of 64 are read along K by the product for dW: zeros)
     const int rows = max((q.rows + kProdBK - 1) / kProdBK * kProdBK, kProdBK);
     if (q.row0 >= rows) return;

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
     const int at = p.place ? p.place[r] : r;
     float v[8] = {};
     if (at >= 0 && p.row[at].g != 0.f) {
+#pragma unroll 8
       for (int k = 0; k < p.splits; ++k) {
         const float* in = p.sum + k * p.split_stride + at * p.ld + j;
         const float4 a = __ldcs(reinterpret_cast<const float4*>(in)), b = __ldcs(reinterpret_cast<const float4*>(in) + 1);
@@ -194,8 +195,10 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
   }
 }
 
-cudaError_t launch_head_stats(ProductParams& p, const StatsEpi::Params& e, cudaStream_t s) {
-  return launch_product<false, false, StatsEpi>(p, e, s);
+cudaError_t launch_head_stats(ProductParams& p, const HeadStatsParams& e, cudaStream_t s) {
+  if (p.K <= kStatsChunk * kProdBK) return launch_product<false, false, StatsEpi<false>>(p, e, s);
+  p.chunk = kStatsChunk;
+  return launch_product<false, false, StatsEpi<true>>(p, e, s);
 }
 cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s) {
   return launch_product<false, false, ProbEpi>(p, e, s);

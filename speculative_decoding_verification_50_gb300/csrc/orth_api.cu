@@ -137,9 +137,12 @@ struct OrthRun {
   specv_status s_map(CUtensorMap* m, size_t off) const {
     return operand_map(m, false, false, at(off), w.s, w.s, a->B, w.lds, zs());
   }
+  specv_status box_map(CUtensorMap* m, size_t off, int64_t cols, int64_t rows, int64_t ld) const {
+    return product_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at(off), cols, rows, a->B, 2 * ld, 2 * rows * ld, 32);
+  }
   specv_status out_map(Out16& o, size_t off, int64_t cols, int64_t rows, int64_t ld) const {
     o.cols = static_cast<int32_t>(cols);
-    return product_map(&o.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at(off), cols, rows, a->B, 2 * ld, 2 * rows * ld, 32);
+    return box_map(&o.map, off, cols, rows, ld);
   }
 
   // S, then P = b S + c S S
@@ -161,7 +164,8 @@ struct OrthRun {
     p.b = p.a, p.b_low = p.a_low;
     typename SymEpi<true, FINE>::Params e = {};
     TRY(sym_out(e, w.poly, FINE));
-    e.chi = at(w.gram[0]), e.clo = at(w.gram[FINE]);
+    TRY(box_map(&e.chi, w.gram[0], w.s, w.s, w.lds));
+    if (FINE) TRY(box_map(&e.clo, w.gram[1], w.s, w.s, w.lds));
     e.alpha = static_cast<float>(a->c * sp / (ss * ss)), e.beta = static_cast<float>(a->b * sp / ss);
     return done(launch_orth_poly<FINE>(p, e, s), "orthogonalize-poly");
   }
@@ -207,7 +211,8 @@ struct OrthRun {
         StepEpi<false>::Params e = {};
         TRY(out_map(e.hi, w.hi[from ^ 1], a->n, a->m, w.ld));
         TRY(out_map(e.lo, w.lo[from ^ 1], a->n, a->m, w.ld));
-        e.xhi = at(w.hi[from]), e.xlo = at(w.lo[from]), e.ld = w.ld, e.zstride = zx();
+        TRY(box_map(&e.xhi, w.hi[from], a->n, a->m, w.ld));
+        TRY(box_map(&e.xlo, w.lo[from], a->n, a->m, w.ld));
         e.rows = a->m, e.cols = a->n, e.alpha = alpha, e.beta = beta;
         TRY(done(launch_orth_step(!w.tall, p, e, s), "orthogonalize-step"));
       } else {
@@ -218,7 +223,8 @@ struct OrthRun {
           TRY(product_map(&e.hi.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, a->n, a->m, a->B, 2 * rs, 2 * bs, 32));
         else
           e.hi.direct = static_cast<uint16_t*>(a->out);
-        e.xhi = at(w.hi[from]), e.xlo = at(w.lo[from]), e.ld = w.ld, e.zstride = zx();
+        TRY(box_map(&e.xhi, w.hi[from], a->n, a->m, w.ld));
+        TRY(box_map(&e.xlo, w.lo[from], a->n, a->m, w.ld));
         e.rows = a->m, e.cols = a->n, e.alpha = alpha, e.beta = beta;
         TRY(done(launch_orth_last(!w.tall, p, e, s), "orthogonalize-last"));
       }

@@ -43,16 +43,6 @@ struct OrthInParams {
   int32_t* status;                    // optional [batch]
 };
 
-// 64 columns of a 16-bit matrix [..][rows][ld] at this lane's row (ld a multiple of 8, what
-// lies behind it in the row is not used).
-__device__ __forceinline__ void load16(const uint16_t* at, bool row_ok, int left, uint32_t (&w)[32]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row_ok && 8 * j < left) v = *(reinterpret_cast<const uint4*>(at) + j);
-    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-  }
-}
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 // Lanes hold rows: pairs of lanes swap, so that each stores two rows of one column.
@@ -71,17 +61,20 @@ __device__ __forceinline__ void put_mirror(uint16_t* to, int64_t ld, int n, int 
 // A symmetric matrix in fp16 from its upper tiles, alpha A B^T (ADD: + beta C), and (FINE)
 // what fp16 leaves out.
 template <bool ADD, bool FINE>
-struct SymEpi {
+struct SymEpi : PlainEpi {
   static constexpr int kStaging = FINE ? 8192 : 4096;
   struct Params {
     Out16 hi, lo;
     uint16_t *mirror_hi, *mirror_lo;   // the matrices themselves
-    const uint16_t *chi, *clo;         // ADD: [batch][n][ld]
+    CUtensorMap chi, clo;              // ADD: C (boxes of 64 x 32)
     int64_t ld, zstride;
     int32_t n;
     float alpha, beta;
   };
-  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+  static __device__ __forceinline__ void ahead(const Params& e, EpiTile& q) {
+    if (ADD && q.row0 < e.n && q.col0 < e.n) fetch16<FINE>(&e.chi, &e.clo, q, q.col0);
+  }
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
     if (q.row0 >= e.n) return;
     const int row = q.row0 + q.lane;
 #pragma unroll 1
@@ -90,9 +83,11 @@ struct SymEpi {
       if (col >= e.n) break;
       uint32_t w[32], l[32];
       if (ADD) {
-        const int64_t at = q.z * e.zstride + row * e.ld + col;
-        load16(e.chi + at, row < e.n, e.n - col, w);
-        if (FINE) load16(e.clo + at, row < e.n, e.n - col, l);
+        if (c > 0) fetch16<FINE>(&e.chi, &e.clo, q, col);
+        if (!fetched(q)) return;
+        unstage16(q.staging, q.lane, w);
+        if (FINE) unstage16(q.staging + 4096, q.lane, l);
+        __syncwarp();
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -118,8 +113,15 @@ struct SymEpi {
           }
         }
       }
-      put16(e.hi, q.staging, q.lane, q.row0, col, q.z, q.rows, w);
-      if (FINE) put16(e.lo, q.staging + 4096, q.lane, q.row0, col, q.z, q.rows, l);
+      if (FINE) {
+        if (!ADD) {
+          if (q.lane == 0) tma_wait_read<0>();
+          __syncwarp();
+        }
+        put16_pair(e.hi, e.lo, q.staging, q.lane, q.row0, col, q.z, w, l);
+      } else {
+        put16(e.hi, q.staging, q.lane, q.row0, col, q.z, q.rows, w);
+      }
       if (q.unit.m != q.unit.n) {
         put_mirror(e.mirror_hi + q.z * e.zstride, e.ld, e.n, row, q.lane, col, w);
         if (FINE) put_mirror(e.mirror_lo + q.z * e.zstride, e.ld, e.n, row, q.lane, col, l);
@@ -130,26 +132,29 @@ struct SymEpi {
 
 // X' = a X + A B^T, as fp16 and what that leaves out, or (LAST) in bf16.
 template <bool LAST>
-struct StepEpi {
-  static constexpr int kStaging = LAST ? 4096 : 8192;
+struct StepEpi : PlainEpi {
+  static constexpr int kStaging = 8192;
   struct Params {
     Out16 hi, lo;             // LAST: hi alone
-    const uint16_t *xhi, *xlo;
-    int64_t ld, zstride;
+    CUtensorMap xhi, xlo;     // X (boxes of 64 x 32)
     int32_t rows, cols;
     float alpha, beta;        // of the product, of X
   };
-  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+  static __device__ __forceinline__ void ahead(const Params& e, EpiTile& q) {
+    if (q.row0 < e.rows && q.col0 < e.cols) fetch16<true>(&e.xhi, &e.xlo, q, q.col0);
+  }
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
     if (q.row0 >= e.rows) return;
-    const int row = q.row0 + q.lane;
 #pragma unroll 1
     for (int c = 0; c < kProdHalf; c += 64) {
       const int col = q.col0 + c;
       if (col >= e.cols) break;
       uint32_t w[32], l[32];
-      const int64_t at = q.z * e.zstride + row * e.ld + col;
-      load16(e.xhi + at, row < e.rows, e.cols - col, w);
-      load16(e.xlo + at, row < e.rows, e.cols - col, l);
+      if (c > 0) fetch16<true>(&e.xhi, &e.xlo, q, col);
+      if (!fetched(q)) return;
+      unstage16(q.staging, q.lane, w);
+      unstage16(q.staging + 4096, q.lane, l);
+      __syncwarp();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
@@ -167,8 +172,10 @@ struct StepEpi {
           }
         }
       }
-      put16(e.hi, q.staging, q.lane, q.row0, col, q.z, q.rows, w);
-      if (!LAST) put16(e.lo, q.staging + 4096, q.lane, q.row0, col, q.z, q.rows, l);
+      if (LAST)
+        put16(e.hi, q.staging, q.lane, q.row0, col, q.z, q.rows, w);
+      else
+        put16_pair(e.hi, e.lo, q.staging, q.lane, q.row0, col, q.z, w, l);
     }
   }
 };

@@ -29,7 +29,10 @@ constexpr int kProdTile = 256;              // rows and columns of a cluster's t
 constexpr int kProdHalf = kProdTile / 2;    // rows of A, and of B, that one CTA loads
 constexpr int kProdBK = 64;                 // K per stage: 128 bytes, the width of the swizzle
 constexpr int kProdEpiWarps = 8;
-constexpr int kProdThreads = 32 * (kProdEpiWarps + 2);
+constexpr int kProdThreads = 32 * (kProdEpiWarps + 4);
+// Registers a thread: launched with at most 168 (12 warps), of which the last four warps
+// give up most to the epilogue's: 2 x 216 + 72 = 3 x 168.
+constexpr int kEpiRegs = 216, kLoadRegs = 72;
 constexpr int kOperandBytes = kProdHalf * kProdBK * 2;  // 16 KB
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kProdBarrierBytes = 256;
@@ -50,6 +53,7 @@ struct ProductParams {
   int32_t rows_k;
   int32_t tn;              // tiles along N
   int32_t batch, splits;   // splits: parts of K that are summed apart
+  int32_t chunk;           // blocks of K per accumulator (0: all): the epilogue adds up several
   int32_t symmetric;       // M == N, C symmetric: only tiles on and above the diagonal
   uint32_t idesc;
   int32_t late_wait;       // the previous launch is waited for at the end alone
@@ -87,6 +91,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// A box into this CTA's shared memory, counted on its own barrier.
+__device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
@@ -217,6 +228,9 @@ struct EpiTile {
   int z, split, lane;
   int rows;           // rows in use (M)
   Unit unit;
+  uint64_t* bar;      // the warp's own, for what the epilogue reads, and its phase
+  uint32_t phase;
+  volatile int* gone;
 };
 
 // A bounded wait (about two seconds); false once any wait of the CTA ran out.
@@ -240,10 +254,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* staging = base + S * kStageBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kProdEpiWarps * Epi::kStaging);
-  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2, *epi = drain + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(epi + kProdEpiWarps);
   volatile int* gone = reinterpret_cast<volatile int*>(tmem_at + 1);
-  static_assert((2 * S + 5) * 8 + 8 <= kProdBarrierBytes, "barriers");
+  static_assert((2 * S + 5 + kProdEpiWarps) * 8 + 8 <= kProdBarrierBytes, "barriers");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -259,6 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
       mbar_init(&tempty[s], 2 * kProdEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int w = 0; w < kProdEpiWarps; ++w) mbar_init(&epi[w], 1);
     *gone = 0;
     fence_mbar_init();
     prefetch_map(&p.a);
@@ -276,6 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
 
   const Units units(p);
   if (warp == kProdEpiWarps) {  // ---- loads
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0) {
       int it = 0;
       bool ok = true;
@@ -318,15 +334,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
       }
     }
   } else if (warp == kProdEpiWarps + 1) {  // ---- products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0 && rank == 0) {
       int it = 0, n = 0;
       bool ok = true;
       for (int u = cluster; ok && u < units.count; u += clusters, ++n) {
         const Unit t = units.at(u);
-        const int acc = n & 1;
+        int acc = n & 1, first = t.k0;
         if (n >= 2 && !prod_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, gone)) break;
         tc_fence_after();
         for (int k = t.k0; k < t.k1; ++k, ++it) {
+          if (Epi::kChunks && p.chunk && k == first + p.chunk) {  // on in the other accumulator
+            tc_commit_pair(smem_u32(&tfull[acc]));
+            ++n;
+            acc = n & 1, first = k;
+            if (n >= 2 && !prod_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, gone)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
           const int s = it % S;
           if (!prod_wait(&full[s], (it / S) & 1, gone)) {
             ok = false;
@@ -338,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
 #pragma unroll
           for (int j = 0; j < kProdBK / 16; ++j)
             tc_mma(tmem + acc * kProdTile, da + j * kOperandStep<A_MN>, db + j * kOperandStep<B_MN>, p.idesc,
-                   k > t.k0 || j > 0);
+                   k > first || j > 0);
           tc_commit_pair(smem_u32(&empty[s]));
         }
         if (ok) tc_commit_pair(smem_u32(&tfull[acc]));
@@ -350,28 +377,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
         }
       }
     }
+  } else if (warp > kProdEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
   } else {  // ---- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quarter = warp & 3, half = warp >> 2;
+    EpiTile q;
+    q.staging = staging + warp * Epi::kStaging;
+    q.lane = lane;
+    q.rows = p.rows && !p.rows_k ? *p.rows : p.M;
+    q.bar = &epi[warp];
+    q.phase = 0;
+    q.gone = gone;
     int n = 0;
-    for (int u = cluster; u < units.count; u += clusters, ++n) {
+    bool ok = true;
+    typename Epi::State state;
+    for (int u = cluster; ok && u < units.count; u += clusters) {
       const Unit t = units.at(u);
-      const int acc = n & 1;
-      if (!__all_sync(0xffffffffu, prod_wait(&tfull[acc], (n >> 1) & 1, gone))) break;
-      tc_fence_after();
-      EpiTile q;
-      q.tmem = tmem + acc * kProdTile + half * kProdHalf + (static_cast<uint32_t>(quarter * 32) << 16);
-      q.staging = staging + warp * Epi::kStaging;
       q.row0 = t.m + static_cast<int>(rank) * kProdHalf + quarter * 32;
       q.col0 = t.n + half * kProdHalf;
       q.z = t.z;
       q.split = t.split;
-      q.lane = lane;
       q.unit = t;
-      q.rows = p.rows && !p.rows_k ? *p.rows : p.M;
-      Epi::tile(e, q);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(in_first_cta(smem_u32(&tempty[acc])));
+      Epi::ahead(e, q);
+      Epi::start(state);
+      const int chunk = Epi::kChunks && p.chunk ? p.chunk : t.k1 - t.k0;
+      for (int k = t.k0; k < t.k1; k += chunk, ++n) {
+        const int acc = n & 1;
+        q.tmem = tmem + acc * kProdTile + half * kProdHalf + (static_cast<uint32_t>(quarter * 32) << 16);
+        ok = __all_sync(0xffffffffu, prod_wait(&tfull[acc], (n >> 1) & 1, gone));
+        if (!ok) break;
+        tc_fence_after();
+        if (Epi::kChunks)
+          Epi::add(q, state);
+        else
+          Epi::tile(e, q, state);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(in_first_cta(smem_u32(&tempty[acc])));
+      }
+      if (Epi::kChunks && ok) Epi::tile(e, q, state);
     }
     if (Epi::kStaging > 0 && lane == 0) tma_wait_all();
   }
@@ -436,6 +481,20 @@ __device__ __forceinline__ void put16(const Out16& o, uint8_t* staging, int lane
   }
 }
 
+// Two boxes of the same place (o's and low's), after fetch16 has emptied the staging buffer.
+__device__ __forceinline__ void put16_pair(const Out16& o, const Out16& low, uint8_t* staging, int lane, int row0, int col0,
+                                           int z, const uint32_t (&w)[32], const uint32_t (&l)[32]) {
+  stage16(staging, lane, w);
+  stage16(staging + 4096, lane, l);
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store(&o.map, col0, row0, z, smem_u32(staging));
+    tma_store(&low.map, col0, row0, z, smem_u32(staging) + 4096);
+    tma_commit();
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -445,14 +504,50 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// An epilogue of whole tiles that reads nothing of its own.
+struct PlainEpi {
+  struct State {};
+  static constexpr bool kChunks = false;
+  template <typename P>
+  static __device__ __forceinline__ void ahead(const P&, EpiTile&) {}
+  static __device__ __forceinline__ void start(State&) {}
+  static __device__ __forceinline__ void add(EpiTile&, State&) {}
+};
+
+// What an epilogue reads of a tile comes by TMA into the warp's staging buffer, a box of 64
+// columns of 16-bit values (and a second one of what they leave out) at a time: its own
+// loads, each lane a row, would touch 32 lines each (1024 x 1024: steps of 74 us, now 45).
+template <bool LOW>
+__device__ __forceinline__ void fetch16(const CUtensorMap* hi, const CUtensorMap* lo, const EpiTile& q, int col) {
+  if (q.lane == 0) {
+    tma_wait_read<0>();
+    mbar_arrive_expect_tx(q.bar, LOW ? 8192 : 4096);
+    tma_load_own(smem_u32(q.staging), hi, col, q.row0, q.z, q.bar);
+    if (LOW) tma_load_own(smem_u32(q.staging) + 4096, lo, col, q.row0, q.z, q.bar);
+  }
+}
+// This lane's row of a box; the warp's wait for it comes first (false: it ran out).
+__device__ __forceinline__ bool fetched(EpiTile& q) {
+  const bool ok = __all_sync(0xffffffffu, prod_wait(q.bar, q.phase, q.gone));
+  q.phase ^= 1;
+  return ok;
+}
+__device__ __forceinline__ void unstage16(const uint8_t* staging, int lane, uint32_t (&w)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint4 v = *reinterpret_cast<const uint4*>(staging + lane * 128 + ((j ^ (lane & 7)) << 4));
+    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+  }
+}
+
 // C = alpha A B^T in bf16.
-struct StoreEpi {
+struct StoreEpi : PlainEpi {
   static constexpr int kStaging = 4096;
   struct Params {
     Out16 out;
     float alpha;
   };
-  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
 #pragma unroll 1
     for (int c = 0; c < kProdHalf; c += 64) {
       uint32_t w[32];
@@ -470,14 +565,14 @@ struct StoreEpi {
 
 // C in fp32 (boxes of 32 x 32), stored or added to what is there; a part of K (split)
 // goes to its own matrix.
-struct SumEpi {
+struct SumEpi : PlainEpi {
   static constexpr int kStaging = 4096;
   struct Params {
     CUtensorMap out;  // [splits][rows][cols]
     int32_t cols;
     int32_t add;
   };
-  static __device__ __forceinline__ void tile(const Params& e, const EpiTile& q) {
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
 #pragma unroll 1
     for (int c = 0; c < kProdHalf; c += 32) {
       float v[32];
