@@ -193,14 +193,16 @@ struct Units {
     per = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * splits;
     count = per * p.batch;
   }
-  // Rows in groups of 16 tiles, along which the tile index runs first: clusters that run
+  // A part of K after the other: clusters that run at the same time read the same slices of
+  // A and B, which stay in L2 (4096 x 4096 x 32768 in three parts: 3.2 GB from HBM with
+  // parts side by side).  Rows in groups of 16 tiles, along which the tile index runs first: clusters that run
   // at the same time share columns of B, and the group's rows of A stay in L2.
   __device__ __forceinline__ Unit at(int u) const {
     Unit r;
     r.z = u / per;
     int t = u - r.z * per;
-    r.split = t % splits;
-    t /= splits;
+    r.split = t / (per / splits);
+    t -= r.split * (per / splits);
     int i, j;
     if (symmetric) {
       for (i = 0; t >= tn - i; ++i) t -= tn - i;
@@ -232,6 +234,17 @@ struct EpiTile {
   uint32_t phase;
   volatile int* gone;
 };
+
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // A bounded wait (about two seconds); false once any wait of the CTA ran out.
 __device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, volatile int* gone) {
@@ -336,39 +349,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
   } else if (warp == kProdEpiWarps + 1) {  // ---- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0 && rank == 0) {
-      int it = 0, n = 0;
-      bool ok = true;
-      for (int u = cluster; ok && u < units.count; u += clusters, ++n) {
+      // Whether the next block has landed is asked before the products of this one are
+      // issued, and looked at after them: a wait between them leaves the tensor core idle.
+      const uint64_t a0 = operand_desc<A_MN>(smem_u32(base)), b0 = operand_desc<B_MN>(smem_u32(base) + kOperandBytes);
+      int n = 0, s = 0;
+      uint32_t phase = 0;
+      bool ok = true, landed = false, freed = true;
+      const int chunk = Epi::kChunks && p.chunk ? p.chunk : 0x7fffffff;
+      for (int u = cluster; ok && u < units.count; u += clusters) {
         const Unit t = units.at(u);
-        int acc = n & 1, first = t.k0;
-        if (n >= 2 && !prod_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, gone)) break;
-        tc_fence_after();
-        for (int k = t.k0; k < t.k1; ++k, ++it) {
-          if (Epi::kChunks && p.chunk && k == first + p.chunk) {  // on in the other accumulator
-            tc_commit_pair(smem_u32(&tfull[acc]));
-            ++n;
-            acc = n & 1, first = k;
-            if (n >= 2 && !prod_wait(&tempty[acc], ((n >> 1) & 1) ^ 1, gone)) {
+        for (int first = t.k0; ok && first < t.k1; first += min(chunk, t.k1 - first), ++n) {
+          const int end = first + min(chunk, t.k1 - first);
+          if (!freed && !prod_wait(&tempty[n & 1], ((n >> 1) & 1) ^ 1, gone)) {
+            ok = false;
+            break;
+          }
+          const uint32_t d = tmem + (n & 1) * kProdTile;
+          for (int k = first; k < end; ++k) {
+            if (!landed && !prod_wait(&full[s], phase, gone)) {
               ok = false;
               break;
             }
             tc_fence_after();
-          }
-          const int s = it % S;
-          if (!prod_wait(&full[s], (it / S) & 1, gone)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(base + s * kStageBytes);
-          const uint64_t da = operand_desc<A_MN>(sa), db = operand_desc<B_MN>(sa + kOperandBytes);
+            const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+            uint64_t* emptied = &empty[s];
+            if (++s == S) s = 0, phase ^= 1;
+            landed = mbar_test(&full[s], phase);
+            freed = n < 1 || mbar_test(&tempty[(n + 1) & 1], (((n + 1) >> 1) & 1) ^ 1);
 #pragma unroll
-          for (int j = 0; j < kProdBK / 16; ++j)
-            tc_mma(tmem + acc * kProdTile, da + j * kOperandStep<A_MN>, db + j * kOperandStep<B_MN>, p.idesc,
-                   k > first || j > 0);
-          tc_commit_pair(smem_u32(&empty[s]));
+            for (int j = 0; j < kProdBK / 16; ++j)
+              tc_mma(d, da + j * kOperandStep<A_MN>, db + j * kOperandStep<B_MN>, p.idesc, k > first || j > 0);
+            tc_commit_pair(smem_u32(emptied));
+          }
+          if (ok) tc_commit_pair(smem_u32(&tfull[n & 1]));
         }
-        if (ok) tc_commit_pair(smem_u32(&tfull[acc]));
       }
       if (*gone) {  // products in flight end before tensor memory is freed
         tc_commit_pair(smem_u32(drain));
