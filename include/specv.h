@@ -477,8 +477,10 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * specv_head_loss writes loss, and if given the gradients of sum_n loss[n] by hidden and
  * by head (either or both); specv_head_loss_backward the gradients of sum_n grad_loss[n]
  * * loss[n] (grad_loss NULL: ones) from the stats of a call on the same inputs.
- * The vocabulary is taken in pieces: beside the inputs a call needs the workspace alone
- * (with gradients at most 512 MB, and in it rows of 4 bytes x D and 8 bytes x V/128 each).
+ * The vocabulary is taken in pieces, whose logits are computed again for the gradients: the
+ * workspace holds 256 MB of them at most.  specv_head_loss with gradients keeps the logits'
+ * weights in 16 bits instead where all take no more than 1 GB (2 N V bytes), and computes
+ * the logits once.
  * Products are summed in fp32.  The gradients' products read the logits' gradient rounded
  * to bf16 (off by 2^-8 of each element at most), and are rounded once, to bf16.
  * Row status: SPECV_ROW_BAD_TOKEN (a target outside [-1, V)), SPECV_ROW_NONFINITE (a logit

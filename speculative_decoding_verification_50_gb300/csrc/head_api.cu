@@ -19,9 +19,16 @@ int64_t up_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // take the same tile whatever their number.
 bool gathers(int32_t N) { return N > kProdTile; }
 
+// A call that computes the loss and the gradients keeps the logits' weights in fp16 where
+// they take no more than 1 GB (4096 rows of 131072 tokens), and computes the logits once:
+// 6 N D V operations for 8.  Otherwise, and in a backward pass, the vocabulary is taken in
+// pieces and the logits are computed again.
+constexpr int64_t kKeepBytes = 1LL << 30;
+
 // Tokens per piece of the vocabulary: dz of a piece takes 256 MB at most (pieces of equal
 // size, of whole tiles).
-int64_t piece_tokens(int32_t N, int32_t V) {
+int64_t piece_tokens(int32_t N, int32_t V, bool keep) {
+  if (keep && 2 * up_to(N, kProdBK) * up_to(V, kProdTile) <= kKeepBytes) return up_to(V, kProdTile);
   const int64_t most = std::max<int64_t>((256LL << 20) / (2 * up_to(N, kProdBK)) / kProdTile * kProdTile, kProdTile);
   const int64_t pieces = (V + most - 1) / most;
   return up_to((V + pieces - 1) / pieces, kProdTile);
@@ -44,10 +51,11 @@ struct HeadSpace {
   size_t count, err, place, source, target, row, bad, z_target, part, hidden, head, dz, sum, bytes;
   int64_t rows, ld, Dp, Ds, tokens;  // rows: N up to a block; ld: of part; Dp, Ds: strides of gathered rows and sums
   int splits;
-  bool gather, copy_hidden, copy_head, grads;
+  bool gather, copy_hidden, copy_head, grads, keep;
 };
 
-HeadSpace head_space(const specv_head_args* a) {
+// keep: of a call that computes the loss too.
+HeadSpace head_space(const specv_head_args* a, bool keep) {
   HeadSpace w = {};
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -77,7 +85,8 @@ HeadSpace head_space(const specv_head_args* a) {
   if (w.copy_hidden) w.hidden = take(2 * w.rows * w.Dp);
   if (w.copy_head) w.head = take(2 * static_cast<size_t>(V) * w.Dp);
   if (w.grads) {
-    w.tokens = piece_tokens(a->N, a->V);
+    w.tokens = piece_tokens(a->N, a->V, keep);
+    w.keep = keep && w.tokens >= a->V;
     w.dz = take(2 * static_cast<size_t>(w.rows) * w.tokens);
     if (a->grad_hidden) {
       w.splits = hidden_splits(a->N, a->D, w.tokens);
@@ -144,20 +153,21 @@ struct HeadRun {
 
   // Rows in use, and copies of operands that TMA cannot read in place.
   specv_status rows(bool backward) {
-    if (w.gather || w.grads) {
-      HeadRowsParams p = {};
-      p.N = a->N, p.V = a->V, p.D = a->D, p.gathered = w.gather;
-      p.target = a->targets, p.weight = a->weights, p.scale = a->scale;
-      if (backward) p.up = a->grad_loss, p.stats = a->stats, p.row = at<HeadRow>(w.row);
-      p.count = at<int32_t>(w.count);
-      p.place = at<int32_t>(w.place), p.source = at<int32_t>(w.source), p.use_target = at<int32_t>(w.target);
-      TRY(done(launch_head_rows(p, s), "head-rows"));
+    HeadRowsParams r = {};
+    r.N = a->N, r.V = a->V;
+    r.target = a->targets, r.weight = a->weights, r.scale = a->scale;
+    if (backward) r.up = a->grad_loss, r.stats = a->stats, r.row = at<HeadRow>(w.row);
+    if (w.gather) {
+      r.count = at<int32_t>(w.count);
+      r.place = at<int32_t>(w.place), r.source = at<int32_t>(w.source), r.use_target = at<int32_t>(w.target);
+      TRY(done(launch_head_rows(r, s), "head-rows"));
     }
     if (w.copy_hidden) {
       HeadGatherParams p = {};
       p.N = a->N, p.D = a->D, p.pad_to = kProdBK;
       p.vec = aligned(a->hidden, 16) && (a->N <= 1 || a->hidden_stride % 8 == 0);
-      if (w.gather || w.grads) p.count = at<int32_t>(w.count), p.source = at<int32_t>(w.source);
+      if (w.gather) p.count = r.count, p.source = r.source;
+      else p.info = r;
       if (w.grads) p.bad = at<int32_t>(w.bad);
       p.in = static_cast<const uint16_t*>(a->hidden), p.in_stride = a->N > 1 ? a->hidden_stride : a->D;
       p.out = at<uint16_t>(w.hidden), p.out_stride = w.Dp;
@@ -196,7 +206,15 @@ struct HeadRun {
     e.target = w.gather ? at<int32_t>(w.target) : a->targets;
     e.part = at<float2>(w.part), e.ld = w.ld, e.z_target = at<float>(w.z_target);
     e.V = a->V, e.c2 = a->scale * kLog2e;
-    TRY(done(launch_head_stats(p, e, s), "head-stats"));
+    if (w.keep) {
+      KeepEpi::Params k = {};
+      k.s = e;
+      TRY(product_map(&k.out.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at<uint16_t>(w.dz), a->V, w.rows, 1, 2 * w.tokens, 0, 32));
+      k.out.cols = a->V;
+      TRY(done(launch_head_keep(p, k, s), "head-stats"));
+    } else {
+      TRY(done(launch_head_stats(p, e, s), "head-stats"));
+    }
     HeadJoinParams j = {};
     j.N = a->N, j.V = a->V, j.parts = (a->V + kPart - 1) / kPart;
     j.part = e.part, j.z_target = e.z_target, j.ld = w.ld, j.scale = a->scale;
@@ -215,7 +233,14 @@ struct HeadRun {
     for (int64_t v = 0; v < a->V; v += w.tokens, ++piece) {
       const int32_t n = static_cast<int32_t>(std::min<int64_t>(w.tokens, a->V - v));
       uint16_t* dz = at<uint16_t>(w.dz);
-      {  // dz of the piece
+      if (w.keep) {
+        HeadWeightParams p = {};
+        p.N = a->N, p.V = a->V, p.count = w.gather ? at<int32_t>(w.count) : nullptr;
+        p.part = at<float2>(w.part), p.ld = w.ld, p.row = at<HeadRow>(w.row), p.c2 = a->scale * kLog2e;
+        p.w = dz, p.stride = w.tokens;
+        const int64_t blocks = (w.rows * ((a->V + 255) / 256) + 7) / 8;
+        TRY(done(launch_head_weight(p, static_cast<int>(std::min<int64_t>(blocks, 8 * api_sm_count())), s), "head-dz"));
+      } else {  // dz of the piece
         ProductParams p = product(a->N, n, a->D, false, false);
         TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0));
         TRY(head_map(&p.b, false, v, n));
@@ -295,7 +320,7 @@ extern "C" {
 
 size_t specv_head_workspace_bytes(const specv_head_args* a) {
   if (!a || a->N < 1 || a->V < 1 || a->D < 1) return 0;
-  return head_space(a).bytes;
+  return std::max(head_space(a, true).bytes, head_space(a, false).bytes);
 }
 
 specv_status specv_head_loss(const specv_head_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -304,7 +329,7 @@ specv_status specv_head_loss(const specv_head_args* a, void* workspace, size_t w
   if (a->grad_loss) return api_fail(SPECV_ERR_INVALID_ARG, "grad_loss belongs to specv_head_loss_backward");
   if (a->N == 0) return no_rows(a, stream);
   if (!a->loss) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
-  HeadRun run = {a, head_space(a), static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
+  HeadRun run = {a, head_space(a, true), static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
   TRY(check_space(a, run.w, workspace, workspace_bytes));
   TRY(run.rows(false));
   TRY(run.forward());
@@ -317,7 +342,7 @@ specv_status specv_head_loss_backward(const specv_head_args* a, void* workspace,
   TRY(check_head(a));
   if (a->N == 0) return no_rows(a, stream);
   if (!a->stats || (!a->grad_hidden && !a->grad_head)) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
-  HeadRun run = {a, head_space(a), static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
+  HeadRun run = {a, head_space(a, false), static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
   TRY(check_space(a, run.w, workspace, workspace_bytes));
   TRY(run.rows(true));
   TRY(run.backward());

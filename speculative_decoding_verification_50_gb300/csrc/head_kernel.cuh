@@ -51,8 +51,10 @@ struct HeadStatsParams {
 // pairs, one fused multiply-add, one exponential, one addition), under the products of
 // the next tile.  The tensor core cuts each sum off (towards zero), so that the error of a
 // long sum grows with its length: sums over more than kStatsChunk blocks of K are taken in
-// chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum).
-constexpr int kStatsChunk = 16;
+// chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum, 5e-7 in
+// chunks of 16 blocks).  Rows of one tile, bound by the head's bytes, take chunks of
+// kStatsChunkFew blocks at no cost.
+constexpr int kStatsChunk = 16, kStatsChunkFew = 4;
 template <bool LONG>
 struct StatsEpi : PlainEpi {
   static constexpr bool kChunks = LONG;
@@ -134,6 +136,58 @@ struct StatsEpi : PlainEpi {
   }
 };
 
+// The forward pass where the gradients follow in the same call and the weights exp(z - m),
+// m a row's largest logit of 128 columns, are kept for them: times 2^15 in fp16 (off by 2^-11 of
+// a weight at most, and by 2^-40 of the largest of 128), so that the logits need no second
+// product.
+constexpr float kKeepScale = 15.f;  // (its logarithm)
+struct KeepEpi : StatsEpi<true> {
+  static constexpr int kStaging = 4096;
+  struct Params {
+    HeadStatsParams s;
+    Out16 out;
+  };
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State& sum) {
+    if (q.row0 >= q.rows || q.col0 >= e.s.V) return;
+    const int i = q.row0 + q.lane, at = (i < q.rows ? e.s.target[i] : -1) - q.col0, left = e.s.V - q.col0;
+    float hi = sum.v[0], lo = sum.v[0];
+#pragma unroll
+    for (int j = 1; j < kPart - 1; j += 2) {
+      hi = max3_nan(hi, sum.v[j], sum.v[j + 1]);
+      lo = min3(lo, sum.v[j], sum.v[j + 1]);
+    }
+    hi = max3_nan(hi, sum.v[kPart - 1], sum.v[kPart - 1]);
+    lo = fminf(lo, sum.v[kPart - 1]);
+    const bool bad = !(hi < pos_inf()) || !(lo > neg_inf());
+    if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < static_cast<unsigned>(kPart)) || left < kPart) {
+      hi = neg_inf();
+#pragma unroll
+      for (int j = 0; j < kPart; ++j) {
+        if (j == at) e.s.z_target[i] = sum.v[j];
+        if (j == at || j >= left) sum.v[j] = neg_inf();
+        hi = fmaxf(hi, sum.v[j]);
+      }
+    }
+    const float m = fmaxf(hi, kNegMax), mc = kKeepScale - m * e.s.c2;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) {
+      sum.v[j] = ex2(fmaf(sum.v[j], e.s.c2, mc));
+      s[j & 3] += sum.v[j];
+    }
+    const float total = hi > neg_inf() ? ((s[0] + s[1]) + (s[2] + s[3])) * (1.f / 32768.f) : 0.f;
+    if (i < q.rows)
+      e.s.part[static_cast<int64_t>(q.col0 / kPart) * e.s.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
+#pragma unroll
+    for (int c = 0; c < kPart; c += 64) {
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = pack_f16(sum.v[c + 2 * j], sum.v[c + 2 * j + 1]);
+      put16(e.out, q.staging, q.lane, q.row0, q.col0 + c, 0, q.rows, w);
+    }
+  }
+};
+
 // dz of a tile in bf16.
 struct ProbEpi : PlainEpi {
   static constexpr int kStaging = 4096;
@@ -186,7 +240,7 @@ __device__ __forceinline__ void soft_join(float& m, float& s, float m2, float s2
 // ---- rows
 
 struct HeadRowsParams {
-  int32_t N, V, D, gathered;  // gathered: rows without weight are left out
+  int32_t N, V;
   const int32_t* target;
   const float* weight;     // optional
   const float* up;         // optional (backward)
@@ -202,6 +256,7 @@ struct HeadRowsParams {
 constexpr int kRowsThreads = 1024;
 
 struct HeadGatherParams {
+  HeadRowsParams info;     // info.row not null: rows are where they are, and what is known of them is written
   int32_t N, D, pad_to;    // rows up to a multiple of pad_to behind those in use are zeros
   int32_t vec;             // source rows start at 16-byte boundaries
   int32_t* bad;            // optional [N], by place: 1 for a row with an entry that is not finite; it becomes zeros
@@ -234,6 +289,17 @@ struct HeadJoinParams {
 };
 
 constexpr int kJoinThreads = 256;
+
+struct HeadWeightParams {
+  int32_t N, V;
+  const int32_t* count;    // optional: rows in use
+  const float2* part;
+  int64_t ld;
+  const HeadRow* row;
+  float c2;
+  uint16_t* w;             // [rows up to a block][stride]: weights in, dz out
+  int64_t stride;
+};
 
 struct HeadFinishParams {
   int32_t N, D, splits;

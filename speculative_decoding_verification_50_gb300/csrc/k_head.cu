@@ -5,6 +5,28 @@
 
 namespace specv {
 
+namespace {
+
+// What is known of row r: its target if it counts (else -1), and in the backward pass its
+// gradient's factors.
+__device__ __forceinline__ HeadRow head_row(const HeadRowsParams& p, int r) {
+  const int t = p.target[r];
+  const float w = p.weight ? p.weight[r] : 1.f;
+  HeadRow row = {0.f, 0.f, 0.f, -1};
+  if (t < 0 || t >= p.V || w == 0.f) return row;
+  if (p.stats) {
+    const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
+    if (!(lse - lse == 0.f) || !(nll - nll == 0.f)) return row;
+    const float g = w * (p.up ? p.up[r] : 1.f) * p.scale;
+    row = {lse * kLog2e, g, g * expm1f(-nll), t};
+  }
+  row.target = t;
+  return row;
+}
+
+}  // namespace
+
+// Which rows count, and where they go (in order).  One CTA.
 __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRowsParams p) {
   __shared__ int warps[32];
   __shared__ int before;
@@ -14,43 +36,26 @@ __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRo
   pdl_launch_dependents();
   for (int first = 0; first < p.N; first += kRowsThreads) {
     const int r = first + threadIdx.x;
-    bool use = false;
-    HeadRow row = {0.f, 0.f, 0.f, -1};
-    if (r < p.N) {
-      const int t = p.target[r];
-      const float w = p.weight ? p.weight[r] : 1.f;
-      use = t >= 0 && t < p.V && w != 0.f;
-      if (p.stats) {
-        const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
-        use = use && lse - lse == 0.f && nll - nll == 0.f;
-        if (use) {
-          const float g = w * (p.up ? p.up[r] : 1.f) * p.scale;
-          row = {lse * kLog2e, g, g * expm1f(-nll), t};
-        }
-      }
-      if (use) row.target = t;
-    }
-    int at = r;
-    if (p.gathered) {
-      const unsigned votes = __ballot_sync(0xffffffffu, use);
-      if (lane == 0) warps[warp] = __popc(votes);
-      __syncthreads();
-      if (warp == 0) {
-        const int n = warps[lane];
-        int x = n;
+    const HeadRow row = r < p.N ? head_row(p, r) : HeadRow{0.f, 0.f, 0.f, -1};
+    const bool use = row.target >= 0;
+    const unsigned votes = __ballot_sync(0xffffffffu, use);
+    if (lane == 0) warps[warp] = __popc(votes);
+    __syncthreads();
+    if (warp == 0) {
+      const int n = warps[lane];
+      int x = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        warps[lane] = before + x - n;
-        __syncwarp();
-        if (lane == 31) before += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
       }
-      __syncthreads();
-      at = use ? warps[warp] + __popc(votes & ((1u << lane) - 1)) : -1;
-      __syncthreads();
+      warps[lane] = before + x - n;
+      __syncwarp();
+      if (lane == 31) before += x;
     }
+    __syncthreads();
+    const int at = use ? warps[warp] + __popc(votes & ((1u << lane) - 1)) : -1;
+    __syncthreads();
     if (r < p.N) {
       p.place[r] = at;
       if (at >= 0) {
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRo
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) *p.count = p.gathered ? before : p.N;
+  if (threadIdx.x == 0) *p.count = before;
 }
 
 // A row of 16-bit values per CTA: the rows in use brought together at 16-byte boundaries.
@@ -72,6 +77,7 @@ __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadG
   const int n = p.count ? *p.count : p.N;
   const int all = (n + p.pad_to - 1) / p.pad_to * p.pad_to;
   for (int i = blockIdx.x; i < max(all, p.pad_to); i += gridDim.x) {
+    if (p.info.row && threadIdx.x == 0 && i < n) p.info.row[i] = head_row(p.info, i);
     uint16_t* out = p.out + i * p.out_stride;
     const int D8 = (p.D + 7) / 8;
     const uint16_t* in = i < n ? p.in + static_cast<int64_t>(p.source ? p.source[i] : i) * p.in_stride : nullptr;
@@ -166,6 +172,38 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   if (p.row && at >= 0) p.row[at] = row;
 }
 
+// dz from the weights that were kept, in their place (fp16 in, bf16 out).  A warp takes 256
+// columns of a row.  Bound by bytes (4 per logit).
+__global__ void __launch_bounds__(256) head_weight_kernel(const HeadWeightParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int n = p.count ? *p.count : p.N, rows = max((n + kProdBK - 1) / kProdBK * kProdBK, kProdBK);
+  const int lane = threadIdx.x & 31, pieces = (p.V + 255) / 256;
+  const int64_t all = static_cast<int64_t>(rows) * pieces;
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); x < all; x += static_cast<int64_t>(gridDim.x) * 8) {
+    const int i = static_cast<int>(x / pieces), col = static_cast<int>(x - static_cast<int64_t>(i) * pieces) * 256 + lane * 8;
+    if (col >= p.V) continue;
+    uint4* at = reinterpret_cast<uint4*>(p.w + i * p.stride + col);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const HeadRow r = i < n ? p.row[i] : HeadRow{0.f, 0.f, 0.f, -1};
+    if (r.g != 0.f) {
+      v = __ldcs(at);
+      const float f = r.g * ex2(fmaf(p.part[(col / kPart) * p.ld + i].x, p.c2, -r.lse2) - kKeepScale);
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        float a = e.x * f, b = e.y * f;
+        if (col + 2 * k == r.target) a = r.at;
+        if (col + 2 * k + 1 == r.target) b = r.at;
+        w[k] = pack_bf16(a, b);
+      }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *at = v;
+  }
+}
+
 // dh from the sums of K's parts, rows back in their places.
 __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams p) {
   pdl_wait_primary();
@@ -195,10 +233,19 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
   }
 }
 
+static int stats_chunk(const ProductParams& p) { return p.M <= kProdTile ? kStatsChunkFew : kStatsChunk; }
+
 cudaError_t launch_head_stats(ProductParams& p, const HeadStatsParams& e, cudaStream_t s) {
-  if (p.K <= kStatsChunk * kProdBK) return launch_product<false, false, StatsEpi<false>>(p, e, s);
-  p.chunk = kStatsChunk;
+  p.chunk = stats_chunk(p);
+  if (p.K <= p.chunk * kProdBK) return launch_product<false, false, StatsEpi<false>>(p, e, s);
   return launch_product<false, false, StatsEpi<true>>(p, e, s);
+}
+cudaError_t launch_head_keep(ProductParams& p, const KeepEpi::Params& e, cudaStream_t s) {
+  p.chunk = stats_chunk(p);
+  return launch_product<false, false, KeepEpi>(p, e, s);
+}
+cudaError_t launch_head_weight(const HeadWeightParams& p, int blocks, cudaStream_t s) {
+  return launch_grid(head_weight_kernel, blocks, 256, s, p);
 }
 cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s) {
   return launch_product<false, false, ProbEpi>(p, e, s);

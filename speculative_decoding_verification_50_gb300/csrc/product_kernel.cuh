@@ -30,7 +30,8 @@ constexpr int kProdHalf = kProdTile / 2;    // rows of A, and of B, that one CTA
 constexpr int kProdBK = 64;                 // K per stage: 128 bytes, the width of the swizzle
 constexpr int kProdEpiWarps = 8;
 constexpr int kProdThreads = 32 * (kProdEpiWarps + 4);
-// Registers a thread: launched with at most 168 (12 warps), of which the last four warps
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp = 4;  // the first epilogue warp
+// Registers a thread: launched with at most 168 (12 warps), of which the first four warps
 // give up most to the epilogue's: 2 x 216 + 72 = 3 x 168.
 constexpr int kEpiRegs = 216, kLoadRegs = 72;
 constexpr int kOperandBytes = kProdHalf * kProdBK * 2;  // 16 KB
@@ -292,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
     prefetch_map(&p.a);
     prefetch_map(&p.b);
   }
-  if (warp == kProdEpiWarps + 1) tmem_alloc_all(smem_u32(tmem_at));
+  if (warp == kMmaWarp) tmem_alloc_all(smem_u32(tmem_at));
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -303,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
   pdl_launch_dependents();
 
   const Units units(p);
-  if (warp == kProdEpiWarps) {  // ---- loads
+  if (warp == kLoadWarp) {  // ---- loads
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0) {
       int it = 0;
@@ -346,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
           }
       }
     }
-  } else if (warp == kProdEpiWarps + 1) {  // ---- products
+  } else if (warp == kMmaWarp) {  // ---- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0 && rank == 0) {
       // Whether the next block has landed is asked before the products of this one are
@@ -391,16 +392,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
         }
       }
     }
-  } else if (warp > kProdEpiWarps) {
+  } else if (warp < kEpiWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
   } else {  // ---- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, half = warp / 4 - 1;
     EpiTile q;
-    q.staging = staging + warp * Epi::kStaging;
+    q.staging = staging + (warp - kEpiWarp) * Epi::kStaging;
     q.lane = lane;
     q.rows = p.rows && !p.rows_k ? *p.rows : p.M;
-    q.bar = &epi[warp];
+    q.bar = &epi[warp - kEpiWarp];
     q.phase = 0;
     q.gone = gone;
     int n = 0;
@@ -440,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == kProdEpiWarps + 1) tmem_free_all(tmem);
+  if (warp == kMmaWarp) tmem_free_all(tmem);
   const int failed = *gone;
   if (threadIdx.x == 0 && p.err) p.err[blockIdx.x] = failed;
   if (failed && p.status)

@@ -11,7 +11,7 @@ sums; each gradient is rounded once more.
 """
 import torch
 
-HALF = torch.finfo(torch.bfloat16).eps / 2
+HALF, HALF16 = torch.finfo(torch.bfloat16).eps / 2, torch.finfo(torch.float16).eps / 2
 
 
 def head64(h, W, t, scale=1.0, weights=None, up=None):
@@ -40,8 +40,10 @@ def head64(h, W, t, scale=1.0, weights=None, up=None):
     d = torch.exp(logp)
     d.scatter_(1, at, -rest[:, None])
     d = torch.where(use[:, None], d * g[:, None], 0.0)
-    share = HALF + 2 * dz[:, None] + 2.0 ** -20 + 2.0 ** -23 * lse.abs()[:, None]
-    doff = torch.where(use[:, None], d.abs() * share, 0.0)
+    share = HALF + HALF16 + 2 * dz[:, None] + 2.0 ** -20 + 2.0 ** -23 * lse.abs()[:, None]
+    around = torch.nn.functional.pad(d.scatter(1, at, 0.0).abs(), (0, -V % 128)).view(N, -1, 128)
+    around = around.amax(2, keepdim=True).expand_as(around).reshape(N, -1)[:, :V]
+    doff = torch.where(use[:, None], d.abs() * share + 2.0 ** -40 * around, 0.0)
     gh, gW = scale * (d @ W), scale * (d.T @ h)
     # (sums in fp32: 2^-23 an addition of 16)
     gh_off = scale * ((doff + (V / 16 + 34) * 2.0 ** -23 * d.abs()) @ W.abs()) + HALF * gh.abs()
