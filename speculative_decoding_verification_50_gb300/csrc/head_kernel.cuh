@@ -54,7 +54,7 @@ struct HeadStatsParams {
 // chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum, 5e-7 in
 // chunks of 16 blocks).  Rows of one tile, bound by the head's bytes, take chunks of
 // kStatsChunkFew blocks at no cost.
-constexpr int kStatsChunk = 16, kStatsChunkFew = 4;
+constexpr int kStatsChunk = 16, kStatsChunkFew = 8;
 template <bool LONG>
 struct StatsEpi : PlainEpi {
   static constexpr bool kChunks = LONG;
