@@ -186,7 +186,6 @@ struct HeadRun {
   ProductParams product(int32_t M, int32_t N, int32_t K, bool a_mn, bool b_mn) const {
     ProductParams p = {};
     p.M = M, p.N = N, p.K = K, p.batch = 1, p.splits = 1;
-    p.tn = static_cast<int32_t>(up_to(N, kProdTile) / kProdTile);
     p.idesc = prod_idesc(true, a_mn, b_mn);
     p.rows = w.gather ? at<int32_t>(w.count) : nullptr;
     p.rows_k = a_mn;
@@ -221,7 +220,7 @@ struct HeadRun {
     j.place = w.gather ? at<int32_t>(w.place) : nullptr;
     j.target = a->targets, j.weight = a->weights;
     j.bad = w.grads ? at<int32_t>(w.bad) : nullptr;
-    j.err = p.err, j.errs = product_grid(p);
+    j.err = p.err, j.errs = product_grid<true>(p);
     j.loss = a->loss, j.stats = a->stats, j.status = a->row_status;
     j.row = w.grads ? at<HeadRow>(w.row) : nullptr;
     return done(launch_head_join(j, s), "head-join");

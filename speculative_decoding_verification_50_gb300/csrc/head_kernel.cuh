@@ -114,6 +114,7 @@ struct StatsEpi : PlainEpi {
       for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], e.c2, mc));
     }
   }
+  template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State& sum) {
     if (q.row0 >= q.rows || q.col0 >= e.V) return;
     const int i = q.row0 + q.lane;
@@ -147,6 +148,7 @@ struct KeepEpi : StatsEpi<true> {
     HeadStatsParams s;
     Out16 out;
   };
+  template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State& sum) {
     if (q.row0 >= q.rows || q.col0 >= e.s.V) return;
     const int i = q.row0 + q.lane, at = (i < q.rows ? e.s.target[i] : -1) - q.col0, left = e.s.V - q.col0;
@@ -197,6 +199,7 @@ struct ProbEpi : PlainEpi {
     int32_t first;       // the piece's first token
     float c2;
   };
+  template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
     // (the rows up to a multiple of 64 are read along K by the product for dW: zeros)
     const int rows = max((q.rows + kProdBK - 1) / kProdBK * kProdBK, kProdBK);
@@ -208,7 +211,7 @@ struct ProbEpi : PlainEpi {
       r = {x.x, x.y, x.z, __float_as_int(x.w)};
     }
 #pragma unroll 1
-    for (int c = 0; c < kProdHalf; c += 64) {
+    for (int c = 0; c < COLS; c += 64) {
       if (q.col0 + c >= e.out.cols) break;
       uint32_t w[32];
 #pragma unroll

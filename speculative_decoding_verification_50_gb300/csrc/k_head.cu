@@ -237,24 +237,24 @@ static int stats_chunk(const ProductParams& p) { return p.M <= kProdTile ? kStat
 
 cudaError_t launch_head_stats(ProductParams& p, const HeadStatsParams& e, cudaStream_t s) {
   p.chunk = stats_chunk(p);
-  if (p.K <= p.chunk * kProdBK) return launch_product<false, false, StatsEpi<false>>(p, e, s);
-  return launch_product<false, false, StatsEpi<true>>(p, e, s);
+  if (p.K <= p.chunk * kProdBK) return launch_product<true, false, false, StatsEpi<false>>(p, e, s);
+  return launch_product<true, false, false, StatsEpi<true>>(p, e, s);
 }
 cudaError_t launch_head_keep(ProductParams& p, const KeepEpi::Params& e, cudaStream_t s) {
   p.chunk = stats_chunk(p);
-  return launch_product<false, false, KeepEpi>(p, e, s);
+  return launch_product<true, false, false, KeepEpi>(p, e, s);
 }
 cudaError_t launch_head_weight(const HeadWeightParams& p, int blocks, cudaStream_t s) {
   return launch_grid(head_weight_kernel, blocks, 256, s, p);
 }
 cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s) {
-  return launch_product<false, false, ProbEpi>(p, e, s);
+  return launch_product<true, false, false, ProbEpi>(p, e, s);
 }
 cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s) {
-  return launch_product<false, true, SumEpi>(p, e, s);
+  return launch_product<true, false, true, SumEpi>(p, e, s);
 }
 cudaError_t launch_head_head(ProductParams& p, const StoreEpi::Params& e, cudaStream_t s) {
-  return launch_product<true, true, StoreEpi>(p, e, s);
+  return launch_product<true, true, true, StoreEpi>(p, e, s);
 }
 cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t s) {
   return launch_grid(head_rows_kernel, 1, kRowsThreads, s, p);

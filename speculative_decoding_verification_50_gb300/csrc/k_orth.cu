@@ -161,23 +161,29 @@ cudaError_t launch_orth_squares(int dtype, const OrthInParams& p, cudaStream_t s
 cudaError_t launch_orth_scale(int dtype, const OrthInParams& p, cudaStream_t s) {
   return dtype == SPECV_BF16 ? launch_in(orth_scale_kernel<0>, p, s) : launch_in(orth_scale_kernel<1>, p, s);
 }
+template <bool A_MN, bool B_MN, class Epi>
+static cudaError_t launch_tiles(bool half, ProductParams& p, const typename Epi::Params& e, cudaStream_t s) {
+  return half ? launch_product<false, A_MN, B_MN, Epi>(p, e, s) : launch_product<true, A_MN, B_MN, Epi>(p, e, s);
+}
+
 template <bool FINE>
-cudaError_t launch_orth_gram(bool mn, ProductParams& p, const typename SymEpi<false, FINE>::Params& e, cudaStream_t s) {
-  return mn ? launch_product<true, true, SymEpi<false, FINE>>(p, e, s) : launch_product<false, false, SymEpi<false, FINE>>(p, e, s);
+cudaError_t launch_orth_gram(bool half, bool mn, ProductParams& p, const typename SymEpi<false, FINE>::Params& e, cudaStream_t s) {
+  return mn ? launch_tiles<true, true, SymEpi<false, FINE>>(half, p, e, s)
+            : launch_tiles<false, false, SymEpi<false, FINE>>(half, p, e, s);
 }
 template <bool FINE>
-cudaError_t launch_orth_poly(ProductParams& p, const typename SymEpi<true, FINE>::Params& e, cudaStream_t s) {
-  return launch_product<false, false, SymEpi<true, FINE>>(p, e, s);
+cudaError_t launch_orth_poly(bool half, ProductParams& p, const typename SymEpi<true, FINE>::Params& e, cudaStream_t s) {
+  return launch_tiles<false, false, SymEpi<true, FINE>>(half, p, e, s);
 }
-template cudaError_t launch_orth_gram<false>(bool, ProductParams&, const SymEpi<false, false>::Params&, cudaStream_t);
-template cudaError_t launch_orth_gram<true>(bool, ProductParams&, const SymEpi<false, true>::Params&, cudaStream_t);
-template cudaError_t launch_orth_poly<false>(ProductParams&, const SymEpi<true, false>::Params&, cudaStream_t);
-template cudaError_t launch_orth_poly<true>(ProductParams&, const SymEpi<true, true>::Params&, cudaStream_t);
-cudaError_t launch_orth_step(bool mn, ProductParams& p, const StepEpi<false>::Params& e, cudaStream_t s) {
-  return mn ? launch_product<false, true, StepEpi<false>>(p, e, s) : launch_product<false, false, StepEpi<false>>(p, e, s);
+template cudaError_t launch_orth_gram<false>(bool, bool, ProductParams&, const SymEpi<false, false>::Params&, cudaStream_t);
+template cudaError_t launch_orth_gram<true>(bool, bool, ProductParams&, const SymEpi<false, true>::Params&, cudaStream_t);
+template cudaError_t launch_orth_poly<false>(bool, ProductParams&, const SymEpi<true, false>::Params&, cudaStream_t);
+template cudaError_t launch_orth_poly<true>(bool, ProductParams&, const SymEpi<true, true>::Params&, cudaStream_t);
+cudaError_t launch_orth_step(bool half, bool mn, ProductParams& p, const StepEpi<false>::Params& e, cudaStream_t s) {
+  return mn ? launch_tiles<false, true, StepEpi<false>>(half, p, e, s) : launch_tiles<false, false, StepEpi<false>>(half, p, e, s);
 }
-cudaError_t launch_orth_last(bool mn, ProductParams& p, const StepEpi<true>::Params& e, cudaStream_t s) {
-  return mn ? launch_product<false, true, StepEpi<true>>(p, e, s) : launch_product<false, false, StepEpi<true>>(p, e, s);
+cudaError_t launch_orth_last(bool half, bool mn, ProductParams& p, const StepEpi<true>::Params& e, cudaStream_t s) {
+  return mn ? launch_tiles<false, true, StepEpi<true>>(half, p, e, s) : launch_tiles<false, false, StepEpi<true>>(half, p, e, s);
 }
 
 }  // namespace specv

@@ -46,6 +46,16 @@ struct OrthSpace {
   bool tall, fine;
 };
 
+// Whether a product goes by tiles of 128 x 128, a CTA each, in the place of 256 x 256, a pair
+// each: where that ends sooner.  Cycles of a round of tiles: those of a block of K, 620 and
+// 420 (256 are the tensor core's, the rest L2's), and of what is not hidden under the next
+// tile, about 6000 and 4000.
+bool small_tiles(const ProductParams& p) {
+  const int64_t blocks = (p.K + kProdBK - 1) / kProdBK * (p.fine ? 3 : 1);
+  auto rounds = [&](int tile, int64_t ctas) { return (product_units(p, tile) + ctas - 1) / ctas; };
+  return rounds(kProdHalf, api_sm_count()) * blocks * 420 + 4000 < rounds(kProdTile, api_sm_count() / 2) * blocks * 620 + 6000;
+}
+
 OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
   OrthSpace w = {};
   size_t at = 0;
@@ -63,8 +73,10 @@ OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
       1, std::min((vectors + 8 * kOrthThreads - 1) / (8 * kOrthThreads), std::max<int64_t>(1, 8LL * api_sm_count() / B))));
   w.part = take(sizeof(ScaledSquares) * static_cast<size_t>(B) * w.blocks);
   const size_t x = 2 * static_cast<size_t>(B) * m * w.ld, q = 2 * static_cast<size_t>(B) * w.s * w.lds;
-  for (int k = 0; k < 2; ++k) w.hi[k] = take(x), w.lo[k] = take(x);
+  w.hi[0] = take(x), w.hi[1] = take(x), w.lo[0] = take(x);
   w.fine = w.s <= kProdTile;
+  // (what X's fp16 leaves out is read and written by the same epilogue alone, unless products read it)
+  w.lo[1] = w.fine ? take(x) : w.lo[0];
   for (int k = 0; k <= w.fine; ++k) w.gram[k] = take(q), w.poly[k] = take(q);
   w.bytes = at;
   return w;
@@ -121,11 +133,13 @@ struct OrthRun {
     ++launches;
     return SPECV_OK;
   }
-  ProductParams product(int32_t M, int32_t N, int32_t K, bool a_mn, bool b_mn, bool symmetric) const {
+  // half: tiles of 128 x 128 by one CTA each.
+  ProductParams product(int32_t M, int32_t N, int32_t K, bool a_mn, bool b_mn, bool symmetric, bool& half) const {
     ProductParams p = {};
-    p.M = M, p.N = N, p.K = K, p.batch = a->B, p.splits = 1, p.symmetric = symmetric, p.fine = w.fine;
-    p.tn = static_cast<int32_t>(up_to(N, kProdTile) / kProdTile);
-    p.idesc = prod_idesc(false, a_mn, b_mn);
+    p.M = M, p.N = N, p.K = K, p.batch = a->B, p.splits = 1;
+    p.symmetric = symmetric, p.fine = w.fine;
+    half = small_tiles(p);
+    p.idesc = prod_idesc(false, a_mn, b_mn, half ? kProdHalf : kProdTile);
     p.status = a->row_status, p.status_n = a->B;
     return p;
   }
@@ -137,28 +151,25 @@ struct OrthRun {
   specv_status s_map(CUtensorMap* m, size_t off) const {
     return operand_map(m, false, false, at(off), w.s, w.s, a->B, w.lds, zs());
   }
-  specv_status box_map(CUtensorMap* m, size_t off, int64_t cols, int64_t rows, int64_t ld) const {
-    return product_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at(off), cols, rows, a->B, 2 * ld, 2 * rows * ld, 32);
-  }
-  specv_status out_map(Out16& o, size_t off, int64_t cols, int64_t rows, int64_t ld) const {
-    o.cols = static_cast<int32_t>(cols);
-    return box_map(&o.map, off, cols, rows, ld);
+  specv_status box_map(CUtensorMap* m, size_t off, int64_t cols, int64_t rows, int64_t ld, int width = 64) const {
+    return product_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at(off), cols, rows, a->B, 2 * ld, 2 * rows * ld, 32, width);
   }
 
   // S, then P = b S + c S S
   template <bool FINE>
   specv_status symmetric(int from, double sx, double ss, double sp) {
+    bool half;
     {
-      ProductParams p = product(w.s, w.s, w.t, w.tall, w.tall, true);
+      ProductParams p = product(w.s, w.s, w.t, w.tall, w.tall, true, half);
       TRY(x_map(&p.a, w.tall, w.hi[from]));
       if (FINE) TRY(x_map(&p.a_low, w.tall, w.lo[from]));
       p.b = p.a, p.b_low = p.a_low;
       typename SymEpi<false, FINE>::Params e = {};
       TRY(sym_out(e, w.gram, FINE));
       e.alpha = static_cast<float>(ss / (sx * sx));
-      TRY(done(launch_orth_gram<FINE>(w.tall, p, e, s), "orthogonalize-gram"));
+      TRY(done(launch_orth_gram<FINE>(half, w.tall, p, e, s), "orthogonalize-gram"));
     }
-    ProductParams p = product(w.s, w.s, w.s, false, false, true);
+    ProductParams p = product(w.s, w.s, w.s, false, false, true, half);
     TRY(s_map(&p.a, w.gram[0]));
     if (FINE) TRY(s_map(&p.a_low, w.gram[1]));
     p.b = p.a, p.b_low = p.a_low;
@@ -167,14 +178,15 @@ struct OrthRun {
     TRY(box_map(&e.chi, w.gram[0], w.s, w.s, w.lds));
     if (FINE) TRY(box_map(&e.clo, w.gram[1], w.s, w.s, w.lds));
     e.alpha = static_cast<float>(a->c * sp / (ss * ss)), e.beta = static_cast<float>(a->b * sp / ss);
-    return done(launch_orth_poly<FINE>(p, e, s), "orthogonalize-poly");
+    return done(launch_orth_poly<FINE>(half, p, e, s), "orthogonalize-poly");
   }
   template <typename Params>
   specv_status sym_out(Params& e, const size_t (&to)[2], bool fine) const {
-    TRY(out_map(e.hi, to[0], w.s, w.s, w.lds));
-    if (fine) TRY(out_map(e.lo, to[1], w.s, w.s, w.lds));
-    e.mirror_hi = at(to[0]), e.mirror_lo = at(to[fine]);
-    e.ld = w.lds, e.zstride = zs(), e.n = w.s;
+    TRY(box_map(&e.hi, to[0], w.s, w.s, w.lds));
+    TRY(box_map(&e.mirror_hi, to[0], w.s, w.s, w.lds, 0));
+    if (fine) TRY(box_map(&e.lo, to[1], w.s, w.s, w.lds));
+    if (fine) TRY(box_map(&e.mirror_lo, to[1], w.s, w.s, w.lds, 0));
+    e.n = w.s;
     return SPECV_OK;
   }
 
@@ -199,34 +211,37 @@ struct OrthRun {
       const double next = 1.01 * step_bound(a->a, a->b, a->c, r), sn = last ? 1.0 : keep_scale(next);
       TRY(w.fine ? symmetric<true>(from, sx, ss, sp) : symmetric<false>(from, sx, ss, sp));
       // X' = a X + P X, or a X + X P (P is its own transpose)
-      ProductParams p = product(a->m, a->n, w.s, false, !w.tall, false);
+      bool half;
+      ProductParams p = product(a->m, a->n, w.s, false, !w.tall, false, half);
       TRY(s_map(w.tall ? &p.b : &p.a, w.poly[0]));
       TRY(x_map(w.tall ? &p.a : &p.b, !w.tall, w.hi[from]));
       if (w.fine) {
         TRY(s_map(w.tall ? &p.b_low : &p.a_low, w.poly[1]));
         TRY(x_map(w.tall ? &p.a_low : &p.b_low, !w.tall, w.lo[from]));
       }
-      const float alpha = static_cast<float>(sn / (sp * sx)), beta = static_cast<float>(a->a * sn / sx);
+      auto step = [&](auto& e) {
+        TRY(box_map(&e.xhi, w.hi[from], a->n, a->m, w.ld));
+        TRY(box_map(&e.xlo, w.lo[from], a->n, a->m, w.ld));
+        e.rows = a->m, e.cols = a->n;
+        e.alpha = static_cast<float>(sn / (sp * sx)), e.beta = static_cast<float>(a->a * sn / sx);
+        return SPECV_OK;
+      };
       if (!last) {
         StepEpi<false>::Params e = {};
-        TRY(out_map(e.hi, w.hi[from ^ 1], a->n, a->m, w.ld));
-        TRY(out_map(e.lo, w.lo[from ^ 1], a->n, a->m, w.ld));
-        TRY(box_map(&e.xhi, w.hi[from], a->n, a->m, w.ld));
-        TRY(box_map(&e.xlo, w.lo[from], a->n, a->m, w.ld));
-        e.rows = a->m, e.cols = a->n, e.alpha = alpha, e.beta = beta;
-        TRY(done(launch_orth_step(!w.tall, p, e, s), "orthogonalize-step"));
+        TRY(step(e));
+        TRY(box_map(&e.hi, w.hi[from ^ 1], a->n, a->m, w.ld));
+        TRY(box_map(&e.lo, w.lo[from ^ 1], a->n, a->m, w.ld));
+        TRY(done(launch_orth_step(half, !w.tall, p, e, s), "orthogonalize-step"));
       } else {
         StepEpi<true>::Params e = {};
+        TRY(step(e));
         const int64_t rs = a->m > 1 ? a->out_row_stride : up_to(a->n, 8), bs = a->B > 1 ? a->out_batch_stride : 0;
-        e.hi.cols = a->n, e.hi.stride = rs, e.hi.zstride = bs;
+        e.stride = rs, e.zstride = bs;
         if (aligned(a->out, 16) && rs % 8 == 0 && bs % 8 == 0)
-          TRY(product_map(&e.hi.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, a->n, a->m, a->B, 2 * rs, 2 * bs, 32));
+          TRY(product_map(&e.hi, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, a->n, a->m, a->B, 2 * rs, 2 * bs, 32, 64));
         else
-          e.hi.direct = static_cast<uint16_t*>(a->out);
-        TRY(box_map(&e.xhi, w.hi[from], a->n, a->m, w.ld));
-        TRY(box_map(&e.xlo, w.lo[from], a->n, a->m, w.ld));
-        e.rows = a->m, e.cols = a->n, e.alpha = alpha, e.beta = beta;
-        TRY(done(launch_orth_last(!w.tall, p, e, s), "orthogonalize-last"));
+          e.direct = static_cast<uint16_t*>(a->out);
+        TRY(done(launch_orth_last(half, !w.tall, p, e, s), "orthogonalize-last"));
       }
       r = next, sx = sn;
     }

@@ -7,12 +7,12 @@ namespace specv {
 
 cudaError_t launch_orth_squares(int dtype, const OrthInParams& p, cudaStream_t s);
 cudaError_t launch_orth_scale(int dtype, const OrthInParams& p, cudaStream_t s);
-// mn: the operands as they lie are [K][rows]
+// mn: the operands as they lie are [K][rows]; half: tiles of 128 x 128
 template <bool FINE>
-cudaError_t launch_orth_gram(bool mn, ProductParams& p, const typename SymEpi<false, FINE>::Params& e, cudaStream_t s);
+cudaError_t launch_orth_gram(bool half, bool mn, ProductParams& p, const typename SymEpi<false, FINE>::Params& e, cudaStream_t s);
 template <bool FINE>
-cudaError_t launch_orth_poly(ProductParams& p, const typename SymEpi<true, FINE>::Params& e, cudaStream_t s);
-cudaError_t launch_orth_step(bool mn, ProductParams& p, const StepEpi<false>::Params& e, cudaStream_t s);
-cudaError_t launch_orth_last(bool mn, ProductParams& p, const StepEpi<true>::Params& e, cudaStream_t s);
+cudaError_t launch_orth_poly(bool half, ProductParams& p, const typename SymEpi<true, FINE>::Params& e, cudaStream_t s);
+cudaError_t launch_orth_step(bool half, bool mn, ProductParams& p, const StepEpi<false>::Params& e, cudaStream_t s);
+cudaError_t launch_orth_last(bool half, bool mn, ProductParams& p, const StepEpi<true>::Params& e, cudaStream_t s);
 
 }  // namespace specv

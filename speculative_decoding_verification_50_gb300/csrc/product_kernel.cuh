@@ -36,7 +36,7 @@ constexpr int kLoadWarp = 0, kMmaWarp = 1, kEpiWarp = 4;  // the first epilogue 
 constexpr int kEpiRegs = 216, kLoadRegs = 72;
 constexpr int kOperandBytes = kProdHalf * kProdBK * 2;  // 16 KB
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kProdBarrierBytes = 256;
+constexpr int kProdBarrierBytes = 512;
 constexpr int kProdSmemMost = 227 * 1024;
 
 // Stages that fit beside STAGING bytes per epilogue warp, and all of a CTA's bytes.
@@ -64,10 +64,10 @@ struct ProductParams {
   int32_t stall;           // test hook: 1 + the unit whose first copy is late
 };
 
-// Instruction descriptor of tcgen05.mma kind::f16 for 256 x 256 tiles, fp32 accumulators.
-constexpr uint32_t prod_idesc(bool bf16, bool a_mn, bool b_mn) {
+// Instruction descriptor of tcgen05.mma kind::f16 for tiles of tile x tile, fp32 accumulators.
+constexpr uint32_t prod_idesc(bool bf16, bool a_mn, bool b_mn, int tile = kProdTile) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-         (static_cast<uint32_t>(kProdTile >> 3) << 17) | (static_cast<uint32_t>(kProdTile >> 4) << 24);
+         (static_cast<uint32_t>(tile >> 3) << 17) | (static_cast<uint32_t>(tile >> 4) << 24);
 }
 
 // ---- instructions
@@ -90,18 +90,19 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // A box into this CTA's shared memory; its bytes count on `bar`, which may be the pair's other CTA's.
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (!PAIR) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+    return;
+  }
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-// A box into this CTA's shared memory, counted on its own barrier.
-__device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
@@ -124,24 +125,49 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc_all(uint32_t at) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  if (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
 }
+template <bool PAIR>
 __device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if (!PAIR) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+    return;
+  }
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs once the products issued so far are done.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+// Arrives on the barrier (PAIR: at this offset in both CTAs) once the products issued so far
+// are done.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  if (!PAIR) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    return;
+  }
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"(static_cast<uint16_t>(3))
@@ -183,12 +209,12 @@ struct Unit {
 };
 
 struct Units {
-  int tm, tn, per, span, blocks, count, splits, symmetric;  // span: blocks of K; blocks: with the parts of a fine product
-  __device__ __forceinline__ Units(const ProductParams& p) {
+  int tile, tm, tn, per, span, blocks, count, splits, symmetric;  // span: blocks of K; blocks: with the parts of a fine product
+  __device__ __forceinline__ Units(const ProductParams& p, int size) : tile(size) {
     int M = p.M, K = p.K;
     if (p.rows) (p.rows_k ? K : M) = *p.rows;
     // (without any row one tile is computed all the same: its zeros are read)
-    tm = max((M + kProdTile - 1) / kProdTile, 1);
+    tm = max((M + tile - 1) / tile, 1);
     tn = p.tn;
     splits = p.splits;
     symmetric = p.symmetric;
@@ -218,8 +244,8 @@ struct Units {
       i = g * kGroup + t % rows;
       j = t / rows;
     }
-    r.m = i * kProdTile;
-    r.n = j * kProdTile;
+    r.m = i * tile;
+    r.n = j * tile;
     r.k0 = static_cast<int>(static_cast<int64_t>(blocks) * r.split / splits);
     r.k1 = static_cast<int>(static_cast<int64_t>(blocks) * (r.split + 1) / splits);
     return r;
@@ -234,7 +260,7 @@ struct EpiTile {
   int z, split, lane;
   int rows;           // rows in use (M)
   Unit unit;
-  uint64_t* bar;      // the warp's own, for what the epilogue reads, and its phase
+  uint64_t* bar;      // two of the warp's own, for what the epilogue reads, and their phases (bits)
   uint32_t phase;
   volatile int* gone;
 };
@@ -263,8 +289,10 @@ __device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
-template <bool A_MN, bool B_MN, class Epi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
+// PAIR: a cluster of two CTAs per tile of 256 x 256; else a CTA per tile of 128 x 128, for
+// products of few tiles (each operand byte then serves 128 rows, and L2 limits the rate).
+template <bool PAIR, bool A_MN, bool B_MN, class Epi>
+__global__ void __launch_bounds__(kProdThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p, const __grid_constant__ typename Epi::Params e) {
   constexpr int S = kProdStages<Epi::kStaging>;  // 6 with a 4 KB box per epilogue warp
   extern __shared__ uint8_t raw[];
@@ -272,13 +300,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
   uint8_t* staging = base + S * kStageBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kProdEpiWarps * Epi::kStaging);
   uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2, *epi = drain + 1;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(epi + kProdEpiWarps);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(epi + 2 * kProdEpiWarps);
   volatile int* gone = reinterpret_cast<volatile int*>(tmem_at + 1);
-  static_assert((2 * S + 5 + kProdEpiWarps) * 8 + 8 <= kProdBarrierBytes, "barriers");
+  static_assert((2 * S + 5 + 2 * kProdEpiWarps) * 8 + 8 <= kProdBarrierBytes, "barriers");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_rank();
-  const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+  constexpr int kTile = PAIR ? kProdTile : kProdHalf, kCtas = PAIR ? 2 : 1;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const int cluster = blockIdx.x / kCtas, clusters = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -287,26 +316,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], 2 * kProdEpiWarps);
+      mbar_init(&tempty[s], kCtas * kProdEpiWarps);
     }
     mbar_init(drain, 1);
-    for (int w = 0; w < kProdEpiWarps; ++w) mbar_init(&epi[w], 1);
+    for (int w = 0; w < 2 * kProdEpiWarps; ++w) mbar_init(&epi[w], 1);
     *gone = 0;
     fence_mbar_init();
     prefetch_map(&p.a);
     prefetch_map(&p.b);
   }
-  if (warp == kMmaWarp) tmem_alloc_all(smem_u32(tmem_at));
+  if (warp == kMmaWarp) tmem_alloc_all<PAIR>(smem_u32(tmem_at));
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
   if (!p.late_wait) pdl_wait_primary();
   pdl_launch_dependents();
 
-  const Units units(p);
+  const Units units(p, kTile);
   if (warp == kLoadWarp) {  // ---- loads
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0) {
@@ -321,23 +350,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
             break;
           }
           if (rank == 0)
-            mbar_arrive_expect_tx(&full[s], 2 * kStageBytes + ((p.stall == u + 1 && k == t.k0) ? 16 : 0));
-          const uint32_t bar = in_first_cta(smem_u32(&full[s]));
+            mbar_arrive_expect_tx(&full[s], kCtas * kStageBytes + ((p.stall == u + 1 && k == t.k0) ? 16 : 0));
+          const uint32_t bar = PAIR ? in_first_cta(smem_u32(&full[s])) : smem_u32(&full[s]);
           const uint32_t sa = smem_u32(base + s * kStageBytes), sb = sa + kOperandBytes;
           const int part = p.fine ? k / units.span : 0;
           const CUtensorMap *pa = part == 2 ? &p.a_low : &p.a, *pb = part == 1 ? &p.b_low : &p.b;
           const int kk = (k - part * units.span) * kProdBK, m = t.m + static_cast<int>(rank) * kProdHalf, n = t.n + static_cast<int>(rank) * kProdHalf;
           if (A_MN) {
-            tma_load(sa, pa, m, kk, t.z, bar);
-            tma_load(sa + kOperandBytes / 2, pa, m + 64, kk, t.z, bar);
+            tma_load<PAIR>(sa, pa, m, kk, t.z, bar);
+            tma_load<PAIR>(sa + kOperandBytes / 2, pa, m + 64, kk, t.z, bar);
           } else {
-            tma_load(sa, pa, kk, m, t.z, bar);
+            tma_load<PAIR>(sa, pa, kk, m, t.z, bar);
           }
           if (B_MN) {
-            tma_load(sb, pb, n, kk, t.z, bar);
-            tma_load(sb + kOperandBytes / 2, pb, n + 64, kk, t.z, bar);
+            tma_load<PAIR>(sb, pb, n, kk, t.z, bar);
+            tma_load<PAIR>(sb + kOperandBytes / 2, pb, n + 64, kk, t.z, bar);
           } else {
-            tma_load(sb, pb, kk, n, t.z, bar);
+            tma_load<PAIR>(sb, pb, kk, n, t.z, bar);
           }
         }
       }
@@ -368,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t d = tmem + (n & 1) * kProdTile;
+          const uint32_t d = tmem + (n & 1) * kTile;
           for (int k = first; k < end; ++k) {
             if (!landed && !prod_wait(&full[s], phase, gone)) {
               ok = false;
@@ -382,14 +411,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
             freed = n < 1 || mbar_test(&tempty[(n + 1) & 1], (((n + 1) >> 1) & 1) ^ 1);
 #pragma unroll
             for (int j = 0; j < kProdBK / 16; ++j)
-              tc_mma(d, da + j * kOperandStep<A_MN>, db + j * kOperandStep<B_MN>, p.idesc, k > first || j > 0);
-            tc_commit_pair(smem_u32(emptied));
+              tc_mma<PAIR>(d, da + j * kOperandStep<A_MN>, db + j * kOperandStep<B_MN>, p.idesc, k > first || j > 0);
+            tc_commit<PAIR>(smem_u32(emptied));
           }
-          if (ok) tc_commit_pair(smem_u32(&tfull[n & 1]));
+          if (ok) tc_commit<PAIR>(smem_u32(&tfull[n & 1]));
         }
       }
       if (*gone) {  // products in flight end before tensor memory is freed
-        tc_commit_pair(smem_u32(drain));
+        tc_commit<PAIR>(smem_u32(drain));
         const long long t0 = clock64();
         while (!mbar_try_wait_sleep(drain, 0, 20000u) && clock64() - t0 < 1000000000LL) {
         }
@@ -404,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
     q.staging = staging + (warp - kEpiWarp) * Epi::kStaging;
     q.lane = lane;
     q.rows = p.rows && !p.rows_k ? *p.rows : p.M;
-    q.bar = &epi[warp - kEpiWarp];
+    q.bar = &epi[2 * (warp - kEpiWarp)];
     q.phase = 0;
     q.gone = gone;
     int n = 0;
@@ -413,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
     for (int u = cluster; ok && u < units.count; u += clusters) {
       const Unit t = units.at(u);
       q.row0 = t.m + static_cast<int>(rank) * kProdHalf + quarter * 32;
-      q.col0 = t.n + half * kProdHalf;
+      q.col0 = t.n + half * (kTile / 2);
       q.z = t.z;
       q.split = t.split;
       q.unit = t;
@@ -422,19 +451,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
       const int chunk = Epi::kChunks && p.chunk ? p.chunk : t.k1 - t.k0;
       for (int k = t.k0; k < t.k1; k += chunk, ++n) {
         const int acc = n & 1;
-        q.tmem = tmem + acc * kProdTile + half * kProdHalf + (static_cast<uint32_t>(quarter * 32) << 16);
+        q.tmem = tmem + acc * kTile + half * (kTile / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
         ok = __all_sync(0xffffffffu, prod_wait(&tfull[acc], (n >> 1) & 1, gone));
         if (!ok) break;
         tc_fence_after();
         if (Epi::kChunks)
           Epi::add(q, state);
         else
-          Epi::tile(e, q, state);
+          Epi::template tile<kTile / 2>(e, q, state);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(in_first_cta(smem_u32(&tempty[acc])));
+        if (lane == 0) mbar_arrive_pair(PAIR ? in_first_cta(smem_u32(&tempty[acc])) : smem_u32(&tempty[acc]));
       }
-      if (Epi::kChunks && ok) Epi::tile(e, q, state);
+      if (Epi::kChunks && ok) Epi::template tile<kTile / 2>(e, q, state);
     }
     if (Epi::kStaging > 0 && lane == 0) tma_wait_all();
   }
@@ -442,9 +471,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProdThreads, 1)
   if (p.late_wait) pdl_wait_primary();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (PAIR) cluster_sync();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_free_all(tmem);
+  if (warp == kMmaWarp) tmem_free_all<PAIR>(tmem);
   const int failed = *gone;
   if (threadIdx.x == 0 && p.err) p.err[blockIdx.x] = failed;
   if (failed && p.status)
@@ -499,20 +528,6 @@ __device__ __forceinline__ void put16(const Out16& o, uint8_t* staging, int lane
   }
 }
 
-// Two boxes of the same place (o's and low's), after fetch16 has emptied the staging buffer.
-__device__ __forceinline__ void put16_pair(const Out16& o, const Out16& low, uint8_t* staging, int lane, int row0, int col0,
-                                           int z, const uint32_t (&w)[32], const uint32_t (&l)[32]) {
-  stage16(staging, lane, w);
-  stage16(staging + 4096, lane, l);
-  fence_async_shared();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store(&o.map, col0, row0, z, smem_u32(staging));
-    tma_store(&low.map, col0, row0, z, smem_u32(staging) + 4096);
-    tma_commit();
-  }
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -532,32 +547,6 @@ struct PlainEpi {
   static __device__ __forceinline__ void add(EpiTile&, State&) {}
 };
 
-// What an epilogue reads of a tile comes by TMA into the warp's staging buffer, a box of 64
-// columns of 16-bit values (and a second one of what they leave out) at a time: its own
-// loads, each lane a row, would touch 32 lines each (1024 x 1024: steps of 74 us, now 45).
-template <bool LOW>
-__device__ __forceinline__ void fetch16(const CUtensorMap* hi, const CUtensorMap* lo, const EpiTile& q, int col) {
-  if (q.lane == 0) {
-    tma_wait_read<0>();
-    mbar_arrive_expect_tx(q.bar, LOW ? 8192 : 4096);
-    tma_load_own(smem_u32(q.staging), hi, col, q.row0, q.z, q.bar);
-    if (LOW) tma_load_own(smem_u32(q.staging) + 4096, lo, col, q.row0, q.z, q.bar);
-  }
-}
-// This lane's row of a box; the warp's wait for it comes first (false: it ran out).
-__device__ __forceinline__ bool fetched(EpiTile& q) {
-  const bool ok = __all_sync(0xffffffffu, prod_wait(q.bar, q.phase, q.gone));
-  q.phase ^= 1;
-  return ok;
-}
-__device__ __forceinline__ void unstage16(const uint8_t* staging, int lane, uint32_t (&w)[32]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint4 v = *reinterpret_cast<const uint4*>(staging + lane * 128 + ((j ^ (lane & 7)) << 4));
-    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-  }
-}
-
 // C = alpha A B^T in bf16.
 struct StoreEpi : PlainEpi {
   static constexpr int kStaging = 4096;
@@ -565,9 +554,10 @@ struct StoreEpi : PlainEpi {
     Out16 out;
     float alpha;
   };
+  template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
 #pragma unroll 1
-    for (int c = 0; c < kProdHalf; c += 64) {
+    for (int c = 0; c < COLS; c += 64) {
       uint32_t w[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -590,9 +580,10 @@ struct SumEpi : PlainEpi {
     int32_t cols;
     int32_t add;
   };
+  template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
 #pragma unroll 1
-    for (int c = 0; c < kProdHalf; c += 32) {
+    for (int c = 0; c < COLS; c += 32) {
       float v[32];
       tmem_load32(q.tmem + c, v);
       if (q.row0 >= q.rows || q.col0 + c >= e.cols) continue;
