@@ -34,16 +34,15 @@ int64_t piece_tokens(int32_t N, int32_t V, bool keep) {
   return up_to((V + pieces - 1) / pieces, kProdTile);
 }
 
-// Parts that K (a piece's tokens) is cut into for dh, whose tiles alone are few: eight units
-// for each pair of SMs, so that a last round that is not full costs little (4096 x 4096 of
-// 128256 tokens, 0.7 of the rows in use: 192 tiles on 76 pairs), in parts of 64 blocks at
-// least; of 8 blocks at least as long as there are not two units a pair.
+// Parts that K (a piece's tokens) is cut into for dh, whose tiles alone are few.  Tiles for
+// every pair of SMs: eight units for each pair, so that a last round that is not full costs
+// little (4096 x 4096 of 128256 tokens, 0.7 of the rows in use: 192 tiles on 76 pairs), in
+// parts of 64 blocks at least.  Fewer: one unit for each pair, of 8 blocks at least.
 int hidden_splits(int32_t N, int32_t D, int64_t tokens) {
   const int64_t tiles = up_to(N, kProdTile) / kProdTile * (up_to(D, kProdTile) / kProdTile);
-  const int64_t pairs = api_sm_count() / 2, blocks = tokens / kProdBK;
-  const int64_t fine = std::min((8 * pairs + tiles - 1) / tiles, blocks / 64);
-  const int64_t few = std::min<int64_t>({(2 * pairs + tiles - 1) / tiles, blocks / 8, 32});
-  return static_cast<int>(std::max<int64_t>({1, fine, few}));
+  const int64_t pairs = api_sm_count() / 2, blocks = up_to(tokens, kProdBK) / kProdBK;
+  const int64_t n = tiles >= pairs ? std::min((8 * pairs + tiles - 1) / tiles, blocks / 64) : std::min(pairs / tiles, blocks / 8);
+  return static_cast<int>(std::max<int64_t>(n, 1));
 }
 
 // Offsets of the workspace's parts (bytes; all multiples of 256).
@@ -255,14 +254,14 @@ struct HeadRun {
         TRY(operand_map(&p.a, true, true, dz, n, w.rows, 1, w.tokens, 0));
         TRY(operand_map(&p.b, true, true, hidden(), a->D, w.rows, 1, hidden_stride(), 0));
         p.status = a->row_status, p.status_n = a->N;
-        StoreEpi::Params e = {};
+        Out16 e = {};
         uint16_t* out = static_cast<uint16_t*>(a->grad_head) + v * a->grad_head_stride;
         const int64_t stride = a->V > 1 ? a->grad_head_stride : up_to(a->D, 8);
         if (tma)
-          TRY(product_map(&e.out.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, a->D, n, 1, 2 * stride, 0, 32));
+          TRY(product_map(&e.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, a->D, n, 1, 2 * stride, 0, 32));
         else
-          e.out.direct = out;
-        e.out.stride = stride, e.out.cols = a->D, e.alpha = 1.f;
+          e.direct = out;
+        e.stride = stride, e.cols = a->D;
         TRY(done(launch_head_head(p, e, s), "head-dW"));
       }
       if (a->grad_hidden) {  // the piece's part of dh

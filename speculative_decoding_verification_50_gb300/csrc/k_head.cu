@@ -253,8 +253,9 @@ cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStr
 cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s) {
   return launch_product<true, false, true, SumEpi>(p, e, s);
 }
-cudaError_t launch_head_head(ProductParams& p, const StoreEpi::Params& e, cudaStream_t s) {
-  return launch_product<true, true, true, StoreEpi>(p, e, s);
+cudaError_t launch_head_head(ProductParams& p, const Out16& out, cudaStream_t s) {
+  if (p.K <= 16 * kProdBK) return launch_product<true, true, true, StoreEpi<true>>(p, {out, 1.f}, s);
+  return launch_product<true, true, true, StoreEpi<false>>(p, {out, 1.f}, s);
 }
 cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t s) {
   return launch_grid(head_rows_kernel, 1, kRowsThreads, s, p);

@@ -43,7 +43,7 @@ __device__ __forceinline__ void squares_add(ScaledSquares& a, float& inv, const 
 
 // Vector j of a row: VW elements, zeros past its end.
 template <int DT>
-__device__ __forceinline__ void row_vec(const void* row, int j, int cols, bool vec, float (&x)[Elem<DT>::VW]) {
+__device__ __forceinline__ void row_vec(const void* row, int64_t j, int64_t cols, bool vec, float (&x)[Elem<DT>::VW]) {
   constexpr int VW = Elem<DT>::VW;
   if (vec && (j + 1) * VW <= cols) {
     Elem<DT>::unpack(Elem<DT>::vec(row, j * VW), x);
@@ -53,8 +53,28 @@ __device__ __forceinline__ void row_vec(const void* row, int j, int cols, bool v
   }
 }
 
+// f(row, vector) over this CTA's share of a matrix's rows of nv vectors: a share of a long
+// row's vectors per CTA (rows without gaps are one), or rows in turn.
+template <typename F>
+__device__ __forceinline__ void each_vec(const OrthInParams& p, int64_t nv, F&& f) {
+  if (p.rows == 1) {
+#pragma unroll 4
+    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x; j < nv;
+         j += static_cast<int64_t>(gridDim.x) * kOrthThreads)
+      f(0, j);
+    return;
+  }
+  // a row per `lanes` threads, the power of two that is at most its vectors
+  int lanes = 32;
+  while (lanes < kOrthThreads && 2 * lanes <= nv) lanes *= 2;
+  const int per = kOrthThreads / lanes, first = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * per + first; r < p.rows; r += static_cast<int64_t>(gridDim.x) * per)
+#pragma unroll 4
+    for (int64_t j = lane; j < nv; j += lanes) f(r, j);
+}
+
 template <int DT>
-__device__ __forceinline__ const void* row_at(const OrthInParams& p, int z, int r) {
+__device__ __forceinline__ const void* row_at(const OrthInParams& p, int z, int64_t r) {
   return static_cast<const char*>(p.in) + (z * p.batch_stride + r * p.row_stride) * Elem<DT>::ES;
 }
 
@@ -68,17 +88,15 @@ __global__ void __launch_bounds__(kOrthThreads) orth_squares_kernel(const OrthIn
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int VW = Elem<DT>::VW;
-  const int z = blockIdx.y, nv = (p.cols + VW - 1) / VW;
+  const int z = blockIdx.y;
+  const int64_t nv = (p.cols + VW - 1) / VW;
   ScaledSquares a = {kSquaresLeast, 0.f};
   float inv = 1.f / kSquaresLeast;
-  const int64_t all = static_cast<int64_t>(p.rows) * nv;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x; i < all;
-       i += static_cast<int64_t>(gridDim.x) * kOrthThreads) {
-    const int r = static_cast<int>(i / nv), j = static_cast<int>(i - static_cast<int64_t>(r) * nv);
+  each_vec(p, nv, [&](int64_t r, int64_t j) {
     float x[VW];
     row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec, x);
     squares_add<VW>(a, inv, x);
-  }
+  });
   squares_warp(a);
   if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = a;
   __syncthreads();
@@ -111,11 +129,7 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInPa
     if (p.norm) p.norm[z] = bad ? __int_as_float(0x7fc00000) : sum.m * root;
     if (p.status) p.status[z] = bad ? kNonFinite : 0;
   }
-  const int nv = static_cast<int>(p.ld / VW);
-  const int64_t all = static_cast<int64_t>(p.rows) * nv;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x; i < all;
-       i += static_cast<int64_t>(gridDim.x) * kOrthThreads) {
-    const int r = static_cast<int>(i / nv), j = static_cast<int>(i - static_cast<int64_t>(r) * nv);
+  each_vec(p, p.ld / VW, [&](int64_t r, int64_t j) {
     float x[VW];
     row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec, x);
     uint32_t hi[VW / 2], lo[VW / 2];
@@ -126,7 +140,7 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInPa
       const float2 g = unpack_f16(hi[k]);
       lo[k] = pack_f16(u - g.x, v - g.y);
     }
-    const int64_t at = (static_cast<int64_t>(z) * p.rows + r) * p.ld + j * VW;
+    const int64_t at = z * p.matrix + r * p.ld + j * VW;
     if constexpr (VW == 8) {
       *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -134,7 +148,7 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInPa
       *reinterpret_cast<uint2*>(p.hi + at) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(p.lo + at) = make_uint2(lo[0], lo[1]);
     }
-  }
+  });
 }
 
 namespace {

@@ -47,13 +47,18 @@ struct OrthSpace {
 };
 
 // Whether a product goes by tiles of 128 x 128, a CTA each, in the place of 256 x 256, a pair
-// each: where that ends sooner.  Cycles of a round of tiles: those of a block of K, 620 and
-// 420 (256 are the tensor core's, the rest L2's), and of what is not hidden under the next
-// tile, about 6000 and 4000.
+// each: where that ends sooner.  Cycles of a block of K: 256 and 512 are the tensor core's,
+// the more SMs take part the more are L2's (up to 540 and 620); and of what is not hidden
+// under the next tile, about 4000 and 6000.  us of a call by 128, by 256 and by this rule:
+// 128 x 512 134, 160, 134; 1000 x 2333 205, 240, 205; 1024 x 4096 257, 261, 242;
+// 24 x 1024 x 1024 830, 687, 687; 4096 x 4096 1611, 1040, 1040.
 bool small_tiles(const ProductParams& p) {
-  const int64_t blocks = (p.K + kProdBK - 1) / kProdBK * (p.fine ? 3 : 1);
-  auto rounds = [&](int tile, int64_t ctas) { return (product_units(p, tile) + ctas - 1) / ctas; };
-  return rounds(kProdHalf, api_sm_count()) * blocks * 420 + 4000 < rounds(kProdTile, api_sm_count() / 2) * blocks * 620 + 6000;
+  const double blocks = static_cast<double>((p.K + kProdBK - 1) / kProdBK * (p.fine ? 3 : 1));
+  auto cycles = [&](int tile, int64_t ctas, double least, double shared, double rest) {
+    const int64_t units = product_units(p, tile), rounds = (units + ctas - 1) / ctas;
+    return rounds * blocks * (least + shared * std::min(1.0, static_cast<double>(units) / ctas)) + rest;
+  };
+  return cycles(kProdHalf, api_sm_count(), 280, 260, 4000) < cycles(kProdTile, api_sm_count() / 2, 540, 80, 6000);
 }
 
 OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
@@ -199,8 +204,9 @@ struct OrthRun {
       const int vw = a->dtype == SPECV_BF16 ? 8 : 4;
       p.vec = aligned(a->update, 16) && p.row_stride % vw == 0 && p.batch_stride % vw == 0;
       p.part = reinterpret_cast<ScaledSquares*>(ws + w.part);
-      p.hi = at(w.hi[0]), p.lo = at(w.lo[0]), p.ld = w.ld, p.scale = static_cast<float>(sx);
+      p.hi = at(w.hi[0]), p.lo = at(w.lo[0]), p.ld = w.ld, p.matrix = zx(), p.scale = static_cast<float>(sx);
       p.norm = a->norm, p.status = a->row_status;
+      if (p.row_stride == a->n && w.ld == a->n) p.cols *= p.rows, p.ld = p.cols, p.rows = 1;
       TRY(done(launch_orth_squares(a->dtype, p, s), "orthogonalize-norm"));
       TRY(done(launch_orth_scale(a->dtype, p, s), "orthogonalize-scale"));
     }

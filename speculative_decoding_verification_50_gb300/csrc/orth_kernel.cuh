@@ -30,14 +30,15 @@ struct ScaledSquares {
 };
 
 struct OrthInParams {
-  int32_t rows, cols, batch, blocks;  // blocks per matrix
+  int64_t rows, cols;                 // (a matrix without gaps, also in X: one row)
+  int32_t batch, blocks;              // blocks per matrix
   int32_t vec;                        // rows start at 16-byte boundaries
   const void* in;
   int64_t batch_stride, row_stride;
   ScaledSquares* part;                // [batch][blocks]
   // orth_scale_kernel
   uint16_t *hi, *lo;                  // [batch][rows][ld]
-  int64_t ld;
+  int64_t ld, matrix;                 // strides of a row and a matrix
   float scale;                        // X is kept times this
   float* norm;                        // optional [batch]
   int32_t* status;                    // optional [batch]

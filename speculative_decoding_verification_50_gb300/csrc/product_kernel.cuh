@@ -120,7 +120,6 @@ template <int LEFT>
 __device__ __forceinline__ void tma_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
-__device__ __forceinline__ void tma_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(kProdThreads, 1)
       }
       if (Epi::kChunks && ok) Epi::template tile<kTile / 2>(e, q, state);
     }
-    if (Epi::kStaging > 0 && lane == 0) tma_wait_all();
+    if (Epi::kStaging > 0 && lane == 0) tma_wait_read<0>();  // (the grid's end waits for the writes)
   }
   __syncwarp();
   if (p.late_wait) pdl_wait_primary();
@@ -499,12 +498,14 @@ __device__ __forceinline__ void stage16(uint8_t* staging, int lane, const uint32
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// (rows: those of C in use; row0 and col0 of the 32 x 64 box)
+// (rows: those of C in use; row0 and col0 of the 32 x 64 box; LEFT: stores that may still
+// read other buffers)
+template <int LEFT = 0>
 __device__ __forceinline__ void put16(const Out16& o, uint8_t* staging, int lane, int row0, int col0, int z, int rows,
                                       const uint32_t (&w)[32]) {
   if (row0 >= rows || col0 >= o.cols) return;
   if (!o.direct) {
-    if (lane == 0) tma_wait_read<0>();
+    if (lane == 0) tma_wait_read<LEFT>();
     __syncwarp();
     stage16(staging, lane, w);
     fence_async_shared();
@@ -547,9 +548,11 @@ struct PlainEpi {
   static __device__ __forceinline__ void add(EpiTile&, State&) {}
 };
 
-// C = alpha A B^T in bf16.
+// C = alpha A B^T in bf16.  TWICE: two staging buffers, for products of so short a K that
+// writing C bounds them (64 rows x 1024 x 32000: 23 us, with two 17).
+template <bool TWICE>
 struct StoreEpi : PlainEpi {
-  static constexpr int kStaging = 4096;
+  static constexpr int kStaging = TWICE ? 8192 : 4096;
   struct Params {
     Out16 out;
     float alpha;
@@ -566,7 +569,7 @@ struct StoreEpi : PlainEpi {
 #pragma unroll
         for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16(v[2 * j] * e.alpha, v[2 * j + 1] * e.alpha);
       }
-      put16(e.out, q.staging, q.lane, q.row0, q.col0 + c, q.z, q.rows, w);
+      put16<TWICE ? 1 : 0>(e.out, q.staging + (TWICE ? (c & 64) * 64 : 0), q.lane, q.row0, q.col0 + c, q.z, q.rows, w);
     }
   }
 };
