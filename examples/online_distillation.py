@@ -5,8 +5,10 @@ A round: the drafter samples K tokens under temperature, top-k, top-p and min-p
 (specv_sample, which also writes the rows it sampled from); the target's rows
 are kept as their top logits (specv_top_logits), put under the same rules
 (specv_filter_logits) and verified against the drafts (specv_verify); and the
-drafter takes a step on the distillation loss (distill_loss) at the positions
-whose context the target agreed with.  Both models are bigram tables of random
+drafter takes a step at the positions whose context the target agreed with: on the
+distillation loss (distill_loss), or with --loss tokens on the cross entropy of the
+tokens that the target kept, from the drafter's hidden states (head_loss); by Adam, or with
+--update orthogonal by the head's orthogonalised momentum (specv_orthogonalize).  Both models are bigram tables of random
 weights, the drafter's of lower rank, so that the example needs no data.
 
     python examples/online_distillation.py --rounds 200
@@ -35,18 +37,36 @@ class Bigram(torch.nn.Module):
         self.head = table(dim, vocab)
         self.scale = scale / dim ** 0.5
 
+    def hidden(self, tokens):
+        return self.embed[tokens.long()].bfloat16()
+
     def forward(self, tokens):
-        x = self.embed[tokens.long()].bfloat16()
-        return (x @ self.head.bfloat16()) * self.scale
+        return (self.hidden(tokens) @ self.head.bfloat16()) * self.scale
+
+
+class Orthogonal:
+    """Steps along a matrix's momentum with its singular values drawn towards one."""
+
+    def __init__(self, matrix, lr, momentum=0.9):
+        self.matrix, self.lr, self.momentum = matrix, lr, momentum
+        self.sum = torch.zeros_like(matrix)
+
+    def step(self):
+        self.sum.mul_(self.momentum).add_(self.matrix.grad)
+        o = sv.specv_orthogonalize(self.sum)["orthogonal"]
+        with torch.no_grad():
+            self.matrix.add_(o, alpha=-self.lr * max(1.0, self.matrix.shape[1] / self.matrix.shape[0]) ** 0.5)
 
 
 def run(rounds=200, batch=64, drafts=4, vocab=2048, top=64, lr=0.02, temperature=0.8, top_k=50,
-        top_p=0.95, min_p=0.02, device="cuda:0", seed=1):
+        top_p=0.95, min_p=0.02, device="cuda:0", seed=1, loss="distill", update="adam"):
     """Accepted drafts per entry and round (the mean), and the loss, per round."""
     gen = torch.Generator(device=device).manual_seed(seed)
     target = Bigram(vocab, 32, 4.0, device, seed + 1).requires_grad_(False)
     drafter = Bigram(vocab, 24, 1.0, device, seed + 2)
-    adam = torch.optim.Adam(drafter.parameters(), lr=lr)
+    tokens_loss, orthogonal = loss == "tokens", update == "orthogonal"
+    adam = torch.optim.Adam([drafter.embed] if orthogonal else drafter.parameters(), lr=lr)
+    steps = [adam] + ([Orthogonal(drafter.head, lr)] if orthogonal else [])
     rules = dict(top_k=torch.full((batch,), top_k, dtype=torch.int32, device=device),
                  top_p=torch.full((batch,), top_p, device=device),
                  min_p=torch.full((batch,), min_p, device=device))
@@ -72,12 +92,17 @@ def run(rounds=200, batch=64, drafts=4, vocab=2048, top=64, lr=0.02, temperature
         n = out["accept_len"]
         # positions 0 .. n: their contexts are tokens that the target kept
         weights = (torch.arange(drafts + 1, device=device) <= n[:, None]).float().view(-1)
-        loss = sv.distill_loss(drafter(context.view(-1)), teacher["ids"], teacher["values"],
-                               teacher_lse=teacher["lse"], weights=weights, tail=True)
+        if tokens_loss:  # positions behind the last kept token have none (-1)
+            loss = sv.head_loss(drafter.hidden(context.view(-1)), drafter.head.t().bfloat16().contiguous(),
+                                out["out_tokens"].view(-1), scale=drafter.scale, weights=weights)
+        else:
+            loss = sv.distill_loss(drafter(context.view(-1)), teacher["ids"], teacher["values"],
+                                   teacher_lse=teacher["lse"], weights=weights, tail=True)
         loss = loss.sum() / weights.sum()
-        adam.zero_grad(set_to_none=True)
+        drafter.zero_grad(set_to_none=True)
         loss.backward()
-        adam.step()
+        for s in steps:
+            s.step()
         last = out["out_tokens"].gather(1, n[:, None].long())[:, 0].contiguous()
         accepted.append(n.float().mean())
         losses.append(loss.detach())
@@ -89,8 +114,10 @@ def main():
     ap.add_argument("--rounds", type=int, default=200)
     ap.add_argument("--batch", type=int, default=64)
     ap.add_argument("--vocab", type=int, default=2048)
+    ap.add_argument("--loss", choices=("distill", "tokens"), default="distill")
+    ap.add_argument("--update", choices=("adam", "orthogonal"), default="adam")
     a = ap.parse_args()
-    accepted, losses = run(a.rounds, a.batch, vocab=a.vocab)
+    accepted, losses = run(a.rounds, a.batch, vocab=a.vocab, loss=a.loss, update=a.update)
     step = max(1, a.rounds // 10)
     for i in range(0, a.rounds, step):
         part = slice(i, i + step)

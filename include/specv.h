@@ -85,7 +85,7 @@ typedef enum { SPECV_BF16 = 0, SPECV_FP32 = 1 } specv_dtype;
                                  the row instead of waiting forever (not
                                  expected on a healthy GPU; for tests, the
                                  environment variable SPECV_TEST_STALL="A:<i>"
-                                 to "D:<n>", read once per process, makes one
+                                 to "F:<n>", read once per process, makes one
                                  such wait run out) */
 
 /*
@@ -525,7 +525,7 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
  * out = X in bf16; norm[k] = |G|_F.  With (3.4445, -4.7750, 2.0315) five steps bring singular
  * values from 0.01 |G|_F on to between 0.7 and 1.2.
  * Products are of fp16 operands, summed in fp32; X is kept to 21 bits beside them: out is off
- * the exact steps by about 2e-3 of its norm at most, most of it the rounding to bf16
+ * five exact steps by about 2e-3 of its norm at most, most of it the rounding to bf16
  * (low-rank and badly scaled updates too).
  * A matrix of zeros gives zeros.  Status of a matrix: SPECV_ROW_NONFINITE (an entry that is
  * NaN or infinite): out 0, norm NaN; SPECV_ROW_DEVICE_TIMEOUT, on every matrix: out undefined.

@@ -226,7 +226,8 @@ struct HeadRun {
   }
 
   specv_status backward() {
-    const bool tma = aligned(a->grad_head, 16) && a->grad_head_stride % 8 == 0;
+    // (TMA stores whole 16-byte words: what lies behind a row stays as it is)
+    const bool tma = aligned(a->grad_head, 16) && a->grad_head_stride % 8 == 0 && a->D % 8 == 0;
     int piece = 0;
     for (int64_t v = 0; v < a->V; v += w.tokens, ++piece) {
       const int32_t n = static_cast<int32_t>(std::min<int64_t>(w.tokens, a->V - v));

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   }
   if (k != 0 || r >= p.N) return;
   float lse = 0.f, nll = 0.f, loss = 0.f;
-  int status = t < -1 || t >= p.V ? kBadToken : 0;
+  int status = (t < -1 || t >= p.V) && w != 0.f ? kBadToken : 0;
   HeadRow row = {0.f, 0.f, 0.f, -1};
   if (use) {
     const float zt = p.z_target[at], d2 = (m - zt) * c2;
@@ -155,14 +155,13 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
     if (failed) status |= kTimeout;
     if (p.bad && p.bad[at]) status |= kNonFinite;
     if (!(s - s == 0.f) || !(lse - lse == 0.f)) status |= kNonFinite;
-    if (status) {
-      lse = nll = __int_as_float(0x7fc00000);
-    } else {
+    if (!status) {
       loss = w * nll;
       const float g = w * p.scale;
       row = {lse * kLog2e, g, g * expm1f(-nll), t};
     }
   }
+  if (status) lse = nll = __int_as_float(0x7fc00000);
   p.loss[r] = loss;
   if (p.stats) {
     p.stats[2 * r] = lse;

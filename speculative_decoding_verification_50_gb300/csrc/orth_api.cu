@@ -172,6 +172,7 @@ struct OrthRun {
       typename SymEpi<false, FINE>::Params e = {};
       TRY(sym_out(e, w.gram, FINE));
       e.alpha = static_cast<float>(ss / (sx * sx));
+      if (launches == 2) p.stall = api_test_stall('F');
       TRY(done(launch_orth_gram<FINE>(half, w.tall, p, e, s), "orthogonalize-gram"));
     }
     ProductParams p = product(w.s, w.s, w.s, false, false, true, half);
@@ -243,7 +244,8 @@ struct OrthRun {
         TRY(step(e));
         const int64_t rs = a->m > 1 ? a->out_row_stride : up_to(a->n, 8), bs = a->B > 1 ? a->out_batch_stride : 0;
         e.stride = rs, e.zstride = bs;
-        if (aligned(a->out, 16) && rs % 8 == 0 && bs % 8 == 0)
+        // (TMA stores whole 16-byte words: what lies behind a row stays as it is)
+        if (aligned(a->out, 16) && rs % 8 == 0 && bs % 8 == 0 && a->n % 8 == 0)
           TRY(product_map(&e.hi, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->out, a->n, a->m, a->B, 2 * rs, 2 * bs, 32, 64));
         else
           e.direct = static_cast<uint16_t*>(a->out);

@@ -279,8 +279,9 @@ bool persistent_path() {
 // ring stage of row-statistics item i (staged path) wait for 16 bytes that no
 // copy brings, "B:<b>" the first residual stage of batch row b in the decision
 // kernel, "C:<n>" and "D:<n>" the first copy of the first and of the second pass
-// over row n in the distillation kernel; the bounded wait then runs out (about a second) and the row comes
-// back flagged SPECV_ROW_DEVICE_TIMEOUT.  Returns 1 + that index for kernel
+// over row n in the distillation kernel, "E:<t>" and "F:<t>" the first copy of tile t of the
+// logits of the head's loss and of an update's first product; the bounded wait then runs out
+// (about a second) and the row (there: every row) comes back flagged SPECV_ROW_DEVICE_TIMEOUT.  Returns 1 + that index for kernel
 // `which`, else 0.
 int test_stall(char which) {
   struct Stall {
@@ -289,7 +290,7 @@ int test_stall(char which) {
   };
   static const Stall st = [] {
     const char* e = getenv("SPECV_TEST_STALL");
-    if (e && e[0] >= 'A' && e[0] <= 'D' && e[1] == ':') return Stall{e[0], atoi(e + 2)};
+    if (e && e[0] >= 'A' && e[0] <= 'F' && e[1] == ':') return Stall{e[0], atoi(e + 2)};
     return Stall{0, -1};
   }();
   return (st.v >= 0 && st.k == which) ? st.v + 1 : 0;

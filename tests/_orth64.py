@@ -6,9 +6,9 @@ each of the three roundings and the operands' own makes an error of relative siz
 at most (roundings of many entries, evenly spread over their half step, are independent), in
 terms whose sizes are |b| s^2 and |c| s^4 for singular values up to s = 1.21.  With the
 default coefficients these are below 7 and 4.4 times X, and the sum that they are part of is
-X' itself, at least 0.65 X for a direction that has arrived.  A step's derivative by a
-singular value that has arrived is below 3.5, its usual size below one, so that errors of
-earlier steps fade.  In all: (7 (u) + 4.4 (2 u)) / sqrt(3) / 0.65 = 14 u where errors agree in
+X' itself, at least 0.65 X for a direction that has arrived.  Five steps bring most directions
+just there.  A later step multiplies what is off by its derivative a + 3 b s^2 + 5 c s^4: -1.1
+at s = 0.7, -1.6 at 0.87, -0.7 at 1, 1.7 at 1.13: by 1.5.  In all: (7 (u) + 4.4 (2 u)) / sqrt(3) / 0.65 = 14 u where errors agree in
 every direction; over directions that do not agree they add as squares, which leaves less the
 wider the matrix is: a third for more than 256 rows, 2.3e-3.  Up to 256 rows S, P and the
 products' X have 21 bits: u = 2^-21, without the third.  The result's own rounding to bf16 is
@@ -35,8 +35,8 @@ def orth64(G, steps=5, coefficients=COEFFICIENTS):
     return X, norm[..., 0, 0]
 
 
-def bound(m, n):
-    steps = 14 * 2.0 ** -21 if min(m, n) <= 256 else 14 * 2.0 ** -11 / 3
+def bound(m, n, steps=5):
+    steps = 1.5 ** max(0, steps - 5) * (14 * 2.0 ** -21 if min(m, n) <= 256 else 14 * 2.0 ** -11 / 3)
     return (steps ** 2 + (2.0 ** -8) ** 2 / (3 if m * n >= 4096 else 1)) ** 0.5
 
 
