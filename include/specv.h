@@ -532,8 +532,8 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
  * Coefficients that may let a singular value grow past 1024 within the steps (by bounds over
  * [0, 1]) are refused with SPECV_ERR_INVALID_ARG.
  * out may be update itself (bf16).  workspace: device memory of
- * specv_orthogonalize_workspace_bytes() bytes (8 m n + 4 min(m, n)^2 per matrix, about),
- * 256-byte aligned.
+ * specv_orthogonalize_workspace_bytes() bytes (8 m n + 4 min(m, n)^2 per matrix, about; 0 for
+ * matrices of a side up to 128 and another up to 2048, one kernel), 256-byte aligned.
  */
 typedef struct {
   int32_t B, m, n;

@@ -15,7 +15,7 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int64_t up_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-constexpr int kMostSteps = 32;
+constexpr int kMostSteps = kSmallSteps;
 constexpr double kMostGrowth = 1024;
 
 // The largest |a x + b x^3 + c x^5| for x in [0, r], and |b t + c t^2| for t in [0, r^2].
@@ -45,6 +45,15 @@ struct OrthSpace {
   int32_t s, t, blocks;
   bool tall, fine;
 };
+
+// CTAs of a cluster that holds a matrix of a smaller side up to 128 in its shared memory
+// (powers of two up to 16, so that they share its rows evenly), or 0: it does not fit.
+int small_ctas(int32_t s, int32_t t) {
+  if (s > kSmallSide || t > 16 * kSmallSide) return 0;
+  int C = 1;
+  while (C * kSmallSide < t) C *= 2;
+  return C;
+}
 
 // Whether a product goes by tiles of 128 x 128, a CTA each, in the place of 256 x 256, a pair
 // each: where that ends sooner.  Cycles of a block of K: 256 and 512 are the tensor core's,
@@ -76,6 +85,7 @@ OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
   const int64_t vectors = static_cast<int64_t>(m) * ((n + 3) / 4);
   w.blocks = static_cast<int32_t>(std::max<int64_t>(
       1, std::min((vectors + 8 * kOrthThreads - 1) / (8 * kOrthThreads), std::max<int64_t>(1, 8LL * api_sm_count() / B))));
+  if (small_ctas(w.s, w.t)) return w;  // (in one kernel, on chip)
   w.part = take(sizeof(ScaledSquares) * static_cast<size_t>(B) * w.blocks);
   const size_t x = 2 * static_cast<size_t>(B) * m * w.ld, q = 2 * static_cast<size_t>(B) * w.s * w.lds;
   w.hi[0] = take(x), w.hi[1] = take(x), w.lo[0] = take(x);
@@ -162,7 +172,7 @@ struct OrthRun {
 
   // S, then P = b S + c S S
   template <bool FINE>
-  specv_status symmetric(int from, double sx, double ss, double sp) {
+  specv_status symmetric(int from, const SmallStep& f) {
     bool half;
     {
       ProductParams p = product(w.s, w.s, w.t, w.tall, w.tall, true, half);
@@ -171,7 +181,7 @@ struct OrthRun {
       p.b = p.a, p.b_low = p.a_low;
       typename SymEpi<false, FINE>::Params e = {};
       TRY(sym_out(e, w.gram, FINE));
-      e.alpha = static_cast<float>(ss / (sx * sx));
+      e.alpha = f.gram;
       if (launches == 2) p.stall = api_test_stall('F');
       TRY(done(launch_orth_gram<FINE>(half, w.tall, p, e, s), "orthogonalize-gram"));
     }
@@ -183,7 +193,7 @@ struct OrthRun {
     TRY(sym_out(e, w.poly, FINE));
     TRY(box_map(&e.chi, w.gram[0], w.s, w.s, w.lds));
     if (FINE) TRY(box_map(&e.clo, w.gram[1], w.s, w.s, w.lds));
-    e.alpha = static_cast<float>(a->c * sp / (ss * ss)), e.beta = static_cast<float>(a->b * sp / ss);
+    e.alpha = f.poly, e.beta = f.poly_s;
     return done(launch_orth_poly<FINE>(half, p, e, s), "orthogonalize-poly");
   }
   template <typename Params>
@@ -196,7 +206,35 @@ struct OrthRun {
     return SPECV_OK;
   }
 
+  // The factors that a step multiplies its products by: what they are kept times, before and after.
+  SmallStep factors(double r, double sx, double sn) const {
+    const double ss = keep_scale(r * r), sp = keep_scale(poly_bound(a->b, a->c, r));
+    return {static_cast<float>(ss / (sx * sx)), static_cast<float>(a->c * sp / (ss * ss)), static_cast<float>(a->b * sp / ss),
+            static_cast<float>(sn / (sp * sx)), static_cast<float>(a->a * sn / sx)};
+  }
+
+  specv_status small() {
+    SmallParams p = {};
+    p.m = a->m, p.n = a->n, p.s = w.s, p.t = w.t, p.tall = w.tall, p.steps = a->steps;
+    p.C = small_ctas(w.s, w.t);
+    p.in = a->update, p.row_stride = a->m > 1 ? a->row_stride : a->n, p.batch_stride = a->B > 1 ? a->batch_stride : 0;
+    p.out = static_cast<uint16_t*>(a->out);
+    p.out_row_stride = a->m > 1 ? a->out_row_stride : a->n, p.out_batch_stride = a->B > 1 ? a->out_batch_stride : 0;
+    p.vec = aligned(a->update, a->dtype == SPECV_BF16 ? 8 : 16) && p.row_stride % 4 == 0 && p.batch_stride % 4 == 0;
+    p.out_vec = aligned(a->out, 8) && p.out_row_stride % 4 == 0 && p.out_batch_stride % 4 == 0;
+    p.norm = a->norm, p.status = a->row_status;
+    double r = 1, sx = keep_scale(r);
+    p.scale = static_cast<float>(sx);
+    for (int k = 0; k < a->steps; ++k) {
+      const double next = 1.01 * step_bound(a->a, a->b, a->c, r), sn = k + 1 == a->steps ? 1.0 : keep_scale(next);
+      p.step[k] = factors(r, sx, sn);
+      r = next, sx = sn;
+    }
+    return done(launch_orth_small(a->dtype, p, a->B, s), "orthogonalize");
+  }
+
   specv_status all() {
+    if (small_ctas(w.s, w.t)) return small();
     double r = 1, sx = keep_scale(r);
     {
       OrthInParams p = {};
@@ -214,9 +252,9 @@ struct OrthRun {
     for (int k = 0; k < a->steps; ++k) {
       const int from = k & 1;
       const bool last = k + 1 == a->steps;
-      const double ss = keep_scale(r * r), sp = keep_scale(poly_bound(a->b, a->c, r));
       const double next = 1.01 * step_bound(a->a, a->b, a->c, r), sn = last ? 1.0 : keep_scale(next);
-      TRY(w.fine ? symmetric<true>(from, sx, ss, sp) : symmetric<false>(from, sx, ss, sp));
+      const SmallStep f = factors(r, sx, sn);
+      TRY(w.fine ? symmetric<true>(from, f) : symmetric<false>(from, f));
       // X' = a X + P X, or a X + X P (P is its own transpose)
       bool half;
       ProductParams p = product(a->m, a->n, w.s, false, !w.tall, false, half);
@@ -230,7 +268,7 @@ struct OrthRun {
         TRY(box_map(&e.xhi, w.hi[from], a->n, a->m, w.ld));
         TRY(box_map(&e.xlo, w.lo[from], a->n, a->m, w.ld));
         e.rows = a->m, e.cols = a->n;
-        e.alpha = static_cast<float>(sn / (sp * sx)), e.beta = static_cast<float>(a->a * sn / sx);
+        e.alpha = f.step, e.beta = f.step_y;
         return SPECV_OK;
       };
       if (!last) {
@@ -271,7 +309,7 @@ specv_status specv_orthogonalize(const specv_orth_args* a, void* workspace, size
   TRY(check_orth(a));
   if (a->B == 0) return api_done(0);
   OrthRun run = {a, orth_space(a->B, a->m, a->n), static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)};
-  if (!workspace || workspace_bytes < run.w.bytes)
+  if (run.w.bytes && (!workspace || workspace_bytes < run.w.bytes))
     return api_fail(SPECV_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu", run.w.bytes, workspace ? workspace_bytes : 0);
   if (!aligned(workspace, 256)) return api_fail(SPECV_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   TRY(run.all());

@@ -41,7 +41,8 @@ def check(G, **how):
 
 
 SHAPES = [(1, 1), (1, 7), (2, 2), (3, 300), (64, 64), (65, 127), (128, 512), (255, 257), (256, 256), (300, 200), (512, 100),
-          (700, 1111), (1030, 520), (2000, 64)]
+          (700, 1111), (1030, 520), (2000, 64),
+          (128, 128), (128, 129), (127, 2048), (2048, 128), (128, 2049), (2500, 33), (1, 2048), (130, 1), (16, 1025)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -56,7 +57,7 @@ def test_spectra(shape, kind):
     check(matrix(shape, kind))
 
 
-@pytest.mark.parametrize("shape", [(3, 64, 64), (5, 100, 333), (4, 333, 100), (24, 130, 130), (2, 1, 9)])
+@pytest.mark.parametrize("shape", [(3, 64, 64), (5, 100, 333), (4, 333, 100), (24, 130, 130), (2, 1, 9), (200, 40, 90), (30, 600, 128)])
 def test_batches(shape):
     G = matrix(shape, dtype=torch.bfloat16)
     G *= torch.logspace(-6, 6, shape[0], device="cuda").to(G.dtype)[:, None, None]
@@ -169,7 +170,7 @@ def test_graphs_and_streams():
     assert all(torch.equal(o, direct[k % 2]) for k, o in enumerate(got))
 
 
-@pytest.mark.parametrize("shape", [(1, 64, 100), (2, 300, 333)])
+@pytest.mark.parametrize("shape", [(1, 130, 200), (2, 300, 333)])
 def test_workspace_of_the_size_asked_for(shape):
     G = matrix(shape)
     need = sv.load_library().specv_orthogonalize_workspace_bytes(*shape)

@@ -24,7 +24,7 @@ def head(**how):
 
 
 def orth(**how):
-    a = sv.OrthArgs(2, 64, 100, sv.SPECV_BF16, 256, 6400, 100, 5, 3.4445, -4.7750, 2.0315, 256, 6400, 100, 256, 256)
+    a = sv.OrthArgs(2, 200, 300, sv.SPECV_BF16, 256, 60000, 300, 5, 3.4445, -4.7750, 2.0315, 256, 60000, 300, 256, 256)
     for k, v in how.items():
         setattr(a, k, v)
     return a
@@ -76,8 +76,8 @@ def test_head_loss_workspace(lib):
 
 ORTH_BAD = [dict(B=-1), dict(m=0), dict(n=0), dict(dtype=9), dict(steps=0), dict(steps=33), dict(a=float("nan")),
             dict(c=float("inf")), dict(a=5.0), dict(b=0.0), dict(a=2.0, b=1.0, c=0.0, steps=32), dict(update=None), dict(out=None),
-            dict(update=257), dict(out=1), dict(norm=2), dict(row_status=6), dict(row_stride=99), dict(out_row_stride=99),
-            dict(batch_stride=6399), dict(out_batch_stride=6399)]
+            dict(update=257), dict(out=1), dict(norm=2), dict(row_status=6), dict(row_stride=299), dict(out_row_stride=299),
+            dict(batch_stride=59999), dict(out_batch_stride=59999)]
 
 
 @pytest.mark.parametrize("how", ORTH_BAD, ids=str)
@@ -89,8 +89,9 @@ def test_orthogonalize_refusals(lib, how):
 def test_orthogonalize_other_refusals(lib):
     call = lib.specv_orthogonalize
     assert call(None, 256, 1 << 40, None) == sv.SPECV_ERR_INVALID_ARG
-    need = lib.specv_orthogonalize_workspace_bytes(2, 64, 100)
-    assert need > 0 and lib.specv_orthogonalize_workspace_bytes(0, 64, 100) == 0
+    need = lib.specv_orthogonalize_workspace_bytes(2, 200, 300)
+    assert need > 0 and lib.specv_orthogonalize_workspace_bytes(0, 200, 300) == 0
+    assert lib.specv_orthogonalize_workspace_bytes(9, 2048, 128) == 0 < lib.specv_orthogonalize_workspace_bytes(9, 2049, 128)
     assert call(ctypes.byref(orth()), 256, need - 1, None) == sv.SPECV_ERR_WORKSPACE
     assert call(ctypes.byref(orth()), None, need, None) == sv.SPECV_ERR_WORKSPACE
     assert call(ctypes.byref(orth()), 384, need, None) == sv.SPECV_ERR_INVALID_ARG
