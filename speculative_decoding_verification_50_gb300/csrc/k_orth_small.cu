@@ -31,7 +31,7 @@ __device__ __forceinline__ void small_product(uint32_t tmem, uint32_t a, uint32_
 
 }  // namespace
 
-template <int DT>
+template <int DT, int C>
 __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __grid_constant__ SmallParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t done;
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   const uint32_t y_at = smem_u32(y), s_at = smem_u32(sq), sum_at = smem_u32(sums);
   volatile int* gone = &gone_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank()), z = blockIdx.x / p.C, C = p.C;
+  const int rank = static_cast<int>(cluster_rank()), z = blockIdx.x / C;
   const int t0 = rank * kSmallSide;
   if (threadIdx.x == 0) {
     mbar_init(&done, 1);
@@ -173,21 +173,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    const int share = kSmallSide / C;
-    for (int i = threadIdx.x; i < share * 32; i += kSmallThreads) {
-      const int r = rank * share + (i >> 5), w = i & 31;
-      const uint32_t from = sum_at + small_sum_at(r, w);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int q = 0; q < C; ++q) {
-        const float4 o = load_cluster(in_cta(from, q));
-        x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
-      }
+    // (16 / C words of this CTA's rows per thread, 16 loads in flight)
+    constexpr int kShare = kSmallSide / C, kItems = kShare * 32 / kSmallThreads;
+    float4 part[kItems][C];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int r = rank * kShare + 8 * i + warp;
+#pragma unroll
+      for (int q = 0; q < C; ++q) part[i][q] = load_cluster(in_cta(sum_at + small_sum_at(r, lane), q));
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      float4 x = part[i][0];
+#pragma unroll
+      for (int q = 1; q < C; ++q) x.x += part[i][q].x, x.y += part[i][q].y, x.z += part[i][q].z, x.w += part[i][q].w;
       x.x *= st.gram, x.y *= st.gram, x.z *= st.gram, x.w *= st.gram;
       const uint32_t h0 = pack_f16(x.x, x.y), h1 = pack_f16(x.z, x.w);
       const float2 g0 = unpack_f16(h0), g1 = unpack_f16(h1);
       const uint32_t l0 = pack_f16(x.x - g0.x, x.y - g0.y), l1 = pack_f16(x.z - g1.x, x.w - g1.y);
-      const uint32_t to = s_at + small_at(r, 4 * w);
+      const uint32_t to = s_at + small_at(rank * kShare + 8 * i + warp, 4 * lane);
+#pragma unroll
       for (int q = 0; q < C; ++q) {
         store_cluster(in_cta(to, q), h0, h1);
         store_cluster(in_cta(to + kPlane, q), l0, l1);
@@ -272,11 +277,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
 }
 
-template <int DT>
+template <int DT, int C>
 static cudaError_t launch_small(const SmallParams& p, int B, cudaStream_t s) {
   constexpr int kDevices = 64;
   static std::atomic<bool> allowed[kDevices];
-  auto kern = orth_small_kernel<DT>;
+  auto kern = orth_small_kernel<DT, C>;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -287,7 +292,7 @@ static cudaError_t launch_small(const SmallParams& p, int B, cudaStream_t s) {
     if (dev < kDevices) allowed[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(B * p.C), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(B * C), 1, 1);
   cfg.blockDim = dim3(kSmallThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmallSmem;
   cfg.stream = s;
@@ -295,7 +300,7 @@ static cudaError_t launch_small(const SmallParams& p, int B, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(p.C);
+  attr[1].val.clusterDim.x = C;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -303,8 +308,19 @@ static cudaError_t launch_small(const SmallParams& p, int B, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-cudaError_t launch_orth_small(int dtype, const SmallParams& p, int B, cudaStream_t s) {
-  return dtype == SPECV_BF16 ? launch_small<0>(p, B, s) : launch_small<1>(p, B, s);
+template <int DT>
+static cudaError_t launch_small_of(const SmallParams& p, int C, int B, cudaStream_t s) {
+  switch (C) {
+    case 1: return launch_small<DT, 1>(p, B, s);
+    case 2: return launch_small<DT, 2>(p, B, s);
+    case 4: return launch_small<DT, 4>(p, B, s);
+    case 8: return launch_small<DT, 8>(p, B, s);
+    default: return launch_small<DT, 16>(p, B, s);
+  }
+}
+
+cudaError_t launch_orth_small(int dtype, const SmallParams& p, int C, int B, cudaStream_t s) {
+  return dtype == SPECV_BF16 ? launch_small_of<0>(p, C, B, s) : launch_small_of<1>(p, C, B, s);
 }
 
 }  // namespace specv

@@ -215,8 +215,7 @@ struct OrthRun {
 
   specv_status small() {
     SmallParams p = {};
-    p.m = a->m, p.n = a->n, p.s = w.s, p.t = w.t, p.tall = w.tall, p.steps = a->steps;
-    p.C = small_ctas(w.s, w.t);
+    p.s = w.s, p.t = w.t, p.tall = w.tall, p.steps = a->steps;
     p.in = a->update, p.row_stride = a->m > 1 ? a->row_stride : a->n, p.batch_stride = a->B > 1 ? a->batch_stride : 0;
     p.out = static_cast<uint16_t*>(a->out);
     p.out_row_stride = a->m > 1 ? a->out_row_stride : a->n, p.out_batch_stride = a->B > 1 ? a->out_batch_stride : 0;
@@ -230,7 +229,7 @@ struct OrthRun {
       p.step[k] = factors(r, sx, sn);
       r = next, sx = sn;
     }
-    return done(launch_orth_small(a->dtype, p, a->B, s), "orthogonalize");
+    return done(launch_orth_small(a->dtype, p, small_ctas(w.s, w.t), a->B, s), "orthogonalize");
   }
 
   specv_status all() {

@@ -6,8 +6,8 @@
 
 namespace specv {
 
-// B clusters of p.C CTAs
-cudaError_t launch_orth_small(int dtype, const SmallParams& p, int B, cudaStream_t s);
+// B clusters of C CTAs
+cudaError_t launch_orth_small(int dtype, const SmallParams& p, int C, int B, cudaStream_t s);
 cudaError_t launch_orth_squares(int dtype, const OrthInParams& p, cudaStream_t s);
 cudaError_t launch_orth_scale(int dtype, const OrthInParams& p, cudaStream_t s);
 // mn: the operands as they lie are [K][rows]; half: tiles of 128 x 128
