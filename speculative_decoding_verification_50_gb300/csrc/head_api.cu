@@ -274,7 +274,7 @@ struct HeadRun {
         SumEpi::Params e = {};
         TRY(product_map(&e.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, at<float>(w.sum), w.Ds, w.rows, w.splits, 4 * w.Ds,
                         4 * w.rows * w.Ds, 32));
-        e.cols = a->D, e.add = piece > 0;
+        e.cols = a->D, e.add = piece > 0, e.splits = p.splits;
         TRY(done(launch_head_hidden(p, e, s), "head-dh"));
       }
     }

@@ -117,23 +117,58 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInPa
   });
 }
 
-namespace {
-
-template <typename Kern>
-cudaError_t launch_in(Kern k, const OrthInParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(p.batch), 1);
-  cfg.blockDim = dim3(kOrthThreads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, p);
+__global__ void __launch_bounds__(256) orth_join_kernel(const OrthJoinParams p) {
+  __shared__ uint16_t turned[2][64][72];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  int u = blockIdx.x, pi = 0;
+  for (; u >= p.patches - pi; ++pi) u -= p.patches - pi;
+  const int pj = pi + u, z = blockIdx.y;
+  const int64_t matrix = p.n * p.ld;
+  const float* sum = p.sum + z * p.splits * matrix;
+  const int c = (threadIdx.x & 15) * 4, j = pj * 64 + c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = k * 16 + (threadIdx.x >> 4), i = pi * 64 + r;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < p.n && j < p.n) {  // (ld is a multiple of 8: words at the end of a row are whole)
+#pragma unroll 4
+      for (int q = 0; q < p.splits; ++q) {
+        const float4 o = __ldcs(reinterpret_cast<const float4*>(sum + q * matrix + i * p.ld + j));
+        x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
+      }
+    }
+    x.x *= p.alpha, x.y *= p.alpha, x.z *= p.alpha, x.w *= p.alpha;
+    const uint32_t h[2] = {pack_f16(x.x, x.y), pack_f16(x.z, x.w)};
+    const float2 g0 = unpack_f16(h[0]), g1 = unpack_f16(h[1]);
+    const uint32_t l[2] = {pack_f16(x.x - g0.x, x.y - g0.y), pack_f16(x.z - g1.x, x.w - g1.y)};
+    if (i < p.n && j < p.n) {
+      const int64_t at = z * matrix + i * p.ld + j;
+      *reinterpret_cast<uint2*>(p.hi + at) = make_uint2(h[0], h[1]);
+      if (p.lo) *reinterpret_cast<uint2*>(p.lo + at) = make_uint2(l[0], l[1]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      turned[0][c + t][r] = static_cast<uint16_t>(h[t >> 1] >> (16 * (t & 1)));
+      turned[1][c + t][r] = static_cast<uint16_t>(l[t >> 1] >> (16 * (t & 1)));
+    }
+  }
+  if (pi == pj) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = k * 16 + (threadIdx.x >> 4), i = pj * 64 + r, jj = pi * 64 + c;
+    if (i >= p.n) continue;
+    const int64_t at = z * matrix + i * p.ld + jj;
+    *reinterpret_cast<uint2*>(p.hi + at) = *reinterpret_cast<const uint2*>(&turned[0][r][c]);
+    if (p.lo) *reinterpret_cast<uint2*>(p.lo + at) = *reinterpret_cast<const uint2*>(&turned[1][r][c]);
+  }
 }
 
-}  // namespace
+template <typename Kern>
+static cudaError_t launch_in(Kern k, const OrthInParams& p, cudaStream_t s) {
+  return launch_grid(k, dim3(p.blocks, p.batch, 1), kOrthThreads, s, p);
+}
 
 cudaError_t launch_orth_squares(int dtype, const OrthInParams& p, cudaStream_t s) {
   return dtype == SPECV_BF16 ? launch_in(orth_squares_kernel<0>, p, s) : launch_in(orth_squares_kernel<1>, p, s);
@@ -150,6 +185,12 @@ template <bool FINE>
 cudaError_t launch_orth_gram(bool half, bool mn, ProductParams& p, const typename SymEpi<false, FINE>::Params& e, cudaStream_t s) {
   return mn ? launch_tiles<true, true, SymEpi<false, FINE>>(half, p, e, s)
             : launch_tiles<false, false, SymEpi<false, FINE>>(half, p, e, s);
+}
+cudaError_t launch_orth_sums(bool half, bool mn, ProductParams& p, const SumEpi::Params& e, cudaStream_t s) {
+  return mn ? launch_tiles<true, true, SumEpi>(half, p, e, s) : launch_tiles<false, false, SumEpi>(half, p, e, s);
+}
+cudaError_t launch_orth_join(const OrthJoinParams& p, int B, cudaStream_t s) {
+  return launch_grid(orth_join_kernel, dim3(p.patches * (p.patches + 1) / 2, B, 1), 256, s, p);
 }
 template <bool FINE>
 cudaError_t launch_orth_poly(bool half, ProductParams& p, const typename SymEpi<true, FINE>::Params& e, cudaStream_t s) {

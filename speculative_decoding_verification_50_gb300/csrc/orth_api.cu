@@ -39,13 +39,6 @@ double poly_bound(double b, double c, double r) {
 // half of its range: the bounds hold for exact steps).
 double keep_scale(double most) { return std::exp2(std::floor(std::log2(32768.0 / std::max(most, 1e-30)))); }
 
-struct OrthSpace {
-  size_t part, hi[2], lo[2], gram[2], poly[2], bytes;  // (of S and P: fp16, and what that leaves out)
-  int64_t ld, lds;  // strides of X, of S and P
-  int32_t s, t, blocks;
-  bool tall, fine;
-};
-
 // CTAs of a cluster that holds a matrix of a smaller side up to 128 in its shared memory
 // (powers of two up to 16, so that they share its rows evenly), or 0: it does not fit.
 int small_ctas(int32_t s, int32_t t) {
@@ -55,20 +48,45 @@ int small_ctas(int32_t s, int32_t t) {
   return C;
 }
 
-// Whether a product goes by tiles of 128 x 128, a CTA each, in the place of 256 x 256, a pair
-// each: where that ends sooner.  Cycles of a block of K: 256 and 512 are the tensor core's,
-// the more SMs take part the more are L2's (up to 540 and 620); and of what is not hidden
-// under the next tile, about 4000 and 6000.  us of a call by 128, by 256 and by this rule:
-// 128 x 512 134, 160, 134; 1000 x 2333 205, 240, 205; 1024 x 4096 257, 261, 242;
-// 24 x 1024 x 1024 830, 687, 687; 4096 x 4096 1611, 1040, 1040.
-bool small_tiles(const ProductParams& p) {
-  const double blocks = static_cast<double>((p.K + kProdBK - 1) / kProdBK * (p.fine ? 3 : 1));
-  auto cycles = [&](int tile, int64_t ctas, double least, double shared, double rest) {
-    const int64_t units = product_units(p, tile), rounds = (units + ctas - 1) / ctas;
-    return rounds * blocks * (least + shared * std::min(1.0, static_cast<double>(units) / ctas)) + rest;
-  };
-  return cycles(kProdHalf, api_sm_count(), 280, 260, 4000) < cycles(kProdTile, api_sm_count() / 2, 540, 80, 6000);
+// How a product is cut: into tiles of 128 x 128, a CTA each (half), or of 256 x 256, a pair
+// each, and K into parts whose sums a pass of its own joins; whatever ends soonest.  Cycles of
+// a block of K: 256 and 512 are the tensor core's, the more SMs take part the more are L2's
+// (up to 540 and 620); and of what is not hidden under the next tile, about 4000 and 6000.
+// The join: a launch, and the sums' bytes.  us of a call by 128, by 256 and by the better of
+// the two: 1000 x 2333 205, 240, 205; 1024 x 4096 257, 261, 242; 24 x 1024 x 1024 830, 687,
+// 687; 4096 x 4096 1611, 1040, 1040.  With and without parts of K: 100 x 9000 239, 831;
+// 250 x 16384 297, 1347; 8192 x 500 225, 425; 8192 x 2048 600, 632.
+struct Cut {
+  bool half;
+  int32_t splits;
+};
+
+Cut product_cut(ProductParams p, bool parts) {
+  const int64_t blocks = (p.K + kProdBK - 1) / kProdBK * (p.fine ? 3 : 1);
+  Cut best = {};
+  double least = 1e30;
+  for (bool half : {false, true}) {
+    const int64_t ctas = half ? api_sm_count() : api_sm_count() / 2;
+    p.splits = 1;
+    const int64_t tiles = product_units(p, half ? kProdHalf : kProdTile);
+    for (int64_t splits = 1; splits == 1 || (parts && splits <= 64 && splits * tiles <= 2 * ctas && splits * 8 <= blocks); ++splits) {
+      const int64_t units = tiles * splits, rounds = (units + ctas - 1) / ctas, part = (blocks + splits - 1) / splits;
+      const double busy = std::min(1.0, static_cast<double>(units) / ctas);
+      double cycles = half ? rounds * part * (280 + 260 * busy) + 4000 : rounds * part * (540 + 80 * busy) + 6000;
+      if (splits > 1) cycles += 9000 + 4.0 * p.batch * p.M * p.N * (splits + 1) / 4000;
+      if (cycles < least) least = cycles, best = {half, static_cast<int32_t>(splits)};
+    }
+  }
+  return best;
 }
+
+struct OrthSpace {
+  size_t part, hi[2], lo[2], gram[2], poly[2], sums, bytes;  // (of S and P: fp16, and what that leaves out)
+  int64_t ld, lds;  // strides of X, of S and P
+  int32_t s, t, blocks;
+  bool tall, fine;
+  Cut gram_cut;
+};
 
 OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
   OrthSpace w = {};
@@ -93,6 +111,10 @@ OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
   // (what X's fp16 leaves out is read and written by the same epilogue alone, unless products read it)
   w.lo[1] = w.fine ? take(x) : w.lo[0];
   for (int k = 0; k <= w.fine; ++k) w.gram[k] = take(q), w.poly[k] = take(q);
+  ProductParams p = {};
+  p.M = p.N = w.s, p.K = w.t, p.batch = B, p.symmetric = 1, p.fine = w.fine;
+  w.gram_cut = product_cut(p, true);
+  if (w.gram_cut.splits > 1) w.sums = take(2 * q * w.gram_cut.splits);
   w.bytes = at;
   return w;
 }
@@ -153,7 +175,7 @@ struct OrthRun {
     ProductParams p = {};
     p.M = M, p.N = N, p.K = K, p.batch = a->B, p.splits = 1;
     p.symmetric = symmetric, p.fine = w.fine;
-    half = small_tiles(p);
+    half = product_cut(p, false).half;
     p.idesc = prod_idesc(false, a_mn, b_mn, half ? kProdHalf : kProdTile);
     p.status = a->row_status, p.status_n = a->B;
     return p;
@@ -176,14 +198,28 @@ struct OrthRun {
     bool half;
     {
       ProductParams p = product(w.s, w.s, w.t, w.tall, w.tall, true, half);
+      half = w.gram_cut.half;
+      p.splits = w.gram_cut.splits;
+      p.idesc = prod_idesc(false, w.tall, w.tall, half ? kProdHalf : kProdTile);
       TRY(x_map(&p.a, w.tall, w.hi[from]));
       if (FINE) TRY(x_map(&p.a_low, w.tall, w.lo[from]));
       p.b = p.a, p.b_low = p.a_low;
-      typename SymEpi<false, FINE>::Params e = {};
-      TRY(sym_out(e, w.gram, FINE));
-      e.alpha = f.gram;
       if (launches == 2) p.stall = api_test_stall('F');
-      TRY(done(launch_orth_gram<FINE>(half, w.tall, p, e, s), "orthogonalize-gram"));
+      if (p.splits > 1) {
+        SumEpi::Params e = {};
+        TRY(product_map(&e.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, at(w.sums), w.s, w.s, a->B * p.splits, 4 * w.lds, 4 * zs(), 32));
+        e.cols = w.s, e.splits = p.splits;
+        TRY(done(launch_orth_sums(half, w.tall, p, e, s), "orthogonalize-gram"));
+        OrthJoinParams j = {};
+        j.n = w.s, j.splits = p.splits, j.patches = (w.s + 63) / 64, j.sum = reinterpret_cast<const float*>(at(w.sums));
+        j.hi = at(w.gram[0]), j.lo = FINE ? at(w.gram[1]) : nullptr, j.ld = w.lds, j.alpha = f.gram;
+        TRY(done(launch_orth_join(j, a->B, s), "orthogonalize-join"));
+      } else {
+        typename SymEpi<false, FINE>::Params e = {};
+        TRY(sym_out(e, w.gram, FINE));
+        e.alpha = f.gram;
+        TRY(done(launch_orth_gram<FINE>(half, w.tall, p, e, s), "orthogonalize-gram"));
+      }
     }
     ProductParams p = product(w.s, w.s, w.s, false, false, true, half);
     TRY(s_map(&p.a, w.gram[0]));

@@ -190,6 +190,16 @@ struct SymEpi : PlainEpi {
   }
 };
 
+// S from parts of K that were summed apart (tiles on and above the diagonal): a patch of
+// 64 x 64 per CTA, and its transposed.  Bound by bytes.
+struct OrthJoinParams {
+  int32_t n, splits, patches;   // patches along a side
+  const float* sum;             // [batch][splits][n][ld]
+  uint16_t *hi, *lo;            // [batch][n][ld]; lo: optional
+  int64_t ld;
+  float alpha;
+};
+
 // X' = a X + A B^T, as fp16 and what that leaves out, or (LAST) in bf16.
 template <bool LAST>
 struct StepEpi : PlainEpi {

@@ -579,9 +579,10 @@ struct StoreEpi : PlainEpi {
 struct SumEpi : PlainEpi {
   static constexpr int kStaging = 4096;
   struct Params {
-    CUtensorMap out;  // [splits][rows][cols]
+    CUtensorMap out;  // [batch x splits][rows][cols]
     int32_t cols;
     int32_t add;
+    int32_t splits;
   };
   template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
@@ -600,9 +601,9 @@ struct SumEpi : PlainEpi {
       __syncwarp();
       if (q.lane == 0) {
         if (e.add)
-          tma_add(&e.out, q.col0 + c, q.row0, q.split, smem_u32(q.staging));
+          tma_add(&e.out, q.col0 + c, q.row0, q.z * e.splits + q.split, smem_u32(q.staging));
         else
-          tma_store(&e.out, q.col0 + c, q.row0, q.split, smem_u32(q.staging));
+          tma_store(&e.out, q.col0 + c, q.row0, q.z * e.splits + q.split, smem_u32(q.staging));
         tma_commit();
       }
     }

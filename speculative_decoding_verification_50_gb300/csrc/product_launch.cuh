@@ -26,9 +26,9 @@ inline specv_status operand_map(CUtensorMap* map, bool bf16, bool mn, const void
 // A launch that may be scheduled while the one before it on the stream drains (it waits
 // for it with griddepcontrol.wait).
 template <typename Kern, typename Params>
-cudaError_t launch_grid(Kern k, int blocks, int threads, cudaStream_t stream, const Params& p) {
+cudaError_t launch_grid(Kern k, dim3 blocks, int threads, cudaStream_t stream, const Params& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.gridDim = blocks;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

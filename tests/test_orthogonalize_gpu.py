@@ -42,7 +42,8 @@ def check(G, **how):
 
 SHAPES = [(1, 1), (1, 7), (2, 2), (3, 300), (64, 64), (65, 127), (128, 512), (255, 257), (256, 256), (300, 200), (512, 100),
           (700, 1111), (1030, 520), (2000, 64),
-          (128, 128), (128, 129), (127, 2048), (2048, 128), (128, 2049), (2500, 33), (1, 2048), (130, 1), (16, 1025)]
+          (128, 128), (128, 129), (127, 2048), (2048, 128), (128, 2049), (2500, 33), (1, 2048), (130, 1), (16, 1025),
+          (100, 9001), (250, 12000), (6000, 90), (600, 9000), (4001, 300)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -57,7 +58,7 @@ def test_spectra(shape, kind):
     check(matrix(shape, kind))
 
 
-@pytest.mark.parametrize("shape", [(3, 64, 64), (5, 100, 333), (4, 333, 100), (24, 130, 130), (2, 1, 9), (200, 40, 90), (30, 600, 128)])
+@pytest.mark.parametrize("shape", [(3, 64, 64), (5, 100, 333), (4, 333, 100), (24, 130, 130), (2, 1, 9), (200, 40, 90), (30, 600, 128), (2, 60, 5000), (3, 300, 4000)])
 def test_batches(shape):
     G = matrix(shape, dtype=torch.bfloat16)
     G *= torch.logspace(-6, 6, shape[0], device="cuda").to(G.dtype)[:, None, None]
