@@ -127,9 +127,12 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   const float c2 = p.scale * kLog2e;
   float m = kNegMax, s = 0.f;
   if (use && at >= 0) {
-    for (int j = k; j < p.parts; j += T) {
-      const float2 x = p.part[j * p.ld + at];
-      soft_join(m, s, x.x, x.y, c2);
+    for (int j = k; j < p.parts; j += 8 * T) {
+      float2 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = j + u * T < p.parts ? p.part[(j + u * T) * p.ld + at] : make_float2(kNegMax, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) soft_join(m, s, x[u].x, x[u].y, c2);
     }
   }
   got[threadIdx.x] = make_float2(m, s);

@@ -9,34 +9,44 @@ namespace {
 
 // Vector j of a row: VW elements, zeros past its end.
 template <int DT>
-__device__ __forceinline__ void row_vec(const void* row, int64_t j, int64_t cols, bool vec, float (&x)[Elem<DT>::VW]) {
+__device__ __forceinline__ typename Elem<DT>::Vec row_vec(const void* row, int64_t j, int64_t cols, bool vec) {
   constexpr int VW = Elem<DT>::VW;
-  if (vec && (j + 1) * VW <= cols) {
-    Elem<DT>::unpack(Elem<DT>::vec(row, j * VW), x);
-  } else {
+  if (vec && (j + 1) * VW <= cols) return Elem<DT>::vec(row, j * VW);
+  union {
+    typename Elem<DT>::Raw e[VW];
+    typename Elem<DT>::Vec v;
+  } x;
 #pragma unroll
-    for (int k = 0; k < VW; ++k) x[k] = j * VW + k < cols ? Elem<DT>::scalar(row, j * VW + k) : 0.f;
-  }
+  for (int k = 0; k < VW; ++k) x.e[k] = j * VW + k < cols ? Elem<DT>::raw(row, j * VW + k) : typename Elem<DT>::Raw(0);
+  return x.v;
 }
 
-// f(row, vector) over this CTA's share of a matrix's rows of nv vectors: a share of a long
-// row's vectors per CTA (rows without gaps are one), or rows in turn.
-template <typename F>
-__device__ __forceinline__ void each_vec(const OrthInParams& p, int64_t nv, F&& f) {
-  if (p.rows == 1) {
-#pragma unroll 4
-    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x; j < nv;
-         j += static_cast<int64_t>(gridDim.x) * kOrthThreads)
-      f(0, j);
-    return;
+// use(row, vector, load(row, vector)) over this CTA's share of a matrix's rows of nv vectors:
+// a share of a long row's vectors per CTA (rows without gaps are one), or rows in turn.  Four
+// loads are under way before the first is used.
+template <typename V, typename L, typename U>
+__device__ __forceinline__ void each_vec(const OrthInParams& p, int64_t nv, L&& load, U&& use) {
+  constexpr int kAhead = 4;
+  int64_t r = 0, rows = 1, row_step = 1, j0 = static_cast<int64_t>(blockIdx.x) * kOrthThreads + threadIdx.x,
+          step = static_cast<int64_t>(gridDim.x) * kOrthThreads;
+  if (p.rows > 1) {
+    // a row per `step` threads, the power of two that is at most its vectors
+    int lanes = 32;
+    while (lanes < kOrthThreads && 2 * lanes <= nv) lanes *= 2;
+    const int per = kOrthThreads / lanes;
+    r = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes, rows = p.rows;
+    row_step = static_cast<int64_t>(gridDim.x) * per, j0 = threadIdx.x % lanes, step = lanes;
   }
-  // a row per `lanes` threads, the power of two that is at most its vectors
-  int lanes = 32;
-  while (lanes < kOrthThreads && 2 * lanes <= nv) lanes *= 2;
-  const int per = kOrthThreads / lanes, first = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * per + first; r < p.rows; r += static_cast<int64_t>(gridDim.x) * per)
-#pragma unroll 4
-    for (int64_t j = lane; j < nv; j += lanes) f(r, j);
+  for (; r < rows; r += row_step)
+    for (int64_t j = j0; j < nv; j += kAhead * step) {
+      V x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j + u * step < nv) x[u] = load(r, j + u * step);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j + u * step < nv) use(r, j + u * step, x[u]);
+    }
 }
 
 template <int DT>
@@ -50,7 +60,7 @@ __device__ __forceinline__ const void* row_at(const OrthInParams& p, int z, int6
 // nor huge entries leave fp32's range).  Bound by bytes.
 template <int DT>
 __global__ void __launch_bounds__(kOrthThreads) orth_squares_kernel(const OrthInParams p) {
-  __shared__ ScaledSquares warps[kOrthThreads / 32];
+  __shared__ ScaledSquares warps[kOrthThreads / 32], sum;
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int VW = Elem<DT>::VW;
@@ -58,36 +68,30 @@ __global__ void __launch_bounds__(kOrthThreads) orth_squares_kernel(const OrthIn
   const int64_t nv = (p.cols + VW - 1) / VW;
   ScaledSquares a = {kSquaresLeast, 0.f};
   float inv = 1.f / kSquaresLeast;
-  each_vec(p, nv, [&](int64_t r, int64_t j) {
-    float x[VW];
-    row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec, x);
-    squares_add<VW>(a, inv, x);
-  });
-  squares_warp(a);
-  if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = a;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kOrthThreads / 32; ++k) squares_join(a, warps[k]);
-    p.part[z * p.blocks + blockIdx.x] = a;
-  }
+  using Vec = typename Elem<DT>::Vec;
+  each_vec<Vec>(
+      p, nv, [&](int64_t r, int64_t j) { return row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec); },
+      [&](int64_t, int64_t, const Vec& w) {
+        float x[VW];
+        Elem<DT>::unpack(w, x);
+        squares_add<VW>(a, inv, x);
+      });
+  squares_cta(a, warps, sum);
+  if (threadIdx.x == 0) p.part[z * p.blocks + blockIdx.x] = sum;
 }
 
 // X = G / |G| in fp16 and what that leaves out; zeros for a matrix that is zero, or not
 // finite (flagged).
 template <int DT>
 __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInParams p) {
-  __shared__ ScaledSquares sum;
+  __shared__ ScaledSquares warps[kOrthThreads / 32], sum;
   pdl_wait_primary();
   pdl_launch_dependents();
   constexpr int VW = Elem<DT>::VW;
   const int z = blockIdx.y;
-  if (threadIdx.x < 32) {
-    ScaledSquares a = {kSquaresLeast, 0.f};
-    for (int k = threadIdx.x; k < p.blocks; k += 32) squares_join(a, p.part[z * p.blocks + k]);
-    squares_warp(a);
-    if (threadIdx.x == 0) sum = a;
-  }
-  __syncthreads();
+  ScaledSquares a = {kSquaresLeast, 0.f};
+  for (int k = threadIdx.x; k < p.blocks; k += kOrthThreads) squares_join(a, p.part[z * p.blocks + k]);
+  squares_cta(a, warps, sum);
   const float root = sqrtf(sum.s);
   const bool bad = !(sum.s < pos_inf());
   const float inv = 1.f / sum.m, f = bad || sum.s == 0.f ? 0.f : p.scale / root;
@@ -95,9 +99,11 @@ __global__ void __launch_bounds__(kOrthThreads) orth_scale_kernel(const OrthInPa
     if (p.norm) p.norm[z] = bad ? __int_as_float(0x7fc00000) : sum.m * root;
     if (p.status) p.status[z] = bad ? kNonFinite : 0;
   }
-  each_vec(p, p.ld / VW, [&](int64_t r, int64_t j) {
+  using Vec = typename Elem<DT>::Vec;
+  auto load = [&](int64_t r, int64_t j) { return row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec); };
+  each_vec<Vec>(p, p.ld / VW, load, [&](int64_t r, int64_t j, const Vec& raw) {
     float x[VW];
-    row_vec<DT>(row_at<DT>(p, z, r), j, p.cols, p.vec, x);
+    Elem<DT>::unpack(raw, x);
     uint32_t hi[VW / 2], lo[VW / 2];
 #pragma unroll
     for (int k = 0; k < VW / 2; ++k) {

@@ -90,14 +90,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) squares_add<4>(a, inv_m, v[i]);
-  squares_warp(a);
-  if (lane == 0) warps[warp] = a;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kSmallThreads / 32; ++k) squares_join(a, warps[k]);
-    mine = a;
-  }
-  __syncthreads();
+  squares_cta(a, warps, mine);
   cluster_sync();
   ScaledSquares sum = {kSquaresLeast, 0.f};
   for (int q = 0; q < C; ++q) {

@@ -99,10 +99,10 @@ OrthSpace orth_space(int32_t B, int32_t m, int32_t n) {
   w.tall = m > n;
   w.s = std::min(m, n), w.t = std::max(m, n);
   w.ld = up_to(n, 8), w.lds = up_to(w.s, 8);
-  // blocks of the passes over G: 8 vectors a thread, four blocks an SM over the batch at most
+  // blocks of the passes over G: 8 vectors a thread, or four blocks an SM over the batch
   const int64_t vectors = static_cast<int64_t>(m) * ((n + 3) / 4);
   w.blocks = static_cast<int32_t>(std::max<int64_t>(
-      1, std::min((vectors + 8 * kOrthThreads - 1) / (8 * kOrthThreads), std::max<int64_t>(1, 8LL * api_sm_count() / B))));
+      1, std::min((vectors + 8 * kOrthThreads - 1) / (8 * kOrthThreads), std::max<int64_t>(1, 4LL * api_sm_count() / B))));
   if (small_ctas(w.s, w.t)) return w;  // (in one kernel, on chip)
   w.part = take(sizeof(ScaledSquares) * static_cast<size_t>(B) * w.blocks);
   const size_t x = 2 * static_cast<size_t>(B) * m * w.ld, q = 2 * static_cast<size_t>(B) * w.s * w.lds;

@@ -18,6 +18,20 @@ __device__ __forceinline__ void squares_warp(ScaledSquares& a) {
   for (int o = 16; o > 0; o >>= 1) squares_join(a, squares_shfl(a, o));
 }
 
+// The sum over a CTA of 256 threads, in a fixed order, for all of them.
+__device__ __forceinline__ void squares_cta(ScaledSquares& a, ScaledSquares (&warps)[8], ScaledSquares& sum) {
+  squares_warp(a);
+  if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = a;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    ScaledSquares w = warps[threadIdx.x % 8];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) squares_join(w, squares_shfl(w, o));
+    if (threadIdx.x == 0) sum = w;
+  }
+  __syncthreads();
+}
+
 constexpr float kSquaresLeast = 1.17549435e-38f;  // 2^-126
 
 template <int VW>
@@ -28,7 +42,7 @@ __device__ __forceinline__ void squares_add(ScaledSquares& a, float& inv, const 
   if (most >= 2.f * a.m) {
     // the power of two at or below it (infinity: its own, and the sum becomes NaN)
     const float m = __uint_as_float(__float_as_uint(most) & 0x7f800000u);
-    const float f = a.m / m;
+    const float f = a.m / m;  // (rarely: the first vector, and where entries double)
     a.s *= f * f;
     a.m = m;
     inv = 1.f / m;
