@@ -19,6 +19,11 @@ int64_t up_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // take the same tile whatever their number.
 bool gathers(int32_t N) { return N > kProdTile; }
 
+// Up to 128 rows go by tiles of 128 x 128, a CTA each: a pair's 256 rows cost the tensor core
+// twice the time for the same bytes of the head, more than those take from HBM (1 x 2048 x
+// 32000: kFewTimes).
+bool few_rows(int32_t N) { return N <= kProdHalf; }
+
 // A call that computes the loss and the gradients keeps the logits' weights in fp16 where
 // they take no more than 1 GB (4096 rows of 131072 tokens), and computes the logits once:
 // 6 N D V operations for 8.  Otherwise, and in a backward pass, the vocabulary is taken in
@@ -35,13 +40,14 @@ int64_t piece_tokens(int32_t N, int32_t V, bool keep) {
 }
 
 // Parts that K (a piece's tokens) is cut into for dh, whose tiles alone are few.  Tiles for
-// every pair of SMs: eight units for each pair, so that a last round that is not full costs
+// every pair of SMs (or SM): eight units for each, so that a last round that is not full costs
 // little (4096 x 4096 of 128256 tokens, 0.7 of the rows in use: 192 tiles on 76 pairs), in
-// parts of 64 blocks at least.  Fewer: one unit for each pair, of 8 blocks at least.
+// parts of 64 blocks at least.  Fewer: one unit for each, of 8 blocks at least.
 int hidden_splits(int32_t N, int32_t D, int64_t tokens) {
-  const int64_t tiles = up_to(N, kProdTile) / kProdTile * (up_to(D, kProdTile) / kProdTile);
-  const int64_t pairs = api_sm_count() / 2, blocks = up_to(tokens, kProdBK) / kProdBK;
-  const int64_t n = tiles >= pairs ? std::min((8 * pairs + tiles - 1) / tiles, blocks / 64) : std::min(pairs / tiles, blocks / 8);
+  const int size = few_rows(N) ? kProdHalf : kProdTile;
+  const int64_t tiles = up_to(N, size) / size * (up_to(D, size) / size);
+  const int64_t groups = few_rows(N) ? api_sm_count() : api_sm_count() / 2, blocks = up_to(tokens, kProdBK) / kProdBK;
+  const int64_t n = tiles >= groups ? std::min((8 * groups + tiles - 1) / tiles, blocks / 64) : std::min(groups / tiles, blocks / 8);
   return static_cast<int>(std::max<int64_t>(n, 1));
 }
 
@@ -50,7 +56,8 @@ struct HeadSpace {
   size_t count, err, place, source, target, row, bad, z_target, part, hidden, head, dz, sum, bytes;
   int64_t rows, ld, Dp, Ds, tokens;  // rows: N up to a block; ld: of part; Dp, Ds: strides of gathered rows and sums
   int splits;
-  bool gather, copy_hidden, copy_head, grads, keep;
+  int part_cols;  // tokens per partial sum
+  bool gather, copy_hidden, copy_head, grads, keep, half;
 };
 
 // keep: of a call that computes the loss too.
@@ -80,7 +87,9 @@ HeadSpace head_space(const specv_head_args* a, bool keep) {
   w.row = take(sizeof(HeadRow) * N);
   w.bad = take(4 * N);
   w.z_target = take(4 * N);
-  w.part = take(sizeof(float2) * static_cast<size_t>((V + kPart - 1) / kPart) * w.ld);
+  w.half = few_rows(a->N);
+  w.part_cols = w.half ? kProdHalf / 2 : kProdTile / 2;
+  w.part = take(sizeof(float2) * static_cast<size_t>((V + w.part_cols - 1) / w.part_cols) * w.ld);
   if (w.copy_hidden) w.hidden = take(2 * w.rows * w.Dp);
   if (w.copy_head) w.head = take(2 * static_cast<size_t>(V) * w.Dp);
   if (w.grads) {
@@ -182,12 +191,13 @@ struct HeadRun {
     return SPECV_OK;
   }
 
-  ProductParams product(int32_t M, int32_t N, int32_t K, bool a_mn, bool b_mn) const {
+  // rows_k: the rows in use are K, not M.
+  ProductParams product(int32_t M, int32_t N, int32_t K, bool rows_k) const {
     ProductParams p = {};
     p.M = M, p.N = N, p.K = K, p.batch = 1, p.splits = 1;
-    p.idesc = prod_idesc(true, a_mn, b_mn);
+    p.bf16 = 1;
     p.rows = w.gather ? at<int32_t>(w.count) : nullptr;
-    p.rows_k = a_mn;
+    p.rows_k = rows_k;
     return p;
   }
   specv_status head_map(CUtensorMap* m, bool mn, int64_t first, int64_t n) const {
@@ -195,7 +205,7 @@ struct HeadRun {
   }
 
   specv_status forward() {
-    ProductParams p = product(a->N, a->V, a->D, false, false);
+    ProductParams p = product(a->N, a->V, a->D, false);
     TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0));
     TRY(head_map(&p.b, false, 0, a->V));
     p.err = at<int32_t>(w.err);
@@ -205,21 +215,20 @@ struct HeadRun {
     e.part = at<float2>(w.part), e.ld = w.ld, e.z_target = at<float>(w.z_target);
     e.V = a->V, e.c2 = a->scale * kLog2e;
     if (w.keep) {
-      KeepEpi::Params k = {};
-      k.s = e;
-      TRY(product_map(&k.out.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at<uint16_t>(w.dz), a->V, w.rows, 1, 2 * w.tokens, 0, 32));
-      k.out.cols = a->V;
-      TRY(done(launch_head_keep(p, k, s), "head-stats"));
+      Out16 out = {};
+      TRY(product_map(&out.map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at<uint16_t>(w.dz), a->V, w.rows, 1, 2 * w.tokens, 0, 32));
+      out.cols = a->V;
+      TRY(done(launch_head_keep(p, e, out, s), "head-stats"));
     } else {
       TRY(done(launch_head_stats(p, e, s), "head-stats"));
     }
     HeadJoinParams j = {};
-    j.N = a->N, j.V = a->V, j.parts = (a->V + kPart - 1) / kPart;
+    j.N = a->N, j.V = a->V, j.parts = (a->V + w.part_cols - 1) / w.part_cols;
     j.part = e.part, j.z_target = e.z_target, j.ld = w.ld, j.scale = a->scale;
     j.place = w.gather ? at<int32_t>(w.place) : nullptr;
     j.target = a->targets, j.weight = a->weights;
     j.bad = w.grads ? at<int32_t>(w.bad) : nullptr;
-    j.err = p.err, j.errs = product_grid<true>(p);
+    j.err = p.err, j.errs = w.half ? product_grid<false>(p) : product_grid<true>(p);
     j.loss = a->loss, j.stats = a->stats, j.status = a->row_status;
     j.row = w.grads ? at<HeadRow>(w.row) : nullptr;
     return done(launch_head_join(j, s), "head-join");
@@ -236,11 +245,11 @@ struct HeadRun {
         HeadWeightParams p = {};
         p.N = a->N, p.V = a->V, p.count = w.gather ? at<int32_t>(w.count) : nullptr;
         p.part = at<float2>(w.part), p.ld = w.ld, p.row = at<HeadRow>(w.row), p.c2 = a->scale * kLog2e;
-        p.w = dz, p.stride = w.tokens;
+        p.w = dz, p.stride = w.tokens, p.part_cols = w.part_cols;
         const int64_t blocks = (w.rows * ((a->V + 255) / 256) + 7) / 8;
         TRY(done(launch_head_weight(p, static_cast<int>(std::min<int64_t>(blocks, 8 * api_sm_count())), s), "head-dz"));
       } else {  // dz of the piece
-        ProductParams p = product(a->N, n, a->D, false, false);
+        ProductParams p = product(a->N, n, a->D, false);
         TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0));
         TRY(head_map(&p.b, false, v, n));
         p.status = a->row_status, p.status_n = a->N;
@@ -251,7 +260,7 @@ struct HeadRun {
         TRY(done(launch_head_prob(p, e, s), "head-dz"));
       }
       if (a->grad_head) {  // dW of the piece
-        ProductParams p = product(n, a->D, a->N, true, true);
+        ProductParams p = product(n, a->D, a->N, true);
         TRY(operand_map(&p.a, true, true, dz, n, w.rows, 1, w.tokens, 0));
         TRY(operand_map(&p.b, true, true, hidden(), a->D, w.rows, 1, hidden_stride(), 0));
         p.status = a->row_status, p.status_n = a->N;
@@ -266,7 +275,7 @@ struct HeadRun {
         TRY(done(launch_head_head(p, e, s), "head-dW"));
       }
       if (a->grad_hidden) {  // the piece's part of dh
-        ProductParams p = product(a->N, a->D, n, false, true);
+        ProductParams p = product(a->N, a->D, n, false);
         p.splits = std::min<int>(w.splits, static_cast<int>(up_to(n, kProdBK) / kProdBK));
         TRY(operand_map(&p.a, true, false, dz, n, w.rows, 1, w.tokens, 0));
         TRY(head_map(&p.b, true, v, n));

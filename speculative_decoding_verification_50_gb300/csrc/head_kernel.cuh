@@ -21,8 +21,6 @@ namespace specv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPart = kProdHalf;  // columns per partial sum
-
 // What the backward pass knows of a row.
 struct HeadRow {
   float lse2;  // lse log2(e)
@@ -40,7 +38,7 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 
 struct HeadStatsParams {
   const int32_t* target;  // [rows], -1: none
-  float2* part;           // [ceil(V / 128)][ld]: largest accumulator, sum relative to it
+  float2* part;           // [ceil(V / PART)][ld]: largest accumulator, sum relative to it
   float* z_target;        // [rows]: the target's accumulator
   int64_t ld;
   int32_t V;
@@ -53,24 +51,24 @@ struct HeadStatsParams {
 // long sum grows with its length: sums over more than kStatsChunk blocks of K are taken in
 // chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum, 5e-7 in
 // chunks of 16 blocks).  Rows of one tile, bound by the head's bytes, take chunks of
-// kStatsChunkFew blocks at no cost.
+// kStatsChunkFew blocks at no cost.  PART: columns per partial sum, those of an epilogue warp.
 constexpr int kStatsChunk = 16, kStatsChunkFew = 8;
-template <bool LONG>
+template <bool LONG, int PART>
 struct StatsEpi : PlainEpi {
   static constexpr bool kChunks = LONG;
   struct State {
-    float v[LONG ? kPart : 1];
+    float v[LONG ? PART : 1];
   };
   static __device__ __forceinline__ void start(State& sum) {
     if constexpr (LONG) {
 #pragma unroll
-      for (int j = 0; j < kPart; ++j) sum.v[j] = 0.f;
+      for (int j = 0; j < PART; ++j) sum.v[j] = 0.f;
     }
   }
   static __device__ __forceinline__ void add(EpiTile& q, State& sum) {
     if constexpr (LONG) {
 #pragma unroll
-      for (int c = 0; c < kPart; c += 32) {
+      for (int c = 0; c < PART; c += 32) {
         float v[32];
         tmem_load32(q.tmem + c, v);
 #pragma unroll
@@ -121,8 +119,8 @@ struct StatsEpi : PlainEpi {
     const int target = i < q.rows ? e.target[i] : -1;
     float m = kNegMax, s[4] = {0.f, 0.f, 0.f, 0.f};
     bool bad = false;
-#pragma unroll(LONG ? kPart / 32 : 1)
-    for (int c = 0; c < kPart; c += 32) {
+#pragma unroll(LONG ? PART / 32 : 1)
+    for (int c = 0; c < PART; c += 32) {
       float v[32];
       if constexpr (LONG) {
 #pragma unroll
@@ -133,38 +131,39 @@ struct StatsEpi : PlainEpi {
       part32(e, v, i, target - (q.col0 + c), e.V - (q.col0 + c), m, s, bad);
     }
     const float total = (s[0] + s[1]) + (s[2] + s[3]);
-    if (i < q.rows) e.part[static_cast<int64_t>(q.col0 / kPart) * e.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
+    if (i < q.rows) e.part[static_cast<int64_t>(q.col0 / PART) * e.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
   }
 };
 
 // The forward pass where the gradients follow in the same call and the weights exp(z - m),
-// m a row's largest logit of 128 columns, are kept for them: times 2^15 in fp16 (off by 2^-11 of
+// m a row's largest logit of 128 (64) columns, are kept for them: times 2^15 in fp16 (off by 2^-11 of
 // a weight at most, and by 2^-40 of the largest of 128), so that the logits need no second
 // product.
 constexpr float kKeepScale = 15.f;  // (its logarithm)
-struct KeepEpi : StatsEpi<true> {
+template <int PART>
+struct KeepEpi : StatsEpi<true, PART> {
   static constexpr int kStaging = 4096;
   struct Params {
     HeadStatsParams s;
     Out16 out;
   };
   template <int COLS>
-  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State& sum) {
+  static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, typename StatsEpi<true, PART>::State& sum) {
     if (q.row0 >= q.rows || q.col0 >= e.s.V) return;
     const int i = q.row0 + q.lane, at = (i < q.rows ? e.s.target[i] : -1) - q.col0, left = e.s.V - q.col0;
     float hi = sum.v[0], lo = sum.v[0];
 #pragma unroll
-    for (int j = 1; j < kPart - 1; j += 2) {
+    for (int j = 1; j < PART - 1; j += 2) {
       hi = max3_nan(hi, sum.v[j], sum.v[j + 1]);
       lo = min3(lo, sum.v[j], sum.v[j + 1]);
     }
-    hi = max3_nan(hi, sum.v[kPart - 1], sum.v[kPart - 1]);
-    lo = fminf(lo, sum.v[kPart - 1]);
+    hi = max3_nan(hi, sum.v[PART - 1], sum.v[PART - 1]);
+    lo = fminf(lo, sum.v[PART - 1]);
     const bool bad = !(hi < pos_inf()) || !(lo > neg_inf());
-    if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < static_cast<unsigned>(kPart)) || left < kPart) {
+    if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < static_cast<unsigned>(PART)) || left < PART) {
       hi = neg_inf();
 #pragma unroll
-      for (int j = 0; j < kPart; ++j) {
+      for (int j = 0; j < PART; ++j) {
         if (j == at) e.s.z_target[i] = sum.v[j];
         if (j == at || j >= left) sum.v[j] = neg_inf();
         hi = fmaxf(hi, sum.v[j]);
@@ -173,15 +172,15 @@ struct KeepEpi : StatsEpi<true> {
     const float m = fmaxf(hi, kNegMax), mc = kKeepScale - m * e.s.c2;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < kPart; ++j) {
+    for (int j = 0; j < PART; ++j) {
       sum.v[j] = ex2(fmaf(sum.v[j], e.s.c2, mc));
       s[j & 3] += sum.v[j];
     }
     const float total = hi > neg_inf() ? ((s[0] + s[1]) + (s[2] + s[3])) * (1.f / 32768.f) : 0.f;
     if (i < q.rows)
-      e.s.part[static_cast<int64_t>(q.col0 / kPart) * e.s.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
+      e.s.part[static_cast<int64_t>(q.col0 / PART) * e.s.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
 #pragma unroll
-    for (int c = 0; c < kPart; c += 64) {
+    for (int c = 0; c < PART; c += 64) {
       uint32_t w[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) w[j] = pack_f16(sum.v[c + 2 * j], sum.v[c + 2 * j + 1]);
@@ -300,6 +299,7 @@ struct HeadWeightParams {
   int64_t ld;
   const HeadRow* row;
   float c2;
+  int32_t part_cols;       // columns per part
   uint16_t* w;             // [rows up to a block][stride]: weights in, dz out
   int64_t stride;
 };

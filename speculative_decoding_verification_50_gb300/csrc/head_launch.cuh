@@ -7,7 +7,7 @@ namespace specv {
 
 // in chunks of kStatsChunk blocks where D is longer
 cudaError_t launch_head_stats(ProductParams& p, const HeadStatsParams& e, cudaStream_t s);
-cudaError_t launch_head_keep(ProductParams& p, const KeepEpi::Params& e, cudaStream_t s);
+cudaError_t launch_head_keep(ProductParams& p, const HeadStatsParams& e, const Out16& out, cudaStream_t s);
 cudaError_t launch_head_weight(const HeadWeightParams& p, int blocks, cudaStream_t s);
 cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s);
 cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s);

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256) head_weight_kernel(const HeadWeightParams
     const HeadRow r = i < n ? p.row[i] : HeadRow{0.f, 0.f, 0.f, -1};
     if (r.g != 0.f) {
       v = __ldcs(at);
-      const float f = r.g * ex2(fmaf(p.part[(col / kPart) * p.ld + i].x, p.c2, -r.lse2) - kKeepScale);
+      const float f = r.g * ex2(fmaf(p.part[(col / p.part_cols) * p.ld + i].x, p.c2, -r.lse2) - kKeepScale);
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -235,25 +235,32 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
   }
 }
 
+// Up to 128 rows: tiles of 128 x 128.
+static bool few(const ProductParams& p) { return p.M <= kProdHalf; }
 static int stats_chunk(const ProductParams& p) { return p.M <= kProdTile ? kStatsChunkFew : kStatsChunk; }
 
+template <bool LONG>
+static cudaError_t launch_stats_of(ProductParams& p, const HeadStatsParams& e, cudaStream_t s) {
+  return few(p) ? launch_product<false, false, false, StatsEpi<LONG, kProdHalf / 2>>(p, e, s)
+                : launch_product<true, false, false, StatsEpi<LONG, kProdTile / 2>>(p, e, s);
+}
 cudaError_t launch_head_stats(ProductParams& p, const HeadStatsParams& e, cudaStream_t s) {
   p.chunk = stats_chunk(p);
-  if (p.K <= p.chunk * kProdBK) return launch_product<true, false, false, StatsEpi<false>>(p, e, s);
-  return launch_product<true, false, false, StatsEpi<true>>(p, e, s);
+  return p.K <= p.chunk * kProdBK ? launch_stats_of<false>(p, e, s) : launch_stats_of<true>(p, e, s);
 }
-cudaError_t launch_head_keep(ProductParams& p, const KeepEpi::Params& e, cudaStream_t s) {
+cudaError_t launch_head_keep(ProductParams& p, const HeadStatsParams& e, const Out16& out, cudaStream_t s) {
   p.chunk = stats_chunk(p);
-  return launch_product<true, false, false, KeepEpi>(p, e, s);
+  return few(p) ? launch_product<false, false, false, KeepEpi<kProdHalf / 2>>(p, {e, out}, s)
+                : launch_product<true, false, false, KeepEpi<kProdTile / 2>>(p, {e, out}, s);
 }
 cudaError_t launch_head_weight(const HeadWeightParams& p, int blocks, cudaStream_t s) {
   return launch_grid(head_weight_kernel, blocks, 256, s, p);
 }
 cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s) {
-  return launch_product<true, false, false, ProbEpi>(p, e, s);
+  return few(p) ? launch_product<false, false, false, ProbEpi>(p, e, s) : launch_product<true, false, false, ProbEpi>(p, e, s);
 }
 cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s) {
-  return launch_product<true, false, true, SumEpi>(p, e, s);
+  return few(p) ? launch_product<false, false, true, SumEpi>(p, e, s) : launch_product<true, false, true, SumEpi>(p, e, s);
 }
 cudaError_t launch_head_head(ProductParams& p, const Out16& out, cudaStream_t s) {
   if (p.K <= 16 * kProdBK) return launch_product<true, true, true, StoreEpi<true>>(p, {out, 1.f}, s);

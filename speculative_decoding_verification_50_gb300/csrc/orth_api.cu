@@ -171,12 +171,11 @@ struct OrthRun {
     return SPECV_OK;
   }
   // half: tiles of 128 x 128 by one CTA each.
-  ProductParams product(int32_t M, int32_t N, int32_t K, bool a_mn, bool b_mn, bool symmetric, bool& half) const {
+  ProductParams product(int32_t M, int32_t N, int32_t K, bool symmetric, bool& half) const {
     ProductParams p = {};
     p.M = M, p.N = N, p.K = K, p.batch = a->B, p.splits = 1;
     p.symmetric = symmetric, p.fine = w.fine;
     half = product_cut(p, false).half;
-    p.idesc = prod_idesc(false, a_mn, b_mn, half ? kProdHalf : kProdTile);
     p.status = a->row_status, p.status_n = a->B;
     return p;
   }
@@ -197,10 +196,9 @@ struct OrthRun {
   specv_status symmetric(int from, const SmallStep& f) {
     bool half;
     {
-      ProductParams p = product(w.s, w.s, w.t, w.tall, w.tall, true, half);
+      ProductParams p = product(w.s, w.s, w.t, true, half);
       half = w.gram_cut.half;
       p.splits = w.gram_cut.splits;
-      p.idesc = prod_idesc(false, w.tall, w.tall, half ? kProdHalf : kProdTile);
       TRY(x_map(&p.a, w.tall, w.hi[from]));
       if (FINE) TRY(x_map(&p.a_low, w.tall, w.lo[from]));
       p.b = p.a, p.b_low = p.a_low;
@@ -221,7 +219,7 @@ struct OrthRun {
         TRY(done(launch_orth_gram<FINE>(half, w.tall, p, e, s), "orthogonalize-gram"));
       }
     }
-    ProductParams p = product(w.s, w.s, w.s, false, false, true, half);
+    ProductParams p = product(w.s, w.s, w.s, true, half);
     TRY(s_map(&p.a, w.gram[0]));
     if (FINE) TRY(s_map(&p.a_low, w.gram[1]));
     p.b = p.a, p.b_low = p.a_low;
@@ -292,7 +290,7 @@ struct OrthRun {
       TRY(w.fine ? symmetric<true>(from, f) : symmetric<false>(from, f));
       // X' = a X + P X, or a X + X P (P is its own transpose)
       bool half;
-      ProductParams p = product(a->m, a->n, w.s, false, !w.tall, false, half);
+      ProductParams p = product(a->m, a->n, w.s, false, half);
       TRY(s_map(w.tall ? &p.b : &p.a, w.poly[0]));
       TRY(x_map(w.tall ? &p.a : &p.b, !w.tall, w.hi[from]));
       if (w.fine) {

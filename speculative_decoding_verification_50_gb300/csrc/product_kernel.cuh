@@ -56,7 +56,8 @@ struct ProductParams {
   int32_t batch, splits;   // splits: parts of K that are summed apart
   int32_t chunk;           // blocks of K per accumulator (0: all): the epilogue adds up several
   int32_t symmetric;       // M == N, C symmetric: only tiles on and above the diagonal
-  uint32_t idesc;
+  int32_t bf16;            // operands: bf16, or fp16
+  uint32_t idesc;          // (set by the launch)
   int32_t late_wait;       // the previous launch is waited for at the end alone
   int32_t* err;            // [clusters]: 0, or 1 where a wait ran out
   int32_t* status;         // optional [status_n]: a wait that ran out is added (kTimeout)

@@ -81,6 +81,7 @@ cudaError_t launch_product(ProductParams& p, const typename Epi::Params& e, cuda
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   p.tn = (p.N + (PAIR ? kProdTile : kProdHalf) - 1) / (PAIR ? kProdTile : kProdHalf);
+  p.idesc = prod_idesc(p.bf16, A_MN, B_MN, PAIR ? kProdTile : kProdHalf);
   return cudaLaunchKernelEx(&cfg, kern, p, e);
 }
 
