@@ -39,7 +39,9 @@
  *     (per-chunk statistics and candidates into the workspace), then one
  *     decision per batch row (launched as a programmatic dependent of the
  *     first).  specv_sample, specv_top_logits, specv_distill and
- *     specv_distill_backward are one kernel each, without a workspace.
+ *     specv_distill_backward are one kernel each, without a workspace;
+ *     specv_head_loss, its backward pass and specv_orthogonalize a few kernels,
+ *     each a programmatic dependent of the one before.
  *     The workspace needs no initialisation: everything a call
  *     reads from it is written earlier in the same call.  A call only
  *     enqueues kernels on the given stream, so it can be captured in a CUDA

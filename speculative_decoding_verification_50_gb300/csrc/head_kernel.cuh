@@ -21,6 +21,7 @@ namespace specv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
 // What the backward pass knows of a row.
 struct HeadRow {
   float lse2;  // lse log2(e)
