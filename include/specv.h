@@ -475,7 +475,9 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * and the log-probabilities of given tokens.
  *   loss[n] = weights[n] * nll[n],  nll[n] = log sum_v exp(z_nv) - z_n,targets[n]
  *   stats[n] = (log sum_v exp(z_nv), nll[n])
- * A row whose target is -1 or whose weight is 0 is left out: loss 0, stats 0, no gradient.
+ * A row whose weight is 0 is left out: loss 0, stats 0, no gradient.  So is one whose target
+ * is -1, in calls with gradients and under SPECV_HEAD_TARGETS_ONLY; in others it has its
+ * log-sum-exp (whatever its logits, without a status), and loss and nll 0.
  * specv_head_loss writes loss, and if given the gradients of sum_n loss[n] by hidden and
  * by head (either or both); specv_head_loss_backward the gradients of sum_n grad_loss[n]
  * * loss[n] (grad_loss NULL: ones) from the stats of a call on the same inputs.
@@ -494,6 +496,8 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * 16-byte boundaries are read and written in place; others are copied into the workspace.
  * fp32 is refused with SPECV_ERR_UNSUPPORTED.  The gradients overlap nothing.
  */
+#define SPECV_HEAD_TARGETS_ONLY 1
+
 typedef struct {
   int32_t N, V, D;             /* rows; vocabulary; width of a hidden state */
   int32_t dtype;               /* SPECV_BF16, of hidden, head and their gradients */
@@ -504,6 +508,7 @@ typedef struct {
   const int32_t* targets;      /* [N], -1: none */
   const float* weights;        /* optional [N] */
   float scale;                 /* in [1e-6, 1e6] */
+  int32_t flags;               /* SPECV_HEAD_TARGETS_ONLY or 0 */
   float* loss;                 /* OUT [N] (specv_head_loss) */
   float* stats;                /* [N, 2]: OUT, optional (specv_head_loss), or in (backward) */
   int32_t* row_status;         /* OUT, optional [N] */

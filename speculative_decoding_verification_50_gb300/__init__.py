@@ -39,6 +39,7 @@ ROW_BAD_COUNT = 32
 ROW_BAD_FILTER = 64
 SPECV_MAX_TOP = 1024
 SPECV_DISTILL_TAIL = 1
+SPECV_HEAD_TARGETS_ONLY = 1
 SPECV_NO_DRAFT_PROBS = 1
 SPECV_MSS_NAIVE = 1
 
@@ -109,7 +110,7 @@ class DistillArgs(ctypes.Structure):
 class HeadArgs(ctypes.Structure):
     _fields_ = [("N", _I32), ("V", _I32), ("D", _I32), ("dtype", _I32),
                 ("hidden", _P), ("hidden_stride", _I64), ("head", _P), ("head_stride", _I64),
-                ("targets", _P), ("weights", _P), ("scale", ctypes.c_float),
+                ("targets", _P), ("weights", _P), ("scale", ctypes.c_float), ("flags", _I32),
                 ("loss", _P), ("stats", _P), ("row_status", _P), ("grad_loss", _P),
                 ("grad_hidden", _P), ("grad_hidden_stride", _I64),
                 ("grad_head", _P), ("grad_head_stride", _I64)]
@@ -810,20 +811,22 @@ def _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head):
             _cuda(grad, what, at)
     of = lambda t: (None, 0) if t is None else (t.data_ptr(), _stride(t, 0, D))  # noqa: E731
     return HeadArgs(N, V, D, code, *of(hidden), *of(head), _of(targets, (N,), torch.int32, "targets", at),
-                    _of(weights, (N,), torch.float32, "weights", at), float(scale), None, None, None, None,
+                    _of(weights, (N,), torch.float32, "weights", at), float(scale), 0, None, None, None, None,
                     *of(grad_hidden), *of(grad_head))
 
 
 def specv_head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None, with_grad: bool = False,
-                    loss=None, stats=None, row_status=None, grad_hidden=None, grad_head=None,
+                    targets_only: bool = False, loss=None, stats=None, row_status=None, grad_hidden=None, grad_head=None,
                     workspace=None, stream=None) -> dict:
     """Cross entropy of the tokens `targets` under softmax(scale * hidden @ head.T), without
     the logits in memory (see include/specv.h, specv_head_loss).
 
-    hidden [N, D] and head [V, D] (bf16, CUDA, last dim contiguous); targets int32 [N] (-1: a
-    row that is left out); weights fp32 [N] or None.  Returns loss fp32 [N], stats fp32 [N, 2]
-    (the row's log-sum-exp and minus the target's log-probability), row_status int32 [N], and
-    with with_grad, or where a buffer is given, grad_hidden and grad_head (of loss.sum()).
+    hidden [N, D] and head [V, D] (bf16, CUDA, last dim contiguous); targets int32 [N] (-1:
+    none); weights fp32 [N] or None (0: a row that is left out).  Returns loss fp32 [N], stats
+    fp32 [N, 2] (the row's log-sum-exp and minus the target's log-probability), row_status
+    int32 [N], and with with_grad, or where a buffer is given, grad_hidden and grad_head (of
+    loss.sum()).  Rows without a target are left out of a call with gradients, and of one with
+    targets_only; in others they have their log-sum-exp.
     """
     import torch
     N, dev, at = hidden.shape[0], hidden.device, hidden.get_device()
@@ -834,6 +837,7 @@ def specv_head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None, 
     stats = torch.empty((N, 2), dtype=torch.float32, device=dev) if stats is None else stats
     row_status = torch.empty(N, dtype=torch.int32, device=dev) if row_status is None else row_status
     args = _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head)
+    args.flags = SPECV_HEAD_TARGETS_ONLY if targets_only else 0
     args.loss = _of(loss, (N,), torch.float32, "loss", at)
     args.stats = _of(stats, (N, 2), torch.float32, "stats", at)
     args.row_status = _of(row_status, (N,), torch.int32, "row_status", at)
@@ -888,7 +892,7 @@ def head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None):
         class HeadLoss(torch.autograd.Function):
             @staticmethod
             def forward(ctx, hidden, head, targets, scale, weights):
-                out = specv_head_loss(hidden, head, targets, scale=scale, weights=weights)
+                out = specv_head_loss(hidden, head, targets, scale=scale, weights=weights, targets_only=True)
                 ctx.save_for_backward(hidden, head, targets, weights, out["stats"])
                 ctx.scale = scale
                 return out["loss"]

@@ -53,7 +53,7 @@ int hidden_splits(int32_t N, int32_t D, int64_t tokens) {
 
 // Offsets of the workspace's parts (bytes; all multiples of 256).
 struct HeadSpace {
-  size_t count, err, place, source, target, row, bad, z_target, part, hidden, head, dz, sum, bytes;
+  size_t count, most, err, place, source, target, row, bad, z_target, part, hidden, head, dz, sum, bytes;
   int64_t rows, ld, Dp, Ds, tokens;  // rows: N up to a block; ld: of part; Dp, Ds: strides of gathered rows and sums
   int splits;
   int part_cols;  // tokens per partial sum
@@ -80,6 +80,7 @@ HeadSpace head_space(const specv_head_args* a, bool keep) {
   w.copy_hidden = w.gather || w.grads || !fits;
   w.copy_head = !(aligned(a->head, 16) && (V <= 1 || a->head_stride % 8 == 0));
   w.count = take(4);
+  w.most = take(4);
   w.err = take(4 * 1024);
   w.place = take(4 * N);
   w.source = take(4 * N);
@@ -115,6 +116,7 @@ specv_status check_head(const specv_head_args* a) {
   if (a->dtype != SPECV_BF16) return api_fail(SPECV_ERR_UNSUPPORTED, "hidden states and head are bf16");
   if (!(a->scale >= 1e-6f && a->scale <= 1e6f))
     return api_fail(SPECV_ERR_INVALID_ARG, "scale=%g outside [1e-6, 1e6]", static_cast<double>(a->scale));
+  if (a->flags & ~SPECV_HEAD_TARGETS_ONLY) return api_fail(SPECV_ERR_INVALID_ARG, "unknown flags 0x%x", a->flags);
   if (a->N == 0 && !a->grad_head) return SPECV_OK;
   if (a->N > 0 && (!a->hidden || !a->targets)) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
   if (a->N > 0 && !a->head) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
@@ -159,11 +161,15 @@ struct HeadRun {
   const uint16_t* head() const { return w.copy_head ? at<uint16_t>(w.head) : static_cast<const uint16_t*>(a->head); }
   int64_t head_stride() const { return w.copy_head ? w.Dp : a->V > 1 ? a->head_stride : up_to(a->D, 8); }
 
+  // Whether rows without a target have statistics.
+  bool every_row() const { return !w.grads && !(a->flags & SPECV_HEAD_TARGETS_ONLY); }
+
   // Rows in use, and copies of operands that TMA cannot read in place.
   specv_status rows(bool backward) {
     HeadRowsParams r = {};
     r.N = a->N, r.V = a->V;
-    r.target = a->targets, r.weight = a->weights, r.scale = a->scale;
+    r.target = a->targets, r.weight = a->weights, r.scale = a->scale, r.all = !backward && every_row();
+    if (w.gather || w.grads) r.most = at<float>(w.most);
     if (backward) r.up = a->grad_loss, r.stats = a->stats, r.row = at<HeadRow>(w.row);
     if (w.gather) {
       r.count = at<int32_t>(w.count);
@@ -226,11 +232,11 @@ struct HeadRun {
     j.N = a->N, j.V = a->V, j.parts = (a->V + w.part_cols - 1) / w.part_cols;
     j.part = e.part, j.z_target = e.z_target, j.ld = w.ld, j.scale = a->scale;
     j.place = w.gather ? at<int32_t>(w.place) : nullptr;
-    j.target = a->targets, j.weight = a->weights;
+    j.target = a->targets, j.weight = a->weights, j.all = every_row();
     j.bad = w.grads ? at<int32_t>(w.bad) : nullptr;
     j.err = p.err, j.errs = w.half ? product_grid<false>(p) : product_grid<true>(p);
     j.loss = a->loss, j.stats = a->stats, j.status = a->row_status;
-    j.row = w.grads ? at<HeadRow>(w.row) : nullptr;
+    j.row = w.grads ? at<HeadRow>(w.row) : nullptr, j.most = at<float>(w.most);
     return done(launch_head_join(j, s), "head-join");
   }
 
@@ -272,7 +278,7 @@ struct HeadRun {
         else
           e.direct = out;
         e.stride = stride, e.cols = a->D;
-        TRY(done(launch_head_head(p, e, s), "head-dW"));
+        TRY(done(launch_head_head(p, e, at<float>(w.most), s), "head-dW"));
       }
       if (a->grad_hidden) {  // the piece's part of dh
         ProductParams p = product(a->N, a->D, n, false);
@@ -293,7 +299,7 @@ struct HeadRun {
     // (a last piece of few blocks is cut into fewer parts: its first parts are added to)
     f.splits = std::min<int>(w.splits, static_cast<int>(up_to(std::min<int64_t>(w.tokens, a->V), kProdBK) / kProdBK));
     f.sum = at<float>(w.sum), f.ld = w.Ds, f.split_stride = w.rows * w.Ds;
-    f.place = w.gather ? at<int32_t>(w.place) : nullptr, f.row = at<HeadRow>(w.row);
+    f.place = w.gather ? at<int32_t>(w.place) : nullptr, f.row = at<HeadRow>(w.row), f.most = at<float>(w.most);
     f.out = static_cast<uint16_t*>(a->grad_hidden), f.stride = a->N > 1 ? a->grad_hidden_stride : a->D;
     f.vec = aligned(a->grad_hidden, 16) && f.stride % 8 == 0;
     const int64_t blocks = (static_cast<int64_t>(a->N) * ((a->D + 7) / 8) + 255) / 256;

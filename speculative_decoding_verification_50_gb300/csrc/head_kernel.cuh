@@ -25,7 +25,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // What the backward pass knows of a row.
 struct HeadRow {
   float lse2;  // lse log2(e)
-  float g;     // upstream weight x s; 0: no gradient
+  float g;     // upstream weight x s, over the call's largest (HeadRowsParams::most); 0: no gradient
   float at;    // dz at the target
   int32_t target;
 };
@@ -53,7 +53,7 @@ struct HeadStatsParams {
 // chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum, 5e-7 in
 // chunks of 16 blocks).  Rows of one tile, bound by the head's bytes, take chunks of
 // kStatsChunkFew blocks at no cost.  PART: columns per partial sum, those of an epilogue warp.
-constexpr int kStatsChunk = 16, kStatsChunkFew = 8;
+constexpr int kStatsChunk = 16, kStatsChunkFew = 4;
 template <bool LONG, int PART>
 struct StatsEpi : PlainEpi {
   static constexpr bool kChunks = LONG;
@@ -244,11 +244,17 @@ __device__ __forceinline__ void soft_join(float& m, float& s, float m2, float s2
 
 struct HeadRowsParams {
   int32_t N, V;
+  int32_t all;             // rows without a target count too
   const int32_t* target;
   const float* weight;     // optional
   const float* up;         // optional (backward)
   const float* stats;      // backward: [N, 2]; forward: null
   float scale;
+  // The largest |g| of the rows (1 where none counts, or it is not finite).  dz is kept over
+  // it, and the products of dz are multiplied by it in fp32: rows of one weight then have
+  // -(1 - p) at their targets, which bf16 holds where p is small, in the place of a weight
+  // like 1 / 2870 whose rounding every row would share (2e-3 of the gradients).
+  float* most;
   int32_t* count;          // rows in use
   int32_t* place;          // [N]: a row's place among those in use, or -1
   int32_t* source;         // [N]: and back
@@ -280,9 +286,11 @@ struct HeadJoinParams {
   int64_t ld;
   float scale;
   const int32_t* place;    // optional (null: a row is where it is)
+  int32_t all;             // HeadRowsParams
   const int32_t* target;
   const float* weight;     // optional
   const int32_t* bad;      // optional, by place: rows with entries that are not finite
+  const float* most;       // HeadRowsParams (where row is given)
   const int32_t* err;      // [errs] of the forward pass
   int32_t errs;
   float* loss;
@@ -311,6 +319,7 @@ struct HeadFinishParams {
   int64_t ld, split_stride;
   const int32_t* place;    // optional
   const HeadRow* row;      // by place
+  const float* most;       // HeadRowsParams
   uint16_t* out;
   int64_t stride;
   int32_t vec;

@@ -11,7 +11,7 @@ cudaError_t launch_head_keep(ProductParams& p, const HeadStatsParams& e, const O
 cudaError_t launch_head_weight(const HeadWeightParams& p, int blocks, cudaStream_t s);
 cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStream_t s);
 cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s);
-cudaError_t launch_head_head(ProductParams& p, const Out16& out, cudaStream_t s);
+cudaError_t launch_head_head(ProductParams& p, const Out16& out, const float* factor, cudaStream_t s);
 cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t s);
 cudaError_t launch_head_gather(const HeadGatherParams& p, int blocks, cudaStream_t s);
 cudaError_t launch_head_join(const HeadJoinParams& p, cudaStream_t s);

@@ -7,21 +7,32 @@ namespace specv {
 
 namespace {
 
-// What is known of row r: its target if it counts (else -1), and in the backward pass its
-// gradient's factors.
-__device__ __forceinline__ HeadRow head_row(const HeadRowsParams& p, int r) {
+// Row r's target if it counts, else -1.
+__device__ __forceinline__ int head_target(const HeadRowsParams& p, int r) {
   const int t = p.target[r];
-  const float w = p.weight ? p.weight[r] : 1.f;
-  HeadRow row = {0.f, 0.f, 0.f, -1};
-  if (t < 0 || t >= p.V || w == 0.f) return row;
+  if (t < 0 || t >= p.V || (p.weight && p.weight[r] == 0.f)) return -1;
   if (p.stats) {
     const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
-    if (!(lse - lse == 0.f) || !(nll - nll == 0.f)) return row;
-    const float g = w * (p.up ? p.up[r] : 1.f) * p.scale;
-    row = {lse * kLog2e, g, g * expm1f(-nll), t};
+    if (!(lse - lse == 0.f) || !(nll - nll == 0.f)) return -1;
   }
-  row.target = t;
-  return row;
+  return t;
+}
+// Its gradient's weight.
+__device__ __forceinline__ float head_weight(const HeadRowsParams& p, int r) {
+  return (p.weight ? p.weight[r] : 1.f) * (p.up ? p.up[r] : 1.f) * p.scale;
+}
+__device__ __forceinline__ HeadRow head_row(float lse, float nll, float g, int target) {
+  return {lse * kLog2e, g, g * expm1f(-nll), target};
+}
+// The largest weight of a CTA's threads (a power of two of them up to 1024).
+__device__ __forceinline__ float head_most(float g, float (&warps)[32]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = g;
+  __syncthreads();
+  for (int k = 0; k < static_cast<int>(blockDim.x) / 32; ++k) g = fmaxf(g, warps[k]);
+  return g > 0.f && g < pos_inf() ? g : 1.f;
 }
 
 }  // namespace
@@ -29,15 +40,21 @@ __device__ __forceinline__ HeadRow head_row(const HeadRowsParams& p, int r) {
 // Which rows count, and where they go (in order).  One CTA.
 __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRowsParams p) {
   __shared__ int warps[32];
+  __shared__ float weights[32];
   __shared__ int before;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) before = 0;
   pdl_wait_primary();
   pdl_launch_dependents();
+  float most = 0.f;
+  for (int r = threadIdx.x; r < p.N; r += kRowsThreads)
+    if (head_target(p, r) >= 0) most = fmaxf(most, fabsf(head_weight(p, r)));
+  most = head_most(most, weights);
+  if (threadIdx.x == 0) *p.most = most;
   for (int first = 0; first < p.N; first += kRowsThreads) {
     const int r = first + threadIdx.x;
-    const HeadRow row = r < p.N ? head_row(p, r) : HeadRow{0.f, 0.f, 0.f, -1};
-    const bool use = row.target >= 0;
+    const int target = r < p.N ? head_target(p, r) : -1;
+    const bool use = target >= 0 || (p.all && r < p.N && p.target[r] == -1 && !(p.weight && p.weight[r] == 0.f));
     const unsigned votes = __ballot_sync(0xffffffffu, use);
     if (lane == 0) warps[warp] = __popc(votes);
     __syncthreads();
@@ -60,8 +77,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRo
       p.place[r] = at;
       if (at >= 0) {
         p.source[at] = r;
-        p.use_target[at] = row.target;
-        if (p.row) p.row[at] = row;
+        p.use_target[at] = target;
+        if (p.row) p.row[at] = head_row(p.stats[2 * r], p.stats[2 * r + 1], head_weight(p, r) / most, target);
       }
     }
   }
@@ -74,10 +91,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRo
 __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadGatherParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
+  __shared__ float weights[32];
   const int n = p.count ? *p.count : p.N;
+  float most = 1.f;
+  if (p.info.most) {  // (up to 256 rows, which every CTA looks through)
+    const int r = threadIdx.x;
+    most = head_most(r < n && head_target(p.info, r) >= 0 ? fabsf(head_weight(p.info, r)) : 0.f, weights);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.info.most = most;
+  }
   const int all = (n + p.pad_to - 1) / p.pad_to * p.pad_to;
   for (int i = blockIdx.x; i < max(all, p.pad_to); i += gridDim.x) {
-    if (p.info.row && threadIdx.x == 0 && i < n) p.info.row[i] = head_row(p.info, i);
+    if (p.info.row && threadIdx.x == 0 && i < n) {
+      const int t = head_target(p.info, i);
+      p.info.row[i] = t < 0 ? HeadRow{0.f, 0.f, 0.f, -1}
+                            : head_row(p.info.stats[2 * i], p.info.stats[2 * i + 1], head_weight(p.info, i) / most, t);
+    }
     uint16_t* out = p.out + i * p.out_stride;
     const int D8 = (p.D + 7) / 8;
     const uint16_t* in = i < n ? p.in + static_cast<int64_t>(p.source ? p.source[i] : i) * p.in_stride : nullptr;
@@ -122,7 +150,7 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   const int r = blockIdx.x * RB + threadIdx.x % RB, k = threadIdx.x / RB;
   const int t = r < p.N ? p.target[r] : -1;
   const float w = r < p.N && p.weight ? p.weight[r] : 1.f;
-  const bool use = t >= 0 && t < p.V && w != 0.f;
+  const bool use = (t >= 0 || (p.all && t == -1 && r < p.N)) && t < p.V && w != 0.f;
   const int at = r < p.N ? (p.place ? p.place[r] : r) : -1;
   const float c2 = p.scale * kLog2e;
   float m = kNegMax, s = 0.f;
@@ -150,7 +178,10 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   float lse = 0.f, nll = 0.f, loss = 0.f;
   int status = (t < -1 || t >= p.V) && w != 0.f ? kBadToken : 0;
   HeadRow row = {0.f, 0.f, 0.f, -1};
-  if (use) {
+  if (use && t < 0) {
+    lse = s == 0.f ? neg_inf() : p.scale * m + logf(s);
+    if (failed) status |= kTimeout;
+  } else if (use) {
     const float zt = p.z_target[at], d2 = (m - zt) * c2;
     // (relative to the target's logit where that is the largest, else to the largest of the others)
     nll = s == 0.f ? 0.f : d2 <= 0.f ? log1pf(s * exp2f(d2)) : d2 * kLn2 + logf(s + exp2f(-d2));
@@ -160,8 +191,7 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
     if (!(s - s == 0.f) || !(lse - lse == 0.f)) status |= kNonFinite;
     if (!status) {
       loss = w * nll;
-      const float g = w * p.scale;
-      row = {lse * kLog2e, g, g * expm1f(-nll), t};
+      if (p.row) row = head_row(lse, nll, w * p.scale / *p.most, t);
     }
   }
   if (status) lse = nll = __int_as_float(0x7fc00000);
@@ -211,6 +241,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
   pdl_wait_primary();
   pdl_launch_dependents();
   const int D8 = (p.D + 7) / 8;
+  const float f = *p.most;
   const int64_t all = static_cast<int64_t>(p.N) * D8;
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < all; x += static_cast<int64_t>(gridDim.x) * 256) {
     const int r = static_cast<int>(x / D8), j = static_cast<int>(x - static_cast<int64_t>(r) * D8) * 8;
@@ -225,7 +256,8 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
       }
     }
     uint16_t* out = p.out + r * p.stride + j;
-    const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    const uint4 w = make_uint4(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f), pack_bf16(v[4] * f, v[5] * f),
+                               pack_bf16(v[6] * f, v[7] * f));
     if (p.vec && j + 8 <= p.D) {
       *reinterpret_cast<uint4*>(out) = w;
     } else {
@@ -262,9 +294,9 @@ cudaError_t launch_head_prob(ProductParams& p, const ProbEpi::Params& e, cudaStr
 cudaError_t launch_head_hidden(ProductParams& p, const SumEpi::Params& e, cudaStream_t s) {
   return few(p) ? launch_product<false, false, true, SumEpi>(p, e, s) : launch_product<true, false, true, SumEpi>(p, e, s);
 }
-cudaError_t launch_head_head(ProductParams& p, const Out16& out, cudaStream_t s) {
-  if (p.K <= 16 * kProdBK) return launch_product<true, true, true, StoreEpi<true>>(p, {out, 1.f}, s);
-  return launch_product<true, true, true, StoreEpi<false>>(p, {out, 1.f}, s);
+cudaError_t launch_head_head(ProductParams& p, const Out16& out, const float* factor, cudaStream_t s) {
+  if (p.K <= 16 * kProdBK) return launch_product<true, true, true, StoreEpi<true>>(p, {out, factor}, s);
+  return launch_product<true, true, true, StoreEpi<false>>(p, {out, factor}, s);
 }
 cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t s) {
   return launch_grid(head_rows_kernel, 1, kRowsThreads, s, p);

@@ -554,17 +554,18 @@ struct PlainEpi {
   static __device__ __forceinline__ void add(EpiTile&, State&) {}
 };
 
-// C = alpha A B^T in bf16.  TWICE: two staging buffers, for products of so short a K that
+// C = factor A B^T in bf16.  TWICE: two staging buffers, for products of so short a K that
 // writing C bounds them (64 rows x 1024 x 32000: 23 us, with two 17).
 template <bool TWICE>
 struct StoreEpi : PlainEpi {
   static constexpr int kStaging = TWICE ? 8192 : 4096;
   struct Params {
     Out16 out;
-    float alpha;
+    const float* factor;
   };
   template <int COLS>
   static __device__ __forceinline__ void tile(const Params& e, EpiTile& q, State&) {
+    const float f = *e.factor;
 #pragma unroll 1
     for (int c = 0; c < COLS; c += 64) {
       uint32_t w[32];
@@ -573,7 +574,7 @@ struct StoreEpi : PlainEpi {
         float v[32];
         tmem_load32(q.tmem + c + 32 * h, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16(v[2 * j] * e.alpha, v[2 * j + 1] * e.alpha);
+        for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
       }
       put16<TWICE ? 1 : 0>(e.out, q.staging + (TWICE ? (c & 64) * 64 : 0), q.lane, q.row0, q.col0 + c, q.z, q.rows, w);
     }

@@ -21,7 +21,7 @@ def check(h, W, t, **how):
     if up is None:
         o = sv.specv_head_loss(h, W, t, with_grad=True, **how)
     else:
-        o = sv.specv_head_loss(h, W, t, **how)
+        o = sv.specv_head_loss(h, W, t, targets_only=True, **how)
         o.update(sv.specv_head_loss_backward(h, W, t, o["stats"], grad_loss=up, **how))
     assert (o["row_status"] == 0).all()
     hold(o["loss"], want, "loss")
@@ -89,6 +89,24 @@ def test_rows_that_are_left_out(N):
         o, _ = check(h, W, t, weights=w, **({} if up is None else dict(up=up)))
     out = (t < 0) | (w == 0)
     assert (o["loss"][out] == 0).all() and (o["stats"][out] == 0).all() and (o["grad_hidden"][out] == 0).all()
+
+
+@pytest.mark.parametrize("N", [1, 45, 200, 700])
+def test_log_sum_exp_of_rows_without_a_target(N):
+    h, W, t = inputs(N, 136, 999, seed=N)
+    t[::3] = -1
+    w = torch.ones(N, device="cuda")
+    w[1::5] = 0
+    o = sv.specv_head_loss(h, W, t, weights=w, scale=1.25)
+    want = head64(h, W, t.clamp_min(0), weights=w, scale=1.25)
+    hold(o["stats"][:, 0], want, "lse")
+    none = t < 0
+    assert (o["row_status"] == 0).all() and (o["loss"][none] == 0).all() and (o["stats"][none, 1] == 0).all()
+    only = sv.specv_head_loss(h, W, t, weights=w, scale=1.25, targets_only=True)
+    assert (only["stats"][none] == 0).all() and torch.equal(only["stats"][~none], o["stats"][~none])
+    h[0] = float("nan")
+    o = sv.specv_head_loss(h, W, t, weights=w)
+    assert o["row_status"][0] == 0 and o["stats"][0, 0].isnan() and o["loss"][0] == 0
 
 
 @pytest.mark.parametrize("N", [5, 300])

@@ -17,7 +17,7 @@ def lib():
 
 
 def head(**how):
-    a = sv.HeadArgs(64, 1000, 128, sv.SPECV_BF16, 256, 128, 256, 128, 256, None, 1.0, 256, 256, 256, None, 256, 128, 256, 128)
+    a = sv.HeadArgs(64, 1000, 128, sv.SPECV_BF16, 256, 128, 256, 128, 256, None, 1.0, 0, 256, 256, 256, None, 256, 128, 256, 128)
     for k, v in how.items():
         setattr(a, k, v)
     return a
@@ -31,7 +31,7 @@ def orth(**how):
 
 
 HEAD_BAD = [dict(N=-1), dict(V=0), dict(D=0), dict(dtype=7), dict(scale=0.0), dict(scale=float("nan")), dict(scale=-1.0),
-            dict(scale=1e7), dict(hidden=None), dict(head=None), dict(targets=None), dict(hidden=257), dict(targets=258),
+            dict(scale=1e7), dict(flags=2), dict(hidden=None), dict(head=None), dict(targets=None), dict(hidden=257), dict(targets=258),
             dict(weights=255), dict(stats=2), dict(row_status=3), dict(grad_head=11), dict(hidden_stride=127),
             dict(head_stride=100), dict(grad_hidden_stride=1), dict(grad_head_stride=127), dict(loss=None), dict(grad_loss=256)]
 
