@@ -197,6 +197,8 @@ struct HeadRun {
     return SPECV_OK;
   }
 
+  // Rows of a box of few rows (whole groups of the swizzle), or 0.
+  int few_box() const { return w.half ? static_cast<int>(up_to(a->N, 8)) : 0; }
   // rows_k: the rows in use are K, not M.
   ProductParams product(int32_t M, int32_t N, int32_t K, bool rows_k) const {
     ProductParams p = {};
@@ -204,6 +206,7 @@ struct HeadRun {
     p.bf16 = 1;
     p.rows = w.gather ? at<int32_t>(w.count) : nullptr;
     p.rows_k = rows_k;
+    p.a_rows = rows_k ? 0 : few_box();
     return p;
   }
   specv_status head_map(CUtensorMap* m, bool mn, int64_t first, int64_t n) const {
@@ -212,7 +215,7 @@ struct HeadRun {
 
   specv_status forward() {
     ProductParams p = product(a->N, a->V, a->D, false);
-    TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0));
+    TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0, few_box()));
     TRY(head_map(&p.b, false, 0, a->V));
     p.err = at<int32_t>(w.err);
     p.stall = api_test_stall('E');
@@ -256,7 +259,7 @@ struct HeadRun {
         TRY(done(launch_head_weight(p, static_cast<int>(std::min<int64_t>(blocks, 8 * api_sm_count())), s), "head-dz"));
       } else {  // dz of the piece
         ProductParams p = product(a->N, n, a->D, false);
-        TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0));
+        TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0, few_box()));
         TRY(head_map(&p.b, false, v, n));
         p.status = a->row_status, p.status_n = a->N;
         ProbEpi::Params e = {};
@@ -283,7 +286,7 @@ struct HeadRun {
       if (a->grad_hidden) {  // the piece's part of dh
         ProductParams p = product(a->N, a->D, n, false);
         p.splits = std::min<int>(w.splits, static_cast<int>(up_to(n, kProdBK) / kProdBK));
-        TRY(operand_map(&p.a, true, false, dz, n, w.rows, 1, w.tokens, 0));
+        TRY(operand_map(&p.a, true, false, dz, n, w.rows, 1, w.tokens, 0, few_box()));
         TRY(head_map(&p.b, true, v, n));
         p.status = a->row_status, p.status_n = a->N;
         SumEpi::Params e = {};

@@ -56,6 +56,7 @@ struct ProductParams {
   CUtensorMap a_low, b_low;  // fine: what a and b leave out
   int32_t fine;              // C = A B^T + A B_low^T + A_low B^T, one after the other
   int32_t M, N, K;         // the largest sizes (host), N exact
+  int32_t a_rows;          // not PAIR, A K-major: rows of A's boxes (0: all 128), where M has no more
   const int32_t* rows;     // device: the number of rows in use, in the place of M (rows_k: of K)
   int32_t rows_k;
   int32_t tn;              // tiles along N
@@ -345,6 +346,10 @@ __global__ void __launch_bounds__(kProdThreads, 1)
   if (warp == kLoadWarp) {  // ---- loads
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     if (lane == 0) {
+      // (rows of A that are not there take an SM's intake as others do, zeros or not: few rows
+      // come in boxes of their own, and what lies in the rest of the buffer gives rows of C
+      // that nothing reads)
+      const int spare = !PAIR && !A_MN && p.a_rows ? (kProdHalf - p.a_rows) * kProdBK * 2 : 0;
       int it = 0;
       bool ok = true;
       for (int u = cluster; ok && u < units.count; u += clusters) {
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(kProdThreads, 1)
             break;
           }
           if (rank == 0)
-            mbar_arrive_expect_tx(&full[s], kCtas * kStageBytes + ((p.stall == u + 1 && k == t.k0) ? 16 : 0));
+            mbar_arrive_expect_tx(&full[s], kCtas * kStageBytes - spare + ((p.stall == u + 1 && k == t.k0) ? 16 : 0));
           const uint32_t bar = PAIR ? in_first_cta(smem_u32(&full[s])) : smem_u32(&full[s]);
           const uint32_t sa = smem_u32(base + s * kStageBytes), sb = sa + kOperandBytes;
           const int part = p.fine ? k / units.span : 0;

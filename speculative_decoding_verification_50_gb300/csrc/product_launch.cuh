@@ -18,9 +18,9 @@ specv_status product_map(CUtensorMap* map, CUtensorMapDataType type, const void*
 
 // An operand: K-major [rows of A or B][K], or MN-major [K][rows of A or B].
 inline specv_status operand_map(CUtensorMap* map, bool bf16, bool mn, const void* base, int64_t cols, int64_t rows,
-                                int64_t batch, int64_t stride, int64_t batch_stride) {
+                                int64_t batch, int64_t stride, int64_t batch_stride, int box_rows = 0) {
   return product_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, rows, batch,
-                     2 * stride, 2 * batch_stride, mn ? kProdBK : kProdHalf);
+                     2 * stride, 2 * batch_stride, box_rows ? box_rows : mn ? kProdBK : kProdHalf);
 }
 
 // A launch that may be scheduled while the one before it on the stream drains (it waits
