@@ -305,7 +305,7 @@ struct HeadRun {
     f.place = w.gather ? at<int32_t>(w.place) : nullptr, f.row = at<HeadRow>(w.row), f.most = at<float>(w.most);
     f.out = static_cast<uint16_t*>(a->grad_hidden), f.stride = a->N > 1 ? a->grad_hidden_stride : a->D;
     f.vec = aligned(a->grad_hidden, 16) && f.stride % 8 == 0;
-    const int64_t blocks = (static_cast<int64_t>(a->N) * ((a->D + 7) / 8) + 255) / 256;
+    const int64_t blocks = (static_cast<int64_t>(a->N) * ((a->D + 3) / 4) + 255) / 256;
     return done(launch_head_finish(f, static_cast<int>(std::min<int64_t>(blocks, 16 * api_sm_count())), s), "head-dh");
   }
 };

@@ -163,16 +163,27 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
       for (int u = 0; u < 8; ++u) soft_join(m, s, x[u].x, x[u].y, c2);
     }
   }
-  got[threadIdx.x] = make_float2(m, s);
-  __syncthreads();
+  if (RB == 1) {  // a row's threads: within warps, then over the warps
 #pragma unroll
-  for (int o = T / 2; o > 0; o >>= 1) {
-    if (k < o) {
-      const float2 x = got[threadIdx.x + o * RB];
-      soft_join(m, s, x.x, x.y, c2);
-      got[threadIdx.x] = make_float2(m, s);
-    }
+    for (int o = 16; o > 0; o >>= 1)
+      soft_join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o), c2);
+    if ((threadIdx.x & 31) == 0) got[threadIdx.x >> 5] = make_float2(m, s);
     __syncthreads();
+    if (threadIdx.x == 0)
+#pragma unroll
+      for (int o = 1; o < kJoinThreads / 32; ++o) soft_join(m, s, got[o].x, got[o].y, c2);
+  } else {
+    got[threadIdx.x] = make_float2(m, s);
+    __syncthreads();
+#pragma unroll
+    for (int o = T / 2; o > 0; o >>= 1) {
+      if (k < o) {
+        const float2 x = got[threadIdx.x + o * RB];
+        soft_join(m, s, x.x, x.y, c2);
+        got[threadIdx.x] = make_float2(m, s);
+      }
+      __syncthreads();
+    }
   }
   if (k != 0 || r >= p.N) return;
   float lse = 0.f, nll = 0.f, loss = 0.f;
@@ -240,29 +251,27 @@ __global__ void __launch_bounds__(256) head_weight_kernel(const HeadWeightParams
 __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int D8 = (p.D + 7) / 8;
+  const int D4 = (p.D + 3) / 4;
   const float f = *p.most;
-  const int64_t all = static_cast<int64_t>(p.N) * D8;
+  const int64_t all = static_cast<int64_t>(p.N) * D4;
   for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; x < all; x += static_cast<int64_t>(gridDim.x) * 256) {
-    const int r = static_cast<int>(x / D8), j = static_cast<int>(x - static_cast<int64_t>(r) * D8) * 8;
+    const int r = static_cast<int>(x / D4), j = static_cast<int>(x - static_cast<int64_t>(r) * D4) * 4;
     const int at = p.place ? p.place[r] : r;
-    float v[8] = {};
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (at >= 0 && p.row[at].g != 0.f) {
-#pragma unroll 8
+#pragma unroll 16
       for (int k = 0; k < p.splits; ++k) {
-        const float* in = p.sum + k * p.split_stride + at * p.ld + j;
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(in)), b = __ldcs(reinterpret_cast<const float4*>(in) + 1);
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(p.sum + k * p.split_stride + at * p.ld + j));
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
       }
     }
     uint16_t* out = p.out + r * p.stride + j;
-    const uint4 w = make_uint4(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f), pack_bf16(v[4] * f, v[5] * f),
-                               pack_bf16(v[6] * f, v[7] * f));
-    if (p.vec && j + 8 <= p.D) {
-      *reinterpret_cast<uint4*>(out) = w;
+    const uint2 w = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+    if (p.vec && j + 4 <= p.D) {
+      *reinterpret_cast<uint2*>(out) = w;
     } else {
-      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-      for (int k = 0; k < min(8, p.D - j); ++k) out[k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+      const uint32_t h[2] = {w.x, w.y};
+      for (int k = 0; k < min(4, p.D - j); ++k) out[k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
     }
   }
 }
