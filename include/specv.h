@@ -489,10 +489,11 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * to bf16 (off by 2^-8 of each element at most), and are rounded once, to bf16.
  * Row status: SPECV_ROW_BAD_TOKEN (a target outside [-1, V)), SPECV_ROW_NONFINITE (a logit
  * that is NaN or infinite; rows that are left out may hold anything): loss 0, stats NaN, no
- * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row; in a call's gradients
+ * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row that counts; in a call's gradients
  * (row_status is added to by specv_head_loss_backward, if given) it leaves them undefined.
  * workspace: device memory of specv_head_workspace_bytes(args) bytes (of the same pointers,
- * sizes and strides), 256-byte aligned.  hidden, head and gradients whose rows start at
+ * sizes and strides), 256-byte aligned, not shared with a call that may run at the same
+ * time.  hidden, head and gradients whose rows start at
  * 16-byte boundaries are read and written in place; others are copied into the workspace.
  * fp32 is refused with SPECV_ERR_UNSUPPORTED.  The gradients overlap nothing.
  */
@@ -540,7 +541,8 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
  * [0, 1]) are refused with SPECV_ERR_INVALID_ARG.
  * out may be update itself (bf16).  workspace: device memory of
  * specv_orthogonalize_workspace_bytes() bytes (8 m n + 4 min(m, n)^2 per matrix, about; 0 for
- * matrices of a side up to 128 and another up to 2048, one kernel), 256-byte aligned.
+ * matrices of a side up to 128 and another up to 2048, one kernel), 256-byte aligned, not
+ * shared with a call that may run at the same time.
  */
 typedef struct {
   int32_t B, m, n;
