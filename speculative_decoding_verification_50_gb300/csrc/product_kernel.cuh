@@ -581,7 +581,10 @@ struct StoreEpi : PlainEpi {
 #pragma unroll
         for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
       }
-      put16<TWICE ? 1 : 0>(e.out, q.staging + (TWICE ? (c & 64) * 64 : 0), q.lane, q.row0, q.col0 + c, q.z, q.rows, w);
+      if (q.row0 >= q.rows || q.col0 + c >= e.out.cols) break;
+      // (buffers in turn by the stores made: a tile may make one, two or none)
+      put16<TWICE ? 1 : 0>(e.out, q.staging + (TWICE ? q.phase * 4096 : 0), q.lane, q.row0, q.col0 + c, q.z, q.rows, w);
+      q.phase ^= 1;
     }
   }
 };

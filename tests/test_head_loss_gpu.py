@@ -290,3 +290,37 @@ def test_workspace_of_the_size_asked_for():
         assert all(torch.equal(o[k], v) for k, v in sv.specv_head_loss(h, W, t, with_grad=True).items())
         sv.specv_head_loss_backward(h, W, t, o["stats"], workspace=room[:need])
         assert (room[need:] == 0x5a).all()
+
+
+@pytest.mark.parametrize("N,D,V", [(70001, 16, 700), (3, 24, 1000003), (64, 64, 300000), (200, 320, 50000), (5, 200, 200000)])
+def test_many_rows_and_many_tokens(N, D, V):
+    check(*inputs(N, D, V, seed=13))
+
+
+def test_offsets_past_32_bits():
+    """A head of 2.3 x 10^9 elements: the loss over all of it, gradients of its last rows."""
+    N, D, V = 2, 16384, 140003
+    g = torch.Generator(device="cuda").manual_seed(14)
+    W = torch.empty(V, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g).mul_(2.0 / D ** 0.5)
+    h = torch.randn(N, D, generator=g, device="cuda").bfloat16()
+    t = torch.tensor([V - 1, 5], dtype=torch.int32, device="cuda")
+    o = sv.specv_head_loss(h, W, t, with_grad=True)
+    b = sv.specv_head_loss_backward(h, W, t, o["stats"])
+    z = torch.cat([h.double() @ W[k:k + 20000].double().T for k in range(0, V, 20000)], 1)
+    logp = torch.log_softmax(z, 1)
+    # a sum over 16384 in 256s: (16 + 2) roundings of 2^-23 of the products' absolute sum, and 64 of chunks
+    size = h.double().abs().sum(1) * W.abs().amax().double()
+    assert ((o["loss"].double() + logp.gather(1, t.long()[:, None])[:, 0]).abs() <= 2 * 82 * 2.0 ** -23 * size).all()
+    d = logp.exp()
+    d[torch.arange(N), t.long()] -= 1
+    last = slice(V - 300, V)
+    want = d[:, last].T @ h.double()
+    scale = d[:, last].abs().T @ h.double().abs()
+    for x in (o, b):  # dz and the result rounded to bf16, the weights to fp16; logits off as above
+        off = (x["grad_head"][last].double() - want).abs()
+        assert (off <= (2.0 ** -8 + 2.0 ** -11 + 2 * 82 * 2.0 ** -23 * size.max()) * scale + 2.0 ** -8 * want.abs() + 1e-30).all()
+        part = torch.cat([d[:, k:k + 20000] @ W[k:k + 20000].double() for k in range(0, V, 20000)]).view(-1, N, D).sum(0)
+        bound = torch.cat([d[:, k:k + 20000].abs() @ W[k:k + 20000].double().abs() for k in range(0, V, 20000)]).view(-1, N, D).sum(0)
+        off = (x["grad_hidden"].double() - part).abs()
+        assert (off <= (2.0 ** -8 + 2.0 ** -11 + 2 * 82 * 2.0 ** -23 * size.max() + (V / 16 + 34) * 2.0 ** -23) * bound
+                + 2.0 ** -8 * part.abs()).all()

@@ -181,3 +181,20 @@ def test_workspace_of_the_size_asked_for(shape):
     assert torch.equal(o["orthogonal"], sv.specv_orthogonalize(G)["orthogonal"])
     with pytest.raises(sv.SpecvError):
         sv.specv_orthogonalize(G, workspace=room[:need - 1])
+
+
+@pytest.mark.parametrize("B,m,n", [(33000, 256, 256), (17000, 128, 1000), (140000, 130, 120)])
+def test_offsets_past_32_bits(B, m, n):
+    """Batches of more than 2^31 elements: the last matrices as if they were alone."""
+    G = torch.empty(B, m, n, dtype=torch.bfloat16, device="cuda")
+    if B > 65535:  # (more matrices than a call takes)
+        with pytest.raises(sv.SpecvError):
+            sv.specv_orthogonalize(G)
+        return
+    G.normal_(generator=torch.Generator(device="cuda").manual_seed(15))
+    o = sv.specv_orthogonalize(G)
+    assert (o["row_status"] == 0).all()
+    for k in (0, B // 2, B - 1):
+        alone = sv.specv_orthogonalize(G[k])
+        hold(o["orthogonal"][k], orth64(G[k])[0], bound(m, n))
+        hold(alone["orthogonal"], orth64(G[k])[0], bound(m, n))
