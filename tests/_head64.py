@@ -27,11 +27,11 @@ def head64(h, W, t, scale=1.0, weights=None, up=None):
     dz = (D / 16 + 2) * 2.0 ** -23 * size[:, 0] + 2.0 ** -23 * z.abs().amax(1)
     at = t.clamp(0, V - 1)[:, None]
     logp = torch.log_softmax(z, 1)
-    nll = -logp.gather(1, at)[:, 0]
+    rest = logp.exp().scatter(1, at, 0.0).sum(1)  # the other tokens' mass
+    nll = torch.where(rest < 0.5, -torch.log1p(-rest), -logp.gather(1, at)[:, 0])
     lse = torch.logsumexp(z, 1)
     nll_off = 2 * dz + 2.0 ** -21 * (1 + nll.abs())
-    # a row that is nearly certain: the other tokens' mass, whose digits the loss keeps
-    rest = logp.exp().scatter(1, at, 0.0).sum(1)
+    # a row that is nearly certain: the loss keeps the digits of the other tokens' mass
     nll_off = torch.minimum(nll_off, (rest / (1 - rest).clamp_min(1e-300)) * (torch.expm1(2 * dz) + 2.0 ** -20))
     out = dict(loss=torch.where(use, w * nll, 0.0), loss_off=torch.where(use, w.abs() * nll_off, 0.0),
                nll=torch.where(use, nll, 0.0), nll_off=nll_off,
