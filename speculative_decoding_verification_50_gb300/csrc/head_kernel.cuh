@@ -141,7 +141,8 @@ struct StatsEpi : PlainEpi {
 // m a row's largest logit of PART columns, are kept for them: times 2^15 in fp16 (off by 2^-11
 // of a weight at most, and by 2^-40 of the largest of PART), so that the logits need no second
 // product (4096 x 4096 x 128256, 0.7 of the rows in use: 6.0 ms, 7.7 with it).
-constexpr float kKeepScale = 15.f;  // (its logarithm)
+constexpr float kKeepScale = 15.f;         // (its logarithm)
+constexpr float kUnkeep = 1.f / 32768.f;
 template <int PART>
 struct KeepEpi : StatsEpi<true, PART> {
   static constexpr int kStaging = 4096;
@@ -178,7 +179,7 @@ struct KeepEpi : StatsEpi<true, PART> {
       sum.v[j] = ex2(fmaf(sum.v[j], e.s.c2, mc));
       s[j & 3] += sum.v[j];
     }
-    const float total = hi > neg_inf() ? ((s[0] + s[1]) + (s[2] + s[3])) * (1.f / 32768.f) : 0.f;
+    const float total = hi > neg_inf() ? ((s[0] + s[1]) + (s[2] + s[3])) * kUnkeep : 0.f;
     if (i < q.rows)
       e.s.part[static_cast<int64_t>(q.col0 / PART) * e.s.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
 #pragma unroll

@@ -231,12 +231,14 @@ __global__ void __launch_bounds__(256) head_weight_kernel(const HeadWeightParams
     const HeadRow r = i < n ? p.row[i] : HeadRow{0.f, 0.f, 0.f, -1};
     if (r.g != 0.f) {
       v = __ldcs(at);
-      const float f = r.g * ex2(fmaf(p.part[(col / p.part_cols) * p.ld + i].x, p.c2, -r.lse2) - kKeepScale);
+      const float f = r.g * ex2(fmaf(p.part[(col / p.part_cols) * p.ld + i].x, p.c2, -r.lse2));
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-        float a = e.x * f, b = e.y * f;
+        // (the weights' scale is taken off them, not off f: that would be 0 from 2^-111 on, in the
+        // place of 2^-126)
+        float a = e.x * kUnkeep * f, b = e.y * kUnkeep * f;
         if (col + 2 * k == r.target) a = r.at;
         if (col + 2 * k + 1 == r.target) b = r.at;
         w[k] = pack_bf16(a, b);
