@@ -487,6 +487,9 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * the logits once.
  * Products are summed in fp32.  The gradients' products read the logits' gradient rounded
  * to bf16 (off by 2^-8 of each element at most), and are rounded once, to bf16.
+ * Logits may be of any finite size: losses and probabilities are taken from their differences.
+ * (specv_head_loss_backward has those of a row from stats: where nll and |log-sum-exp| are both
+ * large, its probabilities are off by 2^-21 times the smaller of the two.)
  * Row status: SPECV_ROW_BAD_TOKEN (a target outside [-1, V)), SPECV_ROW_NONFINITE (a logit
  * that is NaN or infinite; rows that are left out may hold anything): loss 0, stats NaN, no
  * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row that counts; in a call's gradients

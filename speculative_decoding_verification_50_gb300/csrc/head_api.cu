@@ -183,6 +183,10 @@ struct HeadRun {
       if (w.gather) p.count = r.count, p.source = r.source;
       else p.info = r;
       if (w.grads) p.bad = at<int32_t>(w.bad);
+      if (backward) {
+        p.stats = a->stats, p.target = r.use_target, p.row = at<HeadRow>(w.row);
+        p.head = static_cast<const uint16_t*>(a->head), p.head_stride = a->V > 1 ? a->head_stride : a->D;
+      }
       p.in = static_cast<const uint16_t*>(a->hidden), p.in_stride = a->N > 1 ? a->hidden_stride : a->D;
       p.out = at<uint16_t>(w.hidden), p.out_stride = w.Dp;
       TRY(done(launch_head_gather(p, static_cast<int>(std::min<int64_t>(w.rows, 8 * api_sm_count())), s), "head-gather"));

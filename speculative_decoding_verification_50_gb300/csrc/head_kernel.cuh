@@ -22,13 +22,24 @@ namespace specv {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// What the backward pass knows of a row.
-struct HeadRow {
-  float lse2;  // lse log2(e)
+// Logits far from zero.  An exponent z s log2(e) - m s log2(e) from two rounded products is off
+// by 2^-24 of their size, not of its own: where the largest logit is above kFar (in powers of
+// two; 4e-6 of a sum there) the difference is taken first.  The probabilities of a row whose
+// log-sum-exp is above kFarRow (1e-4 of them there) are taken relative to a logit of the row.
+// Warps with such a row take a loop that chooses by row: a row's bits do not depend on its
+// neighbours.
+constexpr float kFar = 128.f, kFarRow = 2048.f;
+
+// What the backward pass knows of a row: its probabilities are 2^((z - ref) s log2(e) - off).
+struct alignas(16) HeadRow {
+  float ref;   // 0, or, in rows far from zero, the largest logit or the target's (an accumulator)
+  float off;   // (lse - s ref) log2(e)
   float g;     // upstream weight x s, over the call's largest (HeadRowsParams::most); 0: no gradient
   float at;    // dz at the target
   int32_t target;
+  int32_t none[3];
 };
+__device__ __forceinline__ HeadRow head_no_row() { return {0.f, 0.f, 0.f, 0.f, -1, {0, 0, 0}}; }
 
 // (smallest of three, NaN ignored)
 __device__ __forceinline__ float min3(float a, float b, float c) {
@@ -80,9 +91,10 @@ struct StatsEpi : PlainEpi {
   }
   static constexpr int kStaging = 0;
   using Params = HeadStatsParams;
-  // 32 columns: `at` is the target's place among them, `left` of them are the vocabulary's.
-  static __device__ __forceinline__ void part32(const Params& e, float (&v)[32], int i, int at, int left, float& m, float (&s)[4],
-                                                bool& bad) {
+  // 32 columns: `at` is the target's place among them, `left` of them are the vocabulary's;
+  // mine: whether the lane has a row (what others hold may be anything).
+  static __device__ __forceinline__ void part32(const Params& e, float (&v)[32], int i, bool mine, int at, int left, float& m,
+                                                float (&s)[4], bool& bad) {
     if (left <= 0) return;
     float hi = v[0], lo = v[0];
 #pragma unroll
@@ -108,8 +120,13 @@ struct StatsEpi : PlainEpi {
       for (int j = 0; j < 4; ++j) s[j] *= f;
       m = hi;
     }
-    if (hi > neg_inf()) {
-      const float mc = -m * e.c2;
+    const float mc = -m * e.c2;
+    const bool far = fabsf(mc) > kFar && hi > neg_inf() && mine;
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        s[j & 3] += far ? ex2((v[j] - m) * e.c2) : hi > neg_inf() ? ex2(fmaf(v[j], e.c2, mc)) : 0.f;
+    } else if (hi > neg_inf()) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], e.c2, mc));
     }
@@ -130,7 +147,7 @@ struct StatsEpi : PlainEpi {
       } else {
         tmem_load32(q.tmem + c, v);
       }
-      part32(e, v, i, target - (q.col0 + c), e.V - (q.col0 + c), m, s, bad);
+      part32(e, v, i, i < q.rows, target - (q.col0 + c), e.V - (q.col0 + c), m, s, bad);
     }
     const float total = (s[0] + s[1]) + (s[2] + s[3]);
     if (i < q.rows) e.part[static_cast<int64_t>(q.col0 / PART) * e.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
@@ -174,11 +191,16 @@ struct KeepEpi : StatsEpi<true, PART> {
     }
     const float m = fmaxf(hi, kNegMax), mc = kKeepScale - m * e.s.c2;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool far = fabsf(m * e.s.c2) > kFar && i < q.rows;
+    if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
-    for (int j = 0; j < PART; ++j) {
-      sum.v[j] = ex2(fmaf(sum.v[j], e.s.c2, mc));
-      s[j & 3] += sum.v[j];
+      for (int j = 0; j < PART; ++j) sum.v[j] = ex2(fmaf(far ? sum.v[j] - m : sum.v[j], e.s.c2, far ? kKeepScale : mc));
+    } else {
+#pragma unroll
+      for (int j = 0; j < PART; ++j) sum.v[j] = ex2(fmaf(sum.v[j], e.s.c2, mc));
     }
+#pragma unroll
+    for (int j = 0; j < PART; ++j) s[j & 3] += sum.v[j];
     const float total = hi > neg_inf() ? ((s[0] + s[1]) + (s[2] + s[3])) * kUnkeep : 0.f;
     if (i < q.rows)
       e.s.part[static_cast<int64_t>(q.col0 / PART) * e.s.ld + i] = make_float2(m, bad ? __int_as_float(0x7fc00000) : total);
@@ -207,11 +229,12 @@ struct ProbEpi : PlainEpi {
     const int rows = max((q.rows + kProdBK - 1) / kProdBK * kProdBK, kProdBK);
     if (q.row0 >= rows) return;
     const int i = q.row0 + q.lane;
-    HeadRow r = {0.f, 0.f, 0.f, -1};
+    HeadRow r = head_no_row();
     if (i < q.rows) {
       const float4 x = *reinterpret_cast<const float4*>(e.row + i);
-      r = {x.x, x.y, x.z, __float_as_int(x.w)};
+      r.ref = x.x, r.off = x.y, r.g = x.z, r.at = x.w, r.target = e.row[i].target;
     }
+    const bool far = __any_sync(0xffffffffu, r.ref != 0.f);
 #pragma unroll 1
     for (int c = 0; c < COLS; c += 64) {
       if (q.col0 + c >= e.out.cols) break;
@@ -220,8 +243,14 @@ struct ProbEpi : PlainEpi {
       for (int h = 0; h < 2; ++h) {
         float v[32];
         tmem_load32(q.tmem + c + 32 * h, v);
+        if (far) {  // (no probability is more than one, whatever its row's statistics hold of it)
+          const float most = r.ref != 0.f ? 0.f : pos_inf();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fmaf(v[j], e.c2, -r.lse2));
+          for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fminf(fmaf(v[j] - r.ref, e.c2, -r.off), most));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fmaf(v[j], e.c2, -r.off));
+        }
         const int at = r.target - e.first - (q.col0 + c + 32 * h);
         if (__any_sync(0xffffffffu, static_cast<unsigned>(at) < 32u || r.g == 0.f)) {
 #pragma unroll
@@ -277,6 +306,12 @@ struct HeadGatherParams {
   int64_t in_stride;
   uint16_t* out;
   int64_t out_stride;      // a multiple of 8
+  // backward: the target's logit of rows far from zero, which what is known of them refers to
+  const float* stats;      // [N, 2]; null: none
+  const int32_t* target;   // by place
+  HeadRow* row;            // by place
+  const uint16_t* head;    // rows that need not be aligned
+  int64_t head_stride;
 };
 
 constexpr int kGatherThreads = 256;

@@ -22,8 +22,10 @@ __device__ __forceinline__ float head_weight(const HeadRowsParams& p, int r) {
   return (p.weight ? p.weight[r] : 1.f) * (p.up ? p.up[r] : 1.f) * p.scale;
 }
 __device__ __forceinline__ HeadRow head_row(float lse, float nll, float g, int target) {
-  return {lse * kLog2e, g, g * expm1f(-nll), target};
+  return {0.f, lse * kLog2e, g, g * expm1f(-nll), target, {0, 0, 0}};
 }
+// Whether a row's log-sum-exp does not hold its probabilities' digits.
+__device__ __forceinline__ bool head_far(float lse) { return fabsf(lse) * kLog2e > kFarRow; }
 // The largest weight of a CTA's threads (a power of two of them up to 1024).
 __device__ __forceinline__ float head_most(float g, float (&warps)[32]) {
 #pragma unroll
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadG
   for (int i = blockIdx.x; i < max(all, p.pad_to); i += gridDim.x) {
     if (p.info.row && threadIdx.x == 0 && i < n) {
       const int t = head_target(p.info, i);
-      p.info.row[i] = t < 0 ? HeadRow{0.f, 0.f, 0.f, -1}
+      p.info.row[i] = t < 0 ? head_no_row()
                             : head_row(p.info.stats[2 * i], p.info.stats[2 * i + 1], head_weight(p.info, i) / most, t);
     }
     uint16_t* out = p.out + i * p.out_stride;
@@ -131,6 +133,28 @@ __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadG
     if (p.bad && in && threadIdx.x == 0) p.bad[i] = bad;
     for (int j = threadIdx.x; j < D8; j += kGatherThreads)
       reinterpret_cast<uint4*>(out)[j] = bad ? make_uint4(0, 0, 0, 0) : get(j);
+    if (p.stats && in) {
+      // A row far from zero: nll, where that is smaller than |lse|, and the target's logit.
+      const int r = p.source ? p.source[i] : i, t = p.source ? p.target[i] : head_target(p.info, i);
+      const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
+      if (t >= 0 && head_far(lse) && nll < fabsf(lse)) {  // (the CTA's)
+        float sum = 0.f;
+        const uint16_t* w = p.head + t * p.head_stride;
+        for (int j = threadIdx.x; j < p.D; j += kGatherThreads)
+          sum = fmaf(__uint_as_float(static_cast<uint32_t>(in[j]) << 16), __uint_as_float(static_cast<uint32_t>(w[j]) << 16), sum);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) weights[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+          for (int k = 1; k < kGatherThreads / 32; ++k) sum += weights[k];
+          p.row[i].ref = sum;
+          p.row[i].off = nll * kLog2e;
+        }
+      }
+    }
   }
 }
 
@@ -188,7 +212,7 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   if (k != 0 || r >= p.N) return;
   float lse = 0.f, nll = 0.f, loss = 0.f;
   int status = (t < -1 || t >= p.V) && w != 0.f ? kBadToken : 0;
-  HeadRow row = {0.f, 0.f, 0.f, -1};
+  HeadRow row = head_no_row();
   if (use && t < 0) {
     lse = s == 0.f ? neg_inf() : p.scale * m + logf(s);
     if (failed) status |= kTimeout;
@@ -196,6 +220,7 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
     const float zt = p.z_target[at], d2 = (m - zt) * c2;
     // (relative to the target's logit where that is the largest, else to the largest of the others)
     nll = s == 0.f ? 0.f : d2 <= 0.f ? log1pf(s * exp2f(d2)) : d2 * kLn2 + logf(s + exp2f(-d2));
+    if (d2 == pos_inf()) nll = (m - zt) * p.scale;  // (a difference up to fp32's range, but not times log2(e))
     lse = p.scale * zt + nll;
     if (failed) status |= kTimeout;
     if (p.bad && p.bad[at]) status |= kNonFinite;
@@ -203,6 +228,10 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
     if (!status) {
       loss = w * nll;
       if (p.row) row = head_row(lse, nll, w * p.scale / *p.most, t);
+      if (p.row && head_far(lse)) {  // relative to the largest logit
+        row.ref = s == 0.f || d2 <= 0.f ? zt : m;
+        row.off = s == 0.f || d2 <= 0.f ? nll * kLog2e : log2f(s + exp2f(-d2));
+      }
     }
   }
   if (status) lse = nll = __int_as_float(0x7fc00000);
@@ -228,10 +257,10 @@ __global__ void __launch_bounds__(256) head_weight_kernel(const HeadWeightParams
     if (col >= p.V) continue;
     uint4* at = reinterpret_cast<uint4*>(p.w + i * p.stride + col);
     uint4 v = make_uint4(0, 0, 0, 0);
-    const HeadRow r = i < n ? p.row[i] : HeadRow{0.f, 0.f, 0.f, -1};
+    const HeadRow r = i < n ? p.row[i] : head_no_row();
     if (r.g != 0.f) {
       v = __ldcs(at);
-      const float f = r.g * ex2(fmaf(p.part[(col / p.part_cols) * p.ld + i].x, p.c2, -r.lse2));
+      const float f = r.g * ex2(fmaf(p.part[(col / p.part_cols) * p.ld + i].x - r.ref, p.c2, -r.off));
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
