@@ -498,7 +498,8 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * sizes and strides), 256-byte aligned, not shared with a call that may run at the same
  * time.  hidden, head and gradients whose rows start at
  * 16-byte boundaries are read and written in place; others are copied into the workspace.
- * fp32 is refused with SPECV_ERR_UNSUPPORTED.  The gradients overlap nothing.
+ * fp32, and sizes above 2^31 - 2^11, are refused with SPECV_ERR_UNSUPPORTED.  The gradients
+ * overlap nothing.
  */
 #define SPECV_HEAD_TARGETS_ONLY 1
 
@@ -541,7 +542,8 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
  * A matrix of zeros gives zeros.  Status of a matrix: SPECV_ROW_NONFINITE (an entry that is
  * NaN or infinite): out 0, norm NaN; SPECV_ROW_DEVICE_TIMEOUT, on every matrix: out undefined.
  * Coefficients that may let a singular value grow past 1024 within the steps (by bounds over
- * [0, 1]) are refused with SPECV_ERR_INVALID_ARG.
+ * [0, 1]) are refused with SPECV_ERR_INVALID_ARG, sizes above 2^31 - 2^11 and more than 65535
+ * matrices with SPECV_ERR_UNSUPPORTED.
  * out may be update itself (bf16).  workspace: device memory of
  * specv_orthogonalize_workspace_bytes() bytes (8 m n + 4 min(m, n)^2 per matrix, about; 0 for
  * matrices of a side up to 128 and another up to 2048, one kernel), 256-byte aligned, not

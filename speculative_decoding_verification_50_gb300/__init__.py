@@ -796,10 +796,17 @@ def _work(need, workspace, device, stream):
     return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
+def _sizes(*tensors):
+    """(ctypes cuts a size off that 32 bits do not hold.)"""
+    for t in tensors:
+        assert all(n < 2 ** 31 for n in t.shape), f"a size of {tuple(t.shape)} is 2^31 or more"
+
+
 def _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head):
     import torch
     assert hidden.dim() == 2 and head.dim() == 2 and hidden.shape[1] == head.shape[1], (
         f"hidden [N, D] and head [V, D], got {tuple(hidden.shape)} and {tuple(head.shape)}")
+    _sizes(hidden, head)
     code = _dtype_code(hidden)
     assert head.dtype == hidden.dtype, f"hidden is {hidden.dtype}, head {head.dtype}"
     (N, D), V, at = hidden.shape, head.shape[0], hidden.get_device()
@@ -927,6 +934,7 @@ def specv_orthogonalize(update, *, steps: int = 5, coefficients=(3.4445, -4.7750
     assert update.dim() in (2, 3), "update must be [m, n] or [B, m, n]"
     flat, dev, at = update.dim() == 2, update.device, update.get_device()
     lead = update.shape[:-2]
+    _sizes(update)
     code = _dtype_code(update)
     if out is None:
         out = torch.empty(update.shape, dtype=torch.bfloat16, device=dev)

@@ -117,6 +117,8 @@ specv_status check_head(const specv_head_args* a) {
   if (!(a->scale >= 1e-6f && a->scale <= 1e6f))
     return api_fail(SPECV_ERR_INVALID_ARG, "scale=%g outside [1e-6, 1e6]", static_cast<double>(a->scale));
   if (a->flags & ~SPECV_HEAD_TARGETS_ONLY) return api_fail(SPECV_ERR_INVALID_ARG, "unknown flags 0x%x", a->flags);
+  if (std::max({a->N, a->V, a->D}) > kProdMost)
+    return api_fail(SPECV_ERR_UNSUPPORTED, "N=%d, V=%d, D=%d: more than %d", a->N, a->V, a->D, kProdMost);
   if (a->N == 0 && !a->grad_head) return SPECV_OK;
   if (a->N > 0 && (!a->hidden || !a->targets)) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
   if (a->N > 0 && !a->head) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");

@@ -12,7 +12,7 @@ __device__ __forceinline__ int head_target(const HeadRowsParams& p, int r) {
   const int t = p.target[r];
   if (t < 0 || t >= p.V || (p.weight && p.weight[r] == 0.f)) return -1;
   if (p.stats) {
-    const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
+    const float lse = p.stats[2LL * r], nll = p.stats[2LL * r + 1];
     if (!(lse - lse == 0.f) || !(nll - nll == 0.f)) return -1;
   }
   return t;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) head_rows_kernel(const HeadRo
       if (at >= 0) {
         p.source[at] = r;
         p.use_target[at] = target;
-        if (p.row) p.row[at] = head_row(p.stats[2 * r], p.stats[2 * r + 1], head_weight(p, r) / most, target);
+        if (p.row) p.row[at] = head_row(p.stats[2LL * r], p.stats[2LL * r + 1], head_weight(p, r) / most, target);
       }
     }
   }
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadG
     if (p.info.row && threadIdx.x == 0 && i < n) {
       const int t = head_target(p.info, i);
       p.info.row[i] = t < 0 ? head_no_row()
-                            : head_row(p.info.stats[2 * i], p.info.stats[2 * i + 1], head_weight(p.info, i) / most, t);
+                            : head_row(p.info.stats[2LL * i], p.info.stats[2LL * i + 1], head_weight(p.info, i) / most, t);
     }
     uint16_t* out = p.out + i * p.out_stride;
     const int D8 = (p.D + 7) / 8;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadG
     if (p.stats && in) {
       // A row far from zero: nll, where that is smaller than |lse|, and the target's logit.
       const int r = p.source ? p.source[i] : i, t = p.source ? p.target[i] : head_target(p.info, i);
-      const float lse = p.stats[2 * r], nll = p.stats[2 * r + 1];
+      const float lse = p.stats[2LL * r], nll = p.stats[2LL * r + 1];
       if (t >= 0 && head_far(lse) && nll < fabsf(lse)) {  // (the CTA's)
         float sum = 0.f;
         const uint16_t* w = p.head + t * p.head_stride;
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadJoinP
   if (status) lse = nll = __int_as_float(0x7fc00000);
   p.loss[r] = loss;
   if (p.stats) {
-    p.stats[2 * r] = lse;
-    p.stats[2 * r + 1] = nll;
+    p.stats[2LL * r] = lse;
+    p.stats[2LL * r + 1] = nll;
   }
   if (p.status) p.status[r] = status;
   if (p.row && at >= 0) p.row[at] = row;

@@ -136,6 +136,8 @@ specv_status check_orth(const specv_orth_args* a) {
       return api_fail(SPECV_ERR_INVALID_ARG, "coefficients (%g, %g, %g) may let singular values grow past %g in %d steps",
                       static_cast<double>(a->a), static_cast<double>(a->b), static_cast<double>(a->c), kMostGrowth, a->steps);
   }
+  if (std::max(a->m, a->n) > kProdMost)
+    return api_fail(SPECV_ERR_UNSUPPORTED, "m=%d, n=%d: more than %d", a->m, a->n, kProdMost);
   if (a->B == 0) return SPECV_OK;
   if (!a->update || !a->out) return api_fail(SPECV_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned(a->update, a->dtype == SPECV_BF16 ? 2 : 4) || !aligned(a->out, 2) || !aligned(a->norm, 4) ||

@@ -10,6 +10,10 @@
 
 namespace specv {
 
+// The largest size of a matrix that the kernels' 32-bit counts, rounded up to tiles or a CTA's
+// threads, hold.
+constexpr int32_t kProdMost = 0x7fffffff - 2047;
+
 // A TMA descriptor of a matrix [batch][rows][cols] of 16-bit (or fp32) elements: boxes of
 // `width` bytes x box_rows, swizzled over that width (128, 64; 0: 64 bytes, as they are),
 // zeros outside.  base and the strides (bytes) are multiples of 16.
