@@ -87,7 +87,7 @@ typedef enum { SPECV_BF16 = 0, SPECV_FP32 = 1 } specv_dtype;
                                  the row instead of waiting forever (not
                                  expected on a healthy GPU; for tests, the
                                  environment variable SPECV_TEST_STALL="A:<i>"
-                                 to "F:<n>", read once per process, makes one
+                                 to "I:<n>", read once per process, makes one
                                  such wait run out) */
 
 /*
@@ -492,8 +492,9 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * large, its probabilities are off by 2^-21 times the smaller of the two.)
  * Row status: SPECV_ROW_BAD_TOKEN (a target outside [-1, V)), SPECV_ROW_NONFINITE (a logit
  * that is NaN or infinite; rows that are left out may hold anything): loss 0, stats NaN, no
- * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row that counts; in a call's gradients
- * (row_status is added to by specv_head_loss_backward, if given) it leaves them undefined.
+ * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row that counts; where the wait that
+ * ran out was one of the gradients' products, both gradients are 0 and every row is flagged
+ * (specv_head_loss_backward adds to row_status, if given), and losses stay.
  * workspace: device memory of specv_head_workspace_bytes(args) bytes (of the same pointers,
  * sizes and strides), 256-byte aligned, not shared with a call that may run at the same
  * time.  hidden, head and gradients whose rows start at

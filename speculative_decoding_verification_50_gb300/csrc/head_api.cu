@@ -53,7 +53,7 @@ int hidden_splits(int32_t N, int32_t D, int64_t tokens) {
 
 // Offsets of the workspace's parts (bytes; all multiples of 256).
 struct HeadSpace {
-  size_t count, most, err, place, source, target, row, bad, z_target, part, hidden, head, dz, sum, bytes;
+  size_t count, most, late, err, place, source, target, row, bad, z_target, part, hidden, head, dz, sum, bytes;
   int64_t rows, ld, Dp, Ds, tokens;  // rows: N up to a block; ld: of part; Dp, Ds: strides of gathered rows and sums
   int splits;
   int part_cols;  // tokens per partial sum
@@ -81,6 +81,7 @@ HeadSpace head_space(const specv_head_args* a, bool keep) {
   w.copy_head = !(aligned(a->head, 16) && (V <= 1 || a->head_stride % 8 == 0));
   w.count = take(4);
   w.most = take(4);
+  w.late = take(4);
   w.err = take(4 * 1024);
   w.place = take(4 * N);
   w.source = take(4 * N);
@@ -184,7 +185,7 @@ struct HeadRun {
       p.vec = aligned(a->hidden, 16) && (a->N <= 1 || a->hidden_stride % 8 == 0);
       if (w.gather) p.count = r.count, p.source = r.source;
       else p.info = r;
-      if (w.grads) p.bad = at<int32_t>(w.bad);
+      if (w.grads) p.bad = at<int32_t>(w.bad), p.late = at<int32_t>(w.late);
       if (backward) {
         p.stats = a->stats, p.target = r.use_target, p.row = at<HeadRow>(w.row);
         p.head = static_cast<const uint16_t*>(a->head), p.head_stride = a->V > 1 ? a->head_stride : a->D;
@@ -267,7 +268,7 @@ struct HeadRun {
         ProductParams p = product(a->N, n, a->D, false);
         TRY(operand_map(&p.a, true, false, hidden(), a->D, a->N, 1, hidden_stride(), 0, few_box()));
         TRY(head_map(&p.b, false, v, n));
-        p.status = a->row_status, p.status_n = a->N;
+        p.late = at<int32_t>(w.late), p.stall = piece ? 0 : api_test_stall('G');
         ProbEpi::Params e = {};
         TRY(product_map(&e.out.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dz, n, w.rows, 1, 2 * w.tokens, 0, 32));
         e.out.cols = n;
@@ -278,7 +279,7 @@ struct HeadRun {
         ProductParams p = product(n, a->D, a->N, true);
         TRY(operand_map(&p.a, true, true, dz, n, w.rows, 1, w.tokens, 0));
         TRY(operand_map(&p.b, true, true, hidden(), a->D, w.rows, 1, hidden_stride(), 0));
-        p.status = a->row_status, p.status_n = a->N;
+        p.late = at<int32_t>(w.late), p.stall = piece ? 0 : api_test_stall('H');
         Out16 e = {};
         uint16_t* out = static_cast<uint16_t*>(a->grad_head) + v * a->grad_head_stride;
         const int64_t stride = a->V > 1 ? a->grad_head_stride : up_to(a->D, 8);
@@ -294,7 +295,7 @@ struct HeadRun {
         p.splits = std::min<int>(w.splits, static_cast<int>(up_to(n, kProdBK) / kProdBK));
         TRY(operand_map(&p.a, true, false, dz, n, w.rows, 1, w.tokens, 0, few_box()));
         TRY(head_map(&p.b, true, v, n));
-        p.status = a->row_status, p.status_n = a->N;
+        p.late = at<int32_t>(w.late), p.stall = piece ? 0 : api_test_stall('I');
         SumEpi::Params e = {};
         TRY(product_map(&e.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, at<float>(w.sum), w.Ds, w.rows, w.splits, 4 * w.Ds,
                         4 * w.rows * w.Ds, 32));
@@ -302,9 +303,11 @@ struct HeadRun {
         TRY(done(launch_head_hidden(p, e, s), "head-dh"));
       }
     }
-    if (!a->grad_hidden) return SPECV_OK;
     HeadFinishParams f = {};
-    f.N = a->N, f.D = a->D;
+    f.N = a->N, f.V = a->V, f.D = a->D;
+    f.late = at<int32_t>(w.late), f.status = a->row_status;
+    f.head = static_cast<uint16_t*>(a->grad_head), f.head_stride = a->V > 1 ? a->grad_head_stride : a->D;
+    if (!a->grad_hidden) return done(launch_head_finish(f, api_sm_count(), s), "head-end");
     // (a last piece of few blocks is cut into fewer parts: its first parts are added to)
     f.splits = std::min<int>(w.splits, static_cast<int>(up_to(std::min<int64_t>(w.tokens, a->V), kProdBK) / kProdBK));
     f.sum = at<float>(w.sum), f.ld = w.Ds, f.split_stride = w.rows * w.Ds;

@@ -312,6 +312,7 @@ struct HeadGatherParams {
   HeadRow* row;            // by place
   const uint16_t* head;    // rows that need not be aligned
   int64_t head_stride;
+  int32_t* late;           // optional: the call's word for late products, which begins as 0
 };
 
 constexpr int kGatherThreads = 256;
@@ -350,14 +351,20 @@ struct HeadWeightParams {
   int64_t stride;
 };
 
+// The end of a call's gradients: dh (if any) from its sums; and where a product's wait ran out,
+// zeros in the place of all of them, and the status.
 struct HeadFinishParams {
-  int32_t N, D, splits;
+  int32_t N, V, D, splits;
+  const int32_t* late;
+  int32_t* status;         // optional [N]: added to
+  uint16_t* head;          // dW, optional
+  int64_t head_stride;
   const float* sum;        // [splits][rows][ld]
   int64_t ld, split_stride;
   const int32_t* place;    // optional
   const HeadRow* row;      // by place
   const float* most;       // HeadRowsParams
-  uint16_t* out;
+  uint16_t* out;           // dh, optional
   int64_t stride;
   int32_t vec;
 };

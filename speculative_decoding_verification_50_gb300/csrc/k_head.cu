@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kGatherThreads) head_gather_kernel(const HeadG
   pdl_launch_dependents();
   __shared__ float weights[32];
   const int n = p.count ? *p.count : p.N;
+  if (p.late && blockIdx.x == 0 && threadIdx.x == 0) *p.late = 0;
   float most = 1.f;
   if (p.info.most) {  // (up to 256 rows, which every CTA looks through)
     const int r = threadIdx.x;
@@ -278,10 +279,20 @@ __global__ void __launch_bounds__(256) head_weight_kernel(const HeadWeightParams
   }
 }
 
-// dh from the sums of K's parts, rows back in their places.
+// dh from the sums of K's parts, rows back in their places; nothing but zeros after a late product.
 __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
+  const bool late = *p.late != 0;
+  if (late) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t r = first; p.status && r < p.N; r += step) p.status[r] |= kTimeout;
+    for (int64_t x = first; p.head && x < static_cast<int64_t>(p.V) * p.D; x += step) {
+      const int64_t v = x / p.D;
+      p.head[v * p.head_stride + (x - v * p.D)] = 0;
+    }
+  }
+  if (!p.out) return;
   const int D4 = (p.D + 3) / 4;
   const float f = *p.most;
   const int64_t all = static_cast<int64_t>(p.N) * D4;
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinishParams
     const int r = static_cast<int>(x / D4), j = static_cast<int>(x - static_cast<int64_t>(r) * D4) * 4;
     const int at = p.place ? p.place[r] : r;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (at >= 0 && p.row[at].g != 0.f) {
+    if (at >= 0 && p.row[at].g != 0.f && !late) {
 #pragma unroll 16
       for (int k = 0; k < p.splits; ++k) {
         const float4 a = __ldcs(reinterpret_cast<const float4*>(p.sum + k * p.split_stride + at * p.ld + j));

@@ -68,6 +68,7 @@ struct ProductParams {
   int32_t* err;            // [clusters]: 0, or 1 where a wait ran out
   int32_t* status;         // optional [status_n]: a wait that ran out is added (kTimeout)
   int32_t status_n;
+  int32_t* late;           // optional: one word, made 1 by a wait that ran out
   int32_t stall;           // test hook: 1 + the unit whose first copy is late
 };
 
@@ -486,6 +487,7 @@ __global__ void __launch_bounds__(kProdThreads, 1)
   if (warp == kMmaWarp) tmem_free_all<PAIR>(tmem);
   const int failed = *gone;
   if (threadIdx.x == 0 && p.err) p.err[blockIdx.x] = failed;
+  if (failed && p.late && threadIdx.x == 0) *p.late = 1;
   if (failed && p.status)
     for (int i = threadIdx.x; i < p.status_n; i += kProdThreads) atomicOr(&p.status[i], kTimeout);
 }
