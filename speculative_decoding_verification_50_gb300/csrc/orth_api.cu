@@ -196,6 +196,7 @@ struct OrthRun {
   // S, then P = b S + c S S
   template <bool FINE>
   specv_status symmetric(int from, const SmallStep& f) {
+    const bool first = launches == 2;  // (the test hooks')
     bool half;
     {
       ProductParams p = product(w.s, w.s, w.t, true, half);
@@ -204,7 +205,7 @@ struct OrthRun {
       TRY(x_map(&p.a, w.tall, w.hi[from]));
       if (FINE) TRY(x_map(&p.a_low, w.tall, w.lo[from]));
       p.b = p.a, p.b_low = p.a_low;
-      if (launches == 2) p.stall = api_test_stall('F');
+      if (first) p.stall = api_test_stall('F');
       if (p.splits > 1) {
         SumEpi::Params e = {};
         TRY(product_map(&e.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, at(w.sums), w.s, w.s, a->B * p.splits, 4 * w.lds, 4 * zs(), 32));
@@ -230,6 +231,7 @@ struct OrthRun {
     TRY(box_map(&e.chi, w.gram[0], w.s, w.s, w.lds));
     if (FINE) TRY(box_map(&e.clo, w.gram[1], w.s, w.s, w.lds));
     e.alpha = f.poly, e.beta = f.poly_s;
+    if (first) p.stall_read = api_test_stall('J');
     return done(launch_orth_poly<FINE>(half, p, e, s), "orthogonalize-poly");
   }
   template <typename Params>
@@ -293,6 +295,7 @@ struct OrthRun {
       // X' = a X + P X, or a X + X P (P is its own transpose)
       bool half;
       ProductParams p = product(a->m, a->n, w.s, false, half);
+      if (k == 0) p.stall_read = api_test_stall('J');
       TRY(s_map(w.tall ? &p.b : &p.a, w.poly[0]));
       TRY(x_map(w.tall ? &p.a : &p.b, !w.tall, w.hi[from]));
       if (w.fine) {

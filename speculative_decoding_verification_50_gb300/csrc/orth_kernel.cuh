@@ -85,19 +85,21 @@ struct Boxes {
   // Both inputs of a group (lo: where LOW), by lane 0; the stores of the group before last,
   // which used the buffer, have read it.
   template <bool LOW>
-  static __device__ __forceinline__ void fetch(const CUtensorMap* hi, const CUtensorMap* lo, const EpiTile& q, int g, int col) {
+  static __device__ __forceinline__ void fetch(const CUtensorMap* hi, const CUtensorMap* lo, EpiTile& q, int g, int col) {
+    q.asked ^= 1u << (g & 1);
     if (q.lane == 0) {
       uint8_t* at = q.staging + (g & 1) * BUF;
       uint64_t* bar = q.bar + (g & 1);
-      mbar_arrive_expect_tx(bar, LOW ? 2 * kBox : kBox);
+      mbar_arrive_expect_tx(bar, (LOW ? 2 * kBox : kBox) + q.extra);
       tma_load<false>(smem_u32(at), hi, col, q.row0, q.z, smem_u32(bar));
       if (LOW) tma_load<false>(smem_u32(at) + kBox, lo, col, q.row0, q.z, smem_u32(bar));
     }
+    q.extra = 0;
   }
   // The warp's wait for a group (false: it ran out).
   static __device__ __forceinline__ bool wait(EpiTile& q, int g) {
     const bool ok = __all_sync(0xffffffffu, prod_wait(q.bar + (g & 1), (q.phase >> (g & 1)) & 1, q.gone));
-    q.phase ^= 1u << (g & 1);
+    if (ok) q.phase ^= 1u << (g & 1);
     return ok;
   }
 };
@@ -107,6 +109,7 @@ struct Boxes {
 template <bool ADD, bool FINE>
 struct SymEpi : PlainEpi {
   static constexpr int kBuf = FINE ? 4 * kBox : 2 * kBox, kStaging = 2 * kBuf;  // hi, (lo,) and the transposed ones
+  static constexpr bool kReads = ADD;
   using B = Boxes<kBuf>;
   struct Params {
     CUtensorMap hi, lo;                // boxes of 32 x 32, swizzled
@@ -204,6 +207,7 @@ struct OrthJoinParams {
 template <bool LAST>
 struct StepEpi : PlainEpi {
   static constexpr int kBuf = 2 * kBox, kStaging = 2 * kBuf;
+  static constexpr bool kReads = true;
   using B = Boxes<kBuf>;
   struct Params {
     CUtensorMap hi, lo;       // LAST: hi alone

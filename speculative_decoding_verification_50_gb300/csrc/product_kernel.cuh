@@ -70,6 +70,7 @@ struct ProductParams {
   int32_t status_n;
   int32_t* late;           // optional: one word, made 1 by a wait that ran out
   int32_t stall;           // test hook: 1 + the unit whose first copy is late
+  int32_t stall_read;      // and 1 + that whose epilogue's first copy is
 };
 
 // Instruction descriptor of tcgen05.mma kind::f16 for tiles of tile x tile, fp32 accumulators.
@@ -270,6 +271,8 @@ struct EpiTile {
   Unit unit;
   uint64_t* bar;      // two of the warp's own, for what the epilogue reads, and their phases (bits)
   uint32_t phase;
+  uint32_t asked;     // the phases that copies were asked for
+  int extra;          // bytes that the next copy's wait is for beside the copy's (test hook)
   volatile int* gone;
 };
 
@@ -429,11 +432,10 @@ __global__ void __launch_bounds__(kProdThreads, 1)
           if (ok) tc_commit<PAIR>(smem_u32(&tfull[n & 1]));
         }
       }
-      if (*gone) {  // products in flight end before tensor memory is freed
-        tc_commit<PAIR>(smem_u32(drain));
-        const long long t0 = clock64();
-        while (!mbar_try_wait_sleep(drain, 0, 20000u) && clock64() - t0 < 1000000000LL) {
-        }
+      // (products in flight end before tensor memory is freed, whatever other warps gave up on)
+      tc_commit<PAIR>(smem_u32(drain));
+      const long long t0 = clock64();
+      while (!mbar_try_wait_sleep(drain, 0, 20000u) && clock64() - t0 < 1000000000LL) {
       }
     }
   } else if (warp < kEpiWarp) {
@@ -446,7 +448,8 @@ __global__ void __launch_bounds__(kProdThreads, 1)
     q.lane = lane;
     q.rows = p.rows && !p.rows_k ? *p.rows : p.M;
     q.bar = &epi[2 * (warp - kEpiWarp)];
-    q.phase = 0;
+    q.phase = q.asked = 0;
+    q.extra = 0;
     q.gone = gone;
     int n = 0;
     bool ok = true;
@@ -458,6 +461,7 @@ __global__ void __launch_bounds__(kProdThreads, 1)
       q.z = t.z;
       q.split = t.split;
       q.unit = t;
+      if (Epi::kReads && p.stall_read == u + 1) q.extra = 16;
       Epi::ahead(e, q);
       Epi::start(state);
       const int chunk = Epi::kChunks && p.chunk ? p.chunk : t.k1 - t.k0;
@@ -474,8 +478,19 @@ __global__ void __launch_bounds__(kProdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(PAIR ? in_first_cta(smem_u32(&tempty[acc])) : smem_u32(&tempty[acc]));
+        if (Epi::kReads && __any_sync(0xffffffffu, *gone)) {  // (what the next tile reads is not asked for)
+          ok = false;
+          break;
+        }
       }
       if (Epi::kChunks && ok) Epi::template tile<kTile / 2>(e, q, state);
+    }
+    if (Epi::kReads && lane == 0) {  // copies asked for and not waited for land before the CTA leaves
+      const long long t0 = clock64();
+      for (int b = 0; b < 2; ++b)
+        while ((((q.asked ^ q.phase) >> b) & 1) && !mbar_try_wait_sleep(q.bar + b, (q.phase >> b) & 1, 20000u) &&
+               clock64() - t0 < 1000000000LL) {
+        }
     }
     if (Epi::kStaging > 0 && lane == 0) tma_wait_read<0>();  // (the grid's end waits for the writes)
   }
@@ -554,7 +569,7 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 // An epilogue of whole tiles that reads nothing of its own.
 struct PlainEpi {
   struct State {};
-  static constexpr bool kChunks = false;
+  static constexpr bool kChunks = false, kReads = false;  // kReads: boxes (orth_kernel.cuh)
   template <typename P>
   static __device__ __forceinline__ void ahead(const P&, EpiTile&) {}
   static __device__ __forceinline__ void start(State&) {}

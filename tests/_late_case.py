@@ -1,6 +1,6 @@
-"""Late copies in the gradients' products, in a fresh process with SPECV_TEST_STALL set (the
+"""Late copies in the gradients' products and in what an update's products add to, in a fresh process with SPECV_TEST_STALL set (the
 library reads it once per process).  Run by tests/test_late_gpu.py as
-`python -m tests._late_case <what> <rows>`.
+`python -m tests._late_case <what> <rows>` (or, for an update, its smaller side).
 """
 import sys
 import time
@@ -50,11 +50,18 @@ def head(what, N):
     return h, W, t, want
 
 
+def update(N):
+    """Every matrix flagged."""
+    for shape in ((2, N, 700), (3, 700, N)):
+        o = sv.specv_orthogonalize(torch.randn(*shape, device="cuda"))
+        assert (o["row_status"] == sv.ROW_DEVICE_TIMEOUT).all(), o["row_status"]
+
+
 def main():
     what, N = sys.argv[1], int(sys.argv[2])
     torch.cuda.synchronize()
     t0 = time.perf_counter()
-    head(what, N)
+    update(N) if what == "update" else head(what, N)
     torch.cuda.synchronize()
     dt = time.perf_counter() - t0
     assert 0.3 < dt < 40, dt
