@@ -87,7 +87,7 @@ typedef enum { SPECV_BF16 = 0, SPECV_FP32 = 1 } specv_dtype;
                                  the row instead of waiting forever (not
                                  expected on a healthy GPU; for tests, the
                                  environment variable SPECV_TEST_STALL="A:<i>"
-                                 to "J:<n>", read once per process, makes one
+                                 to "K:<n>", read once per process, makes one
                                  such wait run out) */
 
 /*
@@ -541,7 +541,8 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
  * five exact steps by about 2e-3 of its norm at most, most of it the rounding to bf16
  * (low-rank and badly scaled updates too).
  * A matrix of zeros gives zeros.  Status of a matrix: SPECV_ROW_NONFINITE (an entry that is
- * NaN or infinite): out 0, norm NaN; SPECV_ROW_DEVICE_TIMEOUT, on every matrix: out undefined.
+ * NaN or infinite): out 0, norm NaN; SPECV_ROW_DEVICE_TIMEOUT: out undefined (on every matrix,
+ * or, where all steps run in one kernel, on those whose wait it was).
  * Coefficients that may let a singular value grow past 1024 within the steps (by bounds over
  * [0, 1]) are refused with SPECV_ERR_INVALID_ARG, sizes above 2^31 - 2^11 and more than 65535
  * matrices with SPECV_ERR_UNSUPPORTED.

@@ -18,15 +18,28 @@ __device__ __forceinline__ uint64_t small_desc_mn(uint32_t plane, int k) {
   return ((static_cast<uint64_t>(plane + k * 2048) >> 4) & 0x3fff) | (lead << 16) | (stride << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// A B^T of 128 x 128 matrices of three parts, issued by one thread: blocks of 16 of K.
+// A B^T of 128 x 128 matrices of three parts, issued by one thread: blocks of 16 of K.  Its
+// end arrives on `done`.
 template <bool B_MN>
-__device__ __forceinline__ void small_product(uint32_t tmem, uint32_t a, uint32_t b, int blocks) {
+__device__ __forceinline__ void small_product(uint64_t* done, uint32_t tmem, uint32_t a, uint32_t b, int blocks) {
   constexpr uint32_t idesc = (1u << 4) | (B_MN ? 1u << 16 : 0u) | ((kSmallSide >> 3) << 17) | ((kSmallSide >> 4) << 24);
   for (int part = 0; part < 3; ++part) {
     const uint32_t pa = a + (part == 2 ? kPlane : 0), pb = b + (part == 1 ? kPlane : 0);
     for (int k = 0; k < blocks; ++k)
       tc_mma<false>(tmem, small_desc_k(pa, k), B_MN ? small_desc_mn(pb, k) : small_desc_k(pb, k), idesc, part > 0 || k > 0);
   }
+  tc_commit<false>(smem_u32(done));
+}
+
+// A wait that ran out goes on a little (half a second), so that what products in flight read and
+// write is not used again; once one of these ran out too (*gone is 2) they do not.
+__device__ __forceinline__ bool small_last_wait(uint64_t* bar, uint32_t parity, volatile int* gone) {
+  const long long t0 = clock64();
+  do {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  } while (*gone != 2 && clock64() - t0 < 1000000000LL);
+  *gone = 2;
+  return false;
 }
 
 }  // namespace
@@ -46,7 +59,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   const int rank = static_cast<int>(cluster_rank()), z = blockIdx.x / C;
   const int t0 = rank * kSmallSide;
   if (threadIdx.x == 0) {
-    mbar_init(&done, 1);
+    mbar_init(&done, p.stall == z + 1 && rank == 0 ? 2 : 1);
     fence_mbar_init();
     gone_flag = 0;
   }
@@ -136,9 +149,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   const uint32_t mine_at = tmem + panel * 64 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const int blocks_s = (p.s + 15) / 16;
   uint32_t phase = 0;
-  auto finish = [&] {  // of the products issued by thread 0, for all
-    if (threadIdx.x == 0) tc_commit<false>(smem_u32(&done));
-    prod_wait(&done, phase, gone);
+  // Products are issued by thread 0, and waited for by all.  Where one does not end in time no
+  // more are issued (lost), and the CTA goes on to the end, for the cluster's barriers.
+  bool lost = false;
+  auto finish = [&] {
+    if (!prod_wait(&done, phase, gone)) lost |= !small_last_wait(&done, phase, gone);
     phase ^= 1;
     __syncwarp();
     tc_fence_after();
@@ -152,7 +167,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   for (int k = 0; k < p.steps; ++k) {
     const SmallStep st = p.step[k];
     // S: this CTA's part, then this CTA's rows over all parts
-    if (threadIdx.x == 0) small_product<false>(tmem, y_at, y_at, kSmallSide / 16);
+    if (threadIdx.x == 0 && !lost) small_product<false>(&done, tmem, y_at, y_at, kSmallSide / 16);
     finish();
 #pragma unroll
     for (int c = 0; c < 64; c += 32) {
@@ -195,7 +210,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     cluster_sync();
     ready();
     // P = b S + c S S, in the place of the sums
-    if (threadIdx.x == 0) small_product<false>(tmem, s_at, s_at, blocks_s);
+    if (threadIdx.x == 0 && !lost) small_product<false>(&done, tmem, s_at, s_at, blocks_s);
     finish();
     auto update = [&](const uint8_t* from, uint8_t* to, float alpha, float beta, bool last) {
 #pragma unroll
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     update(sq, sums, st.poly, st.poly_s, false);
     ready();
     // Y <- a Y + P Y
-    if (threadIdx.x == 0) small_product<true>(tmem, sum_at, y_at, blocks_s);
+    if (threadIdx.x == 0 && !lost) small_product<true>(&done, tmem, sum_at, y_at, blocks_s);
     finish();
     update(y, y, st.step, st.step_y, k + 1 == p.steps);
     ready();

@@ -262,6 +262,7 @@ struct OrthRun {
     p.norm = a->norm, p.status = a->row_status;
     double r = 1, sx = keep_scale(r);
     p.scale = static_cast<float>(sx);
+    p.stall = api_test_stall('K');
     for (int k = 0; k < a->steps; ++k) {
       const double next = 1.01 * step_bound(a->a, a->b, a->c, r), sn = k + 1 == a->steps ? 1.0 : keep_scale(next);
       p.step[k] = factors(r, sx, sn);

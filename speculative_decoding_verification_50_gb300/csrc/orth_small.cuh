@@ -39,6 +39,7 @@ struct SmallParams {
   float* norm;
   int32_t* status;
   float scale;                  // Y is kept times this at first
+  int32_t stall;                // test hook: 1 + the matrix whose first products' end is not seen
   SmallStep step[kSmallSteps];
 };
 

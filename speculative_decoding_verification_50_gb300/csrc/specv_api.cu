@@ -282,8 +282,9 @@ bool persistent_path() {
 // over row n in the distillation kernel, "E:<t>" and "F:<t>" the first copy of tile t of the
 // logits of the head's loss and of an update's first product, "G:<t>" to "I:<t>" that of unit t
 // of dz, dW and dh in the head's loss, "J:<t>" the first copies that unit t's epilogues read in
-// an update's first step; the bounded wait then runs out (about a second) and the row (there:
-// every row or matrix) comes back flagged SPECV_ROW_DEVICE_TIMEOUT.  Returns 1 + that index for kernel
+// an update's first step, "K:<n>" the end of matrix n's first products in the kernel of small
+// updates; the bounded wait then runs out (about a second) and the row (there:
+// every row or matrix, in "K" that matrix) comes back flagged SPECV_ROW_DEVICE_TIMEOUT.  Returns 1 + that index for kernel
 // `which`, else 0.
 int test_stall(char which) {
   struct Stall {
@@ -292,7 +293,7 @@ int test_stall(char which) {
   };
   static const Stall st = [] {
     const char* e = getenv("SPECV_TEST_STALL");
-    if (e && e[0] >= 'A' && e[0] <= 'J' && e[1] == ':') return Stall{e[0], atoi(e + 2)};
+    if (e && e[0] >= 'A' && e[0] <= 'K' && e[1] == ':') return Stall{e[0], atoi(e + 2)};
     return Stall{0, -1};
   }();
   return (st.v >= 0 && st.k == which) ? st.v + 1 : 0;

@@ -9,6 +9,8 @@ import torch
 
 import speculative_decoding_verification_50_gb300 as sv
 from tests._head64 import head64, hold, inputs
+from tests._orth64 import bound, orth64
+from tests._orth64 import hold as hold_matrix
 
 
 def late(o, N, given=("grad_hidden", "grad_head")):
@@ -57,11 +59,22 @@ def update(N):
         assert (o["row_status"] == sv.ROW_DEVICE_TIMEOUT).all(), o["row_status"]
 
 
+def small(N):
+    """All steps in one kernel, clusters of 1 to 16 CTAs: the second matrix alone is flagged."""
+    for shape in ((3, N, 100), (3, 100, N)):
+        G = torch.randn(*shape, device="cuda")
+        o = sv.specv_orthogonalize(G)
+        assert o["row_status"].tolist() == [0, sv.ROW_DEVICE_TIMEOUT, 0], o["row_status"]
+        want, norm = orth64(G)
+        hold_matrix(o["orthogonal"][::2], want[::2], bound(*shape[1:]))
+        assert ((o["norm"].double() - norm).abs() <= 2.0 ** -17 * norm).all()
+
+
 def main():
     what, N = sys.argv[1], int(sys.argv[2])
     torch.cuda.synchronize()
     t0 = time.perf_counter()
-    update(N) if what == "update" else head(what, N)
+    {"update": update, "small": small}.get(what, lambda n: head(what, n))(N)
     torch.cuda.synchronize()
     dt = time.perf_counter() - t0
     assert 0.3 < dt < 40, dt

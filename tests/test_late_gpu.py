@@ -1,7 +1,8 @@
 """Copies and products that are late, in every kind of wait that the other stall tests do not
 reach, end in zeros or in a status, without a fault: by a wait for bytes or an arrival that
 nothing brings (the hook SPECV_TEST_STALL; "G:<t>" to "I:<t>": unit t of dz, dW and dh in the
-head's loss; "J:<t>": what unit t's epilogues read in an update's first step).  Each case in a fresh process."""
+head's loss; "J:<t>": what unit t's epilogues read in an update's first
+step; "K:<n>": the end of matrix n's first products in the kernel of small updates).  Each case in a fresh process."""
 import os
 import subprocess
 import sys
@@ -16,7 +17,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("what,stall,N", [("dz", "G:77", 45), ("dz", "G:0", 300), ("dW", "H:0", 45), ("dW", "H:33", 300),
-                                          ("dh", "I:1", 45), ("dh", "I:0", 300), ("update", "J:0", 300), ("update", "J:2", 200)])
+                                          ("dh", "I:1", 45), ("dh", "I:0", 300), ("update", "J:0", 300), ("update", "J:2", 200),
+                                          ("small", "K:1", 90), ("small", "K:1", 500), ("small", "K:1", 2048)])
 def test_late_copies(what, stall, N):
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
