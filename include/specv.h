@@ -536,17 +536,21 @@ specv_status specv_head_loss_backward(const specv_head_args* args, void* workspa
  * [m, n],  X = G / |G|_F, then `steps` times
  *   X <- a X + (b S + c S S) X,  S = X X^T  (rows the longer side: a X + X (b S + c S S), S = X^T X)
  * out = X in bf16; norm[k] = |G|_F.  With (3.4445, -4.7750, 2.0315) five steps bring singular
- * values from 0.01 |G|_F on to between 0.7 and 1.2.
+ * values from 0.006 |G|_F on to between 0.68 and 1.14.
  * Products are of fp16 operands, summed in fp32; X is kept to 21 bits beside them: out is off
- * five exact steps by about 2e-3 of its norm at most, most of it the rounding to bf16
- * (low-rank and badly scaled updates too).
+ * five exact steps by 2.4e-3 of its norm where roundings are independent (1.7e-3 of it the
+ * rounding to bf16; gradients, low-rank and badly scaled updates).  Above a smaller side of 256,
+ * matrices whose roundings agree are further off: few rows that are not zero 4e-3, diagonal,
+ * constant or +-1 matrices 9e-3 measured, 3e-2 at most.  Up to 256, products take operands of
+ * 21 bits, and the rounding to bf16 is all.
  * A matrix of zeros gives zeros.  Status of a matrix: SPECV_ROW_NONFINITE (an entry that is
  * NaN or infinite): out 0, norm NaN; SPECV_ROW_DEVICE_TIMEOUT: out undefined (on every matrix,
  * or, where all steps run in one kernel, on those whose wait it was).
  * Coefficients that may let a singular value grow past 1024 within the steps (by bounds over
  * [0, 1]) are refused with SPECV_ERR_INVALID_ARG, sizes above 2^31 - 2^11 and more than 65535
  * matrices with SPECV_ERR_UNSUPPORTED.
- * out may be update itself (bf16).  workspace: device memory of
+ * out may be update itself (bf16).  A batch's matrices lie one behind the other: strides by
+ * which they overlap, or lie between each other's rows, are refused.  workspace: device memory of
  * specv_orthogonalize_workspace_bytes() bytes (8 m n + 4 min(m, n)^2 per matrix, about; 0 for
  * matrices of a side up to 128 and another up to 2048, one kernel), 256-byte aligned, not
  * shared with a call that may run at the same time.
