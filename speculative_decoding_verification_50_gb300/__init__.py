@@ -799,7 +799,7 @@ def _work(need, workspace, device, stream):
 def _sizes(*tensors):
     """(ctypes cuts a size off that 32 bits do not hold.)"""
     for t in tensors:
-        assert all(n < 2 ** 31 for n in t.shape), f"a size of {tuple(t.shape)} is 2^31 or more"
+        assert max(t.shape) < 2 ** 31, f"a size of {tuple(t.shape)} is 2^31 or more"
 
 
 def _head_args(hidden, head, targets, scale, weights, grad_hidden, grad_head):
