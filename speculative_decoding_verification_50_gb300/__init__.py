@@ -826,7 +826,7 @@ def specv_head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None, 
                     targets_only: bool = False, loss=None, stats=None, row_status=None, grad_hidden=None, grad_head=None,
                     workspace=None, stream=None) -> dict:
     """Cross entropy of the tokens `targets` under softmax(scale * hidden @ head.T), without
-    the logits in memory (see include/specv.h, specv_head_loss).
+    the logits as an input or an output (see include/specv.h, specv_head_loss).
 
     hidden [N, D] and head [V, D] (bf16, CUDA, last dim contiguous); targets int32 [N] (-1:
     none); weights fp32 [N] or None (0: a row that is left out).  Returns loss fp32 [N], stats
@@ -889,7 +889,8 @@ _HeadLoss = None
 
 def head_loss(hidden, head, targets, *, scale: float = 1.0, weights=None):
     """specv_head_loss's loss per row [N], differentiable with respect to hidden and head
-    (once: the backward pass is specv_head_loss_backward, which computes the logits again).
+    (once: the backward pass is specv_head_loss_backward, which computes the logits again;
+    after a device wait that ran out its gradients are zeros).
     To capture a training step in a CUDA graph, call specv_head_loss with gradient buffers, or
     specv_head_loss_backward, in it, as for distill_loss."""
     global _HeadLoss
@@ -928,6 +929,7 @@ def specv_orthogonalize(update, *, steps: int = 5, coefficients=(3.4445, -4.7750
     c S S) X with S = X X^T from X = update / |update|_F (see include/specv.h).
 
     update [m, n], or [B, m, n] for B matrices (bf16 or fp32, CUDA, last dim contiguous).
+    Matrices of a batch that overlap (expand) or lie between each other's rows are refused.
     Returns orthogonal (bf16, shaped as update; `out`, which may be update itself), norm fp32
     and row_status int32 (scalars, or [B])."""
     import torch

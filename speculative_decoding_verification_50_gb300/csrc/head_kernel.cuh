@@ -1,5 +1,5 @@
 // The cross entropy of given tokens from hidden states h [N, D] and the head W [V, D],
-// and its gradients, without the logits in memory.
+// and its gradients, without the logits as an input or an output.
 //
 //   z = s h W^T,  nll_i = log(1 + sum_{v != t} exp(z_iv - z_it)),  lse_i = z_it + nll_i,
 //   dz_iv = g_i exp(z_iv - lse_i), at the target g_i (exp(-nll_i) - 1),
@@ -64,7 +64,9 @@ struct HeadStatsParams {
 // chunks, which are added here (LONG; D = 4096: 2.3e-6 of the loss in one sum, 5e-7 in
 // chunks of 16 blocks).  Rows of one tile, bound by the head's bytes, take shorter ones
 // (45 x 4096 x 128256: 176 us in chunks of 8 blocks, 179 of 4, 194 of 2; 2e-7, 1e-7 and 1e-7
-// off).  PART: columns per partial sum, those of an epilogue warp.
+// off).  PART: columns per partial sum, those of an epilogue warp.  A lane's 128 sums (LONG, PART
+// 128) do not all fit beside the rest in its registers: 40 bytes are spilled here and 60 in
+// KeepEpi<128> (120 and 156 read back), the only product kernels with spills.
 constexpr int kStatsChunk = 16, kStatsChunkFew = 4;
 template <bool LONG, int PART>
 struct StatsEpi : PlainEpi {

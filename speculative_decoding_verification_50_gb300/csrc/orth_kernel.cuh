@@ -9,6 +9,9 @@
 // With X in fp16 alone its rounding, spread over all directions, grows with the small
 // ones, by a factor a per step: a low-rank update then ends 2e-2 off its exact result, in
 // this form 2e-4 (random ones 1.5e-3; bf16 throughout 0.16 and 1e-2).  Sums are fp32.
+// Those are matrices whose entries' roundings are independent.  Where they agree, S and P are
+// off the same way in every direction: five rows that are not zero 3e-3 (one 4e-3), diagonal,
+// constant and +-1 matrices up to 9e-3.
 // Matrices whose smaller side is at most 256 (one tile) cost launches, not products, and
 // errors of few singular values do not average out: there S and P are kept to 21 bits too,
 // and products take three parts (high x high, high x low, low x high).
