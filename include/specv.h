@@ -493,7 +493,7 @@ specv_status specv_distill_backward(const specv_distill_args* args, void* stream
  * largest weight: rows whose weight is below 2^-100 of that lose digits.
  * Logits may be of any finite size: losses and probabilities are taken from their differences.
  * (specv_head_loss_backward has those of a row from stats: where nll and |log-sum-exp| are both
- * large, its probabilities are off by 2^-21 times the smaller of the two.)
+ * large, its probabilities are off by 2^-21 times the smaller of the two, and at most one.)
  * Row status: SPECV_ROW_BAD_TOKEN (a target outside [-1, V)), SPECV_ROW_NONFINITE (a logit
  * that is NaN or infinite; rows that are left out may hold anything): loss 0, stats NaN, no
  * gradient.  SPECV_ROW_DEVICE_TIMEOUT: the same, on every row that counts; where the wait that

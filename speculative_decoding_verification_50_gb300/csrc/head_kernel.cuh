@@ -37,9 +37,10 @@ struct alignas(16) HeadRow {
   float g;     // upstream weight x s, over the call's largest (HeadRowsParams::most); 0: no gradient
   float at;    // dz at the target
   int32_t target;
-  int32_t none[3];
+  float most;  // of its exponents: 0 in rows far from zero, whatever their statistics hold, else infinity
+  int32_t none[2];
 };
-__device__ __forceinline__ HeadRow head_no_row() { return {0.f, 0.f, 0.f, 0.f, -1, {0, 0, 0}}; }
+__device__ __forceinline__ HeadRow head_no_row() { return {0.f, 0.f, 0.f, 0.f, -1, pos_inf(), {0, 0}}; }
 
 // (smallest of three, NaN ignored)
 __device__ __forceinline__ float min3(float a, float b, float c) {
@@ -234,9 +235,9 @@ struct ProbEpi : PlainEpi {
     HeadRow r = head_no_row();
     if (i < q.rows) {
       const float4 x = *reinterpret_cast<const float4*>(e.row + i);
-      r.ref = x.x, r.off = x.y, r.g = x.z, r.at = x.w, r.target = e.row[i].target;
+      r.ref = x.x, r.off = x.y, r.g = x.z, r.at = x.w, r.target = e.row[i].target, r.most = e.row[i].most;
     }
-    const bool far = __any_sync(0xffffffffu, r.ref != 0.f);
+    const bool far = __any_sync(0xffffffffu, r.most == 0.f);
 #pragma unroll 1
     for (int c = 0; c < COLS; c += 64) {
       if (q.col0 + c >= e.out.cols) break;
@@ -245,10 +246,9 @@ struct ProbEpi : PlainEpi {
       for (int h = 0; h < 2; ++h) {
         float v[32];
         tmem_load32(q.tmem + c + 32 * h, v);
-        if (far) {  // (no probability is more than one, whatever its row's statistics hold of it)
-          const float most = r.ref != 0.f ? 0.f : pos_inf();
+        if (far) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fminf(fmaf(v[j] - r.ref, e.c2, -r.off), most));
+          for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fminf(fmaf(v[j] - r.ref, e.c2, -r.off), r.most));
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = r.g * ex2(fmaf(v[j], e.c2, -r.off));

@@ -21,11 +21,11 @@ __device__ __forceinline__ int head_target(const HeadRowsParams& p, int r) {
 __device__ __forceinline__ float head_weight(const HeadRowsParams& p, int r) {
   return (p.weight ? p.weight[r] : 1.f) * (p.up ? p.up[r] : 1.f) * p.scale;
 }
-__device__ __forceinline__ HeadRow head_row(float lse, float nll, float g, int target) {
-  return {0.f, lse * kLog2e, g, g * expm1f(-nll), target, {0, 0, 0}};
-}
 // Whether a row's log-sum-exp does not hold its probabilities' digits.
 __device__ __forceinline__ bool head_far(float lse) { return fabsf(lse) * kLog2e > kFarRow; }
+__device__ __forceinline__ HeadRow head_row(float lse, float nll, float g, int target) {
+  return {0.f, lse * kLog2e, g, g * expm1f(-nll), target, head_far(lse) ? 0.f : pos_inf(), {0, 0}};
+}
 // The largest weight of a CTA's threads (a power of two of them up to 1024).
 __device__ __forceinline__ float head_most(float g, float (&warps)[32]) {
 #pragma unroll

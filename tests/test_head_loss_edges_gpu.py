@@ -134,3 +134,24 @@ def test_rows_beside_one_far_from_zero(N, D):
                 same = (x[k] == y[k]).reshape(N, -1).all(1)
                 same[1] = True
                 assert same.all(), (k, same.nonzero()[:, 0].tolist())
+
+
+@pytest.mark.parametrize("N", [64, 300])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_statistics_that_do_not_hold_the_probabilities(N, sign):
+    """A loss and a log-sum-exp of 10^9: a backward pass from them knows no probability, but takes
+    none for more than one (the call that computes both knows them)."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    W = torch.zeros(300, 16, dtype=torch.bfloat16, device="cuda")
+    W[:, 1] = torch.randn(300, generator=g, device="cuda").bfloat16()
+    W[0, 0], W[7, 0] = (1, -2) if sign > 0 else (-1, -4)
+    W[1:7, 0] = W[8:, 0] = -4 if sign > 0 else -8
+    h = torch.zeros(N, 16, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = (torch.rand(N, generator=g, device="cuda") + 0.5) * 2.0 ** 30
+    t = torch.full((N,), 7, dtype=torch.int32, device="cuda")
+    one, two = both(h, W, t)
+    assert (one["row_status"] == 0).all() and (one["loss"] > 2e8).all()
+    want = (W[0].double() - W[7].double()).bfloat16()
+    assert torch.equal(one["grad_hidden"], want.expand(N, 16))
+    most = 1.01 * (W[0].abs() + W[7].abs()).double()
+    assert (two["grad_hidden"].double().abs() <= most).all(), (two["grad_hidden"].abs() / most).max()
