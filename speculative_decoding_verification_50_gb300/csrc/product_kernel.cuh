@@ -181,6 +181,14 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// The same, on this CTA's barrier alone.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_own(uint32_t bar) {
+  if (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    tc_commit<false>(bar);
+}
 // 32 columns of this warp's 32 lanes: thread l gets row l.
 __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
@@ -432,8 +440,9 @@ __global__ void __launch_bounds__(kProdThreads, 1)
           if (ok) tc_commit<PAIR>(smem_u32(&tfull[n & 1]));
         }
       }
-      // (products in flight end before tensor memory is freed, whatever other warps gave up on)
-      tc_commit<PAIR>(smem_u32(drain));
+      // (products in flight end before tensor memory is freed, whatever other warps gave up on;
+      // nothing waits for them at the pair's other CTA, which may leave)
+      tc_commit_own<PAIR>(smem_u32(drain));
       const long long t0 = clock64();
       while (!mbar_try_wait_sleep(drain, 0, 20000u) && clock64() - t0 < 1000000000LL) {
       }
